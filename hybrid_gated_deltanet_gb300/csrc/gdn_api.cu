@@ -161,12 +161,13 @@ const char* gdn_version(void) { return "libgdn 0.1 (sm_103a)"; }
 gdn_status gdn_device_status(uint32_t* status) {
     if (!status) return fail(GDN_ERR_NULL, "status: found NULL, required a host pointer");
     unsigned a = 0, b = 0;
-    unsigned c = 0, d = 0;
+    unsigned c = 0, d = 0, t = 0;
     cudaError_t e = gdn::take_device_status_decode(&a);
     if (e == cudaSuccess) e = gdn::take_device_status_prefill(&b);
     if (e == cudaSuccess) e = gdn::take_device_status_proj(&c);
     if (e == cudaSuccess) e = gdn::take_device_status_chunk16(&d);
-    *status = a | b | c | d;
+    if (e == cudaSuccess) e = gdn::take_device_status_tree(&t);
+    *status = a | b | c | d | t;
     return cuda_status(e, "gdn_device_status");
 }
 
@@ -734,6 +735,192 @@ gdn_status gdn_attn_prefill(const gdn_attn_config* cfg, const void* q, const voi
     j.max_pages = max_pages; j.n_pages = n_pages; j.n_tokens = n_tokens;
     j.scale = cfg->scale > 0.f ? cfg->scale : 1.0f / sqrtf((float)cfg->head_dim);
     return cuda_status(gdn::launch_attn_prefill(j, (cudaStream_t)stream), "gdn_attn_prefill");
+}
+
+// ---- trees of drafted tokens, page tables -------------------------------------
+
+static gdn_status max_check(const char* name, int32_t v) {
+    if (v < 1 || v > GDN_TREE_MAX_NODES)
+        return fail(GDN_ERR_RANGE, "%s: found %d, required 1..%d", name, v, GDN_TREE_MAX_NODES);
+    return GDN_OK;
+}
+
+size_t gdn_attn_tree_workspace_size(const gdn_attn_config* cfg, int32_t B, int32_t max_nodes, int32_t max_ctx_len) {
+    if (attn_check(cfg) != GDN_OK) return 0;
+    if (B < 0 || B > 65535 || max_ctx_len < 0) {
+        fail(GDN_ERR_RANGE, "B/max_ctx_len: found %d/%d, required 0..65535/>= 0", B, max_ctx_len);
+        return 0;
+    }
+    if (max_check("max_nodes", max_nodes)) return 0;
+    ok();
+    return gdn::attn_tree_workspace_bytes(B, cfg->n_q_heads, cfg->n_kv_heads, cfg->head_dim, max_nodes, max_ctx_len);
+}
+
+gdn_status gdn_attn_tree(const gdn_attn_config* cfg, const void* q, const void* k_new, const void* v_new,
+                         const void* k_pool, const void* v_pool, const int32_t* block_table, const int32_t* cu_nodes,
+                         const int32_t* parents, const int32_t* ctx_lens, int32_t B, int32_t n_nodes,
+                         int32_t max_nodes, int32_t max_pages, int32_t n_pages, int32_t max_ctx_len, void* o,
+                         void* workspace, size_t ws_bytes, void* stream) {
+    gdn_status st = attn_check(cfg);
+    if (st) return st;
+    if (B < 0 || B > 65535) return fail(GDN_ERR_RANGE, "B: found %d, required 0..65535", B);
+    if (n_nodes < 0) return fail(GDN_ERR_RANGE, "n_nodes: found %d, required >= 0", n_nodes);
+    if ((st = max_check("max_nodes", max_nodes))) return st;
+    if (max_pages < 1 || n_pages < 1 || max_ctx_len < 0)
+        return fail(GDN_ERR_RANGE, "max_pages/n_pages/max_ctx_len: found %d/%d/%d, required >= 1/>= 1/>= 0", max_pages,
+                    n_pages, max_ctx_len);
+    if (B == 0 || n_nodes == 0) return ok();
+    GDN_REQUIRE_PTR(q, "q");
+    GDN_REQUIRE_PTR(k_new, "k_new");
+    GDN_REQUIRE_PTR(v_new, "v_new");
+    GDN_REQUIRE_PTR(k_pool, "k_pool");
+    GDN_REQUIRE_PTR(v_pool, "v_pool");
+    GDN_REQUIRE_PTR_A(block_table, "block_table", 4u);
+    GDN_REQUIRE_PTR_A(cu_nodes, "cu_nodes", 4u);
+    GDN_REQUIRE_PTR_A(parents, "parents", 4u);
+    GDN_REQUIRE_PTR_A(ctx_lens, "ctx_lens", 4u);
+    GDN_REQUIRE_PTR(o, "o");
+    const size_t need = gdn::attn_tree_workspace_bytes(B, cfg->n_q_heads, cfg->n_kv_heads, cfg->head_dim, max_nodes,
+                                                       max_ctx_len);
+    if (need > 0) GDN_REQUIRE_PTR(workspace, "workspace");
+    if (ws_bytes < need)
+        return fail(GDN_ERR_WORKSPACE, "workspace: found %zu bytes, required %zu bytes", ws_bytes, need);
+    gdn::AttnTreeJob j;
+    j.q = q; j.k_new = k_new; j.v_new = v_new; j.k_pool = k_pool; j.v_pool = v_pool;
+    j.block_table = block_table; j.cu_nodes = cu_nodes; j.parents = parents; j.ctx_lens = ctx_lens; j.o = o;
+    j.ws = workspace;
+    j.B = B; j.Hq = cfg->n_q_heads; j.Hkv = cfg->n_kv_heads; j.D = cfg->head_dim; j.page = cfg->page_size;
+    j.max_pages = max_pages; j.n_pages = n_pages; j.n_nodes = n_nodes; j.max_nodes = max_nodes;
+    j.max_ctx = max_ctx_len;
+    j.scale = cfg->scale > 0.f ? cfg->scale : 1.0f / sqrtf((float)cfg->head_dim);
+    return cuda_status(gdn::launch_attn_tree(j, (cudaStream_t)stream), "gdn_attn_tree");
+}
+
+gdn_status gdn_verify_tree(const gdn_config* cfg, const gdn_params* prm, const void* x, const void* z, const void* a,
+                           const void* b, const void* conv_pool, const float* state_pool, const int32_t* slot_idx,
+                           const int32_t* cu_nodes, const int32_t* parents, int32_t B, int32_t n_nodes,
+                           int32_t max_nodes, int32_t n_slots, void* y, void* stream) {
+    gdn::Geom g;
+    gdn::LayerParams p;
+    gdn_status st = make_geom(cfg, false, &g);
+    if (st) return st;
+    if (B < 0 || B > 65535) return fail(GDN_ERR_RANGE, "B: found %d, required 0..65535", B);
+    if (n_nodes < 0) return fail(GDN_ERR_RANGE, "n_nodes: found %d, required >= 0", n_nodes);
+    if ((st = max_check("max_nodes", max_nodes))) return st;
+    if (n_slots < 1) return fail(GDN_ERR_RANGE, "n_slots: found %d, required >= 1", n_slots);
+    if (B == 0 || n_nodes == 0) return ok();
+    if ((st = make_params(prm, g, true, &p))) return st;
+    const unsigned ae = g.act_bf16 ? 2u : 4u;
+    GDN_REQUIRE_PTR(x, "x");
+    if (!(g.flags & GDN_FLAG_NO_OUTNORM)) GDN_REQUIRE_PTR(z, "z");
+    GDN_REQUIRE_PTR_A(a, "a", ae);
+    GDN_REQUIRE_PTR_A(b, "b", ae);
+    GDN_REQUIRE_PTR(conv_pool, "conv_pool");
+    GDN_REQUIRE_PTR(state_pool, "state_pool");
+    GDN_REQUIRE_PTR_A(slot_idx, "slot_idx", 4u);
+    GDN_REQUIRE_PTR_A(cu_nodes, "cu_nodes", 4u);
+    GDN_REQUIRE_PTR_A(parents, "parents", 4u);
+    GDN_REQUIRE_PTR(y, "y");
+    // (slots are only read here, so two trees may share one: no GDN_DEBUG check for repeats)
+    gdn::TreeJob job{x, z, a, b, conv_pool, state_pool, slot_idx, cu_nodes, parents, y, B, n_nodes, max_nodes, n_slots};
+    return cuda_status(gdn::launch_tree_verify(g, p, job, (cudaStream_t)stream), "gdn_verify_tree");
+}
+
+gdn_status gdn_commit_tree(const gdn_config* cfg, const gdn_params* prm, const void* x, const void* a, const void* b,
+                           void* conv_pool, float* state_pool, const int32_t* slot_idx, const int32_t* cu_rows,
+                           const int32_t* src_rows, int32_t B, int32_t n_rows, int32_t n_src, int32_t max_rows,
+                           int32_t n_slots, void* stream) {
+    gdn::Geom g;
+    gdn::LayerParams p;
+    gdn_status st = make_geom(cfg, false, &g);
+    if (st) return st;
+    if (B < 0 || B > 65535) return fail(GDN_ERR_RANGE, "B: found %d, required 0..65535", B);
+    if (n_rows < 0 || n_src < 0)
+        return fail(GDN_ERR_RANGE, "n_rows/n_src: found %d/%d, required >= 0", n_rows, n_src);
+    if ((st = max_check("max_rows", max_rows))) return st;
+    if (n_slots < 1) return fail(GDN_ERR_RANGE, "n_slots: found %d, required >= 1", n_slots);
+    if (B == 0 || n_rows == 0 || n_src == 0) return ok();
+    if ((st = make_params(prm, g, true, &p))) return st;
+    const unsigned ae = g.act_bf16 ? 2u : 4u;
+    GDN_REQUIRE_PTR(x, "x");
+    GDN_REQUIRE_PTR_A(a, "a", ae);
+    GDN_REQUIRE_PTR_A(b, "b", ae);
+    GDN_REQUIRE_PTR(conv_pool, "conv_pool");
+    GDN_REQUIRE_PTR(state_pool, "state_pool");
+    GDN_REQUIRE_PTR_A(slot_idx, "slot_idx", 4u);
+    GDN_REQUIRE_PTR_A(cu_rows, "cu_rows", 4u);
+    GDN_OPTIONAL_PTR_A(src_rows, "src_rows", 4u);
+    if ((st = debug_check_slots("slot_idx", slot_idx, B, "slot_idx", nullptr, 0, n_slots, stream))) return st;
+    gdn::TreeCommitJob job{x, a, b, conv_pool, state_pool, slot_idx, cu_rows, src_rows, B, n_rows, n_src, max_rows,
+                           n_slots};
+    return cuda_status(gdn::launch_tree_commit(g, p, job, (cudaStream_t)stream), "gdn_commit_tree");
+}
+
+gdn_status gdn_page_tables(int32_t page_size, int32_t n_pages, const int32_t* ctx_lens, const int32_t* new_lens,
+                           int32_t B, const int32_t* free_pages, int32_t n_free, const int32_t* head,
+                           int32_t* block_table, int32_t max_pages, int32_t* cu_rows, int64_t* slot_map,
+                           int32_t n_rows, int32_t* head_out, const int32_t* path, int32_t path_len,
+                           const int32_t* cu_nodes, int32_t* src_rows, void* stream) {
+    if (page_size < 1 || n_pages < 1 || (int64_t)n_pages * page_size > ((int64_t)1 << 40))
+        return fail(GDN_ERR_RANGE, "page_size/n_pages: found %d/%d, required >= 1 and at most 2^40 rows", page_size,
+                    n_pages);
+    if (B < 0 || B > 65535) return fail(GDN_ERR_RANGE, "B: found %d, required 0..65535", B);
+    if (n_free < 0 || max_pages < 1 || n_rows < 0)
+        return fail(GDN_ERR_RANGE, "n_free/max_pages/n_rows: found %d/%d/%d, required >= 0/>= 1/>= 0", n_free,
+                    max_pages, n_rows);
+    if (B > 0) {
+        GDN_REQUIRE_PTR_A(ctx_lens, "ctx_lens", 4u);
+        GDN_REQUIRE_PTR_A(new_lens, "new_lens", 4u);
+        GDN_REQUIRE_PTR_A(block_table, "block_table", 4u);
+    }
+    if (n_free > 0) GDN_REQUIRE_PTR_A(free_pages, "free_pages", 4u);
+    GDN_REQUIRE_PTR_A(head, "head", 4u);
+    GDN_REQUIRE_PTR_A(cu_rows, "cu_rows", 4u);
+    if (n_rows > 0) GDN_REQUIRE_PTR_A(slot_map, "slot_map", 8u);
+    GDN_REQUIRE_PTR_A(head_out, "head_out", 4u);
+    if (head == head_out)
+        return fail(GDN_ERR_RANGE, "head_out: found the address of head, required another (every block reads head)");
+    if ((path != nullptr) != (src_rows != nullptr) || (path != nullptr) != (cu_nodes != nullptr))
+        return fail(GDN_ERR_NULL, "path/cu_nodes/src_rows: found %p/%p/%p, required all three or none",
+                    (const void*)path, (const void*)cu_nodes, (const void*)src_rows);
+    if (path) {
+        GDN_PTR_ALIGN(path, "path", 4u);
+        GDN_PTR_ALIGN(cu_nodes, "cu_nodes", 4u);
+        GDN_PTR_ALIGN(src_rows, "src_rows", 4u);
+        if (path_len < 1) return fail(GDN_ERR_RANGE, "path_len: found %d, required >= 1", path_len);
+    }
+    gdn::TablesJob job;
+    job.ctx_lens = ctx_lens; job.new_lens = new_lens; job.free_pages = free_pages; job.head = head;
+    job.path = path; job.cu_nodes = cu_nodes;
+    job.block_table = block_table; job.cu_rows = cu_rows; job.src_rows = src_rows; job.head_out = head_out;
+    job.slot_map = slot_map;
+    job.B = B; job.page = page_size; job.n_pages = n_pages; job.max_pages = max_pages; job.n_free = n_free;
+    job.n_rows = n_rows; job.path_len = path_len;
+    return cuda_status(gdn::launch_page_tables(job, (cudaStream_t)stream), "gdn_page_tables");
+}
+
+gdn_status gdn_attn_append(const gdn_attn_config* cfg, const void* k_new, const void* v_new, int64_t n_src,
+                           const int64_t* slot_map, const int32_t* src_rows, int64_t n_rows, void* k_pool,
+                           void* v_pool, int32_t n_pages, void* stream) {
+    gdn_status st = attn_check(cfg);
+    if (st) return st;
+    if (n_rows < 0 || n_rows > (int64_t)1 << 30 || n_src < 0 || n_src > (int64_t)1 << 30)
+        return fail(GDN_ERR_RANGE, "n_rows/n_src: found %lld/%lld, required 0..2^30", (long long)n_rows,
+                    (long long)n_src);
+    if (n_pages < 1) return fail(GDN_ERR_RANGE, "n_pages: found %d, required >= 1", n_pages);
+    if (n_rows == 0 || n_src == 0) return ok();
+    GDN_REQUIRE_PTR(k_new, "k_new");
+    GDN_REQUIRE_PTR(v_new, "v_new");
+    GDN_REQUIRE_PTR_A(slot_map, "slot_map", 8u);
+    GDN_OPTIONAL_PTR_A(src_rows, "src_rows", 4u);
+    GDN_REQUIRE_PTR(k_pool, "k_pool");
+    GDN_REQUIRE_PTR(v_pool, "v_pool");
+    gdn::AppendJob job;
+    job.k_new = k_new; job.v_new = v_new; job.slot_map = slot_map; job.src_rows = src_rows;
+    job.k_pool = k_pool; job.v_pool = v_pool;
+    job.n_rows = n_rows; job.n_src = n_src;
+    job.Hkv = cfg->n_kv_heads; job.D = cfg->head_dim; job.page = cfg->page_size; job.n_pages = n_pages;
+    return cuda_status(gdn::launch_append(job, (cudaStream_t)stream), "gdn_attn_append");
 }
 
 }  // extern "C"

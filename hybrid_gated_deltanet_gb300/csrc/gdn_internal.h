@@ -195,6 +195,72 @@ struct AttnPfJob {
 };
 cudaError_t launch_attn_prefill(const AttnPfJob& job, cudaStream_t st);
 
+// ---- trees of drafted tokens ----
+// nodes cu_nodes[b] .. cu_nodes[b+1] of sequence b; parents[i]: the node within the
+// sequence that node i follows, or the end of the cached sequence where it is outside [0, i)
+
+// attention of every node over the cached tokens, its ancestors and itself
+struct AttnTreeJob {
+    const void *q, *k_new, *v_new, *k_pool, *v_pool;
+    const int32_t* block_table;
+    const int32_t* cu_nodes;
+    const int32_t* parents;
+    const int32_t* ctx_lens;
+    void* o;
+    void* ws;
+    int B, Hq, Hkv, D, page, max_pages, n_pages, n_nodes, max_nodes, max_ctx;
+    float scale;
+};
+size_t attn_tree_workspace_bytes(int B, int Hq, int Hkv, int D, int max_nodes, int max_ctx);
+cudaError_t launch_attn_tree(const AttnTreeJob& job, cudaStream_t st);
+
+// the layer's output at every node; the pools are not written
+struct TreeJob {
+    const void *x, *z, *a, *b;
+    const void* conv_pool;
+    const float* state_pool;
+    const int32_t* slot_idx;
+    const int32_t* cu_nodes;
+    const int32_t* parents;
+    void* y;
+    int B, n_nodes, max_nodes, n_slots;
+};
+cudaError_t launch_tree_verify(const Geom& g, const LayerParams& prm, const TreeJob& job, cudaStream_t st);
+
+// rows src_rows[cu_rows[b]] .. of x, a, b (src_rows NULL: those rows themselves) applied to
+// slot_idx[b] in place, in order
+struct TreeCommitJob {
+    const void *x, *a, *b;
+    void* conv_pool;
+    float* state_pool;
+    const int32_t* slot_idx;
+    const int32_t* cu_rows;
+    const int32_t* src_rows;
+    int B, n_rows, n_src, max_rows, n_slots;
+};
+cudaError_t launch_tree_commit(const Geom& g, const LayerParams& prm, const TreeCommitJob& job, cudaStream_t st);
+
+// pages and row maps from request lengths
+struct TablesJob {
+    const int32_t *ctx_lens, *new_lens, *free_pages, *head;
+    const int32_t *path, *cu_nodes;  // NULL: no source rows
+    int32_t *block_table, *cu_rows, *src_rows, *head_out;
+    int64_t* slot_map;
+    int B, page, n_pages, max_pages, n_free, n_rows, path_len;
+};
+cudaError_t launch_page_tables(const TablesJob& job, cudaStream_t st);
+
+// K and V rows src_rows[i] (NULL: i) into cache rows slot_map[i]
+struct AppendJob {
+    const void *k_new, *v_new;
+    const int64_t* slot_map;
+    const int32_t* src_rows;
+    void *k_pool, *v_pool;
+    int64_t n_rows, n_src;
+    int Hkv, D, page, n_pages;
+};
+cudaError_t launch_append(const AppendJob& job, cudaStream_t st);
+
 // GDN_DEBUG: device-side check that the na + nb indices of idx_a then idx_b lie in
 // [0, n_slots) and are distinct.  A violation ORs kDevBadSlot into the device status
 // word.  With wait, the stream is synchronised and the first bad position (or -1)
@@ -208,5 +274,6 @@ cudaError_t take_device_status_decode(unsigned* out);
 cudaError_t take_device_status_prefill(unsigned* out);
 cudaError_t take_device_status_chunk16(unsigned* out);
 cudaError_t take_device_status_proj(unsigned* out);
+cudaError_t take_device_status_tree(unsigned* out);
 
 }  // namespace gdn

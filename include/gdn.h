@@ -427,6 +427,134 @@ size_t gdn_attn_workspace_size(const gdn_attn_config* cfg, int32_t B, int32_t ma
 size_t gdn_layer_workspace_size(const gdn_config* cfg, int32_t op, int64_t n_tokens, int32_t n_seq,
                                 int32_t hidden);
 
+/* ---- Trees of drafted tokens --------------------------------------------------
+ * Speculative decoding with drafts that branch: sequence b brings a tree of
+ * n_b = cu_nodes[b+1] - cu_nodes[b] drafted tokens ("nodes"), rows cu_nodes[b] .. of the
+ * call's arrays.  parents[row] is the node, counted within the sequence, that the
+ * row's node follows; it lies before its child.  A value outside [0, child) (-1
+ * by convention) means the end of the cached sequence, so a tree may have several
+ * first nodes, and a chain is parents = -1, 0, 1, ...  A node's line is the node and
+ * its ancestors.  "Forge: how I wrote my own inference engine and overtook
+ * llama.cpp" (27 August) verifies a drafted chain as a chunk and rolls back
+ * without touching the cache; these calls do so for trees:
+ *   gdn_verify_tree and gdn_attn_tree, per layer, give every node's output and
+ *   write no state and no page, so that a rejected node leaves nothing behind;
+ *   gdn_page_tables, once per step, reserves pages for the accepted tokens and
+ *   lists their rows; gdn_commit_tree and gdn_attn_append, per layer, then
+ *   bring the accepted rows into the recurrent states and the cache.
+ * Device data (checked on the device, never trusted for an address): a tree
+ * with n_b < 1 or > max_nodes, or with rows outside [0, n_nodes), is skipped
+ * (its output rows are left as they were).  Rows that belong to no tree are left
+ * as they were. */
+enum { GDN_TREE_MAX_NODES = 64 };
+
+/* Tree attention: node i of sequence b attends to the ctx_lens[b] cached tokens and
+ * to its line,
+ *   o[i][h] = softmax over both (scale q[i][h] . k) v,   kv-head floor(h / G).
+ * The nodes' keys and values come from k_new and v_new, not from the cache, and
+ * the pools are read only: pages may be shared between sequences.
+ *   q, o bf16 [n_nodes][n_q_heads][head_dim]; k_new, v_new bf16
+ *   [n_nodes][n_kv_heads][head_dim]; pools, block_table [B][max_pages] as in
+ *   gdn_attn_decode; cu_nodes int32 [B+1], parents int32 [n_nodes], ctx_lens
+ *   int32 [B] (device).
+ *   max_nodes: host bound on every n_b, 1 .. GDN_TREE_MAX_NODES; max_ctx_len:
+ *   host bound on every ctx_lens[b].  A sequence with ctx_lens[b] < 0, above
+ *   max_ctx_len or above max_pages * page_size is skipped; cached tokens on pages
+ *   outside [0, n_pages) are left out.
+ *   Cache rows past ctx_lens[b], and nodes outside a node's line, do not reach its
+ *   output whatever they hold (NaN and infinities included).
+ *   workspace: gdn_attn_tree_workspace_size bytes (NULL when 0); calls that may
+ *   overlap need one each.
+ *   Alignment and precision as gdn_attn_prefill (bf16 operands on the tensor
+ *   cores, fp32 scores, sums and accumulation, weights rounded to bf16). */
+gdn_status gdn_attn_tree(const gdn_attn_config* cfg, const void* q, const void* k_new,
+                         const void* v_new, const void* k_pool, const void* v_pool,
+                         const int32_t* block_table, const int32_t* cu_nodes,
+                         const int32_t* parents, const int32_t* ctx_lens, int32_t B,
+                         int32_t n_nodes, int32_t max_nodes, int32_t max_pages, int32_t n_pages,
+                         int32_t max_ctx_len, void* o, void* workspace, size_t ws_bytes,
+                         void* stream);
+
+/* Workspace bytes of gdn_attn_tree (depends on the sizes only; 0 on invalid
+ * arguments, with gdn_last_error set). */
+size_t gdn_attn_tree_workspace_size(const gdn_attn_config* cfg, int32_t B, int32_t max_nodes,
+                                    int32_t max_ctx_len);
+
+/* Tree verify of the DeltaNet layer: y of every node, its state being its parent's
+ * (the slot's state for a first node) after the node's token.  The conv window of a node
+ * is its line's last d_conv raw inputs, continued into the slot's conv state.
+ * The pools are not written.  Two trees may read the same slot.
+ *   x act [n_nodes][C_ch], z, y act [n_nodes][H_v*d_v], a, b act [n_nodes][H_v];
+ *   x, z and y 16-byte aligned; conv_pool, state_pool, slot_idx [B] as in gdn_verify_rows_nosnap
+ *   (a tree whose slot index is out of range is skipped); max_nodes: host bound
+ *   on every n_b, 1 .. GDN_TREE_MAX_NODES. */
+gdn_status gdn_verify_tree(const gdn_config* cfg, const gdn_params* prm, const void* x,
+                           const void* z, const void* a, const void* b, const void* conv_pool,
+                           const float* state_pool, const int32_t* slot_idx,
+                           const int32_t* cu_nodes, const int32_t* parents, int32_t B,
+                           int32_t n_nodes, int32_t max_nodes, int32_t n_slots, void* y,
+                           void* stream);
+
+/* Commit of accepted paths: rows src_rows[cu_rows[b]] .. src_rows[cu_rows[b+1] - 1] of
+ * x, a and b (the arrays given to gdn_verify_tree) are applied in that order to
+ * the state and conv state of slot_idx[b], in place, as that many decode steps would
+ * (no y is made).  src_rows NULL: row cu_rows[b] + t itself, e.g. drafted
+ * chains of different accepted lengths.
+ *   cu_rows int32 [B+1], src_rows int32 [n_rows] (device; gdn_page_tables writes both);
+ *   n_src: rows of x; an entry of src_rows outside [0, n_src) is passed over.
+ *   max_rows: host bound on a sequence's rows, 1 .. GDN_TREE_MAX_NODES; a
+ *   sequence with more, with none, or with rows outside [0, n_rows) keeps its state, as does one
+ *   whose slot index is out of range.  Slots must be distinct (GDN_DEBUG checks). */
+gdn_status gdn_commit_tree(const gdn_config* cfg, const gdn_params* prm, const void* x,
+                           const void* a, const void* b, void* conv_pool, float* state_pool,
+                           const int32_t* slot_idx, const int32_t* cu_rows,
+                           const int32_t* src_rows, int32_t B, int32_t n_rows, int32_t n_src,
+                           int32_t max_rows, int32_t n_slots, void* stream);
+
+/* ---- Pages and row maps from request lengths ------------------------------------
+ * Sequence b holds ctx_lens[b] tokens in the cache and brings new_lens[b] more (a
+ * prompt's, or the accepted ones of a verify).  The call takes the pages they need from
+ * a list of free ones, writes them into the block table, and lists every new
+ * token's row of the cache, all on the device.
+ *   free_pages int32 [n_free]: page ids; head int32 [1]: how many of them are
+ *   taken already; head_out int32 [1]: how many are after the call (another address than
+ *   head).  Pages are taken in the order of the list, sequence by sequence.
+ *   block_table int32 [B][max_pages]: entries ceil(ctx/page_size) ..
+ *   ceil((ctx+new)/page_size) - 1 of a granted sequence are written, no others.
+ *   cu_rows int32 [B+1]: first row of each sequence; a sequence that is not granted has
+ *   no rows.  slot_map int64 [n_rows]: for row cu_rows[b] + i the cache row page *
+ *   page_size + (ctx + i) % page_size, -1 where the page id lies outside [0, n_pages)
+ *   and on every row from cu_rows[B] on.
+ *   A sequence is granted iff its lengths are >= 0, ctx + new fits max_pages
+ *   pages (and new <= path_len where a path is given), and the pages and the rows
+ *   that it and all sequences before it ask for (the refused ones included, those
+ *   that fail the first condition not) fit the list and n_rows; one that needs no new page
+ *   is not refused for pages.  So a list that runs out refuses sequences from that
+ *   one on, and no page is taken for them.
+ *   path int32 [B][path_len], cu_nodes int32 [B+1], src_rows int32 [n_rows] (all
+ *   or none): path[b][0 .. new-1] are the accepted nodes of b's tree in order, and
+ *   src_rows[cu_rows[b] + i] = cu_nodes[b] + path[b][i], -1 where the node is outside the
+ *   tree and past the last row.
+ *   page_size here is any positive number; slot_map must be 8-byte aligned. */
+gdn_status gdn_page_tables(int32_t page_size, int32_t n_pages, const int32_t* ctx_lens,
+                           const int32_t* new_lens, int32_t B, const int32_t* free_pages,
+                           int32_t n_free, const int32_t* head, int32_t* block_table,
+                           int32_t max_pages, int32_t* cu_rows, int64_t* slot_map, int32_t n_rows,
+                           int32_t* head_out, const int32_t* path, int32_t path_len,
+                           const int32_t* cu_nodes, int32_t* src_rows, void* stream);
+
+/* K and V rows into the cache: row src_rows[i] (i where src_rows is NULL) of k_new
+ * and v_new goes to cache row slot_map[i] (page slot_map[i] / page_size, row
+ * slot_map[i] % page_size) of the pools, for all kv-heads.
+ *   k_new, v_new bf16 [n_src][n_kv_heads][head_dim]; slot_map int64 [n_rows],
+ *   src_rows int32 [n_rows] or NULL (device); pools as in gdn_attn_decode.  Rows with
+ *   slot_map[i] outside [0, n_pages * page_size) or a source outside [0, n_src) are passed over.
+ *   Rows that name the same cache row race.  cfg: n_q_heads and scale are not used. */
+gdn_status gdn_attn_append(const gdn_attn_config* cfg, const void* k_new, const void* v_new,
+                           int64_t n_src, const int64_t* slot_map, const int32_t* src_rows,
+                           int64_t n_rows, void* k_pool, void* v_pool, int32_t n_pages,
+                           void* stream);
+
 /* Message of the last failed call on this host thread ("" if none).  The
  * string stays valid until the next call on this thread. */
 const char* gdn_last_error(void);
