@@ -161,13 +161,14 @@ const char* gdn_version(void) { return "libgdn 0.1 (sm_103a)"; }
 gdn_status gdn_device_status(uint32_t* status) {
     if (!status) return fail(GDN_ERR_NULL, "status: found NULL, required a host pointer");
     unsigned a = 0, b = 0;
-    unsigned c = 0, d = 0, t = 0;
+    unsigned c = 0, d = 0, t = 0, u = 0;
     cudaError_t e = gdn::take_device_status_decode(&a);
     if (e == cudaSuccess) e = gdn::take_device_status_prefill(&b);
     if (e == cudaSuccess) e = gdn::take_device_status_proj(&c);
     if (e == cudaSuccess) e = gdn::take_device_status_chunk16(&d);
     if (e == cudaSuccess) e = gdn::take_device_status_tree(&t);
-    *status = a | b | c | d | t;
+    if (e == cudaSuccess) e = gdn::take_device_status_attn_tree(&u);
+    *status = a | b | c | d | t | u;
     return cuda_status(e, "gdn_device_status");
 }
 
@@ -747,8 +748,8 @@ static gdn_status max_check(const char* name, int32_t v) {
 
 size_t gdn_attn_tree_workspace_size(const gdn_attn_config* cfg, int32_t B, int32_t max_nodes, int32_t max_ctx_len) {
     if (attn_check(cfg) != GDN_OK) return 0;
-    if (B < 0 || B > 65535 || max_ctx_len < 0) {
-        fail(GDN_ERR_RANGE, "B/max_ctx_len: found %d/%d, required 0..65535/>= 0", B, max_ctx_len);
+    if (B < 0 || B > 65535 || max_ctx_len < 0 || max_ctx_len > 1 << 30) {
+        fail(GDN_ERR_RANGE, "B/max_ctx_len: found %d/%d, required 0..65535/0..2^30", B, max_ctx_len);
         return 0;
     }
     if (max_check("max_nodes", max_nodes)) return 0;
@@ -769,6 +770,10 @@ gdn_status gdn_attn_tree(const gdn_attn_config* cfg, const void* q, const void* 
     if (max_pages < 1 || n_pages < 1 || max_ctx_len < 0)
         return fail(GDN_ERR_RANGE, "max_pages/n_pages/max_ctx_len: found %d/%d/%d, required >= 1/>= 1/>= 0", max_pages,
                     n_pages, max_ctx_len);
+    if (max_ctx_len > 1 << 30) return fail(GDN_ERR_RANGE, "max_ctx_len: found %d, required <= 2^30", max_ctx_len);
+    if ((int64_t)n_pages * cfg->n_kv_heads > 0x7fffffff)  // a 32-bit coordinate of the copies
+        return fail(GDN_ERR_RANGE, "n_pages: found %d with %d kv-heads, required n_pages * n_kv_heads < 2^31", n_pages,
+                    cfg->n_kv_heads);
     if (B == 0 || n_nodes == 0) return ok();
     GDN_REQUIRE_PTR(q, "q");
     GDN_REQUIRE_PTR(k_new, "k_new");

@@ -1,78 +1,855 @@
 // gdn_attn_tree.cu -- attention of a tree of drafted tokens per sequence over its paged KV cache:
-// node i attends to the cached tokens 0 .. ctx - 1, to its ancestors and to itself.
+// node i attends to the cached tokens 0 .. ctx - 1, to its ancestors and to itself
+// ("Forge: how I wrote my own inference engine and overtook llama.cpp", 27 August: a draft is
+// verified as a chunk of rows over the cache; here the rows form a tree).
+//
+// The rows of a kv-head are the (node, query head) pairs of its group: up to 64 nodes x G heads, cut
+// into tiles of 128, the M of one tcgen05 product.  K and V are read once per row tile, and one row tile
+// holds everything up to 128 rows, so that short trees are bound by HBM (M flops per byte against a ridge of
+// about 280) and large ones by the tensor cores.
+//
+// Work: every (sequence, kv-head) is a list of key tiles (its context's, then one with the nodes
+// themselves); the lists are laid end to end and cut into equal runs, one per worker, whatever
+// the mix of context lengths.  A worker is RT CTAs, one per row tile, that walk the same run side by side,
+// so that the RT reads of a key tile meet in L2.  A list that lies in one run is finished by its
+// worker; one that is cut leaves (maximum, sum, unnormalised O) per part in the workspace and k_attn_tree_join
+// joins the parts in order (no atomics: results do not change from call to call).
 #include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
 
 #include "gdn_common.cuh"
 #include "gdn_internal.h"
+#include "gdn_tc.cuh"
 #include "gdn_tma.cuh"
 
 namespace gdn {
 namespace {
 
-// The simple form: a warp per (node, query head), lane = D / 32 consecutive dims, one key at
-// a time with a running maximum and sum.
+constexpr int kTreeCtas = 152;    // one CTA per SM
+constexpr int kTreeMinTiles = 4;  // fewest key tiles of a worker's run
+constexpr int kTreeWhole = 8;     // lists of up to this many tiles are not cut while every list has an SM
+
+struct AttnTreeArgs {
+    const __nv_bfloat16* q;      // [N][Hq][D]
+    const __nv_bfloat16* v_new;  // [N][Hkv][D]
+    const int32_t* block_table;  // [B][max_pages]
+    const int32_t* cu_nodes;
+    const int32_t* parents;
+    const int32_t* ctx_lens;
+    __nv_bfloat16* o;  // [N][Hq][D]
+    float* part;       // [worker][RT][2][D + 2][128]: O by columns, then maximum and sum
+    int B, Hq, Hkv, G, W, page, R, max_pages, n_pages, n_nodes, max_nodes, max_ctx;
+    int RT;             // CTAs of a worker: the most row tiles of a tree, or 1 where each row tile is a list of its own
+    int whole;          // > 0: worker w takes list w whole (few short lists: nothing to join), of this many per kv-head
+    float scale_log2;   // scale * log2(e)
+};
+
 template <int D>
-__global__ void __launch_bounds__(128) k_attn_tree(const __grid_constant__ AttnTreeJob J) {
-    constexpr int DPL = D / 32;
+struct TreeLay {
+    static constexpr int NCH = D / 64;             // 64-column chunks of a row (128 bytes)
+    static constexpr int BK = D == 256 ? 64 : 128; // keys per tile: 32 KB of K and 32 KB of V either way
+    static constexpr int GRP = NCH * 1024;         // 8 key rows: NCH swizzle atoms of 8 x 128 bytes
+    static constexpr int TILE = BK / 8 * GRP;
+    static constexpr int QATOM = 128 * 128;
+    static constexpr int Q = 0;                    // [chunk][128 rows][128 bytes], swizzled
+    static constexpr int K = Q + NCH * QATOM;      // 2 stages, [8-row group][chunk][8][128 bytes], swizzled
+    static constexpr int V = K + 2 * TILE;         // 2 stages, the same layout
+    static constexpr int BAR = V + 2 * TILE;
+    static constexpr int GONE = BAR + 24 * 8;      // 4 slots: runs of a tile without keys
+    static constexpr int BAD = GONE + 4 * 8;       // 4 slots: nodes with an infinite or NaN value
+    static constexpr int ANC = BAD + 4 * 8;        // 4 slots: line of each node (64-bit masks)
+    static constexpr int UP = ANC + 4 * 64 * 8;
+    static constexpr int SMEM_ALLOC = UP + 64 * 4 + 1024;
+    static constexpr int O_COL = 2 * BK;           // TMEM: S of two tiles, O, P of two tiles (2 bf16 to a column)
+    static constexpr int P_COL = O_COL + D;
+    static constexpr int TMEM_COLS = 512;
+    static_assert(P_COL + BK <= TMEM_COLS, "TMEM");
+    static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory");
+};
+
+// sequence b: rows, context and key tiles (0: skipped)
+template <int BK>
+__device__ __forceinline__ int tree_tiles(const AttnTreeArgs& A, int b, int& first, int& n, int& ctx) {
+    first = A.cu_nodes[b];
+    const long long cnt = (long long)A.cu_nodes[b + 1] - first;
+    ctx = A.ctx_lens[b];
+    if (first < 0 || cnt < 1 || cnt > A.max_nodes || first + cnt > A.n_nodes || ctx < 0 || ctx > A.max_ctx ||
+        ctx > (long long)A.max_pages * A.page) {
+        n = 0;
+        return 0;
+    }
+    n = (int)cnt;
+    return (ctx + BK - 1) / BK + 1;
+}
+
+// lists of a sequence: its kv-heads, times its row tiles where these are lists of their own
+__device__ __forceinline__ int tree_lists(const AttnTreeArgs& A, int n) {
+    return A.RT > 1 ? A.Hkv : A.Hkv * ((n * A.G + 127) / 128);
+}
+
+// where worker w's run [start, end) begins: list (b, kv-head), tile t of nt.  All threads of the block call it.
+struct TreeRun {
+    long long start, end, per;
+    int b;
+    long long rem;  // start - first tile of sequence b's lists
+};
+
+template <int D, int THREADS>
+__device__ __forceinline__ TreeRun tree_run(const AttnTreeArgs& A, int w) {
+    constexpr int BK = TreeLay<D>::BK;
+    __shared__ long long s_warp[THREADS / 32], s_rem;
+    __shared__ int s_b;
+    TreeRun run;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int first, n, ctx;
+    if (A.whole) {  // (RT 1: A.whole row tiles of each kv-head)
+        run.b = w / (A.Hkv * A.whole);
+        const int nt = tree_tiles<BK>(A, run.b, first, n, ctx), at = w % (A.Hkv * A.whole);
+        run.per = nt;
+        run.start = 0;
+        run.end = at < tree_lists(A, n) ? nt : 0;
+        run.rem = (long long)at * nt;
+        return run;
+    }
+    // each thread sums a run of sequences; a scan of the threads' sums finds the one that holds the start
+    const int each = (A.B + THREADS - 1) / THREADS;
+    const int b0 = min(A.B, tid * each), b1 = min(A.B, b0 + each);
+    long long sum = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int nt = tree_tiles<BK>(A, b, first, n, ctx);
+        sum += (long long)nt * tree_lists(A, n);
+    }
+    long long incl = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += v;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    if (tid == 0) s_b = 0;
+    __syncthreads();
+    long long total = 0, before = 0;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
+        if (i < warp) before += s_warp[i];
+        total += s_warp[i];
+    }
+    run.per = max((long long)kTreeMinTiles, (total + A.W - 1) / A.W);
+    run.start = min(total, w * run.per);
+    run.end = min(total, run.start + run.per);
+    long long at = before + incl - sum;
+    if (run.start < run.end && at <= run.start && run.start < at + sum) {
+        for (int b = b0; b < b1; ++b) {
+            const int nt = tree_tiles<BK>(A, b, first, n, ctx);
+            const long long t = (long long)nt * tree_lists(A, n);
+            if (run.start < at + t) {
+                s_b = b;
+                s_rem = run.start - at;
+                break;
+            }
+            at += t;
+        }
+    }
+    __syncthreads();
+    run.b = s_b;
+    run.rem = s_rem;
+    return run;
+}
+
+// one piece of a worker's run: tiles t0 .. t1 - 1 of the nt of list (b, kvh), rows 128 rt ..
+struct TreeSeg {
+    int b, kvh, rt, t0, t1, nt, first, n, ctx;
+};
+
+template <int BK>
+struct TreeWalk {
+    const AttnTreeArgs& A;
+    int b, rt;
+    long long rem, left;
+    __device__ TreeWalk(const AttnTreeArgs& a, const TreeRun& r, int row_tile)
+        : A(a), b(r.b), rt(row_tile), rem(r.rem), left(r.end - r.start) {}
+    __device__ bool next(TreeSeg& s) {
+        while (left > 0 && b < A.B) {
+            s.nt = tree_tiles<BK>(A, b, s.first, s.n, s.ctx);
+            const int lists = tree_lists(A, s.n);
+            if (s.nt == 0 || rem >= (long long)s.nt * lists) {
+                rem = 0;
+                ++b;
+                continue;
+            }
+            const int list = (int)(rem / s.nt), per_head = lists / A.Hkv;
+            s.b = b;
+            s.kvh = list / per_head;
+            s.rt = A.RT > 1 ? rt : list % per_head;
+            s.t0 = (int)(rem - (long long)list * s.nt);
+            s.t1 = (int)min((long long)s.nt, s.t0 + left);
+            left -= s.t1 - s.t0;
+            rem += s.t1 - s.t0;
+            return true;
+        }
+        return false;
+    }
+};
+
+__device__ __forceinline__ uint64_t tree_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFF);
+    d |= (uint64_t)((lbo >> 4) & 0x3FFF) << 16;
+    d |= (uint64_t)((sbo >> 4) & 0x3FFF) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;  // 128-byte swizzle
+    return d;
+}
+
+__device__ __forceinline__ float tree_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void tree_tma_5d(void* dst, const CUtensorMap* map, int row8, int line, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3, "
+        "%4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row8), "r"(line), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void tree_tma_4d(void* dst, const CUtensorMap* map, int row, int head, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %2, %4}], "
+        "[%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(head), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// The warp that issues products runs converged and one elected lane issues: 48 cycles an instruction at N = 64,
+// the rate of the product itself (67 from a branch on the lane index, 82 with a predicate on each instruction).
+__device__ __forceinline__ bool tree_elect() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+    return r != 0;
+}
+// a product with A in TMEM (lane = row, two bf16 of K to a 32-bit column)
+__device__ __forceinline__ void tree_mma_ta(uint32_t d, uint32_t a, uint64_t bd, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(a), "l"(bd), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// 32 consecutive columns of this warp's lanes, no wait
+__device__ __forceinline__ void tree_st32(uint32_t ta, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(ta),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+// one column of this warp's lanes
+__device__ __forceinline__ uint32_t tree_ld1(uint32_t ta) {
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n tcgen05.wait::ld.sync.aligned;" : "=r"(r) : "r"(ta) : "memory");
+    return r;
+}
+
+// 16 bytes from global to shared memory, or 16 zeros
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
+// an infinity or NaN among the two bf16 of a word (all exponent bits set), as a mask of the halves
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t u) {
+    return ((u & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) | ((u & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
+}
+
+// Warp 0 loads K tiles, warp 6 V tiles (and works out the nodes' lines), warp 1 issues the products, warps 2..5
+// (thread = row) do the softmax and the epilogue.  Tile `it` of the CTA uses stage, S and P buffer and barrier it & 1:
+//   full_k, full_v   the tile's copies have landed
+//   s_done           S = Q K^T is in TMEM (and K's stage is free, and P V of tile it - 2 done)
+//   s_read           the softmax has S in registers (and S's buffer is free)
+//   p_ready          P is in TMEM, O is rescaled, V has no row without a key
+//   pv_done          O += P V is done (V's stage is free)
+// S of tile it + 1 is issued before P V of tile it, so the tensor cores work while the softmax does.
+// Every wait is bounded: a role that gives up stops waiting, and the CTA still runs to its end.
+template <int D>
+__global__ void __launch_bounds__(224, 1)
+    k_attn_tree(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                const __grid_constant__ CUtensorMap tkn, const __grid_constant__ CUtensorMap tvn,
+                const __grid_constant__ AttnTreeArgs A) {
+    using Ly = TreeLay<D>;
+    constexpr int NCH = Ly::NCH, BK = Ly::BK;
     griddep_wait();  // launched with programmatic serialization
     griddep_launch_dependents();
-    const int i = blockIdx.x, h = blockIdx.y * 4 + (threadIdx.x >> 5), b = blockIdx.z, lane = threadIdx.x & 31;
-    const int64_t first = J.cu_nodes[b];
-    const int64_t n = (int64_t)J.cu_nodes[b + 1] - first;
-    const int ctx = J.ctx_lens[b];
-    if (first < 0 || n < 1 || n > J.max_nodes || first + n > J.n_nodes || ctx < 0 || ctx > J.max_ctx ||
-        ctx > (int64_t)J.max_pages * J.page || i >= n || h >= J.Hq)
-        return;
-    const int G = J.Hq / J.Hkv, kvh = h / G;
-    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(J.q) + ((first + i) * J.Hq + h) * D + lane * DPL;
-    float qv[DPL], o[DPL], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int e = 0; e < DPL; ++e) {
-        qv[e] = __bfloat162float(q[e]) * J.scale;
-        o[e] = 0.f;
+    const int w = blockIdx.x / A.RT;
+    const TreeRun run = tree_run<D, 224>(A, w);
+    if (run.start >= run.end) return;  // (the same for all threads)
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* sm = smem_raw + ((1024 - (tc::smem_addr(smem_raw) & 1023)) & 1023);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Ly::BAR);
+    uint64_t *full_k = bars, *full_v = bars + 2, *s_done = bars + 4, *s_read = bars + 6, *pv_done = bars + 8,
+             *p_ready = bars + 10, *anc_ready = bars + 12, *q_ready = bars + 14, *gone_ready = bars + 16;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 20);
+    unsigned* s_gone = reinterpret_cast<unsigned*>(sm + Ly::GONE);
+    unsigned long long* s_bad = reinterpret_cast<unsigned long long*>(sm + Ly::BAD);
+    unsigned long long* s_anc = reinterpret_cast<unsigned long long*>(sm + Ly::ANC);
+    int* s_up = reinterpret_cast<int*>(sm + Ly::UP);
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(full_k + i, 1);
+            mbar_init(full_v + i, 1);
+            mbar_init(s_done + i, 1);
+            mbar_init(s_read + i, 4);  // one arrival per softmax warp
+            mbar_init(pv_done + i, 1);
+            mbar_init(p_ready + i, 4);
+            mbar_init(anc_ready + i, 1);
+        }
+        for (int i = 0; i < 4; ++i) mbar_init(gone_ready + i, 1);
+        mbar_init(q_ready, 4);
+        fence_mbar_init();
     }
-    auto take = [&](const __nv_bfloat16* k, const __nv_bfloat16* v) {
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < DPL; ++e) s = fmaf(qv[e], __bfloat162float(k[lane * DPL + e]), s);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        const float mn = fmaxf(m, s);
-        const float f = m == -INFINITY ? 0.f : __expf(m - mn);
-        const float p = __expf(s - (mn == -INFINITY ? 0.f : mn));
-        l = l * f + p;
-        m = mn;
-#pragma unroll
-        for (int e = 0; e < DPL; ++e) o[e] = fmaf(p, __bfloat162float(v[lane * DPL + e]), o[e] * f);
+    if (warp == 1) tc::alloc(tslot, Ly::TMEM_COLS);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tm = *tslot;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, int phase) {  // warp-wide; after a failure nothing waits any more
+        if (ok && !__all_sync(0xffffffffu, mbar_test(bar, (uint32_t)(phase & 1))))
+            ok = __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)(phase & 1)));
+        return ok;
     };
-    const __nv_bfloat16* kp = static_cast<const __nv_bfloat16*>(J.k_pool);
-    const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(J.v_pool);
-    for (int t = 0; t < ctx; ++t) {
-        const int id = J.block_table[(size_t)b * J.max_pages + t / J.page];
-        if (id < 0 || id >= J.n_pages) continue;
-        const size_t at = (((size_t)id * J.Hkv + kvh) * J.page + t % J.page) * D;
-        take(kp + at, vp + at);
-    }
-    for (int a = i; a >= 0;) {
-        const size_t at = ((size_t)(first + a) * J.Hkv + kvh) * D;
-        take(static_cast<const __nv_bfloat16*>(J.k_new) + at, static_cast<const __nv_bfloat16*>(J.v_new) + at);
-        const int p = J.parents[first + a];
-        a = p >= 0 && p < a ? p : -1;
-    }
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(J.o) + ((size_t)(first + i) * J.Hq + h) * D + lane * DPL;
+
+    // key tile j of a segment: lane i looks up the page of its run of R rows; -1: no such run, past the context, or a
+    // page outside the pool
+    const int nseg = BK / A.R;
+    auto lane_page = [&](const TreeSeg& s, int j) -> int {
+        const int pos = j * BK + lane * A.R;
+        if (lane >= nseg || j >= s.t1 || pos >= s.ctx) return -1;
+        const int pid = __ldg(A.block_table + (size_t)s.b * A.max_pages + pos / A.page);
+        return (pid >= 0 && pid < A.n_pages) ? pid : -1;
+    };
+    // keys of tile j, and their steps of 16 in P V (rows past the last step are not read)
+    auto keys_of = [&](const TreeSeg& s, int j) { return j == s.nt - 1 ? s.n : min(BK, s.ctx - j * BK); };
+    TreeWalk<BK> walk(A, run, blockIdx.x % A.RT);
+    TreeSeg s;
+    auto next = [&](TreeSeg& t) {  // the next piece with rows for this CTA
+        do {
+            if (!walk.next(t)) return false;
+        } while (t.rt * 128 >= t.n * A.G);
+        return true;
+    };
+
+    if (warp == 0 || warp == 6) {
+        // ---- K or V tiles into the two stages -------------------------------------------
+        const bool is_k = warp == 0;
+        const CUtensorMap* pool_map = is_k ? &tk : &tv;
+        const CUtensorMap* new_map = is_k ? &tkn : &tvn;
+        unsigned char* ring = sm + (is_k ? Ly::K : Ly::V);
+        uint64_t *full = is_k ? full_k : full_v, *freed = is_k ? s_done : pv_done;
+        int it = 0, tails = 0;
+        while (ok && next(s)) {
+            int pid_next = lane_page(s, s.t0);
+            for (int j = s.t0; j < s.t1; ++j, ++it) {
+                const int pid = pid_next;
+                pid_next = lane_page(s, j + 1);
+                const int st = it & 1;
+                if (it >= 2 && !wait(freed + st, (it - 2) >> 1)) break;
+                unsigned char* dst = ring + st * Ly::TILE;
+                const unsigned have = __ballot_sync(0xffffffffu, pid >= 0);
+                if (is_k && lane == 0) {  // (s_done(it - 2): the softmax has read the slot of tile it - 4)
+                    s_gone[it & 3] = ~have;
+                    mbar_arrive(gone_ready + (it & 3));
+                }
+                if (j < s.nt - 1) {
+                    if (lane == 0) mbar_arrive_expect_tx(full + st, (uint32_t)(__popc(have) * A.R * D * 2));
+                    __syncwarp();
+                    if (pid >= 0)
+                        tree_tma_5d(dst + lane * (A.R / 8) * Ly::GRP, pool_map, (j * BK + lane * A.R) % A.page / 8,
+                                    pid * A.Hkv + s.kvh, full + st);
+                    continue;
+                }
+                const int groups = (s.n + 7) / 8;
+                if (lane == 0) mbar_arrive_expect_tx(full + st, (uint32_t)(groups * 8 * D * 2));
+                __syncwarp();
+                if (lane < groups) tree_tma_4d(dst + lane * Ly::GRP, new_map, s.first + 8 * lane, s.kvh, full + st);
+                if (is_k) continue;
+                // the line of every node: six rounds of doubling, two nodes to a lane.  Slots are used in turn: the
+                // segment that used this one four tails ago was finished before pv_done(it - 2)
+                unsigned long long* anc = s_anc + (tails & 3) * 64;
 #pragma unroll
-    for (int e = 0; e < DPL; ++e) dst[e] = __float2bfloat16_rn(o[e] / l);
+                for (int e = 0; e < 2; ++e) {
+                    const int i = 32 * e + lane;
+                    int up = -1;
+                    if (i < s.n) {
+                        const int p = A.parents[s.first + i];
+                        up = p >= 0 && p < i ? p : -1;
+                    }
+                    s_up[i] = up;
+                    anc[i] = i < s.n ? 1ull << i : 0ull;
+                }
+                if (lane == 0) s_bad[tails & 3] = 0ull;
+                __syncwarp();
+                for (int step = 0; step < 6; ++step) {
+                    unsigned long long m[2];
+                    int up[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int i = 32 * e + lane, p = s_up[i];
+                        m[e] = anc[i] | (p >= 0 ? anc[p] : 0ull);
+                        up[e] = p >= 0 ? s_up[p] : -1;
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        anc[32 * e + lane] = m[e];
+                        s_up[32 * e + lane] = up[e];
+                    }
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive(anc_ready + (tails & 1));
+                ++tails;
+            }
+        }
+        // copies still in flight land before the CTA leaves
+        for (int i = max(0, it - 2); i < it; ++i) mbar_wait(full + (i & 1), (uint32_t)((i >> 1) & 1));
+    } else if (warp == 1) {
+        constexpr uint32_t idesc_s = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(BK >> 3) << 17) |
+                                     ((uint32_t)(128 >> 4) << 24);
+        constexpr uint32_t idesc_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
+                                     ((uint32_t)(128 >> 4) << 24);
+        // descriptors: only the start address (in 16-byte units, the low bits) changes
+        const uint64_t dq = tc::sdesc(tc::smem_addr(sm + Ly::Q)), dk = tree_desc(tc::smem_addr(sm + Ly::K), 16, Ly::GRP),
+                       dv = tree_desc(tc::smem_addr(sm + Ly::V), 1024, Ly::GRP);
+        // O (+)= P V of tile i with `steps` steps of 16 keys; fresh: the segment's first, which replaces O
+        auto pv = [&](int i, int steps, bool fresh) -> bool {
+            const int st = i & 1;
+            if (!wait(p_ready + st, i >> 1) || !wait(full_v + st, i >> 1)) return false;
+            tc::fence_after();
+            const uint32_t pa = tm + Ly::P_COL + st * (BK / 2);
+            const uint64_t vb = dv + ((uint32_t)(st * Ly::TILE) >> 4);
+            if (tree_elect()) {
+#pragma unroll
+                for (int kk = 0; kk < BK / 16; ++kk)
+                    if (kk < steps)
+                        tree_mma_ta(tm + Ly::O_COL, pa + 8 * kk, vb + (uint32_t)((2 * kk * Ly::GRP) >> 4), idesc_o,
+                                    (!fresh || kk > 0) ? 1u : 0u);
+                tc::commit(pv_done + st);
+            }
+            __syncwarp();
+            return true;
+        };
+        int it = 0, seg = 0, steps = 0;
+        bool fresh = false;  // the pending tile is its segment's first
+        while (ok && next(s)) {
+            // the segment before ends: its last P V, then the softmax warps finish it and bring the new Q
+            if (it > 0 && !pv(it - 1, steps, fresh)) break;
+            if (!wait(q_ready, seg)) break;
+            ++seg;
+            for (int j = s.t0; j < s.t1; ++j, ++it) {
+                const int st = it & 1;
+                if (!wait(full_k + st, it >> 1) || (it >= 2 && !wait(s_read + st, (it - 2) >> 1))) break;
+                tc::fence_after();
+                const uint64_t kb = dk + ((uint32_t)(st * Ly::TILE) >> 4);
+                if (tree_elect()) {
+#pragma unroll
+                    for (int kd = 0; kd < D / 16; ++kd)
+                        tc::mma_f16(tm + st * BK, dq + (uint32_t)(((kd >> 2) * Ly::QATOM + (kd & 3) * 32) >> 4),
+                                    kb + (uint32_t)(((kd >> 2) * 1024 + (kd & 3) * 32) >> 4), idesc_s, kd > 0 ? 1u : 0u);
+                    tc::commit(s_done + st);
+                }
+                __syncwarp();
+                if (j > s.t0 && !pv(it - 1, steps, fresh)) break;
+                fresh = j == s.t0;
+                steps = (keys_of(s, j) + 15) / 16;
+            }
+        }
+        if (ok && it > 0) pv(it - 1, steps, fresh);
+    } else {
+        // ---- softmax and epilogue: thread = row r of the tile (TMEM lane r) ----------------
+        const int q4 = warp & 3, r = 32 * q4 + lane;
+        const uint32_t trow = tc::taddr(tm, 32 * q4, 0);
+        const unsigned run_bits = nseg == 32 ? 0xffffffffu : (1u << nseg) - 1u;
+        int it = 0, tails = 0;
+        // Q of the tile's rows, a row (or two of D = 128) per step, all copies in flight at once.  Rows past the
+        // tree are zeros
+        auto load_q = [&](const TreeSeg& t) {
+            constexpr int CPR = D / 8, RPS = 32 / CPR;  // 16-byte pieces of a row, rows per step
+            const int c = lane % CPR;
+            int row = 32 * q4 + lane / CPR, qn = (t.rt * 128 + row) / A.G, qg = (t.rt * 128 + row) % A.G;
+            const __nv_bfloat16* src = A.q + ((size_t)t.first * A.Hq + t.kvh * A.G) * D + c * 8;
+            const uint32_t dst = smem_u32(sm + Ly::Q + (c >> 3) * Ly::QATOM);
+#pragma unroll 4
+            for (int i = 0; i < 32; i += RPS, row += RPS, qg += RPS) {
+                while (qg >= A.G) {
+                    qg -= A.G;
+                    ++qn;
+                }
+                const bool there = qn < t.n;
+                cp_async16_or_zero(dst + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+                                   there ? src + ((size_t)qn * A.Hq + qg) * D : A.q, there);
+            }
+            cp_async_commit();
+        };
+        bool have = next(s);
+        if (have) load_q(s);
+        while (have) {
+            TreeSeg after;
+            const bool more = next(after);
+            const int node = (s.rt * 128 + r) / A.G, g = (s.rt * 128 + r) % A.G;
+            const bool row_ok = node < s.n;
+            const bool warp_ok = s.rt * 128 + 32 * q4 < s.n * A.G;  // a row of this warp exists
+            const bool tail = s.t1 == s.nt;                       // the segment ends with the nodes' own keys
+            cp_async_wait_all();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_ready);
+            float m_ref = -INFINITY, l = 0.f;
+            unsigned long long mine = 0ull;  // the row's line
+            for (int j = s.t0; j < s.t1; ++j, ++it) {
+                const int st = it & 1;
+                const bool own_keys = j == s.nt - 1;
+                wait(gone_ready + (it & 3), it >> 2);
+                // runs of the tile without keys (a page outside the pool or past the context)
+                const unsigned gone = s_gone[it & 3] & run_bits;
+                wait(s_done + st, it >> 1);
+                tc::fence_after();
+                float sv[BK];
+                if (warp_ok) {
+                    uint32_t raw[BK];
+#pragma unroll
+                    for (int c = 0; c < BK; c += 32) tc::ld32_nowait(trow + st * BK + c, raw + c);
+                    tc::ld_wait();
+#pragma unroll
+                    for (int c = 0; c < BK; ++c) sv[c] = __uint_as_float(raw[c]);
+                }
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_read + st);
+                if (j == s.t1 - 1 && more) load_q(after);  // every product with this segment's Q is done
+                const int keys = keys_of(s, j);
+                const bool full = !own_keys && gone == 0u && keys == BK;
+                if (own_keys) {
+                    wait(anc_ready + (tails & 1), tails >> 1);
+                    if (row_ok) mine = s_anc[(tails & 3) * 64 + node];
+                }
+                float f = 1.f;
+                uint32_t pk[BK / 2];
+                if (warp_ok) {
+                    if (!full) {
+                        uint32_t seen[BK / 32];  // bit c: key c reaches this row
+                        if (own_keys) {
+#pragma unroll
+                            for (int c = 0; c < BK / 32; ++c) seen[c] = c < 2 ? (uint32_t)(mine >> (32 * c)) : 0u;
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < BK / 32; ++c) {
+                                const int k = keys - 32 * c;
+                                seen[c] = k >= 32 ? 0xffffffffu : (k <= 0 ? 0u : (1u << k) - 1u);
+                                for (int e = 0; e < 32; e += 8)  // runs are multiples of 8 keys
+                                    if ((gone >> ((32 * c + e) / A.R)) & 1u) seen[c] &= ~(0xffu << e);
+                            }
+                        }
+#pragma unroll
+                        for (int c = 0; c < BK; ++c) sv[c] = (seen[c >> 5] >> (c & 31)) & 1u ? sv[c] : -INFINITY;
+                    }
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // four chains: a warp has its scheduler alone
+#pragma unroll
+                    for (int c = 0; c < BK; ++c) mx[c & 3] = fmaxf(mx[c & 3], sv[c]);
+                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    // the reference maximum moves when the row's maximum passes it by more than 2^8 in the exponent
+                    if (mt > -INFINITY && (m_ref == -INFINITY || (mt - m_ref) * A.scale_log2 > 8.f)) {
+                        if (m_ref > -INFINITY) {
+                            f = exp2f((m_ref - mt) * A.scale_log2);
+                            l *= f;
+                        }
+                        m_ref = mt;
+                    }
+                    // p = 2^((s - m_ref) scale log2 e), rounded to bf16, the tensor cores' operand; the sum takes the
+                    // rounded weights, like the product
+                    const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref * A.scale_log2;
+                    const float2 sc2 = make_float2(A.scale_log2, A.scale_log2), nm2 = make_float2(neg_m, neg_m);
+                    float2 sum[4] = {};
+#pragma unroll
+                    for (int e = 0; e < BK / 2; ++e) {
+                        const float2 x = __ffma2_rn(make_float2(sv[2 * e], sv[2 * e + 1]), sc2, nm2);
+                        const __nv_bfloat162 h2 = __floats2bfloat162_rn(tree_ex2(x.x), tree_ex2(x.y));
+                        sum[e & 3] = __fadd2_rn(sum[e & 3], __bfloat1622float2(h2));
+                        pk[e] = *reinterpret_cast<const uint32_t*>(&h2);
+                    }
+                    l += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) + ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
+                }
+                // P's buffer is free: S of this tile was issued after P V of tile it - 2, so s_done covers both
+                if (warp_ok) {
+#pragma unroll
+                    for (int c = 0; c < BK / 2; c += 32) tree_st32(trow + Ly::P_COL + st * (BK / 2) + c, pk + c);
+                    if (j > s.t0 && __any_sync(0xffffffffu, f != 1.f)) {  // TMEM accesses are warp-wide
+                        wait(pv_done + (st ^ 1), (it - 1) >> 1);
+                        tc::fence_after();
+#pragma unroll 1
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+                            float ov[32];
+                            tc::ld32(trow + Ly::O_COL + c0, ov);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) ov[c] *= f;
+                            tree_st32(trow + Ly::O_COL + c0, reinterpret_cast<const uint32_t*>(ov));
+                        }
+                    }
+                    tc::st_wait();
+                }
+                if (!full) {
+                    // a row of V without a key is cleared (up to the last step of 16), so that 0 x whatever it holds
+                    // never reaches O; of the nodes' own rows the infinities and NaN are taken out too and added again
+                    // at the end, for the nodes that see them.  The tile lies in order of rows, 8 at a time
+                    wait(full_v + st, it >> 1);
+                    uint4* vt = reinterpret_cast<uint4*>(sm + Ly::V + st * Ly::TILE);
+                    const int upto = (keys + 15) / 16 * 16 * (NCH * 8);
+                    for (int i = r; i < upto; i += 128) {
+                        const int row = i / (NCH * 64) * 8 + (i & 63) / 8;
+                        if (row >= keys || (!own_keys && ((gone >> (row / A.R)) & 1u))) {
+                            vt[i] = make_uint4(0u, 0u, 0u, 0u);
+                        } else if (own_keys) {
+                            const uint4 u = vt[i];
+                            const uint4 x = make_uint4(nonfinite2(u.x), nonfinite2(u.y), nonfinite2(u.z), nonfinite2(u.w));
+                            if (x.x | x.y | x.z | x.w) {
+                                vt[i] = make_uint4(u.x & ~x.x, u.y & ~x.y, u.z & ~x.z, u.w & ~x.w);
+                                atomicOr(s_bad + (tails & 3), 1ull << row);
+                            }
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_ready + st);
+            }
+            // ---- the segment's O: o itself, or a part to be joined -----------------------------
+            wait(pv_done + ((it - 1) & 1), (it - 1) >> 1);
+            tc::fence_after();
+            unsigned long long bad = 0ull, any_bad = 0ull;
+            if (tail) {
+                named_bar_sync(1, 128);
+                any_bad = s_bad[tails & 3];
+                bad = any_bad & mine;
+                ++tails;
+            }
+            const bool complete = s.t0 == 0 && tail;
+            const float inv = 1.f / l;  // (a row without any weight is 0 / 0)
+            __nv_bfloat16* dst = A.o + ((size_t)(s.first + node) * A.Hq + s.kvh * A.G + g) * D;
+            float* part = A.part + (size_t)(blockIdx.x * 2 + (s.t0 > 0 ? 0 : 1)) * (D + 2) * 128 + r;
+            if (warp_ok && ok) {
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    float ov[32];
+                    tc::ld32(trow + Ly::O_COL + c0, ov);
+                    for (unsigned long long m = any_bad; m; m &= m - 1) {  // (the same for all lanes)
+                        const int a = __ffsll((long long)m) - 1;
+                        const uint32_t two = tree_ld1(trow + Ly::P_COL + ((it - 1) & 1) * (BK / 2) + a / 2);
+                        const float p = __uint_as_float(a & 1 ? two & 0xffff0000u : two << 16);
+                        const __nv_bfloat16* v = A.v_new + ((size_t)(s.first + a) * A.Hkv + s.kvh) * D + c0;
+                        if ((bad >> a) & 1ull) {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) {
+                                const float x = __bfloat162float(v[c]);
+                                if (!isfinite(x)) ov[c] = fmaf(p, x, ov[c]);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (complete) {
+                        uint4 out[4];
+                        __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(out);
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) h[c] = __floats2bfloat162_rn(ov[2 * c] * inv, ov[2 * c + 1] * inv);
+                        if (row_ok) {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) reinterpret_cast<uint4*>(dst + c0)[c] = out[c];
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) part[(c0 + c) * 128] = ov[c];
+                    }
+                    __syncwarp();
+                }
+                if (!complete) {
+                    part[D * 128] = m_ref;
+                    part[(D + 1) * 128] = l;
+                }
+            }
+            __syncwarp();
+            s = after;
+            have = more;
+        }
+    }
+    tc::fence_before();
+    __syncthreads();
+    if (!ok && lane == 0) report_device_status(kDevWaitTimeout);
+    if (warp == 1) tc::dealloc(tm, Ly::TMEM_COLS);
+}
+
+// One CTA per (worker w, row tile, 32 columns); thread = row.  If w's run begins inside a list whose first part is
+// worker w - 1's, it joins the parts of that list: o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
+template <int D>
+__global__ void __launch_bounds__(128) k_attn_tree_join(const __grid_constant__ AttnTreeArgs A) {
+    constexpr int BK = TreeLay<D>::BK, COLS = 32;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int w = blockIdx.x / A.RT + 1, sub = blockIdx.x % A.RT, c0 = blockIdx.y * COLS, r = threadIdx.x;
+    const TreeRun run = tree_run<D, 128>(A, w);
+    if (run.start >= run.end) return;
+    TreeSeg s;
+    TreeWalk<BK> walk(A, run, sub);
+    walk.next(s);
+    const long long begin = run.start - s.t0;  // the list's first tile
+    if (s.t0 == 0 || begin / run.per != w - 1) return;
+    const int last = (int)((begin + s.nt - 1) / run.per);
+    const int at = s.rt * 128 + r;
+    if (at >= s.n * A.G) return;
+    auto part = [&](int i) {  // worker i's part: its run ends with the list's beginning, or begins inside it
+        return A.part + (size_t)((i * A.RT + sub) * 2 + (i == w - 1 ? 1 : 0)) * (D + 2) * 128 + r;
+    };
+    float M = -INFINITY;
+    for (int i = w - 1; i <= last; ++i) M = fmaxf(M, part(i)[D * 128]);
+    float l = 0.f, o[COLS] = {};
+    for (int i = w - 1; i <= last; ++i) {
+        const float* p = part(i);
+        const float m = p[D * 128];
+        const float f = m == -INFINITY && M > -INFINITY ? 0.f : exp2f((m - (M == -INFINITY ? 0.f : M)) * A.scale_log2);
+        l = fmaf(f, p[(D + 1) * 128], l);
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) o[c] = fmaf(f, p[(c0 + c) * 128], o[c]);
+    }
+    const float inv = 1.f / l;
+    uint4 out[COLS / 8];
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(out);
+#pragma unroll
+    for (int c = 0; c < COLS / 2; ++c) h[c] = __floats2bfloat162_rn(o[2 * c] * inv, o[2 * c + 1] * inv);
+    uint4* dst = reinterpret_cast<uint4*>(
+        A.o + ((size_t)(s.first + at / A.G) * A.Hq + s.kvh * A.G + at % A.G) * D + c0);
+#pragma unroll
+    for (int c = 0; c < COLS / 8; ++c) dst[c] = out[c];
+}
+
+struct TreePlan {
+    int RT, W, whole;
+};
+
+// sizes only: the workspace is known without a device
+TreePlan tree_plan(int B, int Hq, int Hkv, int D, int max_nodes, int max_ctx) {
+    const int BK = D == 256 ? 64 : 128, row_tiles = (max_nodes * (Hq / Hkv) + 127) / 128;
+    const int64_t lists = (int64_t)B * Hkv * row_tiles, tiles = ((int64_t)max_ctx + BK - 1) / BK + 1;
+    TreePlan p;
+    const char* e = getenv("TREE_GROUP");
+    p.RT = e && e[0] == '1' ? row_tiles : 1;
+    p.whole = tiles <= kTreeWhole && lists <= kTreeCtas ? row_tiles : 0;
+    if (p.whole) p.RT = 1;
+    p.W = p.whole ? (int)lists
+                  : (int)std::min<int64_t>(std::max(1, kTreeCtas / p.RT),
+                                           (lists / p.RT * tiles + kTreeMinTiles - 1) / kTreeMinTiles);
+    return p;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 tree_encode_fn() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
+}
+
+template <int D>
+cudaError_t launch_attn_tree_d(const AttnTreeJob& j, cudaStream_t st) {
+    using Ly = TreeLay<D>;
+    static std::atomic<uint64_t> smem_set{0};
+    cudaError_t e = raise_smem_limit(k_attn_tree<D>, Ly::SMEM_ALLOC, smem_set);
+    if (e != cudaSuccess) return e;
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tree_encode_fn();
+    if (!enc) return cudaErrorInvalidValue;
+    const TreePlan p = tree_plan(j.B, j.Hq, j.Hkv, D, j.max_nodes, j.max_ctx);
+    AttnTreeArgs A;
+    A.q = static_cast<const __nv_bfloat16*>(j.q);
+    A.v_new = static_cast<const __nv_bfloat16*>(j.v_new);
+    A.block_table = j.block_table;
+    A.cu_nodes = j.cu_nodes;
+    A.parents = j.parents;
+    A.ctx_lens = j.ctx_lens;
+    A.o = static_cast<__nv_bfloat16*>(j.o);
+    A.part = static_cast<float*>(j.ws);
+    A.B = j.B;
+    A.Hq = j.Hq;
+    A.Hkv = j.Hkv;
+    A.G = j.Hq / j.Hkv;
+    A.RT = p.RT;
+    A.W = p.W;
+    A.whole = p.whole;
+    A.page = j.page;
+    int R = Ly::BK;
+    while (j.page % R) R >>= 1;  // rows per box: gcd(page, BK); pages hold a multiple of 8 rows
+    A.R = R;
+    A.max_pages = j.max_pages;
+    A.n_pages = j.n_pages;
+    A.n_nodes = j.n_nodes;
+    A.max_nodes = j.max_nodes;
+    A.max_ctx = j.max_ctx;
+    A.scale_log2 = j.scale * 1.4426950408889634f;
+    // A box lands as [8-row group][64-column chunk][8 rows][128 bytes], whatever the page size: one copy per run of
+    // page rows, and one stride between row groups for the products
+    CUtensorMap maps[4];
+    for (int i = 0; i < 2; ++i) {
+        const cuuint64_t dims[5] = {64, 8, (cuuint64_t)Ly::NCH, (cuuint64_t)(j.page / 8),
+                                    (cuuint64_t)j.Hkv * (cuuint64_t)j.n_pages};
+        const cuuint64_t strides[4] = {(cuuint64_t)D * 2, 128, (cuuint64_t)8 * D * 2, (cuuint64_t)j.page * D * 2};
+        const cuuint32_t box[5] = {64, 8, (cuuint32_t)Ly::NCH, (cuuint32_t)(R / 8), 1};
+        const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+        if (enc(&maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(i == 0 ? j.k_pool : j.v_pool), dims,
+                strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    for (int i = 0; i < 2; ++i) {
+        const cuuint64_t dims[4] = {64, (cuuint64_t)j.n_nodes, (cuuint64_t)Ly::NCH, (cuuint64_t)j.Hkv};
+        const cuuint64_t strides[3] = {(cuuint64_t)j.Hkv * D * 2, 128, (cuuint64_t)D * 2};
+        const cuuint32_t box[4] = {64, 8, (cuuint32_t)Ly::NCH, 1};
+        const cuuint32_t es[4] = {1, 1, 1, 1};
+        if (enc(&maps[2 + i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(i == 0 ? j.k_new : j.v_new), dims,
+                strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    e = launch_pdl(k_attn_tree<D>, dim3((unsigned)(p.W * p.RT)), dim3(224), Ly::SMEM_ALLOC, st, maps[0], maps[1],
+                   maps[2], maps[3], A);
+    if (e != cudaSuccess || p.whole || p.W == 1) return e;
+    return launch_pdl(k_attn_tree_join<D>, dim3((unsigned)((p.W - 1) * p.RT), D / 32), dim3(128), 0, st, A);
 }
 
 }  // namespace
 
-size_t attn_tree_workspace_bytes(int B, int Hq, int Hkv, int D, int max_nodes, int max_ctx) { return 0; }
+size_t attn_tree_workspace_bytes(int B, int Hq, int Hkv, int D, int max_nodes, int max_ctx) {
+    if (B == 0) return 0;
+    const TreePlan p = tree_plan(B, Hq, Hkv, D, max_nodes, max_ctx);
+    return p.whole || p.W == 1 ? 0 : (size_t)p.W * p.RT * 2 * (D + 2) * 128 * 4;
+}
 
 cudaError_t launch_attn_tree(const AttnTreeJob& j, cudaStream_t st) {
     if (j.B == 0 || j.n_nodes == 0) return cudaSuccess;
-    const dim3 grid((unsigned)j.max_nodes, (unsigned)((j.Hq + 3) / 4), (unsigned)j.B);
-    if (j.D == 256) return launch_pdl(k_attn_tree<256>, grid, dim3(128), 0, st, j);
-    return launch_pdl(k_attn_tree<128>, grid, dim3(128), 0, st, j);
+    return j.D == 256 ? launch_attn_tree_d<256>(j, st) : launch_attn_tree_d<128>(j, st);
 }
+
+cudaError_t take_device_status_attn_tree(unsigned* out) { return take_device_status_tu(out); }
 
 }  // namespace gdn

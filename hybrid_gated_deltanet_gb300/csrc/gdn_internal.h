@@ -275,5 +275,6 @@ cudaError_t take_device_status_prefill(unsigned* out);
 cudaError_t take_device_status_chunk16(unsigned* out);
 cudaError_t take_device_status_proj(unsigned* out);
 cudaError_t take_device_status_tree(unsigned* out);
+cudaError_t take_device_status_attn_tree(unsigned* out);
 
 }  // namespace gdn
