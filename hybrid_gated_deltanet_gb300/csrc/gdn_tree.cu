@@ -16,8 +16,12 @@
 
 #include <algorithm>
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "gdn_common.cuh"
 #include "gdn_internal.h"
+#include "gdn_tc.cuh"
 #include "gdn_tma.cuh"
 
 namespace cg = cooperative_groups;
@@ -269,6 +273,461 @@ __global__ void __launch_bounds__(kTreeThreads) k_tree_verify(const __grid_const
     }
 }
 
+// ---- the same on the tensor cores (d = 128, bf16 activations) ---------------------
+// One CTA per (k-head, tree): the k-head's K^ and Q^ of all nodes are made once, as the rows of one operand
+// [K^; Q^] (TF32, K-major, 128-byte swizzle), and multiplied twice:
+//   [K^; Q^] K^T    the products of the nodes' keys and queries with keys (M = 128, N = nm, once), and
+//   S_0 [K^; Q^]^T  per v-head (M = 128 state rows, N = 2 nm), with S_0 as it lies in the pool (fp32, brought by
+//                   tensor TMA 32 columns at a time; the tensor core reads its leading 10 fraction bits, as it does of
+//                   K^ and Q^ rounded).
+// Then a thread has a state row: its S_0 k_i and S_0 q_i come from TMEM, and it walks the nodes in order, each
+// with a list of its ancestors and their two coefficients, keeping u in shared memory (its own column, no
+// barrier); o takes u's place, and all warps finish the nodes' y.  TF32's 2^-11 per operand is a quarter of the
+// bf16 rounding of y; the decays, sums and norms are fp32.  The phases are short and bound by latency, so the state's
+// place in shared memory is kept to half a tile: two CTAs per SM up to 32 nodes.
+constexpr int kVtThreads = 288;  // 8 warps and the one that drives the copies and the products
+constexpr int kVtAtom = 16384;   // 128 state rows x 32 columns
+
+struct VtSmem {
+    int S, B, v, ent, gram, node, beta, taps, gate, line, up, off, bar, total;
+};
+
+// entries of a tree's nodes: a node's ancestors, rounded up to groups of 4
+__host__ __device__ inline int vt_entries(int nm) { return nm * (nm - 1) / 2 + 3 * nm; }
+
+__host__ __device__ inline VtSmem vt_smem(int nm, int bufs) {  // nm: nodes, rounded up to 16
+    VtSmem s;
+    int o = 0;
+    s.S = o; o += 2 * kVtAtom;                // ring of state atoms
+    s.B = o; o += 2 * nm * 512;               // [K^; Q^]: 4 atoms of 2 nm rows x 128 bytes
+    s.v = o; o += bufs * nm * 512;            // v, then u, then o: [node][row]
+    s.ent = o; o += bufs * vt_entries(nm) * 16;
+    s.gram = o; o += 2 * nm * (nm + 1) * 4;
+    s.node = o; o += bufs * nm * 16;          // beta, e^G, the node's own coefficient, first entry
+    s.beta = o; o += nm * 8 * 4;              // per (node, v-head of the group)
+    s.taps = o; o += nm * 32;                 // offsets of the conv taps' rows from x
+    s.gate = o; o += nm * 8 * 4;              // log alpha, then its sum along the line
+    s.line = o; o += nm * 8;
+    s.up = o; o += nm * 4;
+    s.off = o; o += (nm + 4) * 4;             // first entry of each node
+    s.bar = o; o += 8 * 8;
+    // the Gram product reads 128 rows of each atom, whatever 2 nm is: all of them lie inside the allocation
+    s.total = o > s.B + 3 * 2 * nm * 128 + kVtAtom ? o : s.B + 3 * 2 * nm * 128 + kVtAtom;
+    return s;
+}
+
+struct VtArgs {
+    Geom g;
+    LayerParams p;
+    TreeJob job;
+    int nm, gv, bufs;  // gv: v-heads per CTA (G, or 1 where that fills the card better)
+};
+
+__device__ __forceinline__ float vt_silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
+
+__device__ __forceinline__ bool vt_elect() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+    return r != 0;
+}
+
+__device__ __forceinline__ void vt_mma(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::tf32 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void vt_ld8(uint32_t ta, uint32_t r[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(ta));
+}
+
+__device__ __forceinline__ void vt_st1(uint32_t ta, float v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(ta), "r"(__float_as_uint(v)) : "memory");
+}
+
+// conv + SiLU of the warp's 128 channels (ch .. ch + 3 of each lane) at the nodes i0 .. i0 + 3, all loads at once.
+// As v: to v[node][4 lane].  As k or q (scale != 0): L2-normalised times scale, to row row0 + node of [K^; Q^].
+// One copy of this code serves every call: the phases run once per CTA, and copies in line were bound by
+// instruction fetch.
+__device__ __noinline__ void vt_conv(const __nv_bfloat16* x, const long long* taps, const __nv_bfloat16* conv_w,
+                                     const __nv_bfloat16* conv_b, int K, int ch, int i0, int n, float* v,
+                                     unsigned char* Bt, int rows, int row0, float scale, float eps) {
+    const int lane = threadIdx.x & 31;
+    uint2 u[4][4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int node = min(i0 + e, n - 1);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) u[e][m] = __ldg(reinterpret_cast<const uint2*>(x + taps[node * 4 + m] + ch));
+    }
+    float w[4][4], bias[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        bias[c] = conv_b ? __bfloat162float(conv_b[ch + c]) : 0.f;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) w[m][c] = m < K ? __bfloat162float(conv_w[(size_t)(ch + c) * K + m]) : 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float y[4] = {bias[0], bias[1], bias[2], bias[3]};
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u[e][m].x));
+            const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u[e][m].y));
+            y[0] = fmaf(w[m][0], lo.x, y[0]);
+            y[1] = fmaf(w[m][1], lo.y, y[1]);
+            y[2] = fmaf(w[m][2], hi.x, y[2]);
+            y[3] = fmaf(w[m][3], hi.y, y[3]);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[c] = vt_silu(y[c]);
+        if (scale != 0.f) {
+            const float ss = tree_warp_sum(fmaf(y[0], y[0], fmaf(y[1], y[1], fmaf(y[2], y[2], y[3] * y[3]))));
+            const float f = scale * rsqrtf(ss + eps);
+            if (i0 + e < n) tc::st_row4(Bt, rows, row0 + i0 + e, 4 * lane, y[0] * f, y[1] * f, y[2] * f, y[3] * f);
+        } else if (i0 + e < n) {
+            *reinterpret_cast<float4*>(v + (i0 + e) * 128 + 4 * lane) = make_float4(y[0], y[1], y[2], y[3]);
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kVtThreads, 2)
+    k_tree_verify_tc(const __grid_constant__ CUtensorMap ts, const __grid_constant__ VtArgs A) {
+    constexpr int D = 128;
+    using bf = __nv_bfloat16;
+    const Geom& g = A.g;
+    const TreeJob& J = A.job;
+    const int nm = A.nm, gv = A.gv, per_k = g.G / gv;
+    const int h = blockIdx.x / per_k, j0 = h * g.G + (blockIdx.x % per_k) * gv, b = blockIdx.y;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int Hk = g.Hk, Hv = g.Hv, K = g.K, Km1 = g.K - 1, C = g.C_ch;
+    griddep_wait();  // launched with programmatic serialization
+    griddep_launch_dependents();
+    const int slot = J.slot_idx[b];
+    const int64_t first = J.cu_nodes[b];
+    const int64_t count = (int64_t)J.cu_nodes[b + 1] - first;
+    if (slot < 0 || slot >= J.n_slots || first < 0 || count < 1 || count > J.max_nodes || first + count > J.n_nodes)
+        return;
+    const int n = (int)count;
+
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* sm = smem_raw + ((1024 - (tc::smem_addr(smem_raw) & 1023)) & 1023);
+    const VtSmem lay = vt_smem(nm, A.bufs);
+    unsigned char* Bt = sm + lay.B;
+    float* gram = reinterpret_cast<float*>(sm + lay.gram);
+    float* betas = reinterpret_cast<float*>(sm + lay.beta);
+    long long* taps = reinterpret_cast<long long*>(sm + lay.taps);
+    float* gate = reinterpret_cast<float*>(sm + lay.gate);
+    unsigned long long* line = reinterpret_cast<unsigned long long*>(sm + lay.line);
+    int* up = reinterpret_cast<int*>(sm + lay.up);
+    int* off = reinterpret_cast<int*>(sm + lay.off);
+    uint64_t *full = reinterpret_cast<uint64_t*>(sm + lay.bar), *freed = full + 2, *done = full + 4, *bar_g = full + 6;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(full + 7);
+    const int tcols = nm <= 16 ? 128 : (nm <= 32 ? 256 : 512);  // products of two v-heads, then the Gram matrix
+    if (tid == 0) {
+        for (int i = 0; i < 7; ++i) mbar_init(full + i, 1);
+        fence_mbar_init();
+    }
+    if (warp == 8) tc::alloc(tslot, tcols);
+    // gates, parents; taps follow the parents
+    if (tid < n) {
+        const int p = J.parents[first + tid];
+        up[tid] = p >= 0 && p < tid ? p : -1;
+        line[tid] = 1ull << tid;
+    }
+    for (int i = tid; i < n * gv; i += kVtThreads) {
+        const int node = i / gv, jj = i % gv;
+        const size_t at = (size_t)(first + node) * Hv + j0 + jj;
+        float gl, beta;
+        gates(__bfloat162float(static_cast<const bf*>(J.a)[at]), __bfloat162float(static_cast<const bf*>(J.b)[at]),
+              A.p.A_log[j0 + jj], A.p.dt_bias ? A.p.dt_bias[j0 + jj] : 0.f, false, gl, beta);
+        gate[node * 8 + jj] = gl;
+        betas[node * 8 + jj] = beta;
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tm = *tslot, tgram = tm + 4 * nm;
+    const bf* xb = static_cast<const bf*>(J.x) + first * C;
+    const bf* cb = static_cast<const bf*>(J.conv_pool) + (size_t)slot * Km1 * C;
+    if (tid < n) {  // tap K - 1 is the node, then its ancestors, then the conv state's rows from the newest on
+        int at = tid, row = Km1 - 1;
+        for (int t = K - 1; t >= 0; --t) {
+            taps[tid * 4 + t] = at >= 0 ? (long long)at * C : (cb - xb) + (long long)(row--) * C;
+            if (at >= 0) at = up[at];
+        }
+        for (int t = K; t < 4; ++t) taps[tid * 4 + t] = (long long)tid * C;  // (weight 0)
+    }
+    __syncthreads();
+    // lines, and the sums of log alpha along them, by doubling: a thread has a node and v-heads jj, jj + 4
+#pragma unroll 1
+    for (int reach = 1; reach < n; reach <<= 1) {
+        const int i = tid & 63, jj = tid >> 6;
+        int p = -1, pp = -1;
+        unsigned long long m = 0;
+        float s0 = 0.f, s1 = 0.f;
+        if (i < n && jj < 4 && (p = up[i]) >= 0) {
+            pp = up[p];
+            m = line[p];
+            if (jj < gv) s0 = gate[p * 8 + jj];
+            if (jj + 4 < gv) s1 = gate[p * 8 + jj + 4];
+        }
+        __syncthreads();
+        if (p >= 0) {
+            if (jj < gv) gate[i * 8 + jj] += s0;
+            if (jj + 4 < gv) gate[i * 8 + jj + 4] += s1;
+            if (jj == 0) {
+                line[i] |= m;
+                up[i] = pp;
+            }
+        }
+        __syncthreads();
+    }
+    bool ok = true;
+    if (warp == 8) {
+        // ---- copies and products: the state of each v-head in 4 atoms through a ring of two ---------
+        const int atoms = 4 * gv;
+        auto load = [&](int a) {
+            mbar_arrive_expect_tx(full + (a & 1), kVtAtom);
+            tma_tile_2d(sm + lay.S + (a & 1) * kVtAtom, &ts, (a & 3) * 32, (slot * Hv + j0 + (a >> 2)) * D, full + (a & 1));
+        };
+        if (lane == 0) {
+            load(0);
+            load(1);
+        }
+        __syncwarp();
+        named_bar_sync(2, kVtThreads);  // [K^; Q^] is there
+        const uint64_t db = tc::sdesc(tc::smem_addr(Bt)), ds = tc::sdesc(tc::smem_addr(sm + lay.S));
+        const uint32_t bstep = (uint32_t)(2 * nm * 128) >> 4;
+        const uint32_t id_g = tc::idesc_tf32(128, nm), id_s = tc::idesc_tf32(128, 2 * nm);
+        if (vt_elect()) {  // lanes are the rows of [K^; Q^] (what lies past them is never read), columns the keys
+#pragma unroll 4
+            for (int k = 0; k < 16; ++k)
+                vt_mma(tgram, db + (k >> 2) * bstep + (k & 3) * 2, db + (k >> 2) * bstep + (k & 3) * 2, id_g, k > 0);
+            tc::commit(bar_g);
+        }
+        __syncwarp();
+#pragma unroll 1
+        for (int a = 0; a < atoms && ok; ++a) {
+            const int i = a >> 2;
+            if ((a & 3) == 0 && i >= 2) named_bar_sync(3, 160);  // v-head i - 2 has been read out of TMEM
+            ok = __all_sync(0xffffffffu, mbar_wait(full + (a & 1), (uint32_t)((a >> 1) & 1)));
+            if (!ok) break;
+            if (vt_elect()) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    vt_mma(tm + (i & 1) * 2 * nm, ds + (uint32_t)(((a & 1) * kVtAtom) >> 4) + k * 2,
+                           db + (a & 3) * bstep + k * 2, id_s, (a & 3) > 0 || k > 0);
+                tc::commit(freed + (a & 1));
+                if ((a & 3) == 3) tc::commit(done + (i & 1));
+            }
+            __syncwarp();
+            if (a + 2 < atoms) {
+                ok = __all_sync(0xffffffffu, mbar_wait(freed + (a & 1), (uint32_t)((a >> 1) & 1)));
+                if (!ok) break;
+                if (lane == 0) load(a + 2);
+                __syncwarp();
+            }
+        }
+        if (!ok) {  // let the copies in flight land (bounded again); the others' waits give up by themselves
+            for (int i = 0; i < 2; ++i) mbar_wait(full + i, 0);
+            if (lane == 0) report_device_status(kDevWaitTimeout);
+        }
+    } else {
+        if (warp == 7) {  // entries before each node: scan of the numbers of proper ancestors, in groups of 4
+            int base = 0;
+            for (int i0 = 0; i0 < nm; i0 += 32) {
+                const int i = i0 + lane;
+                int c = i < n ? (__popcll(line[i]) + 2) / 4 * 4 : 0;
+#pragma unroll
+                for (int s = 1; s < 32; s <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, c, s);
+                    if (lane >= s) c += v;
+                }
+                if (i < nm) off[i + 1] = base + c;
+                base += __shfl_sync(0xffffffffu, c, 31);
+            }
+            if (lane == 0) off[0] = 0;
+        }
+        auto vbuf = [&](int i) { return reinterpret_cast<float*>(sm + lay.v) + (i % A.bufs) * nm * D; };
+        // batches of 4 nodes: of k, q and the first v-head's v by all warps, then of the next v-heads' v
+        const int batches = (n + 3) / 4;
+        auto conv = [&](int what, int i, int batch) {  // what: 0 k, 1 q, 2 v of v-head j0 + i
+            vt_conv(xb, taps, static_cast<const bf*>(A.p.conv_w), static_cast<const bf*>(A.p.conv_b), K,
+                    (what == 0 ? (Hk + h) * D : (what == 1 ? h * D : (2 * Hk + j0 + i) * D)) + 4 * lane, 4 * batch, n,
+                    vbuf(i), Bt, 2 * nm, what == 1 ? nm : 0, what == 0 ? 1.f : (what == 1 ? g.q_scale : 0.f), g.l2_eps);
+        };
+#pragma unroll 1
+        for (int k = warp; k < 2 * batches; k += 8) conv(k & 1, 0, k >> 1);
+        fence_proxy_async_smem();
+        named_bar_sync(2, kVtThreads);
+        // coefficients of v-head j0 + i: a thread per (node, ancestor)
+        auto make_entries = [&](int i, int t0, int nt) {
+            float4* ent = reinterpret_cast<float4*>(sm + lay.ent) + (i % A.bufs) * vt_entries(nm);
+            float4* nd = reinterpret_cast<float4*>(sm + lay.node) + (i % A.bufs) * nm;
+            const int shift = nm <= 16 ? 4 : (nm <= 32 ? 5 : 6);
+#pragma unroll 1
+            for (int k = tid - t0; k < n << shift; k += nt) {
+                const int node = k >> shift, a = k & ((1 << shift) - 1);
+                const unsigned long long m = line[node];
+                if (a > node || !((m >> a) & 1ull)) continue;
+                const float G = gate[node * 8 + i], beta = betas[node * 8 + i];
+                const float gq = gram[(nm + node) * (nm + 1) + a];
+                if (a == node) {
+                    nd[node] = make_float4(beta, __expf(G), gq, 0.f);
+                    // the last group is filled up with zeros times the first ancestor's u
+                    const int c = __popcll(m) - 1, first_a = __ffsll((long long)m) - 1;
+                    for (int e = off[node] + c; e < off[node + 1]; ++e)
+                        ent[e] = make_float4(0.f, 0.f, __int_as_float(first_a * D), 0.f);
+                } else {
+                    const float f = __expf(G - gate[a * 8 + i]);
+                    ent[off[node] + __popcll(m & ((1ull << a) - 1ull))] =
+                        make_float4(beta * f * gram[node * (nm + 1) + a], f * gq, __int_as_float(a * D), 0.f);
+                }
+            }
+        };
+        if (warp < 4 && 32 * warp < 2 * nm) {
+            ok = __all_sync(0xffffffffu, mbar_wait(bar_g, 0));
+            if (ok) {
+                tc::fence_after();
+                const int row = 32 * warp + lane;
+#pragma unroll 1
+                for (int c0 = 0; c0 < n; c0 += 16) {
+                    uint32_t r[16];
+                    vt_ld8(tc::taddr(tgram, 32 * warp, c0), r);
+                    vt_ld8(tc::taddr(tgram, 32 * warp, c0 + 8), r + 8);
+                    tc::ld_wait();
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) gram[row * (nm + 1) + c0 + c] = __uint_as_float(r[c]);
+                }
+            }
+        }
+        for (int i = 0; i < gv; ++i) {
+            float* v = vbuf(i);
+            if (i == 0 || A.bufs == 1) {
+#pragma unroll 1
+                for (int k = warp; k < batches; k += 8) conv(2, i, k);
+                if (i == 0) named_bar_sync(1, 256);  // the Gram matrix is there
+                make_entries(i, 0, 256);
+                named_bar_sync(1, 256);
+            }
+            if (warp < 4) {
+                float* u = v + 32 * warp + lane;
+                const float4* ent = reinterpret_cast<const float4*>(sm + lay.ent) + (i % A.bufs) * vt_entries(nm);
+                const float4* nd = reinterpret_cast<const float4*>(sm + lay.node) + (i % A.bufs) * nm;
+                const uint32_t tr = tc::taddr(tm, 32 * warp, (i & 1) * 2 * nm);
+                if (ok) ok = __all_sync(0xffffffffu, mbar_wait(done + (i & 1), (uint32_t)((i >> 1) & 1)));
+                tc::fence_after();
+                // w_i = beta_i (v_i - e^{G_i} S_0 k_i) in v's place
+#pragma unroll 1
+                for (int c0 = 0; c0 < n; c0 += 8) {
+                    uint32_t rk[8];
+                    vt_ld8(tr + c0, rk);
+                    tc::ld_wait();
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        if (c0 + c < n) {
+                            const float4 s = nd[c0 + c];
+                            u[(c0 + c) * D] = s.x * (u[(c0 + c) * D] - s.y * __uint_as_float(rk[c]));
+                        }
+                    }
+                }
+                // u_i = w_i - sum of the ancestors' terms; the line's part of o_i replaces S_0 k_i
+                int e = 0;
+                float4 s = nd[0];
+                float wi = u[0];
+#pragma unroll 1
+                for (int node = 0; node < n; ++node) {
+                    const int end = off[node + 1], nx = min(node + 1, n - 1);
+                    const float4 s_next = nd[nx];
+                    const float w_next = u[nx * D];
+                    float su[4] = {}, so[4] = {};
+#pragma unroll 1
+                    for (; e < end; e += 4) {
+                        float4 k[4];
+                        float ua[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) k[q] = ent[e + q];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) ua[q] = u[__float_as_int(k[q].z)];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            su[q] = fmaf(k[q].x, ua[q], su[q]);
+                            so[q] = fmaf(k[q].y, ua[q], so[q]);
+                        }
+                    }
+                    const float un = wi - ((su[0] + su[1]) + (su[2] + su[3]));
+                    u[node * D] = un;
+                    vt_st1(tr + node, fmaf(s.z, un, (so[0] + so[1]) + (so[2] + so[3])));
+                    s = s_next;
+                    wi = w_next;
+                }
+                tc::st_wait();
+                // o_i in u's place (its own column: nobody else reads u)
+#pragma unroll 1
+                for (int c0 = 0; c0 < n; c0 += 8) {
+                    uint32_t ro[8], rq[8];
+                    vt_ld8(tr + c0, ro);
+                    vt_ld8(tr + nm + c0, rq);
+                    tc::ld_wait();
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        if (c0 + c < n)
+                            u[(c0 + c) * D] = fmaf(nd[c0 + c].y, __uint_as_float(rq[c]), __uint_as_float(ro[c]));
+                }
+                tc::fence_before();
+            } else if (i + 1 < gv && A.bufs == 2) {
+#pragma unroll 1
+                for (int k = warp - 4; k < batches; k += 4) conv(2, i + 1, k);
+                make_entries(i + 1, 128, 128);
+            }
+            named_bar_sync(1, 256);
+            if (warp < 4 && i + 2 < gv) asm volatile("bar.arrive 3, 160;" ::: "memory");  // this v-head's columns are free
+            // gated RMSNorm, a warp per node, four channels to a lane
+            {
+                const int j = j0 + i;
+                const uint2 nw = __ldg(reinterpret_cast<const uint2*>(A.p.norm_w) + lane);
+                const float2 w01 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&nw.x));
+                const float2 w23 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&nw.y));
+#pragma unroll 1
+                for (int i0 = warp; i0 < n; i0 += 32) {
+                    uint2 zr[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        zr[q] = __ldg(reinterpret_cast<const uint2*>(static_cast<const bf*>(J.z) +
+                                                                    ((size_t)(first + min(i0 + 8 * q, n - 1)) * Hv + j) * D) + lane);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int node = i0 + 8 * q;
+                        if (node >= n) break;
+                        const float4 o = *reinterpret_cast<const float4*>(v + node * D + 4 * lane);
+                        const float ss = tree_warp_sum(fmaf(o.x, o.x, fmaf(o.y, o.y, fmaf(o.z, o.z, o.w * o.w))));
+                        const float inv = rsqrtf(ss / (float)D + g.norm_eps);
+                        const float2 z01 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&zr[q].x));
+                        const float2 z23 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&zr[q].y));
+                        const __nv_bfloat162 y01 = __floats2bfloat162_rn(o.x * inv * w01.x * vt_silu(z01.x),
+                                                                         o.y * inv * w01.y * vt_silu(z01.y));
+                        const __nv_bfloat162 y23 = __floats2bfloat162_rn(o.z * inv * w23.x * vt_silu(z23.x),
+                                                                         o.w * inv * w23.y * vt_silu(z23.y));
+                        uint2 out;
+                        memcpy(&out.x, &y01, 4);
+                        memcpy(&out.y, &y23, 4);
+                        if (ok) *(reinterpret_cast<uint2*>(static_cast<bf*>(J.y) + ((size_t)(first + node) * Hv + j) * D) + lane) = out;
+                    }
+                }
+            }
+            if (i + 1 < gv && A.bufs == 1) named_bar_sync(1, 256);  // o is read: its place takes the next v
+        }
+    }
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 8) tc::dealloc(tm, tcols);
+}
+
 template <int D, typename TA>
 cudaError_t launch_verify_t(const TreeArgs& A, cudaStream_t st) {
     static std::atomic<uint64_t> smem_set{0};
@@ -277,6 +736,42 @@ cudaError_t launch_verify_t(const TreeArgs& A, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     return launch_pdl(k_tree_verify<D, TA>, dim3(A.g.Hv, A.job.B), dim3(kTreeThreads),
                       (size_t)tree_smem(D, A.nmax).total, st, A);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 vt_encode_fn() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
+}
+
+cudaError_t launch_verify_tc(const Geom& g, const LayerParams& p, const TreeJob& job, cudaStream_t st) {
+    static std::atomic<uint64_t> smem_set{0};
+    cudaError_t e = raise_smem_limit(k_tree_verify_tc, 227 * 1024, smem_set);
+    if (e != cudaSuccess) return e;
+    PFN_cuTensorMapEncodeTiled_v12000 enc = vt_encode_fn();
+    if (!enc) return cudaErrorInvalidValue;
+    CUtensorMap map;
+    const cuuint64_t dims[2] = {128, (cuuint64_t)job.n_slots * (cuuint64_t)g.Hv * 128};
+    const cuuint64_t strides[1] = {512};
+    const cuuint32_t box[2] = {32, 128}, es[2] = {1, 1};
+    if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float*>(job.state_pool), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    VtArgs A{g, p, job, (job.max_nodes + 15) / 16 * 16, g.G, 2};
+    if ((long)job.B * g.Hk < sm_count()) A.gv = 1;  // few trees: a CTA per v-head
+    if (A.gv == 1) A.bufs = 1;
+    const int room = A.nm > 32 ? 227 * 1024 : 113 * 1024;  // two CTAs per SM (1 KB of each one's share is the system's)
+    if (vt_smem(A.nm, A.bufs).total + 1024 > room) A.bufs = 1;
+    return launch_pdl(k_tree_verify_tc, dim3((unsigned)(g.Hv / A.gv), (unsigned)job.B), dim3(kVtThreads),
+                      (size_t)vt_smem(A.nm, A.bufs).total + 1024, st, map, A);
 }
 
 // ---- commit ---------------------------------------------------------------------
@@ -458,6 +953,9 @@ cudaError_t launch_commit_t(const CommitArgs& A, cudaStream_t st) {
 
 cudaError_t launch_tree_verify(const Geom& g, const LayerParams& p, const TreeJob& job, cudaStream_t st) {
     if (job.B == 0 || job.n_nodes == 0) return cudaSuccess;
+    if (g.D == 128 && g.act_bf16 && g.flags == 0) {
+        return launch_verify_tc(g, p, job, st);
+    }
     const TreeArgs A{g, p, job, job.max_nodes};
     GDN_BY_TYPE(launch_verify_t);
 }
