@@ -393,36 +393,42 @@ def gdn_attn_prefill(cfg: AttnConfig, q, k_new, v_new, k_pool, v_pool, block_tab
 GDN_TREE_MAX_NODES = 64
 
 
-class _Args:
-    """Device tensors of one call: each is held to its dtype and shape, all to one CUDA
-    device (sizes reach the library from the shapes, so a wrong one would be a wrong
-    address), and the call runs with that device current."""
-    __slots__ = ("device",)
+# A call's tensors are held to their dtypes and shapes and to one CUDA device (sizes reach the library from the
+# shapes, so a wrong one would be a wrong address), and the call runs with that device current.  These calls are
+# made once per layer and step, so the checks are plain expressions.
+_bf16, _f32, _i32, _i64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
-    def __init__(self):
-        self.device = None
 
-    def __call__(self, name, t, dtype, *shape):
-        device = t.get_device()
-        if device != self.device:
-            if device < 0 or self.device is not None:
-                raise ValueError(f"{name}: found a tensor on {t.device}, required one CUDA device for all tensors")
-            self.device = device
-        if t.dtype is not dtype or t.shape != shape:
-            raise ValueError(f"{name}: found {t.dtype} {tuple(t.shape)}, required {dtype} {shape}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: libgdn takes dense row-major tensors")
+def _ptr(t, name, dtype, shape, device):
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
         return t.data_ptr()
+    if t.get_device() != device or device < 0:
+        raise ValueError(f"{name}: found a tensor on {t.device}, required one CUDA device for all tensors")
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name}: found {t.dtype} {tuple(t.shape)}, required {dtype} {tuple(shape)}")
+    raise ValueError(f"{name}: libgdn takes dense row-major tensors")
 
-    def optional(self, name, t, dtype, *shape):
-        return None if t is None else self(name, t, dtype, *shape)
 
-    def run(self, name, stream, *args):
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-        with torch.cuda.device(self.device):
-            _check(getattr(load(), name)(*args, handle))
+def _device(t, name):
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{name}: found a tensor on {t.device}, required one CUDA device for all tensors")
+    return device
+
+
+def _call(fn, device, stream, *args):
+    if stream is None:
+        stream = _raw_stream(device)
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    if _current_device() == device:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream)
+    if status:
+        _check(status)
 
 
 def _dim(name, t, n):
@@ -445,82 +451,85 @@ def gdn_attn_tree(cfg: AttnConfig, q, k_new, v_new, k_pool, v_pool, block_table,
     """q, o [N, Hq, D]; k_new, v_new [N, Hkv, D]; pools [n_pages, Hkv, page, D] (read only);
     block_table int32 [B, max_pages]; the tree of sequence b is rows cu_nodes[b] .. cu_nodes[b+1],
     parents int32 [N] within the sequence (-1: the end of the ctx_lens[b] cached tokens)."""
-    bf, i32, arg = torch.bfloat16, torch.int32, _Args()
-    N, (B, max_pages), n_pages = q.shape[0], _dim("block_table", block_table, 2), k_pool.shape[0]
-    new, pool = (N, cfg.n_kv_heads, cfg.head_dim), (n_pages, cfg.n_kv_heads, cfg.page_size, cfg.head_dim)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    c = cfg.c()
-    arg.run("gdn_attn_tree", stream, ctypes.byref(c), arg("q", q, bf, N, cfg.n_q_heads, cfg.head_dim),
-            arg("k_new", k_new, bf, *new), arg("v_new", v_new, bf, *new), arg("k_pool", k_pool, bf, *pool),
-            arg("v_pool", v_pool, bf, *pool), arg("block_table", block_table, i32, B, max_pages),
-            arg("cu_nodes", cu_nodes, i32, B + 1), arg("parents", parents, i32, N), arg("ctx_lens", ctx_lens, i32, B),
-            B, N, max_nodes, max_pages, n_pages, max_ctx_len, arg("o", o, bf, N, cfg.n_q_heads, cfg.head_dim),
-            arg.optional("workspace", workspace, torch.uint8, ws_bytes), ws_bytes)
+    (B, max_pages), dev, N, n_pages = _dim("block_table", block_table, 2), _device(q, "q"), q.shape[0], k_pool.shape[0]
+    rows, new = (N, cfg.n_q_heads, cfg.head_dim), (N, cfg.n_kv_heads, cfg.head_dim)
+    pool = (n_pages, cfg.n_kv_heads, cfg.page_size, cfg.head_dim)
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        ws_bytes = workspace.nbytes
+        ws = _ptr(workspace, "workspace", torch.uint8, (ws_bytes,), dev)
+    _call(load().gdn_attn_tree, dev, stream, ctypes.byref(cfg.c()), _ptr(q, "q", _bf16, rows, dev),
+          _ptr(k_new, "k_new", _bf16, new, dev), _ptr(v_new, "v_new", _bf16, new, dev),
+          _ptr(k_pool, "k_pool", _bf16, pool, dev), _ptr(v_pool, "v_pool", _bf16, pool, dev),
+          _ptr(block_table, "block_table", _i32, (B, max_pages), dev), _ptr(cu_nodes, "cu_nodes", _i32, (B + 1,), dev),
+          _ptr(parents, "parents", _i32, (N,), dev), _ptr(ctx_lens, "ctx_lens", _i32, (B,), dev), B, N, max_nodes,
+          max_pages, n_pages, max_ctx_len, _ptr(o, "o", _bf16, rows, dev), ws, ws_bytes)
 
 
 def gdn_attn_append(cfg: AttnConfig, k_new, v_new, slot_map, k_pool, v_pool, src_rows=None, stream=None):
     """Rows src_rows[i] (None: i) of k_new, v_new [n_src, Hkv, D] to cache rows slot_map[i] (int64)
     of the pools [n_pages, Hkv, page, D]."""
-    bf, arg = torch.bfloat16, _Args()
-    n_src, n_pages, n = k_new.shape[0], k_pool.shape[0], slot_map.shape[0]
+    dev, n_src, n_pages, n = _device(k_new, "k_new"), k_new.shape[0], k_pool.shape[0], slot_map.shape[0]
     new, pool = (n_src, cfg.n_kv_heads, cfg.head_dim), (n_pages, cfg.n_kv_heads, cfg.page_size, cfg.head_dim)
-    c = cfg.c()
-    arg.run("gdn_attn_append", stream, ctypes.byref(c), arg("k_new", k_new, bf, *new), arg("v_new", v_new, bf, *new),
-            n_src, arg("slot_map", slot_map, torch.int64, n), arg.optional("src_rows", src_rows, torch.int32, n), n,
-            arg("k_pool", k_pool, bf, *pool), arg("v_pool", v_pool, bf, *pool), n_pages)
+    _call(load().gdn_attn_append, dev, stream, ctypes.byref(cfg.c()), _ptr(k_new, "k_new", _bf16, new, dev),
+          _ptr(v_new, "v_new", _bf16, new, dev), n_src, _ptr(slot_map, "slot_map", _i64, (n,), dev),
+          None if src_rows is None else _ptr(src_rows, "src_rows", _i32, (n,), dev), n,
+          _ptr(k_pool, "k_pool", _bf16, pool, dev), _ptr(v_pool, "v_pool", _bf16, pool, dev), n_pages)
 
 
-def _params(arg, cfg: Config, prm: Params):
-    act, f32 = cfg.torch_dtype, torch.float32
-    return CParams(arg.optional("conv_w", prm.conv_w, act, cfg.conv_channels, cfg.d_conv),
-                   arg.optional("conv_b", prm.conv_b, act, cfg.conv_channels),
-                   arg.optional("A_log", prm.A_log, f32, cfg.n_v_heads),
-                   arg.optional("dt_bias", prm.dt_bias, f32, cfg.n_v_heads),
-                   arg.optional("norm_w", prm.norm_w, act, cfg.d_v))
+def _tree_params(cfg: Config, prm: Params, dev):
+    act, ch = cfg.torch_dtype, cfg.conv_channels
+    return CParams(None if prm.conv_w is None else _ptr(prm.conv_w, "conv_w", act, (ch, cfg.d_conv), dev),
+                   None if prm.conv_b is None else _ptr(prm.conv_b, "conv_b", act, (ch,), dev),
+                   None if prm.A_log is None else _ptr(prm.A_log, "A_log", _f32, (cfg.n_v_heads,), dev),
+                   None if prm.dt_bias is None else _ptr(prm.dt_bias, "dt_bias", _f32, (cfg.n_v_heads,), dev),
+                   None if prm.norm_w is None else _ptr(prm.norm_w, "norm_w", act, (cfg.d_v,), dev))
 
 
 def gdn_verify_tree(cfg: Config, prm: Params, x, z, a, b, conv_pool, state_pool, slot_idx, cu_nodes, parents,
                     max_nodes: int, y, stream=None):
     """y [N, H_v*d_v] of every node of the trees in rows cu_nodes[i] .. cu_nodes[i+1] of x [N, C_ch],
     z, a, b; the pools are not written."""
-    act, i32, arg = cfg.torch_dtype, torch.int32, _Args()
-    N, B, n_slots, Hv, D = x.shape[0], slot_idx.shape[0], state_pool.shape[0], cfg.n_v_heads, cfg.d_v
-    c, p = cfg.c(), _params(arg, cfg, prm)
-    arg.run("gdn_verify_tree", stream, ctypes.byref(c), ctypes.byref(p), arg("x", x, act, N, cfg.conv_channels),
-            arg.optional("z", z, act, N, Hv * D), arg("a", a, act, N, Hv), arg("b", b, act, N, Hv),
-            arg("conv_pool", conv_pool, act, n_slots, cfg.d_conv - 1, cfg.conv_channels),
-            arg("state_pool", state_pool, torch.float32, n_slots, Hv, D, cfg.d_k), arg("slot_idx", slot_idx, i32, B),
-            arg("cu_nodes", cu_nodes, i32, B + 1), arg("parents", parents, i32, N), B, N, max_nodes, n_slots,
-            arg("y", y, act, N, Hv * D))
+    dev, act, ch, Hv, D = _device(x, "x"), cfg.torch_dtype, cfg.conv_channels, cfg.n_v_heads, cfg.d_v
+    N, B, n_slots = x.shape[0], slot_idx.shape[0], state_pool.shape[0]
+    heads, values = (N, Hv), (N, Hv * D)
+    _call(load().gdn_verify_tree, dev, stream, ctypes.byref(cfg.c()), ctypes.byref(_tree_params(cfg, prm, dev)),
+          _ptr(x, "x", act, (N, ch), dev), None if z is None else _ptr(z, "z", act, values, dev),
+          _ptr(a, "a", act, heads, dev), _ptr(b, "b", act, heads, dev),
+          _ptr(conv_pool, "conv_pool", act, (n_slots, cfg.d_conv - 1, ch), dev),
+          _ptr(state_pool, "state_pool", _f32, (n_slots, Hv, D, cfg.d_k), dev),
+          _ptr(slot_idx, "slot_idx", _i32, (B,), dev), _ptr(cu_nodes, "cu_nodes", _i32, (B + 1,), dev),
+          _ptr(parents, "parents", _i32, (N,), dev), B, N, max_nodes, n_slots, _ptr(y, "y", act, values, dev))
 
 
 def gdn_commit_tree(cfg: Config, prm: Params, x, a, b, conv_pool, state_pool, slot_idx, cu_rows, src_rows,
                     max_rows: int, stream=None):
     """Rows src_rows[cu_rows[i]] .. of x, a, b [n_src, ...] (src_rows None: those rows themselves) applied to
     slot_idx[i] in place."""
-    act, i32, arg = cfg.torch_dtype, torch.int32, _Args()
-    n_src, B, n_slots, Hv, D = x.shape[0], slot_idx.shape[0], state_pool.shape[0], cfg.n_v_heads, cfg.d_v
+    dev, act, ch, Hv, D = _device(x, "x"), cfg.torch_dtype, cfg.conv_channels, cfg.n_v_heads, cfg.d_v
+    n_src, B, n_slots = x.shape[0], slot_idx.shape[0], state_pool.shape[0]
     n_rows = n_src if src_rows is None else src_rows.shape[0]
-    c, p = cfg.c(), _params(arg, cfg, prm)
-    arg.run("gdn_commit_tree", stream, ctypes.byref(c), ctypes.byref(p), arg("x", x, act, n_src, cfg.conv_channels),
-            arg("a", a, act, n_src, Hv), arg("b", b, act, n_src, Hv),
-            arg("conv_pool", conv_pool, act, n_slots, cfg.d_conv - 1, cfg.conv_channels),
-            arg("state_pool", state_pool, torch.float32, n_slots, Hv, D, cfg.d_k), arg("slot_idx", slot_idx, i32, B),
-            arg("cu_rows", cu_rows, i32, B + 1), arg.optional("src_rows", src_rows, i32, n_rows), B, n_rows, n_src,
-            max_rows, n_slots)
+    _call(load().gdn_commit_tree, dev, stream, ctypes.byref(cfg.c()), ctypes.byref(_tree_params(cfg, prm, dev)),
+          _ptr(x, "x", act, (n_src, ch), dev), _ptr(a, "a", act, (n_src, Hv), dev),
+          _ptr(b, "b", act, (n_src, Hv), dev), _ptr(conv_pool, "conv_pool", act, (n_slots, cfg.d_conv - 1, ch), dev),
+          _ptr(state_pool, "state_pool", _f32, (n_slots, Hv, D, cfg.d_k), dev),
+          _ptr(slot_idx, "slot_idx", _i32, (B,), dev), _ptr(cu_rows, "cu_rows", _i32, (B + 1,), dev),
+          None if src_rows is None else _ptr(src_rows, "src_rows", _i32, (n_rows,), dev), B, n_rows, n_src, max_rows,
+          n_slots)
 
 
 def gdn_page_tables(page_size: int, n_pages: int, ctx_lens, new_lens, free_pages, head, block_table, cu_rows,
                     slot_map, head_out, path=None, cu_nodes=None, src_rows=None, stream=None):
     """Pages for new_lens[b] more tokens of each sequence into block_table [B, max_pages], and their rows into
     cu_rows [B+1], slot_map int64 [n_rows] and, with path [B, path_len] and cu_nodes [B+1], src_rows [n_rows]."""
-    i32, arg = torch.int32, _Args()
-    B, n_free, n_rows = ctx_lens.shape[0], free_pages.shape[0], slot_map.shape[0]
+    dev, B, n_free, n_rows = _device(ctx_lens, "ctx_lens"), ctx_lens.shape[0], free_pages.shape[0], slot_map.shape[0]
     max_pages = _dim("block_table", block_table, 2)[1]
     path_len = 0 if path is None else _dim("path", path, 2)[1]
-    arg.run("gdn_page_tables", stream, page_size, n_pages, arg("ctx_lens", ctx_lens, i32, B),
-            arg("new_lens", new_lens, i32, B), B, arg("free_pages", free_pages, i32, n_free), n_free,
-            arg("head", head, i32, 1), arg("block_table", block_table, i32, B, max_pages), max_pages,
-            arg("cu_rows", cu_rows, i32, B + 1), arg("slot_map", slot_map, torch.int64, n_rows), n_rows,
-            arg("head_out", head_out, i32, 1), arg.optional("path", path, i32, B, path_len), path_len,
-            arg.optional("cu_nodes", cu_nodes, i32, B + 1), arg.optional("src_rows", src_rows, i32, n_rows))
+    _call(load().gdn_page_tables, dev, stream, page_size, n_pages, _ptr(ctx_lens, "ctx_lens", _i32, (B,), dev),
+          _ptr(new_lens, "new_lens", _i32, (B,), dev), B, _ptr(free_pages, "free_pages", _i32, (n_free,), dev), n_free,
+          _ptr(head, "head", _i32, (1,), dev), _ptr(block_table, "block_table", _i32, (B, max_pages), dev), max_pages,
+          _ptr(cu_rows, "cu_rows", _i32, (B + 1,), dev), _ptr(slot_map, "slot_map", _i64, (n_rows,), dev), n_rows,
+          _ptr(head_out, "head_out", _i32, (1,), dev),
+          None if path is None else _ptr(path, "path", _i32, (B, path_len), dev), path_len,
+          None if cu_nodes is None else _ptr(cu_nodes, "cu_nodes", _i32, (B + 1,), dev),
+          None if src_rows is None else _ptr(src_rows, "src_rows", _i32, (n_rows,), dev))

@@ -45,43 +45,91 @@ __device__ __forceinline__ float tree_warp_sum(float v) {
     return v;
 }
 
-// rows of S in shared memory are padded by 16 bytes so that 8 threads reading 16 bytes of
-// 8 rows touch all banks once
-__host__ __device__ inline int tree_s_stride(int D) { return D + 4; }
+// NV values per lane (a power of two, at most 8), summed over groups of 8 lanes; lane l of a group ends with value
+// l / (8 / NV): each step halves the values by exchanging the half that the partner keeps
+template <int NV>
+__device__ __forceinline__ float tree_sum8(float v[NV], int lane) {
+    int count = NV;
+#pragma unroll
+    for (int s = 4; s >= 1; s >>= 1) {
+        if (count > 1) {
+            const bool upper = lane & s;
+            count /= 2;
+#pragma unroll
+            for (int i = 0; i < NV / 2; ++i) {
+                if (i < count) {
+                    const float send = upper ? v[i] : v[i + count];
+                    const float keep = upper ? v[i + count] : v[i];
+                    v[i] = keep + __shfl_xor_sync(0xffffffffu, send, s);
+                }
+            }
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], s);
+        }
+    }
+    return v[0];
+}
+
+// four consecutive activations as fp32
+__device__ __forceinline__ float4 tree_ld4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+__device__ __forceinline__ float4 tree_ld4(const __nv_bfloat16* p) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+    const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+    const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+// acc + a . b on the paired fp32 instructions
+__device__ __forceinline__ float2 tree_dot(const float4& a, const float4& b, float2 acc) {
+    return __ffma2_rn(make_float2(a.z, a.w), make_float2(b.z, b.w), __ffma2_rn(make_float2(a.x, a.y), make_float2(b.x, b.y), acc));
+}
+__device__ __forceinline__ void tree_prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+// x sigmoid(x) by the SFU's exponential and division, 2^-21 relative at the sizes of a conv's outputs
+__device__ __forceinline__ float tree_silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
+
+// entries of a tree's nodes: a node's proper ancestors, rounded up to groups of 4
+__host__ __device__ inline int tree_entries(int n) { return n * (n - 1) / 2 + 3 * n; }
 
 struct TreeSmem {
-    int bar, S, k, q, u, pk, pq, sc, anc, up, total;
+    int k, q, u, p, r, w, ent, node, anc, up, off, taps, total;
 };
 
 __host__ __device__ inline TreeSmem tree_smem(int D, int n) {
     auto round = [](int v) { return (v + 15) & ~15; };
     TreeSmem s;
     int o = 0;
-    s.bar = o; o += 16;
-    s.S = o; o += D * tree_s_stride(D) * 4;
     s.k = o; o += n * D * 4;
-    s.q = o; o += n * D * 4;               // q, then o once the line sums are taken
-    s.u = o; o += n * D * 4;               // v, then u
-    s.pk = o; o = round(o + n * n * 4);    // e^{G_i - G_j} k_i . k_j
-    s.pq = o; o = round(o + n * n * 4);    // e^{G_i - G_j} q_i . k_j
-    s.sc = o; o += n * 4 * 4;              // g, beta, G, e^G per node
-    s.anc = o; o += n * 8;                 // ancestors and the node itself, one bit each
-    s.up = o; o = round(o + n * 4);        // parent within the tree, -1: the cached state
+    s.q = o; o += n * D * 4;
+    s.u = o; o += n * D * 4;                      // v, then u
+    s.p = o; o += n * D * 4;                      // S_0 k_i
+    s.r = o; o += n * D * 4;                      // S_0 q_i, then o
+    s.w = s.p;                                    // conv weights [q, k, v][4 taps][D] (12 rows) and bias [3][D], till p is made
+    if (n < 8) o += (8 - n) * 2 * D * 4;          // (15 rows in p's and r's place)
+    s.ent = o; o += tree_entries(n) * 16;         // per (node, proper ancestor): two coefficients and the ancestor
+    s.node = o; o += n * 16;                      // beta, G, e^G, q_i . k_i
+    s.anc = o; o += n * 8;                        // ancestors and the node itself, one bit each
+    s.up = o; o += n * 4;                         // parent within the tree, -1: the cached state
+    s.off = o; o = round(o + (n + 1) * 4);        // first entry of each node
+    s.taps = o; o += n * 16;                      // rows of the conv taps: a node, or 64 + a row of the conv state
     s.total = o;
     return s;
 }
 
-// One CTA per (v-head, tree).  The simple form: fp32 on the CUDA cores throughout.
+// One CTA per (v-head, tree), fp32 on the CUDA cores throughout: fp32 activations, d < 128 and the flags.  A
+// warp has d / 8 state rows in registers, 8 lanes to a row, and takes the nodes' k and q one after another; the sums
+// of its dot products are reduced together (7 shuffles for 8 of them).  Bound by instructions: 4 d^2 multiply-adds per
+// node against 4 d^2 bytes of state per tree, and as much again for the shuffles, the conv and the line sums.
 template <int D, typename TA>
-__global__ void __launch_bounds__(kTreeThreads) k_tree_verify(const __grid_constant__ TreeArgs A) {
+__global__ void __launch_bounds__(kTreeThreads, 2) k_tree_verify(const __grid_constant__ TreeArgs A) {
     using L = Act<TA>;
+    constexpr int LPN = D / 4, NPW = 32 / LPN;  // lanes of a node's channels, nodes of a warp (conv, output)
+    constexpr int RL = D / 32;                  // state rows and 4-column chunks of a lane
+    constexpr int nwarp = kTreeThreads / 32;
     const Geom& g = A.g;
     const TreeJob& J = A.job;
     const int j = blockIdx.x, h = j / g.G, b = blockIdx.y;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int nwarp = kTreeThreads / 32;
     const int Hk = g.Hk, Hv = g.Hv, K = g.K, Km1 = g.K - 1, C = g.C_ch;
-    const bool raw = g.flags & kFlagRawQKV;
+    const bool raw = g.flags & kFlagRawQKV, direct = g.flags & kFlagGatesDirect;
     griddep_wait();  // launched with programmatic serialization
     griddep_launch_dependents();
     const int slot = J.slot_idx[b];
@@ -93,224 +141,316 @@ __global__ void __launch_bounds__(kTreeThreads) k_tree_verify(const __grid_const
 
     extern __shared__ __align__(128) unsigned char smem[];
     const TreeSmem lay = tree_smem(D, A.nmax);
-    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + lay.bar);
-    float* S = reinterpret_cast<float*>(smem + lay.S);
     float* ks = reinterpret_cast<float*>(smem + lay.k);
     float* qs = reinterpret_cast<float*>(smem + lay.q);
     float* us = reinterpret_cast<float*>(smem + lay.u);
-    float* pk = reinterpret_cast<float*>(smem + lay.pk);
-    float* pq = reinterpret_cast<float*>(smem + lay.pq);
-    float* sc = reinterpret_cast<float*>(smem + lay.sc);
+    float* ps = reinterpret_cast<float*>(smem + lay.p);
+    float* rs = reinterpret_cast<float*>(smem + lay.r);
+    float* ws = reinterpret_cast<float*>(smem + lay.w);
+    float4* ent = reinterpret_cast<float4*>(smem + lay.ent);
+    float4* nd = reinterpret_cast<float4*>(smem + lay.node);
     unsigned long long* anc = reinterpret_cast<unsigned long long*>(smem + lay.anc);
     int* up = reinterpret_cast<int*>(smem + lay.up);
-    constexpr int SS = D + 4;
+    int* off = reinterpret_cast<int*>(smem + lay.off);
+    int* taps = reinterpret_cast<int*>(smem + lay.taps);
 
-    // the state of (slot, j), a row at a time into padded rows
+    // the state on its way to L2 while the inputs are prepared
     const float* Sg = J.state_pool + ((size_t)slot * Hv + j) * D * D;
-    if (tid == 0) {
-        mbar_init(bar, 1);
-        fence_mbar_init();
-        mbar_arrive_expect_tx(bar, D * D * 4);
-        for (int r = 0; r < D; ++r) bulk_g2s(S + r * SS, Sg + (size_t)r * D, D * 4, bar);
-    }
+    for (int i = tid; i < D * D / 32; i += kTreeThreads) tree_prefetch(Sg + i * 32);
     // a parent outside [0, i) stands for the end of the cached sequence
+    float gl = 0.f, beta = 0.f;
     if (tid < n) {
         const int p = J.parents[first + tid];
         up[tid] = p >= 0 && p < tid ? p : -1;
-        float gl, beta;
-        gates(L::ld(J.a, (first + tid) * Hv + j), L::ld(J.b, (first + tid) * Hv + j),
-              g.flags & kFlagGatesDirect ? 0.f : A.p.A_log[j],
-              !(g.flags & kFlagGatesDirect) && A.p.dt_bias ? A.p.dt_bias[j] : 0.f, g.flags & kFlagGatesDirect, gl, beta);
-        sc[4 * tid] = gl;
-        sc[4 * tid + 1] = beta;
+        gates(L::ld(J.a, (first + tid) * Hv + j), L::ld(J.b, (first + tid) * Hv + j), direct ? 0.f : A.p.A_log[j],
+              !direct && A.p.dt_bias ? A.p.dt_bias[j] : 0.f, direct, gl, beta);
+        nd[tid] = make_float4(beta, gl, 0.f, 0.f);
+    }
+    auto channel = [&](int kind) { return (kind == 0 ? h : (kind == 1 ? Hk + h : 2 * Hk + j)) * D; };
+    if (!raw) {
+        for (int i = tid; i < 3 * D; i += kTreeThreads) {
+            const int ch = channel(i / D) + i % D;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {  // (taps are aligned at the newest)
+                const int m = t - (4 - K);
+                ws[(i / D * 4 + t) * D + i % D] = m >= 0 ? L::ld(A.p.conv_w, (size_t)ch * K + m) : 0.f;
+            }
+            ws[12 * D + i] = A.p.conv_b ? L::ld(A.p.conv_b, ch) : 0.f;
+        }
     }
     __syncthreads();
+    float G = 0.f;
     if (tid < n) {  // the node's line, and the decay along it
         unsigned long long m = 0;
-        float G = 0.f;
         for (int i = tid; i >= 0; i = up[i]) {
             m |= 1ull << i;
-            G += sc[4 * i];
+            G += nd[i].y;
         }
         anc[tid] = m;
-        sc[4 * tid + 2] = G;
-        sc[4 * tid + 3] = expf(G);
+    } else if (tid >= 128 && tid - 128 < n) {
+        // its conv taps: the last is the node, then its ancestors, then the conv state, newest first
+        const int i = tid - 128;
+        int at = i, row = Km1 - 1;
+        for (int t = 3; t >= 0; --t) {
+            const bool live = 3 - t < K;
+            taps[i * 4 + t] = !live ? i : (at >= 0 ? at : 64 + row--);
+            if (live && at >= 0) at = up[at];
+        }
     }
-    // conv + SiLU of the k-head's q and k and the v-head's v
+    __syncthreads();
+    if (tid < n) nd[tid] = make_float4(beta, G, expf(G), 0.f);
+    if (warp == nwarp - 1) {  // entries before each node
+        int base = 0;
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            const int i = i0 + lane;
+            int c = i < n ? (__popcll(anc[i]) + 2) / 4 * 4 : 0;
+#pragma unroll
+            for (int s = 1; s < 32; s <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, c, s);
+                if (lane >= s) c += v;
+            }
+            if (i < n) off[i + 1] = base + c;
+            base += __shfl_sync(0xffffffffu, c, 31);
+        }
+        if (lane == 0) off[0] = 0;
+    }
+    // conv + SiLU, then the L2 norm, of q (kind 0), k (1) and v (2): a warp takes NB x NPW nodes at a time
     const TA* x = static_cast<const TA*>(J.x) + first * C;
     const TA* cp = static_cast<const TA*>(J.conv_pool) + (size_t)slot * Km1 * C;
-    for (int w = tid; w < 3 * D * n; w += kTreeThreads) {
-        const int i = w / (3 * D), c = w % (3 * D);
-        const int ch = c < D ? h * D + c : (c < 2 * D ? Hk * D + h * D + c - D : 2 * Hk * D + j * D + c - 2 * D);
-        float val;
-        if (raw) {
-            val = L::ld(x, (size_t)i * C + ch);
-        } else {
-            // taps backwards along the line, then through the conv state
-            float acc = A.p.conv_b ? L::ld(A.p.conv_b, ch) : 0.f;
-            int at = i, row = Km1 - 1;
-            for (int m = K - 1; m >= 0; --m) {
-                const float xv = at >= 0 ? L::ld(x, (size_t)at * C + ch) : L::ld(cp, (size_t)(row--) * C + ch);
-                acc = fmaf(L::ld(A.p.conv_w, (size_t)ch * K + m), xv, acc);
-                if (at >= 0) at = up[at];
-            }
-            val = siluf_(acc);
-        }
-        (c < D ? qs : (c < 2 * D ? ks : us))[i * D + c % D] = val;
-    }
-    __syncthreads();
-    for (int i = warp; i < n; i += nwarp) {  // L2 norms
-        float sq = 0.f, sk = 0.f;
-        for (int c = lane; c < D; c += 32) {
-            sq = fmaf(qs[i * D + c], qs[i * D + c], sq);
-            sk = fmaf(ks[i * D + c], ks[i * D + c], sk);
-        }
-        sq = tree_warp_sum(sq);
-        sk = tree_warp_sum(sk);
-        const bool nol2 = g.flags & kFlagNoL2;
-        const float rq = nol2 ? g.q_scale : g.q_scale * rsqrtf(sq + g.l2_eps);
-        const float rk = nol2 ? 1.f : rsqrtf(sk + g.l2_eps);
-        for (int c = lane; c < D; c += 32) {
-            qs[i * D + c] *= rq;
-            ks[i * D + c] *= rk;
-        }
-    }
-    __syncthreads();
-    // products of a node's k and q with the k of its line, times the decay between them
-    for (int w = warp; w < n * n; w += nwarp) {
-        const int i = w / n, a = w % n;
-        if (!((anc[i] >> a) & 1ull)) continue;
-        float dk = 0.f, dq = 0.f;
-        for (int c = lane; c < D; c += 32) {
-            dk = fmaf(ks[i * D + c], ks[a * D + c], dk);
-            dq = fmaf(qs[i * D + c], ks[a * D + c], dq);
-        }
-        dk = tree_warp_sum(dk);
-        dq = tree_warp_sum(dq);
-        if (lane == 0) {
-            const float f = expf(sc[4 * i + 2] - sc[4 * a + 2]);
-            pk[i * n + a] = f * dk;
-            pq[i * n + a] = f * dq;
-        }
-    }
-    bool ok = true;
-    if (warp == 0) {
-        ok = mbar_wait(bar, 0);
-        if (!ok) mbar_wait(bar, 0);  // bounded again: let the copies in flight land
-    }
-    ok = __syncthreads_and(ok);
-    if (!ok) {
-        if (tid == 0) report_device_status(kDevWaitTimeout);
-        return;
-    }
-    // S_0 k_i and S_0 q_i: a thread has row r of the state and every (256 / D)-th block of 4 nodes
-    constexpr int NB = 4, PARTS = kTreeThreads / D;
-    const int r = tid % D, part = tid / D;
-    float o_first[kTreeMax / PARTS];  // e^{G_i} S_0 q_i of the thread's nodes
-#pragma unroll
-    for (int blk = 0; blk < kTreeMax / (NB * PARTS); ++blk) {
-        const int i0 = (blk * PARTS + part) * NB;
-        if (i0 < n) {
-            float ak[NB] = {}, aq[NB] = {};
-            for (int c = 0; c < D; c += 4) {
-                const float4 s = *reinterpret_cast<const float4*>(S + r * SS + c);
-#pragma unroll
-                for (int e = 0; e < NB; ++e) {
-                    const int i = min(i0 + e, n - 1);
-                    const float4 kv = *reinterpret_cast<const float4*>(ks + i * D + c);
-                    const float4 qv = *reinterpret_cast<const float4*>(qs + i * D + c);
-                    ak[e] = fmaf(s.x, kv.x, fmaf(s.y, kv.y, fmaf(s.z, kv.z, fmaf(s.w, kv.w, ak[e]))));
-                    aq[e] = fmaf(s.x, qv.x, fmaf(s.y, qv.y, fmaf(s.z, qv.z, fmaf(s.w, qv.w, aq[e]))));
-                }
-            }
+    {
+        constexpr int NB = 3;
+        const int sub = lane / LPN, c4 = (lane % LPN) * 4, groups = (n + NB * NPW - 1) / (NB * NPW);
+#pragma unroll 1
+        for (int unit = warp; unit < 3 * groups; unit += nwarp) {
+            const int kind = unit / groups, i0 = unit % groups * NB * NPW + sub, ch = channel(kind) + c4;
+            float4 v[NB][4];
 #pragma unroll
             for (int e = 0; e < NB; ++e) {
-                const int i = i0 + e;
-                o_first[blk * NB + e] = i < n ? aq[e] * sc[4 * i + 3] : 0.f;
-                if (i < n) us[i * D + r] -= sc[4 * i + 3] * ak[e];  // v_i - e^{G_i} S_0 k_i
+                const int i = min(i0 + e * NPW, n - 1);
+                const int4 t4 = *reinterpret_cast<const int4*>(taps + i * 4);
+                const int tap[4] = {t4.x, t4.y, t4.z, t4.w};
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const int at = raw ? i : tap[t];
+                    v[e][t] = tree_ld4(at < 64 ? x + (size_t)at * C + ch : cp + (size_t)(at - 64) * C + ch);
+                }
+            }
+            float y[NB][4], ss[NB];
+#pragma unroll
+            for (int e = 0; e < NB; ++e) {
+                if (raw) {
+                    y[e][0] = v[e][3].x, y[e][1] = v[e][3].y, y[e][2] = v[e][3].z, y[e][3] = v[e][3].w;
+                } else {
+                    const float4 bias = *reinterpret_cast<const float4*>(ws + 12 * D + kind * D + c4);
+                    y[e][0] = bias.x, y[e][1] = bias.y, y[e][2] = bias.z, y[e][3] = bias.w;
+                }
+            }
+            if (!raw) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const float4 w = *reinterpret_cast<const float4*>(ws + (kind * 4 + t) * D + c4);
+#pragma unroll
+                    for (int e = 0; e < NB; ++e) {
+                        y[e][0] = fmaf(w.x, v[e][t].x, y[e][0]);
+                        y[e][1] = fmaf(w.y, v[e][t].y, y[e][1]);
+                        y[e][2] = fmaf(w.z, v[e][t].z, y[e][2]);
+                        y[e][3] = fmaf(w.w, v[e][t].w, y[e][3]);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < NB; ++e)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) y[e][c] = tree_silu(y[e][c]);
+            }
+#pragma unroll
+            for (int e = 0; e < NB; ++e)
+                ss[e] = fmaf(y[e][0], y[e][0], fmaf(y[e][1], y[e][1], fmaf(y[e][2], y[e][2], y[e][3] * y[e][3])));
+            if (kind < 2) {
+#pragma unroll
+                for (int o = LPN / 2; o > 0; o >>= 1)
+#pragma unroll
+                    for (int e = 0; e < NB; ++e) ss[e] += __shfl_xor_sync(0xffffffffu, ss[e], o);
+            }
+            float* to = (kind == 0 ? qs : (kind == 1 ? ks : us)) + c4;
+#pragma unroll
+            for (int e = 0; e < NB; ++e) {
+                float f = kind < 2 && !(g.flags & kFlagNoL2) ? rsqrtf(ss[e] + g.l2_eps) : 1.f;
+                if (kind == 0) f *= g.q_scale;
+                if (i0 + e * NPW < n)
+                    *reinterpret_cast<float4*>(to + (i0 + e * NPW) * D) = make_float4(y[e][0] * f, y[e][1] * f, y[e][2] * f, y[e][3] * f);
             }
         }
     }
-    __syncthreads();  // every q has been read: its place takes o
+    // the warp's state rows: row rl * 4 + group, columns 4 l8 + 32 c of lane l8 of the group
+    const int l8 = lane & 7, grp = lane >> 3, row0 = warp * (D / 8) + grp;
+    float4 S[RL][RL];
 #pragma unroll
-    for (int blk = 0; blk < kTreeMax / (NB * PARTS); ++blk) {
-        const int i0 = (blk * PARTS + part) * NB;
+    for (int r = 0; r < RL; ++r)
 #pragma unroll
-        for (int e = 0; e < NB; ++e)
-            if (i0 + e < n) qs[(i0 + e) * D + r] = o_first[blk * NB + e];
-    }
+        for (int c = 0; c < RL; ++c)
+            S[r][c] = __ldg(reinterpret_cast<const float4*>(Sg + (size_t)(row0 + r * 4) * D + 4 * l8 + 32 * c));
     __syncthreads();
-    if (tid < D) {  // the line sums, in the order of the nodes: a parent comes before its children
-        for (int i = 0; i < n; ++i) {
-            float su = 0.f, so = 0.f;
-            unsigned long long m = anc[i] & ~(1ull << i);
-            while (m) {
-                const int a = __ffsll((long long)m) - 1;
-                m &= m - 1;
-                const float ua = us[a * D + tid];
-                su = fmaf(pk[i * n + a], ua, su);
-                so = fmaf(pq[i * n + a], ua, so);
-            }
-            const float u = sc[4 * i + 1] * (us[i * D + tid] - su);
-            us[i * D + tid] = u;
-            qs[i * D + tid] += fmaf(pq[i * n + i], u, so);
-        }
-    }
-    __syncthreads();
-    // gated RMSNorm over the v-head, a warp per node
-    const bool outnorm = !(g.flags & kFlagNoOutNorm);
+    // a node's products with the keys of its line, times the decay between them: a warp per node, 8 lanes per ancestor
     for (int i = warp; i < n; i += nwarp) {
-        float ss = 0.f;
-        for (int c = lane; c < D; c += 32) ss = fmaf(qs[i * D + c], qs[i * D + c], ss);
-        ss = tree_warp_sum(ss);
-        const float inv = rsqrtf(ss / (float)D + g.norm_eps);
-        const size_t row = ((size_t)first + i) * Hv * D + (size_t)j * D;
-        for (int c = lane; c < D; c += 32) {
-            float y = qs[i * D + c];
-            if (outnorm) y = y * inv * L::ld(A.p.norm_w, c) * siluf_(L::ld(J.z, row + c));
-            L::st(J.y, row + c, y);
+        const float4 me = nd[i];
+        unsigned long long m = anc[i];
+        const int first_a = __ffsll((long long)m) - 1, start = off[i];
+        for (int at = 0; m; at += 4) {
+            int a = i;  // (the node itself again past the end)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (e == grp && m) a = __ffsll((long long)m) - 1;
+                m &= m - 1;
+            }
+            float2 dk = make_float2(0.f, 0.f), dq = dk;
+#pragma unroll
+            for (int c = 0; c < RL; ++c) {
+                const float4 ka = *reinterpret_cast<const float4*>(ks + a * D + 4 * l8 + 32 * c);
+                dk = tree_dot(*reinterpret_cast<const float4*>(ks + i * D + 4 * l8 + 32 * c), ka, dk);
+                dq = tree_dot(*reinterpret_cast<const float4*>(qs + i * D + 4 * l8 + 32 * c), ka, dq);
+            }
+            float v[2] = {dk.x + dk.y, dq.x + dq.y};
+            const float t = tree_sum8<2>(v, lane), q1 = __shfl_down_sync(0xffffffffu, t, 4);  // lane 0 of a group: k; lane 4: q
+            if (l8 == 0) {
+                if (a == i) {
+                    nd[i].w = q1;
+                } else {
+                    const float f = expf(me.y - nd[a].y);
+                    ent[start + at + grp] = make_float4(me.x * f * t, f * q1, __int_as_float(a * D), 0.f);
+                }
+            }
+        }
+        // the last group is filled up with zeros times the first ancestor's u
+        const int c = __popcll(anc[i]) - 1;
+        if (lane < off[i + 1] - start - c) ent[start + c + lane] = make_float4(0.f, 0.f, __int_as_float(first_a * D), 0.f);
+    }
+    // S_0 k_i and S_0 q_i of the warp's rows (ps and rs replace the conv weights: everybody is past them)
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        float2 d[2 * RL];
+#pragma unroll
+        for (int r = 0; r < 2 * RL; ++r) d[r] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < RL; ++c) {
+            const float4 kv = *reinterpret_cast<const float4*>(ks + i * D + 4 * l8 + 32 * c);
+            const float4 qv = *reinterpret_cast<const float4*>(qs + i * D + 4 * l8 + 32 * c);
+#pragma unroll
+            for (int r = 0; r < RL; ++r) {
+                d[2 * r] = tree_dot(S[r][c], kv, d[2 * r]);
+                d[2 * r + 1] = tree_dot(S[r][c], qv, d[2 * r + 1]);
+            }
+        }
+        float v[2 * RL];
+#pragma unroll
+        for (int r = 0; r < 2 * RL; ++r) v[r] = d[r].x + d[r].y;
+        const float t = tree_sum8<2 * RL>(v, lane);
+        const int which = l8 / (4 / RL);  // the lane's value: row which / 2, with k or q
+        if (l8 % (4 / RL) == 0) ((which & 1) ? rs : ps)[i * D + row0 + (which >> 1) * 4] = t;
+    }
+    __syncthreads();
+    if (tid < D / 2) {  // thread = two state rows: u and o, in the order of the nodes (a parent comes before its children)
+        float2* u = reinterpret_cast<float2*>(us) + tid;
+        constexpr int H = D / 2;
+        int e = 0;
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            const float4 s = nd[i];
+            const int end = off[i + 1];
+            const float2 p = reinterpret_cast<const float2*>(ps)[i * H + tid], r = reinterpret_cast<const float2*>(rs)[i * H + tid];
+            const float2 v = u[i * H];
+            float2 su[2] = {}, so[2] = {};
+#pragma unroll 1
+            for (; e < end; e += 4) {
+                float4 c[4];
+                float2 ua[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) c[q] = ent[e + q];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) ua[q] = u[__float_as_int(c[q].z) / 2];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    su[q & 1] = __ffma2_rn(make_float2(c[q].x, c[q].x), ua[q], su[q & 1]);
+                    so[q & 1] = __ffma2_rn(make_float2(c[q].y, c[q].y), ua[q], so[q & 1]);
+                }
+            }
+            const float2 un = make_float2(s.x * (v.x - s.z * p.x) - (su[0].x + su[1].x), s.x * (v.y - s.z * p.y) - (su[0].y + su[1].y));
+            u[i * H] = un;
+            reinterpret_cast<float2*>(rs)[i * H + tid] =
+                make_float2(fmaf(s.w, un.x, fmaf(s.z, r.x, so[0].x + so[1].x)), fmaf(s.w, un.y, fmaf(s.z, r.y, so[0].y + so[1].y)));
+        }
+    }
+    __syncthreads();
+    // gated RMSNorm over the v-head, an LPN-lane group per node
+    const bool outnorm = !(g.flags & kFlagNoOutNorm);
+    const int sub = lane / LPN, c4 = (lane % LPN) * 4;
+    float4 w = make_float4(1.f, 1.f, 1.f, 1.f);
+    if (outnorm) w = tree_ld4(static_cast<const TA*>(A.p.norm_w) + c4);
+#pragma unroll 2
+    for (int i0 = warp * NPW + sub; i0 - sub < n; i0 += nwarp * NPW) {
+        const int i = min(i0, n - 1);
+        const size_t row = ((size_t)first + i) * Hv * D + (size_t)j * D + c4;
+        float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (outnorm) z = tree_ld4(static_cast<const TA*>(J.z) + row);
+        const float4 o = *reinterpret_cast<const float4*>(rs + i * D + c4);
+        float ss = fmaf(o.x, o.x, fmaf(o.y, o.y, fmaf(o.z, o.z, o.w * o.w)));
+#pragma unroll
+        for (int s = LPN / 2; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
+        float y[4] = {o.x, o.y, o.z, o.w};
+        if (outnorm) {
+            const float inv = rsqrtf(ss / (float)D + g.norm_eps);
+            y[0] *= inv * w.x * tree_silu(z.x);
+            y[1] *= inv * w.y * tree_silu(z.y);
+            y[2] *= inv * w.z * tree_silu(z.z);
+            y[3] *= inv * w.w * tree_silu(z.w);
+        }
+        if (i0 < n) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) L::st(J.y, row + c, y[c]);
         }
     }
 }
 
 // ---- the same on the tensor cores (d = 128, bf16 activations) ---------------------
-// One CTA per (k-head, tree): the k-head's K^ and Q^ of all nodes are made once, as the rows of one operand
-// [K^; Q^] (TF32, K-major, 128-byte swizzle), and multiplied twice:
-//   [K^; Q^] K^T    the products of the nodes' keys and queries with keys (M = 128, N = nm, once), and
-//   S_0 [K^; Q^]^T  per v-head (M = 128 state rows, N = 2 nm), with S_0 as it lies in the pool (fp32, brought by
-//                   tensor TMA 32 columns at a time; the tensor core reads its leading 10 fraction bits, as it does of
-//                   K^ and Q^ rounded).
-// Then a thread has a state row: its S_0 k_i and S_0 q_i come from TMEM, and it walks the nodes in order, each
-// with a list of its ancestors and their two coefficients, keeping u in shared memory (its own column, no
-// barrier); o takes u's place, and all warps finish the nodes' y.  TF32's 2^-11 per operand is a quarter of the
-// bf16 rounding of y; the decays, sums and norms are fp32.  The phases are short and bound by latency, so the state's
-// place in shared memory is kept to half a tile: two CTAs per SM up to 32 nodes.
+// One CTA per (k-head, tree).  With p_j = S_0 k_j, r_j = S_0 q_j and w_j = beta_j (v_j - e^{G_j} p_j), the sums above
+// are linear in w: u = T w with T the inverse of the unit triangular matrix of the ancestors' coefficients, and
+//   o_i = e^{G_i} r_i + sum_j M_ij w_j,   M = (the queries' coefficients) T,
+// with M of n x n per v-head and the same for all 128 state rows.  So (all products TF32, fp32 accumulation):
+//   [K^; Q^] K^T    M = 128, N = nm, once: the products of the nodes' keys and queries with keys;
+//   S_0 [K^; Q^]^T  per v-head, M = 128 state rows, N = 2 nm, S_0 as it lies in the pool (fp32, brought by tensor
+//                   TMA 32 columns at a time; the tensor core reads its leading 10 fraction bits, as it does of K^ and
+//                   Q^ rounded): p and r in TMEM;
+//   r += w M^T      w in TMEM in p's place.
+// M comes from one warp (two above 32 nodes), a lane per column of T, walking the nodes in order with the
+// coefficients of each node's line; it runs ahead of the other warps, which make v, w, o and y.  TF32's 2^-11 per
+// operand is a quarter of the bf16 rounding of y; the decays, T's sums and the norms are fp32.  The phases are short
+// and bound by latency and instructions, so the state's place in shared memory is kept to half a tile: two CTAs
+// per SM up to 32 nodes.
 constexpr int kVtThreads = 288;  // 8 warps and the one that drives the copies and the products
 constexpr int kVtAtom = 16384;   // 128 state rows x 32 columns
 
 struct VtSmem {
-    int S, B, v, ent, gram, node, beta, taps, gate, line, up, off, bar, total;
+    int S, B, v, M, T, ring, gram, w, taps, gate, beta, eg, line, up, bar, total;
 };
 
-// entries of a tree's nodes: a node's ancestors, rounded up to groups of 4
-__host__ __device__ inline int vt_entries(int nm) { return nm * (nm - 1) / 2 + 3 * nm; }
-
-__host__ __device__ inline VtSmem vt_smem(int nm, int bufs) {  // nm: nodes, rounded up to 16
+__host__ __device__ inline VtSmem vt_smem(int nm, int gv, int bufs) {  // nm: nodes, rounded up to 16
+    const int halves = (nm + 31) / 32;
     VtSmem s;
     int o = 0;
-    s.S = o; o += 2 * kVtAtom;                // ring of state atoms
-    s.B = o; o += 2 * nm * 512;               // [K^; Q^]: 4 atoms of 2 nm rows x 128 bytes
-    s.v = o; o += bufs * nm * 512;            // v, then u, then o: [node][row]
-    s.ent = o; o += bufs * vt_entries(nm) * 16;
+    s.S = o; o += 2 * kVtAtom;               // ring of state atoms
+    s.B = o; o += 2 * nm * 512;              // [K^; Q^]: 4 atoms of 2 nm rows x 128 bytes
+    s.M = o; o += 2 * halves * nm * 128;     // M of two v-heads: atoms of nm rows x 32 columns
+    s.v = o; o += bufs * nm * 512;           // v, then o: [node][row]
+    s.T = o; o += halves * nm * 128;         // T: [half][node][32 columns]
+    s.ring = o; o += halves * 2 * 68 * 16;   // coefficients of two nodes' lines
     s.gram = o; o += 2 * nm * (nm + 1) * 4;
-    s.node = o; o += bufs * nm * 16;          // beta, e^G, the node's own coefficient, first entry
-    s.beta = o; o += nm * 8 * 4;              // per (node, v-head of the group)
-    s.taps = o; o += nm * 32;                 // offsets of the conv taps' rows from x
-    s.gate = o; o += nm * 8 * 4;              // log alpha, then its sum along the line
+    s.w = o; o += (2 + gv) * 4 * 128 * 2;    // conv weights of k, q and the v-heads: [4 taps][128]
+    s.taps = o; o += nm * 32;                // offsets of the conv taps' rows from x
+    s.gate = o; o += nm * gv * 4;            // log alpha, then its sum G along the line, per (node, v-head)
+    s.beta = o; o += nm * gv * 4;
+    s.eg = o; o += nm * gv * 4;              // e^G
     s.line = o; o += nm * 8;
     s.up = o; o += nm * 4;
-    s.off = o; o += (nm + 4) * 4;             // first entry of each node
-    s.bar = o; o += 8 * 8;
+    s.bar = o; o += 16 * 8;
     // the Gram product reads 128 rows of each atom, whatever 2 nm is: all of them lie inside the allocation
     s.total = o > s.B + 3 * 2 * nm * 128 + kVtAtom ? o : s.B + 3 * 2 * nm * 128 + kVtAtom;
     return s;
@@ -345,53 +485,98 @@ __device__ __forceinline__ void vt_ld8(uint32_t ta, uint32_t r[8]) {
                  : "r"(ta));
 }
 
-__device__ __forceinline__ void vt_st1(uint32_t ta, float v) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(ta), "r"(__float_as_uint(v)) : "memory");
+__device__ __forceinline__ void vt_st8(uint32_t ta, const float v[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(ta),
+                 "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+                 "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+                 "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+                 : "memory");
+}
+
+// a product with A in TMEM (lane = row, column = k)
+__device__ __forceinline__ void vt_mma_ta(uint32_t d, uint32_t a, uint64_t bd, uint32_t idesc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, 1, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(a), "l"(bd), "r"(idesc)
+        : "memory");
+}
+
+// warp-wide bounded wait that lets the hardware park the warp (a spin would take issue slots from the others)
+__device__ __forceinline__ bool vt_wait(uint64_t* bar, int phase) {
+    const uint32_t addr = smem_u32(bar);
+    long long t0 = 0;
+    for (int i = 0;; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(done)
+            : "r"(addr), "r"((uint32_t)(phase & 1)), "r"(20000)  // up to 20 us at a time
+            : "memory");
+        if (__all_sync(0xffffffffu, done)) return true;
+        const long long t = clock64();
+        if (i == 0) t0 = t;
+        if (__any_sync(0xffffffffu, t - t0 > kWaitLimitCycles)) return false;
+    }
 }
 
 // conv + SiLU of the warp's 128 channels (ch .. ch + 3 of each lane) at the nodes i0 .. i0 + 3, all loads at once.
 // As v: to v[node][4 lane].  As k or q (scale != 0): L2-normalised times scale, to row row0 + node of [K^; Q^].
 // One copy of this code serves every call: the phases run once per CTA, and copies in line were bound by
 // instruction fetch.
-__device__ __noinline__ void vt_conv(const __nv_bfloat16* x, const long long* taps, const __nv_bfloat16* conv_w,
-                                     const __nv_bfloat16* conv_b, int K, int ch, int i0, int n, float* v,
-                                     unsigned char* Bt, int rows, int row0, float scale, float eps) {
+__device__ __noinline__ void vt_conv(const __nv_bfloat16* x, const long long* taps, const uint2* w, const __nv_bfloat16* bias,
+                                     int i0, int n, float* v, unsigned char* Bt, int rows, int row0, float scale, float eps) {
     const int lane = threadIdx.x & 31;
     uint2 u[4][4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const int node = min(i0 + e, n - 1);
 #pragma unroll
-        for (int m = 0; m < 4; ++m) u[e][m] = __ldg(reinterpret_cast<const uint2*>(x + taps[node * 4 + m] + ch));
+        for (int m = 0; m < 4; ++m) u[e][m] = __ldg(reinterpret_cast<const uint2*>(x + taps[node * 4 + m]));
     }
-    float w[4][4], bias[4];
+    float y[4][4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        bias[c] = conv_b ? __bfloat162float(conv_b[ch + c]) : 0.f;
+    for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int m = 0; m < 4; ++m) w[m][c] = m < K ? __bfloat162float(conv_w[(size_t)(ch + c) * K + m]) : 0.f;
-    }
+        for (int c = 0; c < 4; ++c) y[e][c] = bias ? __bfloat162float(bias[c]) : 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        float y[4] = {bias[0], bias[1], bias[2], bias[3]};
+    for (int m = 0; m < 4; ++m) {
+        const uint2 wm = w[m * 32 + lane];
+        const float2 w01 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&wm.x));
+        const float2 w23 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&wm.y));
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
+        for (int e = 0; e < 4; ++e) {
             const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u[e][m].x));
             const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u[e][m].y));
-            y[0] = fmaf(w[m][0], lo.x, y[0]);
-            y[1] = fmaf(w[m][1], lo.y, y[1]);
-            y[2] = fmaf(w[m][2], hi.x, y[2]);
-            y[3] = fmaf(w[m][3], hi.y, y[3]);
+            y[e][0] = fmaf(w01.x, lo.x, y[e][0]);
+            y[e][1] = fmaf(w01.y, lo.y, y[e][1]);
+            y[e][2] = fmaf(w23.x, hi.x, y[e][2]);
+            y[e][3] = fmaf(w23.y, hi.y, y[e][3]);
         }
+    }
+    float ss[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) y[c] = vt_silu(y[c]);
-        if (scale != 0.f) {
-            const float ss = tree_warp_sum(fmaf(y[0], y[0], fmaf(y[1], y[1], fmaf(y[2], y[2], y[3] * y[3]))));
-            const float f = scale * rsqrtf(ss + eps);
-            if (i0 + e < n) tc::st_row4(Bt, rows, row0 + i0 + e, 4 * lane, y[0] * f, y[1] * f, y[2] * f, y[3] * f);
-        } else if (i0 + e < n) {
-            *reinterpret_cast<float4*>(v + (i0 + e) * 128 + 4 * lane) = make_float4(y[0], y[1], y[2], y[3]);
+    for (int e = 0; e < 4; ++e) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[e][c] = vt_silu(y[e][c]);
+        ss[e] = fmaf(y[e][0], y[e][0], fmaf(y[e][1], y[e][1], fmaf(y[e][2], y[e][2], y[e][3] * y[e][3])));
+    }
+    if (scale != 0.f) {
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ss[e] += __shfl_xor_sync(0xffffffffu, ss[e], off);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float f = scale * rsqrtf(ss[e] + eps);
+            if (i0 + e < n)
+                tc::st_row4(Bt, rows, row0 + i0 + e, 4 * lane, y[e][0] * f, y[e][1] * f, y[e][2] * f, y[e][3] * f);
         }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (i0 + e < n)
+                *reinterpret_cast<float4*>(v + (i0 + e) * 128 + 4 * lane) = make_float4(y[e][0], y[e][1], y[e][2], y[e][3]);
     }
 }
 
@@ -416,37 +601,47 @@ __global__ void __launch_bounds__(kVtThreads, 2)
 
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = smem_raw + ((1024 - (tc::smem_addr(smem_raw) & 1023)) & 1023);
-    const VtSmem lay = vt_smem(nm, A.bufs);
+    const VtSmem lay = vt_smem(nm, gv, A.bufs);
     unsigned char* Bt = sm + lay.B;
     float* gram = reinterpret_cast<float*>(sm + lay.gram);
-    float* betas = reinterpret_cast<float*>(sm + lay.beta);
+    bf* ws = reinterpret_cast<bf*>(sm + lay.w);
     long long* taps = reinterpret_cast<long long*>(sm + lay.taps);
     float* gate = reinterpret_cast<float*>(sm + lay.gate);
+    float* betas = reinterpret_cast<float*>(sm + lay.beta);
+    float* eg = reinterpret_cast<float*>(sm + lay.eg);
     unsigned long long* line = reinterpret_cast<unsigned long long*>(sm + lay.line);
     int* up = reinterpret_cast<int*>(sm + lay.up);
-    int* off = reinterpret_cast<int*>(sm + lay.off);
-    uint64_t *full = reinterpret_cast<uint64_t*>(sm + lay.bar), *freed = full + 2, *done = full + 4, *bar_g = full + 6;
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(full + 7);
+    // full, freed: state atoms; done: p and r; w_ready: w and e^G r in TMEM; m_ready: M; o_done: o
+    uint64_t *full = reinterpret_cast<uint64_t*>(sm + lay.bar), *freed = full + 2, *done = full + 4, *w_ready = full + 6,
+             *m_ready = full + 8, *o_done = full + 10, *bar_g = full + 12;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(full + 13);
     const int tcols = nm <= 16 ? 128 : (nm <= 32 ? 256 : 512);  // products of two v-heads, then the Gram matrix
+    const int halves = n > 32 ? 2 : 1, workers = 8 - halves;    // warps of M; the others
     if (tid == 0) {
-        for (int i = 0; i < 7; ++i) mbar_init(full + i, 1);
+        for (int i = 0; i < 13; ++i) mbar_init(full + i, i >= 6 && i < 8 ? 4 : (i >= 8 && i < 10 ? halves : 1));
         fence_mbar_init();
     }
     if (warp == 8) tc::alloc(tslot, tcols);
-    // gates, parents; taps follow the parents
+    // gates and parents; conv weights with the taps outside (a missing tap: 0)
     if (tid < n) {
         const int p = J.parents[first + tid];
         up[tid] = p >= 0 && p < tid ? p : -1;
-        line[tid] = 1ull << tid;
     }
     for (int i = tid; i < n * gv; i += kVtThreads) {
         const int node = i / gv, jj = i % gv;
         const size_t at = (size_t)(first + node) * Hv + j0 + jj;
-        float gl, beta;
         gates(__bfloat162float(static_cast<const bf*>(J.a)[at]), __bfloat162float(static_cast<const bf*>(J.b)[at]),
-              A.p.A_log[j0 + jj], A.p.dt_bias ? A.p.dt_bias[j0 + jj] : 0.f, false, gl, beta);
-        gate[node * 8 + jj] = gl;
-        betas[node * 8 + jj] = beta;
+              A.p.A_log[j0 + jj], A.p.dt_bias ? A.p.dt_bias[j0 + jj] : 0.f, false, gate[i], betas[i]);
+    }
+    auto channel = [&](int what, int i) {  // first channel of k (0), q (1), v of v-head j0 + i (2)
+        return (what == 0 ? Hk + h : (what == 1 ? h : 2 * Hk + j0 + i)) * D;
+    };
+#pragma unroll 4
+    for (int k = tid; k < (2 + gv) * D; k += kVtThreads) {
+        const int what = k / D;
+        const bf* src = static_cast<const bf*>(A.p.conv_w) + (size_t)(channel(min(what, 2), what - 2) + k % D) * K;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) ws[(what * 4 + m) * D + k % D] = m < K ? src[m] : __float2bfloat16_rn(0.f);
     }
     tc::fence_before();
     __syncthreads();
@@ -454,40 +649,45 @@ __global__ void __launch_bounds__(kVtThreads, 2)
     const uint32_t tm = *tslot, tgram = tm + 4 * nm;
     const bf* xb = static_cast<const bf*>(J.x) + first * C;
     const bf* cb = static_cast<const bf*>(J.conv_pool) + (size_t)slot * Km1 * C;
-    if (tid < n) {  // tap K - 1 is the node, then its ancestors, then the conv state's rows from the newest on
-        int at = tid, row = Km1 - 1;
+    // the line of every node and the sum of log alpha along it, a thread per (node, v-head): two pairs a thread at most
+    float sums[2] = {0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int k = tid + e * 256, i = k % nm, jj = k / nm;
+        if (tid < 256 && i < n && jj < gv) {
+            unsigned long long m = 0;
+            for (int at = i; at >= 0;) {
+                m |= 1ull << at;
+                const int next = up[at];
+                sums[e] += gate[at * gv + jj];
+                at = next;
+            }
+            if (jj == 0) line[i] = m;
+        }
+    }
+    if (tid >= 192 && tid - 192 < n) {  // tap K - 1 is the node, then its ancestors, then the conv state's rows, newest first
+        const int i = tid - 192;
+        int at = i, row = Km1 - 1;
         for (int t = K - 1; t >= 0; --t) {
-            taps[tid * 4 + t] = at >= 0 ? (long long)at * C : (cb - xb) + (long long)(row--) * C;
+            taps[i * 4 + t] = at >= 0 ? (long long)at * C : (cb - xb) + (long long)(row--) * C;
             if (at >= 0) at = up[at];
         }
-        for (int t = K; t < 4; ++t) taps[tid * 4 + t] = (long long)tid * C;  // (weight 0)
+        for (int t = K; t < 4; ++t) taps[i * 4 + t] = (long long)i * C;  // (weight 0)
     }
     __syncthreads();
-    // lines, and the sums of log alpha along them, by doubling: a thread has a node and v-heads jj, jj + 4
-#pragma unroll 1
-    for (int reach = 1; reach < n; reach <<= 1) {
-        const int i = tid & 63, jj = tid >> 6;
-        int p = -1, pp = -1;
-        unsigned long long m = 0;
-        float s0 = 0.f, s1 = 0.f;
-        if (i < n && jj < 4 && (p = up[i]) >= 0) {
-            pp = up[p];
-            m = line[p];
-            if (jj < gv) s0 = gate[p * 8 + jj];
-            if (jj + 4 < gv) s1 = gate[p * 8 + jj + 4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {  // (read after the next barriers)
+        const int k = tid + e * 256, i = k % nm, jj = k / nm;
+        if (tid < 256 && i < n && jj < gv) {
+            gate[i * gv + jj] = sums[e];
+            eg[i * gv + jj] = __expf(sums[e]);
         }
-        __syncthreads();
-        if (p >= 0) {
-            if (jj < gv) gate[i * 8 + jj] += s0;
-            if (jj + 4 < gv) gate[i * 8 + jj + 4] += s1;
-            if (jj == 0) {
-                line[i] |= m;
-                up[i] = pp;
-            }
-        }
-        __syncthreads();
     }
     bool ok = true;
+    auto wait = [&](uint64_t* bar, int phase) {  // warp-wide; after a failure nothing waits any more
+        if (ok) ok = vt_wait(bar, phase);
+        return ok;
+    };
     if (warp == 8) {
         // ---- copies and products: the state of each v-head in 4 atoms through a ring of two ---------
         const int atoms = 4 * gv;
@@ -501,98 +701,70 @@ __global__ void __launch_bounds__(kVtThreads, 2)
         }
         __syncwarp();
         named_bar_sync(2, kVtThreads);  // [K^; Q^] is there
-        const uint64_t db = tc::sdesc(tc::smem_addr(Bt)), ds = tc::sdesc(tc::smem_addr(sm + lay.S));
-        const uint32_t bstep = (uint32_t)(2 * nm * 128) >> 4;
-        const uint32_t id_g = tc::idesc_tf32(128, nm), id_s = tc::idesc_tf32(128, 2 * nm);
+        const uint64_t db = tc::sdesc(tc::smem_addr(Bt)), ds = tc::sdesc(tc::smem_addr(sm + lay.S)),
+                       dm = tc::sdesc(tc::smem_addr(sm + lay.M));
+        const uint32_t bstep = (uint32_t)(2 * nm * 128) >> 4, mstep = (uint32_t)(nm * 128) >> 4;
+        const uint32_t id_n = tc::idesc_tf32(128, nm), id_2n = tc::idesc_tf32(128, 2 * nm);
         if (vt_elect()) {  // lanes are the rows of [K^; Q^] (what lies past them is never read), columns the keys
 #pragma unroll 4
             for (int k = 0; k < 16; ++k)
-                vt_mma(tgram, db + (k >> 2) * bstep + (k & 3) * 2, db + (k >> 2) * bstep + (k & 3) * 2, id_g, k > 0);
+                vt_mma(tgram, db + (k >> 2) * bstep + (k & 3) * 2, db + (k >> 2) * bstep + (k & 3) * 2, id_n, k > 0);
             tc::commit(bar_g);
         }
         __syncwarp();
+        // r += w M^T of v-head i
+        auto finish = [&](int i) {
+            if (!wait(w_ready + (i & 1), i >> 1) || !wait(m_ready + (i & 1), i >> 1)) return;
+            tc::fence_after();
+            if (vt_elect()) {
+                const uint32_t d = tm + (i & 1) * 2 * nm;
+                for (int k = 0; k < (n + 7) / 8; ++k)
+                    vt_mma_ta(d + nm, d + 8 * k, dm + ((i & 1) * ((nm + 31) / 32) + (k >> 2)) * mstep + (k & 3) * 2, id_n);
+                tc::commit(o_done + (i & 1));
+            }
+            __syncwarp();
+        };
 #pragma unroll 1
         for (int a = 0; a < atoms && ok; ++a) {
             const int i = a >> 2;
-            if ((a & 3) == 0 && i >= 2) named_bar_sync(3, 160);  // v-head i - 2 has been read out of TMEM
-            ok = __all_sync(0xffffffffu, mbar_wait(full + (a & 1), (uint32_t)((a >> 1) & 1)));
-            if (!ok) break;
+            if ((a & 3) == 0 && i >= 1) finish(i - 1);
+            if ((a & 3) == 0 && i >= 2 && ok) named_bar_sync(3, 160);  // o of v-head i - 2 has been read out of TMEM
+            if (!wait(full + (a & 1), a >> 1)) break;
             if (vt_elect()) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     vt_mma(tm + (i & 1) * 2 * nm, ds + (uint32_t)(((a & 1) * kVtAtom) >> 4) + k * 2,
-                           db + (a & 3) * bstep + k * 2, id_s, (a & 3) > 0 || k > 0);
+                           db + (a & 3) * bstep + k * 2, id_2n, (a & 3) > 0 || k > 0);
                 tc::commit(freed + (a & 1));
                 if ((a & 3) == 3) tc::commit(done + (i & 1));
             }
             __syncwarp();
             if (a + 2 < atoms) {
-                ok = __all_sync(0xffffffffu, mbar_wait(freed + (a & 1), (uint32_t)((a >> 1) & 1)));
-                if (!ok) break;
+                if (!wait(freed + (a & 1), a >> 1)) break;
                 if (lane == 0) load(a + 2);
                 __syncwarp();
             }
         }
+        if (ok) finish(gv - 1);
         if (!ok) {  // let the copies in flight land (bounded again); the others' waits give up by themselves
             for (int i = 0; i < 2; ++i) mbar_wait(full + i, 0);
             if (lane == 0) report_device_status(kDevWaitTimeout);
         }
     } else {
-        if (warp == 7) {  // entries before each node: scan of the numbers of proper ancestors, in groups of 4
-            int base = 0;
-            for (int i0 = 0; i0 < nm; i0 += 32) {
-                const int i = i0 + lane;
-                int c = i < n ? (__popcll(line[i]) + 2) / 4 * 4 : 0;
-#pragma unroll
-                for (int s = 1; s < 32; s <<= 1) {
-                    const int v = __shfl_up_sync(0xffffffffu, c, s);
-                    if (lane >= s) c += v;
-                }
-                if (i < nm) off[i + 1] = base + c;
-                base += __shfl_sync(0xffffffffu, c, 31);
-            }
-            if (lane == 0) off[0] = 0;
-        }
         auto vbuf = [&](int i) { return reinterpret_cast<float*>(sm + lay.v) + (i % A.bufs) * nm * D; };
-        // batches of 4 nodes: of k, q and the first v-head's v by all warps, then of the next v-heads' v
-        const int batches = (n + 3) / 4;
-        auto conv = [&](int what, int i, int batch) {  // what: 0 k, 1 q, 2 v of v-head j0 + i
-            vt_conv(xb, taps, static_cast<const bf*>(A.p.conv_w), static_cast<const bf*>(A.p.conv_b), K,
-                    (what == 0 ? (Hk + h) * D : (what == 1 ? h * D : (2 * Hk + j0 + i) * D)) + 4 * lane, 4 * batch, n,
-                    vbuf(i), Bt, 2 * nm, what == 1 ? nm : 0, what == 0 ? 1.f : (what == 1 ? g.q_scale : 0.f), g.l2_eps);
+        const int batches = (n + 3) / 4;  // of 4 nodes
+        auto conv = [&](int what, int i, int batch) {
+            const int ch = channel(what, i) + 4 * lane;
+            vt_conv(xb + ch, taps, reinterpret_cast<const uint2*>(ws + (what + i) * 4 * D),
+                    A.p.conv_b ? static_cast<const bf*>(A.p.conv_b) + ch : nullptr, 4 * batch, n, vbuf(i), Bt, 2 * nm,
+                    what == 1 ? nm : 0, what == 0 ? 1.f : (what == 1 ? g.q_scale : 0.f), g.l2_eps);
         };
 #pragma unroll 1
         for (int k = warp; k < 2 * batches; k += 8) conv(k & 1, 0, k >> 1);
         fence_proxy_async_smem();
         named_bar_sync(2, kVtThreads);
-        // coefficients of v-head j0 + i: a thread per (node, ancestor)
-        auto make_entries = [&](int i, int t0, int nt) {
-            float4* ent = reinterpret_cast<float4*>(sm + lay.ent) + (i % A.bufs) * vt_entries(nm);
-            float4* nd = reinterpret_cast<float4*>(sm + lay.node) + (i % A.bufs) * nm;
-            const int shift = nm <= 16 ? 4 : (nm <= 32 ? 5 : 6);
-#pragma unroll 1
-            for (int k = tid - t0; k < n << shift; k += nt) {
-                const int node = k >> shift, a = k & ((1 << shift) - 1);
-                const unsigned long long m = line[node];
-                if (a > node || !((m >> a) & 1ull)) continue;
-                const float G = gate[node * 8 + i], beta = betas[node * 8 + i];
-                const float gq = gram[(nm + node) * (nm + 1) + a];
-                if (a == node) {
-                    nd[node] = make_float4(beta, __expf(G), gq, 0.f);
-                    // the last group is filled up with zeros times the first ancestor's u
-                    const int c = __popcll(m) - 1, first_a = __ffsll((long long)m) - 1;
-                    for (int e = off[node] + c; e < off[node + 1]; ++e)
-                        ent[e] = make_float4(0.f, 0.f, __int_as_float(first_a * D), 0.f);
-                } else {
-                    const float f = __expf(G - gate[a * 8 + i]);
-                    ent[off[node] + __popcll(m & ((1ull << a) - 1ull))] =
-                        make_float4(beta * f * gram[node * (nm + 1) + a], f * gq, __int_as_float(a * D), 0.f);
-                }
-            }
-        };
-        if (warp < 4 && 32 * warp < 2 * nm) {
-            ok = __all_sync(0xffffffffu, mbar_wait(bar_g, 0));
-            if (ok) {
+        if (warp < 4 && 32 * warp < 2 * nm) {  // the Gram matrix into shared memory
+            if (wait(bar_g, 0)) {
                 tc::fence_after();
                 const int row = 32 * warp + lane;
 #pragma unroll 1
@@ -606,121 +778,196 @@ __global__ void __launch_bounds__(kVtThreads, 2)
                 }
             }
         }
-        for (int i = 0; i < gv; ++i) {
-            float* v = vbuf(i);
-            if (i == 0 || A.bufs == 1) {
+        named_bar_sync(1, 256);
+        if (warp >= workers) {
+            // ---- M of every v-head: column 32 half + lane ------------------------------------------
+            const int half = warp - workers;
+            float* T = reinterpret_cast<float*>(sm + lay.T) + half * nm * 32 + lane;
+            float4* ring = reinterpret_cast<float4*>(sm + lay.ring) + half * 2 * 68;
 #pragma unroll 1
-                for (int k = warp; k < batches; k += 8) conv(2, i, k);
-                if (i == 0) named_bar_sync(1, 256);  // the Gram matrix is there
-                make_entries(i, 0, 256);
-                named_bar_sync(1, 256);
-            }
-            if (warp < 4) {
-                float* u = v + 32 * warp + lane;
-                const float4* ent = reinterpret_cast<const float4*>(sm + lay.ent) + (i % A.bufs) * vt_entries(nm);
-                const float4* nd = reinterpret_cast<const float4*>(sm + lay.node) + (i % A.bufs) * nm;
-                const uint32_t tr = tc::taddr(tm, 32 * warp, (i & 1) * 2 * nm);
-                if (ok) ok = __all_sync(0xffffffffu, mbar_wait(done + (i & 1), (uint32_t)((i >> 1) & 1)));
-                tc::fence_after();
-                // w_i = beta_i (v_i - e^{G_i} S_0 k_i) in v's place
-#pragma unroll 1
-                for (int c0 = 0; c0 < n; c0 += 8) {
-                    uint32_t rk[8];
-                    vt_ld8(tr + c0, rk);
-                    tc::ld_wait();
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        if (c0 + c < n) {
-                            const float4 s = nd[c0 + c];
-                            u[(c0 + c) * D] = s.x * (u[(c0 + c) * D] - s.y * __uint_as_float(rk[c]));
+            for (int i = 0; i < gv; ++i) {
+                unsigned char* Mt = sm + lay.M + ((i & 1) * ((nm + 31) / 32) + half) * nm * 128;
+                if (i >= 2) wait(o_done + (i & 1), (i - 2) >> 1);  // M's place is free
+                // coefficients of a node's proper ancestors, a lane per ancestor, filled up to a multiple of 4 with zeros
+                // times the first one's row; returns their number, sets the node's own
+                auto coefficients = [&](int node, float& own) -> int {
+                    const unsigned long long m = line[node] & ~(1ull << node);
+                    const float G = gate[node * gv + i], beta = betas[node * gv + i];
+                    float4* to = ring + (node & 1) * 68;
+                    const float *gk = gram + node * (nm + 1), *gq = gram + (nm + node) * (nm + 1);
+                    own = gq[node];
+                    const int c = __popcll(m), up4 = (c + 3) & ~3;
+                    for (int a = lane; a < node; a += 32) {
+                        if ((m >> a) & 1ull) {
+                            const float f = __expf(G - gate[a * gv + i]);
+                            to[__popcll(m & ((1ull << a) - 1ull))] =
+                                make_float4(beta * f * gk[a], f * gq[a], __int_as_float(a * 32), 0.f);
                         }
                     }
-                }
-                // u_i = w_i - sum of the ancestors' terms; the line's part of o_i replaces S_0 k_i
-                int e = 0;
-                float4 s = nd[0];
-                float wi = u[0];
+                    if (lane >= 28 && c + lane - 28 < up4)
+                        to[c + lane - 28] = make_float4(0.f, 0.f, __int_as_float((__ffsll((long long)m) - 1) * 32), 0.f);
+                    return up4;
+                };
+                float own, own_next = 0.f;
+                int cnt = coefficients(0, own), cnt_next = 0;
+                __syncwarp();
 #pragma unroll 1
                 for (int node = 0; node < n; ++node) {
-                    const int end = off[node + 1], nx = min(node + 1, n - 1);
-                    const float4 s_next = nd[nx];
-                    const float w_next = u[nx * D];
+                    if (node + 1 < n) cnt_next = coefficients(node + 1, own_next);
+                    const float4* from = ring + (node & 1) * 68;
                     float su[4] = {}, so[4] = {};
 #pragma unroll 1
-                    for (; e < end; e += 4) {
+                    for (int e = 0; e < cnt; e += 4) {
                         float4 k[4];
-                        float ua[4];
+                        float ta[4];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) k[q] = ent[e + q];
+                        for (int q = 0; q < 4; ++q) k[q] = from[e + q];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) ua[q] = u[__float_as_int(k[q].z)];
+                        for (int q = 0; q < 4; ++q) ta[q] = T[__float_as_int(k[q].z)];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            su[q] = fmaf(k[q].x, ua[q], su[q]);
-                            so[q] = fmaf(k[q].y, ua[q], so[q]);
+                            su[q] = fmaf(k[q].x, ta[q], su[q]);
+                            so[q] = fmaf(k[q].y, ta[q], so[q]);
                         }
                     }
-                    const float un = wi - ((su[0] + su[1]) + (su[2] + su[3]));
-                    u[node * D] = un;
-                    vt_st1(tr + node, fmaf(s.z, un, (so[0] + so[1]) + (so[2] + so[3])));
-                    s = s_next;
-                    wi = w_next;
+                    const float t = (node == 32 * half + lane ? 1.f : 0.f) - ((su[0] + su[1]) + (su[2] + su[3]));
+                    T[node * 32] = t;
+                    tc::st_elem(Mt, nm, node, lane, fmaf(own, t, (so[0] + so[1]) + (so[2] + so[3])));
+                    __syncwarp();  // the next node's coefficients are written, this one's are read
+                    own = own_next;
+                    cnt = cnt_next;
                 }
-                tc::st_wait();
-                // o_i in u's place (its own column: nobody else reads u)
-#pragma unroll 1
-                for (int c0 = 0; c0 < n; c0 += 8) {
-                    uint32_t ro[8], rq[8];
-                    vt_ld8(tr + c0, ro);
-                    vt_ld8(tr + nm + c0, rq);
-                    tc::ld_wait();
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        if (c0 + c < n)
-                            u[(c0 + c) * D] = fmaf(nd[c0 + c].y, __uint_as_float(rq[c]), __uint_as_float(ro[c]));
-                }
-                tc::fence_before();
-            } else if (i + 1 < gv && A.bufs == 2) {
-#pragma unroll 1
-                for (int k = warp - 4; k < batches; k += 4) conv(2, i + 1, k);
-                make_entries(i + 1, 128, 128);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(m_ready + (i & 1));
             }
-            named_bar_sync(1, 256);
-            if (warp < 4 && i + 2 < gv) asm volatile("bar.arrive 3, 160;" ::: "memory");  // this v-head's columns are free
-            // gated RMSNorm, a warp per node, four channels to a lane
-            {
+        } else {
+            for (int i = 0; i < gv; ++i) {
+                float* v = vbuf(i);
+                if (i == 0 || A.bufs == 1) {
+#pragma unroll 1
+                    for (int k = warp; k < batches; k += workers) conv(2, i, k);
+                    named_bar_sync(1, 32 * workers);
+                }
+                if (warp < 4) {
+                    // ---- thread = state row: w and e^G r, then o in v's place (its own column) ------------
+                    float* u = v + 32 * warp + lane;
+                    const uint32_t tr = tc::taddr(tm, 32 * warp, (i & 1) * 2 * nm);
+                    unsigned long long bad = 0ull;  // nodes whose w is an infinity or NaN here
+                    wait(done + (i & 1), i >> 1);
+                    tc::fence_after();
+#pragma unroll 1
+                    for (int c0 = 0; c0 < n; c0 += 8) {
+                        uint32_t rk[8], rq[8];
+                        vt_ld8(tr + c0, rk);
+                        vt_ld8(tr + nm + c0, rq);
+                        float be[8], e[8], vi[8];
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const int node = min(c0 + c, n - 1);
+                            be[c] = betas[node * gv + i];
+                            e[c] = eg[node * gv + i];
+                            vi[c] = u[node * D];
+                        }
+                        tc::ld_wait();
+                        float wv[8], ro[8];
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const float w = be[c] * (vi[c] - e[c] * __uint_as_float(rk[c]));
+                            ro[c] = e[c] * __uint_as_float(rq[c]);
+                            // M is 0 off the line, but 0 times an infinity or NaN is not: those are added below
+                            const bool fine = isfinite(w) && c0 + c < n;
+                            wv[c] = fine ? tc::to_tf32_rn(w) : 0.f;
+                            if (!fine && c0 + c < n) {
+                                bad |= 1ull << (c0 + c);
+                                u[(c0 + c) * D] = w;
+                            }
+                        }
+                        vt_st8(tr + c0, wv);
+                        vt_st8(tr + nm + c0, ro);
+                    }
+                    tc::st_wait();
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(w_ready + (i & 1));
+                    wait(o_done + (i & 1), i >> 1);
+                    tc::fence_after();
+                    const unsigned char* Mt = sm + lay.M + (i & 1) * ((nm + 31) / 32) * nm * 128;
+#pragma unroll 1
+                    for (int c0 = (n - 1) & ~7; c0 >= 0; c0 -= 8) {  // from the last node on: see below
+                        uint32_t ro[8];
+                        vt_ld8(tr + nm + c0, ro);
+                        tc::ld_wait();
+                        if (bad) {
+                            // a line's nodes come before its end, so their w are still there
+                            for (int node = min(c0 + 7, n - 1); node >= c0; --node) {
+                                float more = 0.f;
+                                for (unsigned long long m = bad & line[node]; m; m &= m - 1) {
+                                    const int a = __ffsll((long long)m) - 1;
+                                    more = fmaf(*reinterpret_cast<const float*>(Mt + tc::sw_off(nm, node, a)), u[a * D], more);
+                                }
+                                float o = 0.f;
+#pragma unroll
+                                for (int c = 0; c < 8; ++c)
+                                    if (c0 + c == node) o = __uint_as_float(ro[c]);
+                                u[node * D] = o + more;
+                            }
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+                                if (c0 + c < n) u[(c0 + c) * D] = __uint_as_float(ro[c]);
+                        }
+                        __syncwarp();
+                    }
+                    tc::fence_before();
+                } else if (i + 1 < gv && A.bufs == 2) {
+#pragma unroll 1
+                    for (int k = warp - 4; k < batches; k += workers - 4) conv(2, i + 1, k);
+                }
+                named_bar_sync(1, 32 * workers);
+                if (warp < 4 && i + 2 < gv) asm volatile("bar.arrive 3, 160;" ::: "memory");  // this v-head's columns are free
+                // gated RMSNorm, a warp per node, two nodes at once, four channels to a lane
                 const int j = j0 + i;
                 const uint2 nw = __ldg(reinterpret_cast<const uint2*>(A.p.norm_w) + lane);
                 const float2 w01 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&nw.x));
                 const float2 w23 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&nw.y));
 #pragma unroll 1
-                for (int i0 = warp; i0 < n; i0 += 32) {
-                    uint2 zr[4];
+                for (int i0 = warp; i0 < n; i0 += 2 * workers) {
+                    uint2 zr[2];
+                    float4 o[2];
+                    float ss[2];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
+                    for (int q = 0; q < 2; ++q)
                         zr[q] = __ldg(reinterpret_cast<const uint2*>(static_cast<const bf*>(J.z) +
-                                                                    ((size_t)(first + min(i0 + 8 * q, n - 1)) * Hv + j) * D) + lane);
+                                                                    ((size_t)(first + min(i0 + workers * q, n - 1)) * Hv + j) * D) + lane);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int node = i0 + 8 * q;
-                        if (node >= n) break;
-                        const float4 o = *reinterpret_cast<const float4*>(v + node * D + 4 * lane);
-                        const float ss = tree_warp_sum(fmaf(o.x, o.x, fmaf(o.y, o.y, fmaf(o.z, o.z, o.w * o.w))));
-                        const float inv = rsqrtf(ss / (float)D + g.norm_eps);
+                    for (int q = 0; q < 2; ++q) {
+                        o[q] = *reinterpret_cast<const float4*>(v + min(i0 + workers * q, n - 1) * D + 4 * lane);
+                        ss[q] = fmaf(o[q].x, o[q].x, fmaf(o[q].y, o[q].y, fmaf(o[q].z, o[q].z, o[q].w * o[q].w)));
+                    }
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) ss[q] += __shfl_xor_sync(0xffffffffu, ss[q], off);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const int node = i0 + workers * q;
+                        const float inv = rsqrtf(ss[q] / (float)D + g.norm_eps);
                         const float2 z01 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&zr[q].x));
                         const float2 z23 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&zr[q].y));
-                        const __nv_bfloat162 y01 = __floats2bfloat162_rn(o.x * inv * w01.x * vt_silu(z01.x),
-                                                                         o.y * inv * w01.y * vt_silu(z01.y));
-                        const __nv_bfloat162 y23 = __floats2bfloat162_rn(o.z * inv * w23.x * vt_silu(z23.x),
-                                                                         o.w * inv * w23.y * vt_silu(z23.y));
+                        const __nv_bfloat162 y01 = __floats2bfloat162_rn(o[q].x * inv * w01.x * vt_silu(z01.x),
+                                                                         o[q].y * inv * w01.y * vt_silu(z01.y));
+                        const __nv_bfloat162 y23 = __floats2bfloat162_rn(o[q].z * inv * w23.x * vt_silu(z23.x),
+                                                                         o[q].w * inv * w23.y * vt_silu(z23.y));
                         uint2 out;
                         memcpy(&out.x, &y01, 4);
                         memcpy(&out.y, &y23, 4);
-                        if (ok) *(reinterpret_cast<uint2*>(static_cast<bf*>(J.y) + ((size_t)(first + node) * Hv + j) * D) + lane) = out;
+                        if (ok && node < n)
+                            *(reinterpret_cast<uint2*>(static_cast<bf*>(J.y) + ((size_t)(first + node) * Hv + j) * D) + lane) = out;
                     }
                 }
+                if (i + 1 < gv && A.bufs == 1) named_bar_sync(1, 32 * workers);  // o is read: its place takes the next v
             }
-            if (i + 1 < gv && A.bufs == 1) named_bar_sync(1, 256);  // o is read: its place takes the next v
         }
     }
     tc::fence_before();
@@ -769,9 +1016,9 @@ cudaError_t launch_verify_tc(const Geom& g, const LayerParams& p, const TreeJob&
     if ((long)job.B * g.Hk < sm_count()) A.gv = 1;  // few trees: a CTA per v-head
     if (A.gv == 1) A.bufs = 1;
     const int room = A.nm > 32 ? 227 * 1024 : 113 * 1024;  // two CTAs per SM (1 KB of each one's share is the system's)
-    if (vt_smem(A.nm, A.bufs).total + 1024 > room) A.bufs = 1;
+    if (vt_smem(A.nm, A.gv, A.bufs).total + 1024 > room) A.bufs = 1;
     return launch_pdl(k_tree_verify_tc, dim3((unsigned)(g.Hv / A.gv), (unsigned)job.B), dim3(kVtThreads),
-                      (size_t)vt_smem(A.nm, A.bufs).total + 1024, st, map, A);
+                      (size_t)vt_smem(A.nm, A.gv, A.bufs).total + 1024, st, map, A);
 }
 
 // ---- commit ---------------------------------------------------------------------
