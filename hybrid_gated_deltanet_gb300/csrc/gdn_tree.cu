@@ -248,6 +248,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) k_tree_verify(const __grid_co
             if (!raw) {
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
+                    if (t < 4 - K) continue;
                     const float4 w = *reinterpret_cast<const float4*>(ws + (kind * 4 + t) * D + c4);
 #pragma unroll
                     for (int e = 0; e < NB; ++e) {
@@ -429,27 +430,34 @@ constexpr int kVtThreads = 288;  // 8 warps and the one that drives the copies a
 constexpr int kVtAtom = 16384;   // 128 state rows x 32 columns
 
 struct VtSmem {
-    int S, B, v, M, T, ring, gram, w, taps, gate, beta, eg, line, up, bar, total;
+    int S, B, M, v, gram, ent, who, w, own, taps, gate, beta, eg, line, up, off, bar, total;
 };
 
-__host__ __device__ inline VtSmem vt_smem(int nm, int gv, int bufs) {  // nm: nodes, rounded up to 16
-    const int halves = (nm + 31) / 32;
+// entries of a tree's nodes: a node's proper ancestors, rounded up to pairs
+__host__ __device__ inline int vt_entries(int nm) { return nm * (nm - 1) / 2 + nm; }
+
+__host__ __device__ inline VtSmem vt_smem(int nm, int gv) {  // nm: nodes, rounded up to 16
+    const int halves = (nm + 31) / 32, two = gv > 1 ? 2 : 1;   // v-heads are taken two at a time
     VtSmem s;
     int o = 0;
     s.S = o; o += 2 * kVtAtom;               // ring of state atoms
     s.B = o; o += 2 * nm * 512;              // [K^; Q^]: 4 atoms of 2 nm rows x 128 bytes
-    s.M = o; o += 2 * halves * nm * 128;     // M of two v-heads: atoms of nm rows x 32 columns
-    s.v = o; o += bufs * nm * 512;           // v, then o: [node][row]
-    s.T = o; o += halves * nm * 128;         // T: [half][node][32 columns]
-    s.ring = o; o += halves * 2 * 68 * 16;   // coefficients of two nodes' lines
-    s.gram = o; o += 2 * nm * (nm + 1) * 4;
-    s.w = o; o += (2 + gv) * 4 * 128 * 2;    // conv weights of k, q and the v-heads: [4 taps][128]
-    s.taps = o; o += nm * 32;                // offsets of the conv taps' rows from x
+    s.M = o; o += two * halves * nm * 128;   // M of two v-heads: atoms of nm rows x 32 columns
+    s.v = o; o += nm * 512;                  // v, then o: [node][row]; at first, from M on: raw q, k of [K - 1 + n] rows
+    if (o < s.M + (nm + 3) * 512) o = s.M + (nm + 3) * 512;
+    s.gram = o;                              // the products of the nodes' k and q with keys; then T: [v-head][half][node][32]
+    o += 2 * nm * (nm + 1) * 4 > two * halves * nm * 128 ? 2 * nm * (nm + 1) * 4 : two * halves * nm * 128;
+    s.ent = o; o += two * vt_entries(nm) * 8;         // two coefficients per (node, proper ancestor)
+    s.who = o; o += (vt_entries(nm) + 15) / 16 * 16;  // and that ancestor
+    s.w = o; o += (2 + two) * 4 * 128 * 2;   // conv weights of k, q and two v-heads: [4 taps][128]
+    s.own = o; o += nm * 4;                  // q_i . k_i
+    s.taps = o; o += nm * 16;                // rows of the conv taps: a node, or 64 + a row of the conv state
     s.gate = o; o += nm * gv * 4;            // log alpha, then its sum G along the line, per (node, v-head)
     s.beta = o; o += nm * gv * 4;
     s.eg = o; o += nm * gv * 4;              // e^G
     s.line = o; o += nm * 8;
     s.up = o; o += nm * 4;
+    s.off = o; o += (nm + 4) * 4;            // first entry of each node
     s.bar = o; o += 16 * 8;
     // the Gram product reads 128 rows of each atom, whatever 2 nm is: all of them lie inside the allocation
     s.total = o > s.B + 3 * 2 * nm * 128 + kVtAtom ? o : s.B + 3 * 2 * nm * 128 + kVtAtom;
@@ -460,7 +468,7 @@ struct VtArgs {
     Geom g;
     LayerParams p;
     TreeJob job;
-    int nm, gv, bufs;  // gv: v-heads per CTA (G, or 1 where that fills the card better)
+    int nm, gv;  // gv: v-heads per CTA (G, or 1 where that fills the card better)
 };
 
 __device__ __forceinline__ float vt_silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
@@ -524,15 +532,18 @@ __device__ __forceinline__ bool vt_wait(uint64_t* bar, int phase) {
 // As v: to v[node][4 lane].  As k or q (scale != 0): L2-normalised times scale, to row row0 + node of [K^; Q^].
 // One copy of this code serves every call: the phases run once per CTA, and copies in line were bound by
 // instruction fetch.
-__device__ __noinline__ void vt_conv(const __nv_bfloat16* x, const long long* taps, const uint2* w, const __nv_bfloat16* bias,
-                                     int i0, int n, float* v, unsigned char* Bt, int rows, int row0, float scale, float eps) {
+__device__ __noinline__ void vt_conv(const __nv_bfloat16* x, const __nv_bfloat16* state, int C, const int4* taps, const uint2* w,
+                                     const __nv_bfloat16* bias, int dead, int i0, int n, float* v, unsigned char* Bt, int rows,
+                                     int row0, float scale, float eps) {
     const int lane = threadIdx.x & 31;
     uint2 u[4][4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const int node = min(i0 + e, n - 1);
+        const int4 t4 = taps[min(i0 + e, n - 1)];
+        const int tap[4] = {t4.x, t4.y, t4.z, t4.w};
 #pragma unroll
-        for (int m = 0; m < 4; ++m) u[e][m] = __ldg(reinterpret_cast<const uint2*>(x + taps[node * 4 + m]));
+        for (int m = 0; m < 4; ++m)  // (x and state lie in global or in shared memory)
+            u[e][m] = *reinterpret_cast<const uint2*>(tap[m] < 64 ? x + (size_t)tap[m] * C : state + (size_t)(tap[m] - 64) * C);
     }
     float y[4][4];
 #pragma unroll
@@ -541,6 +552,7 @@ __device__ __noinline__ void vt_conv(const __nv_bfloat16* x, const long long* ta
         for (int c = 0; c < 4; ++c) y[e][c] = bias ? __bfloat162float(bias[c]) : 0.f;
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
+        if (m < dead) continue;  // a tap that d_conv < 4 does not have
         const uint2 wm = w[m * 32 + lane];
         const float2 w01 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&wm.x));
         const float2 w23 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&wm.y));
@@ -601,27 +613,49 @@ __global__ void __launch_bounds__(kVtThreads, 2)
 
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = smem_raw + ((1024 - (tc::smem_addr(smem_raw) & 1023)) & 1023);
-    const VtSmem lay = vt_smem(nm, gv, A.bufs);
+    const VtSmem lay = vt_smem(nm, gv);
     unsigned char* Bt = sm + lay.B;
+    unsigned char* who = sm + lay.who;
     float* gram = reinterpret_cast<float*>(sm + lay.gram);
+    float2* ent = reinterpret_cast<float2*>(sm + lay.ent);
     bf* ws = reinterpret_cast<bf*>(sm + lay.w);
-    long long* taps = reinterpret_cast<long long*>(sm + lay.taps);
+    float* own = reinterpret_cast<float*>(sm + lay.own);
+    int4* taps = reinterpret_cast<int4*>(sm + lay.taps);
     float* gate = reinterpret_cast<float*>(sm + lay.gate);
     float* betas = reinterpret_cast<float*>(sm + lay.beta);
     float* eg = reinterpret_cast<float*>(sm + lay.eg);
     unsigned long long* line = reinterpret_cast<unsigned long long*>(sm + lay.line);
     int* up = reinterpret_cast<int*>(sm + lay.up);
+    int* off = reinterpret_cast<int*>(sm + lay.off);
     // full, freed: state atoms; done: p and r; w_ready: w and e^G r in TMEM; m_ready: M; o_done: o
     uint64_t *full = reinterpret_cast<uint64_t*>(sm + lay.bar), *freed = full + 2, *done = full + 4, *w_ready = full + 6,
              *m_ready = full + 8, *o_done = full + 10, *bar_g = full + 12;
     uint32_t* tslot = reinterpret_cast<uint32_t*>(full + 13);
-    const int tcols = nm <= 16 ? 128 : (nm <= 32 ? 256 : 512);  // products of two v-heads, then the Gram matrix
-    const int halves = n > 32 ? 2 : 1, workers = 8 - halves;    // warps of M; the others
+    const int tcols = nm <= 16 ? 128 : (nm <= 32 ? 256 : 512);     // products of two v-heads, then the Gram matrix
+    const int halves = n > 32 ? 2 : 1, workers = 8 - 2 * halves;   // warps 0 .. workers - 1; the others make M
     if (tid == 0) {
         for (int i = 0; i < 13; ++i) mbar_init(full + i, i >= 6 && i < 8 ? 4 : (i >= 8 && i < 10 ? halves : 1));
         fence_mbar_init();
     }
     if (warp == 8) tc::alloc(tslot, tcols);
+    const bf* xb = static_cast<const bf*>(J.x) + first * C;
+    const bf* cb = static_cast<const bf*>(J.conv_pool) + (size_t)slot * Km1 * C;
+    auto channel = [&](int what, int i) {  // first channel of k (0), q (1), v of v-head j0 + i (2)
+        return (what == 0 ? Hk + h : (what == 1 ? h : 2 * Hk + j0 + i)) * D;
+    };
+    // the raw inputs of k and q, conv state first, into the places of M and v; those of v and z to L2
+    bf* raw = reinterpret_cast<bf*>(sm + lay.M);
+    for (int i = tid; i < (Km1 + n) * 32; i += kVtThreads) {
+        const int row = i / 32, what = i / 16 % 2, c = i % 16 * 8;
+        cp_async16(raw + row * 2 * D + what * D + c,
+                   (row < Km1 ? cb + (size_t)row * C : xb + (size_t)(row - Km1) * C) + channel(what, 0) + c);
+    }
+    cp_async_commit();
+    for (int i = tid; i < n * gv * 4; i += kVtThreads) {
+        const int node = i / (4 * gv), jj = i / 4 % gv, piece = i % 4;
+        tree_prefetch(piece < 2 ? xb + (size_t)node * C + channel(2, jj) + piece * 64
+                                : static_cast<const bf*>(J.z) + ((size_t)(first + node) * Hv + j0 + jj) * D + (piece - 2) * 64);
+    }
     // gates and parents; conv weights with the taps outside (a missing tap: 0)
     if (tid < n) {
         const int p = J.parents[first + tid];
@@ -633,22 +667,22 @@ __global__ void __launch_bounds__(kVtThreads, 2)
         gates(__bfloat162float(static_cast<const bf*>(J.a)[at]), __bfloat162float(static_cast<const bf*>(J.b)[at]),
               A.p.A_log[j0 + jj], A.p.dt_bias ? A.p.dt_bias[j0 + jj] : 0.f, false, gate[i], betas[i]);
     }
-    auto channel = [&](int what, int i) {  // first channel of k (0), q (1), v of v-head j0 + i (2)
-        return (what == 0 ? Hk + h : (what == 1 ? h : 2 * Hk + j0 + i)) * D;
-    };
-#pragma unroll 4
-    for (int k = tid; k < (2 + gv) * D; k += kVtThreads) {
-        const int what = k / D;
-        const bf* src = static_cast<const bf*>(A.p.conv_w) + (size_t)(channel(min(what, 2), what - 2) + k % D) * K;
+    // weights of k, q and v-heads i0, i0 + 1 (what: from .. 3), by `nt` threads
+    auto stage_weights = [&](int i0, int from, int nt) {
+#pragma unroll 2
+        for (int k = from * D + tid; k < (2 + min(2, gv - i0)) * D; k += nt) {
+            const int what = k / D;
+            const bf* src = static_cast<const bf*>(A.p.conv_w) + (size_t)(channel(min(what, 2), i0 + what - 2) + k % D) * K;
 #pragma unroll
-        for (int m = 0; m < 4; ++m) ws[(what * 4 + m) * D + k % D] = m < K ? src[m] : __float2bfloat16_rn(0.f);
-    }
+            for (int m = 0; m < 4; ++m)
+                ws[(what * 4 + m) * D + k % D] = m >= 4 - K ? src[m - (4 - K)] : __float2bfloat16_rn(0.f);
+        }
+    };
+    stage_weights(0, 0, kVtThreads);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     const uint32_t tm = *tslot, tgram = tm + 4 * nm;
-    const bf* xb = static_cast<const bf*>(J.x) + first * C;
-    const bf* cb = static_cast<const bf*>(J.conv_pool) + (size_t)slot * Km1 * C;
     // the line of every node and the sum of log alpha along it, a thread per (node, v-head): two pairs a thread at most
     float sums[2] = {0.f, 0.f};
 #pragma unroll
@@ -665,15 +699,18 @@ __global__ void __launch_bounds__(kVtThreads, 2)
             if (jj == 0) line[i] = m;
         }
     }
-    if (tid >= 192 && tid - 192 < n) {  // tap K - 1 is the node, then its ancestors, then the conv state's rows, newest first
+    if (tid >= 192 && tid - 192 < n) {  // the last tap is the node, then its ancestors, then the conv state's rows, newest first
         const int i = tid - 192;
-        int at = i, row = Km1 - 1;
-        for (int t = K - 1; t >= 0; --t) {
-            taps[i * 4 + t] = at >= 0 ? (long long)at * C : (cb - xb) + (long long)(row--) * C;
-            if (at >= 0) at = up[at];
+        int at = i, row = Km1 - 1, t[4];
+#pragma unroll
+        for (int m = 3; m >= 0; --m) {
+            const bool live = 3 - m < K;
+            t[m] = !live ? i : (at >= 0 ? at : 64 + row--);
+            if (live && at >= 0) at = up[at];
         }
-        for (int t = K; t < 4; ++t) taps[i * 4 + t] = (long long)i * C;  // (weight 0)
+        taps[i] = make_int4(t[0], t[1], t[2], t[3]);
     }
+    cp_async_wait_all();
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < 2; ++e) {  // (read after the next barriers)
@@ -751,104 +788,133 @@ __global__ void __launch_bounds__(kVtThreads, 2)
             if (lane == 0) report_device_status(kDevWaitTimeout);
         }
     } else {
-        auto vbuf = [&](int i) { return reinterpret_cast<float*>(sm + lay.v) + (i % A.bufs) * nm * D; };
+        float* v = reinterpret_cast<float*>(sm + lay.v);
         const int batches = (n + 3) / 4;  // of 4 nodes
-        auto conv = [&](int what, int i, int batch) {
+        auto conv = [&](int what, int i, int batch) {  // what: k (0) and q (1) from shared memory, v of v-head j0 + i (2)
             const int ch = channel(what, i) + 4 * lane;
-            vt_conv(xb + ch, taps, reinterpret_cast<const uint2*>(ws + (what + i) * 4 * D),
-                    A.p.conv_b ? static_cast<const bf*>(A.p.conv_b) + ch : nullptr, 4 * batch, n, vbuf(i), Bt, 2 * nm,
+            const bf* x = what < 2 ? raw + Km1 * 2 * D + what * D + 4 * lane : xb + ch;
+            vt_conv(x, what < 2 ? x - Km1 * 2 * D : cb + ch, what < 2 ? 2 * D : C, taps,
+                    reinterpret_cast<const uint2*>(ws + (what + (i & 1)) * 4 * D),
+                    A.p.conv_b ? static_cast<const bf*>(A.p.conv_b) + ch : nullptr, 4 - K, 4 * batch, n, v, Bt, 2 * nm,
                     what == 1 ? nm : 0, what == 0 ? 1.f : (what == 1 ? g.q_scale : 0.f), g.l2_eps);
         };
+        if (warp == 7) {  // entries before each node: scan of the numbers of proper ancestors, rounded up to pairs
+            int base = 0;
+            for (int i0 = 0; i0 < nm; i0 += 32) {
+                const int i = i0 + lane;
+                int c = i < n ? __popcll(line[i]) & ~1 : 0;
+#pragma unroll
+                for (int s = 1; s < 32; s <<= 1) {
+                    const int x = __shfl_up_sync(0xffffffffu, c, s);
+                    if (lane >= s) c += x;
+                }
+                if (i < nm) off[i + 1] = base + c;
+                base += __shfl_sync(0xffffffffu, c, 31);
+            }
+            if (lane == 0) off[0] = 0;
+        }
 #pragma unroll 1
         for (int k = warp; k < 2 * batches; k += 8) conv(k & 1, 0, k >> 1);
         fence_proxy_async_smem();
         named_bar_sync(2, kVtThreads);
-        if (warp < 4 && 32 * warp < 2 * nm) {  // the Gram matrix into shared memory
-            if (wait(bar_g, 0)) {
-                tc::fence_after();
-                const int row = 32 * warp + lane;
 #pragma unroll 1
-                for (int c0 = 0; c0 < n; c0 += 16) {
-                    uint32_t r[16];
-                    vt_ld8(tc::taddr(tgram, 32 * warp, c0), r);
-                    vt_ld8(tc::taddr(tgram, 32 * warp, c0 + 8), r + 8);
-                    tc::ld_wait();
+        for (int i0 = 0; i0 < gv; i0 += 2) {  // v-heads i0 and i0 + 1
+            const int two = min(2, gv - i0);
+            if (i0 > 0) {
+                named_bar_sync(1, 256);  // T and the first two v-heads' weights are no longer read
+                stage_weights(i0, 2, 256);
+            }
+            if (warp < 4 && 32 * warp < 2 * nm) {  // the Gram matrix into shared memory
+                if (wait(bar_g, 0)) {
+                    tc::fence_after();
+                    const int row = 32 * warp + lane;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < n; c0 += 16) {
+                        uint32_t r[16];
+                        vt_ld8(tc::taddr(tgram, 32 * warp, c0), r);
+                        vt_ld8(tc::taddr(tgram, 32 * warp, c0 + 8), r + 8);
+                        tc::ld_wait();
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) gram[row * (nm + 1) + c0 + c] = __uint_as_float(r[c]);
+                        for (int c = 0; c < 16; ++c) gram[row * (nm + 1) + c0 + c] = __uint_as_float(r[c]);
+                    }
                 }
             }
-        }
-        named_bar_sync(1, 256);
-        if (warp >= workers) {
-            // ---- M of every v-head: column 32 half + lane ------------------------------------------
-            const int half = warp - workers;
-            float* T = reinterpret_cast<float*>(sm + lay.T) + half * nm * 32 + lane;
-            float4* ring = reinterpret_cast<float4*>(sm + lay.ring) + half * 2 * 68;
+            named_bar_sync(1, 256);
+            // coefficients of the nodes' proper ancestors, a warp per node, a lane per ancestor
 #pragma unroll 1
-            for (int i = 0; i < gv; ++i) {
-                unsigned char* Mt = sm + lay.M + ((i & 1) * ((nm + 31) / 32) + half) * nm * 128;
-                if (i >= 2) wait(o_done + (i & 1), (i - 2) >> 1);  // M's place is free
-                // coefficients of a node's proper ancestors, a lane per ancestor, filled up to a multiple of 4 with zeros
-                // times the first one's row; returns their number, sets the node's own
-                auto coefficients = [&](int node, float& own) -> int {
-                    const unsigned long long m = line[node] & ~(1ull << node);
-                    const float G = gate[node * gv + i], beta = betas[node * gv + i];
-                    float4* to = ring + (node & 1) * 68;
-                    const float *gk = gram + node * (nm + 1), *gq = gram + (nm + node) * (nm + 1);
-                    own = gq[node];
-                    const int c = __popcll(m), up4 = (c + 3) & ~3;
-                    for (int a = lane; a < node; a += 32) {
-                        if ((m >> a) & 1ull) {
-                            const float f = __expf(G - gate[a * gv + i]);
-                            to[__popcll(m & ((1ull << a) - 1ull))] =
-                                make_float4(beta * f * gk[a], f * gq[a], __int_as_float(a * 32), 0.f);
+            for (int node = warp; node < n; node += 8) {
+                const unsigned long long m = line[node] & ~(1ull << node);
+                const float *gk = gram + node * (nm + 1), *gq = gram + (nm + node) * (nm + 1);
+                const int start = off[node], c = __popcll(m);
+                for (int a = lane; a < node; a += 32) {
+                    if ((m >> a) & 1ull) {
+                        const int at = start + __popcll(m & ((1ull << a) - 1ull));
+                        const float k1 = gk[a], q1 = gq[a];
+                        for (int e = 0; e < two; ++e) {
+                            const float f = __expf(gate[node * gv + i0 + e] - gate[a * gv + i0 + e]);
+                            ent[e * vt_entries(nm) + at] = make_float2(betas[node * gv + i0 + e] * f * k1, f * q1);
                         }
+                        who[at] = (unsigned char)a;
                     }
-                    if (lane >= 28 && c + lane - 28 < up4)
-                        to[c + lane - 28] = make_float4(0.f, 0.f, __int_as_float((__ffsll((long long)m) - 1) * 32), 0.f);
-                    return up4;
-                };
-                float own, own_next = 0.f;
-                int cnt = coefficients(0, own), cnt_next = 0;
-                __syncwarp();
-#pragma unroll 1
-                for (int node = 0; node < n; ++node) {
-                    if (node + 1 < n) cnt_next = coefficients(node + 1, own_next);
-                    const float4* from = ring + (node & 1) * 68;
-                    float su[4] = {}, so[4] = {};
-#pragma unroll 1
-                    for (int e = 0; e < cnt; e += 4) {
-                        float4 k[4];
-                        float ta[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) k[q] = from[e + q];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) ta[q] = T[__float_as_int(k[q].z)];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            su[q] = fmaf(k[q].x, ta[q], su[q]);
-                            so[q] = fmaf(k[q].y, ta[q], so[q]);
-                        }
-                    }
-                    const float t = (node == 32 * half + lane ? 1.f : 0.f) - ((su[0] + su[1]) + (su[2] + su[3]));
-                    T[node * 32] = t;
-                    tc::st_elem(Mt, nm, node, lane, fmaf(own, t, (so[0] + so[1]) + (so[2] + so[3])));
-                    __syncwarp();  // the next node's coefficients are written, this one's are read
-                    own = own_next;
-                    cnt = cnt_next;
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(m_ready + (i & 1));
+                if (lane < two && (c & 1)) ent[lane * vt_entries(nm) + start + c] = make_float2(0.f, 0.f);
+                if (lane == 31) {
+                    if (c & 1) who[start + c] = (unsigned char)(__ffsll((long long)m) - 1);  // (0 times the first one's row)
+                    own[node] = gq[node];
+                }
             }
-        } else {
-            for (int i = 0; i < gv; ++i) {
-                float* v = vbuf(i);
-                if (i == 0 || A.bufs == 1) {
+            named_bar_sync(1, 256);
+            if (warp >= workers) {
+                // ---- M: column 32 half + lane of v-head i0 + e; T in the Gram matrix's place -----------
+                const int e = (warp - workers) / halves, half = (warp - workers) % halves;
+                if (e < two) {
+                    float* T = gram + (e * ((nm + 31) / 32) + half) * nm * 32 + lane;
+                    unsigned char* Mt = sm + lay.M + (e * ((nm + 31) / 32) + half) * nm * 128;
+                    const float2* from = ent + e * vt_entries(nm);
+                    int at = 0;
 #pragma unroll 1
-                    for (int k = warp; k < batches; k += workers) conv(2, i, k);
-                    named_bar_sync(1, 32 * workers);
+                    for (int node = 0; node < n; ++node) {
+                        const int end = off[node + 1];
+                        const float mine = own[node];
+                        float su[4] = {}, so[4] = {};
+#pragma unroll 1
+                        for (; at + 2 < end; at += 4) {
+                            float2 k[4];
+                            float t[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) t[q] = T[who[at + q] * 32];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) k[q] = from[at + q];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                su[q] = fmaf(k[q].x, t[q], su[q]);
+                                so[q] = fmaf(k[q].y, t[q], so[q]);
+                            }
+                        }
+                        if (at < end) {
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                const float2 k = from[at + q];
+                                const float t = T[who[at + q] * 32];
+                                su[q] = fmaf(k.x, t, su[q]);
+                                so[q] = fmaf(k.y, t, so[q]);
+                            }
+                            at += 2;
+                        }
+                        const float t = (node == 32 * half + lane ? 1.f : 0.f) - ((su[0] + su[1]) + (su[2] + su[3]));
+                        T[node * 32] = t;
+                        tc::st_elem(Mt, nm, node, lane, fmaf(mine, t, (so[0] + so[1]) + (so[2] + so[3])));
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(m_ready + e);
                 }
+                continue;
+            }
+            for (int i = i0; i < i0 + two; ++i) {
+#pragma unroll 1
+                for (int k = warp; k < batches; k += workers) conv(2, i, k);
+                named_bar_sync(4, 32 * workers);
                 if (warp < 4) {
                     // ---- thread = state row: w and e^G r, then o in v's place (its own column) ------------
                     float* u = v + 32 * warp + lane;
@@ -920,11 +986,8 @@ __global__ void __launch_bounds__(kVtThreads, 2)
                         __syncwarp();
                     }
                     tc::fence_before();
-                } else if (i + 1 < gv && A.bufs == 2) {
-#pragma unroll 1
-                    for (int k = warp - 4; k < batches; k += workers - 4) conv(2, i + 1, k);
                 }
-                named_bar_sync(1, 32 * workers);
+                named_bar_sync(4, 32 * workers);
                 if (warp < 4 && i + 2 < gv) asm volatile("bar.arrive 3, 160;" ::: "memory");  // this v-head's columns are free
                 // gated RMSNorm, a warp per node, two nodes at once, four channels to a lane
                 const int j = j0 + i;
@@ -966,7 +1029,7 @@ __global__ void __launch_bounds__(kVtThreads, 2)
                             *(reinterpret_cast<uint2*>(static_cast<bf*>(J.y) + ((size_t)(first + node) * Hv + j) * D) + lane) = out;
                     }
                 }
-                if (i + 1 < gv && A.bufs == 1) named_bar_sync(1, 32 * workers);  // o is read: its place takes the next v
+                if (i + 1 < gv) named_bar_sync(4, 32 * workers);  // o is read: its place takes the next v
             }
         }
     }
@@ -1012,53 +1075,70 @@ cudaError_t launch_verify_tc(const Geom& g, const LayerParams& p, const TreeJob&
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    VtArgs A{g, p, job, (job.max_nodes + 15) / 16 * 16, g.G, 2};
-    if ((long)job.B * g.Hk < sm_count()) A.gv = 1;  // few trees: a CTA per v-head
-    if (A.gv == 1) A.bufs = 1;
-    const int room = A.nm > 32 ? 227 * 1024 : 113 * 1024;  // two CTAs per SM (1 KB of each one's share is the system's)
-    if (vt_smem(A.nm, A.gv, A.bufs).total + 1024 > room) A.bufs = 1;
+    VtArgs A{g, p, job, (job.max_nodes + 15) / 16 * 16, g.G};
+    // few trees: a CTA per v-head; and as many v-heads as shared memory holds the decays of
+    if ((long)job.B * g.Hk < sm_count()) A.gv = 1;
+    while (vt_smem(A.nm, A.gv).total + 1024 > 227 * 1024 || A.g.G % A.gv) --A.gv;
     return launch_pdl(k_tree_verify_tc, dim3((unsigned)(g.Hv / A.gv), (unsigned)job.B), dim3(kVtThreads),
-                      (size_t)vt_smem(A.nm, A.gv, A.bufs).total + 1024, st, map, A);
+                      (size_t)vt_smem(A.nm, A.gv).total + 1024, st, map, A);
 }
 
 // ---- commit ---------------------------------------------------------------------
 // One CTA per (v-head, sequence), a cluster per k-head.  A warp holds D / 8 state rows in registers
-// through all rows of the path (a state row's update touches no other row), so the
-// state is read once and written once, straight from and to HBM, and shared memory holds only
-// the k, v and gates of kComRows path rows at a time.  The G CTAs of a k-head read the
-// same conv rows of k, which one of them replaces: the cluster barrier stands between.
-constexpr int kComRows = 16;
+// through all rows of the path (a state row's update touches no other row), 8 lanes to a row as in
+// k_tree_verify, so the state is read once and written once, and shared memory holds only
+// the inputs, k and v of a chunk of path rows at a time.  HBM-bound: while a CTA prepares k and v, its state is on the
+// way to L2, asked for by the CTA that ran a wave before it.  The G CTAs of a k-head read the same conv rows of k,
+// which one of them replaces: the cluster barrier stands between.
+template <typename TA>
+constexpr int kComChunk = sizeof(TA) == 2 ? 16 : 8;
 
 struct CommitArgs {
     Geom g;
     LayerParams p;
     TreeCommitJob job;
+    int ahead;  // sequences between a CTA and the one whose state it asks for
 };
 
 template <int D, typename TA>
-__global__ void __launch_bounds__(kTreeThreads) k_tree_commit(const __grid_constant__ CommitArgs A) {
+__global__ void __launch_bounds__(kTreeThreads, 2) k_tree_commit(const __grid_constant__ CommitArgs A) {
     using L = Act<TA>;
-    constexpr int LPR = D / 4;                       // lanes of a state row, 4 floats each
-    constexpr int RPI = 32 / LPR;                    // rows of one warp-wide 128-bit access
-    constexpr int NA = D / (8 * RPI);                // accesses per warp: D / 8 rows
-    constexpr int nwarp = kTreeThreads / 32;
+    constexpr int LPN = D / 4, NPW = 32 / LPN;  // lanes of a path row's channels, rows of a warp (conv)
+    constexpr int RL = D / 32;                  // state rows and 4-column chunks of a lane
+    constexpr int nwarp = kTreeThreads / 32, kComRows = kComChunk<TA>;
     const Geom& g = A.g;
     const TreeCommitJob& J = A.job;
     const int gi = blockIdx.x, h = blockIdx.y, j = h * g.G + gi, b = blockIdx.z;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int Hk = g.Hk, Hv = g.Hv, K = g.K, Km1 = g.K - 1, C = g.C_ch;
     const bool raw = g.flags & kFlagRawQKV;
-    __shared__ __align__(16) float ks[kComRows][D];
-    __shared__ float vs[kComRows][D];
-    __shared__ float alpha_s[kComRows], beta_s[kComRows];
+    __shared__ __align__(16) float ks[kComRows][D], vs[kComRows][D];
+    __shared__ __align__(16) TA ws[2][5][D];                // conv taps and bias of k and v
+    __shared__ __align__(16) TA hs[kComRows + 3][3][D];     // raw inputs of q, k, v: K - 1 before the chunk, then its rows
+    __shared__ float alpha_s[kTreeMax], beta_s[kTreeMax];
     __shared__ int rows[kTreeMax];
     __shared__ int n_s;
     griddep_wait();
     griddep_launch_dependents();
     const int slot = J.slot_idx[b];
     const int64_t first = J.cu_rows[b], count = (int64_t)J.cu_rows[b + 1] - first;
+    for (int far = b < A.ahead ? 0 : A.ahead; far <= A.ahead; far += A.ahead) {  // (the first wave asks for its own too)
+        if (b + far >= J.B) break;
+        const int s2 = J.slot_idx[b + far];
+        if (s2 >= 0 && s2 < J.n_slots && J.cu_rows[b + far + 1] > J.cu_rows[b + far]) {
+            const float* p = J.state_pool + ((size_t)s2 * Hv + j) * D * D;
+            for (int i = tid; i < D * D / 32; i += kTreeThreads) tree_prefetch(p + i * 32);
+        }
+    }
     if (slot < 0 || slot >= J.n_slots || first < 0 || count < 1 || count > J.max_rows || first + count > J.n_rows)
         return;  // the whole cluster shares b
+    const int l8 = lane & 7, grp = lane >> 3, row0 = warp * (D / 8) + grp;  // state row r * 4 + group, columns 4 l8 + 32 c
+    float* Sg = J.state_pool + (((size_t)slot * Hv + j) * D + row0) * D + 4 * l8;
+    float4 S[RL][RL];
+#pragma unroll
+    for (int r = 0; r < RL; ++r)
+#pragma unroll
+        for (int c = 0; c < RL; ++c) S[r][c] = *reinterpret_cast<const float4*>(Sg + (size_t)r * 4 * D + 32 * c);
     // the rows of the path that exist, in order (64 at most: two per lane of a warp)
     if (warp == 0) {
         int src[2];
@@ -1075,90 +1155,128 @@ __global__ void __launch_bounds__(kTreeThreads) k_tree_commit(const __grid_const
         if (src[1] >= 0) rows[__popc(has[0]) + __popc(has[1] & below)] = src[1];
         if (lane == 0) n_s = __popc(has[0]) + __popc(has[1]);
     }
-    // the warp's state rows
-    float* Sg = J.state_pool + (((size_t)slot * Hv + j) * D + warp * (D / 8)) * D;
-    const int rsub = lane / LPR, col = (lane % LPR) * 4;
-    float4 s[NA];
+    auto channel = [&](int kind) { return (kind == 0 ? h : (kind == 1 ? Hk + h : 2 * Hk + j)) * D; };  // q, k, v
+    if (!raw) {
+        for (int i = tid; i < 2 * D; i += kTreeThreads) {
+            const int ch = channel(1 + i / D) + i % D;
+            TA zero;
+            L::st(&zero, 0, 0.f);
 #pragma unroll
-    for (int i = 0; i < NA; ++i) s[i] = *reinterpret_cast<const float4*>(Sg + (size_t)(i * RPI + rsub) * D + col);
+            for (int t = 0; t < 4; ++t) {  // (taps are aligned at the newest)
+                const int m = t - (4 - K);
+                ws[i / D][t][i % D] = m >= 0 ? static_cast<const TA*>(A.p.conv_w)[(size_t)ch * K + m] : zero;
+            }
+            ws[i / D][4][i % D] = A.p.conv_b ? static_cast<const TA*>(A.p.conv_b)[ch] : zero;
+        }
+    }
     __syncthreads();
     const int n = n_s;
     if (n == 0) return;  // no row that exists (the whole cluster)
     const TA* x = static_cast<const TA*>(J.x);
     TA* cp = static_cast<TA*>(J.conv_pool) + (size_t)slot * Km1 * C;
-    // raw input p of the sequence: the conv state's rows, then the path's
-    auto hist = [&](int p, int ch) -> TA { return p < Km1 ? cp[(size_t)p * C + ch] : x[(size_t)rows[p - Km1] * C + ch]; };
     for (int t0 = 0; t0 < n; t0 += kComRows) {
         const int m = min(kComRows, n - t0);
-        for (int w = tid; w < 2 * D * m; w += kTreeThreads) {
-            const int t = w / (2 * D), c = w % (2 * D);
-            const int ch = c < D ? Hk * D + h * D + c : 2 * Hk * D + j * D + c - D;
-            float val;
-            if (raw) {
-                val = L::ld(x, (size_t)rows[t0 + t] * C + ch);
-            } else {
-                float acc = A.p.conv_b ? L::ld(A.p.conv_b, ch) : 0.f;
-                for (int e = 0; e < K; ++e) {
-                    const TA xv = hist(t0 + t + e, ch);
-                    acc = fmaf(L::ld(A.p.conv_w, (size_t)ch * K + e), L::ld(&xv, 0), acc);
-                }
-                val = siluf_(acc);
+        // the chunk's raw inputs, all on their way at once (through shared memory: the state has the registers): input p
+        // of the sequence is row p of the conv state, then the path's rows
+        {
+            constexpr int PER = D * (int)sizeof(TA) / 16;  // 16-byte pieces of a row's head
+            for (int i = tid; i < (m + Km1) * 3 * PER; i += kTreeThreads) {
+                const int row = i / (3 * PER), kind = i / PER % 3, c = i % PER * (16 / (int)sizeof(TA)), p = t0 + row;
+                cp_async16(&hs[row][kind][c], (p < Km1 ? cp + (size_t)p * C : x + (size_t)rows[p - Km1] * C) + channel(kind) + c);
             }
-            if (c < D) ks[t][c] = val;
-            else vs[t][c - D] = val;
+            cp_async_commit();
         }
-        if (tid < m) {
-            float gl, beta;
-            const size_t at = (size_t)rows[t0 + tid] * Hv + j;
+        if (t0 == 0) {
             const bool direct = g.flags & kFlagGatesDirect;
-            gates(L::ld(J.a, at), L::ld(J.b, at), direct ? 0.f : A.p.A_log[j],
-                  !direct && A.p.dt_bias ? A.p.dt_bias[j] : 0.f, direct, gl, beta);
-            alpha_s[tid] = expf(gl);
-            beta_s[tid] = beta;
+            for (int t = tid - (kTreeThreads - 64); t >= 0 && t < n; t += 64) {
+                float gl, beta;
+                gates(L::ld(J.a, (size_t)rows[t] * Hv + j), L::ld(J.b, (size_t)rows[t] * Hv + j), direct ? 0.f : A.p.A_log[j],
+                      !direct && A.p.dt_bias ? A.p.dt_bias[j] : 0.f, direct, gl, beta);
+                alpha_s[t] = expf(gl);
+                beta_s[t] = beta;
+            }
+        }
+        cp_async_wait_all();
+        __syncthreads();
+        // the conv state is read (rows past the first K - 1 do not reach it): the cluster's other CTAs may replace it
+        if (t0 == 0) cluster_arrive_release();
+        // conv + SiLU of k and v, L2 norm of k: an LPN-lane group has a path row's D channels
+        {
+            const int sub = lane / LPN, c4 = (lane % LPN) * 4;
+            auto ld4 = [&](const TA* p) { return make_float4(L::ld(p, 0), L::ld(p, 1), L::ld(p, 2), L::ld(p, 3)); };
+#pragma unroll 2
+            for (int unit = warp; unit < 2 * ((m + NPW - 1) / NPW); unit += nwarp) {
+                const int kind = unit & 1, i0 = (unit >> 1) * NPW + sub, i = min(i0, m - 1);
+                float4 y = ld4(&hs[i + Km1][1 + kind][c4]);
+                if (!raw) {
+                    const float4 v3 = y;
+                    y = ld4(&ws[kind][4][c4]);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        if (t < 4 - K) continue;
+                        const float4 w = ld4(&ws[kind][t][c4]), v = t == 3 ? v3 : ld4(&hs[i + Km1 - 3 + t][1 + kind][c4]);
+                        y.x = fmaf(w.x, v.x, y.x);
+                        y.y = fmaf(w.y, v.y, y.y);
+                        y.z = fmaf(w.z, v.z, y.z);
+                        y.w = fmaf(w.w, v.w, y.w);
+                    }
+                    y = make_float4(tree_silu(y.x), tree_silu(y.y), tree_silu(y.z), tree_silu(y.w));
+                }
+                if (kind == 0 && !(g.flags & kFlagNoL2)) {
+                    float ss = fmaf(y.x, y.x, fmaf(y.y, y.y, fmaf(y.z, y.z, y.w * y.w)));
+#pragma unroll
+                    for (int o = LPN / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                    const float f = rsqrtf(ss + g.l2_eps);
+                    y = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
+                }
+                if (i0 < m) *reinterpret_cast<float4*>(&(kind == 0 ? ks : vs)[i0][c4]) = y;
+            }
         }
         __syncthreads();
-        if (!(g.flags & kFlagNoL2)) {
-            for (int t = warp; t < m; t += nwarp) {
-                float sk = 0.f;
-                for (int c = lane; c < D; c += 32) sk = fmaf(ks[t][c], ks[t][c], sk);
-                const float rk = rsqrtf(tree_warp_sum(sk) + g.l2_eps);
-                for (int c = lane; c < D; c += 32) ks[t][c] *= rk;
-            }
-            __syncthreads();
-        }
+#pragma unroll 1
         for (int t = 0; t < m; ++t) {
-            const float4 kv = *reinterpret_cast<const float4*>(&ks[t][col]);
-            const float alpha = alpha_s[t], beta = beta_s[t];
+            float4 k[RL];
+            float2 d[RL];
+            float dot[RL];
 #pragma unroll
-            for (int i = 0; i < NA; ++i) {
-                float d = fmaf(s[i].x, kv.x, fmaf(s[i].y, kv.y, fmaf(s[i].z, kv.z, s[i].w * kv.w)));
+            for (int c = 0; c < RL; ++c) k[c] = *reinterpret_cast<const float4*>(&ks[t][4 * l8 + 32 * c]);
 #pragma unroll
-                for (int off = LPR / 2; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-                const float be = beta * (vs[t][warp * (D / 8) + i * RPI + rsub] - alpha * d);
-                s[i].x = fmaf(alpha, s[i].x, be * kv.x);
-                s[i].y = fmaf(alpha, s[i].y, be * kv.y);
-                s[i].z = fmaf(alpha, s[i].z, be * kv.z);
-                s[i].w = fmaf(alpha, s[i].w, be * kv.w);
+            for (int r = 0; r < RL; ++r) {
+                d[r] = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int c = 0; c < RL; ++c) d[r] = tree_dot(S[r][c], k[c], d[r]);
+                dot[r] = d[r].x + d[r].y;
+            }
+            // lane l8 of a group: the sum of state row l8 / (8 / RL); beta (v - alpha S k) of it, handed to the group
+            const float sum = tree_sum8<RL>(dot, lane);
+            const float alpha = alpha_s[t0 + t];
+            const float be = beta_s[t0 + t] * (vs[t][row0 + (l8 / (8 / RL)) * 4] - alpha * sum);
+            const float2 al2 = make_float2(alpha, alpha);
+#pragma unroll
+            for (int r = 0; r < RL; ++r) {
+                const float ber = __shfl_sync(0xffffffffu, be, (lane & 24) + r * (8 / RL));
+                const float2 b2 = make_float2(ber, ber);
+#pragma unroll
+                for (int c = 0; c < RL; ++c) {
+                    const float2 lo = __ffma2_rn(al2, make_float2(S[r][c].x, S[r][c].y), __fmul2_rn(b2, make_float2(k[c].x, k[c].y)));
+                    const float2 hi = __ffma2_rn(al2, make_float2(S[r][c].z, S[r][c].w), __fmul2_rn(b2, make_float2(k[c].z, k[c].w)));
+                    S[r][c] = make_float4(lo.x, lo.y, hi.x, hi.y);
+                }
             }
         }
-        __syncthreads();  // ks and vs are read
+        if (t0 + kComRows < n) __syncthreads();  // ks, vs and the inputs are read
     }
+    // the new conv state: the last K - 1 raw inputs, bit for bit, from shared memory
 #pragma unroll
-    for (int i = 0; i < NA; ++i) *reinterpret_cast<float4*>(Sg + (size_t)(i * RPI + rsub) * D + col) = s[i];
-    // the new conv state: the last K - 1 raw inputs, bit for bit.  A thread reads a channel's
-    // inputs before it writes them; the k-head's k channels are read by the cluster's other
-    // CTAs above, its q channels by none
-    cg::this_cluster().sync();
+    for (int r = 0; r < RL; ++r)
+#pragma unroll
+        for (int c = 0; c < RL; ++c) *reinterpret_cast<float4*>(Sg + (size_t)r * 4 * D + 32 * c) = S[r][c];
+    cluster_wait_acquire();
+    const int tail = (n - 1) % kComRows + 1;  // rows of the last chunk
     for (int c = tid; c < 3 * D; c += kTreeThreads) {
-        if (c < 2 * D && c % g.G != gi) continue;
-        const int ch = c < D ? h * D + c : (c < 2 * D ? Hk * D + h * D + c - D : 2 * Hk * D + j * D + c - 2 * D);
-        TA v[3];
-#pragma unroll
-        for (int m = 0; m < 3; ++m)
-            if (m < Km1) v[m] = hist(n + m, ch);
-#pragma unroll
-        for (int m = 0; m < 3; ++m)
-            if (m < Km1) cp[(size_t)m * C + ch] = v[m];
+        const int kind = c / D;
+        if (kind < 2 && c % g.G != gi) continue;  // (q and k channels: one CTA of the cluster each)
+        for (int m = 0; m < Km1; ++m) cp[(size_t)m * C + channel(kind) + c % D] = hs[tail + m][kind][c % D];
     }
 }
 
@@ -1209,7 +1327,7 @@ cudaError_t launch_tree_verify(const Geom& g, const LayerParams& p, const TreeJo
 
 cudaError_t launch_tree_commit(const Geom& g, const LayerParams& p, const TreeCommitJob& job, cudaStream_t st) {
     if (job.B == 0 || job.n_rows == 0) return cudaSuccess;
-    const CommitArgs A{g, p, job};
+    const CommitArgs A{g, p, job, std::max(1, 2 * sm_count() / g.Hv)};
     GDN_BY_TYPE(launch_commit_t);
 }
 
