@@ -8,12 +8,12 @@
 // holds everything up to 128 rows, so that short trees are bound by HBM (M flops per byte against a ridge of
 // about 280) and large ones by the tensor cores.
 //
-// Work: every (sequence, kv-head) is a list of key tiles (its context's, then one with the nodes
-// themselves); the lists are laid end to end and cut into equal runs, one per worker, whatever
-// the mix of context lengths.  A worker is RT CTAs, one per row tile, that walk the same run side by side,
-// so that the RT reads of a key tile meet in L2.  A list that lies in one run is finished by its
-// worker; one that is cut leaves (maximum, sum, unnormalised O) per part in the workspace and k_attn_tree_join
-// joins the parts in order (no atomics: results do not change from call to call).
+// Work: every (sequence, kv-head, row tile) is a list of key tiles (its context's, then one with the nodes
+// themselves).  While there is an SM for each list, lists are cut into equal pieces, one per worker (a CTA), as few as
+// balance allows; the row tiles of a kv-head are cut at the same places, so their reads of K and V come at the same time
+// and meet in L2.  With more lists they are laid end to end and cut into equal runs, whatever the mix of lengths.
+// A list that lies with one worker is finished by it; one that is cut leaves (maximum, sum, unnormalised O) per part
+// in the workspace and k_attn_tree_join joins the parts in order (no atomics: results do not change from call to call).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -41,10 +41,11 @@ struct AttnTreeArgs {
     const int32_t* parents;
     const int32_t* ctx_lens;
     __nv_bfloat16* o;  // [N][Hq][D]
-    float* part;       // [worker][RT][2][D + 2][128]: O by columns, then maximum and sum
+    int4* share;       // [worker][2]: workers of the list that its share begins in, row tile, kv-head; first row, nodes
+    float* part;       // [worker][2][D + 2][128]: O by columns, then maximum and sum
     int B, Hq, Hkv, G, W, page, R, max_pages, n_pages, n_nodes, max_nodes, max_ctx;
-    int RT;             // CTAs of a worker: the most row tiles of a tree, or 1 where each row tile is a list of its own
     int whole;          // > 0: worker w takes list w whole (few short lists: nothing to join), of this many per kv-head
+    int even;           // lists in equal pieces (at most W lists); else equal runs of all lists
     float scale_log2;   // scale * log2(e)
 };
 
@@ -59,7 +60,9 @@ struct TreeLay {
     static constexpr int K = Q + NCH * QATOM;      // 2 stages, [8-row group][chunk][8][128 bytes], swizzled
     static constexpr int V = K + 2 * TILE;         // 2 stages, the same layout
     static constexpr int BAR = V + 2 * TILE;
-    static constexpr int GONE = BAR + 24 * 8;      // 4 slots: runs of a tile without keys
+    static constexpr int MREF = BAR + 40 * 8;      // reference maximum of each row
+    static constexpr int LSUM = MREF + 128 * 4;    // sums of the rows, per softmax group
+    static constexpr int GONE = LSUM + 256 * 4;    // 4 slots: runs of a tile without keys
     static constexpr int BAD = GONE + 4 * 8;       // 4 slots: nodes with an infinite or NaN value
     static constexpr int ANC = BAD + 4 * 8;        // 4 slots: line of each node (64-bit masks)
     static constexpr int UP = ANC + 4 * 64 * 8;
@@ -86,81 +89,115 @@ __device__ __forceinline__ int tree_tiles(const AttnTreeArgs& A, int b, int& fir
     return (ctx + BK - 1) / BK + 1;
 }
 
-// lists of a sequence: its kv-heads, times its row tiles where these are lists of their own
-__device__ __forceinline__ int tree_lists(const AttnTreeArgs& A, int n) {
-    return A.RT > 1 ? A.Hkv : A.Hkv * ((n * A.G + 127) / 128);
-}
+// lists of a sequence: a list per kv-head and row tile
+__device__ __forceinline__ int tree_lists(const AttnTreeArgs& A, int n) { return A.Hkv * ((n * A.G + 127) / 128); }
 
-// where worker w's run [start, end) begins: list (b, kv-head), tile t of nt.  All threads of the block call it.
-struct TreeRun {
-    long long start, end, per;
-    int b;
-    long long rem;  // start - first tile of sequence b's lists
-};
-
-template <int D, int THREADS>
-__device__ __forceinline__ TreeRun tree_run(const AttnTreeArgs& A, int w) {
-    constexpr int BK = TreeLay<D>::BK;
-    __shared__ long long s_warp[THREADS / 32], s_rem;
-    __shared__ int s_b;
-    TreeRun run;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int first, n, ctx;
-    if (A.whole) {  // (RT 1: A.whole row tiles of each kv-head)
-        run.b = w / (A.Hkv * A.whole);
-        const int nt = tree_tiles<BK>(A, run.b, first, n, ctx), at = w % (A.Hkv * A.whole);
-        run.per = nt;
-        run.start = 0;
-        run.end = at < tree_lists(A, n) ? nt : 0;
-        run.rem = (long long)at * nt;
-        return run;
-    }
-    // each thread sums a run of sequences; a scan of the threads' sums finds the one that holds the start
-    const int each = (A.B + THREADS - 1) / THREADS;
-    const int b0 = min(A.B, tid * each), b1 = min(A.B, b0 + each);
-    long long sum = 0;
-    for (int b = b0; b < b1; ++b) {
-        const int nt = tree_tiles<BK>(A, b, first, n, ctx);
-        sum += (long long)nt * tree_lists(A, n);
-    }
-    long long incl = sum;
+// sum of v over the block's threads, and of the threads before this one
+template <int THREADS>
+__device__ __forceinline__ void tree_scan(long long v, long long* s_warp, long long& before, long long& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long incl = v;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += v;
+        const long long x = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += x;
     }
+    __syncthreads();  // s_warp may be in use
     if (lane == 31) s_warp[warp] = incl;
-    if (tid == 0) s_b = 0;
     __syncthreads();
-    long long total = 0, before = 0;
+    before = incl - v;
+    total = 0;
 #pragma unroll
     for (int i = 0; i < THREADS / 32; ++i) {
         if (i < warp) before += s_warp[i];
         total += s_warp[i];
     }
-    run.per = max((long long)kTreeMinTiles, (total + A.W - 1) / A.W);
-    run.start = min(total, w * run.per);
-    run.end = min(total, run.start + run.per);
-    long long at = before + incl - sum;
-    if (run.start < run.end && at <= run.start && run.start < at + sum) {
+}
+
+// worker w's share: `left` tiles from tile `rem` of sequence b's lists on.  All threads of the block call it.
+struct TreeRun {
+    int b;
+    long long rem, left;
+    int first, last;  // workers that hold the list the share begins in
+};
+
+template <int D, int THREADS>
+__device__ __forceinline__ TreeRun tree_run(const AttnTreeArgs& A, int w) {
+    constexpr int BK = TreeLay<D>::BK;
+    __shared__ long long s_warp[THREADS / 32], s_rem, s_left;
+    __shared__ int s_b, s_first, s_last;
+    TreeRun run;
+    const int tid = threadIdx.x;
+    int first, n, ctx;
+    if (A.whole) {
+        run.b = w / (A.Hkv * A.whole);
+        const int nt = tree_tiles<BK>(A, run.b, first, n, ctx), at = w % (A.Hkv * A.whole);
+        run.left = at < tree_lists(A, n) ? nt : 0;
+        run.rem = (long long)at * nt;
+        run.first = run.last = w;
+        return run;
+    }
+    // each thread sums some sequences; a scan of the threads' sums finds the one that holds the start
+    const int each = (A.B + THREADS - 1) / THREADS;
+    const int b0 = min(A.B, tid * each), b1 = min(A.B, b0 + each);
+    long long sum = 0, before, total;
+    for (int b = b0; b < b1; ++b) {
+        const int nt = tree_tiles<BK>(A, b, first, n, ctx);
+        sum += (long long)nt * tree_lists(A, n);
+    }
+    tree_scan<THREADS>(sum, s_warp, before, total);
+    long long per = max((long long)kTreeMinTiles, (total + A.W - 1) / A.W);
+    if (A.even) {  // the shortest pieces of which there are at most W (a piece per list always fits)
+        while (true) {
+            sum = 0;
+            for (int b = b0; b < b1; ++b) {
+                const int nt = tree_tiles<BK>(A, b, first, n, ctx);
+                sum += (long long)tree_lists(A, n) * ((nt + per - 1) / per);
+            }
+            tree_scan<THREADS>(sum, s_warp, before, total);
+            if (total <= A.W) break;
+            per += max(1ll, per / 16);
+        }
+    }
+    // A.even: positions count pieces, and worker w takes piece w; else they count tiles
+    const long long start = A.even ? w : w * per;
+    if (tid == 0) s_left = 0;
+    __syncthreads();
+    if (start < total && before <= start && start < before + sum) {
+        long long at = before;
         for (int b = b0; b < b1; ++b) {
             const int nt = tree_tiles<BK>(A, b, first, n, ctx);
-            const long long t = (long long)nt * tree_lists(A, n);
-            if (run.start < at + t) {
+            const long long pieces = A.even ? (nt + per - 1) / per : nt, len = tree_lists(A, n) * pieces;
+            if (start < at + len) {
+                const long long list = (start - at) / pieces, piece = (start - at) % pieces;
                 s_b = b;
-                s_rem = run.start - at;
+                if (A.even) {
+                    const long long t0 = nt * piece / pieces;
+                    s_rem = list * nt + t0;
+                    s_left = nt * (piece + 1) / pieces - t0;
+                    s_first = w - (int)piece;
+                    s_last = s_first + (int)pieces - 1;
+                } else {
+                    s_rem = start - at;
+                    s_left = min(per, total - start);
+                    s_first = (int)((start - piece) / per);
+                    s_last = (int)((start - piece + nt - 1) / per);
+                }
                 break;
             }
-            at += t;
+            at += len;
         }
     }
     __syncthreads();
     run.b = s_b;
     run.rem = s_rem;
+    run.left = s_left;
+    run.first = s_first;
+    run.last = s_last;
     return run;
 }
 
-// one piece of a worker's run: tiles t0 .. t1 - 1 of the nt of list (b, kvh), rows 128 rt ..
+// one piece of a worker's share: tiles t0 .. t1 - 1 of the nt of list (b, kvh), rows 128 rt ..
 struct TreeSeg {
     int b, kvh, rt, t0, t1, nt, first, n, ctx;
 };
@@ -168,10 +205,9 @@ struct TreeSeg {
 template <int BK>
 struct TreeWalk {
     const AttnTreeArgs& A;
-    int b, rt;
+    int b;
     long long rem, left;
-    __device__ TreeWalk(const AttnTreeArgs& a, const TreeRun& r, int row_tile)
-        : A(a), b(r.b), rt(row_tile), rem(r.rem), left(r.end - r.start) {}
+    __device__ TreeWalk(const AttnTreeArgs& a, const TreeRun& r) : A(a), b(r.b), rem(r.rem), left(r.left) {}
     __device__ bool next(TreeSeg& s) {
         while (left > 0 && b < A.B) {
             s.nt = tree_tiles<BK>(A, b, s.first, s.n, s.ctx);
@@ -184,7 +220,7 @@ struct TreeWalk {
             const int list = (int)(rem / s.nt), per_head = lists / A.Hkv;
             s.b = b;
             s.kvh = list / per_head;
-            s.rt = A.RT > 1 ? rt : list % per_head;
+            s.rt = list % per_head;
             s.t0 = (int)(rem - (long long)list * s.nt);
             s.t1 = (int)min((long long)s.nt, s.t0 + left);
             left -= s.t1 - s.t0;
@@ -272,17 +308,20 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t u) {
     return ((u & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) | ((u & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
 }
 
-// Warp 0 loads K tiles, warp 6 V tiles (and works out the nodes' lines), warp 1 issues the products, warps 2..5
-// (thread = row) do the softmax and the epilogue.  Tile `it` of the CTA uses stage, S and P buffer and barrier it & 1:
+// Warp 0 loads K tiles, warp 10 V tiles (and works out the nodes' lines), warps 1 and 11 issue the two products, and
+// two groups of four warps (2..5 and 6..9, thread = row) take the tiles in turn, so that one group's softmax runs
+// while the other waits, loads or stores.  Tile `it` of the CTA uses group, stage, S and P buffer and barrier it & 1:
 //   full_k, full_v   the tile's copies have landed
-//   s_done           S = Q K^T is in TMEM (and K's stage is free, and P V of tile it - 2 done)
-//   s_read           the softmax has S in registers (and S's buffer is free)
+//   s_done           S = Q K^T is in TMEM (and K's stage is free)
+//   s_read           the group has read S for the last time (and S's buffer is free)
+//   decided          (per 32 rows) the rows' reference maxima after this tile are in shared memory
 //   p_ready          P is in TMEM, O is rescaled, V has no row without a key
-//   pv_done          O += P V is done (V's stage is free)
-// S of tile it + 1 is issued before P V of tile it, so the tensor cores work while the softmax does.
+//   pv_done          O += P V is done (V's stage and P's buffer are free)
 // Every wait is bounded: a role that gives up stops waiting, and the CTA still runs to its end.
+constexpr int kTreeThreads = 384;
+
 template <int D>
-__global__ void __launch_bounds__(224, 1)
+__global__ void __launch_bounds__(kTreeThreads, 1)
     k_attn_tree(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                 const __grid_constant__ CUtensorMap tkn, const __grid_constant__ CUtensorMap tvn,
                 const __grid_constant__ AttnTreeArgs A) {
@@ -290,16 +329,25 @@ __global__ void __launch_bounds__(224, 1)
     constexpr int NCH = Ly::NCH, BK = Ly::BK;
     griddep_wait();  // launched with programmatic serialization
     griddep_launch_dependents();
-    const int w = blockIdx.x / A.RT;
-    const TreeRun run = tree_run<D, 224>(A, w);
-    if (run.start >= run.end) return;  // (the same for all threads)
+    const TreeRun run = tree_run<D, kTreeThreads>(A, blockIdx.x);
+    if (A.share && threadIdx.x == 0) {  // for the join
+        TreeSeg s;
+        TreeWalk<BK> walk(A, run);
+        const bool any = walk.next(s);
+        A.share[2 * blockIdx.x] = any ? make_int4(run.first, run.last, s.rt, s.kvh) : make_int4(-2, 0, 0, 0);
+        A.share[2 * blockIdx.x + 1] = any ? make_int4(s.first, s.n, 0, 0) : make_int4(0, 0, 0, 0);
+    }
+    if (run.left <= 0) return;  // (the same for all threads)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = smem_raw + ((1024 - (tc::smem_addr(smem_raw) & 1023)) & 1023);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Ly::BAR);
     uint64_t *full_k = bars, *full_v = bars + 2, *s_done = bars + 4, *s_read = bars + 6, *pv_done = bars + 8,
-             *p_ready = bars + 10, *anc_ready = bars + 12, *q_ready = bars + 14, *gone_ready = bars + 16;
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 20);
+             *p_ready = bars + 10, *anc_ready = bars + 12, *q_ready = bars + 14, *o_free = bars + 15, *gone_ready = bars + 16,
+             *decided = bars + 20;  // [group][quarter of the rows]
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 28);
+    float* s_mref = reinterpret_cast<float*>(sm + Ly::MREF);
+    float* s_l = reinterpret_cast<float*>(sm + Ly::LSUM);
     unsigned* s_gone = reinterpret_cast<unsigned*>(sm + Ly::GONE);
     unsigned long long* s_bad = reinterpret_cast<unsigned long long*>(sm + Ly::BAD);
     unsigned long long* s_anc = reinterpret_cast<unsigned long long*>(sm + Ly::ANC);
@@ -309,13 +357,15 @@ __global__ void __launch_bounds__(224, 1)
             mbar_init(full_k + i, 1);
             mbar_init(full_v + i, 1);
             mbar_init(s_done + i, 1);
-            mbar_init(s_read + i, 4);  // one arrival per softmax warp
+            mbar_init(s_read + i, 4);  // one arrival per warp of the group
             mbar_init(pv_done + i, 1);
             mbar_init(p_ready + i, 4);
             mbar_init(anc_ready + i, 1);
         }
         for (int i = 0; i < 4; ++i) mbar_init(gone_ready + i, 1);
-        mbar_init(q_ready, 4);
+        for (int i = 0; i < 8; ++i) mbar_init(decided + i, 1);
+        mbar_init(q_ready, 8);
+        mbar_init(o_free, 8);
         fence_mbar_init();
     }
     if (warp == 1) tc::alloc(tslot, Ly::TMEM_COLS);
@@ -341,16 +391,10 @@ __global__ void __launch_bounds__(224, 1)
     };
     // keys of tile j, and their steps of 16 in P V (rows past the last step are not read)
     auto keys_of = [&](const TreeSeg& s, int j) { return j == s.nt - 1 ? s.n : min(BK, s.ctx - j * BK); };
-    TreeWalk<BK> walk(A, run, blockIdx.x % A.RT);
+    TreeWalk<BK> walk(A, run);
     TreeSeg s;
-    auto next = [&](TreeSeg& t) {  // the next piece with rows for this CTA
-        do {
-            if (!walk.next(t)) return false;
-        } while (t.rt * 128 >= t.n * A.G);
-        return true;
-    };
 
-    if (warp == 0 || warp == 6) {
+    if (warp == 0 || warp == 10) {
         // ---- K or V tiles into the two stages -------------------------------------------
         const bool is_k = warp == 0;
         const CUtensorMap* pool_map = is_k ? &tk : &tv;
@@ -358,7 +402,7 @@ __global__ void __launch_bounds__(224, 1)
         unsigned char* ring = sm + (is_k ? Ly::K : Ly::V);
         uint64_t *full = is_k ? full_k : full_v, *freed = is_k ? s_done : pv_done;
         int it = 0, tails = 0;
-        while (ok && next(s)) {
+        while (ok && walk.next(s)) {
             int pid_next = lane_page(s, s.t0);
             for (int j = s.t0; j < s.t1; ++j, ++it) {
                 const int pid = pid_next;
@@ -367,7 +411,7 @@ __global__ void __launch_bounds__(224, 1)
                 if (it >= 2 && !wait(freed + st, (it - 2) >> 1)) break;
                 unsigned char* dst = ring + st * Ly::TILE;
                 const unsigned have = __ballot_sync(0xffffffffu, pid >= 0);
-                if (is_k && lane == 0) {  // (s_done(it - 2): the softmax has read the slot of tile it - 4)
+                if (is_k && lane == 0) {  // (S of tile it - 2 is done, so tile it - 4 was read and with it this slot)
                     s_gone[it & 3] = ~have;
                     mbar_arrive(gone_ready + (it & 3));
                 }
@@ -424,73 +468,72 @@ __global__ void __launch_bounds__(224, 1)
         // copies still in flight land before the CTA leaves
         for (int i = max(0, it - 2); i < it; ++i) mbar_wait(full + (i & 1), (uint32_t)((i >> 1) & 1));
     } else if (warp == 1) {
-        constexpr uint32_t idesc_s = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(BK >> 3) << 17) |
-                                     ((uint32_t)(128 >> 4) << 24);
-        constexpr uint32_t idesc_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
-                                     ((uint32_t)(128 >> 4) << 24);
+        // ---- S = Q K^T ----------------------------------------------------------------------
+        constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(BK >> 3) << 17) |
+                                   ((uint32_t)(128 >> 4) << 24);
         // descriptors: only the start address (in 16-byte units, the low bits) changes
-        const uint64_t dq = tc::sdesc(tc::smem_addr(sm + Ly::Q)), dk = tree_desc(tc::smem_addr(sm + Ly::K), 16, Ly::GRP),
-                       dv = tree_desc(tc::smem_addr(sm + Ly::V), 1024, Ly::GRP);
-        // O (+)= P V of tile i with `steps` steps of 16 keys; fresh: the segment's first, which replaces O
-        auto pv = [&](int i, int steps, bool fresh) -> bool {
-            const int st = i & 1;
-            if (!wait(p_ready + st, i >> 1) || !wait(full_v + st, i >> 1)) return false;
-            tc::fence_after();
-            const uint32_t pa = tm + Ly::P_COL + st * (BK / 2);
-            const uint64_t vb = dv + ((uint32_t)(st * Ly::TILE) >> 4);
-            if (tree_elect()) {
-#pragma unroll
-                for (int kk = 0; kk < BK / 16; ++kk)
-                    if (kk < steps)
-                        tree_mma_ta(tm + Ly::O_COL, pa + 8 * kk, vb + (uint32_t)((2 * kk * Ly::GRP) >> 4), idesc_o,
-                                    (!fresh || kk > 0) ? 1u : 0u);
-                tc::commit(pv_done + st);
-            }
-            __syncwarp();
-            return true;
-        };
-        int it = 0, seg = 0, steps = 0;
-        bool fresh = false;  // the pending tile is its segment's first
-        while (ok && next(s)) {
-            // the segment before ends: its last P V, then the softmax warps finish it and bring the new Q
-            if (it > 0 && !pv(it - 1, steps, fresh)) break;
+        const uint64_t dq = tc::sdesc(tc::smem_addr(sm + Ly::Q)), dk = tree_desc(tc::smem_addr(sm + Ly::K), 16, Ly::GRP);
+        int it = 0, seg = 0;
+        while (ok && walk.next(s)) {
             if (!wait(q_ready, seg)) break;
             ++seg;
             for (int j = s.t0; j < s.t1; ++j, ++it) {
                 const int st = it & 1;
                 if (!wait(full_k + st, it >> 1) || (it >= 2 && !wait(s_read + st, (it - 2) >> 1))) break;
                 tc::fence_after();
-                const uint64_t kb = dk + ((uint32_t)(st * Ly::TILE) >> 4);
                 if (tree_elect()) {
+                    const uint64_t kb = dk + ((uint32_t)(st * Ly::TILE) >> 4);
 #pragma unroll
                     for (int kd = 0; kd < D / 16; ++kd)
                         tc::mma_f16(tm + st * BK, dq + (uint32_t)(((kd >> 2) * Ly::QATOM + (kd & 3) * 32) >> 4),
-                                    kb + (uint32_t)(((kd >> 2) * 1024 + (kd & 3) * 32) >> 4), idesc_s, kd > 0 ? 1u : 0u);
+                                    kb + (uint32_t)(((kd >> 2) * 1024 + (kd & 3) * 32) >> 4), idesc, kd > 0 ? 1u : 0u);
                     tc::commit(s_done + st);
                 }
                 __syncwarp();
-                if (j > s.t0 && !pv(it - 1, steps, fresh)) break;
-                fresh = j == s.t0;
-                steps = (keys_of(s, j) + 15) / 16;
             }
         }
-        if (ok && it > 0) pv(it - 1, steps, fresh);
+    } else if (warp == 11) {
+        // ---- O (+)= P V ---------------------------------------------------------------------
+        constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
+                                   ((uint32_t)(128 >> 4) << 24);
+        const uint64_t dv = tree_desc(tc::smem_addr(sm + Ly::V), 1024, Ly::GRP);
+        int it = 0, seg = 0;
+        while (ok && walk.next(s)) {
+            if (seg > 0 && !wait(o_free, seg - 1)) break;  // O of the segment before has been read
+            ++seg;
+            for (int j = s.t0; j < s.t1; ++j, ++it) {
+                const int st = it & 1, steps = (keys_of(s, j) + 15) / 16;
+                if (!wait(full_v + st, it >> 1) || !wait(p_ready + st, it >> 1)) break;
+                tc::fence_after();
+                if (tree_elect()) {
+                    const uint32_t pa = tm + Ly::P_COL + st * (BK / 2);
+                    const uint64_t vb = dv + ((uint32_t)(st * Ly::TILE) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < BK / 16; ++kk)
+                        if (kk < steps)
+                            tree_mma_ta(tm + Ly::O_COL, pa + 8 * kk, vb + (uint32_t)((2 * kk * Ly::GRP) >> 4), idesc,
+                                        (j > s.t0 || kk > 0) ? 1u : 0u);
+                    tc::commit(pv_done + st);
+                }
+                __syncwarp();
+            }
+        }
     } else {
-        // ---- softmax and epilogue: thread = row r of the tile (TMEM lane r) ----------------
-        const int q4 = warp & 3, r = 32 * q4 + lane;
+        // ---- softmax and epilogue: thread = row r of the tile (TMEM lane r), of group wg ---------
+        const int q4 = warp & 3, r = 32 * q4 + lane, wg = (warp - 2) >> 2;
         const uint32_t trow = tc::taddr(tm, 32 * q4, 0);
-        const unsigned run_bits = nseg == 32 ? 0xffffffffu : (1u << nseg) - 1u;
+        const unsigned run_bits = (1u << nseg) - 1u;  // (at most 16 runs)
         int it = 0, tails = 0;
         // Q of the tile's rows, a row (or two of D = 128) per step, all copies in flight at once.  Rows past the
         // tree are zeros
         auto load_q = [&](const TreeSeg& t) {
             constexpr int CPR = D / 8, RPS = 32 / CPR;  // 16-byte pieces of a row, rows per step
             const int c = lane % CPR;
-            int row = 32 * q4 + lane / CPR, qn = (t.rt * 128 + row) / A.G, qg = (t.rt * 128 + row) % A.G;
+            int row = 32 * q4 + 16 * wg + lane / CPR, qn = (t.rt * 128 + row) / A.G, qg = (t.rt * 128 + row) % A.G;
             const __nv_bfloat16* src = A.q + ((size_t)t.first * A.Hq + t.kvh * A.G) * D + c * 8;
             const uint32_t dst = smem_u32(sm + Ly::Q + (c >> 3) * Ly::QATOM);
 #pragma unroll 4
-            for (int i = 0; i < 32; i += RPS, row += RPS, qg += RPS) {
+            for (int i = 0; i < 16; i += RPS, row += RPS, qg += RPS) {
                 while (qg >= A.G) {
                     qg -= A.G;
                     ++qn;
@@ -501,98 +544,129 @@ __global__ void __launch_bounds__(224, 1)
             }
             cp_async_commit();
         };
-        bool have = next(s);
+        bool have = walk.next(s);
         if (have) load_q(s);
         while (have) {
             TreeSeg after;
-            const bool more = next(after);
+            const bool more = walk.next(after);
             const int node = (s.rt * 128 + r) / A.G, g = (s.rt * 128 + r) % A.G;
             const bool row_ok = node < s.n;
             const bool warp_ok = s.rt * 128 + 32 * q4 < s.n * A.G;  // a row of this warp exists
-            const bool tail = s.t1 == s.nt;                       // the segment ends with the nodes' own keys
+            const bool tail = s.t1 == s.nt;                         // the segment ends with the nodes' own keys
             cp_async_wait_all();
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_ready);
-            float m_ref = -INFINITY, l = 0.f;
-            unsigned long long mine = 0ull;  // the row's line
+            float m_used = -INFINITY, l = 0.f;  // the group's sum, relative to the reference maximum it last used
             for (int j = s.t0; j < s.t1; ++j, ++it) {
                 const int st = it & 1;
+                if (st != wg) continue;
                 const bool own_keys = j == s.nt - 1;
                 wait(gone_ready + (it & 3), it >> 2);
-                // runs of the tile without keys (a page outside the pool or past the context)
-                const unsigned gone = s_gone[it & 3] & run_bits;
-                wait(s_done + st, it >> 1);
-                tc::fence_after();
-                float sv[BK];
-                if (warp_ok) {
-                    uint32_t raw[BK];
-#pragma unroll
-                    for (int c = 0; c < BK; c += 32) tc::ld32_nowait(trow + st * BK + c, raw + c);
-                    tc::ld_wait();
-#pragma unroll
-                    for (int c = 0; c < BK; ++c) sv[c] = __uint_as_float(raw[c]);
-                }
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(s_read + st);
-                if (j == s.t1 - 1 && more) load_q(after);  // every product with this segment's Q is done
+                const unsigned gone = s_gone[it & 3] & run_bits;  // runs without keys (no page, or past the context)
                 const int keys = keys_of(s, j);
                 const bool full = !own_keys && gone == 0u && keys == BK;
-                if (own_keys) {
-                    wait(anc_ready + (tails & 1), tails >> 1);
-                    if (row_ok) mine = s_anc[(tails & 3) * 64 + node];
+                uint32_t seen[BK / 32];  // bit c: key c reaches this row
+                if (!full) {
+                    if (own_keys) {
+                        wait(anc_ready + (tails & 1), tails >> 1);
+                        const unsigned long long mine = row_ok ? s_anc[(tails & 3) * 64 + node] : 0ull;
+#pragma unroll
+                        for (int c = 0; c < BK / 32; ++c) seen[c] = c < 2 ? (uint32_t)(mine >> (32 * c)) : 0u;
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < BK / 32; ++c) {
+                            const int k = keys - 32 * c;
+                            seen[c] = k >= 32 ? 0xffffffffu : (k <= 0 ? 0u : (1u << k) - 1u);
+                            for (int e = 0; e < 32; e += 8)  // runs are multiples of 8 keys
+                                if ((gone >> ((32 * c + e) / A.R)) & 1u) seen[c] &= ~(0xffu << e);
+                        }
+                    }
+                }
+                wait(s_done + st, it >> 1);
+                tc::fence_after();
+                // 64 columns at a time (BK = 128: the maximum first takes the first half, which is loaded again below)
+                float sv[64];
+                auto load_s = [&](int half) {
+                    uint32_t raw[64];
+                    tc::ld32_nowait(trow + st * BK + 64 * half, raw);
+                    tc::ld32_nowait(trow + st * BK + 64 * half + 32, raw + 32);
+                    tc::ld_wait();
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) sv[c] = __uint_as_float(raw[c]);
+                    if (!full) {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c)
+                            sv[c] = (seen[(2 * half + (c >> 5)) % (BK / 32)] >> (c & 31)) & 1u ? sv[c] : -INFINITY;
+                    }
+                };
+                auto top = [&]() {
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], sv[c]);
+                    return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                };
+                float mt = -INFINITY;
+                if (warp_ok) {
+#pragma unroll
+                    for (int half = 0; half < BK / 64; ++half) {
+                        load_s(half);
+                        if (BK == 64) {  // S is in registers
+                            tc::fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(s_read + st);
+                        }
+                        mt = fmaxf(mt, top());
+                    }
+                } else if (lane == 0) {
+                    mbar_arrive(s_read + st);
+                }
+                // the reference maximum after the tile before, moved when the row's maximum passes it by more than 2^8 in
+                // the exponent; the next tile's group takes it from here
+                float m_ref = -INFINITY;
+                if (j > s.t0) {
+                    wait(decided + 4 * (wg ^ 1) + q4, (it - 1) >> 1);
+                    m_ref = s_mref[r];
                 }
                 float f = 1.f;
-                uint32_t pk[BK / 2];
+                if (mt > -INFINITY && (m_ref == -INFINITY || (mt - m_ref) * A.scale_log2 > 8.f)) {
+                    if (m_ref > -INFINITY) f = exp2f((m_ref - mt) * A.scale_log2);
+                    m_ref = mt;
+                }
+                s_mref[r] = m_ref;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(decided + 4 * wg + q4);
+                if (m_ref != m_used) {
+                    if (m_used > -INFINITY) l *= exp2f((m_used - m_ref) * A.scale_log2);
+                    m_used = m_ref;
+                }
+                if (it >= 2) wait(pv_done + st, (it - 2) >> 1);  // P's buffer is free
+                tc::fence_after();
                 if (warp_ok) {
-                    if (!full) {
-                        uint32_t seen[BK / 32];  // bit c: key c reaches this row
-                        if (own_keys) {
-#pragma unroll
-                            for (int c = 0; c < BK / 32; ++c) seen[c] = c < 2 ? (uint32_t)(mine >> (32 * c)) : 0u;
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < BK / 32; ++c) {
-                                const int k = keys - 32 * c;
-                                seen[c] = k >= 32 ? 0xffffffffu : (k <= 0 ? 0u : (1u << k) - 1u);
-                                for (int e = 0; e < 32; e += 8)  // runs are multiples of 8 keys
-                                    if ((gone >> ((32 * c + e) / A.R)) & 1u) seen[c] &= ~(0xffu << e);
-                            }
-                        }
-#pragma unroll
-                        for (int c = 0; c < BK; ++c) sv[c] = (seen[c >> 5] >> (c & 31)) & 1u ? sv[c] : -INFINITY;
-                    }
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // four chains: a warp has its scheduler alone
-#pragma unroll
-                    for (int c = 0; c < BK; ++c) mx[c & 3] = fmaxf(mx[c & 3], sv[c]);
-                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    // the reference maximum moves when the row's maximum passes it by more than 2^8 in the exponent
-                    if (mt > -INFINITY && (m_ref == -INFINITY || (mt - m_ref) * A.scale_log2 > 8.f)) {
-                        if (m_ref > -INFINITY) {
-                            f = exp2f((m_ref - mt) * A.scale_log2);
-                            l *= f;
-                        }
-                        m_ref = mt;
-                    }
                     // p = 2^((s - m_ref) scale log2 e), rounded to bf16, the tensor cores' operand; the sum takes the
                     // rounded weights, like the product
                     const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref * A.scale_log2;
                     const float2 sc2 = make_float2(A.scale_log2, A.scale_log2), nm2 = make_float2(neg_m, neg_m);
-                    float2 sum[4] = {};
 #pragma unroll
-                    for (int e = 0; e < BK / 2; ++e) {
-                        const float2 x = __ffma2_rn(make_float2(sv[2 * e], sv[2 * e + 1]), sc2, nm2);
-                        const __nv_bfloat162 h2 = __floats2bfloat162_rn(tree_ex2(x.x), tree_ex2(x.y));
-                        sum[e & 3] = __fadd2_rn(sum[e & 3], __bfloat1622float2(h2));
-                        pk[e] = *reinterpret_cast<const uint32_t*>(&h2);
+                    for (int half = BK / 64 - 1; half >= 0; --half) {
+                        if (half < BK / 64 - 1) {
+                            load_s(half);
+                            tc::fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(s_read + st);
+                        }
+                        float2 sum[4] = {};
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float2 x = __ffma2_rn(make_float2(sv[2 * e], sv[2 * e + 1]), sc2, nm2);
+                            const __nv_bfloat162 h2 = __floats2bfloat162_rn(tree_ex2(x.x), tree_ex2(x.y));
+                            sum[e & 3] = __fadd2_rn(sum[e & 3], __bfloat1622float2(h2));
+                            pk[e] = *reinterpret_cast<const uint32_t*>(&h2);
+                        }
+                        l += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) + ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
+                        tree_st32(trow + Ly::P_COL + st * (BK / 2) + 32 * half, pk);
                     }
-                    l += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) + ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
-                }
-                // P's buffer is free: S of this tile was issued after P V of tile it - 2, so s_done covers both
-                if (warp_ok) {
-#pragma unroll
-                    for (int c = 0; c < BK / 2; c += 32) tree_st32(trow + Ly::P_COL + st * (BK / 2) + c, pk + c);
                     if (j > s.t0 && __any_sync(0xffffffffu, f != 1.f)) {  // TMEM accesses are warp-wide
                         wait(pv_done + (st ^ 1), (it - 1) >> 1);
                         tc::fence_after();
@@ -633,14 +707,20 @@ __global__ void __launch_bounds__(224, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_ready + st);
             }
-            // ---- the segment's O: o itself, or a part to be joined -----------------------------
+            // ---- the segment's O: o itself, or a part to be joined; each group has half of the columns --------
+            named_bar_sync(1, 256);  // both groups are past their last tile: s_mref is final, every S is done
+            const float m_ref = s_mref[r];
+            if (m_used > -INFINITY && m_used != m_ref) l *= exp2f((m_used - m_ref) * A.scale_log2);
+            s_l[128 * wg + r] = l;
+            if (more) load_q(after);
             wait(pv_done + ((it - 1) & 1), (it - 1) >> 1);
             tc::fence_after();
+            named_bar_sync(1, 256);
+            l = s_l[r] + s_l[128 + r];
             unsigned long long bad = 0ull, any_bad = 0ull;
             if (tail) {
-                named_bar_sync(1, 128);
                 any_bad = s_bad[tails & 3];
-                bad = any_bad & mine;
+                bad = row_ok ? any_bad & s_anc[(tails & 3) * 64 + node] : 0ull;
                 ++tails;
             }
             const bool complete = s.t0 == 0 && tail;
@@ -649,7 +729,7 @@ __global__ void __launch_bounds__(224, 1)
             float* part = A.part + (size_t)(blockIdx.x * 2 + (s.t0 > 0 ? 0 : 1)) * (D + 2) * 128 + r;
             if (warp_ok && ok) {
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
+                for (int c0 = wg * (D / 2); c0 < (wg + 1) * (D / 2); c0 += 32) {
                     float ov[32];
                     tc::ld32(trow + Ly::O_COL + c0, ov);
                     for (unsigned long long m = any_bad; m; m &= m - 1) {  // (the same for all lanes)
@@ -681,12 +761,14 @@ __global__ void __launch_bounds__(224, 1)
                     }
                     __syncwarp();
                 }
-                if (!complete) {
+                if (!complete && wg == 0) {
                     part[D * 128] = m_ref;
                     part[(D + 1) * 128] = l;
                 }
             }
+            tc::fence_before();
             __syncwarp();
+            if (lane == 0) mbar_arrive(o_free);
             s = after;
             have = more;
         }
@@ -697,51 +779,51 @@ __global__ void __launch_bounds__(224, 1)
     if (warp == 1) tc::dealloc(tm, Ly::TMEM_COLS);
 }
 
-// One CTA per (worker w, row tile, 32 columns); thread = row.  If w's run begins inside a list whose first part is
-// worker w - 1's, it joins the parts of that list: o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
+// One CTA per (worker w, 32 columns); thread = row and 8 columns.  If w holds the second part of a list, it joins the
+// list's parts: o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, four parts in flight at a time.
+constexpr int kJoinThreads = 512;
+
 template <int D>
-__global__ void __launch_bounds__(128) k_attn_tree_join(const __grid_constant__ AttnTreeArgs A) {
-    constexpr int BK = TreeLay<D>::BK, COLS = 32;
+__global__ void __launch_bounds__(kJoinThreads) k_attn_tree_join(const __grid_constant__ AttnTreeArgs A) {
+    constexpr int COLS = 8;
     griddep_wait();
     griddep_launch_dependents();
-    const int w = blockIdx.x / A.RT + 1, sub = blockIdx.x % A.RT, c0 = blockIdx.y * COLS, r = threadIdx.x;
-    const TreeRun run = tree_run<D, 128>(A, w);
-    if (run.start >= run.end) return;
-    TreeSeg s;
-    TreeWalk<BK> walk(A, run, sub);
-    walk.next(s);
-    const long long begin = run.start - s.t0;  // the list's first tile
-    if (s.t0 == 0 || begin / run.per != w - 1) return;
-    const int last = (int)((begin + s.nt - 1) / run.per);
-    const int at = s.rt * 128 + r;
-    if (at >= s.n * A.G) return;
-    auto part = [&](int i) {  // worker i's part: its run ends with the list's beginning, or begins inside it
-        return A.part + (size_t)((i * A.RT + sub) * 2 + (i == w - 1 ? 1 : 0)) * (D + 2) * 128 + r;
+    const int w = blockIdx.x + 1, r = threadIdx.x & 127, c0 = blockIdx.y * 32 + (threadIdx.x >> 7) * COLS;
+    const int4 list = A.share[2 * w];
+    if (list.x != w - 1) return;
+    const int4 rows = A.share[2 * w + 1];
+    const int last = list.y, at = list.z * 128 + r, kvh = list.w;
+    if (at >= rows.y * A.G) return;
+    auto part = [&](int i) {  // worker i's part: its share ends with the list's beginning, or begins inside it
+        return A.part + (size_t)(i * 2 + (i == w - 1 ? 1 : 0)) * (D + 2) * 128 + r;
     };
     float M = -INFINITY;
+#pragma unroll 8
     for (int i = w - 1; i <= last; ++i) M = fmaxf(M, part(i)[D * 128]);
+    const float base = M == -INFINITY ? 0.f : M;
     float l = 0.f, o[COLS] = {};
+#pragma unroll 4
     for (int i = w - 1; i <= last; ++i) {
         const float* p = part(i);
-        const float m = p[D * 128];
-        const float f = m == -INFINITY && M > -INFINITY ? 0.f : exp2f((m - (M == -INFINITY ? 0.f : M)) * A.scale_log2);
-        l = fmaf(f, p[(D + 1) * 128], l);
+        const float m = p[D * 128], li = p[(D + 1) * 128];
+        float v[COLS];
 #pragma unroll
-        for (int c = 0; c < COLS; ++c) o[c] = fmaf(f, p[(c0 + c) * 128], o[c]);
+        for (int c = 0; c < COLS; ++c) v[c] = p[(c0 + c) * 128];
+        const float f = m == -INFINITY && M > -INFINITY ? 0.f : exp2f((m - base) * A.scale_log2);
+        l = fmaf(f, li, l);
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) o[c] = fmaf(f, v[c], o[c]);
     }
     const float inv = 1.f / l;
-    uint4 out[COLS / 8];
-    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(out);
+    uint4 out;
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&out);
 #pragma unroll
     for (int c = 0; c < COLS / 2; ++c) h[c] = __floats2bfloat162_rn(o[2 * c] * inv, o[2 * c + 1] * inv);
-    uint4* dst = reinterpret_cast<uint4*>(
-        A.o + ((size_t)(s.first + at / A.G) * A.Hq + s.kvh * A.G + at % A.G) * D + c0);
-#pragma unroll
-    for (int c = 0; c < COLS / 8; ++c) dst[c] = out[c];
+    *reinterpret_cast<uint4*>(A.o + ((size_t)(rows.x + at / A.G) * A.Hq + kvh * A.G + at % A.G) * D + c0) = out;
 }
 
 struct TreePlan {
-    int RT, W, whole;
+    int W, whole, even;
 };
 
 // sizes only: the workspace is known without a device
@@ -749,13 +831,10 @@ TreePlan tree_plan(int B, int Hq, int Hkv, int D, int max_nodes, int max_ctx) {
     const int BK = D == 256 ? 64 : 128, row_tiles = (max_nodes * (Hq / Hkv) + 127) / 128;
     const int64_t lists = (int64_t)B * Hkv * row_tiles, tiles = ((int64_t)max_ctx + BK - 1) / BK + 1;
     TreePlan p;
-    const char* e = getenv("TREE_GROUP");
-    p.RT = e && e[0] == '1' ? row_tiles : 1;
-    p.whole = tiles <= kTreeWhole && lists <= kTreeCtas ? row_tiles : 0;
-    if (p.whole) p.RT = 1;
+    p.even = lists <= kTreeCtas;
+    p.whole = tiles <= kTreeWhole && p.even ? row_tiles : 0;
     p.W = p.whole ? (int)lists
-                  : (int)std::min<int64_t>(std::max(1, kTreeCtas / p.RT),
-                                           (lists / p.RT * tiles + kTreeMinTiles - 1) / kTreeMinTiles);
+                  : (int)std::min<int64_t>(kTreeCtas, std::max(lists, (lists * tiles + kTreeMinTiles - 1) / kTreeMinTiles));
     return p;
 }
 
@@ -789,14 +868,15 @@ cudaError_t launch_attn_tree_d(const AttnTreeJob& j, cudaStream_t st) {
     A.parents = j.parents;
     A.ctx_lens = j.ctx_lens;
     A.o = static_cast<__nv_bfloat16*>(j.o);
-    A.part = static_cast<float*>(j.ws);
+    A.share = p.whole || p.W == 1 ? nullptr : static_cast<int4*>(j.ws);
     A.B = j.B;
     A.Hq = j.Hq;
     A.Hkv = j.Hkv;
     A.G = j.Hq / j.Hkv;
-    A.RT = p.RT;
+    A.part = A.share ? reinterpret_cast<float*>(A.share + 2 * p.W) : nullptr;
     A.W = p.W;
     A.whole = p.whole;
+    A.even = p.even;
     A.page = j.page;
     int R = Ly::BK;
     while (j.page % R) R >>= 1;  // rows per box: gcd(page, BK); pages hold a multiple of 8 rows
@@ -831,10 +911,10 @@ cudaError_t launch_attn_tree_d(const AttnTreeJob& j, cudaStream_t st) {
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     }
-    e = launch_pdl(k_attn_tree<D>, dim3((unsigned)(p.W * p.RT)), dim3(224), Ly::SMEM_ALLOC, st, maps[0], maps[1],
+    e = launch_pdl(k_attn_tree<D>, dim3((unsigned)p.W), dim3(kTreeThreads), Ly::SMEM_ALLOC, st, maps[0], maps[1],
                    maps[2], maps[3], A);
     if (e != cudaSuccess || p.whole || p.W == 1) return e;
-    return launch_pdl(k_attn_tree_join<D>, dim3((unsigned)((p.W - 1) * p.RT), D / 32), dim3(128), 0, st, A);
+    return launch_pdl(k_attn_tree_join<D>, dim3((unsigned)(p.W - 1), D / 32), dim3(kJoinThreads), 0, st, A);
 }
 
 }  // namespace
@@ -842,7 +922,7 @@ cudaError_t launch_attn_tree_d(const AttnTreeJob& j, cudaStream_t st) {
 size_t attn_tree_workspace_bytes(int B, int Hq, int Hkv, int D, int max_nodes, int max_ctx) {
     if (B == 0) return 0;
     const TreePlan p = tree_plan(B, Hq, Hkv, D, max_nodes, max_ctx);
-    return p.whole || p.W == 1 ? 0 : (size_t)p.W * p.RT * 2 * (D + 2) * 128 * 4;
+    return p.whole || p.W == 1 ? 0 : (size_t)p.W * (32 + 2 * (D + 2) * 128 * 4);
 }
 
 cudaError_t launch_attn_tree(const AttnTreeJob& j, cudaStream_t st) {
