@@ -114,13 +114,84 @@ __device__ __forceinline__ void tree_scan(long long v, long long* s_warp, long l
     }
 }
 
-// worker w's share: `left` tiles from tile `rem` of sequence b's lists on.  All threads of the block call it.
+// worker w's share: `left` tiles from tile `rem` of sequence b's lists on
 struct TreeRun {
     int b;
     long long rem, left;
     int first, last;  // workers that hold the list the share begins in
 };
 
+// A.even: worker w takes piece w.  Every warp works it out by itself (there are at most kTreeCtas sequences, five to a
+// lane): loads of one latency, then a bisection for the shortest pieces of which there are at most W
+template <int BK>
+__device__ __forceinline__ TreeRun tree_run_even(const AttnTreeArgs& A, int w) {
+    constexpr int PER = (kTreeCtas + 31) / 32;
+    const int lane = threadIdx.x & 31, each = (A.B + 31) / 32;
+    uint32_t nt[PER], lists[PER], most = kTreeMinTiles;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+        const int b = lane * each + e;
+        int first, n = 0, ctx;
+        nt[e] = e < each && b < A.B ? tree_tiles<BK>(A, b, first, n, ctx) : 0;
+        lists[e] = tree_lists(A, n);
+        most = max(most, nt[e]);
+    }
+    auto count = [&](uint32_t per) {  // pieces of this lane's sequences
+        uint32_t c = 0;
+#pragma unroll
+        for (int e = 0; e < PER; ++e)
+            if (e < each) c += lists[e] * ((nt[e] + per - 1) / per);
+        return c;
+    };
+    uint32_t lo = kTreeMinTiles, hi = __reduce_max_sync(0xffffffffu, most);  // (one piece per list always fits)
+    while (lo < hi) {
+        const uint32_t per = (lo + hi) / 2;
+        if (__reduce_add_sync(0xffffffffu, count(per)) <= (uint32_t)A.W)
+            hi = per;
+        else
+            lo = per + 1;
+    }
+    const uint32_t mine = count(lo);
+    uint32_t incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += x;
+    }
+    const unsigned owner = __ballot_sync(0xffffffffu, (uint32_t)w >= incl - mine && (uint32_t)w < incl);
+    TreeRun run{0, 0, 0, 0, 0};
+    if (owner == 0u) return run;
+    uint32_t at = incl - mine, piece = 0, pieces = 1, list = 0, tiles = 0;
+    bool found = false;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+        const uint32_t per_list = (nt[e] + lo - 1) / lo, len = e < each ? lists[e] * per_list : 0u;
+        if (!found && (uint32_t)w >= at && (uint32_t)w < at + len) {
+            found = true;
+            run.b = lane * each + e;
+            pieces = per_list;
+            list = ((uint32_t)w - at) / per_list;
+            piece = ((uint32_t)w - at) % per_list;
+            tiles = nt[e];
+        }
+        at += len;
+    }
+    const int src = __ffs(owner) - 1;
+    run.b = __shfl_sync(0xffffffffu, run.b, src);
+    pieces = __shfl_sync(0xffffffffu, pieces, src);
+    piece = __shfl_sync(0xffffffffu, piece, src);
+    list = __shfl_sync(0xffffffffu, list, src);
+    tiles = __shfl_sync(0xffffffffu, tiles, src);
+    // (at most 2^24 tiles and kTreeCtas pieces: the products fit)
+    const uint32_t t0 = tiles * piece / pieces, t1 = tiles * (piece + 1) / pieces;
+    run.rem = (long long)list * tiles + t0;
+    run.left = t1 - t0;
+    run.first = w - (int)piece;
+    run.last = run.first + (int)pieces - 1;
+    return run;
+}
+
+// All threads of the block call it.
 template <int D, int THREADS>
 __device__ __forceinline__ TreeRun tree_run(const AttnTreeArgs& A, int w) {
     constexpr int BK = TreeLay<D>::BK;
@@ -137,6 +208,7 @@ __device__ __forceinline__ TreeRun tree_run(const AttnTreeArgs& A, int w) {
         run.first = run.last = w;
         return run;
     }
+    if (A.even) return tree_run_even<BK>(A, w);
     // each thread sums some sequences; a scan of the threads' sums finds the one that holds the start
     const int each = (A.B + THREADS - 1) / THREADS;
     const int b0 = min(A.B, tid * each), b1 = min(A.B, b0 + each);
@@ -146,43 +218,21 @@ __device__ __forceinline__ TreeRun tree_run(const AttnTreeArgs& A, int w) {
         sum += (long long)nt * tree_lists(A, n);
     }
     tree_scan<THREADS>(sum, s_warp, before, total);
-    long long per = max((long long)kTreeMinTiles, (total + A.W - 1) / A.W);
-    if (A.even) {  // the shortest pieces of which there are at most W (a piece per list always fits)
-        while (true) {
-            sum = 0;
-            for (int b = b0; b < b1; ++b) {
-                const int nt = tree_tiles<BK>(A, b, first, n, ctx);
-                sum += (long long)tree_lists(A, n) * ((nt + per - 1) / per);
-            }
-            tree_scan<THREADS>(sum, s_warp, before, total);
-            if (total <= A.W) break;
-            per += max(1ll, per / 16);
-        }
-    }
-    // A.even: positions count pieces, and worker w takes piece w; else they count tiles
-    const long long start = A.even ? w : w * per;
+    const long long per = max((long long)kTreeMinTiles, (total + A.W - 1) / A.W), start = w * per;
     if (tid == 0) s_left = 0;
     __syncthreads();
     if (start < total && before <= start && start < before + sum) {
         long long at = before;
         for (int b = b0; b < b1; ++b) {
             const int nt = tree_tiles<BK>(A, b, first, n, ctx);
-            const long long pieces = A.even ? (nt + per - 1) / per : nt, len = tree_lists(A, n) * pieces;
+            const long long len = (long long)nt * tree_lists(A, n);
             if (start < at + len) {
-                const long long list = (start - at) / pieces, piece = (start - at) % pieces;
+                const long long in = (start - at) % nt;  // tiles of the list that lie before the share
                 s_b = b;
-                if (A.even) {
-                    const long long t0 = nt * piece / pieces;
-                    s_rem = list * nt + t0;
-                    s_left = nt * (piece + 1) / pieces - t0;
-                    s_first = w - (int)piece;
-                    s_last = s_first + (int)pieces - 1;
-                } else {
-                    s_rem = start - at;
-                    s_left = min(per, total - start);
-                    s_first = (int)((start - piece) / per);
-                    s_last = (int)((start - piece + nt - 1) / per);
-                }
+                s_rem = start - at;
+                s_left = min(per, total - start);
+                s_first = (int)((start - in) / per);
+                s_last = (int)((start - in + nt - 1) / per);
                 break;
             }
             at += len;
@@ -263,6 +313,10 @@ __device__ __forceinline__ void tree_tma_4d(void* dst, const CUtensorMap* map, i
         : "memory");
 }
 
+__device__ __forceinline__ void tree_prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // The warp that issues products runs converged and one elected lane issues: 48 cycles an instruction at N = 64,
 // the rate of the product itself (67 from a branch on the lane index, 82 with a predicate on each instruction).
 __device__ __forceinline__ bool tree_elect() {
@@ -327,17 +381,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 const __grid_constant__ AttnTreeArgs A) {
     using Ly = TreeLay<D>;
     constexpr int NCH = Ly::NCH, BK = Ly::BK;
-    griddep_wait();  // launched with programmatic serialization
-    griddep_launch_dependents();
-    const TreeRun run = tree_run<D, kTreeThreads>(A, blockIdx.x);
-    if (A.share && threadIdx.x == 0) {  // for the join
-        TreeSeg s;
-        TreeWalk<BK> walk(A, run);
-        const bool any = walk.next(s);
-        A.share[2 * blockIdx.x] = any ? make_int4(run.first, run.last, s.rt, s.kvh) : make_int4(-2, 0, 0, 0);
-        A.share[2 * blockIdx.x + 1] = any ? make_int4(s.first, s.n, 0, 0) : make_int4(0, 0, 0, 0);
-    }
-    if (run.left <= 0) return;  // (the same for all threads)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = smem_raw + ((1024 - (tc::smem_addr(smem_raw) & 1023)) & 1023);
@@ -368,11 +411,32 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         mbar_init(o_free, 8);
         fence_mbar_init();
     }
-    if (warp == 1) tc::alloc(tslot, Ly::TMEM_COLS);
-    tc::fence_before();
+    if (tid == 32) {
+        tree_prefetch_map(&tk);
+        tree_prefetch_map(&tv);
+        tree_prefetch_map(&tkn);
+        tree_prefetch_map(&tvn);
+    }
     __syncthreads();
-    tc::fence_after();
-    const uint32_t tm = *tslot;
+    griddep_wait();  // launched with programmatic serialization: what is above runs beside the kernel before
+    griddep_launch_dependents();
+    const TreeRun run = tree_run<D, kTreeThreads>(A, blockIdx.x);
+    if (A.share && tid == 352) {  // for the join
+        TreeSeg s;
+        TreeWalk<BK> walk(A, run);
+        const bool any = walk.next(s);
+        A.share[2 * blockIdx.x] = any ? make_int4(run.first, run.last, s.rt, s.kvh) : make_int4(-2, 0, 0, 0);
+        A.share[2 * blockIdx.x + 1] = any ? make_int4(s.first, s.n, 0, 0) : make_int4(0, 0, 0, 0);
+    }
+    if (run.left <= 0) return;  // (the same for all threads)
+    uint32_t tm = 0;
+    if (warp != 0 && warp != 10) {  // (the warps that load need no TMEM and do not wait for it)
+        if (warp == 1) tc::alloc(tslot, Ly::TMEM_COLS);
+        tc::fence_before();
+        named_bar_sync(2, kTreeThreads - 64);
+        tc::fence_after();
+        tm = *tslot;
+    }
     bool ok = true;
     auto wait = [&](uint64_t* bar, int phase) {  // warp-wide; after a failure nothing waits any more
         if (ok && !__all_sync(0xffffffffu, mbar_test(bar, (uint32_t)(phase & 1))))
@@ -779,41 +843,101 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     if (warp == 1) tc::dealloc(tm, Ly::TMEM_COLS);
 }
 
-// One CTA per (worker w, 32 columns); thread = row and 8 columns.  If w holds the second part of a list, it joins the
-// list's parts: o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, four parts in flight at a time.
+// o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the parts of a list.  Thread = row and 8 columns.  GROUPS = 4
+// (few lists in many parts): four groups of threads take the parts in turn, 4 in flight at a time, and join their
+// results in order; a CTA has 8 columns.  GROUPS = 1 (many lists, few parts each): a thread takes all parts, and a CTA
+// has 32 columns.  Latency counts here, not bytes (the parts lie in L2).
 constexpr int kJoinThreads = 512;
 
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) k_attn_tree_join(const __grid_constant__ AttnTreeArgs A) {
-    constexpr int COLS = 8;
+template <int D, int GROUPS>
+__global__ void __launch_bounds__(kJoinThreads, GROUPS == 4 ? 2 : 3) k_attn_tree_join(const __grid_constant__ AttnTreeArgs A) {
+    constexpr int COLS = 8, DEEP = GROUPS == 4 ? 4 : 2;
+    __shared__ int s_w;
+    __shared__ int s_count[kJoinThreads / 32];
+    __shared__ float s_part[GROUPS > 1 ? GROUPS - 1 : 1][COLS + 2][128];
+    const int tid = threadIdx.x, r = tid & 127, grp = GROUPS == 4 ? tid >> 7 : 0;
+    const int c0 = GROUPS == 4 ? blockIdx.y * COLS : blockIdx.y * 4 * COLS + (tid >> 7) * COLS;
+    if (tid == 0) s_w = -1;
     griddep_wait();
     griddep_launch_dependents();
-    const int w = blockIdx.x + 1, r = threadIdx.x & 127, c0 = blockIdx.y * 32 + (threadIdx.x >> 7) * COLS;
-    const int4 list = A.share[2 * w];
-    if (list.x != w - 1) return;
-    const int4 rows = A.share[2 * w + 1];
-    const int last = list.y, at = list.z * 128 + r, kvh = list.w;
-    if (at >= rows.y * A.G) return;
-    auto part = [&](int i) {  // worker i's part: its share ends with the list's beginning, or begins inside it
-        return A.part + (size_t)(i * 2 + (i == w - 1 ? 1 : 0)) * (D + 2) * 128 + r;
-    };
-    float M = -INFINITY;
-#pragma unroll 8
-    for (int i = w - 1; i <= last; ++i) M = fmaxf(M, part(i)[D * 128]);
-    const float base = M == -INFINITY ? 0.f : M;
-    float l = 0.f, o[COLS] = {};
-#pragma unroll 4
-    for (int i = w - 1; i <= last; ++i) {
-        const float* p = part(i);
-        const float m = p[D * 128], li = p[(D + 1) * 128];
-        float v[COLS];
+    // the blockIdx.x-th list that is cut: the worker that holds its second part
+    static_assert(kTreeCtas <= kJoinThreads, "a thread per worker");
+    const bool second = tid >= 1 && tid < A.W && A.share[2 * tid].x == tid - 1;
+    const unsigned all = __ballot_sync(0xffffffffu, second);
+    if ((tid & 31) == 0) s_count[tid >> 5] = __popc(all);
+    __syncthreads();
+    int rank = __popc(all & ((1u << (tid & 31)) - 1u));
+    for (int i = 0; i < tid >> 5; ++i) rank += s_count[i];
+    if (second && rank == (int)blockIdx.x) s_w = tid;
+    __syncthreads();
+    const int w = s_w;
+    if (w < 0) return;
+    const int4 list = A.share[2 * w], rows = A.share[2 * w + 1];
+    const int first = w - 1, last = list.y, at = list.z * 128 + r, kvh = list.w;
+    const bool there = at < rows.y * A.G;
+    float M = -INFINITY, l = 0.f, o[COLS] = {};
+    if (there) {
+        for (int i0 = first + grp; i0 <= last; i0 += GROUPS * DEEP) {
+            float m[DEEP], li[DEEP], v[DEEP][COLS];
 #pragma unroll
-        for (int c = 0; c < COLS; ++c) v[c] = p[(c0 + c) * 128];
-        const float f = m == -INFINITY && M > -INFINITY ? 0.f : exp2f((m - base) * A.scale_log2);
-        l = fmaf(f, li, l);
+            for (int e = 0; e < DEEP; ++e) {
+                const int i = i0 + GROUPS * e;
+                m[e] = -INFINITY;
+                if (i > last) continue;
+                // worker i's part: its share ends with the list's beginning, or begins inside it
+                const float* p = A.part + (size_t)(i * 2 + (i == first ? 1 : 0)) * (D + 2) * 128 + r;
+                m[e] = p[D * 128];
+                li[e] = p[(D + 1) * 128];
 #pragma unroll
-        for (int c = 0; c < COLS; ++c) o[c] = fmaf(f, v[c], o[c]);
+                for (int c = 0; c < COLS; ++c) v[e][c] = p[(c0 + c) * 128];
+            }
+            float top = M;
+#pragma unroll
+            for (int e = 0; e < DEEP; ++e) top = fmaxf(top, m[e]);
+            if (M > -INFINITY && top > M) {
+                const float f = exp2f((M - top) * A.scale_log2);
+                l *= f;
+#pragma unroll
+                for (int c = 0; c < COLS; ++c) o[c] *= f;
+            }
+            M = top;
+#pragma unroll
+            for (int e = 0; e < DEEP; ++e) {
+                if (i0 + GROUPS * e > last) continue;
+                // (a part without a key has weight 0 and zeros, or NaN where the row has no weight at all)
+                const float f = m[e] == -INFINITY ? (M > -INFINITY ? 0.f : 1.f) : exp2f((m[e] - M) * A.scale_log2);
+                l = fmaf(f, li[e], l);
+#pragma unroll
+                for (int c = 0; c < COLS; ++c) o[c] = fmaf(f, v[e][c], o[c]);
+            }
+        }
     }
+    if (GROUPS > 1) {
+        if (grp > 0) {
+            s_part[grp - 1][COLS][r] = M;
+            s_part[grp - 1][COLS + 1][r] = l;
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) s_part[grp - 1][c][r] = o[c];
+        }
+        __syncthreads();
+        if (grp > 0) return;
+        float top = M;
+#pragma unroll
+        for (int e = 0; e < GROUPS - 1; ++e) top = fmaxf(top, s_part[e][COLS][r]);
+        const float base = top == -INFINITY ? 0.f : top, f0 = M == -INFINITY && top > -INFINITY ? 0.f : exp2f((M - base) * A.scale_log2);
+        l *= f0;
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) o[c] *= f0;
+#pragma unroll
+        for (int e = 0; e < GROUPS - 1; ++e) {
+            const float m = s_part[e][COLS][r];
+            const float f = m == -INFINITY && top > -INFINITY ? 0.f : exp2f((m - base) * A.scale_log2);
+            l = fmaf(f, s_part[e][COLS + 1][r], l);
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) o[c] = fmaf(f, s_part[e][c][r], o[c]);
+        }
+    }
+    if (!there) return;
     const float inv = 1.f / l;
     uint4 out;
     __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&out);
@@ -824,6 +948,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_tree_join(const __grid_co
 
 struct TreePlan {
     int W, whole, even;
+    int joins;  // most lists that can be cut
 };
 
 // sizes only: the workspace is known without a device
@@ -835,6 +960,7 @@ TreePlan tree_plan(int B, int Hq, int Hkv, int D, int max_nodes, int max_ctx) {
     p.whole = tiles <= kTreeWhole && p.even ? row_tiles : 0;
     p.W = p.whole ? (int)lists
                   : (int)std::min<int64_t>(kTreeCtas, std::max(lists, (lists * tiles + kTreeMinTiles - 1) / kTreeMinTiles));
+    p.joins = (int)std::min<int64_t>(lists, p.W - 1);
     return p;
 }
 
@@ -914,7 +1040,8 @@ cudaError_t launch_attn_tree_d(const AttnTreeJob& j, cudaStream_t st) {
     e = launch_pdl(k_attn_tree<D>, dim3((unsigned)p.W), dim3(kTreeThreads), Ly::SMEM_ALLOC, st, maps[0], maps[1],
                    maps[2], maps[3], A);
     if (e != cudaSuccess || p.whole || p.W == 1) return e;
-    return launch_pdl(k_attn_tree_join<D>, dim3((unsigned)(p.W - 1), D / 32), dim3(kJoinThreads), 0, st, A);
+    if (4 * p.joins >= p.W) return launch_pdl(k_attn_tree_join<D, 1>, dim3((unsigned)p.joins, D / 32), dim3(kJoinThreads), 0, st, A);
+    return launch_pdl(k_attn_tree_join<D, 4>, dim3((unsigned)p.joins, D / 8), dim3(kJoinThreads), 0, st, A);
 }
 
 }  // namespace
