@@ -12,7 +12,6 @@
 // once for all nodes, no state of a node is formed, and every exponent is <= 0.  This is the
 // verify without snapshots of "Forge: how I wrote my own inference engine and overtook llama.cpp"
 // (27 August) for drafts that branch.
-#include <cooperative_groups.h>
 
 #include <algorithm>
 
@@ -24,7 +23,6 @@
 #include "gdn_tc.cuh"
 #include "gdn_tma.cuh"
 
-namespace cg = cooperative_groups;
 
 namespace gdn {
 namespace {
@@ -38,12 +36,6 @@ struct TreeArgs {
     TreeJob job;
     int nmax;  // nodes per tree that shared memory has room for
 };
-
-__device__ __forceinline__ float tree_warp_sum(float v) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    return v;
-}
 
 // NV values per lane (a power of two, at most 8), summed over groups of 8 lanes; lane l of a group ends with value
 // l / (8 / NV): each step halves the values by exchanging the half that the partner keeps
@@ -83,8 +75,14 @@ __device__ __forceinline__ float2 tree_dot(const float4& a, const float4& b, flo
     return __ffma2_rn(make_float2(a.z, a.w), make_float2(b.z, b.w), __ffma2_rn(make_float2(a.x, a.y), make_float2(b.x, b.y), acc));
 }
 __device__ __forceinline__ void tree_prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-// x sigmoid(x) by the SFU's exponential and division, 2^-21 relative at the sizes of a conv's outputs
-__device__ __forceinline__ float tree_silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
+// x sigmoid(x) by the SFU's exponential and reciprocal, five instructions (the functions of the math library spend as many
+// again on subnormal arguments, which the sum with 1 absorbs here): 2^-21 relative at the sizes of a conv's outputs
+__device__ __forceinline__ float tree_silu(float x) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return x * r;
+}
 
 // entries of a tree's nodes: a node's proper ancestors, rounded up to groups of 4
 __host__ __device__ inline int tree_entries(int n) { return n * (n - 1) / 2 + 3 * n; }
@@ -471,8 +469,6 @@ struct VtArgs {
     int nm, gv;  // gv: v-heads per CTA (G, or 1 where that fills the card better)
 };
 
-__device__ __forceinline__ float vt_silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
-
 __device__ __forceinline__ bool vt_elect() {
     uint32_t r;
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
@@ -528,52 +524,67 @@ __device__ __forceinline__ bool vt_wait(uint64_t* bar, int phase) {
     }
 }
 
-// conv + SiLU of the warp's 128 channels (ch .. ch + 3 of each lane) at the nodes i0 .. i0 + 3, all loads at once.
-// As v: to v[node][4 lane].  As k or q (scale != 0): L2-normalised times scale, to row row0 + node of [K^; Q^].
-// One copy of this code serves every call: the phases run once per CTA, and copies in line were bound by
-// instruction fetch.
-__device__ __noinline__ void vt_conv(const __nv_bfloat16* x, const __nv_bfloat16* state, int C, const int4* taps, const uint2* w,
-                                     const __nv_bfloat16* bias, int dead, int i0, int n, float* v, unsigned char* Bt, int rows,
-                                     int row0, float scale, float eps) {
+// two bf16 as fp32
+__device__ __forceinline__ float2 vt_two(uint32_t u) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+
+// conv + SiLU of the warp's 128 channels (4 to a lane) at the nodes i0 .. i0 + 3, all loads at once.  `raw` != 0: k or q,
+// its inputs in shared memory from there on (conv state first, 512 bytes to a row), L2-normalised times scale, to row
+// row0 + node of [K^; Q^].  Else v, inputs in global memory, to v[node][4 lane].  One copy of this code serves every
+// call: the phases run once per CTA, and copies in line were bound by instruction fetch.
+__device__ __noinline__ void vt_conv(uint32_t raw, const unsigned char* x, const unsigned char* state, uint32_t row_bytes,
+                                     const int4* taps, const uint2* w, const __nv_bfloat16* bias, int K, int i0, int n,
+                                     float* v, unsigned char* Bt, int rows, int row0, float scale, float eps) {
     const int lane = threadIdx.x & 31;
     uint2 u[4][4];
+    if (raw) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int4 t4 = taps[min(i0 + e, n - 1)];
-        const int tap[4] = {t4.x, t4.y, t4.z, t4.w};
+        for (int e = 0; e < 4; ++e) {
+            const int4 t4 = taps[min(i0 + e, n - 1)];
+            const int tap[4] = {t4.x, t4.y, t4.z, t4.w};
 #pragma unroll
-        for (int m = 0; m < 4; ++m)  // (x and state lie in global or in shared memory)
-            u[e][m] = *reinterpret_cast<const uint2*>(tap[m] < 64 ? x + (size_t)tap[m] * C : state + (size_t)(tap[m] - 64) * C);
+            for (int m = 0; m < 4; ++m) {
+                const uint32_t at = raw + (tap[m] < 64 ? tap[m] + K - 1 : tap[m] - 64) * 512;
+                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(u[e][m].x), "=r"(u[e][m].y) : "r"(at));
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int4 t4 = taps[min(i0 + e, n - 1)];
+            const int tap[4] = {t4.x, t4.y, t4.z, t4.w};
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                u[e][m] = __ldg(reinterpret_cast<const uint2*>((tap[m] < 64 ? x : state) + (uint64_t)(tap[m] & 63) * row_bytes));
+        }
     }
-    float y[4][4];
+    float2 y[4][2];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) y[e][c] = bias ? __bfloat162float(bias[c]) : 0.f;
+        for (int c = 0; c < 2; ++c)
+            y[e][c] = bias ? vt_two(reinterpret_cast<const uint32_t*>(bias)[c]) : make_float2(0.f, 0.f);
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-        if (m < dead) continue;  // a tap that d_conv < 4 does not have
+        if (m < 4 - K) continue;  // a tap that d_conv < 4 does not have
         const uint2 wm = w[m * 32 + lane];
-        const float2 w01 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&wm.x));
-        const float2 w23 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&wm.y));
+        const float2 w01 = vt_two(wm.x), w23 = vt_two(wm.y);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u[e][m].x));
-            const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u[e][m].y));
-            y[e][0] = fmaf(w01.x, lo.x, y[e][0]);
-            y[e][1] = fmaf(w01.y, lo.y, y[e][1]);
-            y[e][2] = fmaf(w23.x, hi.x, y[e][2]);
-            y[e][3] = fmaf(w23.y, hi.y, y[e][3]);
+            y[e][0] = __ffma2_rn(w01, vt_two(u[e][m].x), y[e][0]);
+            y[e][1] = __ffma2_rn(w23, vt_two(u[e][m].y), y[e][1]);
         }
     }
     float ss[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) y[e][c] = vt_silu(y[e][c]);
-        ss[e] = fmaf(y[e][0], y[e][0], fmaf(y[e][1], y[e][1], fmaf(y[e][2], y[e][2], y[e][3] * y[e][3])));
+        for (int c = 0; c < 2; ++c) y[e][c] = make_float2(tree_silu(y[e][c].x), tree_silu(y[e][c].y));
+        const float2 sq = __ffma2_rn(y[e][0], y[e][0], __fmul2_rn(y[e][1], y[e][1]));
+        ss[e] = sq.x + sq.y;
     }
-    if (scale != 0.f) {
+    if (raw) {
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1)
 #pragma unroll
@@ -582,13 +593,13 @@ __device__ __noinline__ void vt_conv(const __nv_bfloat16* x, const __nv_bfloat16
         for (int e = 0; e < 4; ++e) {
             const float f = scale * rsqrtf(ss[e] + eps);
             if (i0 + e < n)
-                tc::st_row4(Bt, rows, row0 + i0 + e, 4 * lane, y[e][0] * f, y[e][1] * f, y[e][2] * f, y[e][3] * f);
+                tc::st_row4(Bt, rows, row0 + i0 + e, 4 * lane, y[e][0].x * f, y[e][0].y * f, y[e][1].x * f, y[e][1].y * f);
         }
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             if (i0 + e < n)
-                *reinterpret_cast<float4*>(v + (i0 + e) * 128 + 4 * lane) = make_float4(y[e][0], y[e][1], y[e][2], y[e][3]);
+                *reinterpret_cast<float4*>(v + (i0 + e) * 128 + 4 * lane) = make_float4(y[e][0].x, y[e][0].y, y[e][1].x, y[e][1].y);
     }
 }
 
@@ -673,9 +684,15 @@ __global__ void __launch_bounds__(kVtThreads, 2)
         for (int k = from * D + tid; k < (2 + min(2, gv - i0)) * D; k += nt) {
             const int what = k / D;
             const bf* src = static_cast<const bf*>(A.p.conv_w) + (size_t)(channel(min(what, 2), i0 + what - 2) + k % D) * K;
+            bf w4[4];
+            if (K == 4) {
+                *reinterpret_cast<uint2*>(w4) = __ldg(reinterpret_cast<const uint2*>(src));
+            } else {
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
-                ws[(what * 4 + m) * D + k % D] = m >= 4 - K ? src[m - (4 - K)] : __float2bfloat16_rn(0.f);
+                for (int m = 0; m < 4; ++m) w4[m] = m >= 4 - K ? src[m - (4 - K)] : __float2bfloat16_rn(0.f);
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m) ws[(what * 4 + m) * D + k % D] = w4[m];
         }
     };
     stage_weights(0, 0, kVtThreads);
@@ -792,11 +809,11 @@ __global__ void __launch_bounds__(kVtThreads, 2)
         const int batches = (n + 3) / 4;  // of 4 nodes
         auto conv = [&](int what, int i, int batch) {  // what: k (0) and q (1) from shared memory, v of v-head j0 + i (2)
             const int ch = channel(what, i) + 4 * lane;
-            const bf* x = what < 2 ? raw + Km1 * 2 * D + what * D + 4 * lane : xb + ch;
-            vt_conv(x, what < 2 ? x - Km1 * 2 * D : cb + ch, what < 2 ? 2 * D : C, taps,
+            vt_conv(what < 2 ? smem_u32(raw + what * D + 4 * lane) : 0u, reinterpret_cast<const unsigned char*>(xb + ch),
+                    reinterpret_cast<const unsigned char*>(cb + ch), (uint32_t)C * 2u, taps,
                     reinterpret_cast<const uint2*>(ws + (what + (i & 1)) * 4 * D),
-                    A.p.conv_b ? static_cast<const bf*>(A.p.conv_b) + ch : nullptr, 4 - K, 4 * batch, n, v, Bt, 2 * nm,
-                    what == 1 ? nm : 0, what == 0 ? 1.f : (what == 1 ? g.q_scale : 0.f), g.l2_eps);
+                    A.p.conv_b ? static_cast<const bf*>(A.p.conv_b) + ch : nullptr, K, 4 * batch, n, v, Bt, 2 * nm,
+                    what == 1 ? nm : 0, what == 0 ? 1.f : g.q_scale, g.l2_eps);
         };
         if (warp == 7) {  // entries before each node: scan of the numbers of proper ancestors, rounded up to pairs
             int base = 0;
@@ -871,39 +888,45 @@ __global__ void __launch_bounds__(kVtThreads, 2)
                     float* T = gram + (e * ((nm + 31) / 32) + half) * nm * 32 + lane;
                     unsigned char* Mt = sm + lay.M + (e * ((nm + 31) / 32) + half) * nm * 128;
                     const float2* from = ent + e * vt_entries(nm);
-                    int at = 0;
+                    // the entries of all nodes lie end to end: those of the next step are loaded before this step's
+                    // rows of T (up to 4 entries past the last one are read, inside the layout, and not used)
+                    int at = 0, end = off[1];
+                    float mine = own[0];
+                    float4 k01, k23;
+                    uint32_t w;
+                    auto fetch = [&]() {
+                        k01 = *reinterpret_cast<const float4*>(from + at);
+                        k23 = *reinterpret_cast<const float4*>(from + at + 2);
+                        w = *reinterpret_cast<const uint16_t*>(who + at) | (uint32_t)*reinterpret_cast<const uint16_t*>(who + at + 2) << 16;
+                    };
+                    fetch();
 #pragma unroll 1
                     for (int node = 0; node < n; ++node) {
-                        const int end = off[node + 1];
-                        const float mine = own[node];
+                        const int next_end = off[min(node + 2, n)];
+                        const float next_mine = own[min(node + 1, n - 1)];
                         float su[4] = {}, so[4] = {};
 #pragma unroll 1
-                        for (; at + 2 < end; at += 4) {
-                            float2 k[4];
-                            float t[4];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) t[q] = T[who[at + q] * 32];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) k[q] = from[at + q];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                su[q] = fmaf(k[q].x, t[q], su[q]);
-                                so[q] = fmaf(k[q].y, t[q], so[q]);
-                            }
-                        }
-                        if (at < end) {
-#pragma unroll
-                            for (int q = 0; q < 2; ++q) {
-                                const float2 k = from[at + q];
-                                const float t = T[who[at + q] * 32];
-                                su[q] = fmaf(k.x, t, su[q]);
-                                so[q] = fmaf(k.y, t, so[q]);
-                            }
-                            at += 2;
+                        while (at < end) {
+                            const bool four = at + 2 < end;
+                            const float t0 = T[(w & 255) * 32], t1 = T[((w >> 8) & 255) * 32];
+                            const float t2 = four ? T[((w >> 16) & 255) * 32] : 0.f, t3 = four ? T[(w >> 24) * 32] : 0.f;
+                            const float4 a = k01, c = four ? k23 : make_float4(0.f, 0.f, 0.f, 0.f);
+                            at += four ? 4 : 2;
+                            fetch();
+                            su[0] = fmaf(a.x, t0, su[0]);
+                            so[0] = fmaf(a.y, t0, so[0]);
+                            su[1] = fmaf(a.z, t1, su[1]);
+                            so[1] = fmaf(a.w, t1, so[1]);
+                            su[2] = fmaf(c.x, t2, su[2]);
+                            so[2] = fmaf(c.y, t2, so[2]);
+                            su[3] = fmaf(c.z, t3, su[3]);
+                            so[3] = fmaf(c.w, t3, so[3]);
                         }
                         const float t = (node == 32 * half + lane ? 1.f : 0.f) - ((su[0] + su[1]) + (su[2] + su[3]));
                         T[node * 32] = t;
                         tc::st_elem(Mt, nm, node, lane, fmaf(mine, t, (so[0] + so[1]) + (so[2] + so[3])));
+                        end = next_end;
+                        mine = next_mine;
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -914,6 +937,14 @@ __global__ void __launch_bounds__(kVtThreads, 2)
             for (int i = i0; i < i0 + two; ++i) {
 #pragma unroll 1
                 for (int k = warp; k < batches; k += workers) conv(2, i, k);
+                uint2 zr[4];  // of the nodes below, four at a time
+                auto load_z = [&](int from) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        zr[q] = __ldg(reinterpret_cast<const uint2*>(static_cast<const bf*>(J.z) +
+                                                                    ((size_t)(first + min(from + workers * q, n - 1)) * Hv + j0 + i) * D) + lane);
+                };
+                if (warp >= 4) load_z(warp);
                 named_bar_sync(4, 32 * workers);
                 if (warp < 4) {
                     // ---- thread = state row: w and e^G r, then o in v's place (its own column) ------------
@@ -956,6 +987,7 @@ __global__ void __launch_bounds__(kVtThreads, 2)
                     tc::fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(w_ready + (i & 1));
+                    load_z(warp);
                     wait(o_done + (i & 1), i >> 1);
                     tc::fence_after();
                     const unsigned char* Mt = sm + lay.M + (i & 1) * ((nm + 31) / 32) * nm * 128;
@@ -989,44 +1021,37 @@ __global__ void __launch_bounds__(kVtThreads, 2)
                 }
                 named_bar_sync(4, 32 * workers);
                 if (warp < 4 && i + 2 < gv) asm volatile("bar.arrive 3, 160;" ::: "memory");  // this v-head's columns are free
-                // gated RMSNorm, a warp per node, two nodes at once, four channels to a lane
-                const int j = j0 + i;
+                // gated RMSNorm, a warp per node, four nodes at once, four channels to a lane
                 const uint2 nw = __ldg(reinterpret_cast<const uint2*>(A.p.norm_w) + lane);
-                const float2 w01 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&nw.x));
-                const float2 w23 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&nw.y));
+                const float2 w01 = vt_two(nw.x), w23 = vt_two(nw.y);
 #pragma unroll 1
-                for (int i0 = warp; i0 < n; i0 += 2 * workers) {
-                    uint2 zr[2];
-                    float4 o[2];
-                    float ss[2];
+                for (int n0 = warp; n0 < n; n0 += 4 * workers) {
+                    if (n0 > warp) load_z(n0);
+                    float4 o[4];
+                    float ss[4];
 #pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        zr[q] = __ldg(reinterpret_cast<const uint2*>(static_cast<const bf*>(J.z) +
-                                                                    ((size_t)(first + min(i0 + workers * q, n - 1)) * Hv + j) * D) + lane);
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        o[q] = *reinterpret_cast<const float4*>(v + min(i0 + workers * q, n - 1) * D + 4 * lane);
+                    for (int q = 0; q < 4; ++q) {
+                        o[q] = *reinterpret_cast<const float4*>(v + min(n0 + workers * q, n - 1) * D + 4 * lane);
                         ss[q] = fmaf(o[q].x, o[q].x, fmaf(o[q].y, o[q].y, fmaf(o[q].z, o[q].z, o[q].w * o[q].w)));
                     }
 #pragma unroll
                     for (int off = 16; off > 0; off >>= 1)
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) ss[q] += __shfl_xor_sync(0xffffffffu, ss[q], off);
+                        for (int q = 0; q < 4; ++q) ss[q] += __shfl_xor_sync(0xffffffffu, ss[q], off);
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const int node = i0 + workers * q;
-                        const float inv = rsqrtf(ss[q] / (float)D + g.norm_eps);
-                        const float2 z01 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&zr[q].x));
-                        const float2 z23 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&zr[q].y));
-                        const __nv_bfloat162 y01 = __floats2bfloat162_rn(o[q].x * inv * w01.x * vt_silu(z01.x),
-                                                                         o[q].y * inv * w01.y * vt_silu(z01.y));
-                        const __nv_bfloat162 y23 = __floats2bfloat162_rn(o[q].z * inv * w23.x * vt_silu(z23.x),
-                                                                         o[q].w * inv * w23.y * vt_silu(z23.y));
+                    for (int q = 0; q < 4; ++q) {
+                        const int node = n0 + workers * q;
+                        const float inv = rsqrtf(fmaf(ss[q], 1.f / D, g.norm_eps));
+                        const float2 z01 = vt_two(zr[q].x), z23 = vt_two(zr[q].y);
+                        const __nv_bfloat162 y01 = __floats2bfloat162_rn(o[q].x * inv * w01.x * tree_silu(z01.x),
+                                                                         o[q].y * inv * w01.y * tree_silu(z01.y));
+                        const __nv_bfloat162 y23 = __floats2bfloat162_rn(o[q].z * inv * w23.x * tree_silu(z23.x),
+                                                                         o[q].w * inv * w23.y * tree_silu(z23.y));
                         uint2 out;
                         memcpy(&out.x, &y01, 4);
                         memcpy(&out.y, &y23, 4);
                         if (ok && node < n)
-                            *(reinterpret_cast<uint2*>(static_cast<bf*>(J.y) + ((size_t)(first + node) * Hv + j) * D) + lane) = out;
+                            *(reinterpret_cast<uint2*>(static_cast<bf*>(J.y) + ((size_t)(first + node) * Hv + j0 + i) * D) + lane) = out;
                     }
                 }
                 if (i + 1 < gv) named_bar_sync(4, 32 * workers);  // o is read: its place takes the next v
