@@ -75,12 +75,16 @@ __device__ __forceinline__ float2 tree_dot(const float4& a, const float4& b, flo
     return __ffma2_rn(make_float2(a.z, a.w), make_float2(b.z, b.w), __ffma2_rn(make_float2(a.x, a.y), make_float2(b.x, b.y), acc));
 }
 __device__ __forceinline__ void tree_prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+__device__ __forceinline__ float tree_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 // x sigmoid(x) by the SFU's exponential and reciprocal, five instructions (the functions of the math library spend as many
 // again on subnormal arguments, which the sum with 1 absorbs here): 2^-21 relative at the sizes of a conv's outputs
 __device__ __forceinline__ float tree_silu(float x) {
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + tree_ex2(x * -1.4426950408889634f)));
     return x * r;
 }
 
@@ -410,53 +414,50 @@ __global__ void __launch_bounds__(kTreeThreads, 2) k_tree_verify(const __grid_co
 }
 
 // ---- the same on the tensor cores (d = 128, bf16 activations) ---------------------
-// One CTA per (k-head, tree).  With p_j = S_0 k_j, r_j = S_0 q_j and w_j = beta_j (v_j - e^{G_j} p_j), the sums above
-// are linear in w: u = T w with T the inverse of the unit triangular matrix of the ancestors' coefficients, and
-//   o_i = e^{G_i} r_i + sum_j M_ij w_j,   M = (the queries' coefficients) T,
-// with M of n x n per v-head and the same for all 128 state rows.  So (all products TF32, fp32 accumulation):
+// One CTA per (k-head, tree).  With p_j = S_0 k_j, r_j = S_0 q_j and w_j = beta_j (v_j - e^{G_j} p_j), the sums above are
+//   u = T w,   o_i = e^{G_i} r_i + sum_j P_ij u_j,   T = (I + A)^-1,
+// with A (keys: beta_i e^{G_i - G_j} k_i . k_j, j a proper ancestor) and P (queries: e^{G_i - G_j} q_i . k_j, j = i too) of
+// n x n per v-head and the same for all 128 state rows.  So (all products TF32, fp32 accumulation):
 //   [K^; Q^] K^T    M = 128, N = nm, once: the products of the nodes' keys and queries with keys;
 //   S_0 [K^; Q^]^T  per v-head, M = 128 state rows, N = 2 nm, S_0 as it lies in the pool (fp32, brought by tensor
 //                   TMA 32 columns at a time; the tensor core reads its leading 10 fraction bits, as it does of K^ and
 //                   Q^ rounded): p and r in TMEM;
-//   r += w M^T      w in TMEM in p's place.
-// M comes from one warp (two above 32 nodes), a lane per column of T, walking the nodes in order with the
-// coefficients of each node's line; it runs ahead of the other warps, which make v, w, o and y.  TF32's 2^-11 per
+//   u = w T^T       w in TMEM in p's place;
+//   r += u P^T      u in TMEM, rounded by way of registers.
+// T is made in place of A, in fp32, by a warp (two above 32 nodes) per v-head: blocks of 16 on the diagonal by
+// substitution, a column to a lane; then T21 = -T22 A21 T11 for the blocks of 16 and of 32 below it.  TF32's 2^-11 per
 // operand is a quarter of the bf16 rounding of y; the decays, T's sums and the norms are fp32.  The phases are short
-// and bound by latency and instructions, so the state's place in shared memory is kept to half a tile: two CTAs
-// per SM up to 32 nodes.
-constexpr int kVtThreads = 288;  // 8 warps and the one that drives the copies and the products
+// and bound by latency and instructions: many warps share each of them, and two CTAs share an SM up to 32 nodes (the
+// state's place in shared memory is half a tile for that).
+constexpr int kVtWorkers = 7;    // and a warp that drives the copies and the products
+constexpr int kVtThreads = 32 * (kVtWorkers + 1);
+constexpr int kVtNodes = 5;      // nodes that a warp takes at a time in the conv and the norm
+constexpr int kVtRows = 4;       // warps 0 .. 3 have the state rows: TMEM lanes by quarter
 constexpr int kVtAtom = 16384;   // 128 state rows x 32 columns
 
 struct VtSmem {
-    int S, B, M, v, gram, ent, who, w, own, taps, gate, beta, eg, line, up, off, bar, total;
+    int S, B, A, P, v, w, taps, gate, beta, eg, line, up, bad, bar, total;
 };
 
-// entries of a tree's nodes: a node's proper ancestors, rounded up to pairs
-__host__ __device__ inline int vt_entries(int nm) { return nm * (nm - 1) / 2 + nm; }
-
 __host__ __device__ inline VtSmem vt_smem(int nm, int gv) {  // nm: nodes, rounded up to 16
-    const int halves = (nm + 31) / 32, two = gv > 1 ? 2 : 1;   // v-heads are taken two at a time
+    const int two = gv > 1 ? 2 : 1;  // v-heads are taken two at a time
     VtSmem s;
     int o = 0;
-    s.S = o; o += 2 * kVtAtom;               // ring of state atoms
-    s.B = o; o += 2 * nm * 512;              // [K^; Q^]: 4 atoms of 2 nm rows x 128 bytes
-    s.M = o; o += two * halves * nm * 128;   // M of two v-heads: atoms of nm rows x 32 columns
-    s.v = o; o += nm * 512;                  // v, then o: [node][row]; at first, from M on: raw q, k of [K - 1 + n] rows
-    if (o < s.M + (nm + 3) * 512) o = s.M + (nm + 3) * 512;
-    s.gram = o;                              // the products of the nodes' k and q with keys; then T: [v-head][half][node][32]
-    o += 2 * nm * (nm + 1) * 4 > two * halves * nm * 128 ? 2 * nm * (nm + 1) * 4 : two * halves * nm * 128;
-    s.ent = o; o += two * vt_entries(nm) * 8;         // two coefficients per (node, proper ancestor)
-    s.who = o; o += (vt_entries(nm) + 15) / 16 * 16;  // and that ancestor
-    s.w = o; o += (2 + two) * 4 * 128 * 2;   // conv weights of k, q and two v-heads: [4 taps][128]
-    s.own = o; o += nm * 4;                  // q_i . k_i
-    s.taps = o; o += nm * 16;                // rows of the conv taps: a node, or 64 + a row of the conv state
-    s.gate = o; o += nm * gv * 4;            // log alpha, then its sum G along the line, per (node, v-head)
+    s.S = o; o += 2 * kVtAtom;                       // ring of state atoms
+    s.B = o; o += 2 * nm * 512;                      // [K^; Q^]: 4 atoms of 2 nm rows x 128 bytes
+    s.A = o; o += two * ((nm + 31) / 32) * nm * 128; // A, then T, of two v-heads: atoms of nm rows x 32 columns
+    s.P = o; o += two * ((nm + 31) / 32) * nm * 128; // (at first, from A on: raw q and k of [K - 1 + n] rows)
+    s.v = o; o += nm * 512;                          // v, then o: [node][row]
+    s.w = o; o += (2 + two) * 4 * 128 * 2;           // conv weights of k, q and two v-heads: [4 taps][128]
+    s.taps = o; o += nm * 16;                        // rows of the conv taps: K - 1 rows of the conv state, then the nodes
+    s.gate = o; o += nm * gv * 4;                    // [v-head][node]: log2 alpha, then its sum G along the line
     s.beta = o; o += nm * gv * 4;
-    s.eg = o; o += nm * gv * 4;              // e^G
+    s.eg = o; o += nm * gv * 4;                      // 2^G
     s.line = o; o += nm * 8;
     s.up = o; o += nm * 4;
-    s.off = o; o += (nm + 4) * 4;            // first entry of each node
-    s.bar = o; o += 16 * 8;
+    s.bad = o; o += 5 * 8;                           // nodes with an infinite or NaN w, and u, per v-head of the pair; and
+                                                     // whether A or P has one
+    s.bar = o; o += 20 * 8;
     // the Gram product reads 128 rows of each atom, whatever 2 nm is: all of them lie inside the allocation
     s.total = o > s.B + 3 * 2 * nm * 128 + kVtAtom ? o : s.B + 3 * 2 * nm * 128 + kVtAtom;
     return s;
@@ -498,11 +499,11 @@ __device__ __forceinline__ void vt_st8(uint32_t ta, const float v[8]) {
 }
 
 // a product with A in TMEM (lane = row, column = k)
-__device__ __forceinline__ void vt_mma_ta(uint32_t d, uint32_t a, uint64_t bd, uint32_t idesc) {
+__device__ __forceinline__ void vt_mma_ta(uint32_t d, uint32_t a, uint64_t bd, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, 1, 0;\n"
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
         " tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-        "r"(a), "l"(bd), "r"(idesc)
+        "r"(a), "l"(bd), "r"(idesc), "r"(acc)
         : "memory");
 }
 
@@ -529,39 +530,40 @@ __device__ __forceinline__ float2 vt_two(uint32_t u) {
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
 
-// conv + SiLU of the warp's 128 channels (4 to a lane) at the nodes i0 .. i0 + 3, all loads at once.  `raw` != 0: k or q,
+// conv + SiLU of the warp's 128 channels (4 to a lane) at kVtNodes nodes from i0 on, all loads at once.  `raw` != 0: k or q,
 // its inputs in shared memory from there on (conv state first, 512 bytes to a row), L2-normalised times scale, to row
-// row0 + node of [K^; Q^].  Else v, inputs in global memory, to v[node][4 lane].  One copy of this code serves every
+// row0 + node of [K^; Q^].  Else v, inputs in global memory (x: from K - 1 rows
+// before the first node's), to v[node][4 lane].  One copy of this code serves every
 // call: the phases run once per CTA, and copies in line were bound by instruction fetch.
 __device__ __noinline__ void vt_conv(uint32_t raw, const unsigned char* x, const unsigned char* state, uint32_t row_bytes,
                                      const int4* taps, const uint2* w, const __nv_bfloat16* bias, int K, int i0, int n,
                                      float* v, unsigned char* Bt, int rows, int row0, float scale, float eps) {
     const int lane = threadIdx.x & 31;
-    uint2 u[4][4];
+    uint2 u[kVtNodes][4];
     if (raw) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < kVtNodes; ++e) {
             const int4 t4 = taps[min(i0 + e, n - 1)];
             const int tap[4] = {t4.x, t4.y, t4.z, t4.w};
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                const uint32_t at = raw + (tap[m] < 64 ? tap[m] + K - 1 : tap[m] - 64) * 512;
+                const uint32_t at = raw + tap[m] * 512;
                 asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(u[e][m].x), "=r"(u[e][m].y) : "r"(at));
             }
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < kVtNodes; ++e) {
             const int4 t4 = taps[min(i0 + e, n - 1)];
             const int tap[4] = {t4.x, t4.y, t4.z, t4.w};
 #pragma unroll
             for (int m = 0; m < 4; ++m)
-                u[e][m] = __ldg(reinterpret_cast<const uint2*>((tap[m] < 64 ? x : state) + (uint64_t)(tap[m] & 63) * row_bytes));
+                u[e][m] = __ldg(reinterpret_cast<const uint2*>((tap[m] < K - 1 ? state : x) + (uint64_t)(uint32_t)tap[m] * row_bytes));
         }
     }
-    float2 y[4][2];
+    float2 y[kVtNodes][2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < kVtNodes; ++e)
 #pragma unroll
         for (int c = 0; c < 2; ++c)
             y[e][c] = bias ? vt_two(reinterpret_cast<const uint32_t*>(bias)[c]) : make_float2(0.f, 0.f);
@@ -571,14 +573,14 @@ __device__ __noinline__ void vt_conv(uint32_t raw, const unsigned char* x, const
         const uint2 wm = w[m * 32 + lane];
         const float2 w01 = vt_two(wm.x), w23 = vt_two(wm.y);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < kVtNodes; ++e) {
             y[e][0] = __ffma2_rn(w01, vt_two(u[e][m].x), y[e][0]);
             y[e][1] = __ffma2_rn(w23, vt_two(u[e][m].y), y[e][1]);
         }
     }
-    float ss[4];
+    float ss[kVtNodes];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < kVtNodes; ++e) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) y[e][c] = make_float2(tree_silu(y[e][c].x), tree_silu(y[e][c].y));
         const float2 sq = __ffma2_rn(y[e][0], y[e][0], __fmul2_rn(y[e][1], y[e][1]));
@@ -588,19 +590,150 @@ __device__ __noinline__ void vt_conv(uint32_t raw, const unsigned char* x, const
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) ss[e] += __shfl_xor_sync(0xffffffffu, ss[e], off);
+            for (int e = 0; e < kVtNodes; ++e) ss[e] += __shfl_xor_sync(0xffffffffu, ss[e], off);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < kVtNodes; ++e) {
             const float f = scale * rsqrtf(ss[e] + eps);
             if (i0 + e < n)
                 tc::st_row4(Bt, rows, row0 + i0 + e, 4 * lane, y[e][0].x * f, y[e][0].y * f, y[e][1].x * f, y[e][1].y * f);
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < kVtNodes; ++e)
             if (i0 + e < n)
                 *reinterpret_cast<float4*>(v + (i0 + e) * 128 + 4 * lane) = make_float4(y[e][0].x, y[e][0].y, y[e][1].x, y[e][1].y);
     }
+}
+
+// A, T and P: [atom of 32 columns][rows][128 bytes], swizzled
+__device__ __forceinline__ float* vt_at(unsigned char* t, int rows, int r, int c) {
+    return reinterpret_cast<float*>(t + tc::sw_off(rows, r, c));
+}
+
+__device__ __forceinline__ float4 vt_ld4(uint32_t at) {
+    float4 x;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(at) : "memory");
+    return x;
+}
+__device__ __forceinline__ float vt_ld1(uint32_t at) {
+    float x;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+    return x;
+}
+__device__ __forceinline__ void vt_st1(uint32_t at, float x) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(x) : "memory"); }
+
+// the inverses of I + A's blocks of 16 on the diagonal at rows 16 b0 and, by the upper half of the warp, 16 (b0 + 1):
+// lane = column, its values in registers
+__device__ __noinline__ void vt_diag(unsigned char* A, int rows, int b0, int nb) {
+    const int lane = threadIdx.x & 31, c = lane & 15;
+    const bool on = b0 + (lane >> 4) < nb;
+    const int r0 = 16 * (on ? b0 + (lane >> 4) : b0);
+    const uint32_t at = smem_u32(vt_at(A, rows, r0, r0)), col = at + (c & 3) * 4;  // (rows r0 + i: i & 7 picks the swizzle)
+    float t[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < i; j += 4) {
+            const float4 a = vt_ld4((at ^ (uint32_t)(((j >> 2) ^ (i & 7)) << 4)) + i * 128);
+            s[0] = fmaf(a.x, t[j], s[0]);
+            if (j + 1 < i) s[1] = fmaf(a.y, t[j + 1], s[1]);
+            if (j + 2 < i) s[0] = fmaf(a.z, t[j + 2], s[0]);
+            if (j + 3 < i) s[1] = fmaf(a.w, t[j + 3], s[1]);
+        }
+        t[i] = (c == i ? 1.f : 0.f) - (s[0] + s[1]);
+    }
+    __syncwarp();
+    if (on) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) vt_st1((col ^ (uint32_t)(((c >> 2) ^ (i & 7)) << 4)) + i * 128, t[i]);
+    }
+    __syncwarp();
+}
+
+// the two warps that make T of v-head e of the pair (constant names: a computed one takes all 16 barriers of the CTA)
+__device__ __forceinline__ void vt_pair_sync(int e) {
+    if (e == 0)
+        named_bar_sync(5, 64);
+    else
+        named_bar_sync(6, 64);
+}
+
+// T in A's place over the nodes' lines alone, row by row; lane = two columns
+__device__ __noinline__ void vt_lines(unsigned char* A, int rows, int n, const unsigned long long* line) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        float s[2] = {0.f, 0.f};
+        for (unsigned long long m = line[i] & ~(1ull << i); m; m &= m - 1) {
+            const int j = __ffsll((long long)m) - 1;
+            const float a = *vt_at(A, rows, i, j);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (lane + 32 * e < rows) s[e] = fmaf(a, *vt_at(A, rows, j, lane + 32 * e), s[e]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (lane + 32 * e < rows) *vt_at(A, rows, i, lane + 32 * e) = (lane + 32 * e == i ? 1.f : 0.f) - s[e];
+        __syncwarp();
+    }
+}
+
+// T21 = -T22 (A21 T11) in A21's place: rows r0 .. r0 + k2 - 1, columns c0 .. c0 + k1 - 1 (both diagonal blocks are
+// inverted).  The warp has the 16 columns from `col` on, a lane a column and 8 rows of each 16; with two warps (pair >= 0)
+// the one waits for the other before A21 is overwritten.
+__device__ __noinline__ void vt_below(unsigned char* A, int rows, int r0, int c0, int k1, int k2, int col, int pair) {
+    const int lane = threadIdx.x & 31, c = col + (lane & 15), g = 8 * (lane >> 4);
+    // (row & 7 picks the swizzle, so that with rows and columns in steps of 8 and 4 the addresses differ by constants)
+    const uint32_t own = smem_u32(vt_at(A, rows, r0 + g, c));
+    auto product = [&](float (&acc)[2][8], int lk, int K) {  // rows r0 + 16 p + g + e: L[.][lk + k] R[lk + k][c]
+        uint32_t right = smem_u32(vt_at(A, rows, lk, c)), left = smem_u32(vt_at(A, rows, r0 + g, lk));
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[p][e] = 0.f;
+#pragma unroll 1
+        for (int k = 0; k < K; k += 8) {
+#pragma unroll
+            for (int h = 0; h < 8; h += 4) {
+                float x[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) x[q] = vt_ld1((right ^ (uint32_t)((h + q) << 4)) + (h + q) * 128);
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    if (16 * p >= k2) break;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float4 l = vt_ld4((left ^ (uint32_t)(((h >> 2) ^ e) << 4)) + (16 * p + e) * 128);
+                        acc[p][e] = fmaf(l.x, x[0], fmaf(l.y, x[1], fmaf(l.z, x[2], fmaf(l.w, x[3], acc[p][e]))));
+                    }
+                }
+            }
+            right += 8 * 128;
+            left ^= (uint32_t)(((k >> 2) ^ ((k + 8) >> 2)) << 4);  // the next 8 columns (K <= 32: inside the atom)
+        }
+    };
+    auto store = [&](const float (&acc)[2][8], float sign) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            if (16 * p >= k2) break;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) vt_st1((own ^ (uint32_t)(e << 4)) + (16 * p + e) * 128, sign * acc[p][e]);
+        }
+    };
+    float acc[2][8];
+    product(acc, c0, k1);
+    if (pair >= 0)
+        vt_pair_sync(pair);
+    else
+        __syncwarp();
+    store(acc, 1.f);
+    __syncwarp();
+    product(acc, r0, k2);
+    __syncwarp();
+    store(acc, -1.f);
+    __syncwarp();
 }
 
 __global__ void __launch_bounds__(kVtThreads, 2)
@@ -613,6 +746,23 @@ __global__ void __launch_bounds__(kVtThreads, 2)
     const int h = blockIdx.x / per_k, j0 = h * g.G + (blockIdx.x % per_k) * gv, b = blockIdx.y;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int Hk = g.Hk, Hv = g.Hv, K = g.K, Km1 = g.K - 1, C = g.C_ch;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* sm = smem_raw + ((1024 - (tc::smem_addr(smem_raw) & 1023)) & 1023);
+    const VtSmem lay = vt_smem(nm, gv);
+    unsigned char* Bt = sm + lay.B;
+    bf* ws = reinterpret_cast<bf*>(sm + lay.w);
+    int4* taps = reinterpret_cast<int4*>(sm + lay.taps);
+    float* gate = reinterpret_cast<float*>(sm + lay.gate);
+    float* betas = reinterpret_cast<float*>(sm + lay.beta);
+    float* eg = reinterpret_cast<float*>(sm + lay.eg);
+    unsigned long long* line = reinterpret_cast<unsigned long long*>(sm + lay.line);
+    unsigned long long* s_bad = reinterpret_cast<unsigned long long*>(sm + lay.bad);
+    int* up = reinterpret_cast<int*>(sm + lay.up);
+    // full, freed: state atoms; done: p and r; w_ready: w and e^G r in TMEM; t_ready: T; u_done, u_ready: u, rounded u;
+    // o_done: o; o_read: o has left TMEM
+    uint64_t *full = reinterpret_cast<uint64_t*>(sm + lay.bar), *freed = full + 2, *done = full + 4, *w_ready = full + 6,
+             *t_ready = full + 8, *u_done = full + 10, *u_ready = full + 12, *o_done = full + 14, *o_read = full + 16, *bar_g = full + 18;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(full + 19);
     griddep_wait();  // launched with programmatic serialization
     griddep_launch_dependents();
     const int slot = J.slot_idx[b];
@@ -621,108 +771,132 @@ __global__ void __launch_bounds__(kVtThreads, 2)
     if (slot < 0 || slot >= J.n_slots || first < 0 || count < 1 || count > J.max_nodes || first + count > J.n_nodes)
         return;
     const int n = (int)count;
-
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char* sm = smem_raw + ((1024 - (tc::smem_addr(smem_raw) & 1023)) & 1023);
-    const VtSmem lay = vt_smem(nm, gv);
-    unsigned char* Bt = sm + lay.B;
-    unsigned char* who = sm + lay.who;
-    float* gram = reinterpret_cast<float*>(sm + lay.gram);
-    float2* ent = reinterpret_cast<float2*>(sm + lay.ent);
-    bf* ws = reinterpret_cast<bf*>(sm + lay.w);
-    float* own = reinterpret_cast<float*>(sm + lay.own);
-    int4* taps = reinterpret_cast<int4*>(sm + lay.taps);
-    float* gate = reinterpret_cast<float*>(sm + lay.gate);
-    float* betas = reinterpret_cast<float*>(sm + lay.beta);
-    float* eg = reinterpret_cast<float*>(sm + lay.eg);
-    unsigned long long* line = reinterpret_cast<unsigned long long*>(sm + lay.line);
-    int* up = reinterpret_cast<int*>(sm + lay.up);
-    int* off = reinterpret_cast<int*>(sm + lay.off);
-    // full, freed: state atoms; done: p and r; w_ready: w and e^G r in TMEM; m_ready: M; o_done: o
-    uint64_t *full = reinterpret_cast<uint64_t*>(sm + lay.bar), *freed = full + 2, *done = full + 4, *w_ready = full + 6,
-             *m_ready = full + 8, *o_done = full + 10, *bar_g = full + 12;
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(full + 13);
-    const int tcols = nm <= 16 ? 128 : (nm <= 32 ? 256 : 512);     // products of two v-heads, then the Gram matrix
-    const int halves = n > 32 ? 2 : 1, workers = 8 - 2 * halves;   // warps 0 .. workers - 1; the others make M
+    const int tcols = nm <= 16 ? 128 : (nm <= 32 ? 256 : 512);  // p and r of two v-heads, the Gram matrix, u of two v-heads
+    const int halves = n > 32 ? 2 : 1;                          // warps that make T of a v-head
     if (tid == 0) {
-        for (int i = 0; i < 13; ++i) mbar_init(full + i, i >= 6 && i < 8 ? 4 : (i >= 8 && i < 10 ? halves : 1));
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(freed + i, 1);
+            mbar_init(done + i, 1);
+            mbar_init(w_ready + i, kVtRows);
+            mbar_init(t_ready + i, halves);
+            mbar_init(u_done + i, 1);
+            mbar_init(u_ready + i, kVtRows);
+            mbar_init(o_done + i, 1);
+            mbar_init(o_read + i, kVtRows);
+        }
+        mbar_init(bar_g, 1);
         fence_mbar_init();
+        for (int i = 0; i < 5; ++i) s_bad[i] = 0ull;
     }
-    if (warp == 8) tc::alloc(tslot, tcols);
+    if (warp == kVtWorkers) tc::alloc(tslot, tcols);
     const bf* xb = static_cast<const bf*>(J.x) + first * C;
     const bf* cb = static_cast<const bf*>(J.conv_pool) + (size_t)slot * Km1 * C;
     auto channel = [&](int what, int i) {  // first channel of k (0), q (1), v of v-head j0 + i (2)
         return (what == 0 ? Hk + h : (what == 1 ? h : 2 * Hk + j0 + i)) * D;
     };
-    // the raw inputs of k and q, conv state first, into the places of M and v; those of v and z to L2
-    bf* raw = reinterpret_cast<bf*>(sm + lay.M);
+    // the raw inputs of k and q, conv state first, into the places of A, P and v; those of v and z to L2
+    bf* raw = reinterpret_cast<bf*>(sm + lay.A);
     for (int i = tid; i < (Km1 + n) * 32; i += kVtThreads) {
         const int row = i / 32, what = i / 16 % 2, c = i % 16 * 8;
         cp_async16(raw + row * 2 * D + what * D + c,
                    (row < Km1 ? cb + (size_t)row * C : xb + (size_t)(row - Km1) * C) + channel(what, 0) + c);
     }
     cp_async_commit();
-    for (int i = tid; i < n * gv * 4; i += kVtThreads) {
-        const int node = i / (4 * gv), jj = i / 4 % gv, piece = i % 4;
-        tree_prefetch(piece < 2 ? xb + (size_t)node * C + channel(2, jj) + piece * 64
+    for (int node = warp; node < n; node += kVtThreads / 32) {
+        const int jj = lane / 4, piece = lane % 4;
+        if (jj < gv) tree_prefetch(piece < 2 ? xb + (size_t)node * C + channel(2, jj) + piece * 64
                                 : static_cast<const bf*>(J.z) + ((size_t)(first + node) * Hv + j0 + jj) * D + (piece - 2) * 64);
     }
-    // gates and parents; conv weights with the taps outside (a missing tap: 0)
-    if (tid < n) {
-        const int p = J.parents[first + tid];
-        up[tid] = p >= 0 && p < tid ? p : -1;
-    }
-    for (int i = tid; i < n * gv; i += kVtThreads) {
-        const int node = i / gv, jj = i % gv;
-        const size_t at = (size_t)(first + node) * Hv + j0 + jj;
-        gates(__bfloat162float(static_cast<const bf*>(J.a)[at]), __bfloat162float(static_cast<const bf*>(J.b)[at]),
-              A.p.A_log[j0 + jj], A.p.dt_bias ? A.p.dt_bias[j0 + jj] : 0.f, false, gate[i], betas[i]);
-    }
+    // gates and parents; conv weights with the taps outside (a missing tap: 0).  What is read here is asked for before
+    // any of it is used
+    const int parent = tid < n ? J.parents[first + tid] : -1;
+    const int jj0 = tid / nm, node0 = tid - jj0 * nm;  // the thread's first (v-head, node)
+    const bool pair0 = jj0 < gv && node0 < n;
+    const size_t at0 = (size_t)(first + (pair0 ? node0 : 0)) * Hv + j0 + (pair0 ? jj0 : 0);
+    const int hv0 = j0 + (pair0 ? jj0 : 0);
+    const bf a0 = static_cast<const bf*>(J.a)[at0], b0 = static_cast<const bf*>(J.b)[at0];
+    const float alog0 = A.p.A_log[hv0], dt0 = A.p.dt_bias ? A.p.dt_bias[hv0] : 0.f;
     // weights of k, q and v-heads i0, i0 + 1 (what: from .. 3), by `nt` threads
     auto stage_weights = [&](int i0, int from, int nt) {
-#pragma unroll 2
-        for (int k = from * D + tid; k < (2 + min(2, gv - i0)) * D; k += nt) {
-            const int what = k / D;
-            const bf* src = static_cast<const bf*>(A.p.conv_w) + (size_t)(channel(min(what, 2), i0 + what - 2) + k % D) * K;
-            bf w4[4];
-            if (K == 4) {
-                *reinterpret_cast<uint2*>(w4) = __ldg(reinterpret_cast<const uint2*>(src));
-            } else {
+        constexpr int AHEAD = 2;
+        const int end = (2 + min(2, gv - i0)) * D;
+#pragma unroll 1
+        for (int k0 = from * D + tid; k0 < end; k0 += AHEAD * nt) {
+            bf w4[AHEAD][4];
 #pragma unroll
-                for (int m = 0; m < 4; ++m) w4[m] = m >= 4 - K ? src[m - (4 - K)] : __float2bfloat16_rn(0.f);
+            for (int e = 0; e < AHEAD; ++e) {
+                const int k = min(k0 + e * nt, end - 1), what = k / D;
+                const bf* src = static_cast<const bf*>(A.p.conv_w) + (size_t)(channel(min(what, 2), i0 + what - 2) + k % D) * K;
+                if (K == 4) {
+                    *reinterpret_cast<uint2*>(w4[e]) = __ldg(reinterpret_cast<const uint2*>(src));
+                } else {
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) w4[e][m] = m >= 4 - K ? src[m - (4 - K)] : __float2bfloat16_rn(0.f);
+                }
             }
 #pragma unroll
-            for (int m = 0; m < 4; ++m) ws[(what * 4 + m) * D + k % D] = w4[m];
+            for (int e = 0; e < AHEAD; ++e) {
+                const int k = k0 + e * nt;
+                if (k < end)
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) ws[(k / D * 4 + m) * D + k % D] = w4[e][m];
+            }
         }
     };
     stage_weights(0, 0, kVtThreads);
+    if (tid < nm) {
+        up[tid] = parent >= 0 && parent < tid ? parent : -1;
+        line[tid] = 0ull;
+    }
+    for (int i = tid; i < nm * gv; i += kVtThreads) {  // (one turn, but for many v-heads)
+        const int jj = i / nm, node = i - jj * nm;
+        float la = 0.f, be = 0.f;
+        if (i == tid) {
+            if (pair0) gates(__bfloat162float(a0), __bfloat162float(b0), alog0, dt0, false, la, be);
+        } else if (node < n) {
+            const size_t at = (size_t)(first + node) * Hv + j0 + jj;
+            gates(__bfloat162float(static_cast<const bf*>(J.a)[at]), __bfloat162float(static_cast<const bf*>(J.b)[at]),
+                  A.p.A_log[j0 + jj], A.p.dt_bias ? A.p.dt_bias[j0 + jj] : 0.f, false, la, be);
+        }
+        gate[i] = la * 1.4426950408889634f;
+        betas[i] = be;
+    }
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    const uint32_t tm = *tslot, tgram = tm + 4 * nm;
-    // the line of every node and the sum of log alpha along it, a thread per (node, v-head): two pairs a thread at most
-    float sums[2] = {0.f, 0.f};
+    const uint32_t tm = *tslot, tgram = tm + 4 * nm, tu = tm + 5 * nm;
+    const int atoms = 4 * gv;
+    auto load = [&](int a) {  // atom a of the CTA's v-heads (4 each)
+        mbar_arrive_expect_tx(full + (a & 1), kVtAtom);
+        tma_tile_2d(sm + lay.S + (a & 1) * kVtAtom, &ts, (a & 3) * 32, (slot * Hv + j0 + (a >> 2)) * D, full + (a & 1));
+    };
+    if (tid == 32 * kVtWorkers) {
+        load(0);
+        load(1);
+    }
+    __syncwarp();
+    // the line of every node and the sums of log2 alpha along it; the conv taps' rows: the last tap is the node, then its
+    // ancestors, then the conv state's rows, newest first
+    for (int i = tid; i < n; i += kVtThreads) {
+        unsigned long long m = 0;
+        for (int at = i; at >= 0; at = up[at]) m |= 1ull << at;
+        line[i] = m;
+    }
+    float sum[2] = {0.f, 0.f};  // (two (node, v-head) pairs to a thread at most: the launch sees to it)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        const int k = tid + e * 256, i = k % nm, jj = k / nm;
-        if (tid < 256 && i < n && jj < gv) {
-            unsigned long long m = 0;
-            for (int at = i; at >= 0;) {
-                m |= 1ull << at;
-                const int next = up[at];
-                sums[e] += gate[at * gv + jj];
-                at = next;
-            }
-            if (jj == 0) line[i] = m;
-        }
+        const int i = tid + e * kVtThreads, base = i / nm * nm;
+        if (i < nm * gv)
+            for (int at = i - base; at >= 0; at = up[at]) sum[e] += gate[base + at];
     }
-    if (tid >= 192 && tid - 192 < n) {  // the last tap is the node, then its ancestors, then the conv state's rows, newest first
-        const int i = tid - 192;
+    if (tid >= kVtThreads - 64 && tid - (kVtThreads - 64) < n) {
+        const int i = tid - (kVtThreads - 64);
         int at = i, row = Km1 - 1, t[4];
 #pragma unroll
         for (int m = 3; m >= 0; --m) {
             const bool live = 3 - m < K;
-            t[m] = !live ? i : (at >= 0 ? at : 64 + row--);
+            t[m] = !live ? Km1 + i : (at >= 0 ? Km1 + at : row--);
             if (live && at >= 0) at = up[at];
         }
         taps[i] = make_int4(t[0], t[1], t[2], t[3]);
@@ -730,11 +904,11 @@ __global__ void __launch_bounds__(kVtThreads, 2)
     cp_async_wait_all();
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {  // (read after the next barriers)
-        const int k = tid + e * 256, i = k % nm, jj = k / nm;
-        if (tid < 256 && i < n && jj < gv) {
-            gate[i * gv + jj] = sums[e];
-            eg[i * gv + jj] = __expf(sums[e]);
+    for (int e = 0; e < 2; ++e) {  // (read after the next barrier)
+        const int i = tid + e * kVtThreads;
+        if (i < nm * gv) {
+            gate[i] = sum[e];
+            eg[i] = tree_ex2(sum[e]);
         }
     }
     bool ok = true;
@@ -742,21 +916,24 @@ __global__ void __launch_bounds__(kVtThreads, 2)
         if (ok) ok = vt_wait(bar, phase);
         return ok;
     };
-    if (warp == 8) {
-        // ---- copies and products: the state of each v-head in 4 atoms through a ring of two ---------
-        const int atoms = 4 * gv;
-        auto load = [&](int a) {
-            mbar_arrive_expect_tx(full + (a & 1), kVtAtom);
-            tma_tile_2d(sm + lay.S + (a & 1) * kVtAtom, &ts, (a & 3) * 32, (slot * Hv + j0 + (a >> 2)) * D, full + (a & 1));
-        };
-        if (lane == 0) {
-            load(0);
-            load(1);
-        }
-        __syncwarp();
-        named_bar_sync(2, kVtThreads);  // [K^; Q^] is there
+    float* v = reinterpret_cast<float*>(sm + lay.v);
+    auto conv = [&](int what, int i, int batch) {  // what: k (0) and q (1) from shared memory, v of v-head j0 + i (2)
+        const int ch = channel(what, i) + 4 * lane;
+        vt_conv(what < 2 ? smem_u32(raw + what * D + 4 * lane) : 0u, reinterpret_cast<const unsigned char*>(xb + ch) - (size_t)Km1 * C * 2,
+                reinterpret_cast<const unsigned char*>(cb + ch), (uint32_t)C * 2u, taps,
+                reinterpret_cast<const uint2*>(ws + (what + (i & 1)) * 4 * D),
+                A.p.conv_b ? static_cast<const bf*>(A.p.conv_b) + ch : nullptr, K, kVtNodes * batch, n, v, Bt, 2 * nm,
+                what == 1 ? nm : 0, what == 0 ? 1.f : g.q_scale, g.l2_eps);
+    };
+    const int batches = (n + kVtNodes - 1) / kVtNodes;
+#pragma unroll 1
+    for (int k = warp; k < 2 * batches; k += kVtWorkers + 1) conv(k & 1, 0, k >> 1);
+    fence_proxy_async_smem();
+    __syncthreads();  // [K^; Q^] is there
+    if (warp == kVtWorkers) {
+        // ---- products, and the state of each v-head in 4 atoms through a ring of two ---------
         const uint64_t db = tc::sdesc(tc::smem_addr(Bt)), ds = tc::sdesc(tc::smem_addr(sm + lay.S)),
-                       dm = tc::sdesc(tc::smem_addr(sm + lay.M));
+                       dt = tc::sdesc(tc::smem_addr(sm + lay.A)), dp = tc::sdesc(tc::smem_addr(sm + lay.P));
         const uint32_t bstep = (uint32_t)(2 * nm * 128) >> 4, mstep = (uint32_t)(nm * 128) >> 4;
         const uint32_t id_n = tc::idesc_tf32(128, nm), id_2n = tc::idesc_tf32(128, 2 * nm);
         if (vt_elect()) {  // lanes are the rows of [K^; Q^] (what lies past them is never read), columns the keys
@@ -766,281 +943,320 @@ __global__ void __launch_bounds__(kVtThreads, 2)
             tc::commit(bar_g);
         }
         __syncwarp();
-        // r += w M^T of v-head i
-        auto finish = [&](int i) {
-            if (!wait(w_ready + (i & 1), i >> 1) || !wait(m_ready + (i & 1), i >> 1)) return;
-            tc::fence_after();
-            if (vt_elect()) {
-                const uint32_t d = tm + (i & 1) * 2 * nm;
-                for (int k = 0; k < (n + 7) / 8; ++k)
-                    vt_mma_ta(d + nm, d + 8 * k, dm + ((i & 1) * ((nm + 31) / 32) + (k >> 2)) * mstep + (k & 3) * 2, id_n);
-                tc::commit(o_done + (i & 1));
-            }
-            __syncwarp();
-        };
+        // whatever can go on does: a reload of the ring, an atom's product, u = w T^T or r += u P^T of a v-head
+        auto ready = [&](uint64_t* bar, int phase) { return __all_sync(0xffffffffu, mbar_test(bar, (uint32_t)(phase & 1))); };
+        int loaded = 2, a = 0, fi = 0;
+        bool u_issued = false;
+        long long since = clock64();
 #pragma unroll 1
-        for (int a = 0; a < atoms && ok; ++a) {
-            const int i = a >> 2;
-            if ((a & 3) == 0 && i >= 1) finish(i - 1);
-            if ((a & 3) == 0 && i >= 2 && ok) named_bar_sync(3, 160);  // o of v-head i - 2 has been read out of TMEM
-            if (!wait(full + (a & 1), a >> 1)) break;
-            if (vt_elect()) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    vt_mma(tm + (i & 1) * 2 * nm, ds + (uint32_t)(((a & 1) * kVtAtom) >> 4) + k * 2,
-                           db + (a & 3) * bstep + k * 2, id_2n, (a & 3) > 0 || k > 0);
-                tc::commit(freed + (a & 1));
-                if ((a & 3) == 3) tc::commit(done + (i & 1));
-            }
-            __syncwarp();
-            if (a + 2 < atoms) {
-                if (!wait(freed + (a & 1), a >> 1)) break;
-                if (lane == 0) load(a + 2);
+        while (a < atoms || fi < gv) {
+            bool moved = false;
+            if (loaded < atoms && loaded < a + 2 && ready(freed + (loaded & 1), (loaded - 2) >> 1)) {
+                if (lane == 0) load(loaded);
                 __syncwarp();
+                ++loaded;
+                moved = true;
+            }
+            if (a < loaded && ready(full + (a & 1), a >> 1) &&
+                ((a & 3) != 0 || a < 8 || ready(o_read + ((a >> 2) & 1), (a >> 3) - 1))) {  // o of v-head i - 2 has left TMEM
+                const int i = a >> 2;
+                tc::fence_after();
+                if (vt_elect()) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        vt_mma(tm + (i & 1) * 2 * nm, ds + (uint32_t)(((a & 1) * kVtAtom) >> 4) + k * 2,
+                               db + (a & 3) * bstep + k * 2, id_2n, (a & 3) > 0 || k > 0);
+                    tc::commit(freed + (a & 1));
+                    if ((a & 3) == 3) tc::commit(done + (i & 1));
+                }
+                __syncwarp();
+                ++a;
+                moved = true;
+            }
+            if (fi < gv) {
+                const int e = fi & 1, ph = fi >> 1;
+                const uint32_t d = tm + e * 2 * nm, u = tu + e * nm;
+                const uint64_t at = (uint64_t)(e * ((nm + 31) / 32)) * mstep;
+                if (!u_issued ? ready(w_ready + e, ph) && ready(t_ready + e, ph) : ready(u_ready + e, ph)) {
+                    tc::fence_after();
+                    if (vt_elect()) {
+#pragma unroll 1
+                        for (int k = 0; k < (n + 7) / 8; ++k)
+                            vt_mma_ta(u_issued ? d + nm : u, (u_issued ? u : d) + 8 * k,
+                                      (u_issued ? dp : dt) + at + (k >> 2) * mstep + (k & 3) * 2, id_n, u_issued || k > 0);
+                        tc::commit((u_issued ? o_done : u_done) + e);
+                    }
+                    __syncwarp();
+                    if (u_issued) ++fi;
+                    u_issued = !u_issued;
+                    moved = true;
+                }
+            }
+            const long long now = clock64();
+            if (moved) {
+                since = now;
+            } else {
+                if (__any_sync(0xffffffffu, now - since > kWaitLimitCycles)) {
+                    ok = false;
+                    break;
+                }
+                __nanosleep(40);
             }
         }
-        if (ok) finish(gv - 1);
         if (!ok) {  // let the copies in flight land (bounded again); the others' waits give up by themselves
-            for (int i = 0; i < 2; ++i) mbar_wait(full + i, 0);
+            for (int i = max(0, loaded - 2); i < loaded; ++i) mbar_wait(full + (i & 1), (uint32_t)((i >> 1) & 1));
             if (lane == 0) report_device_status(kDevWaitTimeout);
         }
     } else {
-        float* v = reinterpret_cast<float*>(sm + lay.v);
-        const int batches = (n + 3) / 4;  // of 4 nodes
-        auto conv = [&](int what, int i, int batch) {  // what: k (0) and q (1) from shared memory, v of v-head j0 + i (2)
-            const int ch = channel(what, i) + 4 * lane;
-            vt_conv(what < 2 ? smem_u32(raw + what * D + 4 * lane) : 0u, reinterpret_cast<const unsigned char*>(xb + ch),
-                    reinterpret_cast<const unsigned char*>(cb + ch), (uint32_t)C * 2u, taps,
-                    reinterpret_cast<const uint2*>(ws + (what + (i & 1)) * 4 * D),
-                    A.p.conv_b ? static_cast<const bf*>(A.p.conv_b) + ch : nullptr, K, 4 * batch, n, v, Bt, 2 * nm,
-                    what == 1 ? nm : 0, what == 0 ? 1.f : g.q_scale, g.l2_eps);
-        };
-        if (warp == 7) {  // entries before each node: scan of the numbers of proper ancestors, rounded up to pairs
-            int base = 0;
-            for (int i0 = 0; i0 < nm; i0 += 32) {
-                const int i = i0 + lane;
-                int c = i < n ? __popcll(line[i]) & ~1 : 0;
-#pragma unroll
-                for (int s = 1; s < 32; s <<= 1) {
-                    const int x = __shfl_up_sync(0xffffffffu, c, s);
-                    if (lane >= s) c += x;
-                }
-                if (i < nm) off[i + 1] = base + c;
-                base += __shfl_sync(0xffffffffu, c, 31);
-            }
-            if (lane == 0) off[0] = 0;
-        }
-#pragma unroll 1
-        for (int k = warp; k < 2 * batches; k += 8) conv(k & 1, 0, k >> 1);
-        fence_proxy_async_smem();
-        named_bar_sync(2, kVtThreads);
+        const int tri = ((nm + 31) / 32) * nm * 128;  // bytes of A and of P of a v-head
 #pragma unroll 1
         for (int i0 = 0; i0 < gv; i0 += 2) {  // v-heads i0 and i0 + 1
             const int two = min(2, gv - i0);
-            if (i0 > 0) {
-                named_bar_sync(1, 256);  // T and the first two v-heads' weights are no longer read
-                stage_weights(i0, 2, 256);
+            if (i0 > 0) {  // (the v-heads before are finished: see the barrier at their end)
+                stage_weights(i0, 2, 32 * kVtWorkers);
+                if (tid < 5) s_bad[tid] = 0ull;
+                named_bar_sync(1, 32 * kVtWorkers);
             }
-            if (warp < 4 && 32 * warp < 2 * nm) {  // the Gram matrix into shared memory
-                if (wait(bar_g, 0)) {
-                    tc::fence_after();
-                    const int row = 32 * warp + lane;
 #pragma unroll 1
-                    for (int c0 = 0; c0 < n; c0 += 16) {
-                        uint32_t r[16];
-                        vt_ld8(tc::taddr(tgram, 32 * warp, c0), r);
-                        vt_ld8(tc::taddr(tgram, 32 * warp, c0 + 8), r + 8);
-                        tc::ld_wait();
+            for (int k = warp; k < batches; k += kVtWorkers) conv(2, i0, k);
+            // A and P from the Gram matrix: thread = row (a node's key, or its query), 8 columns at a time by the warps
+            // of the row's quarter
+            const int q4 = warp & 3, row = 32 * q4 + lane;
+            if (32 * q4 < 2 * nm && wait(bar_g, 0)) {
+                tc::fence_after();
+                const bool is_q = row >= nm;
+                const int i = is_q ? row - nm : row;
+                const bool in = row < 2 * nm;
+                const unsigned long long mine = in ? line[i] & ~(is_q ? 0ull : 1ull << i) : 0ull;
+                const int ig = i0 * nm + (in ? i : 0);
+                const float gi[2] = {gate[ig], gate[ig + (two - 1) * nm]};
+                const float fi[2] = {is_q ? 1.f : betas[ig], is_q ? 1.f : betas[ig + (two - 1) * nm]};
+                unsigned char* to = sm + (is_q ? lay.P : lay.A);
+                float odd = 0.f;  // NaN from the first infinity or NaN on
+#pragma unroll 1
+                for (int c0 = 8 * (warp >> 2); c0 < nm; c0 += 8 * ((kVtWorkers - q4 + 3) / 4)) {
+                    uint32_t r[8];
+                    vt_ld8(tc::taddr(tgram, 32 * q4, c0), r);
+                    tc::ld_wait();
+                    const uint32_t m8 = (uint32_t)(mine >> c0) & 0xffu;
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) gram[row * (nm + 1) + c0 + c] = __uint_as_float(r[c]);
-                    }
-                }
-            }
-            named_bar_sync(1, 256);
-            // coefficients of the nodes' proper ancestors, a warp per node, a lane per ancestor
-#pragma unroll 1
-            for (int node = warp; node < n; node += 8) {
-                const unsigned long long m = line[node] & ~(1ull << node);
-                const float *gk = gram + node * (nm + 1), *gq = gram + (nm + node) * (nm + 1);
-                const int start = off[node], c = __popcll(m);
-                for (int a = lane; a < node; a += 32) {
-                    if ((m >> a) & 1ull) {
-                        const int at = start + __popcll(m & ((1ull << a) - 1ull));
-                        const float k1 = gk[a], q1 = gq[a];
-                        for (int e = 0; e < two; ++e) {
-                            const float f = __expf(gate[node * gv + i0 + e] - gate[a * gv + i0 + e]);
-                            ent[e * vt_entries(nm) + at] = make_float2(betas[node * gv + i0 + e] * f * k1, f * q1);
+                    for (int e = 0; e < 2; ++e) {
+                        if (e == two) break;
+                        float x[8], gc[8];
+                        *reinterpret_cast<float4*>(gc) = *reinterpret_cast<const float4*>(gate + (i0 + e) * nm + c0);
+                        *reinterpret_cast<float4*>(gc + 4) = *reinterpret_cast<const float4*>(gate + (i0 + e) * nm + c0 + 4);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            x[c] = (m8 >> c) & 1u ? tree_ex2(gi[e] - gc[c]) * __uint_as_float(r[c]) * fi[e] : 0.f;
+                            odd = fmaf(x[c], 0.f, odd);
+                            if (is_q) x[c] = tc::to_tf32_rn(x[c]);
                         }
-                        who[at] = (unsigned char)a;
-                    }
-                }
-                if (lane < two && (c & 1)) ent[lane * vt_entries(nm) + start + c] = make_float2(0.f, 0.f);
-                if (lane == 31) {
-                    if (c & 1) who[start + c] = (unsigned char)(__ffsll((long long)m) - 1);  // (0 times the first one's row)
-                    own[node] = gq[node];
-                }
-            }
-            named_bar_sync(1, 256);
-            if (warp >= workers) {
-                // ---- M: column 32 half + lane of v-head i0 + e; T in the Gram matrix's place -----------
-                const int e = (warp - workers) / halves, half = (warp - workers) % halves;
-                if (e < two) {
-                    float* T = gram + (e * ((nm + 31) / 32) + half) * nm * 32 + lane;
-                    unsigned char* Mt = sm + lay.M + (e * ((nm + 31) / 32) + half) * nm * 128;
-                    const float2* from = ent + e * vt_entries(nm);
-                    // the entries of all nodes lie end to end: those of the next step are loaded before this step's
-                    // rows of T (up to 4 entries past the last one are read, inside the layout, and not used)
-                    int at = 0, end = off[1];
-                    float mine = own[0];
-                    float4 k01, k23;
-                    uint32_t w;
-                    auto fetch = [&]() {
-                        k01 = *reinterpret_cast<const float4*>(from + at);
-                        k23 = *reinterpret_cast<const float4*>(from + at + 2);
-                        w = *reinterpret_cast<const uint16_t*>(who + at) | (uint32_t)*reinterpret_cast<const uint16_t*>(who + at + 2) << 16;
-                    };
-                    fetch();
-#pragma unroll 1
-                    for (int node = 0; node < n; ++node) {
-                        const int next_end = off[min(node + 2, n)];
-                        const float next_mine = own[min(node + 1, n - 1)];
-                        float su[4] = {}, so[4] = {};
-#pragma unroll 1
-                        while (at < end) {
-                            const bool four = at + 2 < end;
-                            const float t0 = T[(w & 255) * 32], t1 = T[((w >> 8) & 255) * 32];
-                            const float t2 = four ? T[((w >> 16) & 255) * 32] : 0.f, t3 = four ? T[(w >> 24) * 32] : 0.f;
-                            const float4 a = k01, c = four ? k23 : make_float4(0.f, 0.f, 0.f, 0.f);
-                            at += four ? 4 : 2;
-                            fetch();
-                            su[0] = fmaf(a.x, t0, su[0]);
-                            so[0] = fmaf(a.y, t0, so[0]);
-                            su[1] = fmaf(a.z, t1, su[1]);
-                            so[1] = fmaf(a.w, t1, so[1]);
-                            su[2] = fmaf(c.x, t2, su[2]);
-                            so[2] = fmaf(c.y, t2, so[2]);
-                            su[3] = fmaf(c.z, t3, su[3]);
-                            so[3] = fmaf(c.w, t3, so[3]);
+                        if (in) {
+                            *reinterpret_cast<float4*>(vt_at(to + e * tri, nm, i, c0)) = make_float4(x[0], x[1], x[2], x[3]);
+                            *reinterpret_cast<float4*>(vt_at(to + e * tri, nm, i, c0 + 4)) = make_float4(x[4], x[5], x[6], x[7]);
                         }
-                        const float t = (node == 32 * half + lane ? 1.f : 0.f) - ((su[0] + su[1]) + (su[2] + su[3]));
-                        T[node * 32] = t;
-                        tc::st_elem(Mt, nm, node, lane, fmaf(mine, t, (so[0] + so[1]) + (so[2] + so[3])));
-                        end = next_end;
-                        mine = next_mine;
                     }
-                    fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(m_ready + e);
                 }
-                continue;
+                if (odd != 0.f) s_bad[4] = 1ull;
             }
-            for (int i = i0; i < i0 + two; ++i) {
+            fence_proxy_async_smem();
+            tc::fence_before();
+            named_bar_sync(1, 32 * kVtWorkers);
+            const int tw = kVtWorkers - 1 - warp;
+            if (tw < two * halves) {
+                // ---- T of v-head i0 + e in A's place, columns 32 half .. ------------------------------
+                const int e = tw / halves, half = tw % halves, nb = (n + 15) / 16;
+                unsigned char* T = sm + lay.A + e * tri;
+                if (s_bad[4]) {  // 0 times an infinity or NaN is not 0: row by row, along the lines
+                    if (half == 0) vt_lines(T, nm, n, line);
+                    if (halves == 2) vt_pair_sync(e);
+                } else {
+                    vt_diag(T, nm, 2 * half, nb);
+                    if (2 * half + 1 < nb) vt_below(T, nm, 32 * half + 16, 32 * half, 16, 16, 32 * half, -1);
+                    if (halves == 2) {
+                        vt_pair_sync(e);
+                        vt_below(T, nm, 32, 0, 32, 16 * (nb - 2), 16 * half, e);
+                        vt_pair_sync(e);
+                    }
+                }
+                if (32 * half + lane < nm) {
+                    uint32_t at = smem_u32(vt_at(T, nm, 32 * half, 32 * half + lane));
 #pragma unroll 1
-                for (int k = warp; k < batches; k += workers) conv(2, i, k);
-                uint2 zr[4];  // of the nodes below, four at a time
+                    for (int r = 32 * half; r < 16 * nb; r += 8, at += 8 * 128) {  // the operand's rounding; above the diagonal are zeros
+                        float t[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) t[k] = vt_ld1((at ^ (uint32_t)(k << 4)) + k * 128);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) vt_st1((at ^ (uint32_t)(k << 4)) + k * 128, tc::to_tf32_rn(t[k]));
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(t_ready + e);
+            }
+#pragma unroll 1
+            for (int i = i0; i < i0 + two; ++i) {
+                const int e = i & 1, ph = i >> 1;
+                if (i > i0) {
+#pragma unroll 1
+                    for (int k = warp; k < batches; k += kVtWorkers) conv(2, i, k);
+                    named_bar_sync(1, 32 * kVtWorkers);
+                }
+                uint2 zr[kVtNodes];  // of the nodes below, kVtNodes at a time
                 auto load_z = [&](int from) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        zr[q] = __ldg(reinterpret_cast<const uint2*>(static_cast<const bf*>(J.z) +
-                                                                    ((size_t)(first + min(from + workers * q, n - 1)) * Hv + j0 + i) * D) + lane);
+                    for (int q = 0; q < kVtNodes; ++q)
+                        zr[q] = __ldg(reinterpret_cast<const uint2*>(
+                                          static_cast<const bf*>(J.z) +
+                                          ((size_t)(first + min(from + kVtWorkers * q, n - 1)) * Hv + j0 + i) * D) +
+                                      lane);
                 };
-                if (warp >= 4) load_z(warp);
-                named_bar_sync(4, 32 * workers);
-                if (warp < 4) {
-                    // ---- thread = state row: w and e^G r, then o in v's place (its own column) ------------
-                    float* u = v + 32 * warp + lane;
-                    const uint32_t tr = tc::taddr(tm, 32 * warp, (i & 1) * 2 * nm);
-                    unsigned long long bad = 0ull;  // nodes whose w is an infinity or NaN here
-                    wait(done + (i & 1), i >> 1);
+                if (warp >= kVtRows) load_z(warp);
+                if (warp < kVtRows) {
+                    // ---- thread = state row: w and e^G r, u rounded, then o in v's place --------------------
+                    float* u = v + 32 * q4 + lane;
+                    const int part = 8 * (warp >> 2);
+                    const uint32_t tr = tc::taddr(tm, 32 * q4, e * 2 * nm), ur = tc::taddr(tu, 32 * q4, e * nm);
+                    wait(done + e, ph);
                     tc::fence_after();
 #pragma unroll 1
-                    for (int c0 = 0; c0 < n; c0 += 8) {
+                    for (int c0 = part; c0 < n; c0 += 2 * kVtRows) {
                         uint32_t rk[8], rq[8];
                         vt_ld8(tr + c0, rk);
                         vt_ld8(tr + nm + c0, rq);
-                        float be[8], e[8], vi[8];
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const int node = min(c0 + c, n - 1);
-                            be[c] = betas[node * gv + i];
-                            e[c] = eg[node * gv + i];
-                            vi[c] = u[node * D];
-                        }
                         tc::ld_wait();
-                        float wv[8], ro[8];
+                        float be[8], f[8], w[8], wv[8], ro[8], odd = 0.f;
+#pragma unroll
+                        for (int c = 0; c < 8; c += 4) {
+                            *reinterpret_cast<float4*>(be + c) = *reinterpret_cast<const float4*>(betas + i * nm + c0 + c);
+                            *reinterpret_cast<float4*>(f + c) = *reinterpret_cast<const float4*>(eg + i * nm + c0 + c);
+                        }
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
-                            const float w = be[c] * (vi[c] - e[c] * __uint_as_float(rk[c]));
-                            ro[c] = e[c] * __uint_as_float(rq[c]);
-                            // M is 0 off the line, but 0 times an infinity or NaN is not: those are added below
-                            const bool fine = isfinite(w) && c0 + c < n;
-                            wv[c] = fine ? tc::to_tf32_rn(w) : 0.f;
-                            if (!fine && c0 + c < n) {
-                                bad |= 1ull << (c0 + c);
-                                u[(c0 + c) * D] = w;
+                            w[c] = be[c] * (u[(c0 + c) * D] - f[c] * __uint_as_float(rk[c]));
+                            ro[c] = f[c] * __uint_as_float(rq[c]);
+                            odd = fmaf(w[c], 0.f, odd);
+                            wv[c] = tc::to_tf32_rn(w[c]);
+                        }
+                        if (odd != 0.f || c0 + 8 > n) {
+                            // T and P are 0 off the line, but 0 times an infinity or NaN is not: those are added below
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                const bool fine = isfinite(w[c]);
+                                if (!fine && c0 + c < n) {
+                                    atomicOr(s_bad + e, 1ull << (c0 + c));
+                                    u[(c0 + c) * D] = w[c];
+                                }
+                                if (!fine || c0 + c >= n) wv[c] = 0.f;
                             }
                         }
+                        __syncwarp();
                         vt_st8(tr + c0, wv);
                         vt_st8(tr + nm + c0, ro);
                     }
                     tc::st_wait();
                     tc::fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(w_ready + (i & 1));
+                    if (lane == 0) mbar_arrive(w_ready + e);
                     load_z(warp);
-                    wait(o_done + (i & 1), i >> 1);
-                    tc::fence_after();
-                    const unsigned char* Mt = sm + lay.M + (i & 1) * ((nm + 31) / 32) * nm * 128;
+                    named_bar_sync(4, 32 * kVtRows);
+                    const unsigned char *Tm = sm + lay.A + e * tri, *Pm = sm + lay.P + e * tri;
+                    // columns `cols` plus the bad nodes' part, which the product left out: (T or P) times (w or u)
+                    auto add_bad = [&](uint32_t cols, const unsigned char* m, unsigned long long bad) {
 #pragma unroll 1
-                    for (int c0 = (n - 1) & ~7; c0 >= 0; c0 -= 8) {  // from the last node on: see below
-                        uint32_t ro[8];
-                        vt_ld8(tr + nm + c0, ro);
-                        tc::ld_wait();
-                        if (bad) {
-                            // a line's nodes come before its end, so their w are still there
-                            for (int node = min(c0 + 7, n - 1); node >= c0; --node) {
-                                float more = 0.f;
-                                for (unsigned long long m = bad & line[node]; m; m &= m - 1) {
-                                    const int a = __ffsll((long long)m) - 1;
-                                    more = fmaf(*reinterpret_cast<const float*>(Mt + tc::sw_off(nm, node, a)), u[a * D], more);
+                        for (int c0 = part; c0 < n; c0 += 2 * kVtRows) {
+                            uint32_t r[8];
+                            float x[8];
+                            vt_ld8(cols + c0, r);
+                            tc::ld_wait();
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                x[c] = __uint_as_float(r[c]);
+                                const int node = min(c0 + c, n - 1);
+                                for (unsigned long long left = bad & line[node]; left; left &= left - 1) {
+                                    const int a = __ffsll((long long)left) - 1;
+                                    // (finite here: it was in the product)
+                                    if (!isfinite(u[a * D])) x[c] = fmaf(*vt_at(const_cast<unsigned char*>(m), nm, node, a), u[a * D], x[c]);
                                 }
-                                float o = 0.f;
-#pragma unroll
-                                for (int c = 0; c < 8; ++c)
-                                    if (c0 + c == node) o = __uint_as_float(ro[c]);
-                                u[node * D] = o + more;
                             }
-                        } else {
+                            __syncwarp();
+                            vt_st8(cols + c0, x);
+                        }
+                        tc::st_wait();
+                        named_bar_sync(4, 32 * kVtRows);
+                    };
+                    wait(u_done + e, ph);
+                    tc::fence_after();
+                    if (s_bad[e]) add_bad(ur, Tm, s_bad[e]);  // (the same for all of these warps)
+#pragma unroll 1
+                    for (int c0 = 2 * part; c0 < n; c0 += 4 * kVtRows) {
+                        uint32_t r[16];
+                        float x[16], odd = 0.f;
+                        vt_ld8(ur + c0, r);
+                        vt_ld8(ur + c0 + 8, r + 8);
+                        tc::ld_wait();
 #pragma unroll
-                            for (int c = 0; c < 8; ++c)
-                                if (c0 + c < n) u[(c0 + c) * D] = __uint_as_float(ro[c]);
+                        for (int c = 0; c < 16; ++c) {
+                            odd = fmaf(__uint_as_float(r[c]), 0.f, odd);
+                            x[c] = tc::to_tf32_rn(__uint_as_float(r[c]));
+                        }
+                        if (odd != 0.f) {
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) {
+                                if (isfinite(__uint_as_float(r[c]))) continue;
+                                x[c] = 0.f;
+                                if (c0 + c >= n) continue;
+                                atomicOr(s_bad + 2 + e, 1ull << (c0 + c));
+                                u[(c0 + c) * D] = __uint_as_float(r[c]);
+                            }
                         }
                         __syncwarp();
+                        vt_st8(ur + c0, x);
+                        vt_st8(ur + c0 + 8, x + 8);
+                    }
+                    tc::st_wait();
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(u_ready + e);
+                    named_bar_sync(4, 32 * kVtRows);
+                    wait(o_done + e, ph);
+                    tc::fence_after();
+                    if (s_bad[2 + e]) add_bad(tr + nm, Pm, s_bad[2 + e]);
+#pragma unroll 1
+                    for (int c0 = 2 * part; c0 < n; c0 += 4 * kVtRows) {
+                        uint32_t ro[16];
+                        vt_ld8(tr + nm + c0, ro);
+                        vt_ld8(tr + nm + c0 + 8, ro + 8);
+                        tc::ld_wait();
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) u[(c0 + c) * D] = __uint_as_float(ro[c]);  // (nm rows of room)
                     }
                     tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(o_read + e);  // this v-head's columns are free
                 }
-                named_bar_sync(4, 32 * workers);
-                if (warp < 4 && i + 2 < gv) asm volatile("bar.arrive 3, 160;" ::: "memory");  // this v-head's columns are free
-                // gated RMSNorm, a warp per node, four nodes at once, four channels to a lane
+                named_bar_sync(1, 32 * kVtWorkers);
+                                // gated RMSNorm, a warp per node, kVtNodes at once, four channels to a lane
                 const uint2 nw = __ldg(reinterpret_cast<const uint2*>(A.p.norm_w) + lane);
                 const float2 w01 = vt_two(nw.x), w23 = vt_two(nw.y);
 #pragma unroll 1
-                for (int n0 = warp; n0 < n; n0 += 4 * workers) {
+                for (int n0 = warp; n0 < n; n0 += kVtNodes * kVtWorkers) {
                     if (n0 > warp) load_z(n0);
-                    float4 o[4];
-                    float ss[4];
+                    float4 o[kVtNodes];
+                    float ss[kVtNodes];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        o[q] = *reinterpret_cast<const float4*>(v + min(n0 + workers * q, n - 1) * D + 4 * lane);
+                    for (int q = 0; q < kVtNodes; ++q) {
+                        o[q] = *reinterpret_cast<const float4*>(v + min(n0 + kVtWorkers * q, n - 1) * D + 4 * lane);
                         ss[q] = fmaf(o[q].x, o[q].x, fmaf(o[q].y, o[q].y, fmaf(o[q].z, o[q].z, o[q].w * o[q].w)));
                     }
 #pragma unroll
                     for (int off = 16; off > 0; off >>= 1)
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) ss[q] += __shfl_xor_sync(0xffffffffu, ss[q], off);
+                        for (int q = 0; q < kVtNodes; ++q) ss[q] += __shfl_xor_sync(0xffffffffu, ss[q], off);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int node = n0 + workers * q;
+                    for (int q = 0; q < kVtNodes; ++q) {
+                        const int node = n0 + kVtWorkers * q;
                         const float inv = rsqrtf(fmaf(ss[q], 1.f / D, g.norm_eps));
                         const float2 z01 = vt_two(zr[q].x), z23 = vt_two(zr[q].y);
                         const __nv_bfloat162 y01 = __floats2bfloat162_rn(o[q].x * inv * w01.x * tree_silu(z01.x),
@@ -1054,13 +1270,13 @@ __global__ void __launch_bounds__(kVtThreads, 2)
                             *(reinterpret_cast<uint2*>(static_cast<bf*>(J.y) + ((size_t)(first + node) * Hv + j0 + i) * D) + lane) = out;
                     }
                 }
-                if (i + 1 < gv) named_bar_sync(4, 32 * workers);  // o is read: its place takes the next v
+                if (i + 1 < gv) named_bar_sync(1, 32 * kVtWorkers);  // o is read: its place takes the next v
             }
         }
     }
     tc::fence_before();
     __syncthreads();
-    if (warp == 8) tc::dealloc(tm, tcols);
+    if (warp == kVtWorkers) tc::dealloc(tm, tcols);
 }
 
 template <int D, typename TA>
@@ -1103,7 +1319,7 @@ cudaError_t launch_verify_tc(const Geom& g, const LayerParams& p, const TreeJob&
     VtArgs A{g, p, job, (job.max_nodes + 15) / 16 * 16, g.G};
     // few trees: a CTA per v-head; and as many v-heads as shared memory holds the decays of
     if ((long)job.B * g.Hk < sm_count()) A.gv = 1;
-    while (vt_smem(A.nm, A.gv).total + 1024 > 227 * 1024 || A.g.G % A.gv) --A.gv;
+    while (vt_smem(A.nm, A.gv).total + 1024 > 227 * 1024 || A.nm * A.gv > 2 * kVtThreads || A.gv > 8 || A.g.G % A.gv) --A.gv;
     return launch_pdl(k_tree_verify_tc, dim3((unsigned)(g.Hv / A.gv), (unsigned)job.B), dim3(kVtThreads),
                       (size_t)vt_smem(A.nm, A.gv).total + 1024, st, map, A);
 }
