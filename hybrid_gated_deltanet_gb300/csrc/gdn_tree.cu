@@ -431,7 +431,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2) k_tree_verify(const __grid_co
 // state's place in shared memory is half a tile for that).
 constexpr int kVtWorkers = 7;    // and a warp that drives the copies and the products
 constexpr int kVtThreads = 32 * (kVtWorkers + 1);
-constexpr int kVtNodes = 5;      // nodes that a warp takes at a time in the conv and the norm
+constexpr int kVtNorm = 2;
+constexpr int kVtNodes = 3;      // nodes that a warp takes at a time in the conv and the norm
 constexpr int kVtRows = 4;       // warps 0 .. 3 have the state rows: TMEM lanes by quarter
 constexpr int kVtAtom = 16384;   // 128 state rows x 32 columns
 
@@ -1103,10 +1104,10 @@ __global__ void __launch_bounds__(kVtThreads, 2)
                     for (int k = warp; k < batches; k += kVtWorkers) conv(2, i, k);
                     named_bar_sync(1, 32 * kVtWorkers);
                 }
-                uint2 zr[kVtNodes];  // of the nodes below, kVtNodes at a time
+                uint2 zr[kVtNorm];  // of the nodes below, kVtNorm at a time
                 auto load_z = [&](int from) {
 #pragma unroll
-                    for (int q = 0; q < kVtNodes; ++q)
+                    for (int q = 0; q < kVtNorm; ++q)
                         zr[q] = __ldg(reinterpret_cast<const uint2*>(
                                           static_cast<const bf*>(J.z) +
                                           ((size_t)(first + min(from + kVtWorkers * q, n - 1)) * Hv + j0 + i) * D) +
@@ -1237,25 +1238,25 @@ __global__ void __launch_bounds__(kVtThreads, 2)
                     if (lane == 0) mbar_arrive(o_read + e);  // this v-head's columns are free
                 }
                 named_bar_sync(1, 32 * kVtWorkers);
-                                // gated RMSNorm, a warp per node, kVtNodes at once, four channels to a lane
+                                // gated RMSNorm, a warp per node, kVtNorm at once, four channels to a lane
                 const uint2 nw = __ldg(reinterpret_cast<const uint2*>(A.p.norm_w) + lane);
                 const float2 w01 = vt_two(nw.x), w23 = vt_two(nw.y);
 #pragma unroll 1
-                for (int n0 = warp; n0 < n; n0 += kVtNodes * kVtWorkers) {
+                for (int n0 = warp; n0 < n; n0 += kVtNorm * kVtWorkers) {
                     if (n0 > warp) load_z(n0);
-                    float4 o[kVtNodes];
-                    float ss[kVtNodes];
+                    float4 o[kVtNorm];
+                    float ss[kVtNorm];
 #pragma unroll
-                    for (int q = 0; q < kVtNodes; ++q) {
+                    for (int q = 0; q < kVtNorm; ++q) {
                         o[q] = *reinterpret_cast<const float4*>(v + min(n0 + kVtWorkers * q, n - 1) * D + 4 * lane);
                         ss[q] = fmaf(o[q].x, o[q].x, fmaf(o[q].y, o[q].y, fmaf(o[q].z, o[q].z, o[q].w * o[q].w)));
                     }
 #pragma unroll
                     for (int off = 16; off > 0; off >>= 1)
 #pragma unroll
-                        for (int q = 0; q < kVtNodes; ++q) ss[q] += __shfl_xor_sync(0xffffffffu, ss[q], off);
+                        for (int q = 0; q < kVtNorm; ++q) ss[q] += __shfl_xor_sync(0xffffffffu, ss[q], off);
 #pragma unroll
-                    for (int q = 0; q < kVtNodes; ++q) {
+                    for (int q = 0; q < kVtNorm; ++q) {
                         const int node = n0 + kVtWorkers * q;
                         const float inv = rsqrtf(fmaf(ss[q], 1.f / D, g.norm_eps));
                         const float2 z01 = vt_two(zr[q].x), z23 = vt_two(zr[q].y);
