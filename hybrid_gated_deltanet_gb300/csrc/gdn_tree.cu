@@ -1362,25 +1362,21 @@ __global__ void __launch_bounds__(kTreeThreads, 2) k_tree_commit(const __grid_co
     __shared__ int n_s;
     griddep_wait();
     griddep_launch_dependents();
-    const int slot = J.slot_idx[b];
+    const int far = min(b + A.ahead, J.B - 1);  // (what both sequences need is asked for at once)
+    const int slot = J.slot_idx[b], slot_far = J.slot_idx[far];
     const int64_t first = J.cu_rows[b], count = (int64_t)J.cu_rows[b + 1] - first;
-    for (int far = b < A.ahead ? 0 : A.ahead; far <= A.ahead; far += A.ahead) {  // (the first wave asks for its own too)
-        if (b + far >= J.B) break;
-        const int s2 = J.slot_idx[b + far];
-        if (s2 >= 0 && s2 < J.n_slots && J.cu_rows[b + far + 1] > J.cu_rows[b + far]) {
-            const float* p = J.state_pool + ((size_t)s2 * Hv + j) * D * D;
+    const bool far_too = b + A.ahead < J.B && J.cu_rows[far + 1] > J.cu_rows[far] && slot_far >= 0 && slot_far < J.n_slots;
+    auto ask = [&]() {
+        const float* p = J.state_pool + ((size_t)slot_far * Hv + j) * D * D;
+        if (far_too)
             for (int i = tid; i < D * D / 32; i += kTreeThreads) tree_prefetch(p + i * 32);
-        }
-    }
-    if (slot < 0 || slot >= J.n_slots || first < 0 || count < 1 || count > J.max_rows || first + count > J.n_rows)
+    };
+    if (slot < 0 || slot >= J.n_slots || first < 0 || count < 1 || count > J.max_rows || first + count > J.n_rows) {
+        ask();
         return;  // the whole cluster shares b
+    }
     const int l8 = lane & 7, grp = lane >> 3, row0 = warp * (D / 8) + grp;  // state row r * 4 + group, columns 4 l8 + 32 c
     float* Sg = J.state_pool + (((size_t)slot * Hv + j) * D + row0) * D + 4 * l8;
-    float4 S[RL][RL];
-#pragma unroll
-    for (int r = 0; r < RL; ++r)
-#pragma unroll
-        for (int c = 0; c < RL; ++c) S[r][c] = *reinterpret_cast<const float4*>(Sg + (size_t)r * 4 * D + 32 * c);
     // the rows of the path that exist, in order (64 at most: two per lane of a warp)
     if (warp == 0) {
         int src[2];
@@ -1416,28 +1412,36 @@ __global__ void __launch_bounds__(kTreeThreads, 2) k_tree_commit(const __grid_co
     if (n == 0) return;  // no row that exists (the whole cluster)
     const TA* x = static_cast<const TA*>(J.x);
     TA* cp = static_cast<TA*>(J.conv_pool) + (size_t)slot * Km1 * C;
+    // the raw inputs of the rows t0 .., all on their way at once (through shared memory: the state has the registers):
+    // input p of the sequence is row p of the conv state, then the path's rows
+    auto stage = [&](int t0) {
+        constexpr int PER = D * (int)sizeof(TA) / 16;  // 16-byte pieces of a row's head
+        const int m = min(kComRows, n - t0);
+        for (int i = tid; i < (m + Km1) * 3 * PER; i += kTreeThreads) {
+            const int row = i / (3 * PER), kind = i / PER % 3, c = i % PER * (16 / (int)sizeof(TA)), p = t0 + row;
+            cp_async16(&hs[row][kind][c], (p < Km1 ? cp + (size_t)p * C : x + (size_t)rows[p - Km1] * C) + channel(kind) + c);
+        }
+        cp_async_commit();
+    };
+    stage(0);
+    {
+        const bool direct = g.flags & kFlagGatesDirect;
+        for (int t = tid - (kTreeThreads - 64); t >= 0 && t < n; t += 64) {
+            float gl, beta;
+            gates(L::ld(J.a, (size_t)rows[t] * Hv + j), L::ld(J.b, (size_t)rows[t] * Hv + j), direct ? 0.f : A.p.A_log[j],
+                  !direct && A.p.dt_bias ? A.p.dt_bias[j] : 0.f, direct, gl, beta);
+            alpha_s[t] = expf(gl);
+            beta_s[t] = beta;
+        }
+    }
+    float4 S[RL][RL];  // (asked for after the short loads, which would stand in line behind it)
+#pragma unroll
+    for (int r = 0; r < RL; ++r)
+#pragma unroll
+        for (int c = 0; c < RL; ++c) S[r][c] = *reinterpret_cast<const float4*>(Sg + (size_t)r * 4 * D + 32 * c);
+    ask();
     for (int t0 = 0; t0 < n; t0 += kComRows) {
         const int m = min(kComRows, n - t0);
-        // the chunk's raw inputs, all on their way at once (through shared memory: the state has the registers): input p
-        // of the sequence is row p of the conv state, then the path's rows
-        {
-            constexpr int PER = D * (int)sizeof(TA) / 16;  // 16-byte pieces of a row's head
-            for (int i = tid; i < (m + Km1) * 3 * PER; i += kTreeThreads) {
-                const int row = i / (3 * PER), kind = i / PER % 3, c = i % PER * (16 / (int)sizeof(TA)), p = t0 + row;
-                cp_async16(&hs[row][kind][c], (p < Km1 ? cp + (size_t)p * C : x + (size_t)rows[p - Km1] * C) + channel(kind) + c);
-            }
-            cp_async_commit();
-        }
-        if (t0 == 0) {
-            const bool direct = g.flags & kFlagGatesDirect;
-            for (int t = tid - (kTreeThreads - 64); t >= 0 && t < n; t += 64) {
-                float gl, beta;
-                gates(L::ld(J.a, (size_t)rows[t] * Hv + j), L::ld(J.b, (size_t)rows[t] * Hv + j), direct ? 0.f : A.p.A_log[j],
-                      !direct && A.p.dt_bias ? A.p.dt_bias[j] : 0.f, direct, gl, beta);
-                alpha_s[t] = expf(gl);
-                beta_s[t] = beta;
-            }
-        }
         cp_async_wait_all();
         __syncthreads();
         // the conv state is read (rows past the first K - 1 do not reach it): the cluster's other CTAs may replace it
@@ -1506,7 +1510,10 @@ __global__ void __launch_bounds__(kTreeThreads, 2) k_tree_commit(const __grid_co
                 }
             }
         }
-        if (t0 + kComRows < n) __syncthreads();  // ks, vs and the inputs are read
+        if (t0 + kComRows < n) {
+            __syncthreads();  // ks, vs and the inputs are read
+            stage(t0 + kComRows);
+        }
     }
     // the new conv state: the last K - 1 raw inputs, bit for bit, from shared memory
 #pragma unroll
