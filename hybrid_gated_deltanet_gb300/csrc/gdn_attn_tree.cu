@@ -30,7 +30,7 @@ namespace gdn {
 namespace {
 
 constexpr int kTreeCtas = 152;    // one CTA per SM
-constexpr int kTreeMinTiles = 4;  // fewest key tiles of a worker's run
+constexpr int kTreeMinTiles = 2;  // fewest key tiles of a worker's run
 constexpr int kTreeWhole = 8;     // lists of up to this many tiles are not cut while every list has an SM
 
 struct AttnTreeArgs {

@@ -1329,9 +1329,10 @@ cudaError_t launch_verify_tc(const Geom& g, const LayerParams& p, const TreeJob&
 // One CTA per (v-head, sequence), a cluster per k-head.  A warp holds D / 8 state rows in registers
 // through all rows of the path (a state row's update touches no other row), 8 lanes to a row as in
 // k_tree_verify, so the state is read once and written once, and shared memory holds only
-// the inputs, k and v of a chunk of path rows at a time.  HBM-bound: while a CTA prepares k and v, its state is on the
-// way to L2, asked for by the CTA that ran a wave before it.  The G CTAs of a k-head read the same conv rows of k,
-// which one of them replaces: the cluster barrier stands between.
+// the inputs, k and v of a chunk of path rows at a time.  HBM-bound, with two CTAs an SM in flight: the short loads of the
+// inputs are asked for before the state, which would stand in their way, and k and v are made while it comes (92 us with
+// a prefetch to L2 of the state of a CTA a wave later, 89 without: 64 sequences of up to 6 rows, 48 v-heads of 128 x 128).
+// The G CTAs of a k-head read the same conv rows of k, which one of them replaces: the cluster barrier stands between.
 template <typename TA>
 constexpr int kComChunk = sizeof(TA) == 2 ? 16 : 8;
 
@@ -1339,7 +1340,6 @@ struct CommitArgs {
     Geom g;
     LayerParams p;
     TreeCommitJob job;
-    int ahead;  // sequences between a CTA and the one whose state it asks for
 };
 
 template <int D, typename TA>
@@ -1362,19 +1362,10 @@ __global__ void __launch_bounds__(kTreeThreads, 2) k_tree_commit(const __grid_co
     __shared__ int n_s;
     griddep_wait();
     griddep_launch_dependents();
-    const int far = min(b + A.ahead, J.B - 1);  // (what both sequences need is asked for at once)
-    const int slot = J.slot_idx[b], slot_far = J.slot_idx[far];
+    const int slot = J.slot_idx[b];
     const int64_t first = J.cu_rows[b], count = (int64_t)J.cu_rows[b + 1] - first;
-    const bool far_too = b + A.ahead < J.B && J.cu_rows[far + 1] > J.cu_rows[far] && slot_far >= 0 && slot_far < J.n_slots;
-    auto ask = [&]() {
-        const float* p = J.state_pool + ((size_t)slot_far * Hv + j) * D * D;
-        if (far_too)
-            for (int i = tid; i < D * D / 32; i += kTreeThreads) tree_prefetch(p + i * 32);
-    };
-    if (slot < 0 || slot >= J.n_slots || first < 0 || count < 1 || count > J.max_rows || first + count > J.n_rows) {
-        ask();
+    if (slot < 0 || slot >= J.n_slots || first < 0 || count < 1 || count > J.max_rows || first + count > J.n_rows)
         return;  // the whole cluster shares b
-    }
     const int l8 = lane & 7, grp = lane >> 3, row0 = warp * (D / 8) + grp;  // state row r * 4 + group, columns 4 l8 + 32 c
     float* Sg = J.state_pool + (((size_t)slot * Hv + j) * D + row0) * D + 4 * l8;
     // the rows of the path that exist, in order (64 at most: two per lane of a warp)
@@ -1439,7 +1430,6 @@ __global__ void __launch_bounds__(kTreeThreads, 2) k_tree_commit(const __grid_co
     for (int r = 0; r < RL; ++r)
 #pragma unroll
         for (int c = 0; c < RL; ++c) S[r][c] = *reinterpret_cast<const float4*>(Sg + (size_t)r * 4 * D + 32 * c);
-    ask();
     for (int t0 = 0; t0 < n; t0 += kComRows) {
         const int m = min(kComRows, n - t0);
         cp_async_wait_all();
@@ -1576,7 +1566,7 @@ cudaError_t launch_tree_verify(const Geom& g, const LayerParams& p, const TreeJo
 
 cudaError_t launch_tree_commit(const Geom& g, const LayerParams& p, const TreeCommitJob& job, cudaStream_t st) {
     if (job.B == 0 || job.n_rows == 0) return cudaSuccess;
-    const CommitArgs A{g, p, job, std::max(1, 2 * sm_count() / g.Hv)};
+    const CommitArgs A{g, p, job};
     GDN_BY_TYPE(launch_commit_t);
 }
 
