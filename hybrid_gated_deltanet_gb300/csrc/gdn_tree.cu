@@ -119,7 +119,8 @@ __host__ __device__ inline TreeSmem tree_smem(int D, int n) {
 // One CTA per (v-head, tree), fp32 on the CUDA cores throughout: fp32 activations, d < 128 and the flags.  A
 // warp has d / 8 state rows in registers, 8 lanes to a row, and takes the nodes' k and q one after another; the sums
 // of its dot products are reduced together (7 shuffles for 8 of them).  Bound by instructions: 4 d^2 multiply-adds per
-// node against 4 d^2 bytes of state per tree, and as much again for the shuffles, the conv and the line sums.
+// node against 4 d^2 bytes of state per tree, and as much again for the shuffles, the conv and the line sums (8 chains of
+// 20 nodes, 48 v-heads, d = 128, fp32: 32 us, 14 us per CTA in one wave and a quarter).
 template <int D, typename TA>
 __global__ void __launch_bounds__(kTreeThreads, 2) k_tree_verify(const __grid_constant__ TreeArgs A) {
     using L = Act<TA>;
@@ -426,13 +427,16 @@ __global__ void __launch_bounds__(kTreeThreads, 2) k_tree_verify(const __grid_co
 //   r += u P^T      u in TMEM, rounded by way of registers.
 // T is made in place of A, in fp32, by a warp (two above 32 nodes) per v-head: blocks of 16 on the diagonal by
 // substitution, a column to a lane; then T21 = -T22 A21 T11 for the blocks of 16 and of 32 below it.  TF32's 2^-11 per
-// operand is a quarter of the bf16 rounding of y; the decays, T's sums and the norms are fp32.  The phases are short
-// and bound by latency and instructions: many warps share each of them, and two CTAs share an SM up to 32 nodes (the
-// state's place in shared memory is half a tile for that).
+// operand is a quarter of the bf16 rounding of y; the decays, T's sums and the norms are fp32.
+// The phases are short, so that latency and instructions bound the kernel (64 trees of up to 32 nodes, 16 / 32 heads:
+// 76 us, 2.2 TB/s of the state's bytes; HBM is a third busy, the issue slots 40%).  Two CTAs share an SM up to 32 nodes:
+// the state's place in shared memory is half a tile for that.  Measured there: 16 warps a CTA 87 us, 12 warps 84, 8 warps
+// 76 (what a warp does once weighs more than its waiting); three CTAs an SM, with one v-head at a time and a quarter
+// tile, 74 us, but 83 against 78 at 16 trees of 64 nodes and 48 v-heads.
 constexpr int kVtWorkers = 7;    // and a warp that drives the copies and the products
 constexpr int kVtThreads = 32 * (kVtWorkers + 1);
-constexpr int kVtNorm = 2;
-constexpr int kVtNodes = 3;      // nodes that a warp takes at a time in the conv and the norm
+constexpr int kVtNodes = 3;      // nodes that a warp takes at a time in the conv,
+constexpr int kVtNorm = 2;       // and in the norm
 constexpr int kVtRows = 4;       // warps 0 .. 3 have the state rows: TMEM lanes by quarter
 constexpr int kVtAtom = 16384;   // 128 state rows x 32 columns
 
@@ -1318,7 +1322,9 @@ cudaError_t launch_verify_tc(const Geom& g, const LayerParams& p, const TreeJob&
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
     VtArgs A{g, p, job, (job.max_nodes + 15) / 16 * 16, g.G};
-    // few trees: a CTA per v-head; and as many v-heads as shared memory holds the decays of
+    // Few trees: a CTA per v-head (us, 16 / 32 heads: one tree of 8 nodes 8.6 against 11.3, 8 of 16 nodes 12.0 against
+    // 14.1).  From a CTA per SM on: all v-heads of a k-head, which share its conv and Gram matrix (16 of 16 nodes 18.2
+    // against 21.8, 64 of 32 nodes 76 against 98), or as many as shared memory and two (node, v-head) pairs a thread allow
     if ((long)job.B * g.Hk < sm_count()) A.gv = 1;
     while (vt_smem(A.nm, A.gv).total + 1024 > 227 * 1024 || A.nm * A.gv > 2 * kVtThreads || A.gv > 8 || A.g.G % A.gv) --A.gv;
     return launch_pdl(k_tree_verify_tc, dim3((unsigned)(g.Hv / A.gv), (unsigned)job.B), dim3(kVtThreads),
@@ -1331,7 +1337,8 @@ cudaError_t launch_verify_tc(const Geom& g, const LayerParams& p, const TreeJob&
 // k_tree_verify, so the state is read once and written once, and shared memory holds only
 // the inputs, k and v of a chunk of path rows at a time.  HBM-bound, with two CTAs an SM in flight: the short loads of the
 // inputs are asked for before the state, which would stand in their way, and k and v are made while it comes (92 us with
-// a prefetch to L2 of the state of a CTA a wave later, 89 without: 64 sequences of up to 6 rows, 48 v-heads of 128 x 128).
+// a prefetch to L2 of the state of a CTA a wave later, 89 without, 4.6 TB/s: 64 sequences of up to 6 rows, 48 v-heads of
+// 128 x 128; 96 with the state asked for first).
 // The G CTAs of a k-head read the same conv rows of k, which one of them replaces: the cluster barrier stands between.
 template <typename TA>
 constexpr int kComChunk = sizeof(TA) == 2 ? 16 : 8;
@@ -1557,9 +1564,9 @@ cudaError_t launch_commit_t(const CommitArgs& A, cudaStream_t st) {
 
 cudaError_t launch_tree_verify(const Geom& g, const LayerParams& p, const TreeJob& job, cudaStream_t st) {
     if (job.B == 0 || job.n_nodes == 0) return cudaSuccess;
-    if (g.D == 128 && g.act_bf16 && g.flags == 0) {
-        return launch_verify_tc(g, p, job, st);
-    }
+    // (where the tensor cores' kernel serves it is the faster one: 64 trees of up to 32 nodes 76 us against 152 on the CUDA
+    // cores, one tree of 8 nodes 8.6 against 8.9)
+    if (g.D == 128 && g.act_bf16 && g.flags == 0) return launch_verify_tc(g, p, job, st);
     const TreeArgs A{g, p, job, job.max_nodes};
     GDN_BY_TYPE(launch_verify_t);
 }
