@@ -1335,10 +1335,10 @@ cudaError_t launch_verify_tc(const Geom& g, const LayerParams& p, const TreeJob&
 // One CTA per (v-head, sequence), a cluster per k-head.  A warp holds D / 8 state rows in registers
 // through all rows of the path (a state row's update touches no other row), 8 lanes to a row as in
 // k_tree_verify, so the state is read once and written once, and shared memory holds only
-// the inputs, k and v of a chunk of path rows at a time.  HBM-bound, with two CTAs an SM in flight: the short loads of the
-// inputs are asked for before the state, which would stand in their way, and k and v are made while it comes (92 us with
-// a prefetch to L2 of the state of a CTA a wave later, 89 without, 4.6 TB/s: 64 sequences of up to 6 rows, 48 v-heads of
-// 128 x 128; 96 with the state asked for first).
+// the inputs, k and v of a chunk of path rows at a time.  HBM-bound, two CTAs an SM.  The state is asked for last: the
+// short dependent loads of the inputs stand in line behind it otherwise, and the SM's other CTA keeps HBM busy meanwhile
+// (64 sequences of up to 6 rows, 48 v-heads of 128 x 128: 86 us, 4.8 TB/s; 89 with the state asked for before k and v are
+// made, 96 before the inputs, 98 by a bulk copy at the start, 92 with a prefetch to L2 a wave ahead).
 // The G CTAs of a k-head read the same conv rows of k, which one of them replaces: the cluster barrier stands between.
 template <typename TA>
 constexpr int kComChunk = sizeof(TA) == 2 ? 16 : 8;
@@ -1432,11 +1432,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) k_tree_commit(const __grid_co
             beta_s[t] = beta;
         }
     }
-    float4 S[RL][RL];  // (asked for after the short loads, which would stand in line behind it)
-#pragma unroll
-    for (int r = 0; r < RL; ++r)
-#pragma unroll
-        for (int c = 0; c < RL; ++c) S[r][c] = *reinterpret_cast<const float4*>(Sg + (size_t)r * 4 * D + 32 * c);
+    float4 S[RL][RL];
     for (int t0 = 0; t0 < n; t0 += kComRows) {
         const int m = min(kComRows, n - t0);
         cp_async_wait_all();
@@ -1474,6 +1470,12 @@ __global__ void __launch_bounds__(kTreeThreads, 2) k_tree_commit(const __grid_co
                 }
                 if (i0 < m) *reinterpret_cast<float4*>(&(kind == 0 ? ks : vs)[i0][c4]) = y;
             }
+        }
+        if (t0 == 0) {
+#pragma unroll
+    for (int r = 0; r < RL; ++r)
+#pragma unroll
+        for (int c = 0; c < RL; ++c) S[r][c] = *reinterpret_cast<const float4*>(Sg + (size_t)r * 4 * D + 32 * c);
         }
         __syncthreads();
 #pragma unroll 1
