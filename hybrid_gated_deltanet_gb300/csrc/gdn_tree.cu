@@ -435,8 +435,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) k_tree_verify(const __grid_co
 // tile, 74 us, but 83 against 78 at 16 trees of 64 nodes and 48 v-heads.
 constexpr int kVtWorkers = 7;    // and a warp that drives the copies and the products
 constexpr int kVtThreads = 32 * (kVtWorkers + 1);
-constexpr int kVtNodes = 3;      // nodes that a warp takes at a time in the conv,
-constexpr int kVtNorm = 2;       // and in the norm
+constexpr int kVtNorm = 2;       // nodes that a warp takes at a time in the norm
 constexpr int kVtRows = 4;       // warps 0 .. 3 have the state rows: TMEM lanes by quarter
 constexpr int kVtAtom = 16384;   // 128 state rows x 32 columns
 
@@ -535,19 +534,20 @@ __device__ __forceinline__ float2 vt_two(uint32_t u) {
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
 
-// conv + SiLU of the warp's 128 channels (4 to a lane) at kVtNodes nodes from i0 on, all loads at once.  `raw` != 0: k or q,
+// conv + SiLU of the warp's 128 channels (4 to a lane) at NODES nodes from i0 on, all loads at once.  `raw` != 0: k or q,
 // its inputs in shared memory from there on (conv state first, 512 bytes to a row), L2-normalised times scale, to row
 // row0 + node of [K^; Q^].  Else v, inputs in global memory (x: from K - 1 rows
 // before the first node's), to v[node][4 lane].  One copy of this code serves every
 // call: the phases run once per CTA, and copies in line were bound by instruction fetch.
+template <int NODES>
 __device__ __noinline__ void vt_conv(uint32_t raw, const unsigned char* x, const unsigned char* state, uint32_t row_bytes,
                                      const int4* taps, const uint2* w, const __nv_bfloat16* bias, int K, int i0, int n,
                                      float* v, unsigned char* Bt, int rows, int row0, float scale, float eps) {
     const int lane = threadIdx.x & 31;
-    uint2 u[kVtNodes][4];
+    uint2 u[NODES][4];
     if (raw) {
 #pragma unroll
-        for (int e = 0; e < kVtNodes; ++e) {
+        for (int e = 0; e < NODES; ++e) {
             const int4 t4 = taps[min(i0 + e, n - 1)];
             const int tap[4] = {t4.x, t4.y, t4.z, t4.w};
 #pragma unroll
@@ -558,7 +558,7 @@ __device__ __noinline__ void vt_conv(uint32_t raw, const unsigned char* x, const
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < kVtNodes; ++e) {
+        for (int e = 0; e < NODES; ++e) {
             const int4 t4 = taps[min(i0 + e, n - 1)];
             const int tap[4] = {t4.x, t4.y, t4.z, t4.w};
 #pragma unroll
@@ -566,9 +566,9 @@ __device__ __noinline__ void vt_conv(uint32_t raw, const unsigned char* x, const
                 u[e][m] = __ldg(reinterpret_cast<const uint2*>((tap[m] < K - 1 ? state : x) + (uint64_t)(uint32_t)tap[m] * row_bytes));
         }
     }
-    float2 y[kVtNodes][2];
+    float2 y[NODES][2];
 #pragma unroll
-    for (int e = 0; e < kVtNodes; ++e)
+    for (int e = 0; e < NODES; ++e)
 #pragma unroll
         for (int c = 0; c < 2; ++c)
             y[e][c] = bias ? vt_two(reinterpret_cast<const uint32_t*>(bias)[c]) : make_float2(0.f, 0.f);
@@ -578,14 +578,14 @@ __device__ __noinline__ void vt_conv(uint32_t raw, const unsigned char* x, const
         const uint2 wm = w[m * 32 + lane];
         const float2 w01 = vt_two(wm.x), w23 = vt_two(wm.y);
 #pragma unroll
-        for (int e = 0; e < kVtNodes; ++e) {
+        for (int e = 0; e < NODES; ++e) {
             y[e][0] = __ffma2_rn(w01, vt_two(u[e][m].x), y[e][0]);
             y[e][1] = __ffma2_rn(w23, vt_two(u[e][m].y), y[e][1]);
         }
     }
-    float ss[kVtNodes];
+    float ss[NODES];
 #pragma unroll
-    for (int e = 0; e < kVtNodes; ++e) {
+    for (int e = 0; e < NODES; ++e) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) y[e][c] = make_float2(tree_silu(y[e][c].x), tree_silu(y[e][c].y));
         const float2 sq = __ffma2_rn(y[e][0], y[e][0], __fmul2_rn(y[e][1], y[e][1]));
@@ -595,16 +595,16 @@ __device__ __noinline__ void vt_conv(uint32_t raw, const unsigned char* x, const
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1)
 #pragma unroll
-            for (int e = 0; e < kVtNodes; ++e) ss[e] += __shfl_xor_sync(0xffffffffu, ss[e], off);
+            for (int e = 0; e < NODES; ++e) ss[e] += __shfl_xor_sync(0xffffffffu, ss[e], off);
 #pragma unroll
-        for (int e = 0; e < kVtNodes; ++e) {
+        for (int e = 0; e < NODES; ++e) {
             const float f = scale * rsqrtf(ss[e] + eps);
             if (i0 + e < n)
                 tc::st_row4(Bt, rows, row0 + i0 + e, 4 * lane, y[e][0].x * f, y[e][0].y * f, y[e][1].x * f, y[e][1].y * f);
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < kVtNodes; ++e)
+        for (int e = 0; e < NODES; ++e)
             if (i0 + e < n)
                 *reinterpret_cast<float4*>(v + (i0 + e) * 128 + 4 * lane) = make_float4(y[e][0].x, y[e][0].y, y[e][1].x, y[e][1].y);
     }
@@ -741,9 +741,11 @@ __device__ __noinline__ void vt_below(unsigned char* A, int rows, int r0, int c0
     __syncwarp();
 }
 
-__global__ void __launch_bounds__(kVtThreads, 2)
+// CTAS: what registers allow for on an SM
+template <int CTAS>
+__global__ void __launch_bounds__(kVtThreads, CTAS)
     k_tree_verify_tc(const __grid_constant__ CUtensorMap ts, const __grid_constant__ VtArgs A) {
-    constexpr int D = 128;
+    constexpr int D = 128, NODES = CTAS == 3 ? 2 : 3;  // nodes that a warp takes at a time in the conv
     using bf = __nv_bfloat16;
     const Geom& g = A.g;
     const TreeJob& J = A.job;
@@ -924,13 +926,13 @@ __global__ void __launch_bounds__(kVtThreads, 2)
     float* v = reinterpret_cast<float*>(sm + lay.v);
     auto conv = [&](int what, int i, int batch) {  // what: k (0) and q (1) from shared memory, v of v-head j0 + i (2)
         const int ch = channel(what, i) + 4 * lane;
-        vt_conv(what < 2 ? smem_u32(raw + what * D + 4 * lane) : 0u, reinterpret_cast<const unsigned char*>(xb + ch) - (size_t)Km1 * C * 2,
+        vt_conv<NODES>(what < 2 ? smem_u32(raw + what * D + 4 * lane) : 0u, reinterpret_cast<const unsigned char*>(xb + ch) - (size_t)Km1 * C * 2,
                 reinterpret_cast<const unsigned char*>(cb + ch), (uint32_t)C * 2u, taps,
                 reinterpret_cast<const uint2*>(ws + (what + (i & 1)) * 4 * D),
-                A.p.conv_b ? static_cast<const bf*>(A.p.conv_b) + ch : nullptr, K, kVtNodes * batch, n, v, Bt, 2 * nm,
+                A.p.conv_b ? static_cast<const bf*>(A.p.conv_b) + ch : nullptr, K, NODES * batch, n, v, Bt, 2 * nm,
                 what == 1 ? nm : 0, what == 0 ? 1.f : g.q_scale, g.l2_eps);
     };
-    const int batches = (n + kVtNodes - 1) / kVtNodes;
+    const int batches = (n + NODES - 1) / NODES;
 #pragma unroll 1
     for (int k = warp; k < 2 * batches; k += kVtWorkers + 1) conv(k & 1, 0, k >> 1);
     fence_proxy_async_smem();
@@ -1307,10 +1309,16 @@ PFN_cuTensorMapEncodeTiled_v12000 vt_encode_fn() {
     return fn;
 }
 
-cudaError_t launch_verify_tc(const Geom& g, const LayerParams& p, const TreeJob& job, cudaStream_t st) {
+template <int CTAS>
+cudaError_t launch_verify_ctas(const CUtensorMap& map, const VtArgs& A, cudaStream_t st) {
     static std::atomic<uint64_t> smem_set{0};
-    cudaError_t e = raise_smem_limit(k_tree_verify_tc, 227 * 1024, smem_set);
+    const cudaError_t e = raise_smem_limit(k_tree_verify_tc<CTAS>, 227 * 1024, smem_set);
     if (e != cudaSuccess) return e;
+    return launch_pdl(k_tree_verify_tc<CTAS>, dim3((unsigned)(A.g.Hv / A.gv), (unsigned)A.job.B), dim3(kVtThreads),
+                      (size_t)vt_smem(A.nm, A.gv).total + 1024, st, map, A);
+}
+
+cudaError_t launch_verify_tc(const Geom& g, const LayerParams& p, const TreeJob& job, cudaStream_t st) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = vt_encode_fn();
     if (!enc) return cudaErrorInvalidValue;
     CUtensorMap map;
@@ -1327,8 +1335,11 @@ cudaError_t launch_verify_tc(const Geom& g, const LayerParams& p, const TreeJob&
     // against 21.8, 64 of 32 nodes 76 against 98), or as many as shared memory and two (node, v-head) pairs a thread allow
     if ((long)job.B * g.Hk < sm_count()) A.gv = 1;
     while (vt_smem(A.nm, A.gv).total + 1024 > 227 * 1024 || A.nm * A.gv > 2 * kVtThreads || A.gv > 8 || A.g.G % A.gv) --A.gv;
-    return launch_pdl(k_tree_verify_tc, dim3((unsigned)(g.Hv / A.gv), (unsigned)job.B), dim3(kVtThreads),
-                      (size_t)vt_smem(A.nm, A.gv).total + 1024, st, map, A);
+    // Trees of up to 16 nodes leave shared memory for a third CTA on an SM: with fewer registers each, faster once more than
+    // two have work (us, 16 / 32 heads: 64 trees of 8 nodes 45 against 51; one tree 8.9 against 8.7; trees of up to 32 nodes,
+    // where shared memory holds two, 84 against 76)
+    if (A.nm <= 16 && (long)job.B * (g.Hv / A.gv) > 2L * sm_count()) return launch_verify_ctas<3>(map, A, st);
+    return launch_verify_ctas<2>(map, A, st);
 }
 
 // ---- commit ---------------------------------------------------------------------

@@ -27,6 +27,14 @@ def test_verify_tree_all_v_heads_in_a_cta(geom):
     c.check(c.verify(), heads=sample_heads(geom.n_v_heads, 3), sample=3)
 
 
+@pytest.mark.parametrize("G", [1, 2, 3])
+def test_verify_tree_many_small_trees(G):
+    """More CTAs than two for each SM, trees of up to 16 nodes: a third one on an SM."""
+    r = np.random.default_rng(9)
+    c = test_tree_gdn.Case([int(v) for v in r.integers(0, 17, 170)], synth.Geometry(2, 2 * G, 128, 128, 4), synth.BF16, 43)
+    c.check(c.verify(), heads=[0, 2 * G - 1], sample=2)
+
+
 def unreached(c, b, bad):
     return [i for i in range(c.nodes[b]) if bad not in line(c.trees[b], i)]
 
