@@ -440,7 +440,7 @@ constexpr int kVtRows = 4;       // warps 0 .. 3 have the state rows: TMEM lanes
 constexpr int kVtAtom = 16384;   // 128 state rows x 32 columns
 
 struct VtSmem {
-    int S, B, A, P, v, w, taps, gate, beta, eg, line, up, bad, bar, total;
+    int S, B, A, P, v, w, own, taps, gate, beta, eg, line, up, bad, bar, total;
 };
 
 __host__ __device__ inline VtSmem vt_smem(int nm, int gv) {  // nm: nodes, rounded up to 16
@@ -453,6 +453,7 @@ __host__ __device__ inline VtSmem vt_smem(int nm, int gv) {  // nm: nodes, round
     s.P = o; o += two * ((nm + 31) / 32) * nm * 128; // (at first, from A on: raw q and k of [K - 1 + n] rows)
     s.v = o; o += nm * 512;                          // v, then o: [node][row]
     s.w = o; o += (2 + two) * 4 * 128 * 2;           // conv weights of k, q and two v-heads: [4 taps][128]
+    s.own = o; o += nm * 4;                          // q_i . k_i
     s.taps = o; o += nm * 16;                        // rows of the conv taps: K - 1 rows of the conv state, then the nodes
     s.gate = o; o += nm * gv * 4;                    // [v-head][node]: log2 alpha, then its sum G along the line
     s.beta = o; o += nm * gv * 4;
@@ -534,39 +535,11 @@ __device__ __forceinline__ float2 vt_two(uint32_t u) {
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
 
-// conv + SiLU of the warp's 128 channels (4 to a lane) at NODES nodes from i0 on, all loads at once.  `raw` != 0: k or q,
-// its inputs in shared memory from there on (conv state first, 512 bytes to a row), L2-normalised times scale, to row
-// row0 + node of [K^; Q^].  Else v, inputs in global memory (x: from K - 1 rows
-// before the first node's), to v[node][4 lane].  One copy of this code serves every
-// call: the phases run once per CTA, and copies in line were bound by instruction fetch.
+// the convolution and SiLU of the warp's 128 channels (4 to a lane) at NODES nodes: u: inputs by tap, w: [tap][128] weights
 template <int NODES>
-__device__ __noinline__ void vt_conv(uint32_t raw, const unsigned char* x, const unsigned char* state, uint32_t row_bytes,
-                                     const int4* taps, const uint2* w, const __nv_bfloat16* bias, int K, int i0, int n,
-                                     float* v, unsigned char* Bt, int rows, int row0, float scale, float eps) {
+__device__ __forceinline__ void vt_taps(const uint2 (&u)[NODES][4], const uint2* w, const __nv_bfloat16* bias, int K,
+                                        float2 (&y)[NODES][2]) {
     const int lane = threadIdx.x & 31;
-    uint2 u[NODES][4];
-    if (raw) {
-#pragma unroll
-        for (int e = 0; e < NODES; ++e) {
-            const int4 t4 = taps[min(i0 + e, n - 1)];
-            const int tap[4] = {t4.x, t4.y, t4.z, t4.w};
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const uint32_t at = raw + tap[m] * 512;
-                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(u[e][m].x), "=r"(u[e][m].y) : "r"(at));
-            }
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < NODES; ++e) {
-            const int4 t4 = taps[min(i0 + e, n - 1)];
-            const int tap[4] = {t4.x, t4.y, t4.z, t4.w};
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-                u[e][m] = __ldg(reinterpret_cast<const uint2*>((tap[m] < K - 1 ? state : x) + (uint64_t)(uint32_t)tap[m] * row_bytes));
-        }
-    }
-    float2 y[NODES][2];
 #pragma unroll
     for (int e = 0; e < NODES; ++e)
 #pragma unroll
@@ -583,30 +556,94 @@ __device__ __noinline__ void vt_conv(uint32_t raw, const unsigned char* x, const
             y[e][1] = __ffma2_rn(w23, vt_two(u[e][m].y), y[e][1]);
         }
     }
-    float ss[NODES];
 #pragma unroll
-    for (int e = 0; e < NODES; ++e) {
+    for (int e = 0; e < NODES; ++e)
 #pragma unroll
         for (int c = 0; c < 2; ++c) y[e][c] = make_float2(tree_silu(y[e][c].x), tree_silu(y[e][c].y));
-        const float2 sq = __ffma2_rn(y[e][0], y[e][0], __fmul2_rn(y[e][1], y[e][1]));
-        ss[e] = sq.x + sq.y;
+}
+
+// Both functions: one copy of the code serves every call (the phases run once per CTA, and copies in line were bound by
+// instruction fetch), and all loads of a call are on their way at once.
+
+// v at the nodes i0 .. i0 + NODES - 1, inputs in global memory (x: from K - 1 rows before the first node's), to
+// v[node][4 lane]
+template <int NODES>
+__device__ __noinline__ void vt_conv_v(const unsigned char* x, const unsigned char* state, uint32_t row_bytes, const int4* taps,
+                                       const uint2* w, const __nv_bfloat16* bias, int K, int i0, int n, float* v) {
+    uint2 u[NODES][4];
+#pragma unroll
+    for (int e = 0; e < NODES; ++e) {
+        const int4 t4 = taps[min(i0 + e, n - 1)];
+        const int tap[4] = {t4.x, t4.y, t4.z, t4.w};
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+            u[e][m] = __ldg(reinterpret_cast<const uint2*>((tap[m] < K - 1 ? state : x) + (uint64_t)(uint32_t)tap[m] * row_bytes));
     }
-    if (raw) {
+    float2 y[NODES][2];
+    vt_taps<NODES>(u, w, bias, K, y);
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1)
-#pragma unroll
-            for (int e = 0; e < NODES; ++e) ss[e] += __shfl_xor_sync(0xffffffffu, ss[e], off);
+    for (int e = 0; e < NODES; ++e)
+        if (i0 + e < n)
+            *reinterpret_cast<float4*>(v + (i0 + e) * 128 + 4 * (threadIdx.x & 31)) =
+                make_float4(y[e][0].x, y[e][0].y, y[e][1].x, y[e][1].y);
+}
+
+// k, then q, at the same nodes: inputs in shared memory from `raw` on (conv state first; a row is k's 256 bytes, then
+// q's), L2-normalised to rows `node` and nm + node of [K^; Q^], q times `scale` too.  And own[node] = q . k as it was before
+// the operands' rounding: where the decays leave a node little but its own token, o is v times this number, the norm
+// divides by its size, and of a small one TF32's 2^-11 of |q| |k| would be much.
+template <int NODES>
+__device__ __noinline__ void vt_conv_kq(uint32_t raw, const int4* taps, const uint2* w, const __nv_bfloat16* bias_k,
+                                        const __nv_bfloat16* bias_q, int K, int i0, int n, unsigned char* Bt, int nm, float scale,
+                                        float eps, float* own) {
+    const int lane = threadIdx.x & 31;
+    float2 k[NODES][2], y[NODES][2];
+    float kk[NODES], qq[NODES], qk[NODES];
+#pragma unroll 1
+    for (int what = 0; what < 2; ++what) {
+        uint2 u[NODES][4];
 #pragma unroll
         for (int e = 0; e < NODES; ++e) {
-            const float f = scale * rsqrtf(ss[e] + eps);
-            if (i0 + e < n)
-                tc::st_row4(Bt, rows, row0 + i0 + e, 4 * lane, y[e][0].x * f, y[e][0].y * f, y[e][1].x * f, y[e][1].y * f);
-        }
-    } else {
+            const int4 t4 = taps[min(i0 + e, n - 1)];
+            const int tap[4] = {t4.x, t4.y, t4.z, t4.w};
 #pragma unroll
-        for (int e = 0; e < NODES; ++e)
-            if (i0 + e < n)
-                *reinterpret_cast<float4*>(v + (i0 + e) * 128 + 4 * lane) = make_float4(y[e][0].x, y[e][0].y, y[e][1].x, y[e][1].y);
+            for (int m = 0; m < 4; ++m)
+                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                             : "=r"(u[e][m].x), "=r"(u[e][m].y)
+                             : "r"(raw + what * 256 + tap[m] * 512));
+        }
+        vt_taps<NODES>(u, w + what * 128, what ? bias_q : bias_k, K, y);
+        if (what == 0) {
+#pragma unroll
+            for (int e = 0; e < NODES; ++e)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) k[e][c] = y[e][c];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < NODES; ++e) {
+        const float2 a = __ffma2_rn(k[e][0], k[e][0], __fmul2_rn(k[e][1], k[e][1]));
+        const float2 b = __ffma2_rn(y[e][0], y[e][0], __fmul2_rn(y[e][1], y[e][1]));
+        const float2 c = __ffma2_rn(k[e][0], y[e][0], __fmul2_rn(k[e][1], y[e][1]));
+        kk[e] = a.x + a.y;
+        qq[e] = b.x + b.y;
+        qk[e] = c.x + c.y;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+        for (int e = 0; e < NODES; ++e) {
+            kk[e] += __shfl_xor_sync(0xffffffffu, kk[e], off);
+            qq[e] += __shfl_xor_sync(0xffffffffu, qq[e], off);
+            qk[e] += __shfl_xor_sync(0xffffffffu, qk[e], off);
+        }
+#pragma unroll
+    for (int e = 0; e < NODES; ++e) {
+        if (i0 + e >= n) continue;
+        const float fk = rsqrtf(kk[e] + eps), fq = scale * rsqrtf(qq[e] + eps);
+        tc::st_row4(Bt, 2 * nm, i0 + e, 4 * lane, k[e][0].x * fk, k[e][0].y * fk, k[e][1].x * fk, k[e][1].y * fk);
+        tc::st_row4(Bt, 2 * nm, nm + i0 + e, 4 * lane, y[e][0].x * fq, y[e][0].y * fq, y[e][1].x * fq, y[e][1].y * fq);
+        if (lane == 0) own[i0 + e] = qk[e] * fk * fq;
     }
 }
 
@@ -758,6 +795,7 @@ __global__ void __launch_bounds__(kVtThreads, CTAS)
     const VtSmem lay = vt_smem(nm, gv);
     unsigned char* Bt = sm + lay.B;
     bf* ws = reinterpret_cast<bf*>(sm + lay.w);
+    float* own = reinterpret_cast<float*>(sm + lay.own);
     int4* taps = reinterpret_cast<int4*>(sm + lay.taps);
     float* gate = reinterpret_cast<float*>(sm + lay.gate);
     float* betas = reinterpret_cast<float*>(sm + lay.beta);
@@ -924,17 +962,20 @@ __global__ void __launch_bounds__(kVtThreads, CTAS)
         return ok;
     };
     float* v = reinterpret_cast<float*>(sm + lay.v);
-    auto conv = [&](int what, int i, int batch) {  // what: k (0) and q (1) from shared memory, v of v-head j0 + i (2)
-        const int ch = channel(what, i) + 4 * lane;
-        vt_conv<NODES>(what < 2 ? smem_u32(raw + what * D + 4 * lane) : 0u, reinterpret_cast<const unsigned char*>(xb + ch) - (size_t)Km1 * C * 2,
-                reinterpret_cast<const unsigned char*>(cb + ch), (uint32_t)C * 2u, taps,
-                reinterpret_cast<const uint2*>(ws + (what + (i & 1)) * 4 * D),
-                A.p.conv_b ? static_cast<const bf*>(A.p.conv_b) + ch : nullptr, K, NODES * batch, n, v, Bt, 2 * nm,
-                what == 1 ? nm : 0, what == 0 ? 1.f : g.q_scale, g.l2_eps);
-    };
-    const int batches = (n + NODES - 1) / NODES;
+    const bf* bias = static_cast<const bf*>(A.p.conv_b);
+    auto conv_v = [&](int i) {  // of v-head j0 + i, by the workers
+        const int ch = channel(2, i) + 4 * lane;
 #pragma unroll 1
-    for (int k = warp; k < 2 * batches; k += kVtWorkers + 1) conv(k & 1, 0, k >> 1);
+        for (int i0 = NODES * warp; i0 < n; i0 += NODES * kVtWorkers)
+            vt_conv_v<NODES>(reinterpret_cast<const unsigned char*>(xb + ch) - (size_t)Km1 * C * 2,
+                             reinterpret_cast<const unsigned char*>(cb + ch), (uint32_t)C * 2u, taps,
+                             reinterpret_cast<const uint2*>(ws + (2 + (i & 1)) * 4 * D), bias ? bias + ch : nullptr, K, i0, n, v);
+    };
+#pragma unroll 1
+    for (int i0 = 2 * warp; i0 < n; i0 += 2 * (kVtWorkers + 1))
+        vt_conv_kq<2>(smem_u32(raw + 4 * lane), taps, reinterpret_cast<const uint2*>(ws),
+                      bias ? bias + channel(0, 0) + 4 * lane : nullptr, bias ? bias + channel(1, 0) + 4 * lane : nullptr, K, i0, n, Bt,
+                      nm, g.q_scale, g.l2_eps, own);
     fence_proxy_async_smem();
     __syncthreads();  // [K^; Q^] is there
     if (warp == kVtWorkers) {
@@ -1024,8 +1065,7 @@ __global__ void __launch_bounds__(kVtThreads, CTAS)
                 if (tid < 5) s_bad[tid] = 0ull;
                 named_bar_sync(1, 32 * kVtWorkers);
             }
-#pragma unroll 1
-            for (int k = warp; k < batches; k += kVtWorkers) conv(2, i0, k);
+            conv_v(i0);
             // A and P from the Gram matrix: thread = row (a node's key, or its query), 8 columns at a time by the warps
             // of the row's quarter
             const int q4 = warp & 3, row = 32 * q4 + lane;
@@ -1037,6 +1077,7 @@ __global__ void __launch_bounds__(kVtThreads, CTAS)
                 const unsigned long long mine = in ? line[i] & ~(is_q ? 0ull : 1ull << i) : 0ull;
                 const int ig = i0 * nm + (in ? i : 0);
                 const float gi[2] = {gate[ig], gate[ig + (two - 1) * nm]};
+                const float diag = is_q && in && i < n ? own[i] : 0.f;
                 const float fi[2] = {is_q ? 1.f : betas[ig], is_q ? 1.f : betas[ig + (two - 1) * nm]};
                 unsigned char* to = sm + (is_q ? lay.P : lay.A);
                 float odd = 0.f;  // NaN from the first infinity or NaN on
@@ -1046,6 +1087,9 @@ __global__ void __launch_bounds__(kVtThreads, CTAS)
                     vt_ld8(tc::taddr(tgram, 32 * q4, c0), r);
                     tc::ld_wait();
                     const uint32_t m8 = (uint32_t)(mine >> c0) & 0xffu;
+                    float p8[8];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) p8[c] = c0 + c == i ? diag : __uint_as_float(r[c]);  // (A has no diagonal)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         if (e == two) break;
@@ -1054,7 +1098,7 @@ __global__ void __launch_bounds__(kVtThreads, CTAS)
                         *reinterpret_cast<float4*>(gc + 4) = *reinterpret_cast<const float4*>(gate + (i0 + e) * nm + c0 + 4);
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
-                            x[c] = (m8 >> c) & 1u ? tree_ex2(gi[e] - gc[c]) * __uint_as_float(r[c]) * fi[e] : 0.f;
+                            x[c] = (m8 >> c) & 1u ? tree_ex2(gi[e] - gc[c]) * p8[c] * fi[e] : 0.f;
                             odd = fmaf(x[c], 0.f, odd);
                             if (is_q) x[c] = tc::to_tf32_rn(x[c]);
                         }
@@ -1106,8 +1150,7 @@ __global__ void __launch_bounds__(kVtThreads, CTAS)
             for (int i = i0; i < i0 + two; ++i) {
                 const int e = i & 1, ph = i >> 1;
                 if (i > i0) {
-#pragma unroll 1
-                    for (int k = warp; k < batches; k += kVtWorkers) conv(2, i, k);
+                    conv_v(i);
                     named_bar_sync(1, 32 * kVtWorkers);
                 }
                 uint2 zr[kVtNorm];  // of the nodes below, kVtNorm at a time
