@@ -18,6 +18,7 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libgdn.so")
+MARSHAL_PATH = os.path.join(_PKG, "_marshal.so")
 
 BF16, F32 = 0, 1
 RAW_QKV, NO_L2NORM, GATES_DIRECT, NO_OUTNORM = 1, 2, 4, 8
@@ -395,19 +396,29 @@ GDN_TREE_MAX_NODES = 64
 
 # A call's tensors are held to their dtypes and shapes and to one CUDA device (sizes reach the library from the
 # shapes, so a wrong one would be a wrong address), and the call runs with that device current.  These calls are
-# made once per layer and step, so the checks are plain expressions.
+# made once per layer and step, so the checks are native (_marshal.so); what does not fit comes back here.
 _bf16, _f32, _i32, _i64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
 _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
-def _ptr(t, name, dtype, shape, device):
-    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
-        return t.data_ptr()
+def _explain(t, name, dtype, shape, device):
     if t.get_device() != device or device < 0:
         raise ValueError(f"{name}: found a tensor on {t.device}, required one CUDA device for all tensors")
     if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name}: found {t.dtype} {tuple(t.shape)}, required {dtype} {tuple(shape)}")
     raise ValueError(f"{name}: libgdn takes dense row-major tensors")
+
+
+def _ptr(*args):
+    """The address of a tensor that has this dtype, shape and device and is dense: (tensor, name, dtype, shape, device)."""
+    global _ptr
+    if not os.path.exists(MARSHAL_PATH):
+        raise RuntimeError(f"_marshal.so is not built ({MARSHAL_PATH}); run "
+                           "`python -m hybrid_gated_deltanet_gb300.build`")
+    from . import _marshal
+    _marshal.explain(_explain)
+    _ptr = _marshal.ptr
+    return _ptr(*args)
 
 
 def _device(t, name):

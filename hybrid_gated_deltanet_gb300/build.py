@@ -2,15 +2,18 @@
 
 Each .cu translation unit compiles in parallel into ``_build/`` at the repo
 root; the objects link into ``hybrid_gated_deltanet_gb300/libgdn.so`` with the
-CUDA runtime linked statically.  Usage: ``python -m hybrid_gated_deltanet_gb300.build``.
+CUDA runtime linked statically.  ``gdn_marshal.cpp`` (checks of tensors, against torch's
+headers) becomes the extension module ``_marshal.so`` beside it.  Usage: ``python -m hybrid_gated_deltanet_gb300.build``.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import platform
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,9 +21,11 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["gdn_api.cu", "gdn_decode.cu", "gdn_prefill.cu", "gdn_chunk16.cu", "gdn_noalloc.cu", "gdn_proj.cu",
            "gdn_attn.cu", "gdn_attn_tree.cu", "gdn_tree.cu", "gdn_tables.cu"]
+MARSHAL_SOURCE = "gdn_marshal.cpp"
 HEADERS = ["gdn_common.cuh", "gdn_internal.h", "gdn_prefill_common.cuh", "gdn_tc.cuh", "gdn_tma.cuh"]
 
 
@@ -37,7 +42,7 @@ def _flags(extra=()):
 
 
 def _newest_input() -> float:
-    paths = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(ROOT, "include", "gdn.h"),
+    paths = [os.path.join(CSRC, f) for f in SOURCES + HEADERS + [MARSHAL_SOURCE]] + [os.path.join(ROOT, "include", "gdn.h"),
                                                                    os.path.abspath(__file__)]
     return max(os.path.getmtime(p) for p in paths)
 
@@ -58,10 +63,28 @@ def _built_here(path: str) -> bool:
     return want is None or int.from_bytes(head[18:20], "little") == want
 
 
+def _current(path: str) -> bool:
+    return os.path.exists(path) and _built_here(path) and os.path.getmtime(path) >= _newest_input()
+
+
+def _build_marshal():
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    includes = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"]]
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared"]
+    cmd += [f"-I{d}" for d in includes] + [os.path.join(CSRC, MARSHAL_SOURCE), "-o", tmp]
+    cmd += ["-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {MARSHAL_SOURCE}:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, MARSHAL)
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile and link libgdn.so; skipped when the library exists, was built for this
-    host's architecture and is newer than every source, header and this script."""
-    if not force and os.path.exists(LIB) and _built_here(LIB) and os.path.getmtime(LIB) >= _newest_input():
+    """Compile and link libgdn.so and _marshal.so; skipped when both exist, were built for this
+    host's architecture and are newer than every source, header and this script."""
+    if not force and _current(LIB) and _current(MARSHAL):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -75,8 +98,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             raise RuntimeError(f"nvcc failed on {src}:\n{res.stdout}\n{res.stderr}")
         return obj, res.stderr
 
-    with ThreadPoolExecutor(len(SOURCES)) as ex:
+    with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        marshal = ex.submit(_build_marshal)
         results = list(ex.map(compile_one, SOURCES))
+        marshal.result()
     if verbose or ptxas_info:
         for _, log in results:
             if log:
