@@ -123,12 +123,35 @@ __device__ __forceinline__ void tree_scan(long long v, long long* s_warp, long l
     }
 }
 
-// worker w's share: `left` tiles from tile `rem` of sequence b's lists on
+// one piece of a worker's share: tiles t0 .. t1 - 1 of the nt of list (b, kvh), rows 128 rt ..
+struct TreeSeg {
+    int b, kvh, rt, t0, t1, nt, first, n, ctx;
+};
+
+// worker w's share: `left` tiles, of which `seg` is the first piece
 struct TreeRun {
-    int b;
-    long long rem, left;
+    TreeSeg seg;
+    long long left;
     int first, last;  // workers that hold the list the share begins in
 };
+
+// the piece that begins at tile t0 of list `list` of sequence seg.b (seg.nt, first, n and ctx are known)
+__device__ __forceinline__ void tree_piece(const AttnTreeArgs& A, TreeSeg& seg, int list, int t0, long long left) {
+    const int per_head = (seg.n * A.G + 127) >> 7;
+    seg.kvh = per_head == 1 ? list : list / per_head;
+    seg.rt = list - seg.kvh * per_head;
+    seg.t0 = t0;
+    seg.t1 = (int)min((long long)seg.nt, t0 + left);
+}
+
+// ceil(a / per), rcp about 1 / per: exact up to 2^22, and not below 2^22 above that
+__device__ __forceinline__ uint32_t tree_div_up(uint32_t a, uint32_t per, float rcp) {
+    const uint32_t x = a + per - 1;
+    uint32_t q = (uint32_t)((float)x * rcp);
+    if ((q + 1) * per <= x) ++q;
+    if (q * per > x) --q;
+    return q;
+}
 
 // A.even: worker w takes piece w.  Every warp works it out by itself (there are at most kTreeCtas sequences, five to a
 // lane): loads of one latency, then a bisection for the shortest pieces of which there are at most W
@@ -146,10 +169,11 @@ __device__ __forceinline__ TreeRun tree_run_even(const AttnTreeArgs& A, int w) {
         most = max(most, nt[e]);
     }
     auto count = [&](uint32_t per) {  // pieces of this lane's sequences
+        const float rcp = __fdividef(1.f, (float)per);
         uint32_t c = 0;
 #pragma unroll
         for (int e = 0; e < PER; ++e)
-            if (e < each) c += lists[e] * ((nt[e] + per - 1) / per);
+            if (e < each) c += lists[e] * tree_div_up(nt[e], per, rcp);
         return c;
     };
     uint32_t lo = kTreeMinTiles, hi = __reduce_max_sync(0xffffffffu, most);  // (one piece per list always fits)
@@ -168,33 +192,36 @@ __device__ __forceinline__ TreeRun tree_run_even(const AttnTreeArgs& A, int w) {
         if (lane >= off) incl += x;
     }
     const unsigned owner = __ballot_sync(0xffffffffu, (uint32_t)w >= incl - mine && (uint32_t)w < incl);
-    TreeRun run{0, 0, 0, 0, 0};
+    TreeRun run;
+    run.left = 0;
     if (owner == 0u) return run;
-    uint32_t at = incl - mine, piece = 0, pieces = 1, list = 0, tiles = 0;
+    const float rcp = __fdividef(1.f, (float)lo);
+    uint32_t at = incl - mine, piece = 0, pieces = 1, list = 0;
+    int b = 0;
     bool found = false;
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
-        const uint32_t per_list = (nt[e] + lo - 1) / lo, len = e < each ? lists[e] * per_list : 0u;
+        if (e >= each) break;
+        const uint32_t per_list = tree_div_up(nt[e], lo, rcp), len = lists[e] * per_list;
         if (!found && (uint32_t)w >= at && (uint32_t)w < at + len) {
             found = true;
-            run.b = lane * each + e;
+            b = lane * each + e;
             pieces = per_list;
             list = ((uint32_t)w - at) / per_list;
-            piece = ((uint32_t)w - at) % per_list;
-            tiles = nt[e];
+            piece = (uint32_t)w - at - list * per_list;
         }
         at += len;
     }
     const int src = __ffs(owner) - 1;
-    run.b = __shfl_sync(0xffffffffu, run.b, src);
+    run.seg.b = __shfl_sync(0xffffffffu, b, src);
     pieces = __shfl_sync(0xffffffffu, pieces, src);
     piece = __shfl_sync(0xffffffffu, piece, src);
     list = __shfl_sync(0xffffffffu, list, src);
-    tiles = __shfl_sync(0xffffffffu, tiles, src);
+    run.seg.nt = tree_tiles<BK>(A, run.seg.b, run.seg.first, run.seg.n, run.seg.ctx);
     // (at most 2^24 tiles and kTreeCtas pieces: the products fit)
-    const uint32_t t0 = tiles * piece / pieces, t1 = tiles * (piece + 1) / pieces;
-    run.rem = (long long)list * tiles + t0;
+    const uint32_t tiles = run.seg.nt, t0 = tiles * piece / pieces, t1 = tiles * (piece + 1) / pieces;
     run.left = t1 - t0;
+    tree_piece(A, run.seg, (int)list, (int)t0, run.left);
     run.first = w - (int)piece;
     run.last = run.first + (int)pieces - 1;
     return run;
@@ -210,10 +237,11 @@ __device__ __forceinline__ TreeRun tree_run(const AttnTreeArgs& A, int w) {
     const int tid = threadIdx.x;
     int first, n, ctx;
     if (A.whole) {
-        run.b = w / (A.Hkv * A.whole);
-        const int nt = tree_tiles<BK>(A, run.b, first, n, ctx), at = w % (A.Hkv * A.whole);
-        run.left = at < tree_lists(A, n) ? nt : 0;
-        run.rem = (long long)at * nt;
+        const int lists = A.Hkv * A.whole, b = w / lists, at = w - b * lists;
+        run.seg.b = b;
+        run.seg.nt = tree_tiles<BK>(A, b, run.seg.first, run.seg.n, run.seg.ctx);
+        run.left = at < tree_lists(A, run.seg.n) ? run.seg.nt : 0;
+        if (run.left > 0) tree_piece(A, run.seg, at, 0, run.left);
         run.first = run.last = w;
         return run;
     }
@@ -248,45 +276,42 @@ __device__ __forceinline__ TreeRun tree_run(const AttnTreeArgs& A, int w) {
         }
     }
     __syncthreads();
-    run.b = s_b;
-    run.rem = s_rem;
     run.left = s_left;
     run.first = s_first;
     run.last = s_last;
+    if (run.left > 0) {
+        run.seg.b = s_b;
+        run.seg.nt = tree_tiles<BK>(A, s_b, run.seg.first, run.seg.n, run.seg.ctx);
+        const long long list = s_rem / run.seg.nt;
+        tree_piece(A, run.seg, (int)list, (int)(s_rem - list * run.seg.nt), run.left);
+    }
     return run;
 }
 
-// one piece of a worker's share: tiles t0 .. t1 - 1 of the nt of list (b, kvh), rows 128 rt ..
-struct TreeSeg {
-    int b, kvh, rt, t0, t1, nt, first, n, ctx;
-};
-
+// the pieces of a worker's share, one after another
 template <int BK>
 struct TreeWalk {
     const AttnTreeArgs& A;
-    int b;
-    long long rem, left;
-    __device__ TreeWalk(const AttnTreeArgs& a, const TreeRun& r) : A(a), b(r.b), rem(r.rem), left(r.left) {}
+    TreeSeg at;  // the next piece
+    long long left;
+    __device__ TreeWalk(const AttnTreeArgs& a, const TreeRun& r) : A(a), at(r.seg), left(r.left) {}
     __device__ bool next(TreeSeg& s) {
-        while (left > 0 && b < A.B) {
-            s.nt = tree_tiles<BK>(A, b, s.first, s.n, s.ctx);
-            const int lists = tree_lists(A, s.n);
-            if (s.nt == 0 || rem >= (long long)s.nt * lists) {
-                rem = 0;
-                ++b;
-                continue;
+        if (left <= 0) return false;
+        s = at;
+        left -= at.t1 - at.t0;
+        if (left > 0) {  // on to the next list, or the next sequence that has one
+            int list = at.kvh * ((at.n * A.G + 127) >> 7) + at.rt + 1;
+            while (list >= tree_lists(A, at.n)) {
+                if (++at.b >= A.B) {
+                    left = 0;
+                    return true;
+                }
+                at.nt = tree_tiles<BK>(A, at.b, at.first, at.n, at.ctx);
+                list = 0;
             }
-            const int list = (int)(rem / s.nt), per_head = lists / A.Hkv;
-            s.b = b;
-            s.kvh = list / per_head;
-            s.rt = list % per_head;
-            s.t0 = (int)(rem - (long long)list * s.nt);
-            s.t1 = (int)min((long long)s.nt, s.t0 + left);
-            left -= s.t1 - s.t0;
-            rem += s.t1 - s.t0;
-            return true;
+            tree_piece(A, at, list, 0, left);
         }
-        return false;
+        return true;
     }
 };
 
@@ -431,11 +456,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     griddep_launch_dependents();
     const TreeRun run = tree_run<D, kTreeThreads>(A, blockIdx.x);
     if (A.share && tid == 352) {  // for the join
-        TreeSeg s;
-        TreeWalk<BK> walk(A, run);
-        const bool any = walk.next(s);
-        A.share[2 * blockIdx.x] = any ? make_int4(run.first, run.last, s.rt, s.kvh) : make_int4(-2, 0, 0, 0);
-        A.share[2 * blockIdx.x + 1] = any ? make_int4(s.first, s.n, 0, 0) : make_int4(0, 0, 0, 0);
+        const bool any = run.left > 0;
+        A.share[2 * blockIdx.x] = any ? make_int4(run.first, run.last, run.seg.rt, run.seg.kvh) : make_int4(-2, 0, 0, 0);
+        A.share[2 * blockIdx.x + 1] = any ? make_int4(run.seg.first, run.seg.n, 0, 0) : make_int4(0, 0, 0, 0);
     }
     if (run.left <= 0) return;  // (the same for all threads)
     uint32_t tm = 0;
@@ -761,7 +784,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                     wait(full_v + st, it >> 1);
                     uint4* vt = reinterpret_cast<uint4*>(sm + Ly::V + st * Ly::TILE);
                     const int upto = (keys + 15) / 16 * 16 * (NCH * 8);
-                    for (int i = r; i < upto; i += 128) {
+                    const int from = own_keys || gone != 0u ? 0 : keys / 8 * (NCH * 64);
+                    for (int i = from + r; i < upto; i += 128) {
                         const int row = i / (NCH * 64) * 8 + (i & 63) / 8;
                         if (row >= keys || (!own_keys && ((gone >> (row / A.R)) & 1u))) {
                             vt[i] = make_uint4(0u, 0u, 0u, 0u);
