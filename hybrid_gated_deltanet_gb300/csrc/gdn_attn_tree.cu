@@ -159,7 +159,7 @@ template <int BK>
 __device__ __forceinline__ TreeRun tree_run_even(const AttnTreeArgs& A, int w) {
     constexpr int PER = (kTreeCtas + 31) / 32;
     const int lane = threadIdx.x & 31, each = (A.B + 31) / 32;
-    uint32_t nt[PER], lists[PER], most = kTreeMinTiles;
+    uint32_t nt[PER], lists[PER], most = kTreeMinTiles, tiles_here = 0, lists_here = 0;
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
         const int b = lane * each + e;
@@ -167,6 +167,8 @@ __device__ __forceinline__ TreeRun tree_run_even(const AttnTreeArgs& A, int w) {
         nt[e] = e < each && b < A.B ? tree_tiles<BK>(A, b, first, n, ctx) : 0;
         lists[e] = tree_lists(A, n);
         most = max(most, nt[e]);
+        tiles_here += lists[e] * nt[e];  // (at most kTreeCtas lists of 2^24 tiles: 32 bits hold the sum)
+        lists_here += lists[e];
     }
     auto count = [&](uint32_t per) {  // pieces of this lane's sequences
         const float rcp = __fdividef(1.f, (float)per);
@@ -176,7 +178,12 @@ __device__ __forceinline__ TreeRun tree_run_even(const AttnTreeArgs& A, int w) {
             if (e < each) c += lists[e] * tree_div_up(nt[e], per, rcp);
         return c;
     };
-    uint32_t lo = kTreeMinTiles, hi = __reduce_max_sync(0xffffffffu, most);  // (one piece per list always fits)
+    // at least tiles / W; and tiles / (W - lists) is enough, since rounding up adds less than a piece per list; and so is
+    // one piece per list
+    const uint32_t tiles_all = __reduce_add_sync(0xffffffffu, tiles_here), lists_all = __reduce_add_sync(0xffffffffu, lists_here);
+    uint32_t lo = max((uint32_t)kTreeMinTiles, (tiles_all + A.W - 1) / A.W), hi = __reduce_max_sync(0xffffffffu, most);
+    if (lists_all < (uint32_t)A.W) hi = min(hi, tiles_all / (A.W - lists_all) + 1);
+    hi = max(hi, lo);
     while (lo < hi) {
         const uint32_t per = (lo + hi) / 2;
         if (__reduce_add_sync(0xffffffffu, count(per)) <= (uint32_t)A.W)
