@@ -12,15 +12,15 @@
 // themselves).  While there is an SM for each list, lists are cut into equal pieces, one per worker (a CTA), as few as
 // balance allows; the row tiles of a kv-head are cut at the same places, so their reads of K and V come at the same time
 // and meet in L2.  With more lists they are laid end to end and cut into equal runs, whatever the mix of lengths.
-// Us, pieces against runs: 16 sequences of up to 8192 tokens, two row tiles of d = 128, 52 against 65; 4 of up to
-// 32768, six row tiles of d = 256, 92 against 189; one of 32768, one row tile, 38 against 39.
+// Us, pieces against runs: 16 sequences of up to 8192 tokens, two row tiles of d = 128, 50 against 61; 4 of up to
+// 32768, six row tiles of d = 256, 90 against 183; one of 32768, one row tile, 36 against 39.
 // A list that lies with one worker is finished by it; one that is cut leaves (maximum, sum, unnormalised O) per part
 // in the workspace and k_attn_tree_join joins the parts in order (no atomics: results do not change from call to call).
 //
-// Measured: 64 nodes over 4 x 32768 tokens (24 / 2 heads of 256) 91 us, 0.88 PFLOP/s, bound by the tensor cores and the
+// Measured: 64 nodes over 4 x 32768 tokens (24 / 2 heads of 256) 89 us, 0.90 PFLOP/s, bound by the tensor cores and the
 // hand-overs to them (1820 cycles per tile of 64 keys, 1410 of them products: 16 of N = 64 and 4 of N = 256); 16 nodes over 16 x
-// 8192 (16 / 4 heads of 256) 66 us, 4.6 TB/s, bound by HBM; a call of one list per SM is bound by latency (one tree of 8
-// nodes over 300 tokens: 12.5 us).
+// 8192 (16 / 4 heads of 256) 65 us, 4.7 TB/s, bound by HBM; a call of one list per SM is bound by latency (one tree of 8
+// nodes over 300 tokens: 12.1 us).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -37,9 +37,9 @@ namespace gdn {
 namespace {
 
 constexpr int kTreeCtas = 152;    // one CTA per SM
-constexpr int kTreeMinTiles = 2;  // fewest key tiles of a worker's run (us, 2 x 1000 tokens: 1 16.3, 2 15.5, 4 17.2, 8 19.5)
+constexpr int kTreeMinTiles = 2;  // fewest key tiles of a worker's run (us, 2 x 1000 tokens: 1 15.4, 2 14.8, 4 16.5, 8 19)
 // lists of up to this many tiles are not cut while every list has an SM: nothing to join then (us, whole against cut: 6
-// tiles 12.5 against 15.0, 9 tiles 15.7 against 15.9, 17 tiles 21.3 against 15.5)
+// tiles 12.1 against 13.5, 9 tiles 14.0 against 14.2, 17 tiles 20.2 against 14.8)
 constexpr int kTreeWhole = 8;
 
 struct AttnTreeArgs {
@@ -887,7 +887,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 // (few lists in many parts): four groups of threads take the parts in turn, 4 in flight at a time, and join their
 // results in order; a CTA has 8 columns.  GROUPS = 1 (many lists, few parts each): a thread takes all parts, and a CTA
 // has 32 columns.  Latency counts here, not bytes (the parts lie in L2).  The whole call in us, four groups against one:
-// 4 lists of 38 parts 38 against 56; 256 lists, 151 of them cut, 111 against 86.
+// 4 lists of 38 parts 36 against 46; 256 lists, 151 of them cut, 108 against 83.
 constexpr int kJoinThreads = 512;
 
 template <int D, int GROUPS>
