@@ -37,7 +37,7 @@ namespace gdn {
 namespace {
 
 constexpr int kTreeCtas = 152;    // one CTA per SM
-constexpr int kTreeMinTiles = 2;  // fewest key tiles of a worker's run (us, 2 x 1000 tokens: 1 15.4, 2 14.8, 4 16.5, 8 19)
+constexpr int kTreeMinTiles = 2;  // fewest key tiles of a worker's run (us, 2 x 1000 tokens: 1 15.4, 2 14.8; an earlier build 4 17.2 against 15.5)
 // lists of up to this many tiles are not cut while every list has an SM: nothing to join then (us, whole against cut: 6
 // tiles 12.1 against 13.5, 9 tiles 14.0 against 14.2, 17 tiles 20.2 against 14.8)
 constexpr int kTreeWhole = 8;
