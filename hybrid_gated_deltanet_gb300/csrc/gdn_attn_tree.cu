@@ -153,11 +153,10 @@ __device__ __forceinline__ uint32_t tree_div_up(uint32_t a, uint32_t per, float 
     return q;
 }
 
-// A.even: worker w takes piece w.  Every warp works it out by itself (there are at most kTreeCtas sequences, five to a
+// A.even: worker w takes piece w.  Every warp works it out by itself (there are at most kTreeCtas sequences, PER to a
 // lane): loads of one latency, then a bisection for the shortest pieces of which there are at most W
-template <int BK>
+template <int BK, int PER>
 __device__ __forceinline__ TreeRun tree_run_even(const AttnTreeArgs& A, int w) {
-    constexpr int PER = (kTreeCtas + 31) / 32;
     const int lane = threadIdx.x & 31, each = (A.B + 31) / 32;
     uint32_t nt[PER], lists[PER], most = kTreeMinTiles, tiles_here = 0, lists_here = 0;
 #pragma unroll
@@ -252,7 +251,8 @@ __device__ __forceinline__ TreeRun tree_run(const AttnTreeArgs& A, int w) {
         run.first = run.last = w;
         return run;
     }
-    if (A.even) return tree_run_even<BK>(A, w);
+    // (run once, the code costs its fetch: the short form is a fifth of the other)
+    if (A.even) return A.B <= 32 ? tree_run_even<BK, 1>(A, w) : tree_run_even<BK, (kTreeCtas + 31) / 32>(A, w);
     // each thread sums some sequences; a scan of the threads' sums finds the one that holds the start
     const int each = (A.B + THREADS - 1) / THREADS;
     const int b0 = min(A.B, tid * each), b1 = min(A.B, b0 + each);

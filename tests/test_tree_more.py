@@ -107,6 +107,16 @@ def test_attention_of_more_lists_than_sms(D, page):
     c.check(c.call(), sample=2)
 
 
+def test_attention_of_many_sequences_in_pieces():
+    """More than 32 sequences, fewer lists than SMs: pieces of equal length, some sequences skipped or short."""
+    r = np.random.default_rng(10)
+    seqs = [(int(r.integers(0, 1500)) if i % 5 else int(r.integers(0, 40)), int(r.integers(0, 20))) for i in range(70)]
+    c = test_tree_attn.Case(8, 2, 128, 16, seqs, 44)
+    c.check(c.call(), sample=2)
+    c = test_tree_attn.Case(4, 1, 256, 32, seqs[:40], 45)
+    c.check(c.call(), sample=2)
+
+
 def past_4gb(small, rows):
     """The rows of `small` as the last ones of a tensor of more than 4 GB, and the first one's place."""
     n = (1 << 32) // (small[0].numel() * small.element_size()) + rows + 3
