@@ -17,7 +17,7 @@
 // A list that lies with one worker is finished by it; one that is cut leaves (maximum, sum, unnormalised O) per part
 // in the workspace and k_attn_tree_join joins the parts in order (no atomics: results do not change from call to call).
 //
-// Measured: 64 nodes over 4 x 32768 tokens (24 / 2 heads of 256) 89 us, 0.90 PFLOP/s, bound by the tensor cores and the
+// Measured: 64 nodes over 4 x 32768 tokens (24 / 2 heads of 256) 88 us, 0.90 PFLOP/s, bound by the tensor cores and the
 // hand-overs to them (1820 cycles per tile of 64 keys, 1410 of them products: 16 of N = 64 and 4 of N = 256); 16 nodes over 16 x
 // 8192 (16 / 4 heads of 256) 65 us, 4.7 TB/s, bound by HBM; a call of one list per SM is bound by latency (one tree of 8
 // nodes over 300 tokens: 12.1 us).
