@@ -543,8 +543,8 @@ __device__ __forceinline__ void vt_taps(const uint2 (&u)[NODES][4], const uint2*
 #pragma unroll
     for (int e = 0; e < NODES; ++e)
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-            y[e][c] = bias ? vt_two(reinterpret_cast<const uint32_t*>(bias)[c]) : make_float2(0.f, 0.f);
+        for (int c = 0; c < 2; ++c)  // (a bias may start at any element: no wider loads)
+            y[e][c] = bias ? make_float2(__bfloat162float(bias[2 * c]), __bfloat162float(bias[2 * c + 1])) : make_float2(0.f, 0.f);
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
         if (m < 4 - K) continue;  // a tap that d_conv < 4 does not have
