@@ -255,12 +255,13 @@ __device__ __forceinline__ void conv_weights4x2(const __nv_bfloat16* src, int K,
     }
 }
 
+// (a bias may start at any element: no wider loads)
 __device__ __forceinline__ void bias4x2(const LayerParams& p, int ch, float2 b[2]) {
     b[0] = b[1] = make_float2(0.f, 0.f);
     if (p.conv_b) {
-        const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.conv_b) + ch);
-        b[0] = bf2_to_f2(u.x);
-        b[1] = bf2_to_f2(u.y);
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.conv_b) + ch;
+        b[0] = make_float2(__bfloat162float(src[0]), __bfloat162float(src[1]));
+        b[1] = make_float2(__bfloat162float(src[2]), __bfloat162float(src[3]));
     }
 }
 

@@ -190,38 +190,6 @@ __device__ __forceinline__ void conv_tokens(const uint4 rows[NT + 3], const floa
     }
 }
 
-// conv weights and bias of 8 consecutive channels (ch a multiple of 8) as
-// window-row weights: w[r][c] multiplies row tau-3+r; tap m of the K taps
-// multiplies row tau-(K-1)+m, i.e. window row r = 4-K+m.  The 8 K weights are
-// contiguous ([C_ch][K] bf16, 16-byte aligned): K vector loads.
-__device__ __forceinline__ void conv_weights8(const LayerParams& p, int K, bool raw, int ch, float w[4][8],
-                                              float bias[8]) {
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        bias[c] = 0.f;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) w[r][c] = 0.f;
-    }
-    if (raw) return;
-    if (p.conv_b) unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.conv_b) + ch), bias);
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.conv_w) + (size_t)ch * K);
-    // element e = c KK + m of the 8 KK values is channel c's tap m (register indices
-    // resolved at compile time for each d_conv)
-    auto unpack_taps = [&](auto kk) {
-        constexpr int KK = decltype(kk)::value;
-        float f[8 * KK];
-#pragma unroll
-        for (int v = 0; v < KK; ++v) unpack8(src[v], f + 8 * v);
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-#pragma unroll
-            for (int m = 0; m < KK; ++m) w[4 - KK + m][c] = f[c * KK + m];
-    };
-    if (K == 4) unpack_taps(std::integral_constant<int, 4>{});
-    else if (K == 3) unpack_taps(std::integral_constant<int, 3>{});
-    else unpack_taps(std::integral_constant<int, 2>{});
-}
-
 // ---- the UT transform: T = (I + A)^-1 of a strictly lower 64 x 64 A ----------
 __device__ __forceinline__ uint32_t tf32_bits(float x) {
     uint32_t r;
