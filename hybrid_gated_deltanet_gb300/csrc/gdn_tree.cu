@@ -88,11 +88,24 @@ __device__ __forceinline__ float tree_silu(float x) {
     return x * r;
 }
 
+// The sum of log alpha along a line, as a pair of floats s + lo: lo takes what the rounding of s leaves out.  The decay between a
+// node and an ancestor is the exponential of the difference of two such sums, and after strong decays a single float would have
+// few digits left for the weak ones that follow (eight nodes of -128, then gates of -0.005: 1e-4 of the decay).
+__device__ __forceinline__ void tree_add(float& s, float& lo, float x) {
+    const float t = s + x, b = t - s;
+    lo += (s - (t - b)) + (x - b);
+    s = t;
+}
+// A gate as a term of these sums.  An alpha of e^-1000 is 0 in fp32, as one of e^-inf is, and so is every decay across it; but the
+// sums stay finite, and nodes below it differ by what comes after it
+constexpr float kTreeErased = -1000.f;
+__device__ __forceinline__ float tree_gate(float g) { return g < kTreeErased ? kTreeErased : g; }  // (NaN stays)
+
 // entries of a tree's nodes: a node's proper ancestors, rounded up to groups of 4
 __host__ __device__ inline int tree_entries(int n) { return n * (n - 1) / 2 + 3 * n; }
 
 struct TreeSmem {
-    int k, q, u, p, r, w, ent, node, anc, up, off, taps, total;
+    int k, q, u, p, r, w, ent, node, lo, anc, up, off, taps, total;
 };
 
 __host__ __device__ inline TreeSmem tree_smem(int D, int n) {
@@ -108,6 +121,7 @@ __host__ __device__ inline TreeSmem tree_smem(int D, int n) {
     if (n < 8) o += (8 - n) * 2 * D * 4;          // (15 rows in p's and r's place)
     s.ent = o; o += tree_entries(n) * 16;         // per (node, proper ancestor): two coefficients and the ancestor
     s.node = o; o += n * 16;                      // beta, G, e^G, q_i . k_i
+    s.lo = o; o = (o + n * 4 + 7) & ~7;           // G's lower part
     s.anc = o; o += n * 8;                        // ancestors and the node itself, one bit each
     s.up = o; o += n * 4;                         // parent within the tree, -1: the cached state
     s.off = o; o = round(o + (n + 1) * 4);        // first entry of each node
@@ -152,6 +166,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) k_tree_verify(const __grid_co
     float* ws = reinterpret_cast<float*>(smem + lay.w);
     float4* ent = reinterpret_cast<float4*>(smem + lay.ent);
     float4* nd = reinterpret_cast<float4*>(smem + lay.node);
+    float* lo = reinterpret_cast<float*>(smem + lay.lo);
     unsigned long long* anc = reinterpret_cast<unsigned long long*>(smem + lay.anc);
     int* up = reinterpret_cast<int*>(smem + lay.up);
     int* off = reinterpret_cast<int*>(smem + lay.off);
@@ -167,7 +182,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) k_tree_verify(const __grid_co
         up[tid] = p >= 0 && p < tid ? p : -1;
         gates(L::ld(J.a, (first + tid) * Hv + j), L::ld(J.b, (first + tid) * Hv + j), direct ? 0.f : A.p.A_log[j],
               !direct && A.p.dt_bias ? A.p.dt_bias[j] : 0.f, direct, gl, beta);
-        nd[tid] = make_float4(beta, gl, 0.f, 0.f);
+        nd[tid] = make_float4(beta, tree_gate(gl), 0.f, 0.f);
     }
     auto channel = [&](int kind) { return (kind == 0 ? h : (kind == 1 ? Hk + h : 2 * Hk + j)) * D; };
     if (!raw) {
@@ -182,14 +197,15 @@ __global__ void __launch_bounds__(kTreeThreads, 2) k_tree_verify(const __grid_co
         }
     }
     __syncthreads();
-    float G = 0.f;
+    float G = 0.f, Glo = 0.f;
     if (tid < n) {  // the node's line, and the decay along it
         unsigned long long m = 0;
         for (int i = tid; i >= 0; i = up[i]) {
             m |= 1ull << i;
-            G += nd[i].y;
+            tree_add(G, Glo, nd[i].y);
         }
         anc[tid] = m;
+        lo[tid] = Glo;
     } else if (tid >= 128 && tid - 128 < n) {
         // its conv taps: the last is the node, then its ancestors, then the conv state, newest first
         const int i = tid - 128;
@@ -201,7 +217,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) k_tree_verify(const __grid_co
         }
     }
     __syncthreads();
-    if (tid < n) nd[tid] = make_float4(beta, G, expf(G), 0.f);
+    if (tid < n) nd[tid] = make_float4(beta, G, expf(G + Glo), 0.f);
     if (warp == nwarp - 1) {  // entries before each node
         int base = 0;
         for (int i0 = 0; i0 < n; i0 += 32) {
@@ -319,7 +335,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2) k_tree_verify(const __grid_co
                 if (a == i) {
                     nd[i].w = q1;
                 } else {
-                    const float f = expf(me.y - nd[a].y);
+                    const float f = expf((me.y - nd[a].y) + (lo[i] - lo[a]));
                     ent[start + at + grp] = make_float4(me.x * f * t, f * q1, __int_as_float(a * D), 0.f);
                 }
             }
