@@ -456,7 +456,7 @@ constexpr int kVtRows = 4;       // warps 0 .. 3 have the state rows: TMEM lanes
 constexpr int kVtAtom = 16384;   // 128 state rows x 32 columns
 
 struct VtSmem {
-    int S, B, A, P, v, w, own, taps, gate, beta, eg, line, up, bad, bar, total;
+    int S, B, A, P, v, w, own, taps, gate, lo, beta, eg, line, up, bad, bar, total;
 };
 
 __host__ __device__ inline VtSmem vt_smem(int nm, int gv) {  // nm: nodes, rounded up to 16
@@ -472,6 +472,7 @@ __host__ __device__ inline VtSmem vt_smem(int nm, int gv) {  // nm: nodes, round
     s.own = o; o += nm * 4;                          // q_i . k_i
     s.taps = o; o += nm * 16;                        // rows of the conv taps: K - 1 rows of the conv state, then the nodes
     s.gate = o; o += nm * gv * 4;                    // [v-head][node]: log2 alpha, then its sum G along the line
+    s.lo = o; o += nm * gv * 4;                      // G's lower part
     s.beta = o; o += nm * gv * 4;
     s.eg = o; o += nm * gv * 4;                      // 2^G
     s.line = o; o += nm * 8;
@@ -814,6 +815,7 @@ __global__ void __launch_bounds__(kVtThreads, CTAS)
     float* own = reinterpret_cast<float*>(sm + lay.own);
     int4* taps = reinterpret_cast<int4*>(sm + lay.taps);
     float* gate = reinterpret_cast<float*>(sm + lay.gate);
+    float* glo = reinterpret_cast<float*>(sm + lay.lo);
     float* betas = reinterpret_cast<float*>(sm + lay.beta);
     float* eg = reinterpret_cast<float*>(sm + lay.eg);
     unsigned long long* line = reinterpret_cast<unsigned long long*>(sm + lay.line);
@@ -920,7 +922,7 @@ __global__ void __launch_bounds__(kVtThreads, CTAS)
             gates(__bfloat162float(static_cast<const bf*>(J.a)[at]), __bfloat162float(static_cast<const bf*>(J.b)[at]),
                   A.p.A_log[j0 + jj], A.p.dt_bias ? A.p.dt_bias[j0 + jj] : 0.f, false, la, be);
         }
-        gate[i] = la * 1.4426950408889634f;
+        gate[i] = tree_gate(la) * 1.4426950408889634f;
         betas[i] = be;
     }
     tc::fence_before();
@@ -944,12 +946,12 @@ __global__ void __launch_bounds__(kVtThreads, CTAS)
         for (int at = i; at >= 0; at = up[at]) m |= 1ull << at;
         line[i] = m;
     }
-    float sum[2] = {0.f, 0.f};  // (two (node, v-head) pairs to a thread at most: the launch sees to it)
+    float sum[2] = {0.f, 0.f}, sum_lo[2] = {0.f, 0.f};  // (two (node, v-head) pairs to a thread at most: the launch sees to it)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int i = tid + e * kVtThreads, base = i / nm * nm;
         if (i < nm * gv)
-            for (int at = i - base; at >= 0; at = up[at]) sum[e] += gate[base + at];
+            for (int at = i - base; at >= 0; at = up[at]) tree_add(sum[e], sum_lo[e], gate[base + at]);
     }
     if (tid >= kVtThreads - 64 && tid - (kVtThreads - 64) < n) {
         const int i = tid - (kVtThreads - 64);
@@ -969,7 +971,8 @@ __global__ void __launch_bounds__(kVtThreads, CTAS)
         const int i = tid + e * kVtThreads;
         if (i < nm * gv) {
             gate[i] = sum[e];
-            eg[i] = tree_ex2(sum[e]);
+            glo[i] = sum_lo[e];
+            eg[i] = tree_ex2(sum[e] + sum_lo[e]);
         }
     }
     bool ok = true;
@@ -1092,7 +1095,7 @@ __global__ void __launch_bounds__(kVtThreads, CTAS)
                 const bool in = row < 2 * nm;
                 const unsigned long long mine = in ? line[i] & ~(is_q ? 0ull : 1ull << i) : 0ull;
                 const int ig = i0 * nm + (in ? i : 0);
-                const float gi[2] = {gate[ig], gate[ig + (two - 1) * nm]};
+                const float gi[2] = {gate[ig], gate[ig + (two - 1) * nm]}, li[2] = {glo[ig], glo[ig + (two - 1) * nm]};
                 const float diag = is_q && in && i < n ? own[i] : 0.f;
                 const float fi[2] = {is_q ? 1.f : betas[ig], is_q ? 1.f : betas[ig + (two - 1) * nm]};
                 unsigned char* to = sm + (is_q ? lay.P : lay.A);
@@ -1109,12 +1112,14 @@ __global__ void __launch_bounds__(kVtThreads, CTAS)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         if (e == two) break;
-                        float x[8], gc[8];
+                        float x[8], gc[8], lc[8];
                         *reinterpret_cast<float4*>(gc) = *reinterpret_cast<const float4*>(gate + (i0 + e) * nm + c0);
                         *reinterpret_cast<float4*>(gc + 4) = *reinterpret_cast<const float4*>(gate + (i0 + e) * nm + c0 + 4);
+                        *reinterpret_cast<float4*>(lc) = *reinterpret_cast<const float4*>(glo + (i0 + e) * nm + c0);
+                        *reinterpret_cast<float4*>(lc + 4) = *reinterpret_cast<const float4*>(glo + (i0 + e) * nm + c0 + 4);
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
-                            x[c] = (m8 >> c) & 1u ? tree_ex2(gi[e] - gc[c]) * p8[c] * fi[e] : 0.f;
+                            x[c] = (m8 >> c) & 1u ? tree_ex2((gi[e] - gc[c]) + (li[e] - lc[c])) * p8[c] * fi[e] : 0.f;
                             odd = fmaf(x[c], 0.f, odd);
                             if (is_q) x[c] = tc::to_tf32_rn(x[c]);
                         }

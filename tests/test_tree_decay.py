@@ -16,7 +16,7 @@ from gdn_cases import dev, host, oracle_kwargs, params_dev
 pytestmark = pytest.mark.gpu
 
 GEOMS = [synth.Geometry(2, 4, 128, 128, 4), synth.Geometry(1, 3, 64, 64, 4)]
-FORMS = [(GEOMS[0], synth.F32), (GEOMS[1], synth.F32), (GEOMS[1], synth.BF16)]
+FORMS = [(g, a) for g in GEOMS for a in (synth.BF16, synth.F32)]
 
 
 class Case(test_tree_gdn.Case):
@@ -79,3 +79,12 @@ def test_erased_states_with_direct_gates(act, geom, shape, lowest):
     paths = [list(range(0, 25)), [0, 2, 3]]
     test_tree_gdn.commit(c, paths)
     test_tree_gdn.check_commit(c, paths)
+
+
+def test_decays_of_many_v_heads_in_a_cta():
+    """bf16, d = 128, all 5 v-heads of a k-head in one CTA, each with decays of its own."""
+    c = Case([40, 20] + [3] * 160, synth.Geometry(1, 5, 128, 128, 4), synth.BF16, 85)
+    a = np.full((c.N, 5), -14.0)
+    a[:8, 0], a[3:6, 1], a[40:50, 2], a[:, 3], a[5, 4] = 8.0, 8.0, 8.0, 1.0, 12.0
+    c.gates(a, np.asarray([10.0, 10.0, 10.0, 0.0, 90.0]))
+    c.check(c.verify(), sample=4)
