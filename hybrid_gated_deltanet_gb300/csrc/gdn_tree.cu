@@ -434,8 +434,11 @@ __global__ void __launch_bounds__(kTreeThreads, 2) k_tree_verify(const __grid_co
 // One CTA per (k-head, tree).  With p_j = S_0 k_j, r_j = S_0 q_j and w_j = beta_j (v_j - e^{G_j} p_j), the sums above are
 //   u = T w,   o_i = e^{G_i} r_i + sum_j P_ij u_j,   T = (I + A)^-1,
 // with A (keys: beta_i e^{G_i - G_j} k_i . k_j, j a proper ancestor) and P (queries: e^{G_i - G_j} q_i . k_j, j = i too) of
-// n x n per v-head and the same for all 128 state rows.  So (all products TF32, fp32 accumulation):
-//   [K^; Q^] K^T    M = 128, N = nm, once: the products of the nodes' keys and queries with keys;
+// n x n per v-head and the same for all 128 state rows.  So (products TF32, fp32 accumulation):
+//   [K^; Q^] K^T    M = 128, N = nm, once: the products of the nodes' keys and queries with keys.  These are made to 2^-20 of
+//                   |q| |k| (what TF32 leaves out of the factors, times the values, is added by bf16 products): one of them may
+//                   be all of a node's output, the norm divides by its size, and of a small one TF32's 2^-11 of
+//                   |q| |k| would be much (y off by 20% where |q . k| is 1.5e-4 of it);
 //   S_0 [K^; Q^]^T  per v-head, M = 128 state rows, N = 2 nm, S_0 as it lies in the pool (fp32, brought by tensor
 //                   TMA 32 columns at a time; the tensor core reads its leading 10 fraction bits, as it does of K^ and
 //                   Q^ rounded): p and r in TMEM;
@@ -456,10 +459,13 @@ constexpr int kVtRows = 4;       // warps 0 .. 3 have the state rows: TMEM lanes
 constexpr int kVtAtom = 16384;   // 128 state rows x 32 columns
 
 struct VtSmem {
-    int S, B, A, P, v, w, own, taps, gate, lo, beta, eg, line, up, bad, bar, total;
+    int S, B, L, A, P, v, w, taps, gate, lo, beta, eg, line, up, bad, bar, total;
 };
 
-__host__ __device__ inline VtSmem vt_smem(int nm, int gv) {  // nm: nodes, rounded up to 16
+// atoms of the ring that are free from the start: L has the others' place until the Gram product is done
+__host__ __device__ inline int vt_early(int nm, int apart) { return apart || nm > 32 ? 2 : (nm > 16 ? 0 : 1); }
+
+__host__ __device__ inline VtSmem vt_smem(int nm, int gv, int apart) {  // nm: nodes, rounded up to 16; apart: L has a place of its own
     const int two = gv > 1 ? 2 : 1;  // v-heads are taken two at a time
     VtSmem s;
     int o = 0;
@@ -468,8 +474,10 @@ __host__ __device__ inline VtSmem vt_smem(int nm, int gv) {  // nm: nodes, round
     s.A = o; o += two * ((nm + 31) / 32) * nm * 128; // A, then T, of two v-heads: atoms of nm rows x 32 columns
     s.P = o; o += two * ((nm + 31) / 32) * nm * 128; // (at first, from A on: raw q and k of [K - 1 + n] rows)
     s.v = o; o += nm * 512;                          // v, then o: [node][row]
+    // what rounding [K^; Q^] left out, as B lies, until the Gram product has it: in the ring, or behind the raw q and k
+    s.L = apart ? o : (nm <= 32 ? s.S + vt_early(nm, 0) * kVtAtom : ((s.A + (nm + 3) * 512 + 1023) & ~1023));
+    if ((apart || nm > 32) && o < s.L + 2 * nm * 512) o = s.L + 2 * nm * 512;
     s.w = o; o += (2 + two) * 4 * 128 * 2;           // conv weights of k, q and two v-heads: [4 taps][128]
-    s.own = o; o += nm * 4;                          // q_i . k_i
     s.taps = o; o += nm * 16;                        // rows of the conv taps: K - 1 rows of the conv state, then the nodes
     s.gate = o; o += nm * gv * 4;                    // [v-head][node]: log2 alpha, then its sum G along the line
     s.lo = o; o += nm * gv * 4;                      // G's lower part
@@ -480,8 +488,9 @@ __host__ __device__ inline VtSmem vt_smem(int nm, int gv) {  // nm: nodes, round
     s.bad = o; o += 5 * 8;                           // nodes with an infinite or NaN w, and u, per v-head of the pair; and
                                                      // whether A or P has one
     s.bar = o; o += 20 * 8;
-    // the Gram product reads 128 rows of each atom, whatever 2 nm is: all of them lie inside the allocation
-    s.total = o > s.B + 3 * 2 * nm * 128 + kVtAtom ? o : s.B + 3 * 2 * nm * 128 + kVtAtom;
+    // the Gram product reads 128 rows of each atom of B and L, whatever 2 nm is: all of them lie inside the allocation
+    const int end = (s.L > s.B ? s.L : s.B) + 3 * 2 * nm * 128 + kVtAtom;
+    s.total = o > end ? o : end;
     return s;
 }
 
@@ -490,6 +499,7 @@ struct VtArgs {
     LayerParams p;
     TreeJob job;
     int nm, gv;  // gv: v-heads per CTA (G, or 1 where that fills the card better)
+    int apart;   // L has a place of its own
 };
 
 __device__ __forceinline__ bool vt_elect() {
@@ -605,17 +615,31 @@ __device__ __noinline__ void vt_conv_v(const unsigned char* x, const unsigned ch
                 make_float4(y[e][0].x, y[e][0].y, y[e][1].x, y[e][1].y);
 }
 
+// Four values to row r of the operands: rounded to TF32 to `tile`, and to `low` in bf16, atoms of 64 columns, what that rounding
+// left out (the first two atoms) and the value (the other two)
+__device__ __forceinline__ void vt_split4(unsigned char* tile, unsigned char* low, int rows, int r, int k, const float (&x)[4]) {
+    float h[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = tc::to_tf32_rn(x[e]);
+    *reinterpret_cast<float4*>(tile + tc::sw_off(rows, r, k)) = make_float4(h[0], h[1], h[2], h[3]);
+    const __nv_bfloat162 pair[4] = {__floats2bfloat162_rn(x[0] - h[0], x[1] - h[1]), __floats2bfloat162_rn(x[2] - h[2], x[3] - h[3]),
+                                    __floats2bfloat162_rn(x[0], x[1]), __floats2bfloat162_rn(x[2], x[3])};
+    uint2 u[2];
+    memcpy(u, pair, sizeof u);
+    unsigned char* to = low + (k >> 6) * rows * 128 + tc::h_off(r, (k >> 3) & 7) + (k & 4) * 2;
+    *reinterpret_cast<uint2*>(to) = u[0];
+    *reinterpret_cast<uint2*>(to + 2 * rows * 128) = u[1];
+}
+
 // k, then q, at the same nodes: inputs in shared memory from `raw` on (conv state first; a row is k's 256 bytes, then
-// q's), L2-normalised to rows `node` and nm + node of [K^; Q^], q times `scale` too.  And own[node] = q . k as it was before
-// the operands' rounding: where the decays leave a node little but its own token, o is v times this number, the norm
-// divides by its size, and of a small one TF32's 2^-11 of |q| |k| would be much.
+// q's), L2-normalised to rows `node` and nm + node of [K^; Q^], q times `scale` too
 template <int NODES>
 __device__ __noinline__ void vt_conv_kq(uint32_t raw, const int4* taps, const uint2* w, const __nv_bfloat16* bias_k,
-                                        const __nv_bfloat16* bias_q, int K, int i0, int n, unsigned char* Bt, int nm, float scale,
-                                        float eps, float* own) {
+                                        const __nv_bfloat16* bias_q, int K, int i0, int n, unsigned char* Bt, unsigned char* Lt, int nm,
+                                        float scale, float eps) {
     const int lane = threadIdx.x & 31;
     float2 k[NODES][2], y[NODES][2];
-    float kk[NODES], qq[NODES], qk[NODES];
+    float kk[NODES], qq[NODES];
 #pragma unroll 1
     for (int what = 0; what < 2; ++what) {
         uint2 u[NODES][4];
@@ -641,10 +665,8 @@ __device__ __noinline__ void vt_conv_kq(uint32_t raw, const int4* taps, const ui
     for (int e = 0; e < NODES; ++e) {
         const float2 a = __ffma2_rn(k[e][0], k[e][0], __fmul2_rn(k[e][1], k[e][1]));
         const float2 b = __ffma2_rn(y[e][0], y[e][0], __fmul2_rn(y[e][1], y[e][1]));
-        const float2 c = __ffma2_rn(k[e][0], y[e][0], __fmul2_rn(k[e][1], y[e][1]));
         kk[e] = a.x + a.y;
         qq[e] = b.x + b.y;
-        qk[e] = c.x + c.y;
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
@@ -652,15 +674,15 @@ __device__ __noinline__ void vt_conv_kq(uint32_t raw, const int4* taps, const ui
         for (int e = 0; e < NODES; ++e) {
             kk[e] += __shfl_xor_sync(0xffffffffu, kk[e], off);
             qq[e] += __shfl_xor_sync(0xffffffffu, qq[e], off);
-            qk[e] += __shfl_xor_sync(0xffffffffu, qk[e], off);
         }
 #pragma unroll
     for (int e = 0; e < NODES; ++e) {
         if (i0 + e >= n) continue;
         const float fk = rsqrtf(kk[e] + eps), fq = scale * rsqrtf(qq[e] + eps);
-        tc::st_row4(Bt, 2 * nm, i0 + e, 4 * lane, k[e][0].x * fk, k[e][0].y * fk, k[e][1].x * fk, k[e][1].y * fk);
-        tc::st_row4(Bt, 2 * nm, nm + i0 + e, 4 * lane, y[e][0].x * fq, y[e][0].y * fq, y[e][1].x * fq, y[e][1].y * fq);
-        if (lane == 0) own[i0 + e] = qk[e] * fk * fq;
+        const float kv[4] = {k[e][0].x * fk, k[e][0].y * fk, k[e][1].x * fk, k[e][1].y * fk};
+        const float qv[4] = {y[e][0].x * fq, y[e][0].y * fq, y[e][1].x * fq, y[e][1].y * fq};
+        vt_split4(Bt, Lt, 2 * nm, i0 + e, 4 * lane, kv);
+        vt_split4(Bt, Lt, 2 * nm, nm + i0 + e, 4 * lane, qv);
     }
 }
 
@@ -809,10 +831,10 @@ __global__ void __launch_bounds__(kVtThreads, CTAS)
     const int Hk = g.Hk, Hv = g.Hv, K = g.K, Km1 = g.K - 1, C = g.C_ch;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = smem_raw + ((1024 - (tc::smem_addr(smem_raw) & 1023)) & 1023);
-    const VtSmem lay = vt_smem(nm, gv);
-    unsigned char* Bt = sm + lay.B;
+    const VtSmem lay = vt_smem(nm, gv, A.apart);
+    const int early = vt_early(nm, A.apart);
+    unsigned char *Bt = sm + lay.B, *Lt = sm + lay.L;
     bf* ws = reinterpret_cast<bf*>(sm + lay.w);
-    float* own = reinterpret_cast<float*>(sm + lay.own);
     int4* taps = reinterpret_cast<int4*>(sm + lay.taps);
     float* gate = reinterpret_cast<float*>(sm + lay.gate);
     float* glo = reinterpret_cast<float*>(sm + lay.lo);
@@ -934,11 +956,13 @@ __global__ void __launch_bounds__(kVtThreads, CTAS)
         mbar_arrive_expect_tx(full + (a & 1), kVtAtom);
         tma_tile_2d(sm + lay.S + (a & 1) * kVtAtom, &ts, (a & 3) * 32, (slot * Hv + j0 + (a >> 2)) * D, full + (a & 1));
     };
-    if (tid == 32 * kVtWorkers) {
-        load(0);
-        load(1);
-    }
+    if (tid == 32 * kVtWorkers)
+        for (int i = 0; i < early; ++i) load(i);
     __syncwarp();
+    if (early < 2) {  // the first v-head's state to L2
+        const float* S = J.state_pool + ((size_t)slot * Hv + j0) * D * D;
+        for (int i = tid; i < D * D / 32; i += kVtThreads) tree_prefetch(S + i * 32);
+    }
     // the line of every node and the sums of log2 alpha along it; the conv taps' rows: the last tap is the node, then its
     // ancestors, then the conv state's rows, newest first
     for (int i = tid; i < n; i += kVtThreads) {
@@ -994,7 +1018,7 @@ __global__ void __launch_bounds__(kVtThreads, CTAS)
     for (int i0 = 2 * warp; i0 < n; i0 += 2 * (kVtWorkers + 1))
         vt_conv_kq<2>(smem_u32(raw + 4 * lane), taps, reinterpret_cast<const uint2*>(ws),
                       bias ? bias + channel(0, 0) + 4 * lane : nullptr, bias ? bias + channel(1, 0) + 4 * lane : nullptr, K, i0, n, Bt,
-                      nm, g.q_scale, g.l2_eps, own);
+                      Lt, nm, g.q_scale, g.l2_eps);
     fence_proxy_async_smem();
     __syncthreads();  // [K^; Q^] is there
     if (warp == kVtWorkers) {
@@ -1007,18 +1031,27 @@ __global__ void __launch_bounds__(kVtThreads, CTAS)
 #pragma unroll 4
             for (int k = 0; k < 16; ++k)
                 vt_mma(tgram, db + (k >> 2) * bstep + (k & 3) * 2, db + (k >> 2) * bstep + (k & 3) * 2, id_n, k > 0);
+            // and what their rounding left out, times the values (bf16 is enough: 2^-9 of 2^-11), of either factor
+            constexpr uint32_t id_bf = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(128 >> 4) << 24);
+            const uint64_t dl = tc::sdesc(tc::smem_addr(Lt)), dx = dl + 2 * bstep;
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t at = (k >> 2) * bstep + (k & 3) * 2;
+                tc::mma_f16(tgram, dl + at, dx + at, id_bf | ((uint32_t)(nm >> 3) << 17), 1u);
+                tc::mma_f16(tgram, dx + at, dl + at, id_bf | ((uint32_t)(nm >> 3) << 17), 1u);
+            }
             tc::commit(bar_g);
         }
         __syncwarp();
         // whatever can go on does: a reload of the ring, an atom's product, u = w T^T or r += u P^T of a v-head
         auto ready = [&](uint64_t* bar, int phase) { return __all_sync(0xffffffffu, mbar_test(bar, (uint32_t)(phase & 1))); };
-        int loaded = 2, a = 0, fi = 0;
+        int loaded = early, a = 0, fi = 0;
         bool u_issued = false;
         long long since = clock64();
 #pragma unroll 1
         while (a < atoms || fi < gv) {
             bool moved = false;
-            if (loaded < atoms && loaded < a + 2 && ready(freed + (loaded & 1), (loaded - 2) >> 1)) {
+            if (loaded < atoms && loaded < a + 2 && (loaded < 2 ? ready(bar_g, 0) : ready(freed + (loaded & 1), (loaded - 2) >> 1))) {
                 if (lane == 0) load(loaded);
                 __syncwarp();
                 ++loaded;
@@ -1084,6 +1117,7 @@ __global__ void __launch_bounds__(kVtThreads, CTAS)
                 if (tid < 5) s_bad[tid] = 0ull;
                 named_bar_sync(1, 32 * kVtWorkers);
             }
+            if (nm > 32) wait(bar_g, 0);  // (L reaches into v's place)
             conv_v(i0);
             // A and P from the Gram matrix: thread = row (a node's key, or its query), 8 columns at a time by the warps
             // of the row's quarter
@@ -1096,7 +1130,6 @@ __global__ void __launch_bounds__(kVtThreads, CTAS)
                 const unsigned long long mine = in ? line[i] & ~(is_q ? 0ull : 1ull << i) : 0ull;
                 const int ig = i0 * nm + (in ? i : 0);
                 const float gi[2] = {gate[ig], gate[ig + (two - 1) * nm]}, li[2] = {glo[ig], glo[ig + (two - 1) * nm]};
-                const float diag = is_q && in && i < n ? own[i] : 0.f;
                 const float fi[2] = {is_q ? 1.f : betas[ig], is_q ? 1.f : betas[ig + (two - 1) * nm]};
                 unsigned char* to = sm + (is_q ? lay.P : lay.A);
                 float odd = 0.f;  // NaN from the first infinity or NaN on
@@ -1106,9 +1139,6 @@ __global__ void __launch_bounds__(kVtThreads, CTAS)
                     vt_ld8(tc::taddr(tgram, 32 * q4, c0), r);
                     tc::ld_wait();
                     const uint32_t m8 = (uint32_t)(mine >> c0) & 0xffu;
-                    float p8[8];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) p8[c] = c0 + c == i ? diag : __uint_as_float(r[c]);  // (A has no diagonal)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         if (e == two) break;
@@ -1119,7 +1149,7 @@ __global__ void __launch_bounds__(kVtThreads, CTAS)
                         *reinterpret_cast<float4*>(lc + 4) = *reinterpret_cast<const float4*>(glo + (i0 + e) * nm + c0 + 4);
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
-                            x[c] = (m8 >> c) & 1u ? tree_ex2((gi[e] - gc[c]) + (li[e] - lc[c])) * p8[c] * fi[e] : 0.f;
+                            x[c] = (m8 >> c) & 1u ? tree_ex2((gi[e] - gc[c]) + (li[e] - lc[c])) * __uint_as_float(r[c]) * fi[e] : 0.f;
                             odd = fmaf(x[c], 0.f, odd);
                             if (is_q) x[c] = tc::to_tf32_rn(x[c]);
                         }
@@ -1379,7 +1409,7 @@ cudaError_t launch_verify_ctas(const CUtensorMap& map, const VtArgs& A, cudaStre
     const cudaError_t e = raise_smem_limit(k_tree_verify_tc<CTAS>, 227 * 1024, smem_set);
     if (e != cudaSuccess) return e;
     return launch_pdl(k_tree_verify_tc<CTAS>, dim3((unsigned)(A.g.Hv / A.gv), (unsigned)A.job.B), dim3(kVtThreads),
-                      (size_t)vt_smem(A.nm, A.gv).total + 1024, st, map, A);
+                      (size_t)vt_smem(A.nm, A.gv, A.apart).total + 1024, st, map, A);
 }
 
 cudaError_t launch_verify_tc(const Geom& g, const LayerParams& p, const TreeJob& job, cudaStream_t st) {
@@ -1393,12 +1423,15 @@ cudaError_t launch_verify_tc(const Geom& g, const LayerParams& p, const TreeJob&
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    VtArgs A{g, p, job, (job.max_nodes + 15) / 16 * 16, g.G};
+    VtArgs A{g, p, job, (job.max_nodes + 15) / 16 * 16, g.G, 0};
     // Few trees: a CTA per v-head (us, 16 / 32 heads: one tree of 8 nodes 8.6 against 11.3, 8 of 16 nodes 12.0 against
     // 14.1).  From a CTA per SM on: all v-heads of a k-head, which share its conv and Gram matrix (16 of 16 nodes 18.2
     // against 21.8, 64 of 32 nodes 76 against 98), or as many as shared memory and two (node, v-head) pairs a thread allow
     if ((long)job.B * g.Hk < sm_count()) A.gv = 1;
-    while (vt_smem(A.nm, A.gv).total + 1024 > 227 * 1024 || A.nm * A.gv > 2 * kVtThreads || A.gv > 8 || A.g.G % A.gv) --A.gv;
+    while (vt_smem(A.nm, A.gv, 0).total + 1024 > 227 * 1024 || A.nm * A.gv > 2 * kVtThreads || A.gv > 8 || A.g.G % A.gv) --A.gv;
+    // L in a place of its own while all CTAs are resident all the same: the state is on its way from the start then
+    const long per_sm = ((long)job.B * (g.Hv / A.gv) + sm_count() - 1) / sm_count();
+    A.apart = A.nm <= 32 && per_sm <= 2 && per_sm * (vt_smem(A.nm, A.gv, 1).total + 2048) <= 228 * 1024;
     // Trees of up to 16 nodes leave shared memory for a third CTA on an SM: with fewer registers each, faster once more than
     // two have work (us, 16 / 32 heads: 64 trees of 8 nodes 45 against 51; one tree 8.9 against 8.7; trees of up to 32 nodes,
     // where shared memory holds two, 84 against 76)
