@@ -51,11 +51,11 @@ __device__ __forceinline__ Two block_scan(Two v, Two* warp_tot) {
 
 // last i in [0, n) with start[i] <= at (start is non-decreasing, start[0] <= at); of
 // equal starts the last, which is the one that is not empty
-__device__ __forceinline__ int owner_of(const int* start, int n, int at) {
+__device__ __forceinline__ int owner_of(const int* start, int n, unsigned at) {
     int lo = 0, hi = n - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (start[mid] <= at) lo = mid;
+        if ((unsigned)start[mid] <= at) lo = mid;
         else hi = mid - 1;
     }
     return lo;
@@ -127,15 +127,15 @@ __global__ void __launch_bounds__(kTabThreads) k_page_tables(const __grid_consta
         __syncthreads();
         asked = carry_s;
         const int row_end = s_row[kTabChunk], page_end = s_page[kTabChunk];
-        // the chunk's new pages
-        for (int k = used + blockIdx.x * kTabThreads + tid; k < page_end; k += gridDim.x * kTabThreads) {
+        // the chunk's new pages (counters without a sign: up to 2^31 - 1 of them, and a grid's stride more)
+        for (unsigned k = used + blockIdx.x * kTabThreads + tid; k < (unsigned)page_end; k += gridDim.x * kTabThreads) {
             const int i = owner_of(s_page, nb, k);
-            const long long col = ((long long)s_ctx[i] + J.page - 1) / J.page + (k - s_page[i]);
-            J.block_table[(size_t)(b0 + i) * J.max_pages + col] = J.free_pages[head + k];
+            const long long col = ((long long)s_ctx[i] + J.page - 1) / J.page + (int)(k - s_page[i]);
+            J.block_table[(size_t)(b0 + i) * J.max_pages + col] = J.free_pages[head + (int)k];
         }
         // the chunk's rows
-        for (int k = rows_done + blockIdx.x * kTabThreads + tid; k < row_end; k += gridDim.x * kTabThreads) {
-            const int i = owner_of(s_row, nb, k), at = k - s_row[i];
+        for (unsigned k = rows_done + blockIdx.x * kTabThreads + tid; k < (unsigned)row_end; k += gridDim.x * kTabThreads) {
+            const int i = owner_of(s_row, nb, k), at = (int)(k - s_row[i]);
             const unsigned pos = (unsigned)s_ctx[i] + (unsigned)at, page = (unsigned)J.page;
             const unsigned pc = pos / page, old = ((unsigned)s_ctx[i] + page - 1) / page;
             const int id = pc >= old ? J.free_pages[head + s_page[i] + (int)(pc - old)]
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kTabThreads) k_page_tables(const __grid_consta
         used = page_end;
         __syncthreads();  // the chunk's tables are read
     }
-    for (int k = rows_done + blockIdx.x * kTabThreads + tid; k < J.n_rows; k += gridDim.x * kTabThreads) {
+    for (unsigned k = rows_done + blockIdx.x * kTabThreads + tid; k < (unsigned)J.n_rows; k += gridDim.x * kTabThreads) {
         J.slot_map[k] = -1;
         if (J.src_rows) J.src_rows[k] = -1;
     }
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kAppThreads) k_append_rows(const __grid_consta
 
 cudaError_t launch_page_tables(const TablesJob& job, cudaStream_t st) {
     // about 2 rows a thread, at most one CTA per SM
-    const int64_t want = (job.n_rows + 2 * kTabThreads - 1) / (2 * kTabThreads);
+    const int64_t want = ((int64_t)job.n_rows + 2 * kTabThreads - 1) / (2 * kTabThreads);
     const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(want, sm_count()));
     return launch_pdl(k_page_tables, dim3(grid), dim3(kTabThreads), 0, st, job);
 }
