@@ -885,10 +885,12 @@ gdn_status gdn_page_tables(int32_t page_size, int32_t n_pages, const int32_t* ct
     GDN_REQUIRE_PTR_A(head_out, "head_out", 4u);
     if (head == head_out)
         return fail(GDN_ERR_RANGE, "head_out: found the address of head, required another (every block reads head)");
-    if ((path != nullptr) != (src_rows != nullptr) || (path != nullptr) != (cu_nodes != nullptr))
+    // (arrays without elements may have no address: path of no sequence, src_rows of no row)
+    const bool paths = path || src_rows || cu_nodes;
+    if (paths && (!cu_nodes || (!path && B > 0) || (!src_rows && n_rows > 0)))
         return fail(GDN_ERR_NULL, "path/cu_nodes/src_rows: found %p/%p/%p, required all three or none",
                     (const void*)path, (const void*)cu_nodes, (const void*)src_rows);
-    if (path) {
+    if (paths) {
         GDN_PTR_ALIGN(path, "path", 4u);
         GDN_PTR_ALIGN(cu_nodes, "cu_nodes", 4u);
         GDN_PTR_ALIGN(src_rows, "src_rows", 4u);

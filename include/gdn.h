@@ -532,9 +532,10 @@ gdn_status gdn_commit_tree(const gdn_config* cfg, const gdn_params* prm, const v
  *   is not refused for pages.  So a list that runs out refuses sequences from that
  *   one on, and no page is taken for them.
  *   path int32 [B][path_len], cu_nodes int32 [B+1], src_rows int32 [n_rows] (all
- *   or none): path[b][0 .. new-1] are the accepted nodes of b's tree in order, and
- *   src_rows[cu_rows[b] + i] = cu_nodes[b] + path[b][i], -1 where the node is outside the
- *   tree and past the last row.
+ *   or none; path may be NULL when B is 0, src_rows when n_rows is 0):
+ *   path[b][0 .. new-1] are the accepted nodes of b's tree in order, and
+ *   src_rows[cu_rows[b] + i] = cu_nodes[b] + path[b][i], -1 where the node is outside
+ *   the tree and past the last row.
  *   page_size here is any positive number; slot_map must be 8-byte aligned. */
 gdn_status gdn_page_tables(int32_t page_size, int32_t n_pages, const int32_t* ctx_lens,
                            const int32_t* new_lens, int32_t B, const int32_t* free_pages,

@@ -40,3 +40,16 @@ def test_as_many_pages_as_a_count_holds():
     assert torch.equal(table[0], ids) and bool((buf[:pad] == 7).all())
     for at in range(0, n, 1 << 28):
         assert torch.equal(slots[at:at + (1 << 28)], ids[at:at + (1 << 28)].long()), at
+
+
+@pytest.mark.parametrize("B,n_rows", [(0, 0), (0, 5), (3, 0)])
+def test_paths_of_nothing(B, n_rows):
+    """Paths given to a call without sequences, or without rows to list (torch's empty tensors have no address)."""
+    cu, out = i32([9] * (B + 1)), i32([9])
+    slots, src = torch.full((n_rows,), 9, dtype=torch.int64, device="cuda"), i32([9] * n_rows)
+    table = torch.full((B, 4), -1, dtype=torch.int32, device="cuda")
+    gb.gdn_page_tables(16, 8, i32([5] * B), i32([2] * B), i32([3, 1]), i32([1]), table, cu, slots, out,
+                       i32([[0, 1]] * B).view(B, 2), i32([3 * i for i in range(B + 1)]), src)
+    torch.cuda.synchronize()
+    assert cu.tolist() == [0] * (B + 1) and int(out) == 1 and bool((table == -1).all())
+    assert slots.tolist() == [-1] * n_rows and src.tolist() == [-1] * n_rows
