@@ -4,6 +4,9 @@ Each .cu translation unit compiles in parallel into ``_build/`` at the repo
 root; the objects link into ``hybrid_gated_deltanet_gb300/libgdn.so`` with the
 CUDA runtime linked statically.  ``gdn_marshal.cpp`` (checks of tensors, against torch's
 headers) becomes the extension module ``_marshal.so`` beside it.  Usage: ``python -m hybrid_gated_deltanet_gb300.build``.
+
+libgdn.so needs nvcc alone (``python hybrid_gated_deltanet_gb300/build.py`` where there is no torch): ``_marshal.so`` is left out where
+the headers for it are missing, and if its compilation fails, the error comes after libgdn.so is in its place.
 """
 from __future__ import annotations
 
@@ -14,6 +17,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -67,6 +71,18 @@ def _current(path: str) -> bool:
     return os.path.exists(path) and _built_here(path) and os.path.getmtime(path) >= _newest_input()
 
 
+def _marshal_missing() -> str:
+    """What _marshal.so cannot be compiled without and is not here ("" if nothing)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return "torch"
+    for header in (os.path.join(sysconfig.get_paths()["include"], "Python.h"),
+                   os.path.join(spec.submodule_search_locations[0], "include", "torch", "csrc", "Dtype.h")):
+        if not os.path.exists(header):
+            return header
+    return ""
+
+
 def _build_marshal():
     torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
     tmp = MARSHAL + f".tmp{os.getpid()}"
@@ -82,10 +98,24 @@ def _build_marshal():
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile and link libgdn.so and _marshal.so; skipped when both exist, were built for this
-    host's architecture and are newer than every source, header and this script."""
-    if not force and _current(LIB) and _current(MARSHAL):
-        return LIB
+    """Compile and link libgdn.so and _marshal.so, each unless it exists, was built for this host's
+    architecture and is newer than every source, header and this script."""
+    marshal, missing = None, ""
+    with ThreadPoolExecutor(1) as ex:
+        if force or not _current(MARSHAL):
+            missing = _marshal_missing()
+            if not missing:
+                marshal = ex.submit(_build_marshal)
+        if force or not _current(LIB):
+            _build_lib(verbose, ptxas_info)
+        if marshal:
+            marshal.result()
+    if missing and missing != "torch":
+        warnings.warn(f"_marshal.so is not built: {missing} not found; the calls of binding.py on trees and page tables need it")
+    return LIB
+
+
+def _build_lib(verbose: bool, ptxas_info: bool):
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
     extra = ["-Xptxas", "-v"] if ptxas_info else []
@@ -98,10 +128,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             raise RuntimeError(f"nvcc failed on {src}:\n{res.stdout}\n{res.stderr}")
         return obj, res.stderr
 
-    with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        marshal = ex.submit(_build_marshal)
+    with ThreadPoolExecutor(len(SOURCES)) as ex:
         results = list(ex.map(compile_one, SOURCES))
-        marshal.result()
     if verbose or ptxas_info:
         for _, log in results:
             if log:
@@ -112,7 +140,6 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
