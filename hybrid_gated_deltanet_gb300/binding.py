@@ -18,7 +18,6 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libgdn.so")
-MARSHAL_PATH = os.path.join(_PKG, "_marshal.so")
 
 BF16, F32 = 0, 1
 RAW_QKV, NO_L2NORM, GATES_DIRECT, NO_OUTNORM = 1, 2, 4, 8
@@ -409,15 +408,20 @@ def _explain(t, name, dtype, shape, device):
     raise ValueError(f"{name}: libgdn takes dense row-major tensors")
 
 
-def _ptr(*args):
-    """The address of a tensor that has this dtype, shape and device and is dense: (tensor, name, dtype, shape, device)."""
-    global _ptr
-    if not os.path.exists(MARSHAL_PATH):
-        raise RuntimeError(f"_marshal.so is not built ({MARSHAL_PATH}); run "
+def _load_marshal():
+    from . import build
+    if not build.marshal_fits():  # (loaded all the same it would read tensors by another torch's layout)
+        raise RuntimeError(f"_marshal.so is not built for this Python and torch ({build.MARSHAL}); run "
                            "`python -m hybrid_gated_deltanet_gb300.build`")
     from . import _marshal
     _marshal.explain(_explain)
-    _ptr = _marshal.ptr
+    return _marshal
+
+
+def _ptr(*args):
+    """The address of a tensor that has this dtype, shape and device and is dense: (tensor, name, dtype, shape, device)."""
+    global _ptr
+    _ptr = _load_marshal().ptr
     return _ptr(*args)
 
 

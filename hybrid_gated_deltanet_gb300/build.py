@@ -13,6 +13,7 @@ from __future__ import annotations
 import importlib.util
 import os
 import platform
+import re
 import shutil
 import subprocess
 import sys
@@ -26,6 +27,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
 MARSHAL = os.path.join(PKG, "_marshal.so")
+STAMP = os.path.join(PKG, "_marshal.stamp")  # the Python and torch that _marshal.so was compiled against
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["gdn_api.cu", "gdn_decode.cu", "gdn_prefill.cu", "gdn_chunk16.cu", "gdn_noalloc.cu", "gdn_proj.cu",
            "gdn_attn.cu", "gdn_attn_tree.cu", "gdn_tree.cu", "gdn_tables.cu"]
@@ -71,6 +73,25 @@ def _current(path: str) -> bool:
     return os.path.exists(path) and _built_here(path) and os.path.getmtime(path) >= _newest_input()
 
 
+def marshal_key() -> str:
+    """The Python and torch whose layouts _marshal.so relies on (read without importing torch; "" without one)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return ""
+    with open(os.path.join(spec.submodule_search_locations[0], "version.py")) as f:
+        version = re.search(r"^__version__\s*(?::[^=]*)?=\s*['\"](.+?)['\"]", f.read(), re.M)
+    return f"{sys.implementation.cache_tag} {sysconfig.get_platform()} torch {version.group(1)}"
+
+
+def marshal_fits() -> bool:
+    """_marshal.so is here and was compiled against the Python and torch that are here."""
+    try:
+        with open(STAMP) as f:
+            return os.path.exists(MARSHAL) and f.read() == marshal_key()
+    except OSError:
+        return False
+
+
 def _marshal_missing() -> str:
     """What _marshal.so cannot be compiled without and is not here ("" if nothing)."""
     spec = importlib.util.find_spec("torch")
@@ -94,15 +115,19 @@ def _build_marshal():
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed on {MARSHAL_SOURCE}:\n{res.stdout}\n{res.stderr}")
+    if os.path.exists(STAMP):  # (a stamp never stands beside a module that it is not of)
+        os.remove(STAMP)
     os.replace(tmp, MARSHAL)
+    with open(STAMP, "w") as f:
+        f.write(marshal_key())
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile and link libgdn.so and _marshal.so, each unless it exists, was built for this host's
-    architecture and is newer than every source, header and this script."""
+    architecture (_marshal.so: and Python and torch) and is newer than every source, header and this script."""
     marshal, missing = None, ""
     with ThreadPoolExecutor(1) as ex:
-        if force or not _current(MARSHAL):
+        if force or not _current(MARSHAL) or not marshal_fits():
             missing = _marshal_missing()
             if not missing:
                 marshal = ex.submit(_build_marshal)

@@ -3,7 +3,9 @@ cannot be."""
 import os
 
 import pytest
+import torch
 
+from hybrid_gated_deltanet_gb300 import binding as gb
 from hybrid_gated_deltanet_gb300 import build as gbuild
 
 
@@ -11,7 +13,7 @@ from hybrid_gated_deltanet_gb300 import build as gbuild
 def small(monkeypatch, tmp_path):
     """A build of one source into a folder of its own."""
     monkeypatch.setattr(gbuild, "SOURCES", ["gdn_tables.cu"])
-    for name, path in (("LIB", "libgdn.so"), ("MARSHAL", "_marshal.so"), ("BUILD", "_build")):
+    for name, path in (("LIB", "libgdn.so"), ("MARSHAL", "_marshal.so"), ("STAMP", "_marshal.stamp"), ("BUILD", "_build")):
         monkeypatch.setattr(gbuild, name, str(tmp_path / path))
     return tmp_path
 
@@ -34,3 +36,35 @@ def test_headers_that_are_missing(small, monkeypatch):
     before = os.path.getmtime(gbuild.LIB)
     monkeypatch.setattr(gbuild.importlib.util, "find_spec", lambda name: None)  # no torch: no one to use it, no warning
     assert gbuild.build() == gbuild.LIB and os.path.getmtime(gbuild.LIB) == before
+
+
+def test_the_module_of_another_torch_or_python(small, monkeypatch):
+    """A module compiled against another torch or Python, or with no word of which, is built again, and never loaded
+    by the binding."""
+    gbuild._build_lib(False, False)
+    built = []
+
+    def stands_in():
+        built.append(gbuild.marshal_key())
+        with open(gbuild.LIB, "rb") as lib, open(gbuild.MARSHAL, "wb") as f:
+            f.write(lib.read(64))
+        with open(gbuild.STAMP, "w") as f:
+            f.write(built[-1])
+
+    monkeypatch.setattr(gbuild, "_build_marshal", stands_in)
+    key = gbuild.marshal_key()
+    changes = [lambda: None, lambda: os.remove(gbuild.STAMP)]
+    changes += [lambda other=other: monkeypatch.setattr(gbuild, "marshal_key", lambda: other)
+                for other in (key + ".1", key.replace("cpython", "pypy"), key)]
+    for n, change in enumerate(changes):
+        change()
+        assert not gbuild.marshal_fits()
+        with pytest.raises(RuntimeError, match="_marshal.so is not built for this Python and torch"):
+            gb._load_marshal()
+        for _ in range(2):  # (the second finds it current)
+            gbuild.build()
+            assert gbuild.marshal_fits() and len(built) == n + 1 and built[-1] == gbuild.marshal_key()
+
+
+def test_the_stamp_names_torch_as_it_is_imported():
+    assert gbuild.marshal_key().endswith(f" torch {torch.__version__}")
