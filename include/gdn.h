@@ -49,8 +49,9 @@
  *   rows are left as they were).  Duplicate slots within one call race and
  *   give undefined results.
  * - Debug mode: with the environment variable GDN_DEBUG set (and not "0"),
- *   gdn_decode_step, gdn_verify_rows(_nosnap), gdn_commit_rows(_recompute) and
- *   gdn_varlen_prefill(_ckpt) first check their slot indices on the device
+ *   gdn_decode_step, gdn_verify_rows(_nosnap), gdn_commit_rows(_recompute),
+ *   gdn_commit_tree and gdn_varlen_prefill(_ckpt) first check their slot indices on
+ *   the device
  *   (slot_idx, and snap_idx where the call takes one, together): every index
  *   in [0, n_slots) and no index twice.  Unless the stream is being captured,
  *   the call waits for the check and returns GDN_ERR_RANGE naming the first
