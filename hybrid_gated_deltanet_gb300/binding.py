@@ -472,7 +472,7 @@ def gdn_attn_tree(cfg: AttnConfig, q, k_new, v_new, k_pool, v_pool, block_table,
     ws, ws_bytes = None, 0
     if workspace is not None:
         ws_bytes = workspace.nbytes
-        ws = _ptr(workspace, "workspace", torch.uint8, (ws_bytes,), dev)
+        ws = _ptr(workspace, "workspace", workspace.dtype, workspace.shape, dev)
     _call(load().gdn_attn_tree, dev, stream, ctypes.byref(cfg.c()), _ptr(q, "q", _bf16, rows, dev),
           _ptr(k_new, "k_new", _bf16, new, dev), _ptr(v_new, "v_new", _bf16, new, dev),
           _ptr(k_pool, "k_pool", _bf16, pool, dev), _ptr(v_pool, "v_pool", _bf16, pool, dev),
