@@ -397,7 +397,8 @@ GDN_TREE_MAX_NODES = 64
 # shapes, so a wrong one would be a wrong address), and the call runs with that device current.  These calls are
 # made once per layer and step, so the checks are native (_marshal.so); what does not fit comes back here.
 _bf16, _f32, _i32, _i64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
-_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# (None in a torch built without CUDA, which has no tensor that would come this far)
+_current_device, _raw_stream = (getattr(torch._C, f, None) for f in ("_cuda_getDevice", "_cuda_getCurrentRawStream"))
 
 
 def _explain(t, name, dtype, shape, device):

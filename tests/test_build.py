@@ -1,6 +1,8 @@
 """libgdn.so needs nvcc alone: it is built where _marshal.so, the module against torch's and Python's headers,
 cannot be."""
 import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -68,3 +70,12 @@ def test_the_module_of_another_torch_or_python(small, monkeypatch):
 
 def test_the_stamp_names_torch_as_it_is_imported():
     assert gbuild.marshal_key().endswith(f" torch {torch.__version__}")
+
+
+def test_import_under_a_torch_without_cuda():
+    """The package imports (its generators and the tests' oracle need no GPU) where torch was built without CUDA."""
+    code = ("import torch\nfor name in [n for n in dir(torch._C) if n.startswith('_cuda_')]: delattr(torch._C, name)\n"
+            "import hybrid_gated_deltanet_gb300 as g\nfrom hybrid_gated_deltanet_gb300 import synth\n"
+            "try:\n    g.gdn_page_tables(16, 4, *[torch.zeros(1, dtype=torch.int32)] * 4, torch.zeros(1, 1), *[torch.zeros(2)] * 3)\n"
+            "except ValueError as e:\n    assert 'required one CUDA device' in str(e)\nelse:\n    raise SystemExit('no error')\n")
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=gbuild.ROOT)
