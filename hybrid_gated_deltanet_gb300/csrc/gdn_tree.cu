@@ -1674,9 +1674,12 @@ cudaError_t launch_commit_t(const CommitArgs& A, cudaStream_t st) {
 
 cudaError_t launch_tree_verify(const Geom& g, const LayerParams& p, const TreeJob& job, cudaStream_t st) {
     if (job.B == 0 || job.n_nodes == 0) return cudaSuccess;
-    // (where the tensor cores' kernel serves it is the faster one: 64 trees of up to 32 nodes 76 us against 152 on the CUDA
-    // cores, one tree of 8 nodes 8.6 against 8.9)
-    if (g.D == 128 && g.act_bf16 && g.flags == 0) return launch_verify_tc(g, p, job, st);
+    // d = 128, bf16: on the tensor cores (us against the CUDA cores: 64 trees of up to 32 nodes 81, 155; one of 16 nodes
+    // 10.4, 14.5; of 12 10.5, 13.0; 16 of 8 16.0, 21.2), but for trees of up to 8 nodes while every (tree, v-head) has an SM: the
+    // phases are longer than the work then (one tree of 8 nodes 9.1 on the CUDA cores, 9.4; of 4 6.5, 9.3; of 1 5.1, 8.9;
+    // 4 trees of 8 9.1, 9.9)
+    const bool few = job.max_nodes <= 8 && (long)job.B * g.Hv <= sm_count();
+    if (g.D == 128 && g.act_bf16 && g.flags == 0 && !few) return launch_verify_tc(g, p, job, st);
     const TreeArgs A{g, p, job, job.max_nodes};
     GDN_BY_TYPE(launch_verify_t);
 }

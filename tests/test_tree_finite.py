@@ -26,3 +26,11 @@ def test_outputs_of_many_trees_are_finite(most):
     c = Case([int(v) for v in r.integers(0, most + 1, 200)], synth.Geometry(2, 6, 128, 128, 4), synth.BF16, 98)
     c.max_nodes = most
     c.check(c.verify(), sample=2, heads=[0, 5])
+
+
+@pytest.mark.parametrize("nodes", [[8], [1], [8, 3, 8, 0, 5], [9], [8] * 40])
+@pytest.mark.parametrize("shape", ["tree", "chain"])
+def test_few_small_trees(nodes, shape):
+    """bf16, d = 128: trees of up to 8 nodes on either side of the rule between the two forms of the kernel."""
+    c = Case(nodes, synth.Geometry(2, 4, 128, 128, 4), synth.BF16, 99, shape)
+    c.check(c.verify(), sample=4)
