@@ -17,10 +17,12 @@
 // A list that lies with one worker is finished by it; one that is cut leaves (maximum, sum, unnormalised O) per part
 // in the workspace and k_attn_tree_join joins the parts in order (no atomics: results do not change from call to call).
 //
-// Measured: 64 nodes over 4 x 32768 tokens (24 / 2 heads of 256) 88 us, 0.90 PFLOP/s, bound by the tensor cores and the
-// hand-overs to them (1820 cycles per tile of 64 keys, 1410 of them products: 16 of N = 64 and 4 of N = 256); 16 nodes over 16 x
-// 8192 (16 / 4 heads of 256) 65 us, 4.7 TB/s, bound by HBM; a call of one list per SM is bound by latency (one tree of 8
-// nodes over 300 tokens: 12.1 us).
+// Measured: 64 nodes over 4 x 32768 tokens (24 / 2 heads of 256) 88 us, 0.90 PFLOP/s: its longest piece has 74 tiles of 64 keys
+// (65.7 were equal shares) at 1820 cycles each, 1410 of them products (16 of N = 64 and 4 of N = 256), about 66 us, and the
+// rest is the start, the last tile's chain and the join; 24 nodes over 16 x 8192 (32 / 4 heads of 128) 50 us: the longest piece
+// has 32 tiles where equal shares had 23.3, each a chain of product, softmax and product (the tensor cores are 22% busy); 16
+// nodes over 16 x 8192 (16 / 4 heads of 256) 65 us, 4.7 TB/s, and over 64 x 2048 (runs: 256 lists) 88 us, 3.9 TB/s; a call of one
+// list per SM is bound by latency (one tree of 8 nodes over 300 tokens: 12.1 us).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -36,7 +38,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kTreeCtas = 152;    // one CTA per SM
+constexpr int kTreeCtas = 152;    // one CTA per SM (a constant: the workspace's size is known without a device)
 constexpr int kTreeMinTiles = 2;  // fewest key tiles of a worker's run (us, 2 x 1000 tokens: 1 15.4, 2 14.8; an earlier build 4 17.2 against 15.5)
 // lists of up to this many tiles are not cut while every list has an SM: nothing to join then (us, whole against cut: 6
 // tiles 12.1 against 13.5, 9 tiles 14.0 against 14.2, 17 tiles 20.2 against 14.8)

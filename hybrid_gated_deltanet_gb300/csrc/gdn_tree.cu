@@ -9,7 +9,7 @@
 //   u_i = beta_i (v_i - e^{G_i} S_0 k_i - sum_{j in anc(i), j != i} e^{G_i - G_j} (k_i . k_j) u_j)
 //   o_i = e^{G_i} S_0 q_i + sum_{j in anc(i)} e^{G_i - G_j} (q_i . k_j) u_j
 // (the WY form of a chunk with the tree's mask in the place of the causal one).  The state is read
-// once for all nodes, no state of a node is formed, and every exponent is <= 0.  This is the
+// once for all nodes, no state of a node is formed, and no exponent is positive.  This is the
 // verify without snapshots of "Forge: how I wrote my own inference engine and overtook llama.cpp"
 // (27 August) for drafts that branch.
 
@@ -448,10 +448,10 @@ __global__ void __launch_bounds__(kTreeThreads, 2) k_tree_verify(const __grid_co
 // substitution, a column to a lane; then T21 = -T22 A21 T11 for the blocks of 16 and of 32 below it.  TF32's 2^-11 per
 // operand is a quarter of the bf16 rounding of y; the decays, T's sums and the norms are fp32.
 // The phases are short, so that latency and instructions bound the kernel (64 trees of up to 32 nodes, 16 / 32 heads:
-// 76 us, 2.2 TB/s of the state's bytes; HBM is a third busy, the issue slots 40%).  Two CTAs share an SM up to 32 nodes:
-// the state's place in shared memory is half a tile for that.  Measured there: 16 warps a CTA 87 us, 12 warps 84, 8 warps
-// 76 (what a warp does once weighs more than its waiting); three CTAs an SM, with one v-head at a time and a quarter
-// tile, 74 us, but 83 against 78 at 16 trees of 64 nodes and 48 v-heads.
+// 81 us, 2.1 TB/s of the state's bytes; HBM is a quarter busy, the issue slots 39%).  Two CTAs share an SM up to 32 nodes:
+// the state's place in shared memory is half a tile for that.  Measured there, in an earlier build of 76 us: 16 warps a CTA
+// 87 us, 12 warps 84, 8 warps 76 (what a warp does once weighs more than its waiting); three CTAs an SM, with one v-head at a
+// time and a quarter tile, 74 us, but 83 against 78 at 16 trees of 64 nodes and 48 v-heads.
 constexpr int kVtWorkers = 7;    // and a warp that drives the copies and the products
 constexpr int kVtThreads = 32 * (kVtWorkers + 1);
 constexpr int kVtNorm = 2;       // nodes that a warp takes at a time in the norm
@@ -474,7 +474,8 @@ __host__ __device__ inline VtSmem vt_smem(int nm, int gv, int apart) {  // nm: n
     s.A = o; o += two * ((nm + 31) / 32) * nm * 128; // A, then T, of two v-heads: atoms of nm rows x 32 columns
     s.P = o; o += two * ((nm + 31) / 32) * nm * 128; // (at first, from A on: raw q and k of [K - 1 + n] rows)
     s.v = o; o += nm * 512;                          // v, then o: [node][row]
-    // what rounding [K^; Q^] left out, as B lies, until the Gram product has it: in the ring, or behind the raw q and k
+    // what rounding [K^; Q^] left out and [K^; Q^] itself, in bf16 (2 + 2 atoms of 2 nm rows x 64 columns), until the Gram product
+    // has them: in the ring, or behind the raw q and k
     s.L = apart ? o : (nm <= 32 ? s.S + vt_early(nm, 0) * kVtAtom : ((s.A + (nm + 3) * 512 + 1023) & ~1023));
     if ((apart || nm > 32) && o < s.L + 2 * nm * 512) o = s.L + 2 * nm * 512;
     s.w = o; o += (2 + two) * 4 * 128 * 2;           // conv weights of k, q and two v-heads: [4 taps][128]
@@ -1338,7 +1339,7 @@ __global__ void __launch_bounds__(kVtThreads, CTAS)
                     if (lane == 0) mbar_arrive(o_read + e);  // this v-head's columns are free
                 }
                 named_bar_sync(1, 32 * kVtWorkers);
-                                // gated RMSNorm, a warp per node, kVtNorm at once, four channels to a lane
+                // gated RMSNorm, a warp per node, kVtNorm at once, four channels to a lane
                 const uint2 nw = __ldg(reinterpret_cast<const uint2*>(A.p.norm_w) + lane);
                 const float2 w01 = vt_two(nw.x), w23 = vt_two(nw.y);
 #pragma unroll 1
@@ -1424,17 +1425,18 @@ cudaError_t launch_verify_tc(const Geom& g, const LayerParams& p, const TreeJob&
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
     VtArgs A{g, p, job, (job.max_nodes + 15) / 16 * 16, g.G, 0};
-    // Few trees: a CTA per v-head (us, 16 / 32 heads: one tree of 8 nodes 8.6 against 11.3, 8 of 16 nodes 12.0 against
-    // 14.1).  From a CTA per SM on: all v-heads of a k-head, which share its conv and Gram matrix (16 of 16 nodes 18.2
-    // against 21.8, 64 of 32 nodes 76 against 98), or as many as shared memory and two (node, v-head) pairs a thread allow
+    // Few trees: a CTA per v-head (us, 16 / 32 heads: one tree of 8 nodes 9.4 against 12.3, 8 of 16 nodes 12.5 against
+    // 14.1).  From a CTA per SM on: all v-heads of a k-head, which share its conv and Gram matrix (16 of 16 nodes 18.8
+    // against 22.4, 64 of 32 nodes 81 against 105), or as many as shared memory and two (node, v-head) pairs a thread allow
     if ((long)job.B * g.Hk < sm_count()) A.gv = 1;
     while (vt_smem(A.nm, A.gv, 0).total + 1024 > 227 * 1024 || A.nm * A.gv > 2 * kVtThreads || A.gv > 8 || A.g.G % A.gv) --A.gv;
-    // L in a place of its own while all CTAs are resident all the same: the state is on its way from the start then
+    // L in a place of its own while all CTAs are resident all the same: the state is on its way from the start then (us: 8 of 16
+    // nodes 12.5 against 13.2, 16 of 16 nodes 18.8 against 19.2)
     const long per_sm = ((long)job.B * (g.Hv / A.gv) + sm_count() - 1) / sm_count();
     A.apart = A.nm <= 32 && per_sm <= 2 && per_sm * (vt_smem(A.nm, A.gv, 1).total + 2048) <= 228 * 1024;
     // Trees of up to 16 nodes leave shared memory for a third CTA on an SM: with fewer registers each, faster once more than
-    // two have work (us, 16 / 32 heads: 64 trees of 8 nodes 45 against 51; one tree 8.9 against 8.7; trees of up to 32 nodes,
-    // where shared memory holds two, 84 against 76)
+    // two have work (us, 16 / 32 heads: 64 trees of 8 nodes 49 against 56; one tree 9.6 against 9.4; trees of up to 32 nodes,
+    // where shared memory holds two, 86 against 81)
     if (A.nm <= 16 && (long)job.B * (g.Hv / A.gv) > 2L * sm_count()) return launch_verify_ctas<3>(map, A, st);
     return launch_verify_ctas<2>(map, A, st);
 }
@@ -1443,8 +1445,9 @@ cudaError_t launch_verify_tc(const Geom& g, const LayerParams& p, const TreeJob&
 // One CTA per (v-head, sequence), a cluster per k-head.  A warp holds D / 8 state rows in registers
 // through all rows of the path (a state row's update touches no other row), 8 lanes to a row as in
 // k_tree_verify, so the state is read once and written once, and shared memory holds only
-// the inputs, k and v of a chunk of path rows at a time.  HBM-bound, two CTAs an SM.  The state is asked for last: the
-// short dependent loads of the inputs stand in line behind it otherwise, and the SM's other CTA keeps HBM busy meanwhile
+// the inputs, k and v of a chunk of path rows at a time.  Bound by DRAM latency at two CTAs an SM (HBM half busy).  The state
+// is asked for last: the short dependent loads of the inputs stand in line behind it otherwise, and the SM's other CTA keeps HBM
+// busy meanwhile
 // (64 sequences of up to 6 rows, 48 v-heads of 128 x 128: 86 us, 4.8 TB/s; 89 with the state asked for before k and v are
 // made, 96 before the inputs, 98 by a bulk copy at the start, 92 with a prefetch to L2 a wave ahead).
 // The G CTAs of a k-head read the same conv rows of k, which one of them replaces: the cluster barrier stands between.
@@ -1581,9 +1584,9 @@ __global__ void __launch_bounds__(kTreeThreads, 2) k_tree_commit(const __grid_co
         }
         if (t0 == 0) {
 #pragma unroll
-    for (int r = 0; r < RL; ++r)
+            for (int r = 0; r < RL; ++r)
 #pragma unroll
-        for (int c = 0; c < RL; ++c) S[r][c] = *reinterpret_cast<const float4*>(Sg + (size_t)r * 4 * D + 32 * c);
+                for (int c = 0; c < RL; ++c) S[r][c] = *reinterpret_cast<const float4*>(Sg + (size_t)r * 4 * D + 32 * c);
         }
         __syncthreads();
 #pragma unroll 1
@@ -1622,11 +1625,11 @@ __global__ void __launch_bounds__(kTreeThreads, 2) k_tree_commit(const __grid_co
             stage(t0 + kComRows);
         }
     }
-    // the new conv state: the last K - 1 raw inputs, bit for bit, from shared memory
 #pragma unroll
     for (int r = 0; r < RL; ++r)
 #pragma unroll
         for (int c = 0; c < RL; ++c) *reinterpret_cast<float4*>(Sg + (size_t)r * 4 * D + 32 * c) = S[r][c];
+    // the new conv state: the last K - 1 raw inputs, bit for bit, from shared memory
     cluster_wait_acquire();
     const int tail = (n - 1) % kComRows + 1;  // rows of the last chunk
     for (int c = tid; c < 3 * D; c += kTreeThreads) {

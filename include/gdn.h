@@ -34,9 +34,9 @@
  *   refuse with both numbers).
  * - Alignment (GDN_ERR_ALIGN otherwise): 16 bytes for the state pools, s0,
  *   s_final, the conv pools, conv_w, norm_w, the workspace, x and z, and
- *   the y of the prefill calls (these move with bulk or 128-bit copies);
- *   the element size (2 for bf16, 4 for fp32) for a, b, conv_b, dt_bias,
- *   A_log and the y of decode/verify; 4 bytes for int32 arrays.
+ *   the y of the prefill calls and of gdn_verify_tree (these move with bulk or
+ *   128-bit copies); the element size (2 for bf16, 4 for fp32) for a, b, conv_b,
+ *   dt_bias, A_log and the y of decode/verify; 4 bytes for int32 arrays.
  * - Layouts are row-major and dense.  "act" means the activation dtype of the
  *   config (bf16 or fp32).  Channel order of x is [q | k | v], head-major:
  *   q of k-head h at h*d_k, k at H_k*d_k + h*d_k, v of v-head j at
@@ -50,10 +50,9 @@
  *   give undefined results.
  * - Debug mode: with the environment variable GDN_DEBUG set (and not "0"),
  *   gdn_decode_step, gdn_verify_rows(_nosnap), gdn_commit_rows(_recompute),
- *   gdn_commit_tree and gdn_varlen_prefill(_ckpt) first check their slot indices on
- *   the device
- *   (slot_idx, and snap_idx where the call takes one, together): every index
- *   in [0, n_slots) and no index twice.  Unless the stream is being captured,
+ *   gdn_commit_tree and gdn_varlen_prefill(_ckpt) first check their slot indices
+ *   on the device (slot_idx, and snap_idx where the call takes one, together):
+ *   every index in [0, n_slots) and no index twice.  Unless the stream is being captured,
  *   the call waits for the check and returns GDN_ERR_RANGE naming the first
  *   offending position and value (the refusal convention above, Strata
  *   chapter 6, sections 6.2 and 6.5).  Under stream capture it cannot wait:
@@ -462,6 +461,9 @@ enum { GDN_TREE_MAX_NODES = 64 };
  *   host bound on every ctx_lens[b].  A sequence with ctx_lens[b] < 0, above
  *   max_ctx_len or above max_pages * page_size is skipped; cached tokens on pages
  *   outside [0, n_pages) are left out.
+ *   The work is split by these bounds, as capacities where the call is captured: bounds
+ *   close to the real sizes serve best (16 sequences of up to 8192 tokens and 24 nodes, 32 / 4
+ *   heads of 128: 50 us with them, 62 with max_nodes = 64).
  *   Cache rows past ctx_lens[b], and nodes outside a node's line, do not reach its
  *   output whatever they hold (NaN and infinities included).
  *   workspace: gdn_attn_tree_workspace_size bytes (NULL when 0); calls that may
@@ -488,7 +490,16 @@ size_t gdn_attn_tree_workspace_size(const gdn_attn_config* cfg, int32_t B, int32
  *   x act [n_nodes][C_ch], z, y act [n_nodes][H_v*d_v], a, b act [n_nodes][H_v];
  *   x, z and y 16-byte aligned; conv_pool, state_pool, slot_idx [B] as in gdn_verify_rows_nosnap
  *   (a tree whose slot index is out of range is skipped); max_nodes: host bound
- *   on every n_b, 1 .. GDN_TREE_MAX_NODES. */
+ *   on every n_b, 1 .. GDN_TREE_MAX_NODES.
+ *   Precision: fp32 arithmetic, as gdn_verify_rows_nosnap, with fp32 activations, d < 128, any
+ *   flag, or short trees (max_nodes <= 8 while B * n_v_heads is at most the GPU's
+ *   SMs).  Else (bf16, d = 128) the products are taken on the
+ *   tensor cores with fp32 sums: q^ . k^ and k^ . k^ of two nodes to 2^-20 of |q^| |k^|; the
+ *   others' operands are TF32, S_0 truncated (2^-10 of each element at most), q^, k^ and what
+ *   is made of them rounded (2^-11).  The error of y stays below that of its own bf16
+ *   rounding; but where S_0 q^ is much smaller than |S_0| |q^| in every row, it is good to 2^-10
+ *   of the latter only.  The decays are fp32 whatever the gates (a log alpha below -1000 counts as
+ *   -1000: alpha is 0 either way). */
 gdn_status gdn_verify_tree(const gdn_config* cfg, const gdn_params* prm, const void* x,
                            const void* z, const void* a, const void* b, const void* conv_pool,
                            const float* state_pool, const int32_t* slot_idx,
