@@ -117,6 +117,67 @@ class AttnConfig:
         return CAttnConfig(self.n_q_heads, self.n_kv_heads, self.head_dim, self.page_size, self.scale)
 
 
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+
+
+class CRopeConfig(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("act_dtype", ctypes.c_int32), ("theta", ctypes.c_float), ("factor", ctypes.c_float),
+                ("orig_len", ctypes.c_int32), ("beta_fast", ctypes.c_float), ("beta_slow", ctypes.c_float),
+                ("mscale", ctypes.c_float)]
+
+
+class CRopePlan(ctypes.Structure):
+    """A model's rotations (gdn_rope_plan): made once, given to every gdn_rope."""
+    _fields_ = [("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("act_dtype", ctypes.c_int32), ("mscale", ctypes.c_float), ("turns", ctypes.c_uint64 * 128)]
+
+
+@dataclasses.dataclass
+class RopeConfig:
+    head_dim: int
+    rotary_dim: int
+    theta: float = 10000.0
+    layout: int = ROPE_HALF
+    act_dtype: int = BF16
+    factor: float = 1.0
+    orig_len: int = 0
+    beta_fast: float = 32.0
+    beta_slow: float = 1.0
+    mscale: float = 0.0
+
+    def c(self) -> CRopeConfig:
+        return CRopeConfig(self.head_dim, self.rotary_dim, self.layout, self.act_dtype, self.theta, self.factor,
+                           self.orig_len, self.beta_fast, self.beta_slow, self.mscale)
+
+
+class CLora(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("n_adapters", ctypes.c_int32), ("rank", ctypes.c_int32)]
+
+
+@dataclasses.dataclass
+class Lora:
+    """Low-rank adapters of one projection: a bf16 [n_adapters, rank, k], b bf16 [n_adapters, n_out, rank],
+    scale fp32 [n_adapters] or None (1)."""
+    a: torch.Tensor
+    b: torch.Tensor
+    scale: Optional[torch.Tensor] = None
+
+
+class CFfn(ctypes.Structure):
+    _fields_ = [("w_gate", ctypes.c_void_p), ("w_up", ctypes.c_void_p), ("w_down", ctypes.c_void_p),
+                ("hidden", ctypes.c_int32), ("inter", ctypes.c_int32)]
+
+
+@dataclasses.dataclass
+class Ffn:
+    """Weights of a gated feed-forward block: w_gate, w_up bf16 [inter, hidden], w_down bf16 [hidden, inter]."""
+    w_gate: torch.Tensor
+    w_up: torch.Tensor
+    w_down: torch.Tensor
+
+
 def _p(t: Optional[torch.Tensor]):
     if t is None:
         return None
@@ -163,6 +224,12 @@ def load() -> ctypes.CDLL:
         sigs["gdn_commit_tree"] = [cfgp, prmp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp]
         sigs["gdn_page_tables"] = [i32, i32, vp, vp, i32, vp, i32, vp, vp, i32, vp, vp, i32, vp, vp, i32, vp, vp, vp]
         sigs["gdn_attn_append"] = [acfgp, vp, vp, i64, vp, vp, i64, vp, vp, i32, vp]
+        ropep, lorap, ffnp = (ctypes.POINTER(t) for t in (CRopePlan, CLora, CFfn))
+        sigs["gdn_rope_plan_init"] = [ctypes.POINTER(CRopeConfig), ropep]
+        sigs["gdn_rope"] = [ropep, vp, i64, vp, i64, i32, vp, i64, vp, i64, i32, vp, i64, vp]
+        sigs["gdn_proj_lora"] = [vp, vp, lorap, vp, vp, i32, vp, i64, i32, i32, i64, vp, sz, vp]
+        sigs["gdn_proj_gated"] = [vp, vp, vp, vp, i64, i32, i32, i64, vp]
+        sigs["gdn_ffn"] = [ffnp, vp, i64, vp, vp, sz, vp]
         for name, args in sigs.items():
             fn = getattr(lib, name)
             fn.argtypes = args
@@ -177,6 +244,10 @@ def load() -> ctypes.CDLL:
         lib.gdn_attn_workspace_size.restype = sz
         lib.gdn_attn_tree_workspace_size.argtypes = [acfgp, i32, i32, i32]
         lib.gdn_attn_tree_workspace_size.restype = sz
+        lib.gdn_proj_lora_workspace_size.argtypes = [i64, i32, i32, i32, i32]
+        lib.gdn_proj_lora_workspace_size.restype = sz
+        lib.gdn_ffn_workspace_size.argtypes = [i64, i32, i32]
+        lib.gdn_ffn_workspace_size.restype = sz
         lib.gdn_last_error.argtypes = []
         lib.gdn_last_error.restype = ctypes.c_char_p
         lib.gdn_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint32)]
@@ -549,3 +620,104 @@ def gdn_page_tables(page_size: int, n_pages: int, ctx_lens, new_lens, free_pages
           None if path is None else _ptr(path, "path", _i32, (B, path_len), dev), path_len,
           None if cu_nodes is None else _ptr(cu_nodes, "cu_nodes", _i32, (B + 1,), dev),
           None if src_rows is None else _ptr(src_rows, "src_rows", _i32, (n_rows,), dev))
+
+
+# ---- rotary positions, projections with adapters, the gated feed-forward block ------
+def gdn_rope_plan(cfg: RopeConfig) -> CRopePlan:
+    """The plan that gdn_rope takes, made once per model."""
+    plan = CRopePlan()
+    _check(load().gdn_rope_plan_init(ctypes.byref(cfg.c()), ctypes.byref(plan)))
+    return plan
+
+
+def _rows(t, name, dtype, n, head_dim, device):
+    """Address, elements between tokens and heads of [n, heads, head_dim] whose tokens may lie inside wider rows."""
+    if t.get_device() != device or t.dtype is not dtype or t.dim() != 3 or t.shape[0] != n or t.shape[2] != head_dim:
+        _explain(t, name, dtype, (n, t.shape[1] if t.dim() == 3 else -1, head_dim), device)
+    heads, (ld, per_head, one) = t.shape[1], t.stride()
+    if n <= 1 or heads == 0:
+        ld = heads * head_dim  # (a stride that is never taken)
+    if one != 1 or (heads > 1 and per_head != head_dim) or ld < heads * head_dim:
+        raise ValueError(f"{name}: found strides {t.stride()}, required dense heads, tokens at least "
+                         f"{heads * head_dim} elements apart")
+    return t.data_ptr(), ld, heads
+
+
+def gdn_rope(plan: CRopePlan, positions, q, k, q_out=None, k_out=None, stream=None):
+    """q [N, Hq, D] and k [N, Hkv, D] (either may be None; tokens may lie inside wider rows) rotated by positions int32 [N]
+    into q_out, k_out (None: in place)."""
+    dev, n = _device(positions, "positions"), positions.shape[0]
+    dtype, D = _bf16 if plan.act_dtype == BF16 else _f32, plan.head_dim
+    args = []
+    for name, x, out in (("q", q, q_out), ("k", k, k_out)):
+        if x is None:
+            if out is not None:
+                raise ValueError(f"{name}_out: found a tensor, required None without {name}")
+            args += [None, 0, 0, None, 0]
+            continue
+        p, ld, heads = _rows(x, name, dtype, n, D, dev)
+        if out is None:
+            args += [p, ld, heads, p, ld]
+            continue
+        po, ldo, heads_out = _rows(out, name + "_out", dtype, n, D, dev)
+        if heads_out != heads:
+            raise ValueError(f"{name}_out: found {heads_out} heads, required {heads}")
+        args += [p, ld, heads, po, ldo]
+    _call(load().gdn_rope, dev, stream, ctypes.byref(plan), _ptr(positions, "positions", _i32, (n,), dev), n, *args)
+
+
+def _workspace(workspace, dev):
+    if workspace is None:
+        return None, 0
+    return _ptr(workspace, "workspace", workspace.dtype, workspace.shape, dev), workspace.nbytes
+
+
+def gdn_proj_lora_workspace_size(n_tok: int, n_out: int, k: int, rank: int, n_seg: int) -> int:
+    n = load().gdn_proj_lora_workspace_size(n_tok, n_out, k, rank, n_seg)
+    msg = load().gdn_last_error().decode()
+    if msg:
+        raise GdnError(-5, msg)
+    return n
+
+
+def gdn_proj_lora(act, w, lora: Lora, cu_rows, adapter_idx, out, workspace=None, stream=None):
+    """out[t] = act[t] w^T + scale (act[t] a^T) b^T with the adapter adapter_idx[s] (outside the pool: none) of request s, rows
+    cu_rows[s] .. cu_rows[s+1]: act bf16 [N, k], w bf16 [n_out, k], out bf16 [N, >= n_out]."""
+    dev, (n, k), n_out, n_seg = _device(act, "act"), _dim("act", act, 2), w.shape[0], adapter_idx.shape[0]
+    n_adapters, rank, _ = _dim("lora.a", lora.a, 3)
+    ld = _dim("out", out, 2)[1]
+    ws, ws_bytes = _workspace(workspace, dev)
+    c = CLora(_ptr(lora.a, "lora.a", _bf16, (n_adapters, rank, k), dev),
+              _ptr(lora.b, "lora.b", _bf16, (n_adapters, n_out, rank), dev),
+              None if lora.scale is None else _ptr(lora.scale, "lora.scale", _f32, (n_adapters,), dev), n_adapters, rank)
+    _call(load().gdn_proj_lora, dev, stream, _ptr(act, "act", _bf16, (n, k), dev), _ptr(w, "w", _bf16, (n_out, k), dev),
+          ctypes.byref(c), _ptr(cu_rows, "cu_rows", _i32, (n_seg + 1,), dev),
+          _ptr(adapter_idx, "adapter_idx", _i32, (n_seg,), dev), n_seg, _ptr(out, "out", _bf16, (n, ld), dev), n, n_out, k,
+          ld, ws, ws_bytes)
+
+
+def gdn_proj_gated(act, w_gate, w_up, out, stream=None):
+    """out = silu(act w_gate^T) * (act w_up^T): act bf16 [N, k], w_gate, w_up bf16 [n_out, k], out bf16 [N, >= n_out]."""
+    dev, (n, k), n_out, ld = _device(act, "act"), _dim("act", act, 2), w_gate.shape[0], _dim("out", out, 2)[1]
+    _call(load().gdn_proj_gated, dev, stream, _ptr(act, "act", _bf16, (n, k), dev),
+          _ptr(w_gate, "w_gate", _bf16, (n_out, k), dev), _ptr(w_up, "w_up", _bf16, (n_out, k), dev),
+          _ptr(out, "out", _bf16, (n, ld), dev), n, n_out, k, ld)
+
+
+def gdn_ffn_workspace_size(n_tok: int, hidden: int, inter: int) -> int:
+    n = load().gdn_ffn_workspace_size(n_tok, hidden, inter)
+    msg = load().gdn_last_error().decode()
+    if msg:
+        raise GdnError(-5, msg)
+    return n
+
+
+def gdn_ffn(ffn: Ffn, h, out, workspace=None, stream=None):
+    """out = (silu(h w_gate^T) * (h w_up^T)) w_down^T: h, out bf16 [N, hidden]."""
+    dev, (n, hidden), inter = _device(h, "h"), _dim("h", h, 2), ffn.w_gate.shape[0]
+    ws, ws_bytes = _workspace(workspace, dev)
+    c = CFfn(_ptr(ffn.w_gate, "ffn.w_gate", _bf16, (inter, hidden), dev),
+             _ptr(ffn.w_up, "ffn.w_up", _bf16, (inter, hidden), dev),
+             _ptr(ffn.w_down, "ffn.w_down", _bf16, (hidden, inter), dev), hidden, inter)
+    _call(load().gdn_ffn, dev, stream, ctypes.byref(c), _ptr(h, "h", _bf16, (n, hidden), dev), n,
+          _ptr(out, "out", _bf16, (n, hidden), dev), ws, ws_bytes)

@@ -4,6 +4,7 @@
 // caller's stream.  Nothing here allocates device memory or synchronises.
 // Error messages follow the Strata convention (chapter 6, sections 6.2 and
 // 6.5): name the argument, the value found and the value required.
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -161,14 +162,16 @@ const char* gdn_version(void) { return "libgdn 0.1 (sm_103a)"; }
 gdn_status gdn_device_status(uint32_t* status) {
     if (!status) return fail(GDN_ERR_NULL, "status: found NULL, required a host pointer");
     unsigned a = 0, b = 0;
-    unsigned c = 0, d = 0, t = 0, u = 0;
+    unsigned c = 0, d = 0, t = 0, u = 0, f = 0, l = 0;
     cudaError_t e = gdn::take_device_status_decode(&a);
     if (e == cudaSuccess) e = gdn::take_device_status_prefill(&b);
     if (e == cudaSuccess) e = gdn::take_device_status_proj(&c);
     if (e == cudaSuccess) e = gdn::take_device_status_chunk16(&d);
     if (e == cudaSuccess) e = gdn::take_device_status_tree(&t);
     if (e == cudaSuccess) e = gdn::take_device_status_attn_tree(&u);
-    *status = a | b | c | d | t | u;
+    if (e == cudaSuccess) e = gdn::take_device_status_few(&f);
+    if (e == cudaSuccess) e = gdn::take_device_status_lora(&l);
+    *status = a | b | c | d | t | u | f | l;
     return cuda_status(e, "gdn_device_status");
 }
 
@@ -928,6 +931,233 @@ gdn_status gdn_attn_append(const gdn_attn_config* cfg, const void* k_new, const 
     job.n_rows = n_rows; job.n_src = n_src;
     job.Hkv = cfg->n_kv_heads; job.D = cfg->head_dim; job.page = cfg->page_size; job.n_pages = n_pages;
     return cuda_status(gdn::launch_append(job, (cudaStream_t)stream), "gdn_attn_append");
+}
+
+// ---- rotary positions, projections with adapters, the gated feed-forward block ----
+
+static gdn_status rope_check(const char* what, int32_t head_dim, int32_t rotary_dim, int32_t layout, int32_t act_dtype) {
+    if (head_dim < 16 || head_dim > 256 || head_dim % 8 != 0)
+        return fail(GDN_ERR_SHAPE, "%s.head_dim: found %d, required a multiple of 8, 16..256", what, head_dim);
+    if (rotary_dim < 16 || rotary_dim > head_dim || rotary_dim % 16 != 0)
+        return fail(GDN_ERR_SHAPE, "%s.rotary_dim: found %d, required a multiple of 16, 16..head_dim = %d", what,
+                    rotary_dim, head_dim);
+    if (layout != GDN_ROPE_HALF && layout != GDN_ROPE_INTERLEAVED)
+        return fail(GDN_ERR_SHAPE, "%s.layout: found %d, required GDN_ROPE_HALF (0) or GDN_ROPE_INTERLEAVED (1)", what,
+                    layout);
+    if (act_dtype != GDN_DTYPE_BF16 && act_dtype != GDN_DTYPE_F32)
+        return fail(GDN_ERR_DTYPE, "%s.act_dtype: found %d, required GDN_DTYPE_BF16 (0) or GDN_DTYPE_F32 (1)", what,
+                    act_dtype);
+    return GDN_OK;
+}
+
+static bool finite_above(float v, float low) { return v > low && v <= 3.4e38f; }
+
+gdn_status gdn_rope_plan_init(const gdn_rope_config* cfg, gdn_rope_plan* plan) {
+    if (!cfg) return fail(GDN_ERR_NULL, "cfg: found NULL, required a gdn_rope_config");
+    if (!plan) return fail(GDN_ERR_NULL, "plan: found NULL, required a gdn_rope_plan");
+    const gdn_status st = rope_check("cfg", cfg->head_dim, cfg->rotary_dim, cfg->layout, cfg->act_dtype);
+    if (st) return st;
+    if (!finite_above(cfg->theta, 1.f))
+        return fail(GDN_ERR_RANGE, "cfg.theta: found %g, required a number > 1", (double)cfg->theta);
+    if (!finite_above(cfg->factor, 0.f) || cfg->factor < 1e-6f)
+        return fail(GDN_ERR_RANGE, "cfg.factor: found %g, required a number >= 1e-6", (double)cfg->factor);
+    if (cfg->orig_len < 0) return fail(GDN_ERR_RANGE, "cfg.orig_len: found %d, required >= 0", cfg->orig_len);
+    if (cfg->orig_len > 0 && (!finite_above(cfg->beta_fast, 0.f) || !finite_above(cfg->beta_slow, 0.f)))
+        return fail(GDN_ERR_RANGE, "cfg.beta_fast/beta_slow: found %g/%g, required numbers > 0", (double)cfg->beta_fast,
+                    (double)cfg->beta_slow);
+    if (cfg->mscale != 0.f && !finite_above(cfg->mscale, 0.f))
+        return fail(GDN_ERR_RANGE, "cfg.mscale: found %g, required a number >= 0", (double)cfg->mscale);
+    plan->head_dim = cfg->head_dim;
+    plan->rotary_dim = cfg->rotary_dim;
+    plan->layout = cfg->layout;
+    plan->act_dtype = cfg->act_dtype;
+    plan->mscale = cfg->mscale != 0.f ? cfg->mscale
+                   : cfg->orig_len > 0 && cfg->factor > 1.f ? (float)(0.1 * std::log((double)cfg->factor) + 1.0)
+                                                            : 1.f;
+    for (uint64_t& t : plan->turns) t = 0;
+    gdn::rope_turns(cfg->rotary_dim, cfg->theta, cfg->factor, cfg->orig_len, cfg->beta_fast, cfg->beta_slow, plan->turns);
+    return ok();
+}
+
+gdn_status gdn_rope(const gdn_rope_plan* plan, const int32_t* positions, int64_t n_tok, const void* q, int64_t ld_q,
+                    int32_t n_q_heads, void* q_out, int64_t ld_q_out, const void* k, int64_t ld_k, int32_t n_kv_heads,
+                    void* k_out, int64_t ld_k_out, void* stream) {
+    if (!plan) return fail(GDN_ERR_NULL, "plan: found NULL, required a gdn_rope_plan");
+    const gdn_status st = rope_check("plan", plan->head_dim, plan->rotary_dim, plan->layout, plan->act_dtype);
+    if (st) return st;
+    if (n_tok < 0 || n_tok >= ((int64_t)1 << 31))
+        return fail(GDN_ERR_RANGE, "n_tok: found %lld, required 0..2^31-1", (long long)n_tok);
+    if (n_q_heads < 0 || n_q_heads > 4096 || n_kv_heads < 0 || n_kv_heads > 4096)
+        return fail(GDN_ERR_RANGE, "n_q_heads/n_kv_heads: found %d/%d, required 0..4096", n_q_heads, n_kv_heads);
+    const int es = plan->act_dtype == GDN_DTYPE_BF16 ? 2 : 4;
+    const struct {
+        const char *name, *ld_name;
+        int32_t heads;
+        int64_t ld;
+    } rows[4] = {{"q", "ld_q", n_q_heads, ld_q},
+                 {"q_out", "ld_q_out", n_q_heads, ld_q_out},
+                 {"k", "ld_k", n_kv_heads, ld_k},
+                 {"k_out", "ld_k_out", n_kv_heads, ld_k_out}};
+    for (const auto& r : rows)
+        if (r.heads > 0 && (r.ld < (int64_t)r.heads * plan->head_dim || r.ld > (int64_t)1 << 31 || r.ld * es % 16 != 0))
+            return fail(GDN_ERR_SHAPE, "%s: found %lld, required >= %lld elements, at most 2^31, rows on 16-byte boundaries",
+                        r.ld_name, (long long)r.ld, (long long)r.heads * plan->head_dim);
+    if (n_tok == 0 || (n_q_heads == 0 && n_kv_heads == 0)) return ok();
+    GDN_REQUIRE_PTR_A(positions, "positions", 4u);
+    if (n_q_heads > 0) {
+        GDN_REQUIRE_PTR(q, "q");
+        GDN_REQUIRE_PTR(q_out, "q_out");
+        if (q == q_out && ld_q != ld_q_out)
+            return fail(GDN_ERR_SHAPE, "ld_q_out: found %lld, required ld_q = %lld in place", (long long)ld_q_out,
+                        (long long)ld_q);
+    }
+    if (n_kv_heads > 0) {
+        GDN_REQUIRE_PTR(k, "k");
+        GDN_REQUIRE_PTR(k_out, "k_out");
+        if (k == k_out && ld_k != ld_k_out)
+            return fail(GDN_ERR_SHAPE, "ld_k_out: found %lld, required ld_k = %lld in place", (long long)ld_k_out,
+                        (long long)ld_k);
+    }
+    gdn::RopeJob job = {};
+    if (n_q_heads > 0) job.q = q, job.q_out = q_out, job.ldq = ld_q, job.ldqo = ld_q_out;
+    if (n_kv_heads > 0) job.k = k, job.k_out = k_out, job.ldk = ld_k, job.ldko = ld_k_out;
+    job.positions = positions;
+    job.n_tok = n_tok;
+    job.hq = n_q_heads; job.hkv = n_kv_heads; job.D = plan->head_dim; job.rot = plan->rotary_dim;
+    job.half = plan->layout == GDN_ROPE_HALF;
+    job.bf16 = es == 2;
+    job.mscale = plan->mscale;
+    for (int i = 0; i < plan->rotary_dim / 2; ++i) job.turns[i] = plan->turns[i];
+    return cuda_status(gdn::launch_rope(job, (cudaStream_t)stream), "gdn_rope");
+}
+
+// sizes and output of a projection whose result rows are stored in 16-byte pieces
+static gdn_status proj_sizes(int64_t n_tok, int32_t n_out, int32_t k, int64_t ld_out) {
+    if (n_tok < 0 || n_tok > ((int64_t)1 << 22))
+        return fail(GDN_ERR_RANGE, "n_tok: found %lld, required 0..2^22", (long long)n_tok);
+    if (n_out < 1 || n_out > 1 << 24) return fail(GDN_ERR_SHAPE, "n_out: found %d, required 1..2^24", n_out);
+    if (k < 8 || k % 8 != 0) return fail(GDN_ERR_SHAPE, "k: found %d, required a positive multiple of 8", k);
+    if (ld_out < n_out || ld_out % 8 != 0 || ld_out > ((int64_t)1 << 31))
+        return fail(GDN_ERR_SHAPE, "ld_out: found %lld, required a multiple of 8, >= n_out = %d and at most 2^31",
+                    (long long)ld_out, n_out);
+    return GDN_OK;
+}
+
+gdn_status gdn_proj_gated(const void* act, const void* w_gate, const void* w_up, void* out, int64_t n_tok, int32_t n_out,
+                          int32_t k, int64_t ld_out, void* stream) {
+    const gdn_status st = proj_sizes(n_tok, n_out, k, ld_out);
+    if (st) return st;
+    if (n_tok == 0) return ok();
+    GDN_REQUIRE_PTR(act, "act");
+    GDN_REQUIRE_PTR(w_gate, "w_gate");
+    GDN_REQUIRE_PTR(w_up, "w_up");
+    GDN_REQUIRE_PTR(out, "out");
+    gdn::FewJob job = {};
+    job.x = act; job.w = w_gate; job.w2 = w_up; job.out = out;
+    job.n_tok = n_tok; job.ld = ld_out; job.n_out = n_out; job.k = k;
+    return cuda_status(gdn::launch_few(job, (cudaStream_t)stream), "gdn_proj_gated");
+}
+
+static gdn_status ffn_sizes(int64_t n_tok, int32_t hidden, int32_t inter) {
+    if (n_tok < 0 || n_tok > ((int64_t)1 << 22))
+        return fail(GDN_ERR_RANGE, "n_tok: found %lld, required 0..2^22", (long long)n_tok);
+    if (hidden < 8 || hidden % 8 != 0 || hidden > 1 << 24 || inter < 8 || inter % 8 != 0 || inter > 1 << 24)
+        return fail(GDN_ERR_SHAPE, "hidden/inter: found %d/%d, required positive multiples of 8, at most 2^24", hidden,
+                    inter);
+    return GDN_OK;
+}
+
+size_t gdn_ffn_workspace_size(int64_t n_tok, int32_t hidden, int32_t inter) {
+    if (ffn_sizes(n_tok, hidden, inter)) return 0;
+    ok();
+    return (size_t)n_tok * inter * 2;
+}
+
+gdn_status gdn_ffn(const gdn_ffn_weights* ffn, const void* h, int64_t n_tok, void* out, void* workspace, size_t ws_bytes,
+                   void* stream) {
+    if (!ffn) return fail(GDN_ERR_NULL, "ffn: found NULL, required a gdn_ffn_weights");
+    const gdn_status st = ffn_sizes(n_tok, ffn->hidden, ffn->inter);
+    if (st) return st;
+    GDN_REQUIRE_PTR(ffn->w_gate, "ffn.w_gate");
+    GDN_REQUIRE_PTR(ffn->w_up, "ffn.w_up");
+    GDN_REQUIRE_PTR(ffn->w_down, "ffn.w_down");
+    if (n_tok == 0) return ok();
+    GDN_REQUIRE_PTR(h, "h");
+    GDN_REQUIRE_PTR(out, "out");
+    GDN_REQUIRE_PTR(workspace, "workspace");
+    const size_t need = (size_t)n_tok * ffn->inter * 2;
+    if (ws_bytes < need)
+        return fail(GDN_ERR_WORKSPACE, "workspace: found %zu bytes, required %zu bytes", ws_bytes, need);
+    const cudaStream_t s = (cudaStream_t)stream;
+    gdn::FewJob job = {};
+    job.x = h; job.w = ffn->w_gate; job.w2 = ffn->w_up; job.out = workspace;
+    job.n_tok = n_tok; job.ld = ffn->inter; job.n_out = ffn->inter; job.k = ffn->hidden;
+    const cudaError_t e = gdn::launch_few(job, s);
+    if (e != cudaSuccess) return cuda_status(e, "gdn_ffn (gated half)");
+    gdn::FewJob back = {};
+    back.x = workspace; back.w = ffn->w_down; back.out = out; back.early = 1;
+    back.n_tok = n_tok; back.ld = ffn->hidden; back.n_out = ffn->hidden; back.k = ffn->inter;
+    return cuda_status(gdn::launch_few(back, s), "gdn_ffn (projection back)");
+}
+
+// the tokens' low-rank activations, then their adapters
+struct LoraWs {
+    size_t tok_adapter, bytes;
+};
+static LoraWs lora_ws(int64_t n_tok, int32_t rank) {
+    const size_t low = (size_t)n_tok * (rank <= 32 ? 128 : rank <= 64 ? 256 : 512);
+    return {low, low + (size_t)n_tok * 4};
+}
+
+static gdn_status lora_sizes(int64_t n_tok, int32_t n_out, int32_t k, int32_t rank, int32_t n_seg) {
+    const gdn_status st = proj_sizes(n_tok, n_out, k, ((int64_t)n_out + 7) / 8 * 8);
+    if (st) return st;
+    if (rank < 8 || rank > 128 || rank % 8 != 0)
+        return fail(GDN_ERR_SHAPE, "lora.rank: found %d, required a multiple of 8, 8..128", rank);
+    if (n_seg < 0 || n_seg > 1 << 20) return fail(GDN_ERR_RANGE, "n_seg: found %d, required 0..2^20", n_seg);
+    return GDN_OK;
+}
+
+size_t gdn_proj_lora_workspace_size(int64_t n_tok, int32_t n_out, int32_t k, int32_t rank, int32_t n_seg) {
+    if (lora_sizes(n_tok, n_out, k, rank, n_seg)) return 0;
+    ok();
+    return lora_ws(n_tok, rank).bytes;
+}
+
+gdn_status gdn_proj_lora(const void* act, const void* w, const gdn_lora* lora, const int32_t* cu_rows,
+                         const int32_t* adapter_idx, int32_t n_seg, void* out, int64_t n_tok, int32_t n_out, int32_t k,
+                         int64_t ld_out, void* workspace, size_t ws_bytes, void* stream) {
+    if (!lora) return fail(GDN_ERR_NULL, "lora: found NULL, required a gdn_lora");
+    gdn_status st = lora_sizes(n_tok, n_out, k, lora->rank, n_seg);
+    if (st || (st = proj_sizes(n_tok, n_out, k, ld_out))) return st;
+    if (lora->n_adapters < 1 || lora->n_adapters > 1 << 20)
+        return fail(GDN_ERR_RANGE, "lora.n_adapters: found %d, required 1..2^20", lora->n_adapters);
+    GDN_REQUIRE_PTR(lora->a, "lora.a");
+    GDN_REQUIRE_PTR(lora->b, "lora.b");
+    GDN_OPTIONAL_PTR_A(lora->scale, "lora.scale", 4u);
+    if (n_tok == 0) return ok();
+    GDN_REQUIRE_PTR(act, "act");
+    GDN_REQUIRE_PTR(w, "w");
+    GDN_REQUIRE_PTR(out, "out");
+    GDN_REQUIRE_PTR_A(cu_rows, "cu_rows", 4u);
+    if (n_seg > 0) GDN_REQUIRE_PTR_A(adapter_idx, "adapter_idx", 4u);
+    GDN_REQUIRE_PTR(workspace, "workspace");
+    const LoraWs L = lora_ws(n_tok, lora->rank);
+    if (ws_bytes < L.bytes)
+        return fail(GDN_ERR_WORKSPACE, "workspace: found %zu bytes, required %zu bytes", ws_bytes, L.bytes);
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    const cudaStream_t s = (cudaStream_t)stream;
+    gdn::LowJob low = {};
+    low.x = act; low.a = lora->a; low.scale = lora->scale; low.cu_rows = cu_rows; low.adapter_idx = adapter_idx;
+    low.v = reinterpret_cast<float*>(ws); low.tok_adapter = reinterpret_cast<int32_t*>(ws + L.tok_adapter);
+    low.n_tok = n_tok; low.n_seg = n_seg; low.n_adapters = lora->n_adapters; low.rank = lora->rank; low.k = k;
+    const cudaError_t e = gdn::launch_lora_low(low, s);
+    if (e != cudaSuccess) return cuda_status(e, "gdn_proj_lora (low side)");
+    gdn::FewJob job = {};
+    job.x = act; job.w = w; job.out = out; job.early = 1;
+    job.n_tok = n_tok; job.ld = ld_out; job.n_out = n_out; job.k = k;
+    job.v = low.v; job.tok_adapter = low.tok_adapter; job.b = lora->b; job.rank = lora->rank;
+    return cuda_status(gdn::launch_few(job, s), "gdn_proj_lora");
 }
 
 }  // extern "C"

@@ -48,6 +48,27 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
 }
 
+// The same for a grid of clusters of `size` CTAs along x.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, int size, cudaStream_t st,
+                               Args&&... args) {
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)size;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
+}
+
 // Geometry + options after validation (all derived fields filled in).
 struct Geom {
     int Hk, Hv, D, K, G, C_ch, chunk;
@@ -261,6 +282,49 @@ struct AppendJob {
 };
 cudaError_t launch_append(const AppendJob& job, cudaStream_t st);
 
+// ---- around the attention and the projections ----
+// rotary positions of rows of q and k (out == in: in place); pieces and step_h are the launcher's
+struct RopeJob {
+    const void *q, *k;
+    void *q_out, *k_out;
+    int64_t ldq, ldk, ldqo, ldko;  // elements between tokens
+    const int32_t* positions;
+    int64_t n_tok;
+    int hq, hkv, D, rot, half, bf16;
+    int pieces, step_h;
+    float mscale;
+    unsigned long long turns[128];  // turns per position of pair i, in units of 2^-64
+};
+void rope_turns(int rot, double theta, double factor, int orig_len, double beta_fast, double beta_slow, uint64_t* turns);
+cudaError_t launch_rope(RopeJob job, cudaStream_t st);
+
+// out[t][n] of few tokens: x_t . w_n, plus (rank > 0) v_t . b_n of the token's adapter; or, with w2,
+// silu(x_t . w_n) (x_t . w2_n)
+struct FewJob {
+    const void *x, *w, *w2;
+    void* out;
+    int64_t n_tok, ld;
+    int32_t n_out, k;
+    int early;  // the kernel ahead in the stream is of the same call and its launches follow the rule of `k_few`
+    const float* v;              // [n_tok][rank]
+    const int32_t* tok_adapter;  // [n_tok], -1: none
+    const void* b;               // [n_adapters][n_out][rank]
+    int32_t rank;
+};
+cudaError_t launch_few(const FewJob& job, cudaStream_t st);
+
+// each token's adapter, and v = scale A x; per_cta is the launcher's
+struct LowJob {
+    const void *x, *a;
+    const float* scale;  // NULL: 1
+    const int32_t *cu_rows, *adapter_idx;
+    float* v;              // [n_tok][rank]
+    int32_t* tok_adapter;  // [n_tok], -1: none
+    int64_t n_tok;
+    int32_t n_seg, n_adapters, rank, k, per_cta;
+};
+cudaError_t launch_lora_low(LowJob job, cudaStream_t st);
+
 // GDN_DEBUG: device-side check that the na + nb indices of idx_a then idx_b lie in
 // [0, n_slots) and are distinct.  A violation ORs kDevBadSlot into the device status
 // word.  With wait, the stream is synchronised and the first bad position (or -1)
@@ -276,5 +340,7 @@ cudaError_t take_device_status_chunk16(unsigned* out);
 cudaError_t take_device_status_proj(unsigned* out);
 cudaError_t take_device_status_tree(unsigned* out);
 cudaError_t take_device_status_attn_tree(unsigned* out);
+cudaError_t take_device_status_few(unsigned* out);
+cudaError_t take_device_status_lora(unsigned* out);
 
 }  // namespace gdn

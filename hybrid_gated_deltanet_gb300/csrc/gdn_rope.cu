@@ -1,0 +1,200 @@
+// gdn_rope.cu -- rotary positions of the attention layers' queries and keys (gdn_rope).
+//
+// Pair i of the first rot elements of a head, at position p:
+//   (a, b) -> m (a cos t - b sin t, b cos t + a sin t),   t = p f_i,
+// with f_i from gdn_rope_plan_init (theta^(-2i/rot), slowed down for contexts longer than the trained one).
+//
+// Angles.  f_i is kept as turns per position in units of 2^-64: p f_i modulo whole turns is then the low 64 bits of
+// an integer product, exact however far the position (a float's p f_i is off by a radian at p = 10^7), and its
+// upper 32 bits as a signed number are the angle in (-1/2, 1/2] turns for sincospif.  The frequency itself has the 53
+// bits of a double: 2^-54 p of a turn, 2^-34 at a position of 2^20.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "gdn_common.cuh"
+#include "gdn_internal.h"
+#include "gdn_tma.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeHeads = 4;  // heads whose loads a thread has in flight
+
+// 8 consecutive elements
+template <typename T>
+struct Eight;
+template <>
+struct Eight<__nv_bfloat16> {
+    uint4 r;
+    __device__ __forceinline__ void ld(const void* p) { r = *static_cast<const uint4*>(p); }
+    __device__ __forceinline__ void st(void* p) const { *static_cast<uint4*>(p) = r; }
+    __device__ __forceinline__ void get(float v[8]) const {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = __uint_as_float(w[j] << 16);
+            v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        }
+    }
+    __device__ __forceinline__ void set(const float v[8]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+            w[j] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        r = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+template <>
+struct Eight<float> {
+    float4 a, b;
+    __device__ __forceinline__ void ld(const void* p) {
+        a = static_cast<const float4*>(p)[0];
+        b = static_cast<const float4*>(p)[1];
+    }
+    __device__ __forceinline__ void st(void* p) const {
+        static_cast<float4*>(p)[0] = a;
+        static_cast<float4*>(p)[1] = b;
+    }
+    __device__ __forceinline__ void get(float v[8]) const {
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+    __device__ __forceinline__ void set(const float v[8]) {
+        a = make_float4(v[0], v[1], v[2], v[3]);
+        b = make_float4(v[4], v[5], v[6], v[7]);
+    }
+};
+
+// A thread owns one piece of 16 elements of a token's heads: 8 pairs of the rotated part (two runs of 8 elements, rot / 2
+// apart or side by side), or 16 bytes x 2 of the rest, which is only copied and only where the result goes elsewhere.
+// It makes its 8 angles once and walks over every step_h-th head, kRopeHeads at a time: with every thread making angles for
+// one head, sine and cosine alone would take as long as the memory.  Pieces are fastest among the threads, then heads, so
+// that a warp's accesses are contiguous.  step_h > 1 splits the heads of few tokens over more threads.
+template <typename T>
+__global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ RopeJob J) {
+    __shared__ unsigned long long turns[128];
+    griddep_wait();  // launched with programmatic serialization
+    griddep_launch_dependents();
+    if (threadIdx.x < J.rot / 2) turns[threadIdx.x] = J.turns[threadIdx.x];
+    __syncthreads();
+    const int pieces = J.pieces, pairs = J.rot / 16;
+    const int64_t at = (int64_t)blockIdx.x * kRopeThreads + threadIdx.x;
+    const int64_t row = at / pieces;
+    const int u = (int)(at - row * pieces);
+    const int64_t tok = row / J.step_h;
+    if (tok >= J.n_tok) return;
+    const int h0 = (int)(row - tok * J.step_h), heads = J.hq + J.hkv;
+    const bool turn = u < pairs, half = J.half != 0;
+    // the two runs of 8 elements
+    int e0, e1;
+    if (turn) {
+        e0 = half ? 8 * u : 16 * u;
+        e1 = half ? 8 * u + J.rot / 2 : 16 * u + 8;
+    } else {
+        e0 = J.rot + 16 * (u - pairs);
+        e1 = e0 + 8;
+    }
+    const bool two = e1 < J.D;  // (a head's rest may end on a single run)
+    float c[8], s[8];
+    if (turn) {
+        const unsigned long long p = (unsigned long long)(long long)J.positions[tok];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int t = (int)(unsigned)((p * turns[8 * u + j]) >> 32);
+            sincospif((float)t * 0x1p-31f, &s[j], &c[j]);
+            c[j] *= J.mscale;
+            s[j] *= J.mscale;
+        }
+    }
+    for (int hb = h0; hb < heads; hb += kRopeHeads * J.step_h) {
+        Eight<T> x[kRopeHeads], y[kRopeHeads];
+#pragma unroll
+        for (int e = 0; e < kRopeHeads; ++e) {
+            const int h = hb + e * J.step_h;
+            if (h >= heads) continue;
+            const T* src = h < J.hq ? static_cast<const T*>(J.q) + tok * J.ldq + (int64_t)h * J.D
+                                    : static_cast<const T*>(J.k) + tok * J.ldk + (int64_t)(h - J.hq) * J.D;
+            x[e].ld(src + e0);
+            if (two) y[e].ld(src + e1);
+        }
+#pragma unroll
+        for (int e = 0; e < kRopeHeads; ++e) {
+            const int h = hb + e * J.step_h;
+            if (h >= heads) continue;
+            T* dst = h < J.hq ? static_cast<T*>(J.q_out) + tok * J.ldqo + (int64_t)h * J.D
+                              : static_cast<T*>(J.k_out) + tok * J.ldko + (int64_t)(h - J.hq) * J.D;
+            if (turn) {
+                float a[8], b[8];
+                x[e].get(a);
+                y[e].get(b);
+                if (half) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float a1 = a[j] * c[j] - b[j] * s[j];
+                        b[j] = b[j] * c[j] + a[j] * s[j];
+                        a[j] = a1;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float a1 = a[2 * j] * c[j] - a[2 * j + 1] * s[j];
+                        a[2 * j + 1] = a[2 * j + 1] * c[j] + a[2 * j] * s[j];
+                        a[2 * j] = a1;
+                        const float b1 = b[2 * j] * c[j + 4] - b[2 * j + 1] * s[j + 4];
+                        b[2 * j + 1] = b[2 * j + 1] * c[j + 4] + b[2 * j] * s[j + 4];
+                        b[2 * j] = b1;
+                    }
+                }
+                x[e].set(a);
+                y[e].set(b);
+            }
+            x[e].st(dst + e0);
+            if (two) y[e].st(dst + e1);
+        }
+    }
+}
+
+}  // namespace
+
+// theta^(-2i/rot) / 2 pi in turns, slowed down by `factor` (orig_len 0: every pair; else by parts: pairs that turn more than
+// beta_fast times within orig_len positions keep their frequency, those that turn less than beta_slow times are slowed down, a
+// ramp over the pairs joins them), as multiples of 2^-64
+void rope_turns(int rot, double theta, double factor, int orig_len, double beta_fast, double beta_slow, uint64_t* turns) {
+    constexpr double two_pi = 6.283185307179586476925286766559;
+    double low = 0.0, high = 0.0;
+    if (orig_len > 0) {
+        auto pair_of = [&](double n) { return rot * std::log(orig_len / (n * two_pi)) / (2.0 * std::log(theta)); };
+        low = std::max(std::floor(pair_of(beta_fast)), 0.0);
+        high = std::min(std::ceil(pair_of(beta_slow)), rot - 1.0);
+    }
+    for (int i = 0; i < rot / 2; ++i) {
+        double f = std::pow(theta, -2.0 * i / rot);
+        if (orig_len > 0) {
+            const double ramp = std::min(std::max((i - low) / std::max(high - low, 0.001), 0.0), 1.0);
+            f = f * (1.0 - ramp) + f / factor * ramp;
+        } else {
+            f /= factor;
+        }
+        turns[i] = (uint64_t)std::llround(f / two_pi * 0x1p62) << 2;  // (f <= 1: below a sixth of a turn)
+    }
+}
+
+cudaError_t launch_rope(RopeJob job, cudaStream_t st) {
+    const int heads = job.hq + job.hkv;
+    if (job.n_tok == 0 || heads == 0) return cudaSuccess;
+    const bool same = job.q == job.q_out && job.k == job.k_out;
+    job.pieces = job.rot / 16 + (same ? 0 : (job.D - job.rot + 15) / 16);
+    // one thread per piece and token walks all heads once that fills the GPU (2048 threads an SM); fewer tokens split the heads
+    const int64_t full = (int64_t)sm_count() * 2048, one = job.n_tok * job.pieces;
+    job.step_h = (int)std::min<int64_t>(heads, std::max<int64_t>(1, full / one));
+    const int64_t threads = one * job.step_h;
+    const dim3 grid((unsigned)((threads + kRopeThreads - 1) / kRopeThreads));
+    return job.bf16 ? launch_pdl(k_rope<__nv_bfloat16>, grid, dim3(kRopeThreads), 0, st, job)
+                    : launch_pdl(k_rope<float>, grid, dim3(kRopeThreads), 0, st, job);
+}
+
+}  // namespace gdn

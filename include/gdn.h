@@ -568,6 +568,122 @@ gdn_status gdn_attn_append(const gdn_attn_config* cfg, const void* k_new, const 
                            int64_t n_rows, void* k_pool, void* v_pool, int32_t n_pages,
                            void* stream);
 
+/* ---- Rotary positions -----------------------------------------------------------
+ * The attention layers' queries and keys carry their positions as rotations of
+ * pairs of elements; gdn_attn_decode, gdn_attn_prefill and gdn_attn_tree take
+ * them rotated.  For a token at position p, pair i (of rotary_dim / 2) of every head:
+ *   (a, b) -> m (a cos(p f_i) - b sin(p f_i), b cos(p f_i) + a sin(p f_i)).
+ * GDN_ROPE_HALF: a = x[i], b = x[i + rotary_dim/2]; GDN_ROPE_INTERLEAVED: a = x[2i],
+ * b = x[2i+1].  Elements from rotary_dim on are not rotated.
+ * Frequencies: f_i = theta^(-2i/rotary_dim), and for contexts `factor` times as long as the
+ * trained one:
+ *   orig_len 0: f_i / factor (positions interpolated);
+ *   orig_len > 0 (the trained length): by parts, f_i (1 - r_i) + r_i f_i / factor with
+ *   r_i = clamp((i - lo) / max(hi - lo, 0.001), 0, 1), lo = max(floor(c(beta_fast)), 0),
+ *   hi = min(ceil(c(beta_slow)), rotary_dim - 1), c(n) = rotary_dim
+ *   ln(orig_len / (2 pi n)) / (2 ln theta): pairs that turn more than beta_fast times
+ *   within orig_len keep their frequency, those that turn less than beta_slow times are slowed down.
+ * m = mscale; 0 means the default: 0.1 ln(factor) + 1 where orig_len > 0 and factor > 1, else 1. */
+enum { GDN_ROPE_HALF = 0, GDN_ROPE_INTERLEAVED = 1 };
+
+typedef struct gdn_rope_config {
+    int32_t head_dim;   /* a multiple of 8, 16 .. 256 */
+    int32_t rotary_dim; /* a multiple of 16, 16 .. head_dim */
+    int32_t layout;     /* GDN_ROPE_* */
+    int32_t act_dtype;  /* GDN_DTYPE_* of q and k */
+    float theta;        /* > 1 */
+    float factor;       /* > 0; 1: as trained */
+    int32_t orig_len;   /* >= 0 */
+    float beta_fast, beta_slow; /* > 0 where orig_len > 0 (32 and 1 are usual) */
+    float mscale;       /* >= 0 */
+} gdn_rope_config;
+
+/* The plan of a model's rotations: host data, filled once by gdn_rope_plan_init and read
+ * during each call.  turns[i]: pair i's turns per position in units of 2^-64. */
+typedef struct gdn_rope_plan {
+    int32_t head_dim, rotary_dim, layout, act_dtype;
+    float mscale;
+    uint64_t turns[128];
+} gdn_rope_plan;
+
+gdn_status gdn_rope_plan_init(const gdn_rope_config* cfg, gdn_rope_plan* plan);
+
+/* Rotates the rows of q and k by their tokens' positions.
+ *   positions int32 [n_tok] (device; any value: negative positions turn back, so that a call
+ *   with the positions negated takes gradients of the rotated rows to gradients of q and k).
+ *   q: rows of n_q_heads * head_dim elements, ld_q >= that apart; k likewise with n_kv_heads.
+ *   Either may have 0 heads (pointers and ld unused then).  Rows may lie inside wider ones,
+ *   e.g. [q | k | v] of one projection.
+ *   q_out, k_out: where the rows go, ld_*_out apart; equal to q / k with the same ld: in place,
+ *   and only the rotated elements are read and written.  Else the rest of each head is
+ *   copied.  Outputs that overlap inputs in any other way, or each other, are undefined.
+ *   Pointers 16-byte aligned, ld_* * element size a multiple of 16.
+ *   Precision: angles are exact modulo a turn to 2^-32 of it up to positions of 2^20 (2^-22
+ *   at 2^31), fp32 sine, cosine and products, one rounding to the activation dtype. */
+gdn_status gdn_rope(const gdn_rope_plan* plan, const int32_t* positions, int64_t n_tok, const void* q,
+                    int64_t ld_q, int32_t n_q_heads, void* q_out, int64_t ld_q_out, const void* k,
+                    int64_t ld_k, int32_t n_kv_heads, void* k_out, int64_t ld_k_out, void* stream);
+
+/* ---- Projections with low-rank adapters, and the gated feed-forward block ---------
+ * Beside gdn_proj_gemm, for the other matrices of a hybrid layer and for requests that
+ * bring adapters of their own.  All bf16 operands, fp32 accumulation (tcgen05 tensor cores), one
+ * rounding (to nearest even) of the result; results do not change from call to call. */
+
+/* Low-rank adapters of one projection (device pointers). */
+typedef struct gdn_lora {
+    const void* a;       /* bf16 [n_adapters][rank][k] */
+    const void* b;       /* bf16 [n_adapters][n_out][rank] */
+    const float* scale;  /* [n_adapters], or NULL (1) */
+    int32_t n_adapters;  /* >= 1 */
+    int32_t rank;        /* a multiple of 8, 8 .. 128; adapters of lower rank are padded with zeros */
+} gdn_lora;
+
+/* gdn_proj_gemm with each request's adapter beside the shared weights:
+ *   out[t][n] = sum_k act[t][k] w[n][k] + scale[e] sum_r b[e][n][r] (sum_k a[e][r][k] act[t][k])
+ * for the tokens t = cu_rows[s] .. cu_rows[s+1] - 1 of request s, e = adapter_idx[s].
+ *   cu_rows int32 [n_seg+1] (non-decreasing), adapter_idx int32 [n_seg] (device; checked there,
+ *   never trusted for an address): a request whose adapter_idx is outside [0, n_adapters) (-1 by convention), and tokens
+ *   outside every request, get the shared projection alone.  Requests may share an adapter.  A token meets
+ *   its own request's adapter only: NaN or infinities in another one, or in another token,
+ *   do not reach it.
+ *   act, w, n_tok, n_out, k as in gdn_proj_gemm; out bf16 rows ld_out >= n_out apart, 16-byte
+ *   aligned, ld_out a multiple of 8; 0 <= n_seg <= 2^20; a and b 16-byte aligned, scale 4.
+ *   The low-rank activations scale (a act) are carried to 2^-16 of their value or better.
+ *   workspace: gdn_proj_lora_workspace_size bytes, 16-byte aligned; calls that may overlap need one each. */
+gdn_status gdn_proj_lora(const void* act, const void* w, const gdn_lora* lora, const int32_t* cu_rows,
+                         const int32_t* adapter_idx, int32_t n_seg, void* out, int64_t n_tok, int32_t n_out,
+                         int32_t k, int64_t ld_out, void* workspace, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of gdn_proj_lora (depends on the sizes only; 0 on invalid arguments, with
+ * gdn_last_error set). */
+size_t gdn_proj_lora_workspace_size(int64_t n_tok, int32_t n_out, int32_t k, int32_t rank, int32_t n_seg);
+
+/* The gated half of a feed-forward block: both projections, the activation and the product
+ * in one kernel, out[t][n] = silu(act[t] . w_gate[n]) * (act[t] . w_up[n]).
+ *   act bf16 [n_tok][k], w_gate and w_up bf16 [n_out][k] (dense, 16-byte aligned; the two may be
+ *   halves of one matrix), k a positive multiple of 8, out as in gdn_proj_lora. */
+gdn_status gdn_proj_gated(const void* act, const void* w_gate, const void* w_up, void* out, int64_t n_tok,
+                          int32_t n_out, int32_t k, int64_t ld_out, void* stream);
+
+/* Weights of a gated feed-forward block (device pointers, bf16, row-major, 16-byte aligned). */
+typedef struct gdn_ffn_weights {
+    const void* w_gate;    /* [inter][hidden] */
+    const void* w_up;      /* [inter][hidden] */
+    const void* w_down;    /* [hidden][inter] */
+    int32_t hidden, inter; /* positive multiples of 8 */
+} gdn_ffn_weights;
+
+/* The whole block: out = (silu(h w_gate^T) * (h w_up^T)) w_down^T.
+ *   h, out bf16 [n_tok][hidden], dense, 16-byte aligned (out may not overlap h).  The gated
+ *   half is rounded to bf16 between the two kernels, as gdn_proj_gated would.
+ *   workspace: gdn_ffn_workspace_size bytes, 16-byte aligned (that half of the tokens); calls that may
+ *   overlap need one each. */
+gdn_status gdn_ffn(const gdn_ffn_weights* ffn, const void* h, int64_t n_tok, void* out, void* workspace,
+                   size_t ws_bytes, void* stream);
+
+/* Workspace bytes of gdn_ffn (0 on invalid arguments, with gdn_last_error set, or no tokens). */
+size_t gdn_ffn_workspace_size(int64_t n_tok, int32_t hidden, int32_t inter);
+
 /* Message of the last failed call on this host thread ("" if none).  The
  * string stays valid until the next call on this thread. */
 const char* gdn_last_error(void);
