@@ -30,7 +30,8 @@ MARSHAL = os.path.join(PKG, "_marshal.so")
 STAMP = os.path.join(PKG, "_marshal.stamp")  # the Python and torch that _marshal.so was compiled against
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["gdn_api.cu", "gdn_decode.cu", "gdn_prefill.cu", "gdn_chunk16.cu", "gdn_noalloc.cu", "gdn_proj.cu",
-           "gdn_attn.cu", "gdn_attn_tree.cu", "gdn_tree.cu", "gdn_tables.cu", "gdn_rope.cu", "gdn_few.cu", "gdn_lora.cu"]
+           "gdn_attn.cu", "gdn_attn_tree.cu", "gdn_tree.cu", "gdn_tables.cu", "gdn_rope.cu", "gdn_few.cu", "gdn_wide.cu",
+           "gdn_lora.cu"]
 MARSHAL_SOURCE = "gdn_marshal.cpp"
 HEADERS = ["gdn_common.cuh", "gdn_gemm.cuh", "gdn_internal.h", "gdn_prefill_common.cuh", "gdn_tc.cuh", "gdn_tma.cuh"]
 

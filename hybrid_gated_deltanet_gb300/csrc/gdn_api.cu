@@ -170,7 +170,7 @@ gdn_status gdn_device_status(uint32_t* status) {
     if (e == cudaSuccess) e = gdn::take_device_status_tree(&t);
     if (e == cudaSuccess) e = gdn::take_device_status_attn_tree(&u);
     if (e == cudaSuccess) e = gdn::take_device_status_few(&f);
-    if (e == cudaSuccess) e = gdn::take_device_status_lora(&l);
+    if (e == cudaSuccess) e = gdn::take_device_status_wide(&l);
     *status = a | b | c | d | t | u | f | l;
     return cuda_status(e, "gdn_device_status");
 }
@@ -1043,6 +1043,23 @@ static gdn_status proj_sizes(int64_t n_tok, int32_t n_out, int32_t k, int64_t ld
     return GDN_OK;
 }
 
+// Up to kFewTokens tokens the weights stream past the tokens, from there on tiles of 256 tokens go to pairs of SMs.
+constexpr int64_t kFewTokens = 128;
+
+static cudaError_t launch_fused(const void* x, const void* w, const void* w2, void* out, int64_t n_tok, int32_t n_out,
+                                int32_t k, int64_t ld, bool early, cudaStream_t st) {
+    if (n_tok > kFewTokens) {
+        gdn::WideJob job = {};
+        job.x = x; job.w = w; job.w2 = w2; job.out = out;
+        job.n_tok = n_tok; job.ld = ld; job.n_out = n_out; job.k = k;
+        return gdn::launch_wide(job, st);
+    }
+    gdn::FewJob job = {};
+    job.x = x; job.w = w; job.w2 = w2; job.out = out; job.early = early;
+    job.n_tok = n_tok; job.ld = ld; job.n_out = n_out; job.k = k;
+    return gdn::launch_few(job, st);
+}
+
 gdn_status gdn_proj_gated(const void* act, const void* w_gate, const void* w_up, void* out, int64_t n_tok, int32_t n_out,
                           int32_t k, int64_t ld_out, void* stream) {
     const gdn_status st = proj_sizes(n_tok, n_out, k, ld_out);
@@ -1052,10 +1069,8 @@ gdn_status gdn_proj_gated(const void* act, const void* w_gate, const void* w_up,
     GDN_REQUIRE_PTR(w_gate, "w_gate");
     GDN_REQUIRE_PTR(w_up, "w_up");
     GDN_REQUIRE_PTR(out, "out");
-    gdn::FewJob job = {};
-    job.x = act; job.w = w_gate; job.w2 = w_up; job.out = out;
-    job.n_tok = n_tok; job.ld = ld_out; job.n_out = n_out; job.k = k;
-    return cuda_status(gdn::launch_few(job, (cudaStream_t)stream), "gdn_proj_gated");
+    return cuda_status(launch_fused(act, w_gate, w_up, out, n_tok, n_out, k, ld_out, false, (cudaStream_t)stream),
+                       "gdn_proj_gated");
 }
 
 static gdn_status ffn_sizes(int64_t n_tok, int32_t hidden, int32_t inter) {
@@ -1089,15 +1104,10 @@ gdn_status gdn_ffn(const gdn_ffn_weights* ffn, const void* h, int64_t n_tok, voi
     if (ws_bytes < need)
         return fail(GDN_ERR_WORKSPACE, "workspace: found %zu bytes, required %zu bytes", ws_bytes, need);
     const cudaStream_t s = (cudaStream_t)stream;
-    gdn::FewJob job = {};
-    job.x = h; job.w = ffn->w_gate; job.w2 = ffn->w_up; job.out = workspace;
-    job.n_tok = n_tok; job.ld = ffn->inter; job.n_out = ffn->inter; job.k = ffn->hidden;
-    const cudaError_t e = gdn::launch_few(job, s);
+    const cudaError_t e = launch_fused(h, ffn->w_gate, ffn->w_up, workspace, n_tok, ffn->inter, ffn->hidden, ffn->inter, false, s);
     if (e != cudaSuccess) return cuda_status(e, "gdn_ffn (gated half)");
-    gdn::FewJob back = {};
-    back.x = workspace; back.w = ffn->w_down; back.out = out; back.early = 1;
-    back.n_tok = n_tok; back.ld = ffn->hidden; back.n_out = ffn->hidden; back.k = ffn->inter;
-    return cuda_status(gdn::launch_few(back, s), "gdn_ffn (projection back)");
+    return cuda_status(launch_fused(workspace, ffn->w_down, nullptr, out, n_tok, ffn->hidden, ffn->inter, ffn->hidden, true, s),
+                       "gdn_ffn (projection back)");
 }
 
 // the tokens' low-rank activations, then their adapters
@@ -1149,14 +1159,26 @@ gdn_status gdn_proj_lora(const void* act, const void* w, const gdn_lora* lora, c
     const cudaStream_t s = (cudaStream_t)stream;
     gdn::LowJob low = {};
     low.x = act; low.a = lora->a; low.scale = lora->scale; low.cu_rows = cu_rows; low.adapter_idx = adapter_idx;
-    low.v = reinterpret_cast<float*>(ws); low.tok_adapter = reinterpret_cast<int32_t*>(ws + L.tok_adapter);
+    low.v = ws; low.tok_adapter = reinterpret_cast<int32_t*>(ws + L.tok_adapter);
     low.n_tok = n_tok; low.n_seg = n_seg; low.n_adapters = lora->n_adapters; low.rank = lora->rank; low.k = k;
-    const cudaError_t e = gdn::launch_lora_low(low, s);
+    // Requests of a few tokens each bring an adapter for (nearly) every token, a matrix product for none: they stay with
+    // the kernel that gives each token its adapter on the CUDA cores.
+    low.wide = n_tok > kFewTokens && n_tok >= 16 * (int64_t)n_seg;
+    cudaError_t e = gdn::launch_lora_low(low, s);
     if (e != cudaSuccess) return cuda_status(e, "gdn_proj_lora (low side)");
+    if (low.wide) {
+        if ((e = gdn::launch_wide_low(low, s)) != cudaSuccess) return cuda_status(e, "gdn_proj_lora (low side)");
+        gdn::WideJob job = {};
+        job.x = act; job.w = w; job.out = out;
+        job.n_tok = n_tok; job.ld = ld_out; job.n_out = n_out; job.k = k;
+        job.v = low.v; job.tok_adapter = low.tok_adapter; job.b = lora->b; job.rank = lora->rank;
+        job.n_adapters = lora->n_adapters;
+        return cuda_status(gdn::launch_wide(job, s), "gdn_proj_lora");
+    }
     gdn::FewJob job = {};
     job.x = act; job.w = w; job.out = out; job.early = 1;
     job.n_tok = n_tok; job.ld = ld_out; job.n_out = n_out; job.k = k;
-    job.v = low.v; job.tok_adapter = low.tok_adapter; job.b = lora->b; job.rank = lora->rank;
+    job.v = static_cast<const float*>(low.v); job.tok_adapter = low.tok_adapter; job.b = lora->b; job.rank = lora->rank;
     return cuda_status(gdn::launch_few(job, s), "gdn_proj_lora");
 }
 

@@ -313,17 +313,37 @@ struct FewJob {
 };
 cudaError_t launch_few(const FewJob& job, cudaStream_t st);
 
-// each token's adapter, and v = scale A x; per_cta is the launcher's
+// the same of many tokens; out 16-byte aligned, ld a multiple of 8
+struct WideJob {
+    const void *x, *w, *w2;
+    void* out;
+    int64_t n_tok, ld;
+    int32_t n_out, k;
+    const void* v;               // bf16 [n_tok][low_row(rank)]
+    const int32_t* tok_adapter;  // [n_tok], -1: none
+    const void* b;               // [n_adapters][n_out][rank]
+    int32_t rank, n_adapters;
+};
+cudaError_t launch_wide(const WideJob& job, cudaStream_t st);
+
+// Low-rank activations for launch_wide: v = hi + lo in bf16, a row of low_row(rank) elements being [hi | lo] in parts
+// of 16 ceil(rank / 16) (rank <= 32) or 64 ceil(rank / 64) elements, each padded with zeros to a multiple of 16.
+constexpr int low_row(int rank) { return rank <= 32 ? 64 : 2 * ((rank + 63) / 64 * 64); }
+constexpr int kLongRequest = 1 << 30;  // in tok_adapter of a wide job: v of this token is launch_wide_low's
+
+// each token's adapter, and v = scale A x: for launch_few of every token (wide 0, fp32 [n_tok][rank]), for launch_wide
+// of the tokens of short requests (wide 1), launch_wide_low behind it of the others; per_cta is the launcher's
 struct LowJob {
     const void *x, *a;
     const float* scale;  // NULL: 1
     const int32_t *cu_rows, *adapter_idx;
-    float* v;              // [n_tok][rank]
+    void* v;
     int32_t* tok_adapter;  // [n_tok], -1: none
     int64_t n_tok;
-    int32_t n_seg, n_adapters, rank, k, per_cta;
+    int32_t n_seg, n_adapters, rank, k, wide, per_cta;
 };
 cudaError_t launch_lora_low(LowJob job, cudaStream_t st);
+cudaError_t launch_wide_low(const LowJob& job, cudaStream_t st);
 
 // GDN_DEBUG: device-side check that the na + nb indices of idx_a then idx_b lie in
 // [0, n_slots) and are distinct.  A violation ORs kDevBadSlot into the device status
@@ -341,6 +361,6 @@ cudaError_t take_device_status_proj(unsigned* out);
 cudaError_t take_device_status_tree(unsigned* out);
 cudaError_t take_device_status_attn_tree(unsigned* out);
 cudaError_t take_device_status_few(unsigned* out);
-cudaError_t take_device_status_lora(unsigned* out);
+cudaError_t take_device_status_wide(unsigned* out);
 
 }  // namespace gdn

@@ -15,6 +15,7 @@ namespace {
 
 constexpr int kLowThreads = 256;
 constexpr int kLowWarps = kLowThreads / 32;
+constexpr int kShortRequest = 16;  // tokens from which on the tensor cores take a request of a wide call
 
 // The request that token t belongs to, or -1: the last s with cu[s] <= t, if t < cu[s+1].  By a whole warp, 32 probes a
 // round; where every request is one token (decoding) the first guess is right.  Any contents of cu stay in bounds.
@@ -42,7 +43,7 @@ __device__ __forceinline__ int request_of(const int32_t* cu, int n, int t, int l
 // v by dot products, a warp for ROWS rows of A at a time: tokens of requests short enough that every token (nearly) reads
 // an adapter of its own, so that there is nothing for a matrix product to share.  Bound by the adapters' bytes, or by the
 // latency of one pass over a row when there are few.
-template <int ROWS>
+template <int ROWS, bool WIDE>
 __global__ void __launch_bounds__(kLowThreads) k_lora_low(const __grid_constant__ LowJob J) {
     __shared__ int s_adapter[kLowWarps];
     griddep_wait();  // launched with programmatic serialization
@@ -57,19 +58,21 @@ __global__ void __launch_bounds__(kLowThreads) k_lora_low(const __grid_constant_
             const int s = request_of(J.cu_rows, J.n_seg, (int)t, lane, len);
             if (s >= 0) a = J.adapter_idx[s];
             if (a < 0 || a >= J.n_adapters) a = -1;
-            if (lane == 0 && blockIdx.y == 0) J.tok_adapter[t] = a;
+            const bool later = J.wide && a >= 0 && len >= kShortRequest;
+            if (lane == 0 && blockIdx.y == 0) J.tok_adapter[t] = later ? a | kLongRequest : a;
+            if (later) a = -1;
         }
         if (lane == 0) s_adapter[warp] = a;
     }
     __syncthreads();
-    const int K = J.k, rank = J.rank;
+    const int K = J.k, rank = J.rank, cols = WIDE ? (rank + 15) / 16 * 16 : rank;
     for (int i = 0; i < J.per_cta; ++i) {
         const int a = s_adapter[i];
         if (a < 0) continue;
         const int64_t t = first + i;
         const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(J.x) + t * K;
         const float scale = J.scale ? J.scale[a] : 1.f;
-        for (int j0 = ((int)blockIdx.y * kLowWarps + warp) * ROWS; j0 < rank; j0 += (int)gridDim.y * kLowWarps * ROWS) {
+        for (int j0 = ((int)blockIdx.y * kLowWarps + warp) * ROWS; j0 < cols; j0 += (int)gridDim.y * kLowWarps * ROWS) {
             const __nv_bfloat16* A = static_cast<const __nv_bfloat16*>(J.a) + ((int64_t)a * rank + j0) * K;
             float acc[ROWS] = {};
 #pragma unroll 4
@@ -92,7 +95,17 @@ __global__ void __launch_bounds__(kLowThreads) k_lora_low(const __grid_constant_
             for (int r = 0; r < ROWS; ++r) {
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) acc[r] += __shfl_xor_sync(0xffffffffu, acc[r], o);
-                if (lane == 0 && j0 + r < rank) J.v[t * rank + j0 + r] = acc[r] * scale;
+                if (lane != 0 || j0 + r >= cols) continue;
+                const float v = j0 + r < rank ? acc[r] * scale : 0.f;
+                if (WIDE) {  // v = hi + lo
+                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(J.v) + t * low_row(rank) + j0 + r;
+                    const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+                    const float h = __bfloat162float(hi);
+                    dst[0] = hi;
+                    dst[rank <= 32 ? cols : low_row(rank) / 2] = __float2bfloat16_rn(isfinite(h) ? v - h : 0.f);
+                } else {
+                    static_cast<float*>(J.v)[t * rank + j0 + r] = v;
+                }
             }
         }
     }
@@ -100,13 +113,16 @@ __global__ void __launch_bounds__(kLowThreads) k_lora_low(const __grid_constant_
 
 }  // namespace
 
-cudaError_t take_device_status_lora(unsigned* out) { return take_device_status_tu(out); }
-
 cudaError_t launch_lora_low(LowJob job, cudaStream_t st) {
     if (job.n_tok == 0) return cudaSuccess;
+    if (job.wide) {
+        job.per_cta = kLowWarps;
+        const dim3 grid((unsigned)((job.n_tok + kLowWarps - 1) / kLowWarps));
+        return launch_pdl(k_lora_low<2, true>, grid, dim3(kLowThreads), 0, st, job);
+    }
     job.per_cta = 1;
     const dim3 grid((unsigned)job.n_tok, (unsigned)((job.rank + kLowWarps - 1) / kLowWarps));
-    return launch_pdl(k_lora_low<1>, grid, dim3(kLowThreads), 0, st, job);
+    return launch_pdl(k_lora_low<1, false>, grid, dim3(kLowThreads), 0, st, job);
 }
 
 }  // namespace gdn
