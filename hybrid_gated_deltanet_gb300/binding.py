@@ -487,6 +487,7 @@ def _load_marshal():
                            "`python -m hybrid_gated_deltanet_gb300.build`")
     from . import _marshal
     _marshal.explain(_explain)
+    _marshal.explain_rows(_explain_rows)
     return _marshal
 
 
@@ -630,17 +631,19 @@ def gdn_rope_plan(cfg: RopeConfig) -> CRopePlan:
     return plan
 
 
-def _rows(t, name, dtype, n, head_dim, device):
-    """Address, elements between tokens and heads of [n, heads, head_dim] whose tokens may lie inside wider rows."""
+def _explain_rows(t, name, dtype, n, head_dim, device):
     if t.get_device() != device or t.dtype is not dtype or t.dim() != 3 or t.shape[0] != n or t.shape[2] != head_dim:
         _explain(t, name, dtype, (n, t.shape[1] if t.dim() == 3 else -1, head_dim), device)
-    heads, (ld, per_head, one) = t.shape[1], t.stride()
-    if n <= 1 or heads == 0:
-        ld = heads * head_dim  # (a stride that is never taken)
-    if one != 1 or (heads > 1 and per_head != head_dim) or ld < heads * head_dim:
-        raise ValueError(f"{name}: found strides {t.stride()}, required dense heads, tokens at least "
-                         f"{heads * head_dim} elements apart")
-    return t.data_ptr(), ld, heads
+    raise ValueError(f"{name}: found strides {t.stride()}, required dense heads, tokens at least "
+                     f"{t.shape[1] * head_dim} elements apart")
+
+
+def _rows(*args):
+    """Address, elements between tokens and heads of [n, heads, head_dim] whose tokens may lie inside wider rows: (tensor, name,
+    dtype, n, head_dim, device)."""
+    global _rows
+    _rows = _load_marshal().rows
+    return _rows(*args)
 
 
 def gdn_rope(plan: CRopePlan, positions, q, k, q_out=None, k_out=None, stream=None):
@@ -648,22 +651,22 @@ def gdn_rope(plan: CRopePlan, positions, q, k, q_out=None, k_out=None, stream=No
     into q_out, k_out (None: in place)."""
     dev, n = _device(positions, "positions"), positions.shape[0]
     dtype, D = _bf16 if plan.act_dtype == BF16 else _f32, plan.head_dim
-    args = []
-    for name, x, out in (("q", q, q_out), ("k", k, k_out)):
-        if x is None:
-            if out is not None:
-                raise ValueError(f"{name}_out: found a tensor, required None without {name}")
-            args += [None, 0, 0, None, 0]
-            continue
-        p, ld, heads = _rows(x, name, dtype, n, D, dev)
-        if out is None:
-            args += [p, ld, heads, p, ld]
-            continue
-        po, ldo, heads_out = _rows(out, name + "_out", dtype, n, D, dev)
-        if heads_out != heads:
-            raise ValueError(f"{name}_out: found {heads_out} heads, required {heads}")
-        args += [p, ld, heads, po, ldo]
-    _call(load().gdn_rope, dev, stream, ctypes.byref(plan), _ptr(positions, "positions", _i32, (n,), dev), n, *args)
+    pq = pqo = pk = pko = None
+    ldq = ldqo = hq = ldk = ldko = hkv = 0
+    if q is not None:
+        pqo, ldqo, hq = pq, ldq, _ = _rows(q, "q", dtype, n, D, dev)
+    if k is not None:
+        pko, ldko, hkv = pk, ldk, _ = _rows(k, "k", dtype, n, D, dev)
+    if q_out is not None:
+        pqo, ldqo, heads = _rows(q_out, "q_out", dtype, n, D, dev)
+        if heads != hq or q is None:
+            raise ValueError(f"q_out: found {heads} heads, required {'None without q' if q is None else hq}")
+    if k_out is not None:
+        pko, ldko, heads = _rows(k_out, "k_out", dtype, n, D, dev)
+        if heads != hkv or k is None:
+            raise ValueError(f"k_out: found {heads} heads, required {'None without k' if k is None else hkv}")
+    _call(load().gdn_rope, dev, stream, ctypes.byref(plan), _ptr(positions, "positions", _i32, (n,), dev), n, pq, ldq, hq,
+          pqo, ldqo, pk, ldk, hkv, pko, ldko)
 
 
 def _workspace(workspace, dev):

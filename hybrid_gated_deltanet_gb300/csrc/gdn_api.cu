@@ -1179,6 +1179,7 @@ gdn_status gdn_proj_lora(const void* act, const void* w, const gdn_lora* lora, c
     job.x = act; job.w = w; job.out = out; job.early = 1;
     job.n_tok = n_tok; job.ld = ld_out; job.n_out = n_out; job.k = k;
     job.v = static_cast<const float*>(low.v); job.tok_adapter = low.tok_adapter; job.b = lora->b; job.rank = lora->rank;
+    job.n_adapters = lora->n_adapters;
     return cuda_status(gdn::launch_few(job, s), "gdn_proj_lora");
 }
 

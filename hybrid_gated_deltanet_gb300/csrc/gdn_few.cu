@@ -62,7 +62,7 @@ struct FewArgs {
     const float* v;            // [n_tok][rank]
     const int32_t* tok_adapter;  // [n_tok], -1: none
     const __nv_bfloat16* b;    // [n_adapters][n_out][rank]
-    int32_t rank;
+    int32_t rank, n_adapters;
 };
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             };
             const int ahead = min(S, kb1 - kb0);
             for (int i = 0; i < ahead; ++i) weights(kb0 + i, i);
-            if (P.early) griddep_wait();
+            if (P.early && MODE != kLora) griddep_wait();  // (lora: only v and the adapters come from the kernel ahead)
             for (int i = 0; i < ahead; ++i) tokens(kb0 + i, i);
             for (int i = ahead; i < kb1 - kb0; ++i) {
                 const int s = i % S;
@@ -184,13 +184,11 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 weights(kb0 + i, s);
                 tokens(kb0 + i, s);
             }
-        } else if (P.early) {
+        } else if (P.early && MODE != kLora) {
             griddep_wait();
         }
-        griddep_launch_dependents();
     } else if (warp == 1) {
-        if (P.early) griddep_wait();
-        griddep_launch_dependents();
+        if (P.early && MODE != kLora) griddep_wait();
         if (lane == 0) {
             constexpr uint32_t idesc = idesc_bf16(kFewM, N);
             for (int i = 0; i < kb1 - kb0; ++i) {
@@ -215,7 +213,10 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         const int row = 32 * q4 + lane;
         const int mine = ncol > rank ? (ncol - rank + ks - 1) / ks : 0;  // tokens rank, rank + ks, ... are finished here
         if (MODE == kLora) {
-            for (int c = tid - 64; c < N; c += 128) adapter[c] = c < ncol ? P.tok_adapter[t0 + c] : -1;
+            for (int c = tid - 64; c < N; c += 128) {
+                const int a = c < ncol ? P.tok_adapter[t0 + c] : -1;
+                adapter[c] = a < P.n_adapters ? a : -1;
+            }
             named_bar_sync(1, 128);
             for (int i0 = 0; i0 < mine; i0 += 2 * kTok) {
                 float d[2 * kTok];
@@ -323,6 +324,7 @@ cudaError_t launch_few_n(const FewJob& job, int ks, cudaStream_t st) {
     P.tok_adapter = job.tok_adapter;
     P.b = static_cast<const __nv_bfloat16*>(job.b);
     P.rank = job.rank;
+    P.n_adapters = job.n_adapters;
     const unsigned tiles = (unsigned)((job.n_out + rows - 1) / rows);
     return launch_pdl_cluster(k_few<N, MODE>, dim3(tiles * ks, (unsigned)((job.n_tok + N - 1) / N)), dim3(kFewThreads),
                               L::SMEM_ALLOC, ks, st, mw, mw2, mx, P);

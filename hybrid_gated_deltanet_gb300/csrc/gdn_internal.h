@@ -283,7 +283,7 @@ struct AppendJob {
 cudaError_t launch_append(const AppendJob& job, cudaStream_t st);
 
 // ---- around the attention and the projections ----
-// rotary positions of rows of q and k (out == in: in place); pieces and step_h are the launcher's
+// rotary positions of rows of q and k (out == in: in place); pieces and per_cta are the launcher's
 struct RopeJob {
     const void *q, *k;
     void *q_out, *k_out;
@@ -291,7 +291,7 @@ struct RopeJob {
     const int32_t* positions;
     int64_t n_tok;
     int hq, hkv, D, rot, half, bf16;
-    int pieces, step_h;
+    int pieces, per_cta;
     float mscale;
     unsigned long long turns[128];  // turns per position of pair i, in units of 2^-64
 };
@@ -309,7 +309,7 @@ struct FewJob {
     const float* v;              // [n_tok][rank]
     const int32_t* tok_adapter;  // [n_tok], -1: none
     const void* b;               // [n_adapters][n_out][rank]
-    int32_t rank;
+    int32_t rank, n_adapters;
 };
 cudaError_t launch_few(const FewJob& job, cudaStream_t st);
 
@@ -332,7 +332,7 @@ constexpr int low_row(int rank) { return rank <= 32 ? 64 : 2 * ((rank + 63) / 64
 constexpr int kLongRequest = 1 << 30;  // in tok_adapter of a wide job: v of this token is launch_wide_low's
 
 // each token's adapter, and v = scale A x: for launch_few of every token (wide 0, fp32 [n_tok][rank]), for launch_wide
-// of the tokens of short requests (wide 1), launch_wide_low behind it of the others; per_cta is the launcher's
+// of the tokens of short requests (wide 1), launch_wide_low behind it of the others
 struct LowJob {
     const void *x, *a;
     const float* scale;  // NULL: 1
@@ -340,9 +340,9 @@ struct LowJob {
     void* v;
     int32_t* tok_adapter;  // [n_tok], -1: none
     int64_t n_tok;
-    int32_t n_seg, n_adapters, rank, k, wide, per_cta;
+    int32_t n_seg, n_adapters, rank, k, wide;
 };
-cudaError_t launch_lora_low(LowJob job, cudaStream_t st);
+cudaError_t launch_lora_low(const LowJob& job, cudaStream_t st);
 cudaError_t launch_wide_low(const LowJob& job, cudaStream_t st);
 
 // GDN_DEBUG: device-side check that the na + nb indices of idx_a then idx_b lie in

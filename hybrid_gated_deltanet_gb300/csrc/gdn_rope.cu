@@ -21,7 +21,7 @@ namespace gdn {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeHeads = 4;  // heads whose loads a thread has in flight
+constexpr int kRopeUnroll = 4;  // pieces whose loads a thread has in flight
 
 // 8 consecutive elements
 template <typename T>
@@ -69,69 +69,75 @@ struct Eight<float> {
     }
 };
 
-// A thread owns one piece of 16 elements of a token's heads: 8 pairs of the rotated part (two runs of 8 elements, rot / 2
-// apart or side by side), or 16 bytes x 2 of the rest, which is only copied and only where the result goes elsewhere.
-// It makes its 8 angles once and walks over every step_h-th head, kRopeHeads at a time: with every thread making angles for
-// one head, sine and cosine alone would take as long as the memory.  Pieces are fastest among the threads, then heads, so
-// that a warp's accesses are contiguous.  step_h > 1 splits the heads of few tokens over more threads.
+// A CTA takes a few tokens: its threads make their sines and cosines once, into shared memory, and then rotate the heads
+// from there.  (With every thread making its own angles for one head, sine and cosine took longer than the memory; with a
+// thread walking over the heads of one angle, few tokens leave the GPU empty.)  The unit of work is a piece of 16 elements of a head: 8 pairs
+// of the rotated part (two runs of 8 elements, rot / 2 apart or side by side), or 16 elements of the rest, which are only
+// copied and only where the result goes elsewhere.  Pieces are fastest among the threads, then heads, so that a warp's
+// accesses are contiguous; the first loads are under way while the angles are made.
 template <typename T>
 __global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ RopeJob J) {
-    __shared__ unsigned long long turns[128];
-    griddep_wait();  // launched with programmatic serialization
+    extern __shared__ float2 angle[];  // [token][rot / 2]: cosine and sine
+    griddep_wait();                    // launched with programmatic serialization
     griddep_launch_dependents();
-    if (threadIdx.x < J.rot / 2) turns[threadIdx.x] = J.turns[threadIdx.x];
-    __syncthreads();
-    const int pieces = J.pieces, pairs = J.rot / 16;
-    const int64_t at = (int64_t)blockIdx.x * kRopeThreads + threadIdx.x;
-    const int64_t row = at / pieces;
-    const int u = (int)(at - row * pieces);
-    const int64_t tok = row / J.step_h;
-    if (tok >= J.n_tok) return;
-    const int h0 = (int)(row - tok * J.step_h), heads = J.hq + J.hkv;
-    const bool turn = u < pairs, half = J.half != 0;
-    // the two runs of 8 elements
-    int e0, e1;
-    if (turn) {
-        e0 = half ? 8 * u : 16 * u;
-        e1 = half ? 8 * u + J.rot / 2 : 16 * u + 8;
-    } else {
-        e0 = J.rot + 16 * (u - pairs);
-        e1 = e0 + 8;
-    }
-    const bool two = e1 < J.D;  // (a head's rest may end on a single run)
-    float c[8], s[8];
-    if (turn) {
-        const unsigned long long p = (unsigned long long)(long long)J.positions[tok];
+    const int pieces = J.pieces, pairs = J.rot / 16, heads = J.hq + J.hkv, half_rot = J.rot / 2;
+    const int64_t first = (int64_t)blockIdx.x * J.per_cta;
+    const int n = (int)(J.n_tok - first < J.per_cta ? J.n_tok - first : J.per_cta);
+    const int items = n * heads * pieces, step = (int)gridDim.y * kRopeThreads;
+    bool ready = false;
+    for (int i0 = (int)blockIdx.y * kRopeThreads + (int)threadIdx.x; !ready || i0 < items; i0 += kRopeUnroll * step) {
+        Eight<T> x[kRopeUnroll], y[kRopeUnroll];
+        T* dst[kRopeUnroll];
+        int at[kRopeUnroll], e1[kRopeUnroll];  // the angles (-1: none), the second run's distance (0: none)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int t = (int)(unsigned)((p * turns[8 * u + j]) >> 32);
-            sincospif((float)t * 0x1p-31f, &s[j], &c[j]);
-            c[j] *= J.mscale;
-            s[j] *= J.mscale;
+        for (int e = 0; e < kRopeUnroll; ++e) {
+            const int i = i0 + e * step;
+            dst[e] = nullptr;
+            if (i >= items) continue;
+            const int row = i / pieces, u = i - row * pieces, t = row / heads, h = row - t * heads;
+            const int64_t tok = first + t;
+            int e0;
+            if (u < pairs) {
+                e0 = J.half ? 8 * u : 16 * u;
+                e1[e] = J.half ? half_rot : 8;
+                at[e] = t * half_rot + 8 * u;
+            } else {
+                e0 = J.rot + 16 * (u - pairs);
+                e1[e] = e0 + 8 < J.D ? 8 : 0;  // (a head's rest may end on a single run)
+                at[e] = -1;
+            }
+            const bool q = h < J.hq;
+            const int64_t off = (int64_t)(q ? h : h - J.hq) * J.D + e0;
+            const T* src = static_cast<const T*>(q ? J.q : J.k) + tok * (q ? J.ldq : J.ldk) + off;
+            dst[e] = static_cast<T*>(q ? J.q_out : J.k_out) + tok * (q ? J.ldqo : J.ldko) + off;
+            x[e].ld(src);
+            if (e1[e]) y[e].ld(src + e1[e]);
         }
-    }
-    for (int hb = h0; hb < heads; hb += kRopeHeads * J.step_h) {
-        Eight<T> x[kRopeHeads], y[kRopeHeads];
-#pragma unroll
-        for (int e = 0; e < kRopeHeads; ++e) {
-            const int h = hb + e * J.step_h;
-            if (h >= heads) continue;
-            const T* src = h < J.hq ? static_cast<const T*>(J.q) + tok * J.ldq + (int64_t)h * J.D
-                                    : static_cast<const T*>(J.k) + tok * J.ldk + (int64_t)(h - J.hq) * J.D;
-            x[e].ld(src + e0);
-            if (two) y[e].ld(src + e1);
+        if (!ready) {
+            for (int j = threadIdx.x; j < n * half_rot; j += kRopeThreads) {
+                const int t = j / half_rot;
+                const unsigned long long p = (unsigned long long)(long long)J.positions[first + t];
+                const int turn = (int)(unsigned)((p * J.turns[j - t * half_rot]) >> 32);
+                float s, c;
+                sincospif((float)turn * 0x1p-31f, &s, &c);
+                angle[j] = make_float2(c * J.mscale, s * J.mscale);
+            }
+            __syncthreads();
+            ready = true;
         }
 #pragma unroll
-        for (int e = 0; e < kRopeHeads; ++e) {
-            const int h = hb + e * J.step_h;
-            if (h >= heads) continue;
-            T* dst = h < J.hq ? static_cast<T*>(J.q_out) + tok * J.ldqo + (int64_t)h * J.D
-                              : static_cast<T*>(J.k_out) + tok * J.ldko + (int64_t)(h - J.hq) * J.D;
-            if (turn) {
-                float a[8], b[8];
+        for (int e = 0; e < kRopeUnroll; ++e) {
+            if (!dst[e]) continue;
+            if (at[e] >= 0) {
+                float a[8], b[8], c[8], s[8];
                 x[e].get(a);
                 y[e].get(b);
-                if (half) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float4 w = *reinterpret_cast<const float4*>(angle + at[e] + 2 * j);
+                    c[2 * j] = w.x, s[2 * j] = w.y, c[2 * j + 1] = w.z, s[2 * j + 1] = w.w;
+                }
+                if (J.half) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const float a1 = a[j] * c[j] - b[j] * s[j];
@@ -152,8 +158,8 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ R
                 x[e].set(a);
                 y[e].set(b);
             }
-            x[e].st(dst + e0);
-            if (two) y[e].st(dst + e1);
+            x[e].st(dst[e]);
+            if (e1[e]) y[e].st(dst[e] + e1[e]);
         }
     }
 }
@@ -188,13 +194,16 @@ cudaError_t launch_rope(RopeJob job, cudaStream_t st) {
     if (job.n_tok == 0 || heads == 0) return cudaSuccess;
     const bool same = job.q == job.q_out && job.k == job.k_out;
     job.pieces = job.rot / 16 + (same ? 0 : (job.D - job.rot + 15) / 16);
-    // one thread per piece and token walks all heads once that fills the GPU (2048 threads an SM); fewer tokens split the heads
-    const int64_t full = (int64_t)sm_count() * 2048, one = job.n_tok * job.pieces;
-    job.step_h = (int)std::min<int64_t>(heads, std::max<int64_t>(1, full / one));
-    const int64_t threads = one * job.step_h;
-    const dim3 grid((unsigned)((threads + kRopeThreads - 1) / kRopeThreads));
-    return job.bf16 ? launch_pdl(k_rope<__nv_bfloat16>, grid, dim3(kRopeThreads), 0, st, job)
-                    : launch_pdl(k_rope<float>, grid, dim3(kRopeThreads), 0, st, job);
+    // Tokens of a CTA: angles for its threads to make and a few pieces for each of them; one token where the tokens would not
+    // fill the GPU's CTAs (8 an SM) otherwise.  A token of very many pieces is shared by CTAs along y.
+    const int per_token = heads * job.pieces;
+    job.per_cta = std::max(1, std::min(2 * kRopeThreads / job.rot, 4 * kRopeThreads / per_token));
+    if (job.n_tok < (int64_t)sm_count() * 8 * job.per_cta) job.per_cta = 1;
+    const dim3 grid((unsigned)((job.n_tok + job.per_cta - 1) / job.per_cta),
+                    (unsigned)((job.per_cta * per_token + 8 * kRopeThreads - 1) / (8 * kRopeThreads)));
+    const size_t smem = (size_t)job.per_cta * (job.rot / 2) * sizeof(float2);
+    return job.bf16 ? launch_pdl(k_rope<__nv_bfloat16>, grid, dim3(kRopeThreads), smem, st, job)
+                    : launch_pdl(k_rope<float>, grid, dim3(kRopeThreads), smem, st, job);
 }
 
 }  // namespace gdn

@@ -1,7 +1,7 @@
 // gdn_wide.cu -- projections of many tokens with a fused end (the same three as gdn_few.cu: plain, gated, lora), on
 // pairs of SMs.
 //
-// A tile is 256 tokens x bn accumulator columns.  The two CTAs of a cluster make it together (tcgen05 cta_group::2): each
+// A tile is 256 tokens x 256 accumulator columns.  The two CTAs of a cluster make it together (tcgen05 cta_group::2): each
 // holds 128 of the tokens (its TMEM lanes) and loads half of the weight rows, which the MMA reads from both shared
 // memories, so that a weight row is fetched once per 256 tokens and each SM's shared memory is read at half the rate
 // of two tiles on their own.
@@ -9,7 +9,7 @@
 //   warp 1      MMA issuer (the first CTA's; it commits to both CTAs' barriers)
 //   warps 2..5  epilogue: accumulator -> registers -> bf16 -> shared memory -> TMA store, a token a thread; the other
 //               half of TMEM takes the next tile meanwhile
-// gated: the first CTA loads rows of w_gate and the second the same rows of w_up, so that columns c and c + bn / 2 of
+// gated: the first CTA loads rows of w_gate and the second the same rows of w_up, so that columns c and c + 128 of
 // the accumulator are a gate and its value, in one thread.
 // lora: after the K blocks of x and w come, for each adapter that the tile's tokens use, those of the low-rank
 // activations v and of the adapter's b.  The MMA leaves the lanes of all other tokens as they are (its lane mask), so
@@ -47,7 +47,10 @@ struct WideArgs {
     int64_t n_tok, n_tiles;
     int32_t n_out;
     int32_t kb;          // 64-wide K blocks
-    int32_t bn;          // accumulator columns: 128, 192 or 256 (gated: 128 or 256)
+    // Tiles from n_whole on, which would leave pairs idle in a last wave of their own, are cut into `cut` parts of 256 / cut
+    // columns each: tile n_whole + i is part i % cut of whole tile n_whole + i / cut.
+    int64_t n_whole;
+    int32_t cut;
     int32_t tiles_n, tiles_t;
     int32_t token_fast;  // tile order: token blocks fastest (1) or weight blocks fastest (0)
     int32_t n_full;      // columns that go by TMA: n_out rounded down to 16 bytes
@@ -55,7 +58,7 @@ struct WideArgs {
     int64_t ld;
     // lora
     const int32_t* tok_adapter;
-    int32_t rank;
+    int32_t rank, n_adapters;
 };
 
 __device__ __forceinline__ void mma2_bf16(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc) {
@@ -120,8 +123,22 @@ __device__ __forceinline__ void dealloc2(uint32_t taddr, uint32_t ncols) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
-// tile -> (weight block, token block); the smaller operand goes fastest, it is the one that every sweep reads again
-__device__ __forceinline__ void wide_coords(const WideArgs& P, int64_t tile, int& wn, int& tt) {
+// What a tile covers.  The smaller operand goes fastest, it is the one that every sweep reads again.
+struct Tile {
+    int tt;       // token block
+    int half;     // weight rows of one CTA: half the accumulator's columns
+    int wrow;     // gated: first row of both matrices; else first weight row of the first CTA
+    bool narrow;  // cut: another box of weight rows
+};
+__device__ __forceinline__ Tile wide_tile(const WideArgs& P, int64_t tile, bool gated) {
+    int part = 0, cut = 1;
+    const bool narrow = tile >= P.n_whole && P.cut > 1;
+    if (narrow) {
+        cut = P.cut;
+        part = (int)((tile - P.n_whole) % cut);
+        tile = P.n_whole + (tile - P.n_whole) / cut;
+    }
+    int wn, tt;
     if (P.token_fast) {
         wn = (int)(tile / P.tiles_t);
         tt = (int)(tile % P.tiles_t);
@@ -129,6 +146,8 @@ __device__ __forceinline__ void wide_coords(const WideArgs& P, int64_t tile, int
         wn = (int)(tile % P.tiles_n);
         tt = (int)(tile / P.tiles_n);
     }
+    const int half = 128 / cut;
+    return Tile{tt, half, gated ? wn * 128 + part * half : wn * 256 + part * 2 * half, narrow};
 }
 
 // The adapters that a tile's 256 tokens use, by a whole warp: lane l holds those of tokens l, l + 32, ...
@@ -139,8 +158,8 @@ struct TileAdapters {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int64_t t = (int64_t)tt * kWideTok + 32 * j + lane;
-            const int v = t < P.n_tok ? P.tok_adapter[t] : -1;
-            a[j] = v < 0 ? -1 : v & ~kLongRequest;
+            const int v = t < P.n_tok ? P.tok_adapter[t] : -1, e = v & ~kLongRequest;
+            a[j] = v >= 0 && e < P.n_adapters ? e : -1;
         }
     }
     // the next one in ascending order (INT_MAX: no more)
@@ -168,8 +187,10 @@ __device__ __forceinline__ uint4 pack8(const float v[8]) {
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     k_wide(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw,
-           const __grid_constant__ CUtensorMap tw2, const __grid_constant__ CUtensorMap tout,
-           const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tb, const __grid_constant__ WideArgs P) {
+           const __grid_constant__ CUtensorMap tw2, const __grid_constant__ CUtensorMap twn,
+           const __grid_constant__ CUtensorMap tw2n, const __grid_constant__ CUtensorMap tout,
+           const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tb,
+           const __grid_constant__ CUtensorMap tbn, const __grid_constant__ WideArgs P) {
     constexpr int S = kWideStages;
     griddep_wait();  // launched with programmatic serialization: nothing is held while kernels ahead still run
     extern __shared__ unsigned char smem_raw[];
@@ -204,28 +225,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     const uint32_t tm = *tslot;
     bool ok = true;
 
-    const int bn = P.bn, half = bn / 2;
-    const int cols = MODE == kGated ? half : bn;  // output columns of a tile
-    const uint32_t stage_tx = 2u * (uint32_t)(kHalfBytes + half * kWideK * 2);
     // blocks of v and b for an adapter: up to 32 ranks as one 64-wide block [hi | lo], else blocks of hi, then of lo
     const int rp = (P.rank + 15) / 16, nb = P.rank <= 32 ? 1 : 2 * ((P.rank + 63) / 64);
 
     if (warp == 0) {
         uint32_t it = 0;
         // waits for the stage's turn; the first CTA's barrier expects both CTAs' bytes
-        auto turn = [&](int s) {
+        auto turn = [&](int s, int half) {
             const bool w = mbar_wait(empty + s, ((it / S) & 1u) ^ 1u);
             ok = __all_sync(0xffffffffu, w);
-            if (ok && cta == 0 && lane == 0) mbar_arrive_expect_tx(full + s, stage_tx);
+            if (ok && cta == 0 && lane == 0)
+                mbar_arrive_expect_tx(full + s, 2u * (uint32_t)(kHalfBytes + half * kWideK * 2));
         };
         for (int64_t tile = tile0; tile < P.n_tiles && ok; tile += tstep) {
-            int wn, tt;
-            wide_coords(P, tile, wn, tt);
-            const int row = tt * kWideTok + 128 * cta, wrow = MODE == kGated ? wn * half : wn * bn + half * cta;
-            const void* wmap = MODE == kGated && cta == 1 ? &tw2 : &tw;
+            const Tile T = wide_tile(P, tile, MODE == kGated);
+            const int row = T.tt * kWideTok + 128 * cta, wrow = MODE == kGated ? T.wrow : T.wrow + T.half * cta;
+            const void* wmap = MODE == kGated && cta == 1 ? (T.narrow ? &tw2n : &tw2) : T.narrow ? &twn : &tw;
             for (int kb = 0; kb < P.kb && ok; ++kb, ++it) {
                 const int s = (int)(it % S);
-                turn(s);
+                turn(s, T.half);
                 if (ok && lane == 0) {
                     unsigned char* st = sm + s * kStageBytes;
                     const uint32_t bar = mapa_shared(smem_u32(full + s), 0);
@@ -235,26 +253,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
             }
             if (MODE == kLora && ok) {
                 TileAdapters ta;
-                ta.load(P, tt, lane);
+                ta.load(P, T.tt, lane);
                 for (int a = ta.next(); a != 0x7fffffff && ok; a = ta.next())
                     for (int j = 0; j < nb && ok; ++j, ++it) {
                         const int s = (int)(it % S);
-                        turn(s);
+                        turn(s, T.half);
                         if (ok && lane == 0) {
                             unsigned char* st = sm + s * kStageBytes;
                             const uint32_t bar = mapa_shared(smem_u32(full + s), 0);
                             tma2_2d(st, &tv, j * kWideK, row, bar);
-                            tma2_3d(st + kHalfBytes, &tb, (nb > 1 ? j % (nb / 2) : 0) * kWideK, wrow, a, bar);
+                            tma2_3d(st + kHalfBytes, T.narrow ? &tbn : &tb, (nb > 1 ? j % (nb / 2) : 0) * kWideK, wrow, a, bar);
                         }
                     }
             }
         }
     } else if (warp == 1) {
         if (cta == 0) {
-            const uint32_t idesc = idesc_bf16(256, bn);
             uint32_t it = 0, use = 0;
             for (int64_t tile = tile0; tile < P.n_tiles && ok; tile += tstep, ++use) {
                 const uint32_t buf = use & 1u;
+                const Tile T = wide_tile(P, tile, MODE == kGated);
+                const uint32_t idesc = idesc_bf16(256, 2 * T.half);
                 ok = __all_sync(0xffffffffu, mbar_wait(acc_empty + buf, ((use >> 1) & 1u) ^ 1u));
                 if (!ok) break;
                 tc::fence_after();
@@ -275,10 +294,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                     __syncwarp();
                 }
                 if (MODE == kLora && ok) {
-                    int wn, tt;
-                    wide_coords(P, tile, wn, tt);
                     TileAdapters ta;
-                    ta.load(P, tt, lane);
+                    ta.load(P, T.tt, lane);
                     for (int a = ta.next(); a != 0x7fffffff && ok; a = ta.next()) {
                         uint32_t off[8];
 #pragma unroll
@@ -315,12 +332,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
         uint32_t use = 0, n_store = 0;
         for (int64_t tile = tile0; tile < P.n_tiles; tile += tstep, ++use) {
             const uint32_t buf = use & 1u;
-            int wn, tt;
-            wide_coords(P, tile, wn, tt);
+            const Tile T = wide_tile(P, tile, MODE == kGated);
+            const int half = T.half, cols = MODE == kGated ? half : 2 * half;  // output columns of the tile
             ok = __all_sync(0xffffffffu, mbar_wait(acc_full + buf, (use >> 1) & 1u));
             if (!ok) break;
             tc::fence_after();
-            const int t0 = tt * kWideTok + 128 * cta + 32 * q4, n0 = wn * cols;
+            const int t0 = T.tt * kWideTok + 128 * cta + 32 * q4, n0 = T.wrow;
             for (int c0 = 0; c0 < cols; c0 += 64) {
                 unsigned char* dst = store + (n_store & 1u) * kStoreBytes + lane * 128;
                 // the store before the last has read this buffer
@@ -376,20 +393,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
 }
 
 // ---- v = scale A x of the long requests ---------------------------------------------------------------
-// One CTA per 128 tokens (TMEM lanes) with the rank as the MMA's N side; as above, an adapter's MMAs leave the lanes of
-// other tokens alone.  Bound by the tokens' bytes; the tokens of several adapters in one tile are read once for each.
-constexpr int kLowStages = 6;
+// A cluster per 128 tokens (TMEM lanes), the rank being the MMA's N side; as above, an adapter's MMAs leave the lanes of
+// other tokens alone.  The product is small and its tokens are read once per adapter of a tile, so it is bound by how many
+// loads are in flight: K is split over the cluster until the GPU is full, and the fp32 parts are joined through
+// distributed shared memory in the order of the ranks, each CTA finishing its share of the tokens.
+constexpr int kLowStages = 4;
 constexpr int kLowStage = 2 * kHalfBytes;
 constexpr int kLowBar = kLowStages * kLowStage;  // full[S], empty[S], done, TMEM address
 constexpr int kLowSmem = kLowBar + (2 * kLowStages + 1) * 8 + 8 + 1024;
-static_assert(kLowSmem <= 227 * 1024, "shared memory of a CTA");
+static_assert(128 * 128 * 4 <= kLowBar, "a partial block over the ring");
 
 struct WideLowArgs {
     int64_t n_tok;
     const int32_t* tok_adapter;
     const float* scale;
     __nv_bfloat16* v;
-    int32_t kb, rank;
+    int32_t kb, rank, ks, n_adapters;
 };
 
 __device__ __forceinline__ void mma_bf16_lanes(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t acc,
@@ -422,8 +441,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     uint64_t* done = empty + S;
     uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rp = (P.rank + 15) / 16 * 16;
-    const int64_t t0 = (int64_t)blockIdx.x * 128;
+    const int rp = (P.rank + 15) / 16 * 16, ks = P.ks, rank = (int)(blockIdx.x % ks);
+    const int64_t t0 = (int64_t)(blockIdx.x / ks) * 128;
+    const int kb0 = (int)((int64_t)rank * P.kb / ks), kb1 = (int)((int64_t)(rank + 1) * P.kb / ks);
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(full + s, 1);
@@ -441,13 +461,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     bool ok = true;
 
     // the adapters of the tile's long requests: lane l holds those of tokens l, l + 32, ...
+    auto adapter_of = [&](int64_t t) {
+        const int v = t < P.n_tok ? P.tok_adapter[t] : -1, e = v & ~kLongRequest;
+        return v >= 0 && (v & kLongRequest) && e < P.n_adapters ? e : -1;
+    };
     int a[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int64_t t = t0 + 32 * j + lane;
-        const int v = t < P.n_tok ? P.tok_adapter[t] : -1;
-        a[j] = v >= 0 && (v & kLongRequest) ? v & ~kLongRequest : -1;
-    }
+    for (int j = 0; j < 4; ++j) a[j] = adapter_of(t0 + 32 * j + lane);
     auto next = [&](int last) {
         int m = 0x7fffffff;
 #pragma unroll
@@ -455,12 +475,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             if (a[j] > last) m = min(m, a[j]);
         return (int)__reduce_min_sync(0xffffffffu, m);
     };
-    const int first = next(-1);
+    const int first = next(-1);  // the same in every warp of the cluster
 
     if (warp == 0) {
         uint32_t it = 0;
         for (int e = first; e != 0x7fffffff && ok; e = next(e))
-            for (int kb = 0; kb < P.kb; ++kb, ++it) {
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int s = (int)(it % S);
                 ok = __all_sync(0xffffffffu, mbar_wait(empty + s, ((it / S) & 1u) ^ 1u));
                 if (!ok) break;
@@ -478,7 +498,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             uint32_t off[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) off[j] = ~__ballot_sync(0xffffffffu, a[j] == e);
-            for (int kb = 0; kb < P.kb; ++kb, ++it) {
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int s = (int)(it % S);
                 ok = __all_sync(0xffffffffu, mbar_wait(full + s, (it / S) & 1u));
                 if (!ok) break;
@@ -488,7 +508,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
                     for (int k16 = 0; k16 < kWideK / 16; ++k16)
                         mma_bf16_lanes(tm, tc::sdesc(a0 + k16 * 32), tc::sdesc(b0 + k16 * 32), idesc,
-                                       kb > 0 || k16 > 0 ? 1u : 0u, off);
+                                       kb > kb0 || k16 > 0 ? 1u : 0u, off);
                     tc::commit(empty + s);
                 }
                 __syncwarp();
@@ -501,30 +521,56 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(done, 0));
         if (ok) {
             tc::fence_after();
-            const int e = q4 == 0 ? a[0] : q4 == 1 ? a[1] : q4 == 2 ? a[2] : a[3];
-            const float scale = e >= 0 && P.scale ? P.scale[e] : 1.f;
-            const int lo = P.rank <= 32 ? rp : (P.rank + 63) / 64 * 64, row = low_row(P.rank);
-            __nv_bfloat16* dst = P.v + (t0 + 32 * q4 + lane) * row;
+            float* red = reinterpret_cast<float*>(sm) + 32 * q4 + lane;  // [column][128 tokens]
             for (int c0 = 0; c0 < rp; c0 += 16) {
-                float v[16], l[16];
+                float v[16];
                 tc::ld16(tc::taddr(tm, 32 * q4, c0), v);
-                if (e < 0) continue;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    v[i] *= scale;
-                    const float h = __bfloat162float(__float2bfloat16_rn(v[i]));
-                    l[i] = isfinite(h) ? v[i] - h : 0.f;
-                }
-                *reinterpret_cast<uint4*>(dst + c0) = pack8(v);
-                *reinterpret_cast<uint4*>(dst + c0 + 8) = pack8(v + 8);
-                *reinterpret_cast<uint4*>(dst + lo + c0) = pack8(l);
-                *reinterpret_cast<uint4*>(dst + lo + c0 + 8) = pack8(l + 8);
+                for (int i = 0; i < 16; ++i) red[(c0 + i) * 128] = v[i];
             }
         }
     }
     tc::fence_before();
     const int bad = __syncthreads_or(!ok);
     if (bad && tid == 0) report_device_status(kDevWaitTimeout);
+    if (ks > 1) {
+        cluster_arrive_release();
+        cluster_wait_acquire();
+    }
+    // this CTA's tokens, 8 columns a thread
+    if (!bad && first != 0x7fffffff) {
+        const int lo = P.rank <= 32 ? rp : (P.rank + 63) / 64 * 64, row = low_row(P.rank), mine = 128 / ks;
+        const uint32_t own = smem_u32(sm);
+        for (int i = tid; i < mine * (rp / 8); i += kWideThreads) {
+            const int c0 = i / mine * 8, tok = rank * mine + i % mine, e = adapter_of(t0 + tok);
+            if (e < 0) continue;
+            float v[8] = {}, l[8];
+            for (int r = 0; r < ks; ++r) {
+                const uint32_t src = (ks > 1 ? mapa_shared(own, r) : own) + (uint32_t)(c0 * 128 + tok) * 4;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float p;
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p) : "r"(src + j * 512) : "memory");
+                    v[j] += p;
+                }
+            }
+            const float scale = P.scale ? P.scale[e] : 1.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[j] *= scale;
+                const float h = __bfloat162float(__float2bfloat16_rn(v[j]));
+                l[j] = isfinite(h) ? v[j] - h : 0.f;
+            }
+            __nv_bfloat16* dst = P.v + (t0 + tok) * row + c0;
+            *reinterpret_cast<uint4*>(dst) = pack8(v);
+            *reinterpret_cast<uint4*>(dst + lo) = pack8(l);
+        }
+    }
+    if (ks > 1) {  // no CTA leaves while others read its shared memory
+        cluster_arrive_release();
+        cluster_wait_acquire();
+    }
+    __syncthreads();
     if (warp == 1) tc::dealloc(tm, COLS);
 }
 
@@ -580,32 +626,43 @@ cudaError_t launch_wide_mode(const WideJob& job, cudaStream_t st) {
     P.ld = job.ld;
     P.tok_adapter = job.tok_adapter;
     P.rank = job.rank;
-    // Width of a tile: the one whose waves over the pairs cost least, a tile costing its columns and a start worth about 24.
+    P.n_adapters = job.n_adapters;
+    constexpr int cols = MODE == kGated ? 128 : 256;
+    P.tiles_n = (job.n_out + cols - 1) / cols;
+    const int64_t tiles = (int64_t)P.tiles_n * P.tiles_t;
+    P.n_whole = tiles / pairs * pairs;
+    // the rest, cut where its waves then cost less; a tile costs its columns and a start worth about 24
+    const int64_t rest = tiles - P.n_whole;
     int64_t least = -1;
-    for (int bn : {256, 192, 128}) {
-        if (MODE == kGated && bn == 192) continue;  // (its halves are stored in pieces of 64 columns)
-        const int cols = MODE == kGated ? bn / 2 : bn;
-        const int64_t tiles_n = (job.n_out + cols - 1) / cols, tiles = tiles_n * P.tiles_t;
-        const int64_t cost = (tiles + pairs - 1) / pairs * (bn + 24);
+    for (int cut = 1; cut <= (MODE == kGated ? 2 : 4); cut *= 2) {  // (results are stored in pieces of 64 columns)
+        const int64_t cost = (rest * cut + pairs - 1) / pairs * (256 / cut + 24);
         if (least < 0 || cost < least) {
             least = cost;
-            P.bn = bn;
-            P.tiles_n = (int32_t)tiles_n;
-            P.n_tiles = tiles;
+            P.cut = cut;
         }
     }
+    P.n_tiles = P.n_whole + rest * P.cut;
     P.token_fast = job.n_tok < (MODE == kGated ? 2 : 1) * (int64_t)job.n_out;  // the tokens are the smaller operand
-    CUtensorMap mx, mw, mw2, mo, mv, mb;
-    bool good = map_rows(&mx, job.x, job.n_tok, job.k, 128) && map_rows(&mw, job.w, job.n_out, job.k, P.bn / 2) &&
+    CUtensorMap mx, mw, mw2, mwn, mw2n, mo, mv, mb, mbn;
+    bool good = map_rows(&mx, job.x, job.n_tok, job.k, 128) && map_rows(&mw, job.w, job.n_out, job.k, 128) &&
                 map_rows(&mo, job.out, job.n_tok, std::max(P.n_full, 8), 32, job.ld);
-    mw2 = mw, mv = mx, mb = mx;
-    if (MODE == kGated) good = good && map_rows(&mw2, job.w2, job.n_out, job.k, P.bn / 2);
+    if (MODE == kGated) good = good && map_rows(&mw2, job.w2, job.n_out, job.k, 128);
+    else mw2 = mw;
     if (MODE == kLora)
         good = good && map_rows(&mv, job.v, job.n_tok, low_row(job.rank), 128) &&
-               map_stack(&mb, job.b, job.n_adapters, job.n_out, job.rank, P.bn / 2);
+               map_stack(&mb, job.b, job.n_adapters, job.n_out, job.rank, 128);
+    else mv = mb = mx;
+    mwn = mw, mw2n = mw2, mbn = mb;
+    if (P.cut > 1) {
+        const int box = 128 / P.cut;
+        good = good && map_rows(&mwn, job.w, job.n_out, job.k, box);
+        if (MODE == kGated) good = good && map_rows(&mw2n, job.w2, job.n_out, job.k, box);
+        if (MODE == kLora) good = good && map_stack(&mbn, job.b, job.n_adapters, job.n_out, job.rank, box);
+    }
     if (!good) return cudaErrorInvalidValue;
     const int64_t grid = 2 * std::min<int64_t>(P.n_tiles, pairs);
-    return launch_pdl(k_wide<MODE>, dim3((unsigned)grid), dim3(kWideThreads), kWideSmem, st, mx, mw, mw2, mo, mv, mb, P);
+    return launch_pdl(k_wide<MODE>, dim3((unsigned)grid), dim3(kWideThreads), kWideSmem, st, mx, mw, mw2, mwn, mw2n, mo, mv,
+                      mb, mbn, P);
 }
 
 }  // namespace
@@ -630,10 +687,14 @@ cudaError_t launch_wide_low(const LowJob& job, cudaStream_t st) {
     P.n_tok = job.n_tok;
     P.tok_adapter = job.tok_adapter;
     P.scale = job.scale;
-    P.v = reinterpret_cast<__nv_bfloat16*>(job.v);
+    P.v = static_cast<__nv_bfloat16*>(job.v);
     P.kb = (job.k + kWideK - 1) / kWideK;
     P.rank = job.rank;
-    return launch_pdl(k_wide_low, dim3((unsigned)((job.n_tok + 127) / 128)), dim3(kWideThreads), kLowSmem, st, mx, ma, P);
+    P.n_adapters = job.n_adapters;
+    const int64_t tiles = (job.n_tok + 127) / 128;
+    P.ks = 1;
+    while (P.ks < 8 && tiles * P.ks * 2 <= sm_count() && P.kb >= P.ks * 4) P.ks *= 2;
+    return launch_pdl_cluster(k_wide_low, dim3((unsigned)(tiles * P.ks)), dim3(kWideThreads), kLowSmem, P.ks, st, mx, ma, P);
 }
 
 }  // namespace gdn

@@ -23,7 +23,7 @@ def test_rope_binding_refusals():
             gb.gdn_rope(plan, pos, bad, None)
     with pytest.raises(ValueError, match="q_out: found 2 heads, required 4"):
         gb.gdn_rope(plan, pos, q, None, _t(3, 2, 64))
-    with pytest.raises(ValueError, match="k_out: found a tensor, required None without k"):
+    with pytest.raises(ValueError, match="k_out: found 4 heads, required None without k"):
         gb.gdn_rope(plan, pos, q, None, None, q)
     with pytest.raises(ValueError, match="positions"):
         gb.gdn_rope(plan, pos.long(), q, None)
