@@ -162,7 +162,7 @@ const char* gdn_version(void) { return "libgdn 0.1 (sm_103a)"; }
 gdn_status gdn_device_status(uint32_t* status) {
     if (!status) return fail(GDN_ERR_NULL, "status: found NULL, required a host pointer");
     unsigned a = 0, b = 0;
-    unsigned c = 0, d = 0, t = 0, u = 0, f = 0, l = 0;
+    unsigned c = 0, d = 0, t = 0, u = 0, f = 0, w = 0, l = 0;
     cudaError_t e = gdn::take_device_status_decode(&a);
     if (e == cudaSuccess) e = gdn::take_device_status_prefill(&b);
     if (e == cudaSuccess) e = gdn::take_device_status_proj(&c);
@@ -170,8 +170,9 @@ gdn_status gdn_device_status(uint32_t* status) {
     if (e == cudaSuccess) e = gdn::take_device_status_tree(&t);
     if (e == cudaSuccess) e = gdn::take_device_status_attn_tree(&u);
     if (e == cudaSuccess) e = gdn::take_device_status_few(&f);
-    if (e == cudaSuccess) e = gdn::take_device_status_wide(&l);
-    *status = a | b | c | d | t | u | f | l;
+    if (e == cudaSuccess) e = gdn::take_device_status_wide(&w);
+    if (e == cudaSuccess) e = gdn::take_device_status_lora(&l);
+    *status = a | b | c | d | t | u | f | w | l;
     return cuda_status(e, "gdn_device_status");
 }
 
@@ -1164,10 +1165,9 @@ gdn_status gdn_proj_lora(const void* act, const void* w, const gdn_lora* lora, c
     // Requests of a few tokens each bring an adapter for (nearly) every token, a matrix product for none: they stay with
     // the kernel that gives each token its adapter on the CUDA cores.
     low.wide = n_tok > kFewTokens && n_tok >= 16 * (int64_t)n_seg;
-    cudaError_t e = gdn::launch_lora_low(low, s);
+    const cudaError_t e = gdn::launch_lora_low(low, s);
     if (e != cudaSuccess) return cuda_status(e, "gdn_proj_lora (low side)");
     if (low.wide) {
-        if ((e = gdn::launch_wide_low(low, s)) != cudaSuccess) return cuda_status(e, "gdn_proj_lora (low side)");
         gdn::WideJob job = {};
         job.x = act; job.w = w; job.out = out;
         job.n_tok = n_tok; job.ld = ld_out; job.n_out = n_out; job.k = k;
@@ -1179,7 +1179,7 @@ gdn_status gdn_proj_lora(const void* act, const void* w, const gdn_lora* lora, c
     job.x = act; job.w = w; job.out = out; job.early = 1;
     job.n_tok = n_tok; job.ld = ld_out; job.n_out = n_out; job.k = k;
     job.v = static_cast<const float*>(low.v); job.tok_adapter = low.tok_adapter; job.b = lora->b; job.rank = lora->rank;
-    job.n_adapters = lora->n_adapters;
+    job.n_adapters = lora->n_adapters; job.n_seg = n_seg; job.cu_rows = cu_rows; job.adapter_idx = adapter_idx;
     return cuda_status(gdn::launch_few(job, s), "gdn_proj_lora");
 }
 

@@ -11,9 +11,12 @@
 // there is one launch and no workspace.
 //   warp 0      TMA producer: 64-wide K blocks of the weights and the tokens into a ring of stages
 //   warp 1      MMA issuer (tcgen05, bf16 operands, fp32 accumulators in TMEM)
-//   warps 2..5  lora: the adapters' part of the tokens that this CTA will finish, on the CUDA cores while the weights
-//               stream (a thread is an output channel; each row of b is read by one thread, once, and a token only ever
-//               meets its own adapter, whatever the others hold); then accumulator -> shared memory
+//   warps 2..5  accumulator -> shared memory; lora: before that, while the weights stream, the adapters' part of the
+//               tokens that this CTA will finish, on the CUDA cores (a thread is an output channel; each row of b meets
+//               one token once, and a token only its own adapter, whatever the others hold)
+//   warp 6      lora: the 128 rows of b of each such token, and its v, into a second ring of shared memory.  Bulk copies: the
+//               rows of a token lie together, and while the weights saturate the memory a load takes 3 us, so that threads
+//               which load, use and load again cannot keep up (64 requests: 40 us that way)
 //   all warps   join the ks partial blocks (each CTA finishes every ks-th token), fuse, round, store
 // The join adds the parts in the order of their ranks, so results do not change from call to call.
 #include <cuda.h>
@@ -32,22 +35,30 @@ namespace {
 
 enum { kPlain = 0, kGated = 1, kLora = 2 };
 
-constexpr int kFewThreads = 192;
 constexpr int kFewM = 128;  // weight rows per tile
 constexpr int kFewK = 64;   // K per stage
+template <int MODE>
+constexpr int few_threads() { return MODE == kLora ? 224 : 192; }
 
-template <int N>
+// Two CTAs on an SM.  What they have in flight covers the memory's latency several times over; more of it only makes
+// every other load wait longer, so the weights' ring is the smaller one where the rows of b stream beside them.
+constexpr int kRowSlots = 16;  // lora: tokens in the ring of adapter rows, at most
+template <int N, int MODE>
 struct FewLay {
     static constexpr int W_BYTES = kFewM * kFewK * 2;
     static constexpr int X_BYTES = N * kFewK * 2;
     static constexpr int STAGE = W_BYTES + X_BYTES;
-    static constexpr int STAGES = N == 16 ? 6 : N == 32 ? 5 : N == 64 ? 4 : 3;  // two CTAs on an SM
-    static constexpr int RED = N * kFewM * 4;                                     // fp32 partial block, over the ring
-    static constexpr int RING = STAGES * STAGE > RED ? STAGES * STAGE : RED;
-    static constexpr int BAR_OFF = RING;  // full[S], empty[S], done, TMEM address
-    static constexpr int ADP_OFF = BAR_OFF + (2 * STAGES + 1) * 8 + 8;
-    static constexpr int SMEM_ALLOC = ADP_OFF + N * 4 + 1024;
-    static_assert(2 * (SMEM_ALLOC + 1024) <= 227 * 1024, "two CTAs on an SM");
+    static constexpr int STAGES = MODE == kLora ? (N <= 32 ? 3 : 2) : N == 16 ? 6 : N == 32 ? 5 : N == 64 ? 4 : 3;
+    static constexpr int RING = STAGES * STAGE;  // the fp32 partial block lies over it at the end
+    static constexpr int ROW_OFF = RING;
+    static constexpr int ROW_RING = MODE == kLora ? 108 * 1024 - RING : 0;
+    // full[S], empty[S], done, row_full[], row_empty[], TMEM address, the tokens' adapters
+    static constexpr int BAR_OFF = ROW_OFF + ROW_RING;
+    static constexpr int ADP_OFF = BAR_OFF + (2 * STAGES + 1 + (MODE == kLora ? 2 * kRowSlots : 0)) * 8 + 8;
+    static constexpr int SMEM_ALLOC = ADP_OFF + (MODE == kLora ? N * 4 : 0) + 1024;
+    static_assert(RING >= N * kFewM * 4, "the partial block");
+    static_assert(MODE != kLora || ROW_RING >= kFewM * 128 * 2 + 128 * 4, "a token of the largest rank");
+    static_assert(2 * (SMEM_ALLOC + 1024) <= 227 * 1024, "CTAs on an SM");
 };
 
 struct FewArgs {
@@ -61,8 +72,9 @@ struct FewArgs {
     // lora
     const float* v;            // [n_tok][rank]
     const int32_t* tok_adapter;  // [n_tok], -1: none
+    const int32_t *cu_rows, *adapter_idx;
     const __nv_bfloat16* b;    // [n_adapters][n_out][rank]
-    int32_t rank, n_adapters;
+    int32_t rank, n_adapters, n_seg;
 };
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
@@ -74,54 +86,42 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     return v;
 }
 
-// d[i] = v of token i . row n of its adapter's b, for the kTok tokens `tok` (adapter < 0: 0)
-constexpr int kTok = 8;
-__device__ __forceinline__ void adapter_part(const FewArgs& P, const int* adapter, int n, int64_t t0, int first, int step,
-                                             int count, float d[kTok]) {
-    const __nv_bfloat16* row[kTok];
-    const float* vt[kTok];
-#pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-        d[i] = 0.f;
-        const int c = first + i * step;
-        const int a = i < count ? adapter[c] : -1;
-        row[i] = a >= 0 && n < P.n_out ? P.b + ((int64_t)a * P.n_out + n) * P.rank : nullptr;
-        vt[i] = P.v + (t0 + c) * P.rank;
+__device__ __forceinline__ void st_tmem1(uint32_t taddr, float v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(__float_as_uint(v)) : "memory");
+}
+
+__device__ __forceinline__ void named_bar_arrive(int id, int count) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
+// one row of b (bf16, in shared memory, 16 bytes `pieces` to a row) . v (fp32, in shared memory).  The lanes start at
+// different pieces, so that 8 of them reach all banks whatever the rows' length.
+__device__ __forceinline__ float row_dot(const unsigned char* rows, int row, const float* v, int pieces, int start) {
+    const uint4* b = reinterpret_cast<const uint4*>(rows) + row * pieces;
+    float d = 0.f;
+    int c = start;
+    for (int j = 0; j < pieces; ++j) {
+        const uint4 w = b[c];
+        const float4 v0 = reinterpret_cast<const float4*>(v)[2 * c], v1 = reinterpret_cast<const float4*>(v)[2 * c + 1];
+        d = fmaf(__uint_as_float(w.x << 16), v0.x, d);
+        d = fmaf(__uint_as_float(w.x & 0xffff0000u), v0.y, d);
+        d = fmaf(__uint_as_float(w.y << 16), v0.z, d);
+        d = fmaf(__uint_as_float(w.y & 0xffff0000u), v0.w, d);
+        d = fmaf(__uint_as_float(w.z << 16), v1.x, d);
+        d = fmaf(__uint_as_float(w.z & 0xffff0000u), v1.y, d);
+        d = fmaf(__uint_as_float(w.w << 16), v1.z, d);
+        d = fmaf(__uint_as_float(w.w & 0xffff0000u), v1.w, d);
+        if (++c == pieces) c = 0;
     }
-    for (int j = 0; j < P.rank; j += 16) {
-        uint4 w[kTok][2];
-#pragma unroll
-        for (int i = 0; i < kTok; ++i) {
-            w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);
-            if (row[i]) {
-                w[i][0] = *reinterpret_cast<const uint4*>(row[i] + j);
-                if (j + 8 < P.rank) w[i][1] = *reinterpret_cast<const uint4*>(row[i] + j + 8);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kTok; ++i) {
-            if (!row[i]) continue;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (j + 8 * h >= P.rank) break;
-                const float4 v0 = *reinterpret_cast<const float4*>(vt[i] + j + 8 * h);
-                const float4 v1 = *reinterpret_cast<const float4*>(vt[i] + j + 8 * h + 4);
-                const uint32_t u[4] = {w[i][h].x, w[i][h].y, w[i][h].z, w[i][h].w};
-                d[i] += __uint_as_float(u[0] << 16) * v0.x + __uint_as_float(u[0] & 0xffff0000u) * v0.y +
-                        __uint_as_float(u[1] << 16) * v0.z + __uint_as_float(u[1] & 0xffff0000u) * v0.w;
-                d[i] += __uint_as_float(u[2] << 16) * v1.x + __uint_as_float(u[2] & 0xffff0000u) * v1.y +
-                        __uint_as_float(u[3] << 16) * v1.z + __uint_as_float(u[3] & 0xffff0000u) * v1.w;
-            }
-        }
-    }
+    return d;
 }
 
 template <int N, int MODE>
-__global__ void __launch_bounds__(kFewThreads, 2)
+__global__ void __launch_bounds__(few_threads<MODE>(), 2)
     k_few(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tw2,
           const __grid_constant__ CUtensorMap tx, const __grid_constant__ FewArgs P) {
-    using L = FewLay<N>;
-    constexpr int S = L::STAGES;
+    using L = FewLay<N, MODE>;
+    constexpr int S = L::STAGES, THREADS = few_threads<MODE>();
     // accumulator, then (lora) the adapters' part of this CTA's tokens
     constexpr uint32_t COLS = MODE == kLora ? 2 * N : (N < 32 ? 32 : N);
     // Without `early` nothing is held or asked for before everything ahead in the stream has ended.  With it, the kernel
@@ -133,15 +133,26 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::BAR_OFF);
     uint64_t* empty = full + S;
     uint64_t* done = empty + S;
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
-    int* adapter = reinterpret_cast<int*>(sm + L::ADP_OFF);
+    uint64_t* row_full = done + 1;
+    uint64_t* row_empty = row_full + kRowSlots;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(MODE == kLora ? row_empty + kRowSlots : done + 1);
+    int* adapter = reinterpret_cast<int*>(sm + L::ADP_OFF);  // of the tokens that this CTA finishes
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ks = P.ks, rank = (int)(blockIdx.x % ks), tile = (int)(blockIdx.x / ks);
     const int kb0 = (int)((int64_t)rank * P.kb / ks), kb1 = (int)((int64_t)(rank + 1) * P.kb / ks);
     const int64_t t0 = (int64_t)blockIdx.y * N;
     const int ncol = (int)(P.n_tok - t0 < N ? P.n_tok - t0 : N);
+    const int mine = ncol > rank ? (ncol - rank + ks - 1) / ks : 0;  // tokens rank, rank + ks, ... are finished here
+    // ring of adapter rows: per slot 128 rows of b, then v
+    const int slot_bytes = kFewM * P.rank * 2 + P.rank * 4;
+    const int slots = MODE == kLora ? min(kRowSlots, L::ROW_RING / slot_bytes) : 1;
 
     if (tid == 0) {
+        if (MODE == kLora)
+            for (int s = 0; s < slots; ++s) {
+                mbar_init(row_full + s, 1);
+                mbar_init(row_empty + s, 4);
+            }
         for (int s = 0; s < S; ++s) {
             mbar_init(full + s, 1);
             mbar_init(empty + s, 1);
@@ -206,30 +217,89 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             }
             if (ok) tc::commit(done);
         }
+    } else if (MODE == kLora && warp == 6) {
+        // The adapters of a decoding batch (request t is token t) are known without the kernel ahead, and with them the rows
+        // of b; only v has to be waited for.
+        int a[(N + 31) / 32];
+        bool known = true;
+#pragma unroll
+        for (int j = 0; j < (N + 31) / 32; ++j) {
+            const int i = 32 * j + lane;
+            const int t = (int)t0 + rank + i * ks;
+            a[j] = -1;
+            if (i < mine) {
+                known = known && t < P.n_seg && P.cu_rows[t] <= t && t < P.cu_rows[t + 1];
+                if (t < P.n_seg) a[j] = P.adapter_idx[t];
+            }
+        }
+        known = __all_sync(0xffffffffu, known);
+        if (!known) griddep_wait();
+#pragma unroll
+        for (int j = 0; j < (N + 31) / 32; ++j) {
+            const int i = 32 * j + lane;
+            if (i >= mine) continue;
+            if (!known) a[j] = P.tok_adapter[t0 + rank + i * ks];
+            adapter[i] = a[j] >= 0 && a[j] < P.n_adapters ? a[j] : -1;
+        }
+        __syncwarp();
+        named_bar_arrive(1, 160);
+        if (lane == 0) {
+            const int rows = min(kFewM, P.n_out - tile * kFewM);
+            const uint32_t b_bytes = (uint32_t)rows * P.rank * 2, v_bytes = (uint32_t)P.rank * 4;
+            auto slot_of = [&](int k) { return sm + L::ROW_OFF + (k % slots) * slot_bytes; };
+            auto copy_b = [&](int i, int k) {
+                mbar_arrive_expect_tx(row_full + k % slots, b_bytes + v_bytes);
+                bulk_g2s(slot_of(k), P.b + ((int64_t)adapter[i] * P.n_out + tile * kFewM) * P.rank, b_bytes,
+                         row_full + k % slots);
+            };
+            auto copy_v = [&](int i, int k) {
+                bulk_g2s(slot_of(k) + kFewM * P.rank * 2, P.v + (t0 + rank + (int64_t)i * ks) * P.rank, v_bytes,
+                         row_full + k % slots);
+            };
+            int i = 0, k = 0, i_v = 0, k_v = 0;
+            for (; i < mine && k < slots; ++i)
+                if (adapter[i] >= 0) copy_b(i, k++);
+            griddep_wait();
+            for (; i_v < i; ++i_v)
+                if (adapter[i_v] >= 0) copy_v(i_v, k_v++);
+            for (; i < mine; ++i) {
+                if (adapter[i] < 0) continue;
+                if (!mbar_wait(row_empty + k % slots, (uint32_t)(k / slots - 1) & 1u)) {
+                    ok = false;
+                    break;
+                }
+                copy_b(i, k);
+                copy_v(i, k++);
+            }
+        }
+        __syncwarp();
     } else {
         if (P.early) griddep_wait();
         griddep_launch_dependents();
         const int q4 = warp & 3;  // TMEM lanes 32 q4 .. are this warp's
         const int row = 32 * q4 + lane;
-        const int mine = ncol > rank ? (ncol - rank + ks - 1) / ks : 0;  // tokens rank, rank + ks, ... are finished here
         if (MODE == kLora) {
-            for (int c = tid - 64; c < N; c += 128) {
-                const int a = c < ncol ? P.tok_adapter[t0 + c] : -1;
-                adapter[c] = a < P.n_adapters ? a : -1;
+            named_bar_sync(1, 160);
+            const int pieces = P.rank / 8, shift = pieces & 1 ? 3 : pieces & 2 ? 2 : pieces & 4 ? 1 : 0;
+            const int start = (lane >> shift) % pieces;
+            int k = 0;
+            for (int i = 0; i < mine && ok; ++i) {
+                float d = 0.f;
+                if (adapter[i] >= 0) {
+                    const int s = k % slots;
+                    ok = __all_sync(0xffffffffu, mbar_wait(row_full + s, (uint32_t)(k / slots) & 1u));
+                    const unsigned char* st = sm + L::ROW_OFF + s * slot_bytes;
+                    if (ok) d = row_dot(st, row, reinterpret_cast<const float*>(st + kFewM * P.rank * 2), pieces, start);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(row_empty + s);
+                    ++k;
+                }
+                st_tmem1(tc::taddr(tm, 32 * q4, N + i), d);
             }
-            named_bar_sync(1, 128);
-            for (int i0 = 0; i0 < mine; i0 += 2 * kTok) {
-                float d[2 * kTok];
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    adapter_part(P, adapter, tile * kFewM + row, t0, rank + (i0 + h * kTok) * ks, ks,
-                                 mine - i0 - h * kTok, d + h * kTok);
-                tc::st16(tc::taddr(tm, 32 * q4, N + i0), d);
-            }
+            tc::st_wait();
         }
-        const bool w = mbar_wait(done, 0);
-        ok = w;
-        if (__all_sync(0xffffffffu, w)) {
+        ok = __all_sync(0xffffffffu, mbar_wait(done, 0)) && ok;
+        if (ok) {
             tc::fence_after();
             // every MMA has read its operands: the ring's memory takes the partial block, [token][128 rows]
             float* red = reinterpret_cast<float*>(sm) + row;
@@ -263,7 +333,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         const int n = tile * ROWS + 4 * (tid % LPT);
         const uint32_t own = smem_u32(sm) + 16 * (tid % LPT);
         const bool vec = n + 4 <= P.n_out && (P.ld & 3) == 0 && (reinterpret_cast<uintptr_t>(P.out) & 7) == 0;
-        for (int i = tid / LPT;; i += kFewThreads / LPT) {
+        for (int i = tid / LPT;; i += THREADS / LPT) {
             const int c = rank + i * ks;
             if (c >= ncol) break;
             float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
@@ -301,11 +371,41 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     if (warp == 1) tc::dealloc(tm, COLS);
 }
 
+// Cluster size: the CTAs run in waves of two per SM (fewer where clusters do not fit), and a CTA costs its K blocks and a
+// start and end worth about kFewEnds of them.
+constexpr int kFewEnds = 6;
+
+// CTAs of clusters of ks that run at the same time, two on an SM; once per device.  (Clusters of 3, 5 and more leave some
+// of a GPC's SMs empty: the runtime counts 46 of 3 and 15 of 8 on the 152 SMs, one CTA on each.)
 template <int N, int MODE>
-cudaError_t launch_few_n(const FewJob& job, int ks, cudaStream_t st) {
-    using L = FewLay<N>;
+int few_slots(int ks) {
+    static std::atomic<int> known[64][9];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return ks;
+    std::atomic<int>& slot = known[dev & 63][ks];
+    int n = slot.load(std::memory_order_acquire);
+    if (n > 0) return n;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)ks;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(ks * 512));
+    cfg.blockDim = dim3(few_threads<MODE>());
+    cfg.dynamicSmemBytes = FewLay<N, MODE>::SMEM_ALLOC;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, k_few<N, MODE>, &cfg) != cudaSuccess || n < 1) n = 1;
+    n = 2 * std::min(n * ks, sm_count());
+    slot.store(n, std::memory_order_release);
+    return n;
+}
+
+template <int N, int MODE>
+cudaError_t launch_few_n(const FewJob& job, cudaStream_t st) {
+    using L = FewLay<N, MODE>;
     static std::atomic<uint64_t> smem_set{0};
-    cudaError_t e = raise_smem_limit(k_few<N, MODE>, L::SMEM_ALLOC, smem_set);
+    cudaError_t e = raise_smem_limit_shared(k_few<N, MODE>, L::SMEM_ALLOC, smem_set);
     if (e != cudaSuccess) return e;
     constexpr int rows = MODE == kGated ? kFewM / 2 : kFewM;
     CUtensorMap mw, mw2, mx;
@@ -316,7 +416,6 @@ cudaError_t launch_few_n(const FewJob& job, int ks, cudaStream_t st) {
     P.n_tok = job.n_tok;
     P.n_out = job.n_out;
     P.kb = (job.k + kFewK - 1) / kFewK;
-    P.ks = ks;
     P.early = job.early;
     P.out = static_cast<__nv_bfloat16*>(job.out);
     P.ld = job.ld;
@@ -325,40 +424,32 @@ cudaError_t launch_few_n(const FewJob& job, int ks, cudaStream_t st) {
     P.b = static_cast<const __nv_bfloat16*>(job.b);
     P.rank = job.rank;
     P.n_adapters = job.n_adapters;
+    P.n_seg = job.n_seg;
+    P.cu_rows = job.cu_rows;
+    P.adapter_idx = job.adapter_idx;
     const unsigned tiles = (unsigned)((job.n_out + rows - 1) / rows);
-    return launch_pdl_cluster(k_few<N, MODE>, dim3(tiles * ks, (unsigned)((job.n_tok + N - 1) / N)), dim3(kFewThreads),
-                              L::SMEM_ALLOC, ks, st, mw, mw2, mx, P);
-}
-
-// Cluster size: the CTAs run in waves of two per SM, and a CTA costs its K blocks and a start and end worth about
-// kFewEnds of them.
-constexpr int kFewEnds = 6;
-int few_split(int64_t tiles, int kb) {
-    const int64_t slots = 2 * (int64_t)sm_count();
-    int best = 1;
+    const int64_t all = (int64_t)tiles * ((job.n_tok + N - 1) / N);
     int64_t least = -1;
-    for (int ks = 1; ks <= 8 && ks <= std::max(1, kb / 2); ++ks) {
-        const int64_t cost = (tiles * ks + slots - 1) / slots * ((kb + ks - 1) / ks + kFewEnds);
+    int ks = 1;
+    for (int c = 1; c <= 8 && c <= std::max(1, P.kb / 2); ++c) {
+        const int64_t slots = few_slots<N, MODE>(c);
+        const int64_t cost = (all * c + slots - 1) / slots * ((P.kb + c - 1) / c + kFewEnds);
         if (least < 0 || cost < least) {
             least = cost;
-            best = ks;
+            ks = c;
         }
     }
-    return best;
+    P.ks = ks;
+    return launch_pdl_cluster(k_few<N, MODE>, dim3(tiles * ks, (unsigned)((job.n_tok + N - 1) / N)), dim3(few_threads<MODE>()),
+                              L::SMEM_ALLOC, ks, st, mw, mw2, mx, P);
 }
 
 template <int MODE>
 cudaError_t launch_few_mode(const FewJob& job, cudaStream_t st) {
-    constexpr int rows = MODE == kGated ? kFewM / 2 : kFewM;
-    const int N = job.n_tok <= 16 ? 16 : job.n_tok <= 32 ? 32 : job.n_tok <= 64 ? 64 : 128;
-    const int64_t tiles = (job.n_out + rows - 1) / rows * ((job.n_tok + N - 1) / N);
-    const int ks = few_split(tiles, (job.k + kFewK - 1) / kFewK);
-    switch (N) {
-        case 16: return launch_few_n<16, MODE>(job, ks, st);
-        case 32: return launch_few_n<32, MODE>(job, ks, st);
-        case 64: return launch_few_n<64, MODE>(job, ks, st);
-        default: return launch_few_n<128, MODE>(job, ks, st);
-    }
+    if (job.n_tok <= 16) return launch_few_n<16, MODE>(job, st);
+    if (job.n_tok <= 32) return launch_few_n<32, MODE>(job, st);
+    if (job.n_tok <= 64) return launch_few_n<64, MODE>(job, st);
+    return launch_few_n<128, MODE>(job, st);
 }
 
 }  // namespace

@@ -26,6 +26,18 @@ cudaError_t raise_smem_limit(void (*kernel)(KArgs...), int bytes, std::atomic<ui
     return e;
 }
 
+// The same for kernels of which several CTAs are to share an SM: all of its memory beside the L1 cache goes to them (left to
+// itself the driver provides for one CTA).
+template <typename... KArgs>
+cudaError_t raise_smem_limit_shared(void (*kernel)(KArgs...), int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (done.load(std::memory_order_acquire) & (1ull << (dev & 63))) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    return e == cudaSuccess ? raise_smem_limit(kernel, bytes, done) : e;
+}
+
 // SMs of the current device, queried once per device (1 if the query fails).
 int sm_count();
 
@@ -283,7 +295,7 @@ struct AppendJob {
 cudaError_t launch_append(const AppendJob& job, cudaStream_t st);
 
 // ---- around the attention and the projections ----
-// rotary positions of rows of q and k (out == in: in place); pieces and per_cta are the launcher's
+// rotary positions of rows of q and k (out == in: in place); pieces and step_h are the launcher's
 struct RopeJob {
     const void *q, *k;
     void *q_out, *k_out;
@@ -291,7 +303,7 @@ struct RopeJob {
     const int32_t* positions;
     int64_t n_tok;
     int hq, hkv, D, rot, half, bf16;
-    int pieces, per_cta;
+    int pieces, step_h;
     float mscale;
     unsigned long long turns[128];  // turns per position of pair i, in units of 2^-64
 };
@@ -308,8 +320,9 @@ struct FewJob {
     int early;  // the kernel ahead in the stream is of the same call and its launches follow the rule of `k_few`
     const float* v;              // [n_tok][rank]
     const int32_t* tok_adapter;  // [n_tok], -1: none
+    const int32_t *cu_rows, *adapter_idx;  // what tok_adapter was made from
     const void* b;               // [n_adapters][n_out][rank]
-    int32_t rank, n_adapters;
+    int32_t rank, n_adapters, n_seg;
 };
 cudaError_t launch_few(const FewJob& job, cudaStream_t st);
 
@@ -329,10 +342,8 @@ cudaError_t launch_wide(const WideJob& job, cudaStream_t st);
 // Low-rank activations for launch_wide: v = hi + lo in bf16, a row of low_row(rank) elements being [hi | lo] in parts
 // of 16 ceil(rank / 16) (rank <= 32) or 64 ceil(rank / 64) elements, each padded with zeros to a multiple of 16.
 constexpr int low_row(int rank) { return rank <= 32 ? 64 : 2 * ((rank + 63) / 64 * 64); }
-constexpr int kLongRequest = 1 << 30;  // in tok_adapter of a wide job: v of this token is launch_wide_low's
 
-// each token's adapter, and v = scale A x: for launch_few of every token (wide 0, fp32 [n_tok][rank]), for launch_wide
-// of the tokens of short requests (wide 1), launch_wide_low behind it of the others
+// each token's adapter, and v = scale A x, for launch_few (wide 0: fp32 [n_tok][rank]) or launch_wide (wide 1)
 struct LowJob {
     const void *x, *a;
     const float* scale;  // NULL: 1
@@ -343,7 +354,6 @@ struct LowJob {
     int32_t n_seg, n_adapters, rank, k, wide;
 };
 cudaError_t launch_lora_low(const LowJob& job, cudaStream_t st);
-cudaError_t launch_wide_low(const LowJob& job, cudaStream_t st);
 
 // GDN_DEBUG: device-side check that the na + nb indices of idx_a then idx_b lie in
 // [0, n_slots) and are distinct.  A violation ORs kDevBadSlot into the device status
@@ -362,5 +372,6 @@ cudaError_t take_device_status_tree(unsigned* out);
 cudaError_t take_device_status_attn_tree(unsigned* out);
 cudaError_t take_device_status_few(unsigned* out);
 cudaError_t take_device_status_wide(unsigned* out);
+cudaError_t take_device_status_lora(unsigned* out);
 
 }  // namespace gdn

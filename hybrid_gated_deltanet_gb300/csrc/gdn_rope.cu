@@ -21,7 +21,6 @@ namespace gdn {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeUnroll = 4;  // pieces whose loads a thread has in flight
 
 // 8 consecutive elements
 template <typename T>
@@ -69,74 +68,83 @@ struct Eight<float> {
     }
 };
 
-// A CTA takes a few tokens: its threads make their sines and cosines once, into shared memory, and then rotate the heads
-// from there.  (With every thread making its own angles for one head, sine and cosine took longer than the memory; with a
-// thread walking over the heads of one angle, few tokens leave the GPU empty.)  The unit of work is a piece of 16 elements of a head: 8 pairs
-// of the rotated part (two runs of 8 elements, rot / 2 apart or side by side), or 16 elements of the rest, which are only
-// copied and only where the result goes elsewhere.  Pieces are fastest among the threads, then heads, so that a warp's
-// accesses are contiguous; the first loads are under way while the angles are made.
-template <typename T>
-__global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ RopeJob J) {
-    extern __shared__ float2 angle[];  // [token][rot / 2]: cosine and sine
-    griddep_wait();                    // launched with programmatic serialization
+// A thread owns one piece of 16 elements of a token's heads: 8 pairs of the rotated part (two runs of 8 elements, rot / 2
+// apart or side by side), or 16 elements of the rest, which are only copied and only where the result goes elsewhere.  It
+// walks over every step_h-th head, kRopeHeads of them in flight; pieces are fastest among the threads, then heads, so that a
+// warp's accesses are contiguous.
+// MANY tokens: a thread walks over all heads (step_h 1) and makes its 8 angles by itself.  Else the heads are split over
+// more threads, and the CTA makes the angles of its tokens once, in shared memory, while the loads are under way: made by
+// every thread for its own heads they took 2 us of the 5 that 300 tokens of 26 heads then needed.  (The barrier costs more
+// than the angles where there are many tokens: 197 us against 190 for 65536 tokens of 36 heads.)
+template <typename T, bool MANY>
+__global__ void __launch_bounds__(kRopeThreads, 2) k_rope(const __grid_constant__ RopeJob J) {
+    constexpr int kRopeHeads = MANY ? 4 : 2;  // heads whose loads a thread has in flight
+    // a CTA's threads reach over at most kRopeThreads / pieces + 2 tokens of rot / 2 <= 8 pieces angles
+    __shared__ float2 angle[MANY ? 1 : 8 * kRopeThreads + 2 * 128];  // cosine and sine
+    griddep_wait();                                       // launched with programmatic serialization
     griddep_launch_dependents();
-    const int pieces = J.pieces, pairs = J.rot / 16, heads = J.hq + J.hkv, half_rot = J.rot / 2;
-    const int64_t first = (int64_t)blockIdx.x * J.per_cta;
-    const int n = (int)(J.n_tok - first < J.per_cta ? J.n_tok - first : J.per_cta);
-    const int items = n * heads * pieces, step = (int)gridDim.y * kRopeThreads;
-    bool ready = false;
-    for (int i0 = (int)blockIdx.y * kRopeThreads + (int)threadIdx.x; !ready || i0 < items; i0 += kRopeUnroll * step) {
-        Eight<T> x[kRopeUnroll], y[kRopeUnroll];
-        T* dst[kRopeUnroll];
-        int at[kRopeUnroll], e1[kRopeUnroll];  // the angles (-1: none), the second run's distance (0: none)
+    const int pieces = J.pieces, pairs = J.rot / 16, half_rot = J.rot / 2, heads = J.hq + J.hkv;
+    // (the launcher keeps these in 32 bits: six divisions of 64 bits took longer than everything else of a small call)
+    const unsigned at0 = blockIdx.x * kRopeThreads, at = at0 + threadIdx.x, per_tok = (unsigned)(pieces * J.step_h);
+    const unsigned tok0 = at0 / per_tok, tok1 = min((at0 + kRopeThreads - 1) / per_tok, (unsigned)J.n_tok - 1);
+    const int64_t tok = at / per_tok;
+    const unsigned in_tok = at - (unsigned)tok * per_tok;
+    const int h0 = (int)(in_tok / (unsigned)pieces), u = (int)(in_tok - (unsigned)h0 * pieces);
+    const bool mine = tok < J.n_tok, turn = u < pairs;
+    const int e0 = turn ? (J.half ? 8 * u : 16 * u) : J.rot + 16 * (u - pairs);
+    const int e1 = e0 + (turn && J.half ? half_rot : 8);
+    const bool two = e1 < J.D;  // (a head's rest may end on a single run)
+    float c[8], s[8];
+    for (int hb = h0;; hb += kRopeHeads * J.step_h) {
+        Eight<T> x[kRopeHeads], y[kRopeHeads];
 #pragma unroll
-        for (int e = 0; e < kRopeUnroll; ++e) {
-            const int i = i0 + e * step;
-            dst[e] = nullptr;
-            if (i >= items) continue;
-            const int row = i / pieces, u = i - row * pieces, t = row / heads, h = row - t * heads;
-            const int64_t tok = first + t;
-            int e0;
-            if (u < pairs) {
-                e0 = J.half ? 8 * u : 16 * u;
-                e1[e] = J.half ? half_rot : 8;
-                at[e] = t * half_rot + 8 * u;
-            } else {
-                e0 = J.rot + 16 * (u - pairs);
-                e1[e] = e0 + 8 < J.D ? 8 : 0;  // (a head's rest may end on a single run)
-                at[e] = -1;
-            }
-            const bool q = h < J.hq;
-            const int64_t off = (int64_t)(q ? h : h - J.hq) * J.D + e0;
-            const T* src = static_cast<const T*>(q ? J.q : J.k) + tok * (q ? J.ldq : J.ldk) + off;
-            dst[e] = static_cast<T*>(q ? J.q_out : J.k_out) + tok * (q ? J.ldqo : J.ldko) + off;
-            x[e].ld(src);
-            if (e1[e]) y[e].ld(src + e1[e]);
+        for (int e = 0; e < kRopeHeads; ++e) {
+            const int h = hb + e * J.step_h;
+            if (!mine || h >= heads) continue;
+            const T* src = h < J.hq ? static_cast<const T*>(J.q) + tok * J.ldq + (int64_t)h * J.D
+                                    : static_cast<const T*>(J.k) + tok * J.ldk + (int64_t)(h - J.hq) * J.D;
+            x[e].ld(src + e0);
+            if (two) y[e].ld(src + e1);
         }
-        if (!ready) {
-            for (int j = threadIdx.x; j < n * half_rot; j += kRopeThreads) {
-                const int t = j / half_rot;
-                const unsigned long long p = (unsigned long long)(long long)J.positions[first + t];
-                const int turn = (int)(unsigned)((p * J.turns[j - t * half_rot]) >> 32);
-                float s, c;
-                sincospif((float)turn * 0x1p-31f, &s, &c);
-                angle[j] = make_float2(c * J.mscale, s * J.mscale);
+        if (hb == h0 && MANY) {
+            if (!mine) return;
+            const unsigned long long p = (unsigned long long)(long long)J.positions[tok];
+            if (turn)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    sincospif((float)(int)(unsigned)((p * J.turns[8 * u + j]) >> 32) * 0x1p-31f, &s[j], &c[j]);
+                    c[j] *= J.mscale;
+                    s[j] *= J.mscale;
+                }
+        }
+        if (hb == h0 && !MANY) {
+            for (unsigned j = threadIdx.x; j < (tok1 - tok0 + 1) * half_rot; j += kRopeThreads) {
+                const unsigned t = j / (unsigned)half_rot;
+                const unsigned long long p = (unsigned long long)(long long)J.positions[tok0 + t];
+                float sn, cs;
+                sincospif((float)(int)(unsigned)((p * J.turns[j - t * half_rot]) >> 32) * 0x1p-31f, &sn, &cs);
+                angle[j] = make_float2(cs * J.mscale, sn * J.mscale);
             }
             __syncthreads();
-            ready = true;
+            if (!mine) return;
+            if (turn)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 w = angle[(int)(tok - tok0) * half_rot + 8 * u + j];
+                    c[j] = w.x;
+                    s[j] = w.y;
+                }
         }
 #pragma unroll
-        for (int e = 0; e < kRopeUnroll; ++e) {
-            if (!dst[e]) continue;
-            if (at[e] >= 0) {
-                float a[8], b[8], c[8], s[8];
+        for (int e = 0; e < kRopeHeads; ++e) {
+            const int h = hb + e * J.step_h;
+            if (h >= heads) continue;
+            T* dst = h < J.hq ? static_cast<T*>(J.q_out) + tok * J.ldqo + (int64_t)h * J.D
+                              : static_cast<T*>(J.k_out) + tok * J.ldko + (int64_t)(h - J.hq) * J.D;
+            if (turn) {
+                float a[8], b[8];
                 x[e].get(a);
                 y[e].get(b);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float4 w = *reinterpret_cast<const float4*>(angle + at[e] + 2 * j);
-                    c[2 * j] = w.x, s[2 * j] = w.y, c[2 * j + 1] = w.z, s[2 * j + 1] = w.w;
-                }
                 if (J.half) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
@@ -158,9 +166,10 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ R
                 x[e].set(a);
                 y[e].set(b);
             }
-            x[e].st(dst[e]);
-            if (e1[e]) y[e].st(dst[e] + e1[e]);
+            x[e].st(dst + e0);
+            if (two) y[e].st(dst + e1);
         }
+        if (hb + kRopeHeads * J.step_h >= heads) return;
     }
 }
 
@@ -190,20 +199,33 @@ void rope_turns(int rot, double theta, double factor, int orig_len, double beta_
 }
 
 cudaError_t launch_rope(RopeJob job, cudaStream_t st) {
-    const int heads = job.hq + job.hkv;
-    if (job.n_tok == 0 || heads == 0) return cudaSuccess;
+    const int heads = job.hq + job.hkv, es = job.bf16 ? 2 : 4;
     const bool same = job.q == job.q_out && job.k == job.k_out;
     job.pieces = job.rot / 16 + (same ? 0 : (job.D - job.rot + 15) / 16);
-    // Tokens of a CTA: angles for its threads to make and a few pieces for each of them; one token where the tokens would not
-    // fill the GPU's CTAs (8 an SM) otherwise.  A token of very many pieces is shared by CTAs along y.
-    const int per_token = heads * job.pieces;
-    job.per_cta = std::max(1, std::min(2 * kRopeThreads / job.rot, 4 * kRopeThreads / per_token));
-    if (job.n_tok < (int64_t)sm_count() * 8 * job.per_cta) job.per_cta = 1;
-    const dim3 grid((unsigned)((job.n_tok + job.per_cta - 1) / job.per_cta),
-                    (unsigned)((job.per_cta * per_token + 8 * kRopeThreads - 1) / (8 * kRopeThreads)));
-    const size_t smem = (size_t)job.per_cta * (job.rot / 2) * sizeof(float2);
-    return job.bf16 ? launch_pdl(k_rope<__nv_bfloat16>, grid, dim3(kRopeThreads), smem, st, job)
-                    : launch_pdl(k_rope<float>, grid, dim3(kRopeThreads), smem, st, job);
+    auto at = [&](const void* p, int64_t ld, int64_t tok) {
+        return p ? static_cast<const unsigned char*>(p) + tok * ld * es : nullptr;
+    };
+    auto out_at = [&](void* p, int64_t ld, int64_t tok) { return p ? static_cast<unsigned char*>(p) + tok * ld * es : nullptr; };
+    // one thread per piece and token walks all heads once that fills the GPU (2048 threads an SM); fewer tokens split the
+    // heads.  Thread numbers stay in 32 bits: 2^22 tokens of 16 pieces a launch.
+    constexpr int64_t kTokens = (int64_t)1 << 22;
+    for (int64_t first = 0; first < job.n_tok && heads > 0; first += kTokens) {
+        RopeJob J = job;
+        J.n_tok = std::min(kTokens, job.n_tok - first);
+        J.positions += first;
+        J.q = at(job.q, job.ldq, first);
+        J.k = at(job.k, job.ldk, first);
+        J.q_out = out_at(job.q_out, job.ldqo, first);
+        J.k_out = out_at(job.k_out, job.ldko, first);
+        const int64_t full = (int64_t)sm_count() * 2048, one = J.n_tok * J.pieces;
+        J.step_h = (int)std::min<int64_t>(heads, std::max<int64_t>(1, full / one));
+        const dim3 grid((unsigned)((one * J.step_h + kRopeThreads - 1) / kRopeThreads));
+        const auto kernel = J.step_h == 1 ? (J.bf16 ? k_rope<__nv_bfloat16, true> : k_rope<float, true>)
+                                          : (J.bf16 ? k_rope<__nv_bfloat16, false> : k_rope<float, false>);
+        const cudaError_t e = launch_pdl(kernel, grid, dim3(kRopeThreads), 0, st, J);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace gdn
