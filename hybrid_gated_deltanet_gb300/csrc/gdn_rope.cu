@@ -206,7 +206,7 @@ cudaError_t launch_rope(RopeJob job, cudaStream_t st) {
         return p ? static_cast<const unsigned char*>(p) + tok * ld * es : nullptr;
     };
     auto out_at = [&](void* p, int64_t ld, int64_t tok) { return p ? static_cast<unsigned char*>(p) + tok * ld * es : nullptr; };
-    // one thread per piece and token walks all heads once that fills the GPU (2048 threads an SM); fewer tokens split the
+    // one thread per piece and token walks all heads once that fills the GPU (512 threads an SM); fewer tokens split the
     // heads.  Thread numbers stay in 32 bits: 2^22 tokens of 16 pieces a launch.
     constexpr int64_t kTokens = (int64_t)1 << 22;
     for (int64_t first = 0; first < job.n_tok && heads > 0; first += kTokens) {
@@ -217,7 +217,7 @@ cudaError_t launch_rope(RopeJob job, cudaStream_t st) {
         J.k = at(job.k, job.ldk, first);
         J.q_out = out_at(job.q_out, job.ldqo, first);
         J.k_out = out_at(job.k_out, job.ldko, first);
-        const int64_t full = (int64_t)sm_count() * 2048, one = J.n_tok * J.pieces;
+        const int64_t full = (int64_t)sm_count() * 512, one = J.n_tok * J.pieces;
         J.step_h = (int)std::min<int64_t>(heads, std::max<int64_t>(1, full / one));
         const dim3 grid((unsigned)((one * J.step_h + kRopeThreads - 1) / kRopeThreads));
         const auto kernel = J.step_h == 1 ? (J.bf16 ? k_rope<__nv_bfloat16, true> : k_rope<float, true>)
