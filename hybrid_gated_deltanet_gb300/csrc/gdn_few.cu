@@ -37,6 +37,7 @@ enum { kPlain = 0, kGated = 1, kLora = 2 };
 
 constexpr int kFewM = 128;  // weight rows per tile
 constexpr int kFewK = 64;   // K per stage
+constexpr int kFewAhead = 3;  // stages of weights asked for before the kernel ahead has ended
 template <int MODE>
 constexpr int few_threads() { return MODE == kLora ? 224 : 192; }
 
@@ -182,10 +183,14 @@ __global__ void __launch_bounds__(few_threads<MODE>(), 2)
             auto tokens = [&](int kb, int s) {
                 tma_tile_2d(sm + s * L::STAGE + L::W_BYTES, &tx, kb * kFewK, (int)t0, full + s);
             };
-            const int ahead = min(S, kb1 - kb0);
-            for (int i = 0; i < ahead; ++i) weights(kb0 + i, i);
+            // weights ahead of the wait, but not the whole ring of them: the tokens of the first stage come behind
+            const int ahead = min(S, kb1 - kb0), early = P.early && MODE != kLora ? min(kFewAhead, ahead) : 0;
+            for (int i = 0; i < early; ++i) weights(kb0 + i, i);
             if (P.early && MODE != kLora) griddep_wait();  // (lora: only v and the adapters come from the kernel ahead)
-            for (int i = 0; i < ahead; ++i) tokens(kb0 + i, i);
+            for (int i = 0; i < ahead; ++i) {
+                if (i >= early) weights(kb0 + i, i);
+                tokens(kb0 + i, i);
+            }
             for (int i = ahead; i < kb1 - kb0; ++i) {
                 const int s = i % S;
                 if (!mbar_wait(empty + s, (uint32_t)(i / S - 1) & 1u)) {
@@ -326,49 +331,47 @@ __global__ void __launch_bounds__(few_threads<MODE>(), 2)
         cluster_arrive_release();
         cluster_wait_acquire();
     }
-    // a thread takes 4 rows of a token: 32 lanes are the 128 rows (gated: 16 lanes, each with both matrices' rows)
-    if (!bad) {
-        constexpr int LPT = MODE == kGated ? 16 : 32;
-        constexpr int ROWS = MODE == kGated ? kFewM / 2 : kFewM;
-        const int n = tile * ROWS + 4 * (tid % LPT);
-        const uint32_t own = smem_u32(sm) + 16 * (tid % LPT);
-        const bool vec = n + 4 <= P.n_out && (P.ld & 3) == 0 && (reinterpret_cast<uintptr_t>(P.out) & 7) == 0;
-        for (int i = tid / LPT;; i += THREADS / LPT) {
-            const int c = rank + i * ks;
-            if (c >= ncol) break;
-            float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
-            for (int r = 0; r < ks; ++r) {
-                const uint32_t a = (ks > 1 ? mapa_shared(own, r) : own) + c * (kFewM * 4);
-                const float4 p = ks > 1 ? ld_cluster_f4(a) : *reinterpret_cast<const float4*>(sm + (a - smem_u32(sm)));
-                g.x += p.x, g.y += p.y, g.z += p.z, g.w += p.w;
-                if (MODE == kGated) {
-                    const float4 q = ks > 1 ? ld_cluster_f4(a + kFewM * 2)
-                                            : *reinterpret_cast<const float4*>(sm + (a - smem_u32(sm)) + kFewM * 2);
-                    u.x += q.x, u.y += q.y, u.z += q.z, u.w += q.w;
-                }
-            }
-            float o[4] = {g.x, g.y, g.z, g.w};
+    // A thread takes 4 rows of a token: 32 lanes are the 128 rows (gated: 16 lanes, each with both matrices' rows).  The reads
+    // from four CTAs are under way together.
+    constexpr int LPT = MODE == kGated ? 16 : 32;
+    constexpr int ROWS = MODE == kGated ? kFewM / 2 : kFewM;
+    const int n = tile * ROWS + 4 * (tid % LPT);
+    const uint32_t own = smem_u32(sm) + 16 * (tid % LPT);
+    const bool vec = n + 4 <= P.n_out && (P.ld & 3) == 0 && (reinterpret_cast<uintptr_t>(P.out) & 7) == 0;
+    for (int i = tid / LPT; i < mine && !bad; i += THREADS / LPT) {
+        const int c = rank + i * ks;
+        float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
+#pragma unroll 4
+        for (int r = 0; r < ks; ++r) {
+            const uint32_t at = (ks > 1 ? mapa_shared(own, r) : own) + c * (kFewM * 4);
+            const float4 p = ld_cluster_f4(at);
+            g.x += p.x, g.y += p.y, g.z += p.z, g.w += p.w;
             if (MODE == kGated) {
-                o[0] = siluf_(g.x) * u.x, o[1] = siluf_(g.y) * u.y, o[2] = siluf_(g.z) * u.z, o[3] = siluf_(g.w) * u.w;
-            }
-            __nv_bfloat16* dst = P.out + (t0 + c) * P.ld + n;
-            if (vec) {
-                const __nv_bfloat162 lo = __floats2bfloat162_rn(o[0], o[1]), hi = __floats2bfloat162_rn(o[2], o[3]);
-                *reinterpret_cast<uint2*>(dst) =
-                    make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (n + e < P.n_out) dst[e] = __float2bfloat16_rn(o[e]);
+                const float4 q = ld_cluster_f4(at + kFewM * 2);
+                u.x += q.x, u.y += q.y, u.z += q.z, u.w += q.w;
             }
         }
+        float o[4] = {g.x, g.y, g.z, g.w};
+        if (MODE == kGated) {
+            o[0] = siluf_(g.x) * u.x, o[1] = siluf_(g.y) * u.y, o[2] = siluf_(g.z) * u.z, o[3] = siluf_(g.w) * u.w;
+        }
+        __nv_bfloat16* dst = P.out + (t0 + c) * P.ld + n;
+        if (vec) {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(o[0], o[1]), hi = __floats2bfloat162_rn(o[2], o[3]);
+            *reinterpret_cast<uint2*>(dst) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (n + e < P.n_out) dst[e] = __float2bfloat16_rn(o[e]);
+        }
     }
+    __syncwarp();
+    if (warp == 1) tc::dealloc(tm, COLS);
     if (ks > 1) {  // no CTA leaves while others read its shared memory
         cluster_arrive_release();
         cluster_wait_acquire();
     }
-    __syncthreads();
-    if (warp == 1) tc::dealloc(tm, COLS);
 }
 
 // Cluster size: the CTAs run in waves of two per SM (fewer where clusters do not fit), and a CTA costs its K blocks and a
