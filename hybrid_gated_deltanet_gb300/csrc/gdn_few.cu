@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(few_threads<MODE>(), 2)
         }
         float o[4] = {g.x, g.y, g.z, g.w};
         if (MODE == kGated) {
-            o[0] = siluf_(g.x) * u.x, o[1] = siluf_(g.y) * u.y, o[2] = siluf_(g.z) * u.z, o[3] = siluf_(g.w) * u.w;
+            o[0] = silu_gate(g.x) * u.x, o[1] = silu_gate(g.y) * u.y, o[2] = silu_gate(g.z) * u.z, o[3] = silu_gate(g.w) * u.w;
         }
         __nv_bfloat16* dst = P.out + (t0 + c) * P.ld + n;
         if (vec) {

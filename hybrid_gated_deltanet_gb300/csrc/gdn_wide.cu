@@ -387,7 +387,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                         tc::ld32_nowait(col + half, u);
                         tc::ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = siluf_(__uint_as_float(g[i])) * __uint_as_float(u[i]);
+                        for (int i = 0; i < 32; ++i) v[i] = silu_gate(__uint_as_float(g[i])) * __uint_as_float(u[i]);
                     } else {
                         tc::ld32(col, v);
                     }
