@@ -1047,17 +1047,28 @@ static gdn_status proj_sizes(int64_t n_tok, int32_t n_out, int32_t k, int64_t ld
 // Up to kFewTokens tokens the weights stream past the tokens, from there on tiles of 256 tokens go to pairs of SMs.
 constexpr int64_t kFewTokens = 128;
 
-static cudaError_t launch_fused(const void* x, const void* w, const void* w2, void* out, int64_t n_tok, int32_t n_out,
-                                int32_t k, int64_t ld, bool early, cudaStream_t st) {
-    if (n_tok > kFewTokens) {
+struct Fused {
+    const void *x, *w, *w2;
+    void* out;
+    int64_t n_tok, ld;
+    int32_t n_out, k;
+    bool early;
+    void* split_ws;
+    int32_t* zero;
+    int32_t n_zero;
+};
+static cudaError_t launch_fused(const Fused& f, cudaStream_t st) {
+    if (f.n_tok > kFewTokens) {
         gdn::WideJob job = {};
-        job.x = x; job.w = w; job.w2 = w2; job.out = out;
-        job.n_tok = n_tok; job.ld = ld; job.n_out = n_out; job.k = k;
+        job.x = f.x; job.w = f.w; job.w2 = f.w2; job.out = f.out;
+        job.n_tok = f.n_tok; job.ld = f.ld; job.n_out = f.n_out; job.k = f.k;
+        job.split_ws = f.split_ws; job.zero = f.zero; job.n_zero = f.n_zero;
         return gdn::launch_wide(job, st);
     }
     gdn::FewJob job = {};
-    job.x = x; job.w = w; job.w2 = w2; job.out = out; job.early = early;
-    job.n_tok = n_tok; job.ld = ld; job.n_out = n_out; job.k = k;
+    job.x = f.x; job.w = f.w; job.w2 = f.w2; job.out = f.out; job.early = f.early;
+    job.n_tok = f.n_tok; job.ld = f.ld; job.n_out = f.n_out; job.k = f.k;
+    job.zero = f.zero; job.n_zero = f.n_zero;
     return gdn::launch_few(job, st);
 }
 
@@ -1070,8 +1081,8 @@ gdn_status gdn_proj_gated(const void* act, const void* w_gate, const void* w_up,
     GDN_REQUIRE_PTR(w_gate, "w_gate");
     GDN_REQUIRE_PTR(w_up, "w_up");
     GDN_REQUIRE_PTR(out, "out");
-    return cuda_status(launch_fused(act, w_gate, w_up, out, n_tok, n_out, k, ld_out, false, (cudaStream_t)stream),
-                       "gdn_proj_gated");
+    const Fused f{act, w_gate, w_up, out, n_tok, ld_out, n_out, k, false, nullptr, nullptr, 0};
+    return cuda_status(launch_fused(f, (cudaStream_t)stream), "gdn_proj_gated");
 }
 
 static gdn_status ffn_sizes(int64_t n_tok, int32_t hidden, int32_t inter) {
@@ -1083,10 +1094,24 @@ static gdn_status ffn_sizes(int64_t n_tok, int32_t hidden, int32_t inter) {
     return GDN_OK;
 }
 
+// the gated half, then what the projection back splits along K
+struct FfnWs {
+    size_t split, bytes;
+    int32_t counters;
+};
+static FfnWs ffn_ws(int64_t n_tok, int32_t hidden, int32_t inter) {
+    const size_t half = (size_t)n_tok * inter * 2;
+    if (n_tok <= kFewTokens) return {0, half, 0};
+    const gdn::WidePlan plan = gdn::wide_plan(n_tok, hidden, inter, false);
+    if (plan.ws_bytes == 0) return {0, half, 0};
+    const size_t split = (half + 255) & ~(size_t)255;
+    return {split, split + plan.ws_bytes, plan.counters};
+}
+
 size_t gdn_ffn_workspace_size(int64_t n_tok, int32_t hidden, int32_t inter) {
     if (ffn_sizes(n_tok, hidden, inter)) return 0;
     ok();
-    return (size_t)n_tok * inter * 2;
+    return ffn_ws(n_tok, hidden, inter).bytes;
 }
 
 gdn_status gdn_ffn(const gdn_ffn_weights* ffn, const void* h, int64_t n_tok, void* out, void* workspace, size_t ws_bytes,
@@ -1101,23 +1126,36 @@ gdn_status gdn_ffn(const gdn_ffn_weights* ffn, const void* h, int64_t n_tok, voi
     GDN_REQUIRE_PTR(h, "h");
     GDN_REQUIRE_PTR(out, "out");
     GDN_REQUIRE_PTR(workspace, "workspace");
-    const size_t need = (size_t)n_tok * ffn->inter * 2;
-    if (ws_bytes < need)
-        return fail(GDN_ERR_WORKSPACE, "workspace: found %zu bytes, required %zu bytes", ws_bytes, need);
+    const FfnWs L = ffn_ws(n_tok, ffn->hidden, ffn->inter);
+    if (ws_bytes < L.bytes)
+        return fail(GDN_ERR_WORKSPACE, "workspace: found %zu bytes, required %zu bytes", ws_bytes, L.bytes);
     const cudaStream_t s = (cudaStream_t)stream;
-    const cudaError_t e = launch_fused(h, ffn->w_gate, ffn->w_up, workspace, n_tok, ffn->inter, ffn->hidden, ffn->inter, false, s);
+    void* split = static_cast<unsigned char*>(workspace) + L.split;
+    const Fused half{h, ffn->w_gate, ffn->w_up, workspace, n_tok, ffn->inter, ffn->inter, ffn->hidden, false,
+                     nullptr, static_cast<int32_t*>(split), L.counters};
+    const cudaError_t e = launch_fused(half, s);
     if (e != cudaSuccess) return cuda_status(e, "gdn_ffn (gated half)");
-    return cuda_status(launch_fused(workspace, ffn->w_down, nullptr, out, n_tok, ffn->hidden, ffn->inter, ffn->hidden, true, s),
-                       "gdn_ffn (projection back)");
+    const Fused back{workspace, ffn->w_down, nullptr, out, n_tok, ffn->hidden, ffn->hidden, ffn->inter, true,
+                     split, nullptr, 0};
+    return cuda_status(launch_fused(back, s), "gdn_ffn (projection back)");
 }
 
-// the tokens' low-rank activations, then their adapters
+// Requests of a few tokens each bring an adapter for (nearly) every token, a matrix product for none: they stay with the
+// kernel that gives each token its adapter on the CUDA cores.
+static bool lora_wide(int64_t n_tok, int32_t n_seg) { return n_tok > kFewTokens && n_tok >= 16 * (int64_t)n_seg; }
+
+// the tokens' low-rank activations, their adapters, then what the projection splits along K
 struct LoraWs {
-    size_t tok_adapter, bytes;
+    size_t tok_adapter, split, bytes;
+    int32_t counters;
 };
-static LoraWs lora_ws(int64_t n_tok, int32_t rank) {
-    const size_t low = (size_t)n_tok * (rank <= 32 ? 128 : rank <= 64 ? 256 : 512);
-    return {low, low + (size_t)n_tok * 4};
+static LoraWs lora_ws(int64_t n_tok, int32_t n_out, int32_t k, int32_t rank, int32_t n_seg) {
+    const size_t low = (size_t)n_tok * gdn::low_row(rank) * 2, end = low + (size_t)n_tok * 4;
+    if (!lora_wide(n_tok, n_seg)) return {low, 0, end, 0};
+    const gdn::WidePlan plan = gdn::wide_plan(n_tok, n_out, k, false);
+    if (plan.ws_bytes == 0) return {low, 0, end, 0};
+    const size_t split = (end + 255) & ~(size_t)255;
+    return {low, split, split + plan.ws_bytes, plan.counters};
 }
 
 static gdn_status lora_sizes(int64_t n_tok, int32_t n_out, int32_t k, int32_t rank, int32_t n_seg) {
@@ -1132,7 +1170,7 @@ static gdn_status lora_sizes(int64_t n_tok, int32_t n_out, int32_t k, int32_t ra
 size_t gdn_proj_lora_workspace_size(int64_t n_tok, int32_t n_out, int32_t k, int32_t rank, int32_t n_seg) {
     if (lora_sizes(n_tok, n_out, k, rank, n_seg)) return 0;
     ok();
-    return lora_ws(n_tok, rank).bytes;
+    return lora_ws(n_tok, n_out, k, rank, n_seg).bytes;
 }
 
 gdn_status gdn_proj_lora(const void* act, const void* w, const gdn_lora* lora, const int32_t* cu_rows,
@@ -1153,7 +1191,7 @@ gdn_status gdn_proj_lora(const void* act, const void* w, const gdn_lora* lora, c
     GDN_REQUIRE_PTR_A(cu_rows, "cu_rows", 4u);
     if (n_seg > 0) GDN_REQUIRE_PTR_A(adapter_idx, "adapter_idx", 4u);
     GDN_REQUIRE_PTR(workspace, "workspace");
-    const LoraWs L = lora_ws(n_tok, lora->rank);
+    const LoraWs L = lora_ws(n_tok, n_out, k, lora->rank, n_seg);
     if (ws_bytes < L.bytes)
         return fail(GDN_ERR_WORKSPACE, "workspace: found %zu bytes, required %zu bytes", ws_bytes, L.bytes);
     unsigned char* ws = static_cast<unsigned char*>(workspace);
@@ -1162,9 +1200,8 @@ gdn_status gdn_proj_lora(const void* act, const void* w, const gdn_lora* lora, c
     low.x = act; low.a = lora->a; low.scale = lora->scale; low.cu_rows = cu_rows; low.adapter_idx = adapter_idx;
     low.v = ws; low.tok_adapter = reinterpret_cast<int32_t*>(ws + L.tok_adapter);
     low.n_tok = n_tok; low.n_seg = n_seg; low.n_adapters = lora->n_adapters; low.rank = lora->rank; low.k = k;
-    // Requests of a few tokens each bring an adapter for (nearly) every token, a matrix product for none: they stay with
-    // the kernel that gives each token its adapter on the CUDA cores.
-    low.wide = n_tok > kFewTokens && n_tok >= 16 * (int64_t)n_seg;
+    low.wide = lora_wide(n_tok, n_seg);
+    low.zero = reinterpret_cast<int32_t*>(ws + L.split); low.n_zero = L.counters;
     const cudaError_t e = gdn::launch_lora_low(low, s);
     if (e != cudaSuccess) return cuda_status(e, "gdn_proj_lora (low side)");
     if (low.wide) {
@@ -1172,7 +1209,7 @@ gdn_status gdn_proj_lora(const void* act, const void* w, const gdn_lora* lora, c
         job.x = act; job.w = w; job.out = out;
         job.n_tok = n_tok; job.ld = ld_out; job.n_out = n_out; job.k = k;
         job.v = low.v; job.tok_adapter = low.tok_adapter; job.b = lora->b; job.rank = lora->rank;
-        job.n_adapters = lora->n_adapters;
+        job.n_adapters = lora->n_adapters; job.split_ws = ws + L.split;
         return cuda_status(gdn::launch_wide(job, s), "gdn_proj_lora");
     }
     gdn::FewJob job = {};

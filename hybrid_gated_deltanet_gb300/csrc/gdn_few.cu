@@ -76,6 +76,8 @@ struct FewArgs {
     const int32_t *cu_rows, *adapter_idx;
     const __nv_bfloat16* b;    // [n_adapters][n_out][rank]
     int32_t rank, n_adapters, n_seg;
+    int32_t* zero;  // counters of a kernel behind this one, set to zero here
+    int32_t n_zero;
 };
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
@@ -129,6 +131,8 @@ __global__ void __launch_bounds__(few_threads<MODE>(), 2)
     // ahead is one of the same call, which lets this one start only after its own wait (so all that came before it has
     // ended) and with its TMEM in hand (so holding TMEM here cannot keep it from its own).
     if (!P.early) griddep_wait();
+    if (P.n_zero > 0 && blockIdx.x == 0 && blockIdx.y == 0)
+        for (int i = threadIdx.x; i < P.n_zero; i += few_threads<MODE>()) P.zero[i] = 0;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = smem_raw + ((1024 - (tc::smem_addr(smem_raw) & 1023)) & 1023);
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::BAR_OFF);
@@ -428,6 +432,8 @@ cudaError_t launch_few_n(const FewJob& job, cudaStream_t st) {
     P.rank = job.rank;
     P.n_adapters = job.n_adapters;
     P.n_seg = job.n_seg;
+    P.zero = job.zero;
+    P.n_zero = job.n_zero;
     P.cu_rows = job.cu_rows;
     P.adapter_idx = job.adapter_idx;
     const unsigned tiles = (unsigned)((job.n_out + rows - 1) / rows);

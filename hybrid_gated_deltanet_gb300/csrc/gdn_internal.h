@@ -323,6 +323,8 @@ struct FewJob {
     const int32_t *cu_rows, *adapter_idx;  // what tok_adapter was made from
     const void* b;               // [n_adapters][n_out][rank]
     int32_t rank, n_adapters, n_seg;
+    int32_t* zero;  // as in WideJob
+    int32_t n_zero;
 };
 cudaError_t launch_few(const FewJob& job, cudaStream_t st);
 
@@ -336,8 +338,19 @@ struct WideJob {
     const int32_t* tok_adapter;  // [n_tok], -1: none
     const void* b;               // [n_adapters][n_out][rank]
     int32_t rank, n_adapters;
+    void* split_ws;  // wide_plan().ws_bytes, of which the first `counters` int32 are zero
+    int32_t* zero;   // counters to set to zero, for a launch_wide behind this one
+    int32_t n_zero;
 };
 cudaError_t launch_wide(const WideJob& job, cudaStream_t st);
+// Tiles of a launch_wide: `whole` in whole waves over the GPU, the `rest` in `split` parts along K, joined through a
+// workspace by whichever part of a tile comes last.
+struct WidePlan {
+    int64_t whole, rest;
+    int32_t split, counters;
+    size_t counter_bytes, ws_bytes;
+};
+WidePlan wide_plan(int64_t n_tok, int32_t n_out, int32_t k, bool gated);
 
 // Low-rank activations for launch_wide: v = hi + lo in bf16, a row of low_row(rank) elements being [hi | lo] in parts
 // of 16 ceil(rank / 16) (rank <= 32) or 64 ceil(rank / 64) elements, each padded with zeros to a multiple of 16.
@@ -352,6 +365,8 @@ struct LowJob {
     int32_t* tok_adapter;  // [n_tok], -1: none
     int64_t n_tok;
     int32_t n_seg, n_adapters, rank, k, wide;
+    int32_t* zero;  // as in WideJob
+    int32_t n_zero;
 };
 cudaError_t launch_lora_low(const LowJob& job, cudaStream_t st);
 

@@ -187,6 +187,8 @@ __global__ void __launch_bounds__(kLowTcThreads, 2)
     constexpr uint32_t COLS = 128;
     const LowJob& J = P.J;
     griddep_wait();
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < J.n_zero; i += kLowTcThreads) J.zero[i] = 0;
     if ((int)blockIdx.x >= P.n_split) {  // (whole clusters; no barrier of theirs is used here)
         griddep_launch_dependents();
         const int q = (int)blockIdx.x - P.n_split;

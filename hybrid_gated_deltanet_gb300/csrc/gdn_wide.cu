@@ -44,20 +44,25 @@ constexpr int kStoreOff = 6 * kStageBytes;
 constexpr int kBarOff = kStoreOff + 8 * kStoreBytes;  // full[6], empty[6], acc_full[2], acc_empty[2], v_full, v_empty, TMEM address
 constexpr int kWideSmem = kBarOff + (2 * 6 + 6) * 8 + 16 + 1024;
 static_assert(kWideSmem <= 227 * 1024, "shared memory of a CTA");
+constexpr int64_t kPartFloats = 128 * 256;  // a CTA's accumulator of one part of a tile
 
 struct WideArgs {
     int64_t n_tok, n_tiles;
     int32_t n_out;
     int32_t kb;          // 64-wide K blocks
-    // Tiles from n_whole on, which would leave pairs idle in a last wave of their own, are cut into `cut` parts of 256 / cut
-    // columns each: tile n_whole + i is part i % cut of whole tile n_whole + i / cut.
+    // Tiles from n_whole on, which would leave pairs idle in a last wave of their own, are split along K: job n_whole + i is
+    // part i % split of tile n_whole + i / split.
     int64_t n_whole;
-    int32_t cut;
+    int32_t split;
+    float* part;       // [split tile][part][CTA of the pair][64 groups of 4 columns][128 tokens][4]
+    int32_t* arrived;  // [split tile][CTA][epilogue warp], zero at the start
     int32_t tiles_n, tiles_t;
     int32_t token_fast;  // tile order: token blocks fastest (1) or weight blocks fastest (0)
     int32_t n_full;      // columns that go by TMA: n_out rounded down to 16 bytes
     __nv_bfloat16* out;  // the others
     int64_t ld;
+    int32_t* zero;  // counters of the kernel behind this one, set to zero here
+    int32_t n_zero;
     // lora
     const int32_t* tok_adapter;
     int32_t rank, n_adapters;
@@ -125,31 +130,33 @@ __device__ __forceinline__ void dealloc2(uint32_t taddr, uint32_t ncols) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
-// What a tile covers.  The smaller operand goes fastest, it is the one that every sweep reads again.
+// What a job covers.  The smaller operand goes fastest, it is the one that every sweep reads again.
 struct Tile {
-    int tt;       // token block
-    int half;     // weight rows of one CTA: half the accumulator's columns
-    int wrow;     // gated: first row of both matrices; else first weight row of the first CTA
-    bool narrow;  // cut: another box of weight rows
+    int tt, wn;        // token block, weight block
+    int kb0, kb1;      // K blocks
+    int at, part;      // split tile (-1: whole) and part
+    bool last;         // the part that takes the adapters
 };
-__device__ __forceinline__ Tile wide_tile(const WideArgs& P, int64_t tile, bool gated) {
-    int part = 0, cut = 1;
-    const bool narrow = tile >= P.n_whole && P.cut > 1;
-    if (narrow) {
-        cut = P.cut;
-        part = (int)((tile - P.n_whole) % cut);
-        tile = P.n_whole + (tile - P.n_whole) / cut;
+__device__ __forceinline__ Tile wide_tile(const WideArgs& P, int64_t job) {
+    Tile T;
+    int64_t tile = job;
+    T.at = -1, T.part = 0, T.kb0 = 0, T.kb1 = P.kb;
+    if (job >= P.n_whole && P.split > 1) {
+        T.at = (int)((job - P.n_whole) / P.split);
+        T.part = (int)((job - P.n_whole) % P.split);
+        T.kb0 = (int)((int64_t)T.part * P.kb / P.split);
+        T.kb1 = (int)((int64_t)(T.part + 1) * P.kb / P.split);
+        tile = P.n_whole + T.at;
     }
-    int wn, tt;
+    T.last = T.kb1 == P.kb;
     if (P.token_fast) {
-        wn = (int)(tile / P.tiles_t);
-        tt = (int)(tile % P.tiles_t);
+        T.wn = (int)(tile / P.tiles_t);
+        T.tt = (int)(tile % P.tiles_t);
     } else {
-        wn = (int)(tile % P.tiles_n);
-        tt = (int)(tile / P.tiles_n);
+        T.wn = (int)(tile % P.tiles_n);
+        T.tt = (int)(tile / P.tiles_n);
     }
-    const int half = 128 / cut;
-    return Tile{tt, half, gated ? wn * 128 + part * half : wn * 256 + part * 2 * half, narrow};
+    return T;
 }
 
 constexpr int kNoMore = 0x7fffffff;
@@ -180,12 +187,12 @@ struct TileAdapters {
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     k_wide(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap tw,
-           const __grid_constant__ CUtensorMap tw2, const __grid_constant__ CUtensorMap twn,
-           const __grid_constant__ CUtensorMap tw2n, const __grid_constant__ CUtensorMap tout,
-           const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tb,
-           const __grid_constant__ CUtensorMap tbn, const __grid_constant__ WideArgs P) {
+           const __grid_constant__ CUtensorMap tw2, const __grid_constant__ CUtensorMap tout,
+           const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tb, const __grid_constant__ WideArgs P) {
     const int S = wide_stages(MODE == kLora, P.rank);
     griddep_wait();  // launched with programmatic serialization: nothing is held while kernels ahead still run
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < P.n_zero; i += kWideThreads) P.zero[i] = 0;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = smem_raw + ((1024 - (tc::smem_addr(smem_raw) & 1023)) & 1023);
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + kBarOff);
@@ -243,14 +250,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
             if (ok && cta == 0 && lane == 0) mbar_arrive_expect_tx(full + st_i, 2u * (uint32_t)bytes);
         };
         for (int64_t tile = tile0; tile < P.n_tiles && ok; tile += tstep) {
-            const Tile T = wide_tile(P, tile, MODE == kGated);
-            const int row = T.tt * kWideTok + 128 * cta, wrow = MODE == kGated ? T.wrow : T.wrow + T.half * cta;
-            const void* wmap = MODE == kGated && cta == 1 ? (T.narrow ? &tw2n : &tw2) : T.narrow ? &twn : &tw;
-            const int w_bytes = T.half * kWideK * 2;
+            const Tile T = wide_tile(P, tile);
+            const int row = T.tt * kWideTok + 128 * cta, wrow = MODE == kGated ? T.wn * 128 : T.wn * 256 + 128 * cta;
+            const void* wmap = MODE == kGated && cta == 1 ? &tw2 : &tw;
             TileAdapters ta;
             if (MODE == kLora) ta.load(P, T.tt, lane);
-            for (int kb = 0; kb < P.kb && ok; ++kb, next_stage()) {
-                turn(kHalfBytes + w_bytes);
+            for (int kb = T.kb0; kb < T.kb1 && ok; ++kb, next_stage()) {
+                turn(2 * kHalfBytes);
                 if (ok && lane == 0) {
                     unsigned char* st = sm + st_i * kStageBytes;
                     const uint32_t bar = mapa_shared(smem_u32(full + st_i), 0);
@@ -258,7 +264,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                     tma2_2d(st + kHalfBytes, wmap, kb * kWideK, wrow, bar);
                 }
             }
-            if (MODE == kLora && ok) {
+            if (MODE == kLora && ok && T.last) {
                 int a = ta.next();
                 if (a == kNoMore) continue;
                 const bool w = mbar_wait(v_empty, (n_v & 1u) ^ 1u);
@@ -277,13 +283,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                     if (++j == bb) j = 0, a = ta.next();
                     const int a1 = a, j1 = j;
                     if (a != kNoMore && ++j == bb) j = 0, a = ta.next();
-                    turn(a1 != kNoMore ? 2 * w_bytes : w_bytes);
+                    turn(a1 != kNoMore ? 2 * kHalfBytes : kHalfBytes);
                     if (ok && lane == 0) {
                         unsigned char* st = sm + st_i * kStageBytes;
                         const uint32_t bar = mapa_shared(smem_u32(full + st_i), 0);
-                        const void* bmap = T.narrow ? &tbn : &tb;
-                        tma2_3d(st, bmap, j0 * kWideK, wrow, a0, bar);
-                        if (a1 != kNoMore) tma2_3d(st + kHalfBytes, bmap, j1 * kWideK, wrow, a1, bar);
+                        tma2_3d(st, &tb, j0 * kWideK, wrow, a0, bar);
+                        if (a1 != kNoMore) tma2_3d(st + kHalfBytes, &tb, j1 * kWideK, wrow, a1, bar);
                     }
                     next_stage();
                 }
@@ -294,15 +299,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
             uint32_t use = 0, n_v = 0;
             for (int64_t tile = tile0; tile < P.n_tiles && ok; tile += tstep, ++use) {
                 const uint32_t buf = use & 1u;
-                const Tile T = wide_tile(P, tile, MODE == kGated);
-                const uint32_t idesc = idesc_bf16(256, 2 * T.half);
+                const Tile T = wide_tile(P, tile);
+                constexpr uint32_t idesc = idesc_bf16(256, 256);
                 TileAdapters ta;
                 if (MODE == kLora) ta.load(P, T.tt, lane);
                 ok = __all_sync(0xffffffffu, mbar_wait(acc_empty + buf, ((use >> 1) & 1u) ^ 1u));
                 if (!ok) break;
                 tc::fence_after();
                 const uint32_t d = tm + buf * 256;
-                for (int kb = 0; kb < P.kb; ++kb, next_stage()) {
+                for (int kb = T.kb0; kb < T.kb1; ++kb, next_stage()) {
                     ok = __all_sync(0xffffffffu, mbar_wait(full + st_i, st_ph));
                     if (!ok) break;
                     tc::fence_after();
@@ -311,13 +316,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
 #pragma unroll
                         for (int k16 = 0; k16 < kWideK / 16; ++k16)
                             mma2_bf16(d, tc::sdesc(a0 + k16 * 32), tc::sdesc(b0 + k16 * 32), idesc,
-                                      kb > 0 || k16 > 0 ? 1u : 0u);
+                                      kb > T.kb0 || k16 > 0 ? 1u : 0u);
                         commit2(empty + st_i);
                     }
                     __syncwarp();
                 }
                 if (!ok) break;
-                int a = MODE == kLora ? ta.next() : kNoMore;
+                int a = MODE == kLora && T.last ? ta.next() : kNoMore;
                 if (a != kNoMore) {
                     ok = __all_sync(0xffffffffu, mbar_wait(v_full, n_v & 1u));
                     ++n_v;
@@ -366,12 +371,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
         uint32_t use = 0, n_store = 0;
         for (int64_t tile = tile0; tile < P.n_tiles; tile += tstep, ++use) {
             const uint32_t buf = use & 1u;
-            const Tile T = wide_tile(P, tile, MODE == kGated);
-            const int half = T.half, cols = MODE == kGated ? half : 2 * half;  // output columns of the tile
+            const Tile T = wide_tile(P, tile);
+            constexpr int cols = MODE == kGated ? 128 : 256;  // output columns of the tile
             ok = __all_sync(0xffffffffu, mbar_wait(acc_full + buf, (use >> 1) & 1u));
             if (!ok) break;
             tc::fence_after();
-            const int t0 = T.tt * kWideTok + 128 * cta + 32 * q4, n0 = T.wrow;
+            const int t0 = T.tt * kWideTok + 128 * cta + 32 * q4, n0 = T.wn * cols;
+            const uint32_t acc = tc::taddr(tm, 32 * q4, (int)(buf * 256));
+            const bool there = t0 + lane < P.n_tok;
+            const float4* parts = nullptr;  // of this token, 128 float4 from a group of columns to the next
+            if (MODE != kGated && T.at >= 0) {
+                // a part of a split tile: into the workspace, and on if it is not the last to arrive
+                float4* to = reinterpret_cast<float4*>(P.part) + ((int64_t)T.at * P.split * 2 + cta) * (kPartFloats / 4) +
+                             32 * q4 + lane;
+                parts = to;
+                to += (int64_t)T.part * 2 * (kPartFloats / 4);
+                for (int c0 = 0; c0 < 256 && n0 + c0 < P.n_out; c0 += 32) {
+                    float v[32];
+                    tc::ld32(acc + c0, v);
+                    if (there)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            to[(c0 / 4 + i) * 128] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                }
+                tc::fence_before();
+                __threadfence();
+                __syncwarp();
+                int n = 0;
+                if (lane == 0) {
+                    arrive_cluster(empty_bar[buf]);
+                    n = atomicAdd(P.arrived + (T.at * 2 + cta) * 4 + q4, 1);
+                }
+                n = __shfl_sync(0xffffffffu, n, 0);
+                if (n != P.split - 1) continue;
+                __threadfence();
+            }
+            // 32 columns of the accumulator, or the sum of the parts in their order, whoever came last
+            auto columns = [&](int c, float v[32]) {
+                if (T.at < 0) {
+                    tc::ld32(acc + c, v);
+                    return;
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                const int n_parts = there && n0 + c < P.n_out ? P.split : 0;
+                for (int p = 0; p < n_parts; ++p) {
+                    float4 w[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        w[i] = __ldcg(parts + (int64_t)p * 2 * (kPartFloats / 4) + (c / 4 + i) * 128);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        v[4 * i] += w[i].x, v[4 * i + 1] += w[i].y, v[4 * i + 2] += w[i].z, v[4 * i + 3] += w[i].w;
+                }
+            };
             for (int c0 = 0; c0 < cols; c0 += 64) {
                 unsigned char* dst = store + (n_store & 1u) * kStoreBytes + lane * 128;
                 // the store before the last has read this buffer
@@ -380,18 +433,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float v[32];
-                    const uint32_t col = tc::taddr(tm, 32 * q4, (int)(buf * 256) + c0 + 32 * h);
                     if (MODE == kGated) {
                         uint32_t g[32], u[32];
-                        tc::ld32_nowait(col, g);
-                        tc::ld32_nowait(col + half, u);
+                        tc::ld32_nowait(acc + c0 + 32 * h, g);
+                        tc::ld32_nowait(acc + c0 + 32 * h + 128, u);
                         tc::ld_wait();
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = silu_gate(__uint_as_float(g[i])) * __uint_as_float(u[i]);
                     } else {
-                        tc::ld32(col, v);
+                        columns(c0 + 32 * h, v);
                     }
-                    if (c0 + 64 >= cols && h == 1) {  // the accumulator has been read
+                    if (c0 + 64 >= cols && h == 1 && T.at < 0) {  // the accumulator has been read
                         tc::fence_before();
                         __syncwarp();
                         if (lane == 0) arrive_cluster(empty_bar[buf]);
@@ -401,7 +453,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                         *reinterpret_cast<uint4*>(dst + (((4 * h + i) ^ (lane & 7)) << 4)) = pack8(v + 8 * i);
                 }
                 // columns past the last whole 16 bytes (a TMA store writes those 16 bytes in full)
-                if (n0 + c0 + 64 > P.n_full && t0 + lane < P.n_tok)
+                if (n0 + c0 + 64 > P.n_full && there)
                     for (int n = max(P.n_full, n0 + c0); n < min(P.n_out, n0 + c0 + 64); ++n) {
                         const int c = n - n0 - c0;
                         P.out[(int64_t)(t0 + lane) * P.ld + n] =
@@ -466,23 +518,20 @@ cudaError_t launch_wide_mode(const WideJob& job, cudaStream_t st) {
     P.tok_adapter = job.tok_adapter;
     P.rank = job.rank;
     P.n_adapters = job.n_adapters;
+    const WidePlan plan = wide_plan(job.n_tok, job.n_out, job.k, MODE == kGated);
     constexpr int cols = MODE == kGated ? 128 : 256;
     P.tiles_n = (job.n_out + cols - 1) / cols;
-    const int64_t tiles = (int64_t)P.tiles_n * P.tiles_t;
-    P.n_whole = tiles / pairs * pairs;
-    // the rest, cut where its waves then cost less; a tile costs its columns and a start worth about 24
-    const int64_t rest = tiles - P.n_whole;
-    int64_t least = -1;
-    for (int cut = 1; cut <= (MODE == kGated ? 2 : 4); cut *= 2) {  // (results are stored in pieces of 64 columns)
-        const int64_t cost = (rest * cut + pairs - 1) / pairs * (256 / cut + 24);
-        if (least < 0 || cost < least) {
-            least = cost;
-            P.cut = cut;
-        }
+    P.n_whole = plan.whole;
+    P.split = plan.split;
+    P.n_tiles = plan.whole + plan.rest * plan.split;
+    if (plan.split > 1) {
+        P.arrived = static_cast<int32_t*>(job.split_ws);
+        P.part = reinterpret_cast<float*>(static_cast<unsigned char*>(job.split_ws) + plan.counter_bytes);
     }
-    P.n_tiles = P.n_whole + rest * P.cut;
+    P.zero = job.zero;
+    P.n_zero = job.n_zero;
     P.token_fast = job.n_tok < (MODE == kGated ? 2 : 1) * (int64_t)job.n_out;  // the tokens are the smaller operand
-    CUtensorMap mx, mw, mw2, mwn, mw2n, mo, mv, mb, mbn;
+    CUtensorMap mx, mw, mw2, mo, mv, mb;
     bool good = map_rows(&mx, job.x, job.n_tok, job.k, 128) && map_rows(&mw, job.w, job.n_out, job.k, 128) &&
                 map_rows(&mo, job.out, job.n_tok, std::max(P.n_full, 8), 32, job.ld);
     if (MODE == kGated) good = good && map_rows(&mw2, job.w2, job.n_out, job.k, 128);
@@ -491,20 +540,39 @@ cudaError_t launch_wide_mode(const WideJob& job, cudaStream_t st) {
         good = good && map_rows(&mv, job.v, job.n_tok, low_row(job.rank), 128) &&
                map_stack(&mb, job.b, job.n_adapters, job.n_out, job.rank, 128);
     else mv = mb = mx;
-    mwn = mw, mw2n = mw2, mbn = mb;
-    if (P.cut > 1) {
-        const int box = 128 / P.cut;
-        good = good && map_rows(&mwn, job.w, job.n_out, job.k, box);
-        if (MODE == kGated) good = good && map_rows(&mw2n, job.w2, job.n_out, job.k, box);
-        if (MODE == kLora) good = good && map_stack(&mbn, job.b, job.n_adapters, job.n_out, job.rank, box);
-    }
     if (!good) return cudaErrorInvalidValue;
     const int64_t grid = 2 * std::min<int64_t>(P.n_tiles, pairs);
-    return launch_pdl(k_wide<MODE>, dim3((unsigned)grid), dim3(kWideThreads), kWideSmem, st, mx, mw, mw2, mwn, mw2n, mo, mv,
-                      mb, mbn, P);
+    return launch_pdl(k_wide<MODE>, dim3((unsigned)grid), dim3(kWideThreads), kWideSmem, st, mx, mw, mw2, mo, mv, mb, P);
 }
 
 }  // namespace
+
+// Depends on the sizes only, so that a workspace can be sized without a device: 76 pairs, of which a device with others
+// makes the same jobs.  Cycles: a K block takes 700, and no fewer with fewer columns (the tensor cores read the 128 rows of x in
+// the same time for 64 columns as for 256: halves and quarters of tiles in the last wave cost as much as whole ones); a job's
+// start and end take 1500, and parts of a tile, written and read again, 9000 and 2500 each.
+WidePlan wide_plan(int64_t n_tok, int32_t n_out, int32_t k, bool gated) {
+    constexpr int64_t kPairs = 76;
+    const int kb = (k + kWideK - 1) / kWideK, cols = gated ? 128 : 256;
+    const int64_t tiles = (n_out + cols - 1) / cols * ((n_tok + kWideTok - 1) / kWideTok);
+    WidePlan plan;
+    plan.whole = tiles / kPairs * kPairs;
+    plan.rest = tiles - plan.whole;
+    plan.split = 1;
+    int64_t least = -1;
+    for (int c = 1; c <= (gated ? 1 : 8) && c <= std::max(1, kb / 2); ++c) {
+        const int64_t waves = (plan.rest * c + kPairs - 1) / kPairs;
+        const int64_t cost = waves * ((kb + c - 1) / c * 700 + 1500) + (c > 1 ? 9000 + 2500 * c : 0);
+        if (least < 0 || cost < least) {
+            least = cost;
+            plan.split = c;
+        }
+    }
+    plan.counters = plan.split > 1 ? (int32_t)plan.rest * 8 : 0;
+    plan.counter_bytes = ((size_t)plan.counters * 4 + 255) & ~(size_t)255;
+    plan.ws_bytes = plan.split > 1 ? plan.counter_bytes + (size_t)plan.rest * plan.split * 2 * kPartFloats * 4 : 0;
+    return plan;
+}
 
 cudaError_t take_device_status_wide(unsigned* out) { return take_device_status_tu(out); }
 

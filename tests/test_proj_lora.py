@@ -70,6 +70,19 @@ def test_lora_ranks(rank, lens):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("rank", [16, 40, 64, 128])
+@pytest.mark.parametrize("lens,n_out,k", [([1, 300, 30, 1, 257], 265, 4104), ([200], 96, 2560), ([5000, 1, 1, 15000], 264, 2560)])
+def test_lora_split_along_k(lens, n_out, k, rank):
+    """Few tiles of a long K, alone or behind whole waves of tiles: parts of a tile joined through the workspace, the adapters in
+    one of them; twice, with the counters that the first call left."""
+    c = Case(rank + n_out, lens, [(i * 2) % 5 - 1 for i in range(len(lens))], k, n_out, rank, 4)
+    ws = torch.full((gb.gdn_proj_lora_workspace_size(c.n, n_out, k, rank, len(lens)),), 255, dtype=torch.uint8, device="cuda")
+    out = c.run(ws=ws)
+    c.check(out)
+    assert torch.equal(c.run(ws=ws)[:, :n_out], out[:, :n_out])
+    assert gb.gdn_device_status() == 0
+
+
 @pytest.mark.parametrize("n,n_out,k", [(1, 12352, 2560), (64, 2560, 4096), (1, 1, 8), (200, 1, 8), (33, 2000, 1024)])
 def test_lora_decoding_sizes(n, n_out, k):
     c = Case(n, [1] * n, [i % 5 for i in range(n)], k, n_out, 16, 5)
@@ -137,12 +150,12 @@ def test_lora_out_rows_and_workspace_end(lens):
     assert (out[:c.n, 100:] == 7).all() and (out[c.n:] == 7).all() and (ws[size:] == 9).all()
 
 
-@pytest.mark.parametrize("lens", [[1] * 12, [1, 400, 1, 60]])
-def test_lora_captured_replayed_and_beside_another(lens):
-    c = Case(16, lens, [i % 3 for i in range(len(lens))], 264, 392, 32, 3)
+@pytest.mark.parametrize("lens,k", [([1] * 12, 264), ([1, 400, 1, 60], 264), ([1, 400, 1, 60], 4096)])
+def test_lora_captured_replayed_and_beside_another(lens, k):
+    c = Case(16, lens, [i % 3 for i in range(len(lens))], k, 392, 32, 3)
     x, w, ad = c.x.cuda(), c.w.cuda(), gb.Lora(c.a.cuda(), c.b.cuda(), c.scale.cuda())
     cu, which = i32(c.cu), i32(c.which)
-    size = gb.gdn_proj_lora_workspace_size(c.n, 392, 264, 32, len(lens))
+    size = gb.gdn_proj_lora_workspace_size(c.n, 392, k, 32, len(lens))
     ws, ws2 = (torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(2))
     out, side_out = (torch.zeros((c.n, 392), dtype=BF, device="cuda") for _ in range(2))
     gb.gdn_proj_lora(x, w, ad, cu, which, out, ws)
