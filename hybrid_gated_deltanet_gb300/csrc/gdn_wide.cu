@@ -415,14 +415,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = 0.f;
                 const int n_parts = there && n0 + c < P.n_out ? P.split : 0;
-                for (int p = 0; p < n_parts; ++p) {
-                    float4 w[8];
+                for (int p0 = 0; p0 < n_parts; p0 += 4) {  // four parts' loads under way together
+                    float4 w[4][8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        w[i] = __ldcg(parts + (int64_t)p * 2 * (kPartFloats / 4) + (c / 4 + i) * 128);
+                    for (int q = 0; q < 4; ++q)
+                        if (p0 + q < n_parts)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        v[4 * i] += w[i].x, v[4 * i + 1] += w[i].y, v[4 * i + 2] += w[i].z, v[4 * i + 3] += w[i].w;
+                            for (int i = 0; i < 8; ++i)
+                                w[q][i] = __ldcg(parts + (int64_t)(p0 + q) * 2 * (kPartFloats / 4) + (c / 4 + i) * 128);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (p0 + q < n_parts)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                v[4 * i] += w[q][i].x, v[4 * i + 1] += w[q][i].y, v[4 * i + 2] += w[q][i].z, v[4 * i + 3] += w[q][i].w;
                 }
             };
             for (int c0 = 0; c0 < cols; c0 += 64) {
