@@ -1044,9 +1044,7 @@ static gdn_status proj_sizes(int64_t n_tok, int32_t n_out, int32_t k, int64_t ld
     return GDN_OK;
 }
 
-// Up to kFewTokens tokens the weights stream past the tokens, from there on tiles of 256 tokens go to pairs of SMs.
-constexpr int64_t kFewTokens = 128;
-
+// The weights stream past a few tokens, or tiles of 256 tokens go to pairs of SMs: whichever should take less.
 struct Fused {
     const void *x, *w, *w2;
     void* out;
@@ -1057,12 +1055,21 @@ struct Fused {
     int32_t* zero;
     int32_t n_zero;
 };
-static cudaError_t launch_fused(const Fused& f, cudaStream_t st) {
-    if (f.n_tok > kFewTokens) {
+struct FusedPlan {
+    bool wide;
+    gdn::WidePlan plan;
+};
+static FusedPlan fused_plan(int64_t n_tok, int32_t n_out, int32_t k, bool gated) {
+    const gdn::FewPlan few = gdn::few_plan(n_tok, n_out, k, gated, 0);
+    const gdn::WidePlan wide = gdn::wide_plan(n_tok, n_out, k, gated, 0, 0);
+    return {few.us100 < 0 || (n_tok > 64 && wide.us100 < few.us100), wide};
+}
+static cudaError_t launch_fused(const Fused& f, const FusedPlan& p, cudaStream_t st) {
+    if (p.wide) {
         gdn::WideJob job = {};
         job.x = f.x; job.w = f.w; job.w2 = f.w2; job.out = f.out;
         job.n_tok = f.n_tok; job.ld = f.ld; job.n_out = f.n_out; job.k = f.k;
-        job.split_ws = f.split_ws; job.zero = f.zero; job.n_zero = f.n_zero;
+        job.plan = p.plan; job.split_ws = f.split_ws; job.zero = f.zero; job.n_zero = f.n_zero;
         return gdn::launch_wide(job, st);
     }
     gdn::FewJob job = {};
@@ -1082,7 +1089,7 @@ gdn_status gdn_proj_gated(const void* act, const void* w_gate, const void* w_up,
     GDN_REQUIRE_PTR(w_up, "w_up");
     GDN_REQUIRE_PTR(out, "out");
     const Fused f{act, w_gate, w_up, out, n_tok, ld_out, n_out, k, false, nullptr, nullptr, 0};
-    return cuda_status(launch_fused(f, (cudaStream_t)stream), "gdn_proj_gated");
+    return cuda_status(launch_fused(f, fused_plan(n_tok, n_out, k, true), (cudaStream_t)stream), "gdn_proj_gated");
 }
 
 static gdn_status ffn_sizes(int64_t n_tok, int32_t hidden, int32_t inter) {
@@ -1096,16 +1103,15 @@ static gdn_status ffn_sizes(int64_t n_tok, int32_t hidden, int32_t inter) {
 
 // the gated half, then what the projection back splits along K
 struct FfnWs {
+    FusedPlan back;
     size_t split, bytes;
     int32_t counters;
 };
 static FfnWs ffn_ws(int64_t n_tok, int32_t hidden, int32_t inter) {
-    const size_t half = (size_t)n_tok * inter * 2;
-    if (n_tok <= kFewTokens) return {0, half, 0};
-    const gdn::WidePlan plan = gdn::wide_plan(n_tok, hidden, inter, false);
-    if (plan.ws_bytes == 0) return {0, half, 0};
-    const size_t split = (half + 255) & ~(size_t)255;
-    return {split, split + plan.ws_bytes, plan.counters};
+    const size_t half = (size_t)n_tok * inter * 2, split = (half + 255) & ~(size_t)255;
+    const FusedPlan back = fused_plan(n_tok, hidden, inter, false);
+    if (!back.wide || back.plan.ws_bytes == 0) return {back, 0, half, 0};
+    return {back, split, split + back.plan.ws_bytes, back.plan.counters};
 }
 
 size_t gdn_ffn_workspace_size(int64_t n_tok, int32_t hidden, int32_t inter) {
@@ -1133,29 +1139,30 @@ gdn_status gdn_ffn(const gdn_ffn_weights* ffn, const void* h, int64_t n_tok, voi
     void* split = static_cast<unsigned char*>(workspace) + L.split;
     const Fused half{h, ffn->w_gate, ffn->w_up, workspace, n_tok, ffn->inter, ffn->inter, ffn->hidden, false,
                      nullptr, static_cast<int32_t*>(split), L.counters};
-    const cudaError_t e = launch_fused(half, s);
+    const cudaError_t e = launch_fused(half, fused_plan(n_tok, ffn->inter, ffn->hidden, true), s);
     if (e != cudaSuccess) return cuda_status(e, "gdn_ffn (gated half)");
     const Fused back{workspace, ffn->w_down, nullptr, out, n_tok, ffn->hidden, ffn->hidden, ffn->inter, true,
                      split, nullptr, 0};
-    return cuda_status(launch_fused(back, s), "gdn_ffn (projection back)");
+    return cuda_status(launch_fused(back, L.back, s), "gdn_ffn (projection back)");
 }
-
-// Requests of a few tokens each bring an adapter for (nearly) every token, a matrix product for none: they stay with the
-// kernel that gives each token its adapter on the CUDA cores.
-static bool lora_wide(int64_t n_tok, int32_t n_seg) { return n_tok > kFewTokens && n_tok >= 16 * (int64_t)n_seg; }
 
 // the tokens' low-rank activations, their adapters, then what the projection splits along K
 struct LoraWs {
+    bool wide;
+    gdn::WidePlan plan;
     size_t tok_adapter, split, bytes;
     int32_t counters;
 };
 static LoraWs lora_ws(int64_t n_tok, int32_t n_out, int32_t k, int32_t rank, int32_t n_seg) {
-    const size_t low = (size_t)n_tok * gdn::low_row(rank) * 2, end = low + (size_t)n_tok * 4;
-    if (!lora_wide(n_tok, n_seg)) return {low, 0, end, 0};
-    const gdn::WidePlan plan = gdn::wide_plan(n_tok, n_out, k, false);
-    if (plan.ws_bytes == 0) return {low, 0, end, 0};
-    const size_t split = (end + 255) & ~(size_t)255;
-    return {low, split, split + plan.ws_bytes, plan.counters};
+    const size_t low = (size_t)n_tok * gdn::low_row(rank) * 2, end = low + (size_t)n_tok * 4, split = (end + 255) & ~(size_t)255;
+    // Requests of a few tokens each bring an adapter for (nearly) every token, a matrix product for none: the kernel of few
+    // tokens gives each token its adapter on the CUDA cores, the one of many takes each adapter through the tensor cores.
+    // What comes before them takes 4 and 13 us.
+    const gdn::FewPlan few = gdn::few_plan(n_tok, n_out, k, false, rank);
+    const gdn::WidePlan plan = gdn::wide_plan(n_tok, n_out, k, false, rank, n_tok > 0 ? 256 * (int64_t)n_seg / n_tok + 1 : 0);
+    const bool wide = few.us100 < 0 || (n_tok > 64 && plan.us100 + 1300 < few.us100 + 400);
+    if (!wide || plan.ws_bytes == 0) return {wide, plan, low, 0, end, 0};
+    return {wide, plan, low, split, split + plan.ws_bytes, plan.counters};
 }
 
 static gdn_status lora_sizes(int64_t n_tok, int32_t n_out, int32_t k, int32_t rank, int32_t n_seg) {
@@ -1200,7 +1207,7 @@ gdn_status gdn_proj_lora(const void* act, const void* w, const gdn_lora* lora, c
     low.x = act; low.a = lora->a; low.scale = lora->scale; low.cu_rows = cu_rows; low.adapter_idx = adapter_idx;
     low.v = ws; low.tok_adapter = reinterpret_cast<int32_t*>(ws + L.tok_adapter);
     low.n_tok = n_tok; low.n_seg = n_seg; low.n_adapters = lora->n_adapters; low.rank = lora->rank; low.k = k;
-    low.wide = lora_wide(n_tok, n_seg);
+    low.wide = L.wide;
     low.zero = reinterpret_cast<int32_t*>(ws + L.split); low.n_zero = L.counters;
     const cudaError_t e = gdn::launch_lora_low(low, s);
     if (e != cudaSuccess) return cuda_status(e, "gdn_proj_lora (low side)");
@@ -1209,7 +1216,7 @@ gdn_status gdn_proj_lora(const void* act, const void* w, const gdn_lora* lora, c
         job.x = act; job.w = w; job.out = out;
         job.n_tok = n_tok; job.ld = ld_out; job.n_out = n_out; job.k = k;
         job.v = low.v; job.tok_adapter = low.tok_adapter; job.b = lora->b; job.rank = lora->rank;
-        job.n_adapters = lora->n_adapters; job.split_ws = ws + L.split;
+        job.n_adapters = lora->n_adapters; job.plan = L.plan; job.split_ws = ws + L.split;
         return cuda_status(gdn::launch_wide(job, s), "gdn_proj_lora");
     }
     gdn::FewJob job = {};

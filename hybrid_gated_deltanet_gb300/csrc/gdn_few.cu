@@ -378,41 +378,11 @@ __global__ void __launch_bounds__(few_threads<MODE>(), 2)
     }
 }
 
-// Cluster size: the CTAs run in waves of two per SM (fewer where clusters do not fit), and a CTA costs its K blocks and a
-// start and end worth about kFewEnds of them.
-constexpr int kFewEnds = 6;
-
-// CTAs of clusters of ks that run at the same time, two on an SM; once per device.  (Clusters of 3, 5 and more leave some
-// of a GPC's SMs empty: the runtime counts 46 of 3 and 15 of 8 on the 152 SMs, one CTA on each.)
 template <int N, int MODE>
-int few_slots(int ks) {
-    static std::atomic<int> known[64][9];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return ks;
-    std::atomic<int>& slot = known[dev & 63][ks];
-    int n = slot.load(std::memory_order_acquire);
-    if (n > 0) return n;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)ks;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(ks * 512));
-    cfg.blockDim = dim3(few_threads<MODE>());
-    cfg.dynamicSmemBytes = FewLay<N, MODE>::SMEM_ALLOC;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, k_few<N, MODE>, &cfg) != cudaSuccess || n < 1) n = 1;
-    n = 2 * std::min(n * ks, sm_count());
-    slot.store(n, std::memory_order_release);
-    return n;
-}
-
-template <int N, int MODE>
-cudaError_t launch_few_n(const FewJob& job, cudaStream_t st) {
+cudaError_t launch_few_n(const FewJob& job, int ks, cudaStream_t st) {
     using L = FewLay<N, MODE>;
     static std::atomic<uint64_t> smem_set{0};
-    cudaError_t e = raise_smem_limit_shared(k_few<N, MODE>, L::SMEM_ALLOC, smem_set);
+    const cudaError_t e = raise_smem_limit_shared(k_few<N, MODE>, L::SMEM_ALLOC, smem_set);
     if (e != cudaSuccess) return e;
     constexpr int rows = MODE == kGated ? kFewM / 2 : kFewM;
     CUtensorMap mw, mw2, mx;
@@ -437,38 +407,55 @@ cudaError_t launch_few_n(const FewJob& job, cudaStream_t st) {
     P.cu_rows = job.cu_rows;
     P.adapter_idx = job.adapter_idx;
     const unsigned tiles = (unsigned)((job.n_out + rows - 1) / rows);
-    const int64_t all = (int64_t)tiles * ((job.n_tok + N - 1) / N);
-    int64_t least = -1;
-    int ks = 1;
-    for (int c = 1; c <= 8 && c <= std::max(1, P.kb / 2); ++c) {
-        const int64_t slots = few_slots<N, MODE>(c);
-        const int64_t cost = (all * c + slots - 1) / slots * ((P.kb + c - 1) / c + kFewEnds);
-        if (least < 0 || cost < least) {
-            least = cost;
-            ks = c;
-        }
-    }
     P.ks = ks;
     return launch_pdl_cluster(k_few<N, MODE>, dim3(tiles * ks, (unsigned)((job.n_tok + N - 1) / N)), dim3(few_threads<MODE>()),
                               L::SMEM_ALLOC, ks, st, mw, mw2, mx, P);
 }
 
 template <int MODE>
-cudaError_t launch_few_mode(const FewJob& job, cudaStream_t st) {
-    if (job.n_tok <= 16) return launch_few_n<16, MODE>(job, st);
-    if (job.n_tok <= 32) return launch_few_n<32, MODE>(job, st);
-    if (job.n_tok <= 64) return launch_few_n<64, MODE>(job, st);
-    return launch_few_n<128, MODE>(job, st);
+cudaError_t launch_few_mode(const FewJob& job, const FewPlan& plan, cudaStream_t st) {
+    switch (plan.n) {
+        case 16: return launch_few_n<16, MODE>(job, plan.ks, st);
+        case 32: return launch_few_n<32, MODE>(job, plan.ks, st);
+        case 64: return launch_few_n<64, MODE>(job, plan.ks, st);
+        default: return launch_few_n<128, MODE>(job, plan.ks, st);
+    }
 }
 
 }  // namespace
 
 cudaError_t take_device_status_few(unsigned* out) { return take_device_status_tu(out); }
 
+// Tokens of a tile and cluster size.  The CTAs run in waves, and a CTA costs its K blocks (0.3 us each, more with more
+// tokens), a start and an end, a little for each CTA of its cluster, and with adapters its share of the tokens (0.3 us each at
+// rank 16, 0.7 at 64): `us100` is what that came to against measurements of 100 to 1000 tokens, within a quarter.
+// A tile takes the fewest tokens that hold all of them, 128 at most; with adapters also fewer, where more CTAs then share
+// the tokens at the price of reading the weights again.  Depends on the sizes only.
+FewPlan few_plan(int64_t n_tok, int32_t n_out, int32_t k, bool gated, int32_t rank) {
+    // CTAs of clusters of 1 .. 8 that run at the same time on 152 SMs, two on each: clusters of 3, 5 and more leave some of a
+    // GPC's SMs empty (cudaOccupancyMaxActiveClusters)
+    constexpr int kSlots[9] = {0, 304, 304, 276, 288, 280, 276, 210, 240};
+    const int rows = gated ? kFewM / 2 : kFewM, kb = (k + kFewK - 1) / kFewK;
+    const int most = n_tok <= 16 ? 16 : n_tok <= 32 ? 32 : n_tok <= 64 ? 64 : 128;
+    FewPlan plan{most, 1, -1};
+    for (int n = most; n >= (rank > 0 ? 16 : most); n /= 2) {
+        const int64_t tiles_t = (n_tok + n - 1) / n, tiles = (n_out + rows - 1) / rows * tiles_t;
+        if (tiles_t > 65535) break;
+        for (int c = 1; c <= 8 && c <= std::max(1, kb / 2); ++c) {
+            const int64_t tok = (std::min<int64_t>(n, n_tok) + c - 1) / c;
+            const int64_t one = (kb + c - 1) / c * 10 * (128 + n) / 128 + 80 + 10 * c + (rank > 0 ? tok * (6 + rank / 4) : 0);
+            const int64_t cost = 3 * ((tiles * c + kSlots[c] - 1) / kSlots[c]) * one;
+            if (plan.us100 < 0 || cost < plan.us100) plan = {n, c, cost};
+        }
+    }
+    return plan;
+}
+
 cudaError_t launch_few(const FewJob& job, cudaStream_t st) {
     if (job.n_tok == 0 || job.n_out == 0) return cudaSuccess;
-    return job.rank > 0 ? launch_few_mode<kLora>(job, st)
-                        : job.w2 ? launch_few_mode<kGated>(job, st) : launch_few_mode<kPlain>(job, st);
+    const FewPlan plan = few_plan(job.n_tok, job.n_out, job.k, job.w2 != nullptr, job.rank);
+    return job.rank > 0 ? launch_few_mode<kLora>(job, plan, st)
+                        : job.w2 ? launch_few_mode<kGated>(job, plan, st) : launch_few_mode<kPlain>(job, plan, st);
 }
 
 }  // namespace gdn

@@ -327,7 +327,20 @@ struct FewJob {
     int32_t n_zero;
 };
 cudaError_t launch_few(const FewJob& job, cudaStream_t st);
+struct FewPlan {
+    int n, ks;      // tokens of a tile, CTAs that share a tile's K
+    int64_t us100;  // what the call should take, in hundredths of a microsecond (< 0: too many tokens)
+};
+FewPlan few_plan(int64_t n_tok, int32_t n_out, int32_t k, bool gated, int32_t rank);
 
+// Tiles of a launch_wide: `whole` in whole waves over the GPU, the `rest` in `split` parts along K, joined through a
+// workspace by whichever part of a tile comes last.
+struct WidePlan {
+    int64_t whole, rest;
+    int32_t split, counters;
+    size_t counter_bytes, ws_bytes;
+    int64_t us100;  // as in FewPlan
+};
 // the same of many tokens; out 16-byte aligned, ld a multiple of 8
 struct WideJob {
     const void *x, *w, *w2;
@@ -338,19 +351,14 @@ struct WideJob {
     const int32_t* tok_adapter;  // [n_tok], -1: none
     const void* b;               // [n_adapters][n_out][rank]
     int32_t rank, n_adapters;
-    void* split_ws;  // wide_plan().ws_bytes, of which the first `counters` int32 are zero
+    WidePlan plan;
+    void* split_ws;  // plan.ws_bytes, of which the first `counters` int32 are zero
     int32_t* zero;   // counters to set to zero, for a launch_wide behind this one
     int32_t n_zero;
 };
 cudaError_t launch_wide(const WideJob& job, cudaStream_t st);
-// Tiles of a launch_wide: `whole` in whole waves over the GPU, the `rest` in `split` parts along K, joined through a
-// workspace by whichever part of a tile comes last.
-struct WidePlan {
-    int64_t whole, rest;
-    int32_t split, counters;
-    size_t counter_bytes, ws_bytes;
-};
-WidePlan wide_plan(int64_t n_tok, int32_t n_out, int32_t k, bool gated);
+// adapters: different ones in a block of 256 tokens, about
+WidePlan wide_plan(int64_t n_tok, int32_t n_out, int32_t k, bool gated, int32_t rank, int64_t adapters);
 
 // Low-rank activations for launch_wide: v = hi + lo in bf16, a row of low_row(rank) elements being [hi | lo] in parts
 // of 16 ceil(rank / 16) (rank <= 32) or 64 ceil(rank / 64) elements, each padded with zeros to a multiple of 16.

@@ -524,7 +524,7 @@ cudaError_t launch_wide_mode(const WideJob& job, cudaStream_t st) {
     P.tok_adapter = job.tok_adapter;
     P.rank = job.rank;
     P.n_adapters = job.n_adapters;
-    const WidePlan plan = wide_plan(job.n_tok, job.n_out, job.k, MODE == kGated);
+    const WidePlan& plan = job.plan;
     constexpr int cols = MODE == kGated ? 128 : 256;
     P.tiles_n = (job.n_out + cols - 1) / cols;
     P.n_whole = plan.whole;
@@ -554,13 +554,15 @@ cudaError_t launch_wide_mode(const WideJob& job, cudaStream_t st) {
 }  // namespace
 
 // Depends on the sizes only, so that a workspace can be sized without a device: 76 pairs, of which a device with others
-// makes the same jobs.  Cycles: a K block takes 700, and no fewer with fewer columns (the tensor cores read the 128 rows of x in
-// the same time for 64 columns as for 256: halves and quarters of tiles in the last wave cost as much as whole ones); a job's
-// start and end take 1500, and parts of a tile, written and read again, 9000 and 2500 each.
-WidePlan wide_plan(int64_t n_tok, int32_t n_out, int32_t k, bool gated) {
-    constexpr int64_t kPairs = 76;
+// makes the same jobs.  Cycles, from measurements of 100 to 1000 tokens: a K block takes 585, and no fewer with fewer columns
+// (the tensor cores read the 128 rows of x in the same time for 64 columns as for 256: halves and quarters of tiles in the
+// last wave cost as much as whole ones); a job's start and end 2100; parts of a tile, written and read again, 4000 and 4200
+// each; an adapter's blocks 128 an MMA and 200 around them; a launch 6 us.
+WidePlan wide_plan(int64_t n_tok, int32_t n_out, int32_t k, bool gated, int32_t rank, int64_t adapters) {
+    constexpr int64_t kPairs = 76, kKBlock = 585, kJob = 2100;
     const int kb = (k + kWideK - 1) / kWideK, cols = gated ? 128 : 256;
     const int64_t tiles = (n_out + cols - 1) / cols * ((n_tok + kWideTok - 1) / kWideTok);
+    const int64_t extra = rank > 0 ? adapters * ((rank + 15) / 16 * 256 + 200) : 0;
     WidePlan plan;
     plan.whole = tiles / kPairs * kPairs;
     plan.rest = tiles - plan.whole;
@@ -568,7 +570,7 @@ WidePlan wide_plan(int64_t n_tok, int32_t n_out, int32_t k, bool gated) {
     int64_t least = -1;
     for (int c = 1; c <= (gated ? 1 : 8) && c <= std::max(1, kb / 2); ++c) {
         const int64_t waves = (plan.rest * c + kPairs - 1) / kPairs;
-        const int64_t cost = waves * ((kb + c - 1) / c * 700 + 1500) + (c > 1 ? 9000 + 2500 * c : 0);
+        const int64_t cost = waves * ((kb + c - 1) / c * kKBlock + kJob) + (waves > 0 ? extra : 0) + (c > 1 ? 4000 + 4200 * c : 0);
         if (least < 0 || cost < least) {
             least = cost;
             plan.split = c;
@@ -577,6 +579,7 @@ WidePlan wide_plan(int64_t n_tok, int32_t n_out, int32_t k, bool gated) {
     plan.counters = plan.split > 1 ? (int32_t)plan.rest * 8 : 0;
     plan.counter_bytes = ((size_t)plan.counters * 4 + 255) & ~(size_t)255;
     plan.ws_bytes = plan.split > 1 ? plan.counter_bytes + (size_t)plan.rest * plan.split * 2 * kPartFloats * 4 : 0;
+    plan.us100 = 600 + (plan.whole / kPairs * (kb * kKBlock + kJob + extra) + least) / 19;
     return plan;
 }
 
