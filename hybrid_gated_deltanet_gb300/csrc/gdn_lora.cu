@@ -32,7 +32,7 @@ __device__ __forceinline__ int request_of(const int32_t* cu, int n, int t, int l
         lo += __popc(m) * step;
         hi = min(hi, lo + step);
     }
-    return lo >= 0 && cu[lo] >= 0 && cu[lo] <= t && t < cu[lo + 1] ? lo : -1;
+    return lo >= 0 && cu[lo] <= t && t < cu[lo + 1] ? lo : -1;
 }
 
 // v by dot products, for tokens that share their adapter with few others or none, so that there is nothing for a matrix

@@ -627,7 +627,9 @@ gdn_status gdn_rope(const gdn_rope_plan* plan, const int32_t* positions, int64_t
 /* ---- Projections with low-rank adapters, and the gated feed-forward block ---------
  * Beside gdn_proj_gemm, for the other matrices of a hybrid layer and for requests that
  * bring adapters of their own.  All bf16 operands, fp32 accumulation (tcgen05 tensor cores), one
- * rounding (to nearest even) of the result; results do not change from call to call. */
+ * rounding (to nearest even) of the result; results do not change from call to call.
+ * 0 <= n_tok <= 2^22; n_out, hidden and inter up to 2^24.  Outputs may not overlap inputs
+ * except where a call says so. */
 
 /* Low-rank adapters of one projection (device pointers). */
 typedef struct gdn_lora {
@@ -641,14 +643,15 @@ typedef struct gdn_lora {
 /* gdn_proj_gemm with each request's adapter beside the shared weights:
  *   out[t][n] = sum_k act[t][k] w[n][k] + scale[e] sum_r b[e][n][r] (sum_k a[e][r][k] act[t][k])
  * for the tokens t = cu_rows[s] .. cu_rows[s+1] - 1 of request s, e = adapter_idx[s].
- *   cu_rows int32 [n_seg+1] (non-decreasing), adapter_idx int32 [n_seg] (device; checked there,
- *   never trusted for an address): a request whose adapter_idx is outside [0, n_adapters) (-1 by convention), and tokens
+ *   cu_rows int32 [n_seg+1] (non-decreasing; rows outside [0, n_tok) are passed over),
+ *   adapter_idx int32 [n_seg] (device; checked there, never trusted for an address): a request whose adapter_idx is outside [0, n_adapters) (-1 by convention), and tokens
  *   outside every request, get the shared projection alone.  Requests may share an adapter.  A token meets
  *   its own request's adapter only: NaN or infinities in another one, or in another token,
  *   do not reach it.
  *   act, w, n_tok, n_out, k as in gdn_proj_gemm; out bf16 rows ld_out >= n_out apart, 16-byte
  *   aligned, ld_out a multiple of 8; 0 <= n_seg <= 2^20; a and b 16-byte aligned, scale 4.
- *   The low-rank activations scale (a act) are carried to 2^-16 of their value or better.
+ *   The low-rank activations scale (a act) are carried to 2^-16 of their value or better
+ *   (fp32, or the sum of two bf16 numbers).
  *   workspace: gdn_proj_lora_workspace_size bytes, 16-byte aligned; calls that may overlap need one each. */
 gdn_status gdn_proj_lora(const void* act, const void* w, const gdn_lora* lora, const int32_t* cu_rows,
                          const int32_t* adapter_idx, int32_t n_seg, void* out, int64_t n_tok, int32_t n_out,
@@ -659,7 +662,8 @@ gdn_status gdn_proj_lora(const void* act, const void* w, const gdn_lora* lora, c
 size_t gdn_proj_lora_workspace_size(int64_t n_tok, int32_t n_out, int32_t k, int32_t rank, int32_t n_seg);
 
 /* The gated half of a feed-forward block: both projections, the activation and the product
- * in one kernel, out[t][n] = silu(act[t] . w_gate[n]) * (act[t] . w_up[n]).
+ * in one kernel, out[t][n] = silu(act[t] . w_gate[n]) * (act[t] . w_up[n]), silu to 2^-20
+ * of its value (below -87.3: 0).
  *   act bf16 [n_tok][k], w_gate and w_up bf16 [n_out][k] (dense, 16-byte aligned; the two may be
  *   halves of one matrix), k a positive multiple of 8, out as in gdn_proj_lora. */
 gdn_status gdn_proj_gated(const void* act, const void* w_gate, const void* w_up, void* out, int64_t n_tok,
@@ -674,14 +678,15 @@ typedef struct gdn_ffn_weights {
 } gdn_ffn_weights;
 
 /* The whole block: out = (silu(h w_gate^T) * (h w_up^T)) w_down^T.
- *   h, out bf16 [n_tok][hidden], dense, 16-byte aligned (out may not overlap h).  The gated
- *   half is rounded to bf16 between the two kernels, as gdn_proj_gated would.
- *   workspace: gdn_ffn_workspace_size bytes, 16-byte aligned (that half of the tokens); calls that may
- *   overlap need one each. */
+ *   h, out bf16 [n_tok][hidden], dense, 16-byte aligned; out may be h.  The gated half is
+ *   rounded to bf16 between the two kernels, as gdn_proj_gated would.
+ *   workspace: gdn_ffn_workspace_size bytes, 16-byte aligned (the gated half of the tokens,
+ *   and fp32 parts of result tiles that are split along K); calls that may overlap need one each. */
 gdn_status gdn_ffn(const gdn_ffn_weights* ffn, const void* h, int64_t n_tok, void* out, void* workspace,
                    size_t ws_bytes, void* stream);
 
-/* Workspace bytes of gdn_ffn (0 on invalid arguments, with gdn_last_error set, or no tokens). */
+/* Workspace bytes of gdn_ffn (depends on the sizes only; 0 for no tokens, and on invalid
+ * arguments, with gdn_last_error set). */
 size_t gdn_ffn_workspace_size(int64_t n_tok, int32_t hidden, int32_t inter);
 
 /* Message of the last failed call on this host thread ("" if none).  The

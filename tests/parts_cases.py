@@ -71,9 +71,10 @@ def lora(x, w, a, b, scale, cu, which):
     activations to 2^-16."""
     y, d = product(x, w)
     for s, e in enumerate(which):
-        if not 0 <= e < a.shape[0] or cu[s] >= cu[s + 1]:
+        first, last = max(cu[s], 0), min(cu[s + 1], x.shape[0])
+        if not 0 <= e < a.shape[0] or first >= last:
             continue
-        rows = slice(cu[s], cu[s + 1])
+        rows = slice(first, last)
         v, dv = product(x[rows], a[e])
         v, dv = v * scale[e], dv * abs(scale[e]) + 2.0 ** -16 * (v * scale[e]).abs()
         y[rows] += v @ b[e].T

@@ -19,7 +19,8 @@ def _weights(gen, n, k):
 
 @pytest.mark.parametrize("n,n_out,k", [(1, 1, 8), (1, 65, 72), (2, 64, 64), (16, 200, 136), (17, 63, 520), (33, 640, 256),
                                        (64, 1000, 264), (65, 129, 72), (128, 72, 2560), (129, 136, 64), (257, 385, 136),
-                                       (300, 128, 1024), (520, 260, 72), (1000, 1100, 192), (2049, 96, 64)])
+                                       (300, 128, 1024), (520, 260, 72), (1000, 1100, 192), (2049, 96, 64), (40001, 136, 136),
+                                       (2000, 3001, 264), (30000, 385, 72)])
 def test_gated_shapes(n, n_out, k):
     gen = torch.Generator().manual_seed(n + n_out + k)
     x, g, u = bf16(gen, n, k), _weights(gen, n_out, k), _weights(gen, n_out, k)
@@ -39,7 +40,7 @@ def test_gated_halves_of_one_matrix_and_large_gates():
     gen = torch.Generator().manual_seed(1)
     n, m, k = 40, 96, 64
     x, w = bf16(gen, n, k, std=30.0), bf16(gen, 2 * m, k)
-    for rows in (n, 700):
+    for rows in (n, 700, 50000):
         xs = x.repeat((rows + n - 1) // n, 1)[:rows]
         out = torch.empty((rows, m), dtype=BF, device="cuda")
         wd = w.cuda()
@@ -48,7 +49,7 @@ def test_gated_halves_of_one_matrix_and_large_gates():
         check(out, *gated(xs.double(), w[:m].double(), w[m:].double()))
 
 
-@pytest.mark.parametrize("n", [3, 100, 600])
+@pytest.mark.parametrize("n", [3, 100, 600, 40000])
 def test_gated_not_numbers_stay_in_their_row_and_column(n):
     gen = torch.Generator().manual_seed(2)
     k, m = 136, 200
@@ -66,7 +67,7 @@ def test_gated_not_numbers_stay_in_their_row_and_column(n):
 @pytest.mark.parametrize("n,hidden,inter", [(1, 8, 8), (1, 2560, 1000), (5, 136, 1096), (64, 256, 640), (70, 72, 8),
                                             (129, 264, 520), (300, 128, 384), (1025, 320, 200),
                                             # few tiles of a long K, and a few behind whole waves of them: split along K
-                                            (300, 264, 2600), (513, 520, 4104), (20000, 264, 2560)])
+                                            (300, 264, 2600), (513, 520, 4104), (2000, 520, 16392), (20000, 264, 2560)])
 def test_ffn_shapes(n, hidden, inter):
     gen = torch.Generator().manual_seed(n + hidden + inter)
     h, g, u, d = bf16(gen, n, hidden), _weights(gen, inter, hidden), _weights(gen, inter, hidden), _weights(gen, hidden, inter)
@@ -88,12 +89,11 @@ def test_ffn_shapes(n, hidden, inter):
     assert gb.gdn_device_status() == 0
 
 
-@pytest.mark.parametrize("n,inter", [(2, 712), (200, 712), (700, 712), (300, 4096)])
-def test_ffn_captured_replayed_and_beside_another(n, inter):
+@pytest.mark.parametrize("n,hidden,inter", [(2, 256, 712), (200, 256, 712), (700, 256, 712), (300, 256, 4096), (2000, 520, 16392)])
+def test_ffn_captured_replayed_and_beside_another(n, hidden, inter):
     """Two blocks in a row in one graph, replayed with new inputs, while another stream runs the same block with a workspace of
     its own: the results of plain calls."""
     gen = torch.Generator().manual_seed(4)
-    hidden = 256
     ffn = gb.Ffn(*(t.cuda() for t in (_weights(gen, inter, hidden), _weights(gen, inter, hidden), _weights(gen, hidden, inter))))
     size = gb.gdn_ffn_workspace_size(n, hidden, inter)
     new = lambda: torch.empty(size, dtype=torch.uint8, device="cuda")  # noqa: E731
@@ -118,6 +118,20 @@ def test_ffn_captured_replayed_and_beside_another(n, inter):
         gb.gdn_ffn(ffn, mid.clone(), want, ws)
         assert torch.equal(got, want)
     assert gb.gdn_device_status() == 0
+
+
+@pytest.mark.parametrize("n", [5, 300, 3000])
+def test_ffn_in_place(n):
+    """The result over the input: the input has been read when the first of it is written."""
+    gen = torch.Generator().manual_seed(6)
+    hidden, inter = 264, 520
+    ffn = gb.Ffn(*(t.cuda() for t in (_weights(gen, inter, hidden), _weights(gen, inter, hidden), _weights(gen, hidden, inter))))
+    ws = torch.empty(gb.gdn_ffn_workspace_size(n, hidden, inter), dtype=torch.uint8, device="cuda")
+    h = bf16(gen, n, hidden).cuda()
+    out = torch.empty_like(h)
+    gb.gdn_ffn(ffn, h, out, ws)
+    gb.gdn_ffn(ffn, h, h, ws)
+    assert torch.equal(h, out)
 
 
 def test_no_tokens():

@@ -49,6 +49,8 @@ MIXES = {
     "mixed": ([1, 1, 700, 1, 1, 1, 90, 1], [0, 1, 2, 3, 2, 1, 0, 3]),
     "empty requests, none served": ([0, 5, 0, 0, 33, 0], [0, -1, 1, 2, -1, 3]),
     "some without an adapter": ([5, 60, 1, 400, 2], [-1, 3, 99, -5, 0]),
+    "long prompts": ([1, 2000, 17, 3, 4200, 1, 15, 16, 900], [1, 0, 2, 3, -1, 0, 1, 2, 3]),
+    "long prompts, none served": ([3000, 6000], [-1, 4]),
 }
 
 
@@ -63,7 +65,7 @@ def test_lora_mixes(mix, rank, k, n_out):
 
 
 @pytest.mark.parametrize("rank", [8, 16, 24, 32, 40, 48, 64, 72, 96, 128])
-@pytest.mark.parametrize("lens", [[1] * 9, [2, 200, 100, 1]])
+@pytest.mark.parametrize("lens", [[1] * 9, [2, 200, 100, 1], [2, 4000, 100, 1, 3000]])
 def test_lora_ranks(rank, lens):
     """Every rank in steps of 8, adapters whose part is larger than the shared product, and no scale."""
     c = Case(rank, lens, [i % 3 for i in range(len(lens))], 256, 320, rank, 3, scaled=False, delta=20.0)
@@ -89,10 +91,11 @@ def test_lora_decoding_sizes(n, n_out, k):
     c.check(c.run())
 
 
-@pytest.mark.parametrize("lens", [[1, 2, 1, 3], [1, 150, 1, 400, 2]])
-def test_lora_not_numbers_stay_with_their_request(lens):
+@pytest.mark.parametrize("rank", [16, 72])
+@pytest.mark.parametrize("lens", [[1, 2, 1, 3, 1], [1, 150, 1, 400, 2], [1, 3000, 1, 4500, 498]])
+def test_lora_not_numbers_stay_with_their_request(lens, rank):
     """NaN and infinities in one adapter reach that adapter's requests only; in a token, that token only."""
-    c = Case(11, lens, [0, 1, 2, 1], 136, 200, 16, 4) if len(lens) == 4 else Case(11, lens, [0, 1, 2, 3, 1], 136, 200, 16, 4)
+    c = Case(11, lens, [0, 1, 2, 3, 1], 136, 200, rank, 4)
     clean = c.run()[:, :200]
     c.check(clean)
     c.a[1, 3, 5], c.b[1, 7, 2], c.b[1, 8, 0] = float("nan"), float("inf"), float("nan")
@@ -110,7 +113,7 @@ def test_lora_not_numbers_stay_with_their_request(lens):
 
 
 def test_lora_tokens_outside_every_request():
-    for n, cu in ((30, [4, 4, 9, 21]), (900, [100, 130, 700, 890])):
+    for n, cu in ((30, [4, 4, 9, 21]), (900, [100, 130, 700, 890]), (9000, [100, 107, 7000, 8890]), (9000, [-5, 3000, 3001, 9100])):
         c = Case(12, [n], [0], 136, 96, 24, 4)
         c.cu, c.which = cu, [1, 3, 2]
         out = c.run()
@@ -122,23 +125,23 @@ def test_lora_tokens_outside_every_request():
 
 
 def test_lora_without_requests():
-    for n in (3, 700):
+    for n in (3, 700, 20000):
         c = Case(13, [n], [0], 64, 72, 8, 1)
         c.cu, c.which = [0], []
         c.check(c.run())
 
 
 def test_lora_request_rows_that_are_not_in_order():
-    """cu_rows that are not what they should be address nothing outside: tokens that no reading of them reaches are right."""
-    for n in (40, 800):
+    """cu_rows that are not what they should be address nothing outside, and no wait runs out."""
+    for n in (40, 800, 20000):
         c = Case(14, [n], [0], 64, 72, 16, 2)
         c.cu, c.which = [-7, -3, 2 ** 31 - 1, -2 ** 31, 5, 9], [0, 1, 0, 7, 1]
-        out = c.run()
-        assert torch.isfinite(out[:, :72]).all()
+        c.run()
+        torch.cuda.synchronize()
     assert gb.gdn_device_status() == 0
 
 
-@pytest.mark.parametrize("lens", [[1] * 10, [1, 300, 30, 1, 257]])
+@pytest.mark.parametrize("lens", [[1] * 10, [1, 300, 30, 1, 257], [1, 6000, 30, 1, 2570]])
 def test_lora_out_rows_and_workspace_end(lens):
     """Nothing past the columns, the rows or the workspace's stated size is written."""
     c = Case(15, lens, [i % 3 for i in range(len(lens))], 72, 100, 16, 3)
@@ -150,7 +153,7 @@ def test_lora_out_rows_and_workspace_end(lens):
     assert (out[:c.n, 100:] == 7).all() and (out[c.n:] == 7).all() and (ws[size:] == 9).all()
 
 
-@pytest.mark.parametrize("lens,k", [([1] * 12, 264), ([1, 400, 1, 60], 264), ([1, 400, 1, 60], 4096)])
+@pytest.mark.parametrize("lens,k", [([1] * 12, 264), ([1, 400, 1, 60], 264), ([1, 6400, 1, 60], 264), ([1, 6400, 1, 60], 4096)])
 def test_lora_captured_replayed_and_beside_another(lens, k):
     c = Case(16, lens, [i % 3 for i in range(len(lens))], k, 392, 32, 3)
     x, w, ad = c.x.cuda(), c.w.cuda(), gb.Lora(c.a.cuda(), c.b.cuda(), c.scale.cuda())
