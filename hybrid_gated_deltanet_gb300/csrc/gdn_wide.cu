@@ -190,8 +190,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
            const __grid_constant__ CUtensorMap tw2, const __grid_constant__ CUtensorMap tout,
            const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tb, const __grid_constant__ WideArgs P) {
     const int S = wide_stages(MODE == kLora, P.rank);
-    griddep_wait();  // launched with programmatic serialization: nothing is held while kernels ahead still run
-    if (blockIdx.x == 0)
+    // lora: behind the kernel that makes v, which lets this one start only after its own wait and with its TMEM in hand: x and
+    // the weights are there, only v, the adapters and the counters have to be waited for.  Else nothing is held or asked for
+    // while kernels ahead still run.
+    constexpr bool kEarly = MODE == kLora;
+    if (!kEarly) griddep_wait();
+    if (!kEarly && blockIdx.x == 0)
         for (int i = threadIdx.x; i < P.n_zero; i += kWideThreads) P.zero[i] = 0;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = smem_raw + ((1024 - (tc::smem_addr(smem_raw) & 1023)) & 1023);
@@ -225,7 +229,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     cluster_arrive_release();  // the other CTA's barriers and TMEM are ready
     cluster_wait_acquire();
     tc::fence_after();
-    griddep_launch_dependents();
+    if (!kEarly) griddep_launch_dependents();
     const uint32_t tm = *tslot;
     bool ok = true;
 
@@ -254,7 +258,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
             const int row = T.tt * kWideTok + 128 * cta, wrow = MODE == kGated ? T.wn * 128 : T.wn * 256 + 128 * cta;
             const void* wmap = MODE == kGated && cta == 1 ? &tw2 : &tw;
             TileAdapters ta;
-            if (MODE == kLora) ta.load(P, T.tt, lane);
+            if (MODE == kLora && tile != tile0) ta.load(P, T.tt, lane);
             for (int kb = T.kb0; kb < T.kb1 && ok; ++kb, next_stage()) {
                 turn(2 * kHalfBytes);
                 if (ok && lane == 0) {
@@ -263,6 +267,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                     tma2_2d(st, &tx, kb * kWideK, row, bar);
                     tma2_2d(st + kHalfBytes, wmap, kb * kWideK, wrow, bar);
                 }
+            }
+            if (MODE == kLora && tile == tile0) {
+                griddep_wait();
+                ta.load(P, T.tt, lane);
             }
             if (MODE == kLora && ok && T.last) {
                 int a = ta.next();
@@ -302,7 +310,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                 const Tile T = wide_tile(P, tile);
                 constexpr uint32_t idesc = idesc_bf16(256, 256);
                 TileAdapters ta;
-                if (MODE == kLora) ta.load(P, T.tt, lane);
+                if (MODE == kLora && tile != tile0) ta.load(P, T.tt, lane);
                 ok = __all_sync(0xffffffffu, mbar_wait(acc_empty + buf, ((use >> 1) & 1u) ^ 1u));
                 if (!ok) break;
                 tc::fence_after();
@@ -320,6 +328,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
                         commit2(empty + st_i);
                     }
                     __syncwarp();
+                }
+                if (MODE == kLora && tile == tile0) {
+                    griddep_wait();
+                    ta.load(P, T.tt, lane);
                 }
                 if (!ok) break;
                 int a = MODE == kLora && T.last ? ta.next() : kNoMore;
@@ -365,6 +377,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
             }
         }
     } else {
+        if (kEarly) {
+            griddep_wait();
+            griddep_launch_dependents();
+        }
         const int q4 = warp & 3;  // TMEM lanes 32 q4 .. are this warp's
         unsigned char* store = sm + kStoreOff + q4 * 2 * kStoreBytes;
         const uint32_t empty_bar[2] = {mapa_shared(smem_u32(acc_empty), 0), mapa_shared(smem_u32(acc_empty + 1), 0)};
