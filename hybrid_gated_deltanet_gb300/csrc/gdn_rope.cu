@@ -94,13 +94,14 @@ __global__ void __launch_bounds__(kRopeThreads, 2) k_rope(const __grid_constant_
     const int e0 = turn ? (J.half ? 8 * u : 16 * u) : J.rot + 16 * (u - pairs);
     const int e1 = e0 + (turn && J.half ? half_rot : 8);
     const bool two = e1 < J.D;  // (a head's rest may end on a single run)
+    auto in_place = [&](int h) { return h < J.hq ? J.q == J.q_out : J.k == J.k_out; };
     float c[8], s[8];
     for (int hb = h0;; hb += kRopeHeads * J.step_h) {
         Eight<T> x[kRopeHeads], y[kRopeHeads];
 #pragma unroll
         for (int e = 0; e < kRopeHeads; ++e) {
             const int h = hb + e * J.step_h;
-            if (!mine || h >= heads) continue;
+            if (!mine || h >= heads || (!turn && in_place(h))) continue;
             const T* src = h < J.hq ? static_cast<const T*>(J.q) + tok * J.ldq + (int64_t)h * J.D
                                     : static_cast<const T*>(J.k) + tok * J.ldk + (int64_t)(h - J.hq) * J.D;
             x[e].ld(src + e0);
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) k_rope(const __grid_constant_
 #pragma unroll
         for (int e = 0; e < kRopeHeads; ++e) {
             const int h = hb + e * J.step_h;
-            if (h >= heads) continue;
+            if (h >= heads || (!turn && in_place(h))) continue;
             T* dst = h < J.hq ? static_cast<T*>(J.q_out) + tok * J.ldqo + (int64_t)h * J.D
                               : static_cast<T*>(J.k_out) + tok * J.ldko + (int64_t)(h - J.hq) * J.D;
             if (turn) {

@@ -3,6 +3,9 @@ request's adapter, rotary positions on its rows, attention over the paged cache,
 feed-forward block -- for the prompts, then for a decoding step on what they left.  Against 64 bits, with every tensor
 that passes between two calls rounded to bf16 there as well."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -93,3 +96,35 @@ def test_prompts_then_a_decoding_step():
     for got, ref in ((out, want), (one, want1)):
         assert torch.isfinite(got).all()
         assert float((got.cpu().double() - ref).norm() / ref.norm()) <= 1e-2
+
+
+def test_first_calls_under_capture():
+    """Each call's first use in a process may be inside a stream capture, whichever kernel the sizes choose."""
+    code = """
+import torch
+from hybrid_gated_deltanet_gb300 import binding as gb
+bf, dev = torch.bfloat16, "cuda"
+t = lambda *s: torch.ones(s, dtype=bf, device=dev)
+i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)
+plan = gb.gdn_rope_plan(gb.RopeConfig(64, 32))
+rows, pos, w, a, b = t(3, 2, 64), i32([1, 2, 3]), t(256, 64), t(2, 16, 64), t(2, 256, 16)
+cases = []
+for n in (3, 40000):
+    ws = torch.empty(max(gb.gdn_proj_lora_workspace_size(n, 256, 64, 16, 1), gb.gdn_ffn_workspace_size(n, 64, 256)), dtype=torch.uint8, device=dev)
+    cases.append((t(n, 64), t(n, 256), t(n, 64), i32([0, n]), ws))
+one = i32([1])
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    gb.gdn_rope(plan, pos, rows, None)
+    for x, wide, out, cu, ws in cases:
+        gb.gdn_proj_lora(x, w, gb.Lora(a, b), cu, one, wide, ws)
+        gb.gdn_ffn(gb.Ffn(w, w, w.view(64, 256)), x, out, ws)
+graph.replay()
+torch.cuda.synchronize()
+for x, wide, out, cu, ws in cases:
+    assert (wide == 64 + 16 * 64).all(), wide
+assert gb.gdn_device_status() == 0
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=root, timeout=120)

@@ -158,3 +158,16 @@ def test_rope_empty_captured_and_on_another_stream():
     torch.cuda.synchronize()
     _check(cfg, x, pos, out, freq)
     _check(cfg, x, pos - 1000, out2, freq)
+
+
+def test_rope_in_place_beside_a_copy():
+    """q where it lies and k copied: of q only the rotated elements are touched."""
+    gen = torch.Generator().manual_seed(10)
+    cfg = gb.RopeConfig(128, 32, 1e4)
+    q, k = (_rows(gen, 20, h, 128, torch.bfloat16).cuda() for h in (3, 2))
+    was, pos, k_out = q.clone(), torch.arange(20, dtype=torch.int32, device="cuda"), torch.zeros_like(k)
+    gb.gdn_rope(gb.gdn_rope_plan(cfg), pos, q, k, None, k_out)
+    freq = frequencies(32, 1e4)
+    _check(cfg, was, pos, q, freq)
+    _check(cfg, k, pos, k_out, freq)
+    assert torch.equal(q[..., 32:], was[..., 32:]) and torch.equal(k_out[..., 32:], k[..., 32:])
