@@ -195,7 +195,9 @@ void rope_turns(int rot, double theta, double factor, int orig_len, double beta_
         } else {
             f /= factor;
         }
-        turns[i] = (uint64_t)std::llround(f / two_pi * 0x1p62) << 2;  // (f <= 1: below a sixth of a turn)
+        // whole turns per position (of a factor far below 1) are none
+        const double t = f / two_pi;
+        turns[i] = (uint64_t)std::llround((t - std::floor(t)) * 0x1p62) << 2;
     }
 }
 

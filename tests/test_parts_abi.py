@@ -40,6 +40,17 @@ def test_plan_frequencies(lib, kw):
     assert abs(gb.gdn_rope_plan(gb.RopeConfig(128, 96, mscale=0.25, **kw)).mscale - 0.25) == 0
 
 
+@pytest.mark.parametrize("kw", [dict(theta=1e4, factor=1e-6), dict(theta=1e4, factor=0.07), dict(theta=1e4, factor=0.15),
+                                dict(theta=5e5, factor=1e-3, orig_len=64)])
+def test_plan_frequencies_above_a_turn(lib, kw):
+    """A factor far below 1 gives frequencies of whole turns and more per position, of which only the rest counts."""
+    plan = gb.gdn_rope_plan(gb.RopeConfig(64, 64, **kw))
+    for i, f in enumerate(frequencies(64, **{**kw, "factor": float(torch.tensor(kw["factor"], dtype=torch.float32))})):
+        turns = float(f) / (2 * math.pi)
+        off = (plan.turns[i] / 2.0 ** 64 - turns) % 1.0
+        assert min(off, 1 - off) <= 2.0 ** -50 * turns + 2.0 ** -52
+
+
 @pytest.mark.parametrize("kw,status,needle", [
     (dict(head_dim=12), -2, "cfg.head_dim: found 12"), (dict(head_dim=264), -2, "cfg.head_dim: found 264"),
     (dict(rotary_dim=24), -2, "cfg.rotary_dim: found 24"), (dict(rotary_dim=0), -2, "cfg.rotary_dim: found 0"),
