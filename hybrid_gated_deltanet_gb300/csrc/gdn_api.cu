@@ -1037,7 +1037,8 @@ static gdn_status proj_sizes(int64_t n_tok, int32_t n_out, int32_t k, int64_t ld
     if (n_tok < 0 || n_tok > ((int64_t)1 << 22))
         return fail(GDN_ERR_RANGE, "n_tok: found %lld, required 0..2^22", (long long)n_tok);
     if (n_out < 1 || n_out > 1 << 24) return fail(GDN_ERR_SHAPE, "n_out: found %d, required 1..2^24", n_out);
-    if (k < 8 || k % 8 != 0) return fail(GDN_ERR_SHAPE, "k: found %d, required a positive multiple of 8", k);
+    if (k < 8 || k % 8 != 0 || k > 1 << 24)
+        return fail(GDN_ERR_SHAPE, "k: found %d, required a positive multiple of 8, at most 2^24", k);
     if (ld_out < n_out || ld_out % 8 != 0 || ld_out > ((int64_t)1 << 31))
         return fail(GDN_ERR_SHAPE, "ld_out: found %lld, required a multiple of 8, >= n_out = %d and at most 2^31",
                     (long long)ld_out, n_out);

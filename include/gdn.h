@@ -628,7 +628,7 @@ gdn_status gdn_rope(const gdn_rope_plan* plan, const int32_t* positions, int64_t
  * Beside gdn_proj_gemm, for the other matrices of a hybrid layer and for requests that
  * bring adapters of their own.  All bf16 operands, fp32 accumulation (tcgen05 tensor cores), one
  * rounding (to nearest even) of the result; results do not change from call to call.
- * 0 <= n_tok <= 2^22; n_out, hidden and inter up to 2^24.  Outputs may not overlap inputs
+ * 0 <= n_tok <= 2^22; n_out, k, hidden and inter up to 2^24.  Outputs may not overlap inputs
  * except where a call says so. */
 
 /* Low-rank adapters of one projection (device pointers). */

@@ -113,6 +113,9 @@ def test_gated_refusals(lib):
     _refused(lib, -2, _gated(lib, n_out=0), "n_out: found 0")
     _refused(lib, -2, _gated(lib, k=12), "k: found 12")
     _refused(lib, -2, _gated(lib, k=0), "k: found 0")
+    for k in (2 ** 24 + 8, 2 ** 31 - 8):  # (beyond what a plan's costs are counted in)
+        _refused(lib, -2, _gated(lib, k=k), f"k: found {k}")
+        assert lib.gdn_proj_lora_workspace_size(5, 64, k, 16, 1) == 0
     _refused(lib, -2, _gated(lib, ld=56), "ld_out: found 56")
     _refused(lib, -2, _gated(lib, ld=68), "ld_out: found 68")
     for name, needle in (("x", "act"), ("g", "w_gate"), ("u", "w_up"), ("out", "out")):
