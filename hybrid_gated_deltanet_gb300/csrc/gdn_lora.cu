@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kLowTcThreads, 2)
             const float scale = J.scale ? J.scale[e] : 1.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                v[j] *= scale;
+                v[j] = c0 < J.rank ? v[j] * scale : 0.f;  // (beyond the rank 0 x, which is no 0 for an infinite x)
                 const float h = __bfloat162float(__float2bfloat16_rn(v[j]));
                 l[j] = isfinite(h) ? v[j] - h : 0.f;
             }

@@ -202,3 +202,18 @@ def test_lora_pool_past_2_to_the_32_bytes():
         ws = torch.empty(gb.gdn_proj_lora_workspace_size(n, n_out, k, rank, 3), dtype=torch.uint8, device="cuda")
         gb.gdn_proj_lora(x.cuda(), w.cuda(), gb.Lora(a, b), i32(cu), i32(used), out, ws)
         check(out, *lora(x.double(), w.double(), au.double(), bu.double(), [1.0] * 3, cu, [0, 1, 2]))
+
+
+@pytest.mark.parametrize("rank", [8, 16, 40])
+@pytest.mark.parametrize("lens", [[1] * 6, [3] * 40, [1500, 7, 9000]])
+def test_lora_infinite_activations(lens, rank):
+    """An infinite element of a token, positive weights: infinity, with ranks that fill their tiles and with others."""
+    c = Case(rank, lens, [i % 2 for i in range(len(lens))], 136, 520, rank, 2)
+    c.x, c.w, c.a, c.b = c.x.abs(), c.w.abs() + 0.01, c.a.abs() + 0.01, c.b.abs() + 0.01
+    clean = c.run()
+    c.x[c.n // 2, 7] = float("inf")
+    out = c.run()
+    assert torch.isposinf(out[c.n // 2]).all()
+    rest = torch.arange(c.n) != c.n // 2
+    assert torch.equal(out[rest.cuda()], clean[rest.cuda()])
+    assert gb.gdn_device_status() == 0
