@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kLowTcThreads, 2)
                 __syncwarp();
             }
         }
-        if (ok && lane == 0) tc::commit(done);
+        if (ok && lane == 0 && first != 0x7fffffff) tc::commit(done);  // (nobody would wait for it)
         __syncwarp();
     } else if (first != 0x7fffffff) {
         const int q4 = warp & 3;
