@@ -5,9 +5,11 @@
 // with f_i from gdn_rope_plan_init (theta^(-2i/rot), slowed down for contexts longer than the trained one).
 //
 // Angles.  f_i is kept as turns per position in units of 2^-64: p f_i modulo whole turns is then the low 64 bits of
-// an integer product, exact however far the position (a float's p f_i is off by a radian at p = 10^7), and its
-// upper 32 bits as a signed number are the angle in (-1/2, 1/2] turns for sincospif.  The frequency itself has the 53
-// bits of a double: 2^-54 p of a turn, 2^-34 at a position of 2^20.
+// an integer product, exact however far the position (a float's p f_i is off by a radian at p = 10^7).  Its upper 32
+// bits are the angle; the nearest quarter turn is taken off them as an integer too, because a float has 24 bits: half a
+// turn less 2^-20 would be off by 2^-26 of a turn, 2^-6 of its sine.  What is left, an eighth of a turn at most, is a
+// float to 2^-24 of itself.  The frequency has the 53 bits of a double: with the roundings on the way to it below 2^-52 p
+// of a turn, over the factor where that is below 1.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -68,6 +70,16 @@ struct Eight<float> {
     }
 };
 
+// sine and cosine of p turns / 2^64 of a turn
+__device__ __forceinline__ void sine_cosine(unsigned long long p, unsigned long long turns, float* sn, float* cs) {
+    const unsigned a = (unsigned)((p * turns) >> 32), quarter = (a + 0x20000000u) >> 30;
+    float s, c;
+    sincospif((float)(int)(a - (quarter << 30)) * 0x1p-31f, &s, &c);
+    const float s1 = quarter & 1u ? c : s, c1 = quarter & 1u ? s : c;
+    *sn = quarter & 2u ? -s1 : s1;
+    *cs = (quarter + 1u) & 2u ? -c1 : c1;
+}
+
 // A thread owns one piece of 16 elements of a token's heads: 8 pairs of the rotated part (two runs of 8 elements, rot / 2
 // apart or side by side), or 16 elements of the rest, which are only copied and only where the result goes elsewhere.  It
 // walks over every step_h-th head, kRopeHeads of them in flight; pieces are fastest among the threads, then heads, so that a
@@ -113,7 +125,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) k_rope(const __grid_constant_
             if (turn)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    sincospif((float)(int)(unsigned)((p * J.turns[8 * u + j]) >> 32) * 0x1p-31f, &s[j], &c[j]);
+                    sine_cosine(p, J.turns[8 * u + j], &s[j], &c[j]);
                     c[j] *= J.mscale;
                     s[j] *= J.mscale;
                 }
@@ -123,7 +135,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) k_rope(const __grid_constant_
                 const unsigned t = j / (unsigned)half_rot;
                 const unsigned long long p = (unsigned long long)(long long)J.positions[tok0 + t];
                 float sn, cs;
-                sincospif((float)(int)(unsigned)((p * J.turns[j - t * half_rot]) >> 32) * 0x1p-31f, &sn, &cs);
+                sine_cosine(p, J.turns[j - t * half_rot], &sn, &cs);
                 angle[j] = make_float2(cs * J.mscale, sn * J.mscale);
             }
             __syncthreads();

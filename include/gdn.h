@@ -592,7 +592,7 @@ typedef struct gdn_rope_config {
     int32_t layout;     /* GDN_ROPE_* */
     int32_t act_dtype;  /* GDN_DTYPE_* of q and k */
     float theta;        /* > 1 */
-    float factor;       /* > 0; 1: as trained */
+    float factor;       /* >= 1e-6; 1: as trained */
     int32_t orig_len;   /* >= 0 */
     float beta_fast, beta_slow; /* > 0 where orig_len > 0 (32 and 1 are usual) */
     float mscale;       /* >= 0 */
@@ -618,8 +618,9 @@ gdn_status gdn_rope_plan_init(const gdn_rope_config* cfg, gdn_rope_plan* plan);
  *   and only the rotated elements are read and written.  Else the rest of each head is
  *   copied.  Outputs that overlap inputs in any other way, or each other, are undefined.
  *   Pointers 16-byte aligned, ld_* * element size a multiple of 16.
- *   Precision: angles are exact modulo a turn to 2^-32 of it up to positions of 2^20 (2^-22
- *   at 2^31), fp32 sine, cosine and products, one rounding to the activation dtype. */
+ *   Precision: an angle is off by at most 2^-32 of a turn and by |p| 2^-52 / min(factor, 1) of a turn for
+ *   the roundings of its frequency (2^-32 at positions of 2^20, 2^-21 at 2^31); then fp32 sine, cosine
+ *   and products, one rounding to the activation dtype. */
 gdn_status gdn_rope(const gdn_rope_plan* plan, const int32_t* positions, int64_t n_tok, const void* q,
                     int64_t ld_q, int32_t n_q_heads, void* q_out, int64_t ld_q_out, const void* k,
                     int64_t ld_k, int32_t n_kv_heads, void* k_out, int64_t ld_k_out, void* stream);
