@@ -1045,6 +1045,10 @@ static gdn_status proj_sizes(int64_t n_tok, int32_t n_out, int32_t k, int64_t ld
     return GDN_OK;
 }
 
+constexpr int64_t kFewAlways = 64;  // tokens up to which the kernel of few tokens takes a call
+
+static size_t align_parts(size_t bytes) { return (bytes + 255) & ~(size_t)255; }
+
 // The weights stream past a few tokens, or tiles of 256 tokens go to pairs of SMs: whichever should take less.
 struct Fused {
     const void *x, *w, *w2;
@@ -1063,7 +1067,7 @@ struct FusedPlan {
 static FusedPlan fused_plan(int64_t n_tok, int32_t n_out, int32_t k, bool gated) {
     const gdn::FewPlan few = gdn::few_plan(n_tok, n_out, k, gated, 0);
     const gdn::WidePlan wide = gdn::wide_plan(n_tok, n_out, k, gated, 0, 0);
-    return {few.us100 < 0 || (n_tok > 64 && wide.us100 < few.us100), wide};
+    return {few.us100 < 0 || (n_tok > kFewAlways && wide.us100 < few.us100), wide};
 }
 static cudaError_t launch_fused(const Fused& f, const FusedPlan& p, cudaStream_t st) {
     if (p.wide) {
@@ -1109,16 +1113,23 @@ struct FfnWs {
     int32_t counters;
 };
 static FfnWs ffn_ws(int64_t n_tok, int32_t hidden, int32_t inter) {
-    const size_t half = (size_t)n_tok * inter * 2, split = (half + 255) & ~(size_t)255;
+    const size_t half = (size_t)n_tok * inter * 2, split = align_parts(half);
     const FusedPlan back = fused_plan(n_tok, hidden, inter, false);
     if (!back.wide || back.plan.ws_bytes == 0) return {back, 0, half, 0};
     return {back, split, split + back.plan.ws_bytes, back.plan.counters};
 }
 
+// What the parts of split tiles may take in calls of up to n_tok tokens: fewer tokens may leave more tiles over, so that
+// a workspace made for the largest call would else not serve the others.
+static size_t parts_bytes(int64_t n_tok, int32_t n_out, int32_t k) {
+    return n_tok > kFewAlways ? gdn::wide_ws_most(n_tok, n_out, k) : 0;
+}
+
 size_t gdn_ffn_workspace_size(int64_t n_tok, int32_t hidden, int32_t inter) {
     if (ffn_sizes(n_tok, hidden, inter)) return 0;
     ok();
-    return ffn_ws(n_tok, hidden, inter).bytes;
+    const size_t half = (size_t)n_tok * inter * 2, parts = parts_bytes(n_tok, hidden, inter);
+    return parts > 0 ? align_parts(half) + parts : half;
 }
 
 gdn_status gdn_ffn(const gdn_ffn_weights* ffn, const void* h, int64_t n_tok, void* out, void* workspace, size_t ws_bytes,
@@ -1155,13 +1166,13 @@ struct LoraWs {
     int32_t counters;
 };
 static LoraWs lora_ws(int64_t n_tok, int32_t n_out, int32_t k, int32_t rank, int32_t n_seg) {
-    const size_t low = (size_t)n_tok * gdn::low_row(rank) * 2, end = low + (size_t)n_tok * 4, split = (end + 255) & ~(size_t)255;
+    const size_t low = (size_t)n_tok * gdn::low_row(rank) * 2, end = low + (size_t)n_tok * 4, split = align_parts(end);
     // Requests of a few tokens each bring an adapter for (nearly) every token, a matrix product for none: the kernel of few
     // tokens gives each token its adapter on the CUDA cores, the one of many takes each adapter through the tensor cores.
     // What comes before them and is not hidden takes 4 and 9 us.
     const gdn::FewPlan few = gdn::few_plan(n_tok, n_out, k, false, rank);
     const gdn::WidePlan plan = gdn::wide_plan(n_tok, n_out, k, false, rank, n_tok > 0 ? 256 * (int64_t)n_seg / n_tok + 1 : 0);
-    const bool wide = few.us100 < 0 || (n_tok > 64 && plan.us100 + 900 < few.us100 + 400);
+    const bool wide = few.us100 < 0 || (n_tok > kFewAlways && plan.us100 + 900 < few.us100 + 400);
     if (!wide || plan.ws_bytes == 0) return {wide, plan, low, 0, end, 0};
     return {wide, plan, low, split, split + plan.ws_bytes, plan.counters};
 }
@@ -1178,7 +1189,8 @@ static gdn_status lora_sizes(int64_t n_tok, int32_t n_out, int32_t k, int32_t ra
 size_t gdn_proj_lora_workspace_size(int64_t n_tok, int32_t n_out, int32_t k, int32_t rank, int32_t n_seg) {
     if (lora_sizes(n_tok, n_out, k, rank, n_seg)) return 0;
     ok();
-    return lora_ws(n_tok, n_out, k, rank, n_seg).bytes;
+    const size_t low = (size_t)n_tok * (gdn::low_row(rank) * 2 + 4), parts = parts_bytes(n_tok, n_out, k);
+    return parts > 0 ? align_parts(low) + parts : low;
 }
 
 gdn_status gdn_proj_lora(const void* act, const void* w, const gdn_lora* lora, const int32_t* cu_rows,

@@ -359,6 +359,8 @@ struct WideJob {
 cudaError_t launch_wide(const WideJob& job, cudaStream_t st);
 // adapters: different ones in a block of 256 tokens, about
 WidePlan wide_plan(int64_t n_tok, int32_t n_out, int32_t k, bool gated, int32_t rank, int64_t adapters);
+// the most ws_bytes of such plans (not gated) of up to n_tok tokens
+size_t wide_ws_most(int64_t n_tok, int32_t n_out, int32_t k);
 
 // Low-rank activations for launch_wide: v = hi + lo in bf16, a row of low_row(rank) elements being [hi | lo] in parts
 // of 16 ceil(rank / 16) (rank <= 32) or 64 ceil(rank / 64) elements, each padded with zeros to a multiple of 16.

@@ -569,13 +569,15 @@ cudaError_t launch_wide_mode(const WideJob& job, cudaStream_t st) {
 
 }  // namespace
 
+constexpr int64_t kPairs = 76;
+
 // Depends on the sizes only, so that a workspace can be sized without a device: 76 pairs, of which a device with others
 // makes the same jobs.  Cycles, from measurements of 100 to 1000 tokens: a K block takes 585, and no fewer with fewer columns
 // (the tensor cores read the 128 rows of x in the same time for 64 columns as for 256: halves and quarters of tiles in the
 // last wave cost as much as whole ones); a job's start and end 2100; parts of a tile, written and read again, 4000 and 4200
 // each; an adapter's blocks 128 an MMA and 200 around them; a launch 6 us.
 WidePlan wide_plan(int64_t n_tok, int32_t n_out, int32_t k, bool gated, int32_t rank, int64_t adapters) {
-    constexpr int64_t kPairs = 76, kKBlock = 585, kJob = 2100;
+    constexpr int64_t kKBlock = 585, kJob = 2100;
     const int kb = (k + kWideK - 1) / kWideK, cols = gated ? 128 : 256;
     const int64_t tiles = (n_out + cols - 1) / cols * ((n_tok + kWideTok - 1) / kWideTok);
     const int64_t extra = rank > 0 ? adapters * ((rank + 15) / 16 * 256 + 200) : 0;
@@ -597,6 +599,15 @@ WidePlan wide_plan(int64_t n_tok, int32_t n_out, int32_t k, bool gated, int32_t 
     plan.ws_bytes = plan.split > 1 ? plan.counter_bytes + (size_t)plan.rest * plan.split * 2 * kPartFloats * 4 : 0;
     plan.us100 = 600 + (plan.whole / kPairs * (kb * kKBlock + kJob + extra) + least) / 19;
     return plan;
+}
+
+// The tiles that are left over repeat after kPairs more blocks of 256 tokens at the latest, and adapters cost every split the
+// same, so these plans are all there are.
+size_t wide_ws_most(int64_t n_tok, int32_t n_out, int32_t k) {
+    size_t most = 0;
+    for (int64_t t = std::min<int64_t>((n_tok + kWideTok - 1) / kWideTok, kPairs); t > 0; --t)
+        most = std::max(most, wide_plan(t * kWideTok, n_out, k, false, 0, 0).ws_bytes);
+    return most;
 }
 
 cudaError_t take_device_status_wide(unsigned* out) { return take_device_status_tu(out); }

@@ -660,7 +660,8 @@ gdn_status gdn_proj_lora(const void* act, const void* w, const gdn_lora* lora, c
                          int32_t k, int64_t ld_out, void* workspace, size_t ws_bytes, void* stream);
 
 /* Workspace bytes of gdn_proj_lora (depends on the sizes only; 0 on invalid arguments, with
- * gdn_last_error set). */
+ * gdn_last_error set).  They serve every call of the same n_out and k with at most this rank and n_tok,
+ * whatever its n_seg; a call is refused only where its own need is larger than ws_bytes. */
 size_t gdn_proj_lora_workspace_size(int64_t n_tok, int32_t n_out, int32_t k, int32_t rank, int32_t n_seg);
 
 /* The gated half of a feed-forward block: both projections, the activation and the product
@@ -688,7 +689,8 @@ gdn_status gdn_ffn(const gdn_ffn_weights* ffn, const void* h, int64_t n_tok, voi
                    size_t ws_bytes, void* stream);
 
 /* Workspace bytes of gdn_ffn (depends on the sizes only; 0 for no tokens, and on invalid
- * arguments, with gdn_last_error set). */
+ * arguments, with gdn_last_error set).  They serve every call of the same weights with at most n_tok
+ * tokens; a call is refused only where its own need is larger than ws_bytes. */
 size_t gdn_ffn_workspace_size(int64_t n_tok, int32_t hidden, int32_t inter);
 
 /* Message of the last failed call on this host thread ("" if none).  The
