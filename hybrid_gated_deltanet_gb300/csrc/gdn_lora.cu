@@ -147,6 +147,14 @@ __device__ __forceinline__ void tma_tile_3d(void* dst, const void* map, int x, i
         : "memory");
 }
 
+// v = hi + lo in bf16.  What rounds to infinity is cut to the largest bf16 number first, so that lo can make up for it.
+__device__ __forceinline__ void split_bf16(float v, float* hi, float* lo) {
+    const float most = __uint_as_float(0x7f7f0000u);
+    const float h = __bfloat162float(__float2bfloat16_rn(v));
+    *hi = isinf(h) && !isinf(v) ? copysignf(most, v) : h;
+    *lo = isfinite(*hi) ? v - *hi : 0.f;
+}
+
 // short requests, and every token's adapter; the first and the last request's CTAs also mark what lies outside
 __device__ __forceinline__ void short_request(const LowJob& J, int s, int y) {
     const int warp = threadIdx.x >> 5, n_tok = (int)J.n_tok;
@@ -173,10 +181,10 @@ __device__ __forceinline__ void short_request(const LowJob& J, int s, int y) {
     for (int t = first; t < last; ++t) {
         __nv_bfloat16* v = static_cast<__nv_bfloat16*>(J.v) + (int64_t)t * row;
         low_rows<2>(J, t, a, j0, cols, [&](int c, float x) {
-            const __nv_bfloat16 hi = __float2bfloat16_rn(x);
-            const float h = __bfloat162float(hi);
-            v[c] = hi;
-            v[lo + c] = __float2bfloat16_rn(isfinite(h) ? x - h : 0.f);
+            float h, l;
+            split_bf16(x, &h, &l);
+            v[c] = __float2bfloat16_rn(h);
+            v[lo + c] = __float2bfloat16_rn(l);
         });
     }
 }
@@ -320,7 +328,7 @@ __global__ void __launch_bounds__(kLowTcThreads, 2)
         for (int i = tid; i < mine * (rp / 8); i += kLowTcThreads) {
             const int c0 = i / mine * 8, tok = rank * mine + i % mine, e = adapter_of(t0 + tok);
             if (e < 0) continue;
-            float v[8] = {}, l[8];
+            float v[8] = {}, h[8], l[8];
             for (int r = 0; r < ks; ++r) {
                 const uint32_t src = (ks > 1 ? mapa_shared(own, r) : own) + (uint32_t)(c0 * 128 + tok) * 4;
 #pragma unroll
@@ -334,11 +342,10 @@ __global__ void __launch_bounds__(kLowTcThreads, 2)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 v[j] = c0 < J.rank ? v[j] * scale : 0.f;  // (beyond the rank 0 x, which is no 0 for an infinite x)
-                const float h = __bfloat162float(__float2bfloat16_rn(v[j]));
-                l[j] = isfinite(h) ? v[j] - h : 0.f;
+                split_bf16(v[j], h + j, l + j);
             }
             __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(J.v) + (t0 + tok) * row + c0;
-            *reinterpret_cast<uint4*>(dst) = pack8(v);
+            *reinterpret_cast<uint4*>(dst) = pack8(h);
             *reinterpret_cast<uint4*>(dst + lo) = pack8(l);
         }
     }

@@ -651,8 +651,8 @@ typedef struct gdn_lora {
  *   do not reach it.
  *   act, w, n_tok, n_out, k as in gdn_proj_gemm; out bf16 rows ld_out >= n_out apart, 16-byte
  *   aligned, ld_out a multiple of 8; 0 <= n_seg <= 2^20; a and b 16-byte aligned, scale 4.
- *   The low-rank activations scale (a act) are carried to 2^-16 of their value or better
- *   (fp32, or the sum of two bf16 numbers; an infinite element of b may then give NaN where the
+ *   The low-rank activations scale (a act) are carried to 2^-16 of their value or better, 2^-134 where
+ *   that is more (fp32, or the sum of two bf16 numbers; an infinite element of b may then give NaN where the
  *   exact sum is infinite).
  *   workspace: gdn_proj_lora_workspace_size bytes, 16-byte aligned; calls that may overlap need one each. */
 gdn_status gdn_proj_lora(const void* act, const void* w, const gdn_lora* lora, const int32_t* cu_rows,
