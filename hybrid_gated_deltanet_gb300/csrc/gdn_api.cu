@@ -1034,7 +1034,7 @@ gdn_status gdn_rope(const gdn_rope_plan* plan, const int32_t* positions, int64_t
 
 // sizes and output of a projection whose result rows are stored in 16-byte pieces
 static gdn_status proj_sizes(int64_t n_tok, int32_t n_out, int32_t k, int64_t ld_out) {
-    if (n_tok < 0 || n_tok > ((int64_t)1 << 22))
+    if (n_tok < 0 || n_tok > gdn::kProjTokens)
         return fail(GDN_ERR_RANGE, "n_tok: found %lld, required 0..2^22", (long long)n_tok);
     if (n_out < 1 || n_out > 1 << 24) return fail(GDN_ERR_SHAPE, "n_out: found %d, required 1..2^24", n_out);
     if (k < 8 || k % 8 != 0 || k > 1 << 24)
@@ -1067,7 +1067,7 @@ struct FusedPlan {
 static FusedPlan fused_plan(int64_t n_tok, int32_t n_out, int32_t k, bool gated) {
     const gdn::FewPlan few = gdn::few_plan(n_tok, n_out, k, gated, 0);
     const gdn::WidePlan wide = gdn::wide_plan(n_tok, n_out, k, gated, 0, 0);
-    return {few.us100 < 0 || (n_tok > kFewAlways && wide.us100 < few.us100), wide};
+    return {n_tok > kFewAlways && wide.us100 < few.us100, wide};
 }
 static cudaError_t launch_fused(const Fused& f, const FusedPlan& p, cudaStream_t st) {
     if (p.wide) {
@@ -1098,7 +1098,7 @@ gdn_status gdn_proj_gated(const void* act, const void* w_gate, const void* w_up,
 }
 
 static gdn_status ffn_sizes(int64_t n_tok, int32_t hidden, int32_t inter) {
-    if (n_tok < 0 || n_tok > ((int64_t)1 << 22))
+    if (n_tok < 0 || n_tok > gdn::kProjTokens)
         return fail(GDN_ERR_RANGE, "n_tok: found %lld, required 0..2^22", (long long)n_tok);
     if (hidden < 8 || hidden % 8 != 0 || hidden > 1 << 24 || inter < 8 || inter % 8 != 0 || inter > 1 << 24)
         return fail(GDN_ERR_SHAPE, "hidden/inter: found %d/%d, required positive multiples of 8, at most 2^24", hidden,
@@ -1172,7 +1172,7 @@ static LoraWs lora_ws(int64_t n_tok, int32_t n_out, int32_t k, int32_t rank, int
     // What comes before them and is not hidden takes 4 and 9 us.
     const gdn::FewPlan few = gdn::few_plan(n_tok, n_out, k, false, rank);
     const gdn::WidePlan plan = gdn::wide_plan(n_tok, n_out, k, false, rank, n_tok > 0 ? 256 * (int64_t)n_seg / n_tok + 1 : 0);
-    const bool wide = few.us100 < 0 || (n_tok > kFewAlways && plan.us100 + 900 < few.us100 + 400);
+    const bool wide = n_tok > kFewAlways && plan.us100 + 900 < few.us100 + 400;
     if (!wide || plan.ws_bytes == 0) return {wide, plan, low, 0, end, 0};
     return {wide, plan, low, split, split + plan.ws_bytes, plan.counters};
 }

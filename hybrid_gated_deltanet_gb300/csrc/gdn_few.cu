@@ -432,6 +432,7 @@ cudaError_t take_device_status_few(unsigned* out) { return take_device_status_tu
 // A tile takes the fewest tokens that hold all of them, 128 at most; with adapters also fewer, where more CTAs then share
 // the tokens at the price of reading the weights again.  Depends on the sizes only.
 FewPlan few_plan(int64_t n_tok, int32_t n_out, int32_t k, bool gated, int32_t rank) {
+    static_assert(kProjTokens / 128 <= 65535, "tiles of 128 tokens in the grid's y");
     // CTAs of clusters of 1 .. 8 that run at the same time on 152 SMs, two on each: clusters of 3, 5 and more leave some of a
     // GPC's SMs empty (cudaOccupancyMaxActiveClusters)
     constexpr int kSlots[9] = {0, 304, 304, 276, 288, 280, 276, 210, 240};
@@ -440,7 +441,7 @@ FewPlan few_plan(int64_t n_tok, int32_t n_out, int32_t k, bool gated, int32_t ra
     FewPlan plan{most, 1, -1};
     for (int n = most; n >= (rank > 0 ? 16 : most); n /= 2) {
         const int64_t tiles_t = (n_tok + n - 1) / n, tiles = (n_out + rows - 1) / rows * tiles_t;
-        if (tiles_t > 65535) break;
+        if (tiles_t > 65535) break;  // the grid's limit, which the first of these tiles stays within
         for (int c = 1; c <= 8 && c <= std::max(1, kb / 2); ++c) {
             const int64_t tok = (std::min<int64_t>(n, n_tok) + c - 1) / c;
             const int64_t one = (kb + c - 1) / c * 10 * (128 + n) / 128 + 80 + 10 * c + (rank > 0 ? tok * (6 + rank / 4) : 0);

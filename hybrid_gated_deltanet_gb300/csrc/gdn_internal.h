@@ -310,6 +310,8 @@ struct RopeJob {
 void rope_turns(int rot, double theta, double factor, int orig_len, double beta_fast, double beta_slow, uint64_t* turns);
 cudaError_t launch_rope(RopeJob job, cudaStream_t st);
 
+constexpr int64_t kProjTokens = (int64_t)1 << 22;  // the most tokens of a call of the fused projections
+
 // out[t][n] of few tokens: x_t . w_n, plus (rank > 0) v_t . b_n of the token's adapter; or, with w2,
 // silu(x_t . w_n) (x_t . w2_n)
 struct FewJob {
@@ -329,7 +331,7 @@ struct FewJob {
 cudaError_t launch_few(const FewJob& job, cudaStream_t st);
 struct FewPlan {
     int n, ks;      // tokens of a tile, CTAs that share a tile's K
-    int64_t us100;  // what the call should take, in hundredths of a microsecond (< 0: too many tokens)
+    int64_t us100;  // what the call should take, in hundredths of a microsecond
 };
 FewPlan few_plan(int64_t n_tok, int32_t n_out, int32_t k, bool gated, int32_t rank);
 
