@@ -4,6 +4,7 @@
 // caller's stream.  Nothing here allocates device memory or synchronises.
 // Error messages follow the Strata convention (chapter 6, sections 6.2 and
 // 6.5): name the argument, the value found and the value required.
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -1045,7 +1046,10 @@ static gdn_status proj_sizes(int64_t n_tok, int32_t n_out, int32_t k, int64_t ld
     return GDN_OK;
 }
 
-constexpr int64_t kFewAlways = 64;  // tokens up to which the kernel of few tokens takes a call
+// Tokens up to which the kernel of few tokens takes a call, without and with adapters.  Without, it took less at every size
+// measured up to 64 (gated, 64 tokens: 2560 -> 9216 19.8 us against 22.7, 1024 -> 3584 7.5 against 11.2, 64 -> 262144 59.7 against
+// 77.6, where the estimates are alike; the projection back of 9216 -> 2560 12.6 against 25).
+constexpr int64_t kFewAlways = 64, kFewAlwaysLora = 16;
 
 static size_t align_parts(size_t bytes) { return (bytes + 255) & ~(size_t)255; }
 
@@ -1121,14 +1125,14 @@ static FfnWs ffn_ws(int64_t n_tok, int32_t hidden, int32_t inter) {
 
 // What the parts of split tiles may take in calls of up to n_tok tokens: fewer tokens may leave more tiles over, so that
 // a workspace made for the largest call would else not serve the others.
-static size_t parts_bytes(int64_t n_tok, int32_t n_out, int32_t k) {
-    return n_tok > kFewAlways ? gdn::wide_ws_most(n_tok, n_out, k) : 0;
+static size_t parts_bytes(int64_t n_tok, int64_t few_always, int32_t n_out, int32_t k) {
+    return n_tok > few_always ? gdn::wide_ws_most(n_tok, n_out, k) : 0;
 }
 
 size_t gdn_ffn_workspace_size(int64_t n_tok, int32_t hidden, int32_t inter) {
     if (ffn_sizes(n_tok, hidden, inter)) return 0;
     ok();
-    const size_t half = (size_t)n_tok * inter * 2, parts = parts_bytes(n_tok, hidden, inter);
+    const size_t half = (size_t)n_tok * inter * 2, parts = parts_bytes(n_tok, kFewAlways, hidden, inter);
     return parts > 0 ? align_parts(half) + parts : half;
 }
 
@@ -1169,10 +1173,16 @@ static LoraWs lora_ws(int64_t n_tok, int32_t n_out, int32_t k, int32_t rank, int
     const size_t low = (size_t)n_tok * gdn::low_row(rank) * 2, end = low + (size_t)n_tok * 4, split = align_parts(end);
     // Requests of a few tokens each bring an adapter for (nearly) every token, a matrix product for none: the kernel of few
     // tokens gives each token its adapter on the CUDA cores, the one of many takes each adapter through the tensor cores.
-    // What comes before them and is not hidden takes 4 and 9 us.
+    // What comes before them takes both about as long, but that the tokens of a short request follow one another there, 0.02 us
+    // each for 64 of K.
+    // Up to 16 tokens the first took less at every size and rank (2560 -> 12352, 16 tokens of one request: 16.5 us against 24.4 at
+    // rank 16, 25.5 against 26.4 at 128); with more it depends (64 tokens of one request: 22.9 against 21.7 at rank 16, 70
+    // against 24 at 128; of 64 requests 23 against 45).
     const gdn::FewPlan few = gdn::few_plan(n_tok, n_out, k, false, rank);
-    const gdn::WidePlan plan = gdn::wide_plan(n_tok, n_out, k, false, rank, n_tok > 0 ? 256 * (int64_t)n_seg / n_tok + 1 : 0);
-    const bool wide = n_tok > kFewAlways && plan.us100 + 900 < few.us100 + 400;
+    const int64_t per_tile = n_tok > 0 ? std::min<int64_t>(n_seg, 256 * (int64_t)n_seg / n_tok + 1) : 0;  // requests
+    const gdn::WidePlan plan = gdn::wide_plan(n_tok, n_out, k, false, rank, per_tile);
+    const int64_t len = n_seg > 0 ? (n_tok + n_seg - 1) / n_seg : 0, shorts = len < gdn::kShortRequest ? len * ((k + 63) / 64) * 2 : 0;
+    const bool wide = n_tok > kFewAlwaysLora && plan.us100 + shorts < few.us100;
     if (!wide || plan.ws_bytes == 0) return {wide, plan, low, 0, end, 0};
     return {wide, plan, low, split, split + plan.ws_bytes, plan.counters};
 }
@@ -1189,7 +1199,7 @@ static gdn_status lora_sizes(int64_t n_tok, int32_t n_out, int32_t k, int32_t ra
 size_t gdn_proj_lora_workspace_size(int64_t n_tok, int32_t n_out, int32_t k, int32_t rank, int32_t n_seg) {
     if (lora_sizes(n_tok, n_out, k, rank, n_seg)) return 0;
     ok();
-    const size_t low = (size_t)n_tok * (gdn::low_row(rank) * 2 + 4), parts = parts_bytes(n_tok, n_out, k);
+    const size_t low = (size_t)n_tok * (gdn::low_row(rank) * 2 + 4), parts = parts_bytes(n_tok, kFewAlwaysLora, n_out, k);
     return parts > 0 ? align_parts(low) + parts : low;
 }
 

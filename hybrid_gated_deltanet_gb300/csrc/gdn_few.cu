@@ -44,21 +44,24 @@ constexpr int few_threads() { return MODE == kLora ? 224 : 192; }
 // Two CTAs on an SM.  What they have in flight covers the memory's latency several times over; more of it only makes
 // every other load wait longer, so the weights' ring is the smaller one where the rows of b stream beside them.
 constexpr int kRowSlots = 16;  // lora: tokens in the ring of adapter rows, at most
+constexpr int few_stage(int n) { return (kFewM + n) * kFewK * 2; }
+constexpr int few_lora_stages(int n) { return n <= 32 ? 3 : 2; }
+constexpr int few_row_ring(int n) { return 108 * 1024 - few_lora_stages(n) * few_stage(n); }
+constexpr int few_row_slot(int rank) { return kFewM * rank * 2 + rank * 4; }  // 128 rows of b, then v
 template <int N, int MODE>
 struct FewLay {
     static constexpr int W_BYTES = kFewM * kFewK * 2;
-    static constexpr int X_BYTES = N * kFewK * 2;
-    static constexpr int STAGE = W_BYTES + X_BYTES;
-    static constexpr int STAGES = MODE == kLora ? (N <= 32 ? 3 : 2) : N == 16 ? 6 : N == 32 ? 5 : N == 64 ? 4 : 3;
+    static constexpr int STAGE = few_stage(N);
+    static constexpr int STAGES = MODE == kLora ? few_lora_stages(N) : N == 16 ? 6 : N == 32 ? 5 : N == 64 ? 4 : 3;
     static constexpr int RING = STAGES * STAGE;  // the fp32 partial block lies over it at the end
     static constexpr int ROW_OFF = RING;
-    static constexpr int ROW_RING = MODE == kLora ? 108 * 1024 - RING : 0;
+    static constexpr int ROW_RING = MODE == kLora ? few_row_ring(N) : 0;
     // full[S], empty[S], done, row_full[], row_empty[], TMEM address, the tokens' adapters
     static constexpr int BAR_OFF = ROW_OFF + ROW_RING;
     static constexpr int ADP_OFF = BAR_OFF + (2 * STAGES + 1 + (MODE == kLora ? 2 * kRowSlots : 0)) * 8 + 8;
     static constexpr int SMEM_ALLOC = ADP_OFF + (MODE == kLora ? N * 4 : 0) + 1024;
     static_assert(RING >= N * kFewM * 4, "the partial block");
-    static_assert(MODE != kLora || ROW_RING >= kFewM * 128 * 2 + 128 * 4, "a token of the largest rank");
+    static_assert(MODE != kLora || ROW_RING >= few_row_slot(128), "a token of the largest rank");
     static_assert(2 * (SMEM_ALLOC + 1024) <= 227 * 1024, "CTAs on an SM");
 };
 
@@ -148,8 +151,7 @@ __global__ void __launch_bounds__(few_threads<MODE>(), 2)
     const int64_t t0 = (int64_t)blockIdx.y * N;
     const int ncol = (int)(P.n_tok - t0 < N ? P.n_tok - t0 : N);
     const int mine = ncol > rank ? (ncol - rank + ks - 1) / ks : 0;  // tokens rank, rank + ks, ... are finished here
-    // ring of adapter rows: per slot 128 rows of b, then v
-    const int slot_bytes = kFewM * P.rank * 2 + P.rank * 4;
+    const int slot_bytes = few_row_slot(P.rank);  // in the ring of adapter rows
     const int slots = MODE == kLora ? min(kRowSlots, L::ROW_RING / slot_bytes) : 1;
 
     if (tid == 0) {
@@ -428,7 +430,8 @@ cudaError_t take_device_status_few(unsigned* out) { return take_device_status_tu
 
 // Tokens of a tile and cluster size.  The CTAs run in waves, and a CTA costs its K blocks (0.3 us each, more with more
 // tokens), a start and an end, a little for each CTA of its cluster, and with adapters its share of the tokens (0.3 us each at
-// rank 16, 0.7 at 64): `us100` is what that came to against measurements of 100 to 1000 tokens, within a quarter.
+// rank 16, 0.7 at 64).  `us100` was 0.65 to 1.2 of the time measured at 65 to 1500 tokens without adapters (fewer tokens:
+// 0.5 to 0.9, bound by the weights' bytes, which are not counted), 0.6 to 1.5 with them at 1 to 1500 tokens and ranks 16 to 128.
 // A tile takes the fewest tokens that hold all of them, 128 at most; with adapters also fewer, where more CTAs then share
 // the tokens at the price of reading the weights again.  Depends on the sizes only.
 FewPlan few_plan(int64_t n_tok, int32_t n_out, int32_t k, bool gated, int32_t rank) {
@@ -441,10 +444,12 @@ FewPlan few_plan(int64_t n_tok, int32_t n_out, int32_t k, bool gated, int32_t ra
     FewPlan plan{most, 1, -1};
     for (int n = most; n >= (rank > 0 ? 16 : most); n /= 2) {
         const int64_t tiles_t = (n_tok + n - 1) / n, tiles = (n_out + rows - 1) / rows * tiles_t;
+        // a token's rows of b; where the ring holds those of one token only, nothing is under way while they are used
+        const int per_tok = rank > 0 ? 6 + rank / 4 + (few_row_ring(n) < 2 * few_row_slot(rank) ? 36 : 0) : 0;
         if (tiles_t > 65535) break;  // the grid's limit, which the first of these tiles stays within
         for (int c = 1; c <= 8 && c <= std::max(1, kb / 2); ++c) {
             const int64_t tok = (std::min<int64_t>(n, n_tok) + c - 1) / c;
-            const int64_t one = (kb + c - 1) / c * 10 * (128 + n) / 128 + 80 + 10 * c + (rank > 0 ? tok * (6 + rank / 4) : 0);
+            const int64_t one = (kb + c - 1) / c * 10 * (128 + n) / 128 + 80 + 10 * c + tok * per_tok;
             const int64_t cost = 3 * ((tiles * c + kSlots[c] - 1) / kSlots[c]) * one;
             if (plan.us100 < 0 || cost < plan.us100) plan = {n, c, cost};
         }

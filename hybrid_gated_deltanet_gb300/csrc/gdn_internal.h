@@ -368,6 +368,8 @@ size_t wide_ws_most(int64_t n_tok, int32_t n_out, int32_t k);
 // of 16 ceil(rank / 16) (rank <= 32) or 64 ceil(rank / 64) elements, each padded with zeros to a multiple of 16.
 constexpr int low_row(int rank) { return rank <= 32 ? 64 : 2 * ((rank + 63) / 64 * 64); }
 
+constexpr int kShortRequest = 16;  // tokens from which on the tensor cores make a request's v for launch_wide
+
 // each token's adapter, and v = scale A x, for launch_few (wide 0: fp32 [n_tok][rank]) or launch_wide (wide 1)
 struct LowJob {
     const void *x, *a;

@@ -15,7 +15,6 @@ namespace {
 
 constexpr int kLowThreads = 256;
 constexpr int kLowWarps = kLowThreads / 32;
-constexpr int kShortRequest = 16;  // tokens from which on the tensor cores take a request of a wide call
 
 // The request that token t belongs to, or -1: the last s with cu[s] <= t, if t < cu[s+1].  By a whole warp, 32 probes a
 // round; where every request is one token (decoding) the first guess is right.  Any contents of cu stay in bounds.

@@ -572,15 +572,16 @@ cudaError_t launch_wide_mode(const WideJob& job, cudaStream_t st) {
 constexpr int64_t kPairs = 76;
 
 // Depends on the sizes only, so that a workspace can be sized without a device: 76 pairs, of which a device with others
-// makes the same jobs.  Cycles, from measurements of 100 to 1000 tokens: a K block takes 585, and no fewer with fewer columns
+// makes the same jobs.  Cycles, from measurements of 1 to 1500 tokens: a K block takes 585, and no fewer with fewer columns
 // (the tensor cores read the 128 rows of x in the same time for 64 columns as for 256: halves and quarters of tiles in the
 // last wave cost as much as whole ones); a job's start and end 2100; parts of a tile, written and read again, 4000 and 4200
-// each; an adapter's blocks 128 an MMA and 200 around them; a launch 6 us.
+// each; an adapter's blocks 128 an MMA and 500 around them; a launch 6 us.  Came to 0.7 to 1.1 of the measured time without adapters, 0.5
+// to 1.35 with them (0.5 where every token brings its own, which goes to the other kernel by far).
 WidePlan wide_plan(int64_t n_tok, int32_t n_out, int32_t k, bool gated, int32_t rank, int64_t adapters) {
     constexpr int64_t kKBlock = 585, kJob = 2100;
     const int kb = (k + kWideK - 1) / kWideK, cols = gated ? 128 : 256;
     const int64_t tiles = (n_out + cols - 1) / cols * ((n_tok + kWideTok - 1) / kWideTok);
-    const int64_t extra = rank > 0 ? adapters * ((rank + 15) / 16 * 256 + 200) : 0;
+    const int64_t extra = rank > 0 ? adapters * ((rank + 15) / 16 * 256 + 500) : 0;
     WidePlan plan;
     plan.whole = tiles / kPairs * kPairs;
     plan.rest = tiles - plan.whole;
