@@ -1110,7 +1110,9 @@ static gdn_status ffn_sizes(int64_t n_tok, int32_t hidden, int32_t inter) {
     return GDN_OK;
 }
 
-// the gated half, then what the projection back splits along K
+// the gated half, then what the projection back splits along K.  The half lies there in bf16, as the tensor cores take it: held to
+// 2^-16 in two bf16 numbers it would double the products of the projection back (a third of the block's, at 8192 tokens 200 us
+// more).  With its rounding the block's relative error is 2.35e-3, without it 1.65e-3.
 struct FfnWs {
     FusedPlan back;
     size_t split, bytes;

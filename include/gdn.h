@@ -311,7 +311,8 @@ gdn_status gdn_proj_gemm(const void* act, const void* w, void* out, int64_t n_to
                          int32_t k, int64_t ld_out, void* workspace, size_t ws_bytes, void* stream);
 
 /* Workspace bytes of gdn_proj_gemm for these sizes (0: none needed or invalid
- * sizes).  Depends on the sizes only. */
+ * sizes).  Depends on the sizes only; fewer tokens may need more (K is split over more
+ * CTAs), so a workspace for several sizes is the largest of theirs. */
 size_t gdn_proj_workspace_size(int64_t n_tok, int32_t n_out, int32_t k);
 
 /* Projection weights of one layer (device pointers, bf16, row-major). */
