@@ -1177,7 +1177,7 @@ static LoraWs lora_ws(int64_t n_tok, int32_t n_out, int32_t k, int32_t rank, int
     // tokens gives each token its adapter on the CUDA cores, the one of many takes each adapter through the tensor cores.
     // What comes before them takes both about as long, but that the tokens of a short request follow one another there, 0.02 us
     // each for 64 of K.
-    // Up to 16 tokens the first took less at every size and rank (2560 -> 12352, 16 tokens of one request: 16.5 us against 24.4 at
+    // Up to 16 tokens the first took less at every size and rank measured (2560 -> 12352, 16 tokens of one request: 16.5 us against 24.4 at
     // rank 16, 25.5 against 26.4 at 128); with more it depends (64 tokens of one request: 22.9 against 21.7 at rank 16, 70
     // against 24 at 128; of 64 requests 23 against 45).
     const gdn::FewPlan few = gdn::few_plan(n_tok, n_out, k, false, rank);
